@@ -193,6 +193,40 @@ int kvc_decode_step(kvc_ctx *c, int layer, int n_seq, const int32_t *seq_ids, co
                     const float *k, const float *v, const float *q, float *out, float kq_scale,
                     void *stream);
 
+/* Type of a block's queries and outputs (kvc_attn_cross, kvc_attn_weight). */
+typedef enum kvc_act { KVC_ACT_F32 = 0, KVC_ACT_F16 = 1, KVC_ACT_BF16 = 2 } kvc_act;
+
+/* Attention of a block of query tokens over the cached rows of one layer:
+ * cross attention to rows of another length (an encoder's or an image's
+ * states), a prompt's tokens, drafted tokens.  Sequence entry i brings n_q[i]
+ * tokens (packed one entry after the other: T = sum of n_q tokens in all);
+ * token t sees the leading N_t rows, in row order, of its sequence, N_t =
+ * min(max(n_vis[t], 0), rows of that layer), or every row without n_vis:
+ *   s_j = kq_scale * q[t][h] . K_j,  lse[t][h] = log sum_j exp(s_j),
+ *   out[t][h][:] = sum_j exp(s_j - lse[t][h]) V_j,          j < N_t
+ * with K/V read as stored and query head h reading KV head h / (H/Hk) ([F5]
+ * sections M2/M3: grouped-query heads stay in whole KV-head groups).  A token
+ * that sees no row gets out = 0 and lse = -inf; n_q[i] may be 0.  The causal
+ * attention of a prompt's tokens over themselves and the rows before them is
+ * n_vis[t] = (rows before the block) + (t's place in the block) + 1.
+ * What a row holds that a token does not see never reaches that token.
+ * seq_ids, n_q: HOST int32[n_seq]; an id may come more than once (decoders
+ * that share an encoder's rows).  act: type of q and out (kvc_act).
+ * q, out: device [T][n_head][head_dim], contiguous; out may not overlap q.
+ * lse: device fp32 [T][n_head], or NULL.  n_vis: device int32 [T], or NULL.
+ * q and out 16-byte aligned, lse and n_vis 4-byte aligned.
+ * Results are bitwise repeatable.  32-bit results keep 32-bit accuracy; with
+ * 16-bit queries the products' operands have 11 significant bits or more and
+ * all sums are fp32.
+ * The call only enqueues work on `stream`.  Its work space (split rows'
+ * partial sums) is allocated by the context's first such call, has one size
+ * for good and is shared by all of them, captured ones too, so order them.
+ * That first call cannot be captured into a graph (KVC_EINVAL).
+ * Device-resident contexts only.
+ * Errors: KVC_EINVAL, KVC_ENOMEM, KVC_ECUDA. */
+int kvc_attn_cross(kvc_ctx *c, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_q, int act,
+                   const void *q, void *out, float *lse, const int32_t *n_vis, float kq_scale, void *stream);
+
 /* Remove the rows of `seq` whose position is in [p0, p1), in every layer
  * (MemorySeqRemove, [COLD] section llama - KV-byte offload; the context
  * shift's discard, [F5] section M1).  Rows after the removed ones keep their
@@ -347,6 +381,17 @@ int kvc_debug_chunk_plan(int type, int head_dim, int n_head, int n_head_kv, int 
  * kvc_debug_chunk_plan.  chunk_rows_seq: HOST int32[n_seq].  Errors: KVC_EINVAL. */
 int kvc_debug_chunk_plan_seq(int type, int head_dim, int n_head, int n_head_kv, int sms, int occ, int occ2,
                              int n_seq, const int32_t *rows, int32_t *chunk_rows_seq, int32_t *cfg);
+
+/* Test hook, no context and no GPU needed: how a block attention launch on a
+ * device of `sms` SMs cuts n_seq (1 .. 64) sequences of rows[i] cached rows and
+ * n_q[i] tokens: query tiles of *tile_m rows (tokens x query heads of a KV
+ * head); the cached rows of sequence i in splits[i] parts of split_rows[i]
+ * rows; *items work items; *part_rows partial rows used of the *part_cap that
+ * the work space holds, *tickets arrival counters.  act: kvc_act.
+ * rows, n_q, splits, split_rows: HOST int32[n_seq].  Errors: KVC_EINVAL. */
+int kvc_debug_block_plan(int n_head, int n_head_kv, int head_dim, int act, int sms, int n_seq, const int32_t *rows,
+                         const int32_t *n_q, int32_t *tile_m, int32_t *splits, int32_t *split_rows, int64_t *items,
+                         int64_t *part_rows, int64_t *part_cap, int64_t *tickets);
 
 /* Test hook, no context and no GPU needed: the rows of a sequence holding
  * positions pos[0 .. n) that the sequence operations select for the range

@@ -455,6 +455,7 @@ void kvc_destroy(kvc_ctx *cc) {
     cudaFree(c->pt_dev);
     cudaFree(c->part);
     cudaFree(c->tickets);
+    cudaFree(c->block_part);
     cudaFree(c->err_dev);
     if (c->err_host) cudaFreeHost(c->err_host);
     if (c->up_host) cudaFreeHost(c->up_host);

@@ -1,0 +1,265 @@
+// block_attn.cu - host side of the operators over a block of query tokens
+// (kvc_attn_cross): checks, the split of the cached rows over work items, the
+// work space and the launches.
+#include "block_attn.h"
+#include "ctx.h"
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+
+namespace kvc {
+
+int cuda_fail(Ctx *c, cudaError_t e, const char *what);
+int dev_alloc(Ctx *c, void **p, int64_t bytes, const char *what);
+
+#define KVC_CU(c, call)                                                                                            \
+    do {                                                                                                           \
+        cudaError_t e_ = (call);                                                                                   \
+        if (e_ != cudaSuccess) return cuda_fail((c), e_, #call);                                                   \
+    } while (0)
+
+// Partial rows of the work space: every SM four items of a whole query tile.
+static int64_t part_rows_cap(int sms) { return (int64_t)4 * sms * CROSS_TILE_M; }
+
+// The work space of split rows: partial sums [rows][D], (max, sum) pairs
+// [rows] and arrival counters.  Allocated once, with one size: a captured
+// launch keeps its addresses.
+static int ensure_block_space(Ctx *c, cudaStream_t st) {
+    if (c->block_part) return KVC_OK;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    KVC_CU(c, cudaStreamIsCapturing(st, &cap));
+    if (cap != cudaStreamCaptureStatusNone)
+        return c->fail(KVC_EINVAL, "the first block attention of a context allocates its work space: call it once before a capture");
+    const int64_t rows = part_rows_cap(c->sms);
+    const int64_t floats = rows * (c->D + 2), bytes = floats * 4 + rows * 4;
+    float *p = nullptr;
+    int rc = dev_alloc(c, (void **)&p, bytes, "block attention work space");
+    if (rc) return rc;
+    // the counters start at zero (every launch leaves them at zero)
+    cudaError_t e = cudaMemsetAsync(p + floats, 0, (size_t)rows * 4, c->st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(c->st);
+    if (e != cudaSuccess) {
+        cudaFree(p);
+        c->device_bytes -= bytes;
+        return cuda_fail(c, e, "clearing the block attention work space");
+    }
+    c->block_part = p;
+    return KVC_OK;
+}
+
+// Cut the cached rows of the launch's sequences into parts: none where the
+// query tiles alone give every resident CTA an item, else parts of one length
+// (whole steps of CROSS_TILE_N rows, four at least) as short as `want` items
+// and the work space allow.
+static void plan_splits(BlockParams &p, int64_t want, int64_t part_cap) {
+    int64_t base = 0;
+    int32_t longest = 0;
+    for (int i = 0; i < p.n_seq; ++i) {
+        base += (int64_t)p.seq[i].tiles * p.Hk;
+        if (p.seq[i].tiles) longest = std::max(longest, p.seq[i].n_rows);
+    }
+    auto parts = [](const BlockSeq &s, int64_t len) {
+        return (int32_t)std::max<int64_t>(1, (s.n_rows + len - 1) / len);
+    };
+    auto items = [&](int64_t len, int64_t *slots) {
+        int64_t n = 0;
+        *slots = 0;
+        for (int i = 0; i < p.n_seq; ++i) {
+            const int64_t k = (int64_t)p.seq[i].tiles * p.Hk * parts(p.seq[i], len);
+            n += k;
+            if (parts(p.seq[i], len) > 1) *slots += k;
+        }
+        return n;
+    };
+    const int64_t least = 4 * CROSS_TILE_N;
+    int64_t len = std::max<int64_t>(least, ((int64_t)longest + CROSS_TILE_N - 1) / CROSS_TILE_N * CROSS_TILE_N);
+    if (base < want) {
+        int64_t lo = 1, hi = len / CROSS_TILE_N; // shortest length, in steps, that fits
+        lo = std::min(hi, least / CROSS_TILE_N);
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) / 2;
+            int64_t slots;
+            const int64_t n = items(mid * CROSS_TILE_N, &slots);
+            if (n <= want && slots * p.part_rows <= part_cap) hi = mid; else lo = mid + 1;
+        }
+        len = hi * CROSS_TILE_N;
+    }
+    int32_t item = 0, row = 0, ticket = 0;
+    for (int i = 0; i < p.n_seq; ++i) {
+        BlockSeq &s = p.seq[i];
+        s.splits = parts(s, len);
+        // equal parts, in whole steps
+        const int64_t even = ((int64_t)s.n_rows + s.splits - 1) / s.splits;
+        s.split_rows = (int32_t)std::min<int64_t>(INT32_MAX / 2 / CROSS_TILE_N * CROSS_TILE_N,
+                                                  std::max<int64_t>(1, (even + CROSS_TILE_N - 1) / CROSS_TILE_N) * CROSS_TILE_N);
+        s.item0 = item;
+        s.part_row0 = row;
+        s.ticket0 = ticket;
+        const int32_t k = s.tiles * p.Hk * s.splits;
+        item += k;
+        if (s.splits > 1) {
+            row += k * p.part_rows;
+            ticket += s.tiles * p.Hk;
+        }
+    }
+    p.n_items = item;
+}
+
+// The query tiles and items of a launch over p.n_seq sequences (p.Hk and p.r
+// set); *tok0: the first token, moved on.  Returns whether the tiles are narrow.
+static bool plan_block(BlockParams &p, int sms, const int32_t *rows, const int32_t *n_q, int64_t *tok0) {
+    int32_t most = 0;
+    for (int i = 0; i < p.n_seq; ++i) most = std::max(most, n_q[i]);
+    const bool narrow = (int64_t)most * p.r <= 16;
+    p.tile_m = narrow ? 16 : CROSS_TILE_M;
+    p.part_rows = (int32_t)std::min<int64_t>(p.tile_m, (int64_t)most * p.r);
+    for (int i = 0; i < p.n_seq; ++i) {
+        BlockSeq &s = p.seq[i];
+        s.n_rows = rows[i];
+        s.tok0 = (int32_t)*tok0;
+        s.n_tok = n_q[i];
+        s.tiles = (int32_t)(((int64_t)s.n_tok * p.r + p.tile_m - 1) / p.tile_m);
+        *tok0 += s.n_tok;
+    }
+    plan_splits(p, (int64_t)2 * sms, part_rows_cap(sms));
+    return narrow;
+}
+
+// Checks that the block operators share; *total: tokens of the block.
+static int block_check(Ctx *c, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_q, int act, const void *q,
+                       float kq_scale, int64_t *total) {
+    if (c->host) return c->fail(KVC_EINVAL, "block operators need a device-resident context");
+    if (layer < 0 || layer >= c->L) return c->fail(KVC_EINVAL, "layer out of range");
+    if (n_seq < 1 || !seq_ids || !n_q) return c->fail(KVC_EINVAL, "n_seq >= 1, seq_ids and n_q required");
+    if (act != KVC_ACT_F32 && act != KVC_ACT_F16 && act != KVC_ACT_BF16)
+        return c->fail(KVC_EINVAL, "act must be KVC_ACT_F32, KVC_ACT_F16 or KVC_ACT_BF16");
+    if (!std::isfinite(kq_scale)) return c->fail(KVC_EINVAL, "kq_scale must be finite");
+    int64_t t = 0;
+    for (int i = 0; i < n_seq; ++i) {
+        if (seq_ids[i] < 0 || seq_ids[i] >= (int)c->seqs.size())
+            return c->fail(KVC_EINVAL, "sequence id out of range");
+        if (n_q[i] < 0) return c->fail(KVC_EINVAL, "n_q must not be negative");
+        t += n_q[i];
+    }
+    if (t * c->r > INT32_MAX / 4 / c->Hk) return c->fail(KVC_EINVAL, "too many tokens in one block");
+    *total = t;
+    if (t == 0) return KVC_OK;
+    if (!q) return c->fail(KVC_EINVAL, "q must be non-null");
+    if ((uintptr_t)q & 15) return c->fail(KVC_EINVAL, "q must be 16-byte aligned");
+    return KVC_OK;
+}
+
+static void block_params(const Ctx *c, int layer, float kq_scale, int act, BlockParams &p) {
+    std::memset(&p, 0, sizeof(p));
+    p.H = c->H;
+    p.Hk = c->Hk;
+    p.D = c->D;
+    p.r = c->r;
+    p.P = c->P;
+    p.n_pages = c->n_pages;
+    p.max_pages = c->max_pages;
+    p.act = act;
+    p.scale_log2 = (float)((double)kq_scale * 1.4426950408889634);
+    p.pt = c->pt_dev;
+    const int64_t lo = (int64_t)layer * c->pool_rows;
+    p.kdata = c->kdata + lo * c->krow;
+    p.vdata = c->vdata + lo * c->vrow;
+    p.ks = c->ksb ? reinterpret_cast<const uint16_t *>(c->kscales + lo * c->ksb) : nullptr;
+    p.vs = c->vsb ? reinterpret_cast<const uint16_t *>(c->vscales + lo * c->vsb) : nullptr;
+    p.err = c->err_dev;
+}
+
+static bool overlap(const void *a, const void *b, int64_t bytes) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return x < y + (uintptr_t)bytes && y < x + (uintptr_t)bytes;
+}
+
+} // namespace kvc
+
+using namespace kvc;
+
+extern "C" int kvc_attn_cross(kvc_ctx *cc, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_q, int act,
+                              const void *q, void *out, float *lse, const int32_t *n_vis, float kq_scale,
+                              void *stream) {
+    if (!cc) return KVC_EINVAL;
+    Ctx *c = reinterpret_cast<Ctx *>(cc);
+    int64_t total = 0;
+    int rc = block_check(c, layer, n_seq, seq_ids, n_q, act, q, kq_scale, &total);
+    if (rc) return rc;
+    if (total == 0) return KVC_OK;
+    if (!out) return c->fail(KVC_EINVAL, "out must be non-null");
+    if ((uintptr_t)out & 15) return c->fail(KVC_EINVAL, "out must be 16-byte aligned");
+    if (((uintptr_t)lse | (uintptr_t)n_vis) & 3) return c->fail(KVC_EINVAL, "lse and n_vis must be 4-byte aligned");
+    if (overlap(q, out, total * c->H * c->D * (act == KVC_ACT_F32 ? 4 : 2)))
+        return c->fail(KVC_EINVAL, "out may not overlap q");
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    KVC_CU(c, cudaSetDevice(c->dev));
+    if ((rc = ensure_block_space(c, st))) return rc;
+    int64_t tok0 = 0;
+    for (int base = 0; base < n_seq; base += MAX_SEQ_PER_LAUNCH) {
+        BlockParams p;
+        block_params(c, layer, kq_scale, act, p);
+        p.q = q;
+        p.out = out;
+        p.lse = lse;
+        p.n_vis = n_vis;
+        p.n_seq = std::min(MAX_SEQ_PER_LAUNCH, n_seq - base);
+        int32_t rows[MAX_SEQ_PER_LAUNCH];
+        for (int i = 0; i < p.n_seq; ++i) {
+            const Seq &sq = c->seqs[(size_t)seq_ids[base + i]];
+            p.seq[i].id = seq_ids[base + i];
+            p.seq[i].off = sq.off;
+            rows[i] = sq.lfill[(size_t)layer];
+        }
+        const bool narrow = plan_block(p, c->sms, rows, n_q + base, &tok0);
+        const int64_t cap = part_rows_cap(c->sms);
+        p.part = c->block_part;
+        p.part_cap = cap;
+        p.tickets = reinterpret_cast<int32_t *>(c->block_part + cap * (c->D + 2));
+        cudaError_t e = launch_cross(c->tk, c->tv, p, narrow, st);
+        if (e != cudaSuccess) return cuda_fail(c, e, "block attention kernel");
+    }
+    return KVC_OK;
+}
+
+extern "C" int kvc_debug_block_plan(int n_head, int n_head_kv, int head_dim, int act, int sms, int n_seq,
+                                    const int32_t *rows, const int32_t *n_q, int32_t *tile_m, int32_t *splits,
+                                    int32_t *split_rows, int64_t *items, int64_t *part_rows, int64_t *part_cap,
+                                    int64_t *tickets) {
+    if (n_head_kv < 1 || n_head < n_head_kv || n_head % n_head_kv || n_head / n_head_kv > MAX_GROUP ||
+        (head_dim != 64 && head_dim != 128) || act < KVC_ACT_F32 || act > KVC_ACT_BF16 || sms < 1 || n_seq < 1 ||
+        n_seq > MAX_SEQ_PER_LAUNCH || !rows || !n_q || !tile_m || !splits || !split_rows || !items || !part_rows ||
+        !part_cap || !tickets)
+        return KVC_EINVAL;
+    BlockParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.H = n_head;
+    p.Hk = n_head_kv;
+    p.D = head_dim;
+    p.r = n_head / n_head_kv;
+    p.act = act;
+    p.n_seq = n_seq;
+    int64_t total = 0, tok0 = 0;
+    for (int i = 0; i < n_seq; ++i) {
+        if (rows[i] < 0 || n_q[i] < 0) return KVC_EINVAL;
+        total += n_q[i];
+    }
+    if (total * p.r > INT32_MAX / 4 / p.Hk) return KVC_EINVAL;
+    plan_block(p, sms, rows, n_q, &tok0);
+    *tile_m = p.tile_m;
+    *items = p.n_items;
+    *part_rows = *tickets = 0;
+    *part_cap = part_rows_cap(sms);
+    for (int i = 0; i < n_seq; ++i) {
+        const BlockSeq &s = p.seq[i];
+        splits[i] = s.splits;
+        split_rows[i] = s.split_rows;
+        if (s.splits > 1 && s.tiles) {
+            *part_rows = std::max<int64_t>(*part_rows, (int64_t)s.part_row0 + (int64_t)s.tiles * p.Hk * s.splits * p.part_rows);
+            *tickets = std::max<int64_t>(*tickets, (int64_t)s.ticket0 + (int64_t)s.tiles * p.Hk);
+        }
+    }
+    return KVC_OK;
+}

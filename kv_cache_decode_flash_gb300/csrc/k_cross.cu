@@ -1,0 +1,659 @@
+// k_cross.cu - attention of a block of query tokens over cached rows
+// (kvc_attn_cross): every token t of a sequence attends over its leading
+// N_t = min(max(n_vis[t], 0), rows) cached rows,
+//   s_j = scale * q[t][h] . K_j,   lse = log sum_j exp(s_j),
+//   out = sum_j exp(s_j - lse) V_j        (j < N_t; 0 and -inf where N_t = 0),
+// query head h reading KV head h / r.
+//
+// A work item is one KV head, one tile of up to 64 query rows (tokens x query
+// heads of the group) and a part of the cached rows, walked in steps of 64.
+// A step's rows are turned into fp16 in shared memory once for all warps; the
+// products run on the tensor cores with fp32 sums and the softmax is the
+// online one, so no score leaves the registers.
+//   q8_0 and q4_0 codes are exact in fp16.  The scale of a 32-value block of K
+//   multiplies the block's own partial score in 32 bits; the scale of a block
+//   of V goes into the probabilities, P' = p * d * 2^(12 - E), E the exponent
+//   of the largest V scale met so far (the sums are rescaled when it grows),
+//   which keeps P' in the normal range of fp16 for scales of any size.
+//   A query row is normalised by a power of two (its largest magnitude comes
+//   to lie in [2^13, 2^14)), which is exact for f16 and bf16 queries; 32-bit
+//   queries and their probabilities are split into two fp16 parts (22 bits), so
+//   that 32-bit results keep 32-bit accuracy.  With 16-bit results P' is one
+//   fp16 value: its rounding (2^-12) is below the result's own.
+// Rows behind the sequence's last and rows that a token does not see take no
+// part, whatever they hold: scores are selected, not added to, and a
+// non-finite V value is kept out of the products (0 x inf is NaN) and put into
+// the result only of rows that give it weight.
+// Few query tiles: the cached rows are split over items, the partial sums are
+// joined in their order by the item that comes last (an arrival counter), so a
+// result does not depend on the order in which items finish.
+#include "block_attn.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace kvc {
+namespace {
+
+constexpr int THREADS = 128;
+constexpr int TM = CROSS_TILE_M, TN = CROSS_TILE_N;
+constexpr int E_MIN = -24; // exponent of the smallest fp16 scale
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t h2(float a, float b) {
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 f2(uint32_t u) { return __half22float2(*reinterpret_cast<__half2 *>(&u)); }
+
+// Four offset-binary codes (code + 128) to four halves: the byte becomes the
+// low mantissa of 1024, from which 1152 is taken (exact).
+__device__ __forceinline__ uint2 codes4(uint32_t w) {
+    const uint32_t k = 0x64646464u;
+    uint32_t lo = __byte_perm(w, k, 0x4140), hi = __byte_perm(w, k, 0x4342);
+    const __half2 c = __half2half2(__ushort_as_half(0x6480)); // 1152
+    __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&lo), c), b = __hsub2(*reinterpret_cast<__half2 *>(&hi), c);
+    return make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
+}
+// The low nibbles of four bytes to four halves code - 8.
+__device__ __forceinline__ uint2 nibbles4(uint32_t w) {
+    w &= 0x0f0f0f0fu;
+    const uint32_t k = 0x64646464u;
+    uint32_t lo = __byte_perm(w, k, 0x4140), hi = __byte_perm(w, k, 0x4342);
+    const __half2 c = __half2half2(__ushort_as_half(0x6408)); // 1032
+    __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&lo), c), b = __hsub2(*reinterpret_cast<__half2 *>(&hi), c);
+    return make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
+}
+// Whether either half of the pair is inf or NaN; those set to 0.
+__device__ __forceinline__ bool drop_nonfinite(uint32_t &u) {
+    const bool a = (u & 0x7c00u) == 0x7c00u, b = (u & 0x7c000000u) == 0x7c000000u;
+    if (a) u &= 0xffff0000u;
+    if (b) u &= 0x0000ffffu;
+    return a || b;
+}
+
+template <int D> struct Smem {
+    static constexpr int PITCH = D + 8; // halves: rows 16 bytes off a multiple of 128, so ldmatrix has no conflicts
+    __half qhi[TM][PITCH];
+    __half qlo[TM][PITCH];
+    __half k[TN][PITCH];
+    __half v[TN][PITCH];
+    float ks[D / 32][TN]; // block scales, by block
+    float vs[D / 32][TN];
+    int32_t row[TN];          // pool row of each row of the step, -1 past the end
+    float qscale[TM];         // score per unit of the normalised product, in log2
+    int32_t vis[TM];          // rows that the query row sees
+    float red[THREADS / 32];
+    float m[4][TM], l[4][TM]; // merge of warps that share query rows
+    uint32_t poison[TM][D / 16]; // two bits a value: +inf, -inf (both: NaN) received
+    uint8_t badrow[TN];
+    int32_t vis_max;
+    int32_t bad, any_bad;
+    int32_t last;
+};
+
+template <int KT> __device__ __forceinline__ constexpr int row_bytes(int D) {
+    return KT == KVC_F16 ? 2 * D : (KT == KVC_Q4_0 ? D / 2 : D);
+}
+
+// A step's rows of one tensor as fp16 in shared memory (codes without their scale); returns whether a
+// value of them is not finite (V only: such values are set to 0).
+template <int D, int T, bool V>
+__device__ __forceinline__ bool fill(__half (*dst)[Smem<D>::PITCH], const uint8_t *data, const int32_t *row,
+                                     uint8_t *badrow, int tid) {
+    constexpr int RB = row_bytes<T>(D), PIECES = RB / 16;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < TN * PIECES / THREADS; ++i) {
+        const int at = tid + i * THREADS, j = at / PIECES, c = at % PIECES;
+        const int32_t R = row[j];
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (R >= 0) u = *reinterpret_cast<const uint4 *>(data + (int64_t)R * RB + c * 16);
+        if constexpr (T == KVC_F16) {
+            if constexpr (V) {
+                bool b = drop_nonfinite(u.x);
+                b |= drop_nonfinite(u.y);
+                b |= drop_nonfinite(u.z);
+                b |= drop_nonfinite(u.w);
+                if (b) badrow[j] = 1;
+                bad |= b;
+            }
+            *reinterpret_cast<uint4 *>(&dst[j][c * 8]) = u;
+        } else if constexpr (T == KVC_Q8_0) {
+            const uint2 a = codes4(u.x), b = codes4(u.y), e = codes4(u.z), f = codes4(u.w);
+            *reinterpret_cast<uint4 *>(&dst[j][c * 16]) = make_uint4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<uint4 *>(&dst[j][c * 16 + 8]) = make_uint4(e.x, e.y, f.x, f.y);
+        } else {
+            // byte i of a 32-value block holds the codes i (low) and i + 16 (high)
+            uint2 a = nibbles4(u.x), b = nibbles4(u.y), e = nibbles4(u.z), f = nibbles4(u.w);
+            *reinterpret_cast<uint4 *>(&dst[j][c * 32]) = make_uint4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<uint4 *>(&dst[j][c * 32 + 8]) = make_uint4(e.x, e.y, f.x, f.y);
+            a = nibbles4(u.x >> 4), b = nibbles4(u.y >> 4), e = nibbles4(u.z >> 4), f = nibbles4(u.w >> 4);
+            *reinterpret_cast<uint4 *>(&dst[j][c * 32 + 16]) = make_uint4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<uint4 *>(&dst[j][c * 32 + 24]) = make_uint4(e.x, e.y, f.x, f.y);
+        }
+    }
+    return bad;
+}
+
+// A V value as stored (the rare path of values that are not finite).
+template <int D, int T>
+__device__ float stored_value(const uint8_t *data, const uint16_t *scales, int32_t R, int d) {
+    if constexpr (T == KVC_F16) {
+        return __half2float(reinterpret_cast<const __half *>(data)[(int64_t)R * D + d]);
+    } else {
+        const float s = __half2float(__ushort_as_half(scales[(int64_t)R * (D / QK) + d / QK]));
+        if constexpr (T == KVC_Q8_0) return (float)((int)data[(int64_t)R * D + d] - 128) * s;
+        const int b = d / QK, e = d % QK;
+        const uint8_t byte = data[(int64_t)R * (D / 2) + b * (QK / 2) + (e & 15)];
+        return (float)((int)(e < 16 ? byte & 15 : byte >> 4) - 8) * s;
+    }
+}
+
+// The values of row R that are not finite, marked in the two-bit words of a query row that gives it weight.
+template <int D, int T>
+__device__ __noinline__ void mark_poison(uint32_t *words, const uint8_t *data, const uint16_t *scales, int32_t R) {
+    for (int d = 0; d < D; ++d) {
+        const float x = stored_value<D, T>(data, scales, R, d);
+        if (fabsf(x) <= 3.4e38f) continue;
+        const uint32_t two = x > 0.f ? 1u : (x < 0.f ? 2u : 3u);
+        atomicOr(&words[d / 16], two << (2 * (d % 16)));
+    }
+}
+
+__device__ __forceinline__ float poisoned(float x, uint32_t two_bits) {
+    if (two_bits == 3) return __int_as_float(0x7fffffff);
+    if (two_bits == 0) return x;
+    return x + (two_bits == 1 ? __int_as_float(0x7f800000) : __int_as_float(0xff800000));
+}
+
+__device__ __forceinline__ void store2(void *out, int act, int64_t at, float a, float b) {
+    if (act == KVC_ACT_F32) {
+        *reinterpret_cast<float2 *>(reinterpret_cast<float *>(out) + at) = make_float2(a, b);
+    } else if (act == KVC_ACT_F16) {
+        *reinterpret_cast<__half2 *>(reinterpret_cast<__half *>(out) + at) = __floats2half2_rn(a, b);
+    } else {
+        *reinterpret_cast<__nv_bfloat162 *>(reinterpret_cast<__nv_bfloat16 *>(out) + at) = __floats2bfloat162_rn(a, b);
+    }
+}
+
+// WM: warps along the query rows (16 each); the 4 / WM warps of a row block
+// share a step's cached rows and are joined at the end.  LO: 32-bit queries.
+template <int D, int KT, int VT, int WM, bool LO>
+__global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant__ BlockParams p) {
+    constexpr int WN = 4 / WM, NC = TN / WN, NT = NC / 8, NB = D / QK;
+    constexpr int MROWS = 16 * WM;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Smem<D> &s = *reinterpret_cast<Smem<D> *>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int wm = warp % WM, wn = warp / WM, gid = lane >> 2, qc = lane & 3;
+
+    // the item: sequence, KV head, query tile, part of the rows
+    int si = 0;
+    {
+        int lo = 0, hi = p.n_seq - 1;
+        while (lo < hi) { // last sequence whose first item is <= ours (those without items share it: take the last)
+            const int mid = (lo + hi + 1) / 2;
+            if (p.seq[mid].item0 <= (int)blockIdx.x) lo = mid; else hi = mid - 1;
+        }
+        si = lo;
+    }
+    const BlockSeq q = p.seq[si];
+    const int local = (int)blockIdx.x - q.item0;
+    const int part = local % q.splits, gt = local / q.splits;
+    const int g = gt / q.tiles, tile = q.tiles - 1 - gt % q.tiles; // later tokens see more: they begin first
+    const int m_all = q.n_tok * p.r, m0 = tile * MROWS, mrows = min(MROWS, m_all - m0);
+
+    if (tid == 0) {
+        s.vis_max = 0;
+        s.any_bad = 0;
+        s.bad = 0;
+    }
+    __syncthreads();
+    // query rows: a warp each, normalised by a power of two and split
+    for (int m = warp; m < MROWS; m += THREADS / 32) {
+        float x[D / 32];
+        float top = 0.f;
+        int vis = 0;
+        if (m < mrows) {
+            const int t = (m0 + m) / p.r, j = (m0 + m) % p.r;
+            const int64_t tok = (int64_t)q.tok0 + t;
+            const int64_t at = (tok * p.H + (int64_t)g * p.r + j) * D + lane * (D / 32);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                if (p.act == KVC_ACT_F32)
+                    x[i] = reinterpret_cast<const float *>(p.q)[at + i];
+                else if (p.act == KVC_ACT_F16)
+                    x[i] = __half2float(reinterpret_cast<const __half *>(p.q)[at + i]);
+                else
+                    x[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.q)[at + i]);
+                top = fmaxf(top, fabsf(x[i]));
+            }
+            vis = p.n_vis ? min(max(p.n_vis[tok], 0), q.n_rows) : q.n_rows;
+        } else {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) x[i] = 0.f;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // top = f * 2^e, f in [1/2, 1): scaled by 2^(14 - e)
+        int e = 0;
+        if (top > 0.f && top < __int_as_float(0x7f800000)) frexpf(top, &e);
+        const float up = ldexpf(1.f, min(14 - e, 127)); // (subnormal rows: within 2^-127, their score is 0)
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const float y = x[i] * up;
+            const __half h = __float2half_rn(y);
+            s.qhi[m][lane * (D / 32) + i] = h;
+            if (LO) s.qlo[m][lane * (D / 32) + i] = __float2half_rn(__hisinf(h) ? 0.f : y - __half2float(h));
+        }
+        if (lane == 0) {
+            s.qscale[m] = p.scale_log2 / up;
+            s.vis[m] = vis;
+            if (vis > 0) atomicMax(&s.vis_max, vis);
+        }
+        for (int i = lane; i < D / 16; i += 32) s.poison[m][i] = 0;
+    }
+    __syncthreads();
+    const int r0 = part * q.split_rows;
+    const int r1 = min(r0 + q.split_rows, s.vis_max);
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
+    float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+    int E = VT == KVC_F16 ? 0 : E_MIN;
+    const int mrow = wm * 16 + gid;
+    const float qs[2] = {s.qscale[mrow], s.qscale[mrow + 8]};
+    const int vis[2] = {s.vis[mrow], s.vis[mrow + 8]};
+
+    for (int base = r0; base < r1; base += TN) {
+        // the step's rows; a page that the pool does not have is reported and its rows are left out
+        if (tid < TN) {
+            const int j = base + tid;
+            int32_t R = -1;
+            if (j < q.n_rows) {
+                const int64_t lr = (int64_t)q.off + j;
+                const int64_t pi = lr / p.P;
+                const int32_t page = pi < p.max_pages ? p.pt[(int64_t)q.id * p.max_pages + pi] : -1;
+                if (page >= 0 && page < p.n_pages)
+                    R = (int32_t)(((int64_t)page * p.Hk + g) * p.P + (lr - pi * p.P));
+                else
+                    atomicOr(p.err, ERR_BAD_PAGE);
+            }
+            s.row[tid] = R;
+            s.badrow[tid] = 0;
+        }
+        __syncthreads();
+        fill<D, KT, false>(s.k, p.kdata, s.row, nullptr, tid);
+        bool bad = fill<D, VT, true>(s.v, p.vdata, s.row, s.badrow, tid);
+        float top = 0.f;
+        if constexpr (KT != KVC_F16 || VT != KVC_F16) {
+            for (int i = tid; i < TN * NB; i += THREADS) {
+                const int j = i / NB, b = i % NB;
+                const int32_t R = s.row[j];
+                if constexpr (KT != KVC_F16)
+                    s.ks[b][j] = R >= 0 ? __half2float(__ushort_as_half(p.ks[(int64_t)R * NB + b])) : 0.f;
+                if constexpr (VT != KVC_F16) {
+                    float d = R >= 0 ? __half2float(__ushort_as_half(p.vs[(int64_t)R * NB + b])) : 0.f;
+                    if (!(fabsf(d) <= 65504.f)) {
+                        d = 0.f;
+                        s.badrow[j] = 1;
+                        bad = true;
+                    }
+                    s.vs[b][j] = d;
+                    top = fmaxf(top, fabsf(d));
+                }
+            }
+#pragma unroll
+            for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            if (lane == 0) s.red[warp] = top;
+        }
+        if (bad) s.bad = 1;
+        __syncthreads();
+        float grow = 1.f; // factor of the sums so far when the range exponent grows
+        if constexpr (VT != KVC_F16) {
+            top = fmaxf(fmaxf(s.red[0], s.red[1]), fmaxf(s.red[2], s.red[3]));
+            int e = E_MIN;
+            if (top > 0.f) e = max(E_MIN, ilogbf(top));
+            if (e > E) {
+                grow = ldexpf(1.f, max(E - e, -126));
+                E = e;
+            }
+        }
+
+        // scores of 16 query rows x NC cached rows
+        float sc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc[n][k] = 0.f;
+        const uint32_t qa = smem_u32(&s.qhi[wm * 16 + (lane & 15)][(lane >> 4) * 8]);
+        const uint32_t ql = smem_u32(&s.qlo[wm * 16 + (lane & 15)][(lane >> 4) * 8]);
+        const uint32_t ka = smem_u32(&s.k[wn * NC + (lane & 7) + ((lane >> 4) << 3)][((lane >> 3) & 1) * 8]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float t[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) t[n][k] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t a[4], al[4];
+                ldsm4(a, qa + (b * 32 + k * 16) * 2);
+                if (LO) ldsm4(al, ql + (b * 32 + k * 16) * 2);
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+                    uint32_t kb[4];
+                    ldsm4(kb, ka + n * 8 * Smem<D>::PITCH * 2 + (b * 32 + k * 16) * 2);
+                    mma(t[n], a, kb[0], kb[1]);
+                    mma(t[n + 1], a, kb[2], kb[3]);
+                    if (LO) {
+                        mma(t[n], al, kb[0], kb[1]);
+                        mma(t[n + 1], al, kb[2], kb[3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if constexpr (KT != KVC_F16) {
+                    const float2 d = *reinterpret_cast<const float2 *>(&s.ks[b][wn * NC + n * 8 + qc * 2]);
+                    sc[n][0] = fmaf(t[n][0], d.x, sc[n][0]);
+                    sc[n][1] = fmaf(t[n][1], d.y, sc[n][1]);
+                    sc[n][2] = fmaf(t[n][2], d.x, sc[n][2]);
+                    sc[n][3] = fmaf(t[n][3], d.y, sc[n][3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sc[n][k] += t[n][k];
+                }
+            }
+        }
+        // scale, mask, online softmax
+        float nm[2] = {mx[0], mx[1]};
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int jt = wn * NC + n * 8 + qc * 2 + (k & 1);
+                const float x = sc[n][k] * qs[k >> 1];
+                sc[n][k] = base + jt < vis[k >> 1] && s.row[jt] >= 0 ? x : -INFINITY;
+                nm[k >> 1] = fmaxf(nm[k >> 1], sc[n][k]);
+            }
+        float al[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            nm[h] = fmaxf(nm[h], __shfl_xor_sync(0xffffffffu, nm[h], 1));
+            nm[h] = fmaxf(nm[h], __shfl_xor_sync(0xffffffffu, nm[h], 2));
+            const float use = nm[h] == -INFINITY ? 0.f : nm[h];
+            al[h] = ex2(mx[h] - use); // nothing yet: ex2(-inf) = 0
+            mx[h] = nm[h];
+            float add = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float e = ex2(sc[n][2 * h + k] - use);
+                    sc[n][2 * h + k] = e;
+                    add += e;
+                }
+            sum[h] = sum[h] * al[h] + add;
+            al[h] *= grow;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            o[i][0] *= al[0];
+            o[i][1] *= al[0];
+            o[i][2] *= al[1];
+            o[i][3] *= al[1];
+        }
+        if (s.bad) { // a V value of this step is not finite: it goes to the rows that give it weight
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int jt = wn * NC + n * 8 + qc * 2 + (k & 1);
+                    if (s.badrow[jt] && sc[n][k] > 0.f)
+                        mark_poison<D, VT>(s.poison[mrow + 8 * (k >> 1)], p.vdata, p.vs, s.row[jt]);
+                }
+            s.any_bad = 1;
+        }
+        // P V: a 16-row slab of the step at a time, a 32-value block of V at a time
+        const float fe = VT == KVC_F16 ? 4096.f : ldexpf(1.f, 12 - E);
+#pragma unroll
+        for (int ks = 0; ks < NC / 16; ++ks) {
+            float pr[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                pr[k] = sc[2 * ks][k] * fe;
+                pr[4 + k] = sc[2 * ks + 1][k] * fe;
+            }
+            const uint32_t va = smem_u32(&s.v[wn * NC + ks * 16 + (lane & 15)][(lane >> 4) * 8]);
+            uint32_t a[4], alo[4];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                if (VT != KVC_F16 || b == 0) {
+                    float y[8];
+                    if constexpr (VT != KVC_F16) {
+                        const int j = wn * NC + ks * 16 + qc * 2;
+                        const float2 d0 = *reinterpret_cast<const float2 *>(&s.vs[b][j]);
+                        const float2 d1 = *reinterpret_cast<const float2 *>(&s.vs[b][j + 8]);
+                        y[0] = pr[0] * d0.x, y[1] = pr[1] * d0.y, y[2] = pr[2] * d0.x, y[3] = pr[3] * d0.y;
+                        y[4] = pr[4] * d1.x, y[5] = pr[5] * d1.y, y[6] = pr[6] * d1.x, y[7] = pr[7] * d1.y;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) y[k] = pr[k];
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        a[k] = h2(y[2 * k], y[2 * k + 1]);
+                        if (LO) {
+                            const float2 f = f2(a[k]);
+                            alo[k] = h2(y[2 * k] - f.x, y[2 * k + 1] - f.y);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < 4; n += 2) {
+                    uint32_t vb[4];
+                    ldsm4t(vb, va + (b * 32 + n * 8) * 2);
+                    mma(o[b * 4 + n], a, vb[0], vb[1]);
+                    mma(o[b * 4 + n + 1], a, vb[2], vb[3]);
+                    if (LO) {
+                        mma(o[b * 4 + n], alo, vb[0], vb[1]);
+                        mma(o[b * 4 + n + 1], alo, vb[2], vb[3]);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if (tid == 0) s.bad = 0;
+    }
+
+    // the quad's sums, then the values themselves
+    const float back = VT == KVC_F16 ? 1.f / 4096.f : ldexpf(1.f, E - 12);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+        sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][k] *= back;
+    if constexpr (WN > 1) {
+        // warps that share query rows: joined in warp order by the first of them, through the tiles' memory
+        __syncthreads();
+        float *buf = reinterpret_cast<float *>(&s.k[0][0]); // [WN - 1][MROWS][D]
+        static_assert(sizeof(float) * (WN - 1) * MROWS * D <= sizeof(__half) * 2 * TN * Smem<D>::PITCH, "merge buffer");
+        if (qc == 0)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                s.m[wn][mrow + 8 * h] = mx[h];
+                s.l[wn][mrow + 8 * h] = sum[h];
+            }
+        if (wn > 0)
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<float2 *>(&buf[((wn - 1) * MROWS + mrow + 8 * h) * D + i * 8 + qc * 2]) =
+                        make_float2(o[i][2 * h], o[i][2 * h + 1]);
+        __syncthreads();
+        if (wn == 0)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int m = mrow + 8 * h;
+                float M = mx[h];
+#pragma unroll
+                for (int w = 1; w < WN; ++w) M = fmaxf(M, s.m[w][m]);
+                const float use = M == -INFINITY ? 0.f : M;
+                const float f0 = ex2(mx[h] - use);
+                float L = sum[h] * f0;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    o[i][2 * h] *= f0;
+                    o[i][2 * h + 1] *= f0;
+                }
+#pragma unroll
+                for (int w = 1; w < WN; ++w) {
+                    const float f = ex2(s.m[w][m] - use);
+                    L += s.l[w][m] * f;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        const float2 x =
+                            *reinterpret_cast<const float2 *>(&buf[((w - 1) * MROWS + m) * D + i * 8 + qc * 2]);
+                        o[i][2 * h] = fmaf(x.x, f, o[i][2 * h]);
+                        o[i][2 * h + 1] = fmaf(x.y, f, o[i][2 * h + 1]);
+                    }
+                }
+                mx[h] = M;
+                sum[h] = L;
+            }
+    }
+    const bool bad = s.any_bad != 0;
+    const bool whole = q.splits == 1;
+    const int prow = q.part_row0 + local * p.part_rows; // the item's partial rows
+    if (wn == 0)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int m = mrow + 8 * h;
+            if (m >= mrows) continue;
+            if (bad)
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int d = i * 8 + qc * 2 + k;
+                        o[i][2 * h + k] = poisoned(o[i][2 * h + k], (s.poison[m][d / 16] >> (2 * (d % 16))) & 3u);
+                    }
+            if (whole) {
+                const int t = (m0 + m) / p.r, j = (m0 + m) % p.r;
+                const int64_t head = ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
+                const float inv = sum[h] == 0.f ? 0.f : 1.f / sum[h];
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    store2(p.out, p.act, head * D + i * 8 + qc * 2, o[i][2 * h] * inv, o[i][2 * h + 1] * inv);
+                if (p.lse && qc == 0)
+                    p.lse[head] = sum[h] == 0.f ? -INFINITY : mx[h] * 0.6931471805599453f + logf(sum[h]);
+            } else {
+                float *dst = p.part + (int64_t)(prow + m) * D;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    *reinterpret_cast<float2 *>(dst + i * 8 + qc * 2) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+                if (qc == 0)
+                    *reinterpret_cast<float2 *>(p.part + p.part_cap * D + 2 * (int64_t)(prow + m)) =
+                        make_float2(mx[h], sum[h]);
+            }
+        }
+    if (whole) return;
+
+    // the last part to arrive joins the tile's parts in their order
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        const int n = atomicAdd(&p.tickets[q.ticket0 + gt], 1);
+        s.last = n == q.splits - 1;
+        if (s.last) p.tickets[q.ticket0 + gt] = 0;
+    }
+    __syncthreads();
+    if (!s.last) return;
+    __threadfence();
+    const int first = q.part_row0 + gt * q.splits * p.part_rows;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.part + p.part_cap * D);
+    for (int at = tid; at < mrows * (D / 2); at += THREADS) {
+        const int m = at / (D / 2), d = (at % (D / 2)) * 2;
+        float M = -INFINITY;
+        for (int i = 0; i < q.splits; ++i) M = fmaxf(M, __ldcg(&ml[first + i * p.part_rows + m]).x);
+        const float use = M == -INFINITY ? 0.f : M;
+        float L = 0.f, x = 0.f, y = 0.f;
+        for (int i = 0; i < q.splits; ++i) {
+            const int row = first + i * p.part_rows + m;
+            const float2 c = __ldcg(&ml[row]);
+            const float f = ex2(c.x - use);
+            if (c.y == 0.f || (f == 0.f && c.y == c.y)) continue; // nothing seen there, or nothing left of it
+            L = fmaf(c.y, f, L);
+            const float2 v = __ldcg(reinterpret_cast<const float2 *>(p.part + (int64_t)row * D + d));
+            x = fmaf(v.x, f, x);
+            y = fmaf(v.y, f, y);
+        }
+        const int t = (m0 + m) / p.r, j = (m0 + m) % p.r;
+        const int64_t head = ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        store2(p.out, p.act, head * D + d, x * inv, y * inv);
+        if (p.lse && d == 0) p.lse[head] = L == 0.f ? -INFINITY : M * 0.6931471805599453f + logf(L);
+    }
+}
+
+template <int D, int KT, int VT, int WM, bool LO> cudaError_t go(const BlockParams &p, cudaStream_t st) {
+    auto k = cross_kernel<D, KT, VT, WM, LO>;
+    const int bytes = (int)sizeof(Smem<D>);
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    k<<<(unsigned)p.n_items, THREADS, bytes, st>>>(p);
+    return cudaGetLastError();
+}
+template <int D, int KT, int VT> cudaError_t pick(const BlockParams &p, bool narrow, cudaStream_t st) {
+    const bool lo = p.act == KVC_ACT_F32;
+    if (narrow) return lo ? go<D, KT, VT, 1, true>(p, st) : go<D, KT, VT, 1, false>(p, st);
+    return lo ? go<D, KT, VT, 4, true>(p, st) : go<D, KT, VT, 4, false>(p, st);
+}
+
+} // namespace
+
+cudaError_t launch_cross(int type_k, int type_v, const BlockParams &p, bool narrow, cudaStream_t st) {
+    if (p.n_items <= 0) return cudaSuccess;
+    if (p.D == 64) {
+        if (type_k == KVC_F16) return pick<64, KVC_F16, KVC_F16>(p, narrow, st);
+        return pick<64, KVC_Q8_0, KVC_Q8_0>(p, narrow, st);
+    }
+    if (type_k == KVC_F16) return pick<128, KVC_F16, KVC_F16>(p, narrow, st);
+    if (type_v == KVC_Q4_0) return pick<128, KVC_Q8_0, KVC_Q4_0>(p, narrow, st);
+    return pick<128, KVC_Q8_0, KVC_Q8_0>(p, narrow, st);
+}
+
+} // namespace kvc

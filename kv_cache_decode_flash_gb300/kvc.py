@@ -22,6 +22,7 @@ KVC_EFORMAT, KVC_ECUDA, KVC_ETIMEDOUT, KVC_EINTERNAL = -5, -6, -7, -8
 KVC_F16, KVC_Q4_0, KVC_Q8_0 = 1, 2, 8
 KVC_DEVICE, KVC_HOST_PINNED, KVC_SPLIT_HEADS = 0, 1, 2
 KVC_ROPE_NEOX, KVC_ROPE_NORM = 0, 1
+KVC_ACT_F32, KVC_ACT_F16, KVC_ACT_BF16 = 0, 1, 2
 
 
 class kvc_params(C.Structure):
@@ -77,6 +78,7 @@ def load():
         "kvc_append": (i32, [p, i32, i32, i32, i32, p, p, p]),
         "kvc_attn_decode": (i32, [p, i32, i32, p, p, p, C.c_float, p]),
         "kvc_decode_step": (i32, [p, i32, i32, p, p, p, p, p, p, C.c_float, p]),
+        "kvc_attn_cross": (i32, [p, i32, i32, p, p, i32, p, p, p, p, C.c_float, p]),
         "kvc_seq_rm": (i32, [p, i32, i32, i32]),
         "kvc_seq_cp": (i32, [p, i32, i32, i32, i32]),
         "kvc_seq_add": (i32, [p, i32, i32, i32, i32]),
@@ -96,6 +98,7 @@ def load():
         "kvc_debug_chunk_plan": (i32, [i32, i32, i32, i32, i32, i32, i32, i32, p, C.POINTER(C.c_int32),
                                        C.POINTER(C.c_int32)]),
         "kvc_debug_chunk_plan_seq": (i32, [i32, i32, i32, i32, i32, i32, i32, i32, p, p, C.POINTER(C.c_int32)]),
+        "kvc_debug_block_plan": (i32, [i32] * 6 + [p] * 9),
         "kvc_debug_select_rows": (i32, [p, i32, i32, i32, i32, p, C.POINTER(C.c_int64), C.POINTER(C.c_int64),
                                         C.POINTER(C.c_int32)]),
         "kvc_set_timeout_ms": (i32, [p, i32]),
@@ -193,6 +196,39 @@ def kvc_decode_step(ctx, layer, seq_ids, pos, k, v, q, out, kq_scale, stream=Non
     ps = (C.c_int32 * len(pos))(*[int(x) for x in pos])
     _check(ctx, load().kvc_decode_step(ctx, layer, len(seq_ids), ids, ps, _addr(k), _addr(v), _addr(q), _addr(out),
                                        float(kq_scale), _stream(stream, device)))
+
+
+def _act(q):
+    """kvc_act of a query tensor."""
+    act = {"torch.float32": KVC_ACT_F32, "torch.float16": KVC_ACT_F16, "torch.bfloat16": KVC_ACT_BF16}.get(str(q.dtype))
+    if act is None:
+        raise KvcError(KVC_EINVAL, "queries must be float32, float16 or bfloat16, not %s" % q.dtype)
+    return act
+
+
+def _block_tensor(name, t, device, dtype, numel):
+    """Refuse a tensor that the library would misread (it sees an address only)."""
+    if not (hasattr(t, "is_cuda") and t.is_cuda and t.device.index == device):
+        raise KvcError(KVC_EINVAL, "%s must be a tensor on cuda:%d" % (name, device))
+    if str(t.dtype) != dtype:
+        raise KvcError(KVC_EINVAL, "%s must be %s, not %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise KvcError(KVC_EINVAL, "%s must be contiguous" % name)
+    if t.numel() < numel:
+        raise KvcError(KVC_EINVAL, "%s holds %d values, %d are needed" % (name, t.numel(), numel))
+
+
+def _block(seq_ids, n_q):
+    if len(seq_ids) != len(n_q):
+        raise KvcError(KVC_EINVAL, "one token count per sequence")
+    n = len(seq_ids)
+    return (C.c_int32 * n)(*[int(s) for s in seq_ids]), (C.c_int32 * n)(*[int(t) for t in n_q])
+
+
+def kvc_attn_cross(ctx, layer, seq_ids, n_q, act, q, out, kq_scale, lse=None, n_vis=None, stream=None, device=0):
+    ids, nq = _block(seq_ids, n_q)
+    _check(ctx, load().kvc_attn_cross(ctx, layer, len(seq_ids), ids, nq, int(act), _addr(q), _addr(out), _addr(lse),
+                                      _addr(n_vis), float(kq_scale), _stream(stream, device)))
 
 
 class kvc_trace_event(C.Structure):
@@ -359,6 +395,21 @@ def kvc_debug_chunk_plan_seq(type_, head_dim, n_head, n_head_kv, sms, occ, occ2,
     return list(out), cfg.value
 
 
+def kvc_debug_block_plan(n_head, n_head_kv, head_dim, act, sms, rows, n_q):
+    """How a block attention launch cuts its sequences, without a context or a GPU: a dict of
+    tile_m, splits, split_rows, items, part_rows, part_cap and tickets."""
+    n = len(rows)
+    r, t = (C.c_int32 * n)(*[int(x) for x in rows]), (C.c_int32 * n)(*[int(x) for x in n_q])
+    sp, sr, tm = (C.c_int32 * n)(), (C.c_int32 * n)(), C.c_int32()
+    big = [C.c_int64() for _ in range(4)]
+    st = load().kvc_debug_block_plan(n_head, n_head_kv, head_dim, act, sms, n, r, t, C.byref(tm), sp, sr,
+                                     *[C.byref(b) for b in big])
+    if st != KVC_OK:
+        raise KvcError(st, "bad block-plan arguments")
+    return {"tile_m": tm.value, "splits": list(sp), "split_rows": list(sr),
+            **{k: b.value for k, b in zip(("items", "part_rows", "part_cap", "tickets"), big)}}
+
+
 def kvc_debug_select_rows(pos, p0, p1, linear=False):
     """The rows a sequence operation selects for positions [p0, p1) of a
     sequence holding `pos`, without a context or a GPU: (rows, first,
@@ -421,6 +472,25 @@ class KVCache:
         device, at positions pos) and attend with q ([n_seq][n_head][head_dim]) into out;
         one launch on device-resident contexts (kvc_decode_step)."""
         kvc_decode_step(self.ctx, layer, seq_ids, pos, k, v, q, out, kq_scale, stream, self.device)
+
+    def attn_cross(self, layer, seq_ids, n_q, q, out, kq_scale, lse=None, n_vis=None, stream=None):
+        """Attention of a block of tokens (n_q[i] of sequence seq_ids[i], packed) over the
+        cached rows: q, out [T][n_head][head_dim] (float32, float16 or bfloat16), lse [T][n_head]
+        fp32 or None, n_vis [T] int32 (leading rows that a token sees) or None (all)."""
+        act, total = _act(q), sum(int(t) for t in n_q)
+        self._block_io(q, out, lse, n_vis, total)
+        kvc_attn_cross(self.ctx, layer, seq_ids, n_q, act, q, out, kq_scale, lse, n_vis, stream, self.device)
+
+    def _block_io(self, q, out, lse, n_vis, total):
+        p = self.params
+        size = total * p.n_head * p.head_dim
+        _block_tensor("q", q, self.device, str(q.dtype), size)
+        if out is not None:
+            _block_tensor("out", out, self.device, str(q.dtype), size)
+        if lse is not None:
+            _block_tensor("lse", lse, self.device, "torch.float32", total * p.n_head)
+        if n_vis is not None:
+            _block_tensor("n_vis", n_vis, self.device, "torch.int32", total)
 
     def seq_rm(self, seq, p0, p1):
         kvc_seq_rm(self.ctx, seq, p0, p1)
