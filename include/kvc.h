@@ -227,6 +227,24 @@ typedef enum kvc_act { KVC_ACT_F32 = 0, KVC_ACT_F16 = 1, KVC_ACT_BF16 = 2 } kvc_
 int kvc_attn_cross(kvc_ctx *c, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_q, int act,
                    const void *q, void *out, float *lse, const int32_t *n_vis, float kq_scale, void *stream);
 
+/* Accumulate the attention weight that the cached rows of one layer receive
+ * from a block of query tokens (the statistic behind evicting rows by
+ * accumulated attention; see kvc_seq_evict_weight): for sequence entry i, KV
+ * head g and row j
+ *   w[i][g][j] += sum over the entry's tokens t with j < N_t and the query
+ *                 heads h of g:  exp(kq_scale * q[t][h] . K_j - lse[t][h]),
+ * seq_ids, n_q, act, q, n_vis, kq_scale and N_t as for kvc_attn_cross, and lse
+ * (device fp32 [T][n_head]) as that call wrote it for these tokens and rows.
+ * w: device fp32 [n_seq][n_head_kv][w_stride], w_stride at least the rows of
+ * every sequence; entries behind a sequence's rows are left as they are.  An
+ * id may come more than once (each entry has its own accumulators).  The order of the
+ * sums is fixed: results are bitwise repeatable.  32-bit accuracy for every type
+ * of q.  The call only enqueues work on `stream`; no work space.
+ * Device-resident contexts only.  Errors: KVC_EINVAL, KVC_ECUDA. */
+int kvc_attn_weight(kvc_ctx *c, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_q, int act,
+                    const void *q, const float *lse, const int32_t *n_vis, float kq_scale, float *w,
+                    int64_t w_stride, void *stream);
+
 /* Remove the rows of `seq` whose position is in [p0, p1), in every layer
  * (MemorySeqRemove, [COLD] section llama - KV-byte offload; the context
  * shift's discard, [F5] section M1).  Rows after the removed ones keep their
@@ -251,6 +269,25 @@ int kvc_seq_cp(kvc_ctx *c, int src, int dst, int p0, int p1);
  * and rounded to f16.  V is untouched.  delta == 0 is a no-op.
  * Errors: KVC_EINVAL, KVC_ERANGE (a position would leave [0, INT32_MAX]). */
 int kvc_seq_add(kvc_ctx *c, int seq, int p0, int p1, int delta);
+
+/* Evict the rows of least accumulated attention weight: among the rows of
+ * `seq` whose position is in [p0, p1) the n_remove ones of smallest weight
+ * (all of them if they are fewer) leave every layer and head.  Row j's weight
+ * is w[0][j] + w[1][j] + ... over the KV heads, summed in that order in fp32;
+ * of equal weights the lower row goes first, a NaN counts as above every number.
+ * Ranges protect rows by position: the first tokens below p0, recent ones from p1 on.
+ * The places are filled from the end: with n' rows left, the rows kept among
+ * the last ones (row n' on) move, in row order, into the places of the removed
+ * rows below n', positions and stored bytes with them; rows below n' that stay
+ * do not move.  So row order is no longer position order (kvc_seq_positions has
+ * it); no operation here asks for that, and a token appended later still sees
+ * all of them as its leading rows.  Positions do not change (kvc_seq_add closes gaps).
+ * w: device fp32 [n_head_kv][w_stride], w_stride at least the sequence's rows: the
+ * weights move with their rows, and w[g][n' .. n) becomes 0, for rows to come.
+ * *n_removed: rows removed.  Synchronous, like the other sequence operations.
+ * Errors: KVC_EINVAL, KVC_ENOMEM, KVC_ECUDA. */
+int kvc_seq_evict_weight(kvc_ctx *c, int seq, int p0, int p1, int32_t n_remove, float *w, int64_t w_stride,
+                         int32_t *n_removed);
 
 /* Export the rows of `seq` with position in [p0, p1) (in row order) as bytes
  * (StateSeqGetData, [COLD] section llama - KV-byte offload: evicted KV is

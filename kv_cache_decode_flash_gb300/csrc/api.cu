@@ -2,6 +2,7 @@
 // metadata of sequences, pages and positions) and the sequence and state
 // operations.  The host-resident transport lives in transport.cu.
 #include "ctx.h"
+#include "evict.h"
 
 #include <cuda_fp16.h>
 
@@ -458,6 +459,7 @@ void kvc_destroy(kvc_ctx *cc) {
     cudaFree(c->block_part);
     cudaFree(c->err_dev);
     if (c->err_host) cudaFreeHost(c->err_host);
+    if (c->gone_host) cudaFreeHost(c->gone_host);
     if (c->up_host) cudaFreeHost(c->up_host);
     for (uint8_t *p : c->up_retired) cudaFreeHost(p);
     cudaFree(c->staging);
@@ -1233,6 +1235,96 @@ int kvc_seq_evict_window(kvc_ctx *cc, int seq, int layer, int n_keep, int n_disc
     if ((rc = kvc_seq_rm(cc, seq, first, last + 1))) return rc;
     if ((rc = kvc_seq_add(cc, seq, last + 1, -1, -(last + 1 - first)))) return rc;
     *p0 = first;
+    return KVC_OK;
+}
+
+int kvc_seq_evict_weight(kvc_ctx *cc, int seq, int p0, int p1, int32_t n_remove, float *w, int64_t w_stride,
+                         int32_t *n_removed) {
+    if (!cc) return KVC_EINVAL;
+    Ctx *c = reinterpret_cast<Ctx *>(cc);
+    if (c->host) return c->fail(KVC_EINVAL, "sequence operations need a device-resident context");
+    if (seq < 0 || seq >= (int)c->seqs.size()) return c->fail(KVC_EINVAL, "sequence id out of range");
+    if (n_remove < 0 || !n_removed) return c->fail(KVC_EINVAL, "n_remove must not be negative, n_removed non-null");
+    Seq &q = c->seqs[(size_t)seq];
+    if (!q.synced()) return c->fail(KVC_EINVAL, "layers are not in sync (a step's appends are incomplete)");
+    if (!w || ((uintptr_t)w & 3)) return c->fail(KVC_EINVAL, "w must be non-null and 4-byte aligned");
+    if (w_stride < q.n) return c->fail(KVC_EINVAL, "w_stride is below the sequence's rows");
+    *n_removed = 0;
+    int64_t a, b;
+    norm_range(p0, p1, a, b);
+    RowSel sel;
+    select_rows(q, a, b, sel);
+    const int64_t k = std::min<int64_t>(n_remove, sel.count);
+    if (k == 0) return KVC_OK;
+    int rc = enter_sync(c);
+    if (rc) return rc;
+    auto al = [](int64_t x) { return (x + 255) / 256 * 256; };
+    const int64_t o_gone = al(sel.count * 4), o_pairs = o_gone + al(k * 4), o_rows = o_pairs + al(k * 8);
+    if ((rc = ensure_staging(c, o_rows + (sel.contiguous ? 0 : al(sel.count * 4))))) return rc;
+    if (k > c->gone_cap) {
+        if (!take_alloc(c)) return c->fail(KVC_ENOMEM, "injected allocation failure: removed rows");
+        int32_t *h = nullptr;
+        const int64_t cap = std::max<int64_t>(k, 1024);
+        if (cudaMallocHost((void **)&h, (size_t)cap * 4) != cudaSuccess) {
+            cudaGetLastError();
+            return c->fail(KVC_ENOMEM, "cudaMallocHost failed for the removed rows");
+        }
+        if (c->gone_host) cudaFreeHost(c->gone_host);
+        c->gone_host = h;
+        c->gone_cap = cap;
+    }
+    EvictArgs e;
+    std::memset(&e, 0, sizeof(e));
+    e.n = q.n;
+    e.n_cand = (int32_t)sel.count;
+    e.first = (int32_t)sel.first;
+    if (!sel.contiguous) {
+        std::vector<int32_t> rows(sel.idx.begin(), sel.idx.end());
+        if ((rc = upload(c, c->staging + o_rows, rows.data(), (int64_t)rows.size() * 4))) return rc;
+        e.rows = reinterpret_cast<const int32_t *>(c->staging + o_rows);
+    }
+    e.n_remove = (int32_t)k;
+    e.w = w;
+    e.w_stride = w_stride;
+    e.keys = reinterpret_cast<uint32_t *>(c->staging);
+    e.gone = reinterpret_cast<int32_t *>(c->staging + o_gone);
+    e.pairs = reinterpret_cast<int2 *>(c->staging + o_pairs);
+    e.pt = c->pt_dev + (int64_t)seq * c->max_pages;
+    e.pt_len = c->max_pages;
+    e.n_pages = c->n_pages;
+    e.off = q.off;
+    e.P = c->P;
+    e.Hk = c->Hk;
+    e.L = c->L;
+    const RunCopyArgs pools = pool_args(c);
+    for (int i = 0; i < 4; ++i) {
+        e.base[i] = pools.base[i];
+        e.rowb[i] = pools.rowb[i];
+    }
+    e.pool_rows = c->pool_rows;
+    e.err = c->err_dev;
+    if ((rc = upload_pages(c, seq))) return rc;
+    cudaError_t err = launch_evict(e, c->st);
+    if (err != cudaSuccess) return cuda_fail(c, err, "eviction kernels");
+    KVC_CU(c, cudaMemcpyAsync(c->gone_host, e.gone, (size_t)k * 4, cudaMemcpyDeviceToHost, c->st));
+    if ((rc = wait_internal(c))) return rc;
+    // the same moves in the host's positions: removed rows below the new end take the kept rows behind it, in order
+    const int32_t left = q.n - (int32_t)k;
+    int64_t hole = 0, tail = 0;
+    while (tail < k && c->gone_host[tail] < left) ++tail;
+    for (int32_t j = left; j < q.n; ++j) {
+        if (tail < k && c->gone_host[tail] == j) {
+            ++tail;
+            continue;
+        }
+        q.pos[(size_t)c->gone_host[hole++]] = q.pos[(size_t)j];
+    }
+    q.n = left;
+    q.pos.resize((size_t)left);
+    q.linear = consecutive(q.pos.data(), q.n);
+    for (auto &f : q.lfill) f = q.n;
+    release_tail_pages(c, q);
+    *n_removed = (int32_t)k;
     return KVC_OK;
 }
 

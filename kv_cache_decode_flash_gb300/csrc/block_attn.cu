@@ -1,5 +1,5 @@
 // block_attn.cu - host side of the operators over a block of query tokens
-// (kvc_attn_cross): checks, the split of the cached rows over work items, the
+// (kvc_attn_cross, kvc_attn_weight): checks, the split of the cached rows over work items, the
 // work space and the launches.
 #include "block_attn.h"
 #include "ctx.h"
@@ -220,6 +220,58 @@ extern "C" int kvc_attn_cross(kvc_ctx *cc, int layer, int n_seq, const int32_t *
         p.tickets = reinterpret_cast<int32_t *>(c->block_part + cap * (c->D + 2));
         cudaError_t e = launch_cross(c->tk, c->tv, p, narrow, st);
         if (e != cudaSuccess) return cuda_fail(c, e, "block attention kernel");
+    }
+    return KVC_OK;
+}
+
+extern "C" int kvc_attn_weight(kvc_ctx *cc, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_q, int act,
+                               const void *q, const float *lse, const int32_t *n_vis, float kq_scale, float *w,
+                               int64_t w_stride, void *stream) {
+    if (!cc) return KVC_EINVAL;
+    Ctx *c = reinterpret_cast<Ctx *>(cc);
+    int64_t total = 0;
+    int rc = block_check(c, layer, n_seq, seq_ids, n_q, act, q, kq_scale, &total);
+    if (rc) return rc;
+    for (int i = 0; i < n_seq; ++i)
+        if (w_stride < c->seqs[(size_t)seq_ids[i]].lfill[(size_t)layer])
+            return c->fail(KVC_EINVAL, "w_stride is below the rows of a sequence");
+    if (total == 0) return KVC_OK;
+    if (!lse || !w) return c->fail(KVC_EINVAL, "lse and w must be non-null");
+    if (((uintptr_t)lse | (uintptr_t)n_vis | (uintptr_t)w) & 3)
+        return c->fail(KVC_EINVAL, "lse, n_vis and w must be 4-byte aligned");
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    KVC_CU(c, cudaSetDevice(c->dev));
+    int64_t tok0 = 0;
+    for (int base = 0; base < n_seq; base += MAX_SEQ_PER_LAUNCH) {
+        BlockParams p;
+        block_params(c, layer, kq_scale, act, p);
+        p.q = q;
+        p.lse = const_cast<float *>(lse); // only read
+        p.n_vis = n_vis;
+        p.w = w;
+        p.w_stride = w_stride;
+        p.n_seq = std::min(MAX_SEQ_PER_LAUNCH, n_seq - base);
+        int32_t most = 0;
+        int64_t item = 0;
+        for (int i = 0; i < p.n_seq; ++i) {
+            BlockSeq &s = p.seq[i];
+            const Seq &sq = c->seqs[(size_t)seq_ids[base + i]];
+            s.id = seq_ids[base + i];
+            s.off = sq.off;
+            s.n_rows = sq.lfill[(size_t)layer];
+            s.tok0 = (int32_t)tok0;
+            s.n_tok = n_q[base + i];
+            s.w_index = base + i;
+            s.splits = std::max(1, (s.n_rows + CROSS_TILE_N - 1) / CROSS_TILE_N);
+            s.item0 = (int32_t)item;
+            if (s.n_tok > 0 && s.n_rows > 0) item += (int64_t)s.splits * c->Hk;
+            if (item > INT32_MAX) return c->fail(KVC_EINVAL, "too many rows in one block");
+            tok0 += s.n_tok;
+            most = std::max(most, s.n_tok);
+        }
+        p.n_items = (int32_t)item;
+        cudaError_t e = launch_weight(c->tk, p, (int64_t)most * c->r <= 16, st);
+        if (e != cudaSuccess) return cuda_fail(c, e, "row weight kernel");
     }
     return KVC_OK;
 }

@@ -59,4 +59,7 @@ constexpr int CROSS_TILE_N = 64; // cached rows of a step
 // 16 (one tensor-core row block), so the warps share the cached rows instead.
 cudaError_t launch_cross(int type_k, int type_v, const BlockParams &p, bool narrow, cudaStream_t st);
 
+// The rows' weights: splits of a sequence are its steps of CROSS_TILE_N rows, items (KV head, step).
+cudaError_t launch_weight(int type_k, const BlockParams &p, bool narrow, cudaStream_t st);
+
 } // namespace kvc

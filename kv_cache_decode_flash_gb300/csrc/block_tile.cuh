@@ -1,0 +1,261 @@
+// block_tile.cuh - what the kernels over a block of query tokens share: a
+// step's cached rows as fp16 in shared memory, the query rows, and their
+// products.  Not part of the ABI.
+//
+// Codes are exact in fp16; block scales stay apart, in 32 bits.  A query row is
+// normalised by a power of two (its largest magnitude comes to lie in
+// [2^13, 2^14)): exact for f16 and bf16 queries, while 32-bit queries are split
+// into two fp16 parts, 22 bits together.  A step's scores are then as exact as
+// sums in 32 bits are: a block of 32 products is summed by the tensor cores,
+// scaled in 32 bits and added.
+#pragma once
+
+#include "block_attn.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace kvc {
+
+constexpr int BLOCK_THREADS = 128;
+constexpr int TILE_PAD = 8; // halves behind a row: 16 bytes off a multiple of 128, so ldmatrix has no bank conflicts
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t h2(float a, float b) {
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 f2(uint32_t u) { return __half22float2(*reinterpret_cast<__half2 *>(&u)); }
+
+// Four offset-binary codes (code + 128) to four halves: the byte becomes the
+// low mantissa of 1024, from which 1152 is taken (exact).
+__device__ __forceinline__ uint2 codes4(uint32_t w) {
+    const uint32_t k = 0x64646464u;
+    uint32_t lo = __byte_perm(w, k, 0x4140), hi = __byte_perm(w, k, 0x4342);
+    const __half2 c = __half2half2(__ushort_as_half(0x6480)); // 1152
+    __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&lo), c), b = __hsub2(*reinterpret_cast<__half2 *>(&hi), c);
+    return make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
+}
+// The low nibbles of four bytes to four halves code - 8.
+__device__ __forceinline__ uint2 nibbles4(uint32_t w) {
+    w &= 0x0f0f0f0fu;
+    const uint32_t k = 0x64646464u;
+    uint32_t lo = __byte_perm(w, k, 0x4140), hi = __byte_perm(w, k, 0x4342);
+    const __half2 c = __half2half2(__ushort_as_half(0x6408)); // 1032
+    __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&lo), c), b = __hsub2(*reinterpret_cast<__half2 *>(&hi), c);
+    return make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
+}
+// Whether either half of the pair is inf or NaN; those set to 0.
+__device__ __forceinline__ bool drop_nonfinite(uint32_t &u) {
+    const bool a = (u & 0x7c00u) == 0x7c00u, b = (u & 0x7c000000u) == 0x7c000000u;
+    if (a) u &= 0xffff0000u;
+    if (b) u &= 0x0000ffffu;
+    return a || b;
+}
+
+template <int KT> __device__ __forceinline__ constexpr int row_bytes(int D) {
+    return KT == KVC_F16 ? 2 * D : (KT == KVC_Q4_0 ? D / 2 : D);
+}
+
+// A step's rows of one tensor as fp16 in shared memory (codes without their scale); returns whether a
+// value of them is not finite (V only: such values are set to 0).
+template <int D, int T, bool V>
+__device__ __forceinline__ bool fill(__half (*dst)[D + TILE_PAD], const uint8_t *data, const int32_t *row,
+                                     uint8_t *badrow, int tid) {
+    constexpr int RB = row_bytes<T>(D), PIECES = RB / 16;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < CROSS_TILE_N * PIECES / BLOCK_THREADS; ++i) {
+        const int at = tid + i * BLOCK_THREADS, j = at / PIECES, c = at % PIECES;
+        const int32_t R = row[j];
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (R >= 0) u = *reinterpret_cast<const uint4 *>(data + (int64_t)R * RB + c * 16);
+        if constexpr (T == KVC_F16) {
+            if constexpr (V) {
+                bool b = drop_nonfinite(u.x);
+                b |= drop_nonfinite(u.y);
+                b |= drop_nonfinite(u.z);
+                b |= drop_nonfinite(u.w);
+                if (b) badrow[j] = 1;
+                bad |= b;
+            }
+            *reinterpret_cast<uint4 *>(&dst[j][c * 8]) = u;
+        } else if constexpr (T == KVC_Q8_0) {
+            const uint2 a = codes4(u.x), b = codes4(u.y), e = codes4(u.z), f = codes4(u.w);
+            *reinterpret_cast<uint4 *>(&dst[j][c * 16]) = make_uint4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<uint4 *>(&dst[j][c * 16 + 8]) = make_uint4(e.x, e.y, f.x, f.y);
+        } else {
+            // byte i of a 32-value block holds the codes i (low) and i + 16 (high)
+            uint2 a = nibbles4(u.x), b = nibbles4(u.y), e = nibbles4(u.z), f = nibbles4(u.w);
+            *reinterpret_cast<uint4 *>(&dst[j][c * 32]) = make_uint4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<uint4 *>(&dst[j][c * 32 + 8]) = make_uint4(e.x, e.y, f.x, f.y);
+            a = nibbles4(u.x >> 4), b = nibbles4(u.y >> 4), e = nibbles4(u.z >> 4), f = nibbles4(u.w >> 4);
+            *reinterpret_cast<uint4 *>(&dst[j][c * 32 + 16]) = make_uint4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<uint4 *>(&dst[j][c * 32 + 24]) = make_uint4(e.x, e.y, f.x, f.y);
+        }
+    }
+    return bad;
+}
+
+
+// Pool rows of the step's cached rows base .. base + CROSS_TILE_N - 1 of KV head g: -1 past the sequence's end, and for
+// a page that the pool does not have (reported).
+__device__ __forceinline__ int32_t pool_row(const BlockParams &p, const BlockSeq &q, int g, int j) {
+    if (j >= q.n_rows) return -1;
+    const int64_t lr = (int64_t)q.off + j;
+    const int64_t pi = lr / p.P;
+    const int32_t page = pi < p.max_pages ? p.pt[(int64_t)q.id * p.max_pages + pi] : -1;
+    if (page < 0 || page >= p.n_pages) {
+        atomicOr(p.err, ERR_BAD_PAGE);
+        return -1;
+    }
+    return (int32_t)(((int64_t)page * p.Hk + g) * p.P + (lr - pi * p.P));
+}
+
+// The launch's sequence that work item `item` belongs to: the last one whose
+// first item is not behind it (sequences without items share a first item).
+__device__ __forceinline__ int item_seq(const BlockParams &p, int item) {
+    int lo = 0, hi = p.n_seq - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (p.seq[mid].item0 <= item) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// One warp normalises query row m (of m_all rows; the others are zero) of KV
+// head g into shared memory; returns the rows that it sees (0 for no row) and,
+// in *scale, the score per unit of the normalised product, in log2 units.
+template <int D, bool LO>
+__device__ __forceinline__ int query_row(const BlockParams &p, const BlockSeq &q, int g, int m, int m_all, int lane,
+                                         __half *hi, __half *lo, float *scale) {
+    constexpr int V = D / 32;
+    float x[V];
+    float top = 0.f;
+    int vis = 0;
+    if (m < m_all) {
+        const int t = m / p.r, j = m % p.r;
+        const int64_t tok = (int64_t)q.tok0 + t;
+        const int64_t at = (tok * p.H + (int64_t)g * p.r + j) * D + lane * V;
+        if (p.act == KVC_ACT_F32) {
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                const float2 f = *reinterpret_cast<const float2 *>(reinterpret_cast<const float *>(p.q) + at + i);
+                x[i] = f.x, x[i + 1] = f.y;
+            }
+        } else if (p.act == KVC_ACT_F16) {
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(reinterpret_cast<const __half *>(p.q) + at + i));
+                x[i] = f.x, x[i + 1] = f.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                const float2 f = __bfloat1622float2(
+                    *reinterpret_cast<const __nv_bfloat162 *>(reinterpret_cast<const __nv_bfloat16 *>(p.q) + at + i));
+                x[i] = f.x, x[i + 1] = f.y;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = fmaxf(top, fabsf(x[i]));
+        vis = p.n_vis ? min(max(p.n_vis[tok], 0), q.n_rows) : q.n_rows;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = 0.f;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // top = f * 2^e, f in [1/2, 1): scaled by 2^(14 - e)
+    int e = 0;
+    if (top > 0.f && top < __int_as_float(0x7f800000)) frexpf(top, &e);
+    const float up = ldexpf(1.f, min(14 - e, 127)); // (rows below 2^-113: their scores are as good as 0)
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+        const float a = x[i] * up, b = x[i + 1] * up;
+        const uint32_t h = h2(a, b);
+        *reinterpret_cast<uint32_t *>(hi + lane * V + i) = h;
+        if (LO) {
+            const float2 f = f2(h);
+            *reinterpret_cast<uint32_t *>(lo + lane * V + i) = h2(isinf(f.x) ? 0.f : a - f.x, isinf(f.y) ? 0.f : b - f.y);
+        }
+    }
+    *scale = p.scale_log2 / up;
+    return vis;
+}
+
+// sc += the products of 16 query rows (addresses qa, ql of their fp16 parts) and NT * 8 cached rows (address ka),
+// block scales d[b][col] applied: the accumulator layout of mma.m16n8k16.
+template <int D, int KT, int NT, bool LO>
+__device__ __forceinline__ void scores(float (&sc)[NT][4], uint32_t qa, uint32_t ql, uint32_t ka,
+                                       const float (*d)[CROSS_TILE_N], int col) {
+    constexpr int PITCH = (D + TILE_PAD) * 2;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sc[n][k] = 0.f;
+#pragma unroll
+    for (int b = 0; b < D / QK; ++b) {
+        float t[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[n][k] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t a[4], al[4];
+            ldsm4(a, qa + (b * 32 + k * 16) * 2);
+            if (LO) ldsm4(al, ql + (b * 32 + k * 16) * 2);
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                uint32_t kb[4];
+                ldsm4(kb, ka + n * 8 * PITCH + (b * 32 + k * 16) * 2);
+                mma(t[n], a, kb[0], kb[1]);
+                mma(t[n + 1], a, kb[2], kb[3]);
+                if (LO) {
+                    mma(t[n], al, kb[0], kb[1]);
+                    mma(t[n + 1], al, kb[2], kb[3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if constexpr (KT != KVC_F16) {
+                const float2 f = *reinterpret_cast<const float2 *>(&d[b][col + n * 8]);
+                sc[n][0] = fmaf(t[n][0], f.x, sc[n][0]);
+                sc[n][1] = fmaf(t[n][1], f.y, sc[n][1]);
+                sc[n][2] = fmaf(t[n][2], f.x, sc[n][2]);
+                sc[n][3] = fmaf(t[n][3], f.y, sc[n][3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sc[n][k] += t[n][k];
+            }
+        }
+    }
+}
+
+} // namespace kvc

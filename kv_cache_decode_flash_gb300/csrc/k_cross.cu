@@ -15,11 +15,10 @@
 //   of V goes into the probabilities, P' = p * d * 2^(12 - E), E the exponent
 //   of the largest V scale met so far (the sums are rescaled when it grows),
 //   which keeps P' in the normal range of fp16 for scales of any size.
-//   A query row is normalised by a power of two (its largest magnitude comes
-//   to lie in [2^13, 2^14)), which is exact for f16 and bf16 queries; 32-bit
-//   queries and their probabilities are split into two fp16 parts (22 bits), so
-//   that 32-bit results keep 32-bit accuracy.  With 16-bit results P' is one
-//   fp16 value: its rounding (2^-12) is below the result's own.
+//   With 32-bit queries P' is split into two fp16 parts (22 bits), so that
+//   32-bit results keep 32-bit accuracy.  With 16-bit results P' is one fp16
+//   value: its rounding (at most 2^-11) averages out over the rows, below the
+//   result's own.
 // Rows behind the sequence's last and rows that a token does not see take no
 // part, whatever they hold: scores are selected, not added to, and a
 // non-finite V value is kept out of the products (0 x inf is NaN) and put into
@@ -27,75 +26,17 @@
 // Few query tiles: the cached rows are split over items, the partial sums are
 // joined in their order by the item that comes last (an arrival counter), so a
 // result does not depend on the order in which items finish.
-#include "block_attn.h"
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+#include "block_tile.cuh"
 
 namespace kvc {
 namespace {
 
-constexpr int THREADS = 128;
+constexpr int THREADS = BLOCK_THREADS;
 constexpr int TM = CROSS_TILE_M, TN = CROSS_TILE_N;
 constexpr int E_MIN = -24; // exponent of the smallest fp16 scale
 
-__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                 "{%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t h2(float a, float b) {
-    __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<uint32_t *>(&h);
-}
-__device__ __forceinline__ float2 f2(uint32_t u) { return __half22float2(*reinterpret_cast<__half2 *>(&u)); }
-
-// Four offset-binary codes (code + 128) to four halves: the byte becomes the
-// low mantissa of 1024, from which 1152 is taken (exact).
-__device__ __forceinline__ uint2 codes4(uint32_t w) {
-    const uint32_t k = 0x64646464u;
-    uint32_t lo = __byte_perm(w, k, 0x4140), hi = __byte_perm(w, k, 0x4342);
-    const __half2 c = __half2half2(__ushort_as_half(0x6480)); // 1152
-    __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&lo), c), b = __hsub2(*reinterpret_cast<__half2 *>(&hi), c);
-    return make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
-}
-// The low nibbles of four bytes to four halves code - 8.
-__device__ __forceinline__ uint2 nibbles4(uint32_t w) {
-    w &= 0x0f0f0f0fu;
-    const uint32_t k = 0x64646464u;
-    uint32_t lo = __byte_perm(w, k, 0x4140), hi = __byte_perm(w, k, 0x4342);
-    const __half2 c = __half2half2(__ushort_as_half(0x6408)); // 1032
-    __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&lo), c), b = __hsub2(*reinterpret_cast<__half2 *>(&hi), c);
-    return make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
-}
-// Whether either half of the pair is inf or NaN; those set to 0.
-__device__ __forceinline__ bool drop_nonfinite(uint32_t &u) {
-    const bool a = (u & 0x7c00u) == 0x7c00u, b = (u & 0x7c000000u) == 0x7c000000u;
-    if (a) u &= 0xffff0000u;
-    if (b) u &= 0x0000ffffu;
-    return a || b;
-}
-
 template <int D> struct Smem {
-    static constexpr int PITCH = D + 8; // halves: rows 16 bytes off a multiple of 128, so ldmatrix has no conflicts
+    static constexpr int PITCH = D + TILE_PAD;
     __half qhi[TM][PITCH];
     __half qlo[TM][PITCH];
     __half k[TN][PITCH];
@@ -113,50 +54,6 @@ template <int D> struct Smem {
     int32_t bad, any_bad;
     int32_t last;
 };
-
-template <int KT> __device__ __forceinline__ constexpr int row_bytes(int D) {
-    return KT == KVC_F16 ? 2 * D : (KT == KVC_Q4_0 ? D / 2 : D);
-}
-
-// A step's rows of one tensor as fp16 in shared memory (codes without their scale); returns whether a
-// value of them is not finite (V only: such values are set to 0).
-template <int D, int T, bool V>
-__device__ __forceinline__ bool fill(__half (*dst)[Smem<D>::PITCH], const uint8_t *data, const int32_t *row,
-                                     uint8_t *badrow, int tid) {
-    constexpr int RB = row_bytes<T>(D), PIECES = RB / 16;
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < TN * PIECES / THREADS; ++i) {
-        const int at = tid + i * THREADS, j = at / PIECES, c = at % PIECES;
-        const int32_t R = row[j];
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (R >= 0) u = *reinterpret_cast<const uint4 *>(data + (int64_t)R * RB + c * 16);
-        if constexpr (T == KVC_F16) {
-            if constexpr (V) {
-                bool b = drop_nonfinite(u.x);
-                b |= drop_nonfinite(u.y);
-                b |= drop_nonfinite(u.z);
-                b |= drop_nonfinite(u.w);
-                if (b) badrow[j] = 1;
-                bad |= b;
-            }
-            *reinterpret_cast<uint4 *>(&dst[j][c * 8]) = u;
-        } else if constexpr (T == KVC_Q8_0) {
-            const uint2 a = codes4(u.x), b = codes4(u.y), e = codes4(u.z), f = codes4(u.w);
-            *reinterpret_cast<uint4 *>(&dst[j][c * 16]) = make_uint4(a.x, a.y, b.x, b.y);
-            *reinterpret_cast<uint4 *>(&dst[j][c * 16 + 8]) = make_uint4(e.x, e.y, f.x, f.y);
-        } else {
-            // byte i of a 32-value block holds the codes i (low) and i + 16 (high)
-            uint2 a = nibbles4(u.x), b = nibbles4(u.y), e = nibbles4(u.z), f = nibbles4(u.w);
-            *reinterpret_cast<uint4 *>(&dst[j][c * 32]) = make_uint4(a.x, a.y, b.x, b.y);
-            *reinterpret_cast<uint4 *>(&dst[j][c * 32 + 8]) = make_uint4(e.x, e.y, f.x, f.y);
-            a = nibbles4(u.x >> 4), b = nibbles4(u.y >> 4), e = nibbles4(u.z >> 4), f = nibbles4(u.w >> 4);
-            *reinterpret_cast<uint4 *>(&dst[j][c * 32 + 16]) = make_uint4(a.x, a.y, b.x, b.y);
-            *reinterpret_cast<uint4 *>(&dst[j][c * 32 + 24]) = make_uint4(e.x, e.y, f.x, f.y);
-        }
-    }
-    return bad;
-}
 
 // A V value as stored (the rare path of values that are not finite).
 template <int D, int T>
@@ -211,16 +108,7 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
     const int wm = warp % WM, wn = warp / WM, gid = lane >> 2, qc = lane & 3;
 
     // the item: sequence, KV head, query tile, part of the rows
-    int si = 0;
-    {
-        int lo = 0, hi = p.n_seq - 1;
-        while (lo < hi) { // last sequence whose first item is <= ours (those without items share it: take the last)
-            const int mid = (lo + hi + 1) / 2;
-            if (p.seq[mid].item0 <= (int)blockIdx.x) lo = mid; else hi = mid - 1;
-        }
-        si = lo;
-    }
-    const BlockSeq q = p.seq[si];
+    const BlockSeq q = p.seq[item_seq(p, (int)blockIdx.x)];
     const int local = (int)blockIdx.x - q.item0;
     const int part = local % q.splits, gt = local / q.splits;
     const int g = gt / q.tiles, tile = q.tiles - 1 - gt % q.tiles; // later tokens see more: they begin first
@@ -232,45 +120,11 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
         s.bad = 0;
     }
     __syncthreads();
-    // query rows: a warp each, normalised by a power of two and split
     for (int m = warp; m < MROWS; m += THREADS / 32) {
-        float x[D / 32];
-        float top = 0.f;
-        int vis = 0;
-        if (m < mrows) {
-            const int t = (m0 + m) / p.r, j = (m0 + m) % p.r;
-            const int64_t tok = (int64_t)q.tok0 + t;
-            const int64_t at = (tok * p.H + (int64_t)g * p.r + j) * D + lane * (D / 32);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                if (p.act == KVC_ACT_F32)
-                    x[i] = reinterpret_cast<const float *>(p.q)[at + i];
-                else if (p.act == KVC_ACT_F16)
-                    x[i] = __half2float(reinterpret_cast<const __half *>(p.q)[at + i]);
-                else
-                    x[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.q)[at + i]);
-                top = fmaxf(top, fabsf(x[i]));
-            }
-            vis = p.n_vis ? min(max(p.n_vis[tok], 0), q.n_rows) : q.n_rows;
-        } else {
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) x[i] = 0.f;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // top = f * 2^e, f in [1/2, 1): scaled by 2^(14 - e)
-        int e = 0;
-        if (top > 0.f && top < __int_as_float(0x7f800000)) frexpf(top, &e);
-        const float up = ldexpf(1.f, min(14 - e, 127)); // (subnormal rows: within 2^-127, their score is 0)
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const float y = x[i] * up;
-            const __half h = __float2half_rn(y);
-            s.qhi[m][lane * (D / 32) + i] = h;
-            if (LO) s.qlo[m][lane * (D / 32) + i] = __float2half_rn(__hisinf(h) ? 0.f : y - __half2float(h));
-        }
+        float scale;
+        const int vis = query_row<D, LO>(p, q, g, m0 + m, m_all, lane, s.qhi[m], s.qlo[m], &scale);
         if (lane == 0) {
-            s.qscale[m] = p.scale_log2 / up;
+            s.qscale[m] = scale;
             s.vis[m] = vis;
             if (vis > 0) atomicMax(&s.vis_max, vis);
         }
@@ -294,17 +148,7 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
     for (int base = r0; base < r1; base += TN) {
         // the step's rows; a page that the pool does not have is reported and its rows are left out
         if (tid < TN) {
-            const int j = base + tid;
-            int32_t R = -1;
-            if (j < q.n_rows) {
-                const int64_t lr = (int64_t)q.off + j;
-                const int64_t pi = lr / p.P;
-                const int32_t page = pi < p.max_pages ? p.pt[(int64_t)q.id * p.max_pages + pi] : -1;
-                if (page >= 0 && page < p.n_pages)
-                    R = (int32_t)(((int64_t)page * p.Hk + g) * p.P + (lr - pi * p.P));
-                else
-                    atomicOr(p.err, ERR_BAD_PAGE);
-            }
+            const int32_t R = pool_row(p, q, g, base + tid);
             s.row[tid] = R;
             s.badrow[tid] = 0;
         }
@@ -348,51 +192,10 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
 
         // scores of 16 query rows x NC cached rows
         float sc[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) sc[n][k] = 0.f;
-        const uint32_t qa = smem_u32(&s.qhi[wm * 16 + (lane & 15)][(lane >> 4) * 8]);
-        const uint32_t ql = smem_u32(&s.qlo[wm * 16 + (lane & 15)][(lane >> 4) * 8]);
-        const uint32_t ka = smem_u32(&s.k[wn * NC + (lane & 7) + ((lane >> 4) << 3)][((lane >> 3) & 1) * 8]);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            float t[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) t[n][k] = 0.f;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t a[4], al[4];
-                ldsm4(a, qa + (b * 32 + k * 16) * 2);
-                if (LO) ldsm4(al, ql + (b * 32 + k * 16) * 2);
-#pragma unroll
-                for (int n = 0; n < NT; n += 2) {
-                    uint32_t kb[4];
-                    ldsm4(kb, ka + n * 8 * Smem<D>::PITCH * 2 + (b * 32 + k * 16) * 2);
-                    mma(t[n], a, kb[0], kb[1]);
-                    mma(t[n + 1], a, kb[2], kb[3]);
-                    if (LO) {
-                        mma(t[n], al, kb[0], kb[1]);
-                        mma(t[n + 1], al, kb[2], kb[3]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if constexpr (KT != KVC_F16) {
-                    const float2 d = *reinterpret_cast<const float2 *>(&s.ks[b][wn * NC + n * 8 + qc * 2]);
-                    sc[n][0] = fmaf(t[n][0], d.x, sc[n][0]);
-                    sc[n][1] = fmaf(t[n][1], d.y, sc[n][1]);
-                    sc[n][2] = fmaf(t[n][2], d.x, sc[n][2]);
-                    sc[n][3] = fmaf(t[n][3], d.y, sc[n][3]);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) sc[n][k] += t[n][k];
-                }
-            }
-        }
+        scores<D, KT, NT, LO>(sc, smem_u32(&s.qhi[wm * 16 + (lane & 15)][(lane >> 4) * 8]),
+                              smem_u32(&s.qlo[wm * 16 + (lane & 15)][(lane >> 4) * 8]),
+                              smem_u32(&s.k[wn * NC + (lane & 7) + ((lane >> 4) << 3)][((lane >> 3) & 1) * 8]), s.ks,
+                              wn * NC + qc * 2);
         // scale, mask, online softmax
         float nm[2] = {mx[0], mx[1]};
 #pragma unroll
@@ -424,13 +227,6 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
             sum[h] = sum[h] * al[h] + add;
             al[h] *= grow;
         }
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            o[i][0] *= al[0];
-            o[i][1] *= al[0];
-            o[i][2] *= al[1];
-            o[i][3] *= al[1];
-        }
         if (s.bad) { // a V value of this step is not finite: it goes to the rows that give it weight
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -442,53 +238,67 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
                 }
             s.any_bad = 1;
         }
-        // P V: a 16-row slab of the step at a time, a 32-value block of V at a time
+        // P V, a 32-value block of V at a time.  The tensor cores truncate their sums, so a chain of products is no
+        // longer than the step: its sum is added, with the old ones' rescaling, by a rounded 32-bit operation.
         const float fe = VT == KVC_F16 ? 4096.f : ldexpf(1.f, 12 - E);
 #pragma unroll
-        for (int ks = 0; ks < NC / 16; ++ks) {
-            float pr[8];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc[n][k] *= fe;
+        uint32_t pa[NC / 16][4], plo[LO ? NC / 16 : 1][4];
+        auto split = [&](int ks, const float (&y)[8]) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                pr[k] = sc[2 * ks][k] * fe;
-                pr[4 + k] = sc[2 * ks + 1][k] * fe;
-            }
-            const uint32_t va = smem_u32(&s.v[wn * NC + ks * 16 + (lane & 15)][(lane >> 4) * 8]);
-            uint32_t a[4], alo[4];
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                if (VT != KVC_F16 || b == 0) {
-                    float y[8];
-                    if constexpr (VT != KVC_F16) {
-                        const int j = wn * NC + ks * 16 + qc * 2;
-                        const float2 d0 = *reinterpret_cast<const float2 *>(&s.vs[b][j]);
-                        const float2 d1 = *reinterpret_cast<const float2 *>(&s.vs[b][j + 8]);
-                        y[0] = pr[0] * d0.x, y[1] = pr[1] * d0.y, y[2] = pr[2] * d0.x, y[3] = pr[3] * d0.y;
-                        y[4] = pr[4] * d1.x, y[5] = pr[5] * d1.y, y[6] = pr[6] * d1.x, y[7] = pr[7] * d1.y;
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) y[k] = pr[k];
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        a[k] = h2(y[2 * k], y[2 * k + 1]);
-                        if (LO) {
-                            const float2 f = f2(a[k]);
-                            alo[k] = h2(y[2 * k] - f.x, y[2 * k + 1] - f.y);
-                        }
-                    }
+                pa[ks][k] = h2(y[2 * k], y[2 * k + 1]);
+                if constexpr (LO) {
+                    const float2 f = f2(pa[ks][k]);
+                    plo[ks][k] = h2(y[2 * k] - f.x, y[2 * k + 1] - f.y);
                 }
+            }
+        };
+        if constexpr (VT == KVC_F16) {
+#pragma unroll
+            for (int ks = 0; ks < NC / 16; ++ks) {
+                const float y[8] = {sc[2 * ks][0], sc[2 * ks][1], sc[2 * ks][2], sc[2 * ks][3],
+                                    sc[2 * ks + 1][0], sc[2 * ks + 1][1], sc[2 * ks + 1][2], sc[2 * ks + 1][3]};
+                split(ks, y);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float t[4][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) t[n][k] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < NC / 16; ++ks) {
+                if constexpr (VT != KVC_F16) {
+                    const int j = wn * NC + ks * 16 + qc * 2;
+                    const float2 d0 = *reinterpret_cast<const float2 *>(&s.vs[b][j]);
+                    const float2 d1 = *reinterpret_cast<const float2 *>(&s.vs[b][j + 8]);
+                    const float y[8] = {sc[2 * ks][0] * d0.x, sc[2 * ks][1] * d0.y, sc[2 * ks][2] * d0.x,
+                                        sc[2 * ks][3] * d0.y, sc[2 * ks + 1][0] * d1.x, sc[2 * ks + 1][1] * d1.y,
+                                        sc[2 * ks + 1][2] * d1.x, sc[2 * ks + 1][3] * d1.y};
+                    split(ks, y);
+                }
+                const uint32_t va = smem_u32(&s.v[wn * NC + ks * 16 + (lane & 15)][(lane >> 4) * 8]) + b * 64;
 #pragma unroll
                 for (int n = 0; n < 4; n += 2) {
                     uint32_t vb[4];
-                    ldsm4t(vb, va + (b * 32 + n * 8) * 2);
-                    mma(o[b * 4 + n], a, vb[0], vb[1]);
-                    mma(o[b * 4 + n + 1], a, vb[2], vb[3]);
-                    if (LO) {
-                        mma(o[b * 4 + n], alo, vb[0], vb[1]);
-                        mma(o[b * 4 + n + 1], alo, vb[2], vb[3]);
+                    ldsm4t(vb, va + n * 16);
+                    mma(t[n], pa[ks], vb[0], vb[1]);
+                    mma(t[n + 1], pa[ks], vb[2], vb[3]);
+                    if constexpr (LO) {
+                        mma(t[n], plo[ks], vb[0], vb[1]);
+                        mma(t[n + 1], plo[ks], vb[2], vb[3]);
                     }
                 }
             }
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[b * 4 + n][k] = fmaf(o[b * 4 + n][k], al[k >> 1], t[n][k]);
         }
         __syncthreads();
         if (tid == 0) s.bad = 0;
@@ -510,21 +320,23 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
         __syncthreads();
         float *buf = reinterpret_cast<float *>(&s.k[0][0]); // [WN - 1][MROWS][D]
         static_assert(sizeof(float) * (WN - 1) * MROWS * D <= sizeof(__half) * 2 * TN * Smem<D>::PITCH, "merge buffer");
-        if (qc == 0)
+        if (qc == 0) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 s.m[wn][mrow + 8 * h] = mx[h];
                 s.l[wn][mrow + 8 * h] = sum[h];
             }
-        if (wn > 0)
+        }
+        if (wn > 0) {
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     *reinterpret_cast<float2 *>(&buf[((wn - 1) * MROWS + mrow + 8 * h) * D + i * 8 + qc * 2]) =
                         make_float2(o[i][2 * h], o[i][2 * h + 1]);
+        }
         __syncthreads();
-        if (wn == 0)
+        if (wn == 0) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int m = mrow + 8 * h;
@@ -554,16 +366,17 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
                 mx[h] = M;
                 sum[h] = L;
             }
+        }
     }
     const bool bad = s.any_bad != 0;
     const bool whole = q.splits == 1;
     const int prow = q.part_row0 + local * p.part_rows; // the item's partial rows
-    if (wn == 0)
+    if (wn == 0) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int m = mrow + 8 * h;
             if (m >= mrows) continue;
-            if (bad)
+            if (bad) {
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i)
 #pragma unroll
@@ -571,6 +384,7 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
                         const int d = i * 8 + qc * 2 + k;
                         o[i][2 * h + k] = poisoned(o[i][2 * h + k], (s.poison[m][d / 16] >> (2 * (d % 16))) & 3u);
                     }
+            }
             if (whole) {
                 const int t = (m0 + m) / p.r, j = (m0 + m) % p.r;
                 const int64_t head = ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
@@ -590,6 +404,7 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
                         make_float2(mx[h], sum[h]);
             }
         }
+    }
     if (whole) return;
 
     // the last part to arrive joins the tile's parts in their order

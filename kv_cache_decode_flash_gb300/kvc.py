@@ -79,6 +79,7 @@ def load():
         "kvc_attn_decode": (i32, [p, i32, i32, p, p, p, C.c_float, p]),
         "kvc_decode_step": (i32, [p, i32, i32, p, p, p, p, p, p, C.c_float, p]),
         "kvc_attn_cross": (i32, [p, i32, i32, p, p, i32, p, p, p, p, C.c_float, p]),
+        "kvc_attn_weight": (i32, [p, i32, i32, p, p, i32, p, p, p, C.c_float, p, C.c_int64, p]),
         "kvc_seq_rm": (i32, [p, i32, i32, i32]),
         "kvc_seq_cp": (i32, [p, i32, i32, i32, i32]),
         "kvc_seq_add": (i32, [p, i32, i32, i32, i32]),
@@ -86,6 +87,7 @@ def load():
         "kvc_state_set": (i32, [p, i32, p, sz, C.POINTER(sz)]),
         "kvc_seq_key_scores": (i32, [p, i32, i32, p, C.c_int32, C.POINTER(C.c_int32)]),
         "kvc_seq_evict_window": (i32, [p, i32, i32, i32, i32, i32, C.POINTER(C.c_int32)]),
+        "kvc_seq_evict_weight": (i32, [p, i32, i32, i32, C.c_int32, p, C.c_int64, C.POINTER(C.c_int32)]),
         "kvc_pipeline_depth": (i32, [p, i32]),
         "kvc_pipeline_budget": (i32, [p, sz]),
         "kvc_seq_n_tokens": (i32, [p, i32, C.POINTER(C.c_int32)]),
@@ -231,6 +233,12 @@ def kvc_attn_cross(ctx, layer, seq_ids, n_q, act, q, out, kq_scale, lse=None, n_
                                       _addr(n_vis), float(kq_scale), _stream(stream, device)))
 
 
+def kvc_attn_weight(ctx, layer, seq_ids, n_q, act, q, lse, w, w_stride, kq_scale, n_vis=None, stream=None, device=0):
+    ids, nq = _block(seq_ids, n_q)
+    _check(ctx, load().kvc_attn_weight(ctx, layer, len(seq_ids), ids, nq, int(act), _addr(q), _addr(lse), _addr(n_vis),
+                                       float(kq_scale), _addr(w), int(w_stride), _stream(stream, device)))
+
+
 class kvc_trace_event(C.Structure):
     _fields_ = [("kind", C.c_int32), ("layer", C.c_int32), ("bytes", C.c_int64), ("t0_us", C.c_double),
                 ("t1_us", C.c_double)]
@@ -330,6 +338,13 @@ def kvc_seq_evict_window(ctx, seq, layer, n_keep, n_discard, n_recent) -> int:
     p0 = C.c_int32()
     _check(ctx, load().kvc_seq_evict_window(ctx, seq, layer, n_keep, n_discard, n_recent, C.byref(p0)))
     return p0.value
+
+
+def kvc_seq_evict_weight(ctx, seq, p0, p1, n_remove, w, w_stride) -> int:
+    """Evict the n_remove rows of least weight with positions in [p0, p1); returns the rows removed."""
+    n = C.c_int32()
+    _check(ctx, load().kvc_seq_evict_weight(ctx, seq, p0, p1, int(n_remove), _addr(w), int(w_stride), C.byref(n)))
+    return n.value
 
 
 def kvc_pipeline_depth(ctx, n):
@@ -480,6 +495,24 @@ class KVCache:
         act, total = _act(q), sum(int(t) for t in n_q)
         self._block_io(q, out, lse, n_vis, total)
         kvc_attn_cross(self.ctx, layer, seq_ids, n_q, act, q, out, kq_scale, lse, n_vis, stream, self.device)
+
+    def attn_weight(self, layer, seq_ids, n_q, q, lse, w, kq_scale, n_vis=None, stream=None):
+        """Add the attention weight that the cached rows receive from a block of tokens to
+        w [n_seq][n_head_kv][rows or more] fp32; lse as attn_cross wrote it for these tokens."""
+        act, total = _act(q), sum(int(t) for t in n_q)
+        self._block_io(q, None, lse, n_vis, total)
+        if w.dim() != 3 or w.shape[0] != len(seq_ids) or w.shape[1] != self.params.n_head_kv:
+            raise KvcError(KVC_EINVAL, "w must be [n_seq][n_head_kv][rows]")
+        _block_tensor("w", w, self.device, "torch.float32", 0)
+        kvc_attn_weight(self.ctx, layer, seq_ids, n_q, act, q, lse, w, w.shape[2], kq_scale, n_vis, stream, self.device)
+
+    def evict_weight(self, seq, p0, p1, n_remove, w):
+        """Evict the n_remove rows of least accumulated weight with positions in [p0, p1);
+        w [n_head_kv][rows or more] fp32 follows the rows.  Returns the rows removed."""
+        if w.dim() != 2 or w.shape[0] != self.params.n_head_kv:
+            raise KvcError(KVC_EINVAL, "w must be [n_head_kv][rows]")
+        _block_tensor("w", w, self.device, "torch.float32", 0)
+        return kvc_seq_evict_weight(self.ctx, seq, p0, p1, n_remove, w, w.shape[1])
 
     def _block_io(self, q, out, lse, n_vis, total):
         p = self.params

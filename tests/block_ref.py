@@ -62,3 +62,41 @@ def exact_kv(rng, n, Hk, D, step=2.0**-5):
     x = rng.integers(-127, 128, (n, Hk, D // 32, 32))
     x[..., 0] = 127 * rng.choice([-1, 1], x.shape[:-1])
     return (x.reshape(n, Hk, D) * step).astype(np.float32)
+
+
+def weight(q, K, scale, vis, lse):
+    """(w [Hk][n] that the tokens add, a bound of its distance for 32-bit arithmetic): exp(s - lse) is off by the score's
+    error (operands of 20 bits or more, fp32 sums), by those of s - lse in fp32 (2^-23 of the larger one, twice) and of the exponential
+    (2^-21), the sum over the query rows by 2^-24 for each of them."""
+    T, H, D = q.shape
+    n, Hk = K.shape[0], K.shape[1]
+    r = H // Hk
+    w, bound = np.zeros((Hk, n)), np.zeros((Hk, n))
+    for t in range(T):
+        m = int(min(max(vis[t], 0), n))
+        for g in range(Hk):
+            for h in range(g * r, (g + 1) * r):
+                s = K[:m, g] @ q[t, h] * scale
+                e = np.exp(s - lse[t, h])
+                size = np.abs(K[:m, g]) @ np.abs(q[t, h]) * abs(scale)
+                ds = size * (2.0**-20 + (D + 4) * 2.0**-24) + 2.0**-21 * (1 + np.abs(s) + abs(lse[t, h]))
+                w[g, :m] += e
+                bound[g, :m] += e * (2 * ds + 2.0**-21)
+    return w, bound + w * (T * r + 4) * 2.0**-24
+
+
+def evict(weights, cand, n, n_remove):
+    """Row order after an eviction: rows of smallest (weight, row) among `cand` go, the kept ones behind the new end
+    take their places.  weights [Hk][n] fp32.  Returns (order, removed): row i of the result is row order[i]."""
+    w = weights[0].astype(np.float32)
+    with np.errstate(invalid="ignore"):
+        for g in range(1, len(weights)):
+            w = (w + weights[g]).astype(np.float32)
+    key = [(1, 0.0, j) if np.isnan(w[j]) else (0, float(w[j]), j) for j in cand]
+    gone = sorted(k[2] for k in sorted(key)[:n_remove])
+    left = n - len(gone)
+    order = list(range(left))
+    movers = [j for j in range(left, n) if j not in set(gone)]
+    for hole, j in zip([g for g in gone if g < left], movers):
+        order[hole] = j
+    return order, gone

@@ -43,6 +43,8 @@ def test_null_context_is_refused():
 
     L = kvc.load()
     assert L.kvc_attn_cross(None, 0, 1, None, None, 0, None, None, None, None, 1.0, None) == kvc.KVC_EINVAL
+    assert L.kvc_attn_weight(None, 0, 1, None, None, 0, None, None, None, 1.0, None, 0, None) == kvc.KVC_EINVAL
+    assert L.kvc_seq_evict_weight(None, 0, 0, 0, 0, None, 0, None) == kvc.KVC_EINVAL
 
 
 def test_binding_refuses_tensors_it_would_misread():
