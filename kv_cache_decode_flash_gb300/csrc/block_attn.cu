@@ -49,82 +49,98 @@ static int ensure_block_space(Ctx *c, cudaStream_t st) {
     return KVC_OK;
 }
 
-// Cut the cached rows of the launch's sequences into parts: none where the
-// query tiles alone give every resident CTA an item, else parts of one length
-// (whole steps of CROSS_TILE_N rows, four at least) as short as `want` items
-// and the work space allow.
-static void plan_splits(BlockParams &p, int64_t want, int64_t part_cap) {
-    int64_t base = 0;
-    int32_t longest = 0;
-    for (int i = 0; i < p.n_seq; ++i) {
-        base += (int64_t)p.seq[i].tiles * p.Hk;
-        if (p.seq[i].tiles) longest = std::max(longest, p.seq[i].n_rows);
-    }
+// Cut the cached rows of the launch's units into parts.  `want`: items that run
+// at once; a part has two steps at least (`least` rows), and the partial rows
+// of all parts fit the work space.
+//  One sequence: its units are alike, so those of the last, partly filled wave
+// are cut into as many parts as fill it, the others stay whole.
+//  Several: all rows are cut into parts of at most one length, chosen by a
+// model: an item costs `fixed` steps beside its own, and a schedule ends half
+// the longest item after the mean (or with the longest item, in one wave).
+static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t part_cap) {
+    const int64_t least = 2 * step, fixed = 4;
     auto parts = [](const BlockSeq &s, int64_t len) {
         return (int32_t)std::max<int64_t>(1, (s.n_rows + len - 1) / len);
     };
-    auto items = [&](int64_t len, int64_t *slots) {
-        int64_t n = 0;
-        *slots = 0;
+    int64_t longest = step;
+    for (int i = 0; i < p.n_seq; ++i)
+        if (p.seq[i].tiles) longest = std::max<int64_t>(longest, (p.seq[i].n_rows + step - 1) / step * step);
+    if (p.n_seq == 1) {
+        BlockSeq &s = p.seq[0];
+        const int64_t units = (int64_t)s.tiles * p.Hk, rest = units % want;
+        int64_t k = rest ? std::min<int64_t>({want / rest, s.n_rows / least, part_cap / (rest * p.part_rows)}) : 1;
+        s.splits = (int32_t)std::max<int64_t>(1, k);
+        s.whole = (int32_t)(s.splits > 1 ? units - rest : units);
+    } else {
+        double best = 0;
+        int64_t best_len = longest;
+        for (int64_t len = longest;; len = std::max(least, len * 3 / 4 / step * step)) {
+            int64_t items = 0, slots = 0, most = 0;
+            double total = 0;
+            for (int i = 0; i < p.n_seq; ++i) {
+                const BlockSeq &s = p.seq[i];
+                const int64_t k = parts(s, len), n = (int64_t)s.tiles * p.Hk * k;
+                if (!n) continue;
+                const int64_t cost = fixed + ((s.n_rows + k - 1) / k + step - 1) / step;
+                items += n;
+                if (k > 1) slots += n;
+                total += (double)n * (double)cost;
+                most = std::max(most, cost);
+            }
+            if (slots * p.part_rows > part_cap) break;
+            const double est = items <= want ? (double)most : total / (double)want + 0.5 * (double)most;
+            if (len == longest || est < best) {
+                best = est;
+                best_len = len;
+            }
+            if (len <= least) break;
+        }
         for (int i = 0; i < p.n_seq; ++i) {
-            const int64_t k = (int64_t)p.seq[i].tiles * p.Hk * parts(p.seq[i], len);
-            n += k;
-            if (parts(p.seq[i], len) > 1) *slots += k;
+            BlockSeq &s = p.seq[i];
+            s.splits = parts(s, best_len);
+            s.whole = s.splits > 1 ? 0 : s.tiles * p.Hk;
         }
-        return n;
-    };
-    const int64_t least = 4 * CROSS_TILE_N;
-    int64_t len = std::max<int64_t>(least, ((int64_t)longest + CROSS_TILE_N - 1) / CROSS_TILE_N * CROSS_TILE_N);
-    if (base < want) {
-        int64_t lo = 1, hi = len / CROSS_TILE_N; // shortest length, in steps, that fits
-        lo = std::min(hi, least / CROSS_TILE_N);
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) / 2;
-            int64_t slots;
-            const int64_t n = items(mid * CROSS_TILE_N, &slots);
-            if (n <= want && slots * p.part_rows <= part_cap) hi = mid; else lo = mid + 1;
-        }
-        len = hi * CROSS_TILE_N;
     }
     int32_t item = 0, row = 0, ticket = 0;
     for (int i = 0; i < p.n_seq; ++i) {
         BlockSeq &s = p.seq[i];
-        s.splits = parts(s, len);
         // equal parts, in whole steps
         const int64_t even = ((int64_t)s.n_rows + s.splits - 1) / s.splits;
-        s.split_rows = (int32_t)std::min<int64_t>(INT32_MAX / 2 / CROSS_TILE_N * CROSS_TILE_N,
-                                                  std::max<int64_t>(1, (even + CROSS_TILE_N - 1) / CROSS_TILE_N) * CROSS_TILE_N);
+        s.split_rows = (int32_t)std::min<int64_t>(INT32_MAX / 2 / step * step,
+                                                  std::max<int64_t>(1, (even + step - 1) / step) * step);
         s.item0 = item;
         s.part_row0 = row;
         s.ticket0 = ticket;
-        const int32_t k = s.tiles * p.Hk * s.splits;
-        item += k;
-        if (s.splits > 1) {
-            row += k * p.part_rows;
-            ticket += s.tiles * p.Hk;
-        }
+        const int32_t cut = s.tiles * p.Hk - s.whole;
+        item += s.whole + cut * s.splits;
+        row += cut * s.splits * p.part_rows;
+        ticket += cut;
     }
     p.n_items = item;
 }
 
-// The query tiles and items of a launch over p.n_seq sequences (p.Hk and p.r
-// set); *tok0: the first token, moved on.  Returns whether the tiles are narrow.
-static bool plan_block(BlockParams &p, int sms, const int32_t *rows, const int32_t *n_q, int64_t *tok0) {
+// The query tiles and items of a launch over p.n_seq sequences (p.Hk, p.r and
+// each one's n_rows and n_tok set), for the tcgen05 kernel or the other one.
+// Returns whether the tiles are narrow.
+static bool plan_block(BlockParams &p, int sms, bool tc) {
     int32_t most = 0;
-    for (int i = 0; i < p.n_seq; ++i) most = std::max(most, n_q[i]);
-    const bool narrow = (int64_t)most * p.r <= 16;
-    p.tile_m = narrow ? 16 : CROSS_TILE_M;
-    p.part_rows = (int32_t)std::min<int64_t>(p.tile_m, (int64_t)most * p.r);
+    for (int i = 0; i < p.n_seq; ++i) most = std::max(most, p.seq[i].n_tok);
+    const bool narrow = !tc && (int64_t)most * p.r <= 16;
+    p.tile_m = tc ? CROSS_TC_TILE_M : (narrow ? 16 : CROSS_TILE_M);
+    p.part_rows = (int32_t)std::max<int64_t>(1, std::min<int64_t>(p.tile_m, (int64_t)most * p.r));
     for (int i = 0; i < p.n_seq; ++i) {
         BlockSeq &s = p.seq[i];
-        s.n_rows = rows[i];
-        s.tok0 = (int32_t)*tok0;
-        s.n_tok = n_q[i];
         s.tiles = (int32_t)(((int64_t)s.n_tok * p.r + p.tile_m - 1) / p.tile_m);
-        *tok0 += s.n_tok;
     }
-    plan_splits(p, (int64_t)2 * sms, part_rows_cap(sms));
+    plan_splits(p, tc ? sms : 2 * sms, tc ? CROSS_TC_TILE_N : CROSS_TILE_N, part_rows_cap(sms));
     return narrow;
+}
+
+// Which kernel attends a sequence: the tcgen05 one for 16-bit queries, where its rounding of K to 11 bits leaves the
+// log-sum-exp (an average over the rows) exact to 32 bits' needs: halves always, codes from TC_MIN_ROWS rows on.
+constexpr int TC_MIN_ROWS = 256;
+static bool use_tc(int type_k, int act, int rows) {
+    return act != KVC_ACT_F32 && (type_k == KVC_F16 || rows >= TC_MIN_ROWS);
 }
 
 // Checks that the block operators share; *total: tokens of the block.
@@ -197,29 +213,36 @@ extern "C" int kvc_attn_cross(kvc_ctx *cc, int layer, int n_seq, const int32_t *
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     KVC_CU(c, cudaSetDevice(c->dev));
     if ((rc = ensure_block_space(c, st))) return rc;
-    int64_t tok0 = 0;
-    for (int base = 0; base < n_seq; base += MAX_SEQ_PER_LAUNCH) {
+    const int64_t cap = part_rows_cap(c->sms);
+    for (int tc = 0; tc < 2; ++tc) { // the sequences of either kernel, as many a launch as it carries
         BlockParams p;
         block_params(c, layer, kq_scale, act, p);
         p.q = q;
         p.out = out;
         p.lse = lse;
         p.n_vis = n_vis;
-        p.n_seq = std::min(MAX_SEQ_PER_LAUNCH, n_seq - base);
-        int32_t rows[MAX_SEQ_PER_LAUNCH];
-        for (int i = 0; i < p.n_seq; ++i) {
-            const Seq &sq = c->seqs[(size_t)seq_ids[base + i]];
-            p.seq[i].id = seq_ids[base + i];
-            p.seq[i].off = sq.off;
-            rows[i] = sq.lfill[(size_t)layer];
-        }
-        const bool narrow = plan_block(p, c->sms, rows, n_q + base, &tok0);
-        const int64_t cap = part_rows_cap(c->sms);
         p.part = c->block_part;
         p.part_cap = cap;
         p.tickets = reinterpret_cast<int32_t *>(c->block_part + cap * (c->D + 2));
-        cudaError_t e = launch_cross(c->tk, c->tv, p, narrow, st);
-        if (e != cudaSuccess) return cuda_fail(c, e, "block attention kernel");
+        int64_t tok0 = 0;
+        for (int i = 0; i < n_seq; ++i) {
+            const Seq &sq = c->seqs[(size_t)seq_ids[i]];
+            const int32_t rows = sq.lfill[(size_t)layer];
+            if (n_q[i] > 0 && use_tc(c->tk, act, rows) == (tc != 0)) {
+                BlockSeq &s = p.seq[p.n_seq++];
+                s.id = seq_ids[i];
+                s.off = sq.off;
+                s.n_rows = rows;
+                s.tok0 = (int32_t)tok0;
+                s.n_tok = n_q[i];
+            }
+            tok0 += n_q[i];
+            if (p.n_seq == 0 || (p.n_seq < MAX_SEQ_PER_LAUNCH && i + 1 < n_seq)) continue;
+            const bool narrow = plan_block(p, c->sms, tc != 0);
+            cudaError_t e = tc ? launch_cross_tc(c->tk, c->tv, p, st) : launch_cross(c->tk, c->tv, p, narrow, st);
+            if (e != cudaSuccess) return cuda_fail(c, e, "block attention kernel");
+            p.n_seq = 0;
+        }
     }
     return KVC_OK;
 }
@@ -277,12 +300,12 @@ extern "C" int kvc_attn_weight(kvc_ctx *cc, int layer, int n_seq, const int32_t 
 }
 
 extern "C" int kvc_debug_block_plan(int n_head, int n_head_kv, int head_dim, int act, int sms, int n_seq,
-                                    const int32_t *rows, const int32_t *n_q, int32_t *tile_m, int32_t *splits,
-                                    int32_t *split_rows, int64_t *items, int64_t *part_rows, int64_t *part_cap,
+                                    const int32_t *rows, const int32_t *n_q, int32_t *tile_m, int32_t *whole,
+                                    int32_t *splits, int32_t *split_rows, int64_t *items, int64_t *part_rows, int64_t *part_cap,
                                     int64_t *tickets) {
     if (n_head_kv < 1 || n_head < n_head_kv || n_head % n_head_kv || n_head / n_head_kv > MAX_GROUP ||
         (head_dim != 64 && head_dim != 128) || act < KVC_ACT_F32 || act > KVC_ACT_BF16 || sms < 1 || n_seq < 1 ||
-        n_seq > MAX_SEQ_PER_LAUNCH || !rows || !n_q || !tile_m || !splits || !split_rows || !items || !part_rows ||
+        n_seq > MAX_SEQ_PER_LAUNCH || !rows || !n_q || !tile_m || !whole || !splits || !split_rows || !items || !part_rows ||
         !part_cap || !tickets)
         return KVC_EINVAL;
     BlockParams p;
@@ -293,25 +316,27 @@ extern "C" int kvc_debug_block_plan(int n_head, int n_head_kv, int head_dim, int
     p.r = n_head / n_head_kv;
     p.act = act;
     p.n_seq = n_seq;
-    int64_t total = 0, tok0 = 0;
+    int64_t total = 0;
     for (int i = 0; i < n_seq; ++i) {
         if (rows[i] < 0 || n_q[i] < 0) return KVC_EINVAL;
         total += n_q[i];
+        p.seq[i].n_rows = rows[i];
+        p.seq[i].n_tok = n_q[i];
     }
     if (total * p.r > INT32_MAX / 4 / p.Hk) return KVC_EINVAL;
-    plan_block(p, sms, rows, n_q, &tok0);
+    plan_block(p, sms, act != KVC_ACT_F32);
     *tile_m = p.tile_m;
     *items = p.n_items;
     *part_rows = *tickets = 0;
     *part_cap = part_rows_cap(sms);
     for (int i = 0; i < n_seq; ++i) {
         const BlockSeq &s = p.seq[i];
+        whole[i] = s.whole;
         splits[i] = s.splits;
         split_rows[i] = s.split_rows;
-        if (s.splits > 1 && s.tiles) {
-            *part_rows = std::max<int64_t>(*part_rows, (int64_t)s.part_row0 + (int64_t)s.tiles * p.Hk * s.splits * p.part_rows);
-            *tickets = std::max<int64_t>(*tickets, (int64_t)s.ticket0 + (int64_t)s.tiles * p.Hk);
-        }
+        const int64_t cut = (int64_t)s.tiles * p.Hk - s.whole;
+        *part_rows = std::max<int64_t>(*part_rows, s.part_row0 + cut * s.splits * p.part_rows);
+        *tickets = std::max<int64_t>(*tickets, s.ticket0 + cut);
     }
     return KVC_OK;
 }

@@ -9,7 +9,7 @@ namespace kvc {
 
 // One sequence of a launch.  Its query rows are the pairs (token t, query head
 // j of the KV head's group), row m = t * r + j, cut into tiles of tile_m rows;
-// a work item is (KV head, tile, part of the cached rows).
+// a unit is (KV head, tile), a work item a unit or a part of its cached rows.
 struct BlockSeq {
     int32_t id;         // sequence id (row of the page table)
     int32_t off;        // offset of logical row 0 in the first page
@@ -18,7 +18,8 @@ struct BlockSeq {
     int32_t n_tok;      // its tokens
     int32_t tiles;      // query tiles of a KV head
     int32_t item0;      // first work item of the launch that is this sequence's
-    int32_t splits;     // parts that the cached rows are cut into (>= 1)
+    int32_t whole;      // leading units (KV head, query tile) that are one item each; the others are `splits` items
+    int32_t splits;     // parts that the cached rows of a unit are cut into (>= 1)
     int32_t split_rows; // rows of a part (the last one may have fewer)
     int32_t part_row0;  // first partial row of its items (splits > 1)
     int32_t ticket0;    // first arrival counter of its tiles (splits > 1)
@@ -52,12 +53,16 @@ struct BlockParams {
 };
 static_assert(sizeof(BlockParams) <= 4000, "launch parameters stay within 4 KB");
 
-constexpr int CROSS_TILE_M = 64; // query rows of a tile
-constexpr int CROSS_TILE_N = 64; // cached rows of a step
+constexpr int CROSS_TILE_M = 64;     // query rows of a tile
+constexpr int CROSS_TILE_N = 64;     // cached rows of a step
+constexpr int CROSS_TC_TILE_M = 256; // the same of the tcgen05 kernel
+constexpr int CROSS_TC_TILE_N = 128;
 
 // The block attention.  narrow: every sequence's query rows of a KV head fit
 // 16 (one tensor-core row block), so the warps share the cached rows instead.
 cudaError_t launch_cross(int type_k, int type_v, const BlockParams &p, bool narrow, cudaStream_t st);
+// The same for 16-bit queries, by tcgen05 (tiles of CROSS_TC_TILE_M query rows).
+cudaError_t launch_cross_tc(int type_k, int type_v, const BlockParams &p, cudaStream_t st);
 
 // The rows' weights: splits of a sequence are its steps of CROSS_TILE_N rows, items (KV head, step).
 cudaError_t launch_weight(int type_k, const BlockParams &p, bool narrow, cudaStream_t st);

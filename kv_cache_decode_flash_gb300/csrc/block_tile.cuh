@@ -147,12 +147,21 @@ __device__ __forceinline__ int item_seq(const BlockParams &p, int item) {
     return lo;
 }
 
+// Item `local` of a sequence: the unit (KV head, query tile) and the part of the rows that it is.
+__device__ __forceinline__ void item_unit(const BlockSeq &q, int local, int &unit, int &part, int &parts) {
+    const bool whole = local < q.whole;
+    unit = whole ? local : q.whole + (local - q.whole) / q.splits;
+    part = whole ? 0 : (local - q.whole) % q.splits;
+    parts = whole ? 1 : q.splits;
+}
+
 // One warp normalises query row m (of m_all rows; the others are zero) of KV
-// head g into shared memory; returns the rows that it sees (0 for no row) and,
-// in *scale, the score per unit of the normalised product, in log2 units.
+// head g: lane l gets the D / 32 values from l * D / 32 on as pairs of halves hi
+// (and lo, what hi leaves).  Returns the rows that it sees (0 for no row) and, in
+// *scale, the score per unit of the normalised product, in log2 units.
 template <int D, bool LO>
 __device__ __forceinline__ int query_row(const BlockParams &p, const BlockSeq &q, int g, int m, int m_all, int lane,
-                                         __half *hi, __half *lo, float *scale) {
+                                         uint32_t (&hi)[D / 64], uint32_t (&lo)[D / 64], float *scale) {
     constexpr int V = D / 32;
     float x[V];
     float top = 0.f;
@@ -198,17 +207,102 @@ __device__ __forceinline__ int query_row(const BlockParams &p, const BlockSeq &q
     for (int i = 0; i < V; i += 2) {
         const float a = x[i] * up, b = x[i + 1] * up;
         const uint32_t h = h2(a, b);
-        *reinterpret_cast<uint32_t *>(hi + lane * V + i) = h;
+        hi[i / 2] = h;
         if (LO) {
             const float2 f = f2(h);
-            *reinterpret_cast<uint32_t *>(lo + lane * V + i) = h2(isinf(f.x) ? 0.f : a - f.x, isinf(f.y) ? 0.f : b - f.y);
+            lo[i / 2] = h2(isinf(f.x) ? 0.f : a - f.x, isinf(f.y) ? 0.f : b - f.y);
         }
     }
     *scale = p.scale_log2 / up;
     return vis;
 }
 
-// sc += the products of 16 query rows (addresses qa, ql of their fp16 parts) and NT * 8 cached rows (address ka),
+// A V value as stored (the rare path of values that are not finite).
+template <int D, int T>
+__device__ float stored_value(const uint8_t *data, const uint16_t *scales, int32_t R, int d) {
+    if constexpr (T == KVC_F16) {
+        return __half2float(reinterpret_cast<const __half *>(data)[(int64_t)R * D + d]);
+    } else {
+        const float s = __half2float(__ushort_as_half(scales[(int64_t)R * (D / QK) + d / QK]));
+        if constexpr (T == KVC_Q8_0) return (float)((int)data[(int64_t)R * D + d] - 128) * s;
+        const int b = d / QK, e = d % QK;
+        const uint8_t byte = data[(int64_t)R * (D / 2) + b * (QK / 2) + (e & 15)];
+        return (float)((int)(e < 16 ? byte & 15 : byte >> 4) - 8) * s;
+    }
+}
+
+// The values of row R that are not finite, marked in the two-bit words of a query row that gives it weight.
+template <int D, int T>
+__device__ __noinline__ void mark_poison(uint32_t *words, const uint8_t *data, const uint16_t *scales, int32_t R) {
+    for (int d = 0; d < D; ++d) {
+        const float x = stored_value<D, T>(data, scales, R, d);
+        if (fabsf(x) <= 3.4e38f) continue;
+        const uint32_t two = x > 0.f ? 1u : (x < 0.f ? 2u : 3u);
+        atomicOr(&words[d / 16], two << (2 * (d % 16)));
+    }
+}
+
+__device__ __forceinline__ float poisoned(float x, uint32_t two_bits) {
+    if (two_bits == 3) return __int_as_float(0x7fffffff);
+    if (two_bits == 0) return x;
+    return x + (two_bits == 1 ? __int_as_float(0x7f800000) : __int_as_float(0xff800000));
+}
+
+// Two values as the pair of a 16-bit type.
+__device__ __forceinline__ uint32_t pack16(int act, float a, float b) {
+    if (act == KVC_ACT_F16) return h2(a, b);
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+__device__ __forceinline__ void store2(void *out, int act, int64_t at, float a, float b) {
+    if (act == KVC_ACT_F32)
+        *reinterpret_cast<float2 *>(reinterpret_cast<float *>(out) + at) = make_float2(a, b);
+    else
+        *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(out) + at) = pack16(act, a, b);
+}
+
+// The end of an item that is a part of its tile's rows (all threads of the CTA, whose partial rows are written): the
+// part that arrives last joins the tile's parts, in their order.
+template <int D, int NTHREADS>
+__device__ __forceinline__ void join_parts(const BlockParams &p, const BlockSeq &q, int g, int m0, int mrows, int parts,
+                                           int ticket, int first, int32_t *last) {
+    const int tid = threadIdx.x;
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        const int n = atomicAdd(&p.tickets[ticket], 1);
+        *last = n == parts - 1;
+        if (*last) p.tickets[ticket] = 0;
+    }
+    __syncthreads();
+    if (!*last) return;
+    __threadfence();
+    const float2 *ml = reinterpret_cast<const float2 *>(p.part + p.part_cap * D);
+    for (int at = tid; at < mrows * (D / 2); at += NTHREADS) {
+        const int m = at / (D / 2), d = (at % (D / 2)) * 2;
+        float M = -INFINITY;
+        for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(&ml[first + i * p.part_rows + m]).x);
+        const float use = M == -INFINITY ? 0.f : M;
+        float L = 0.f, x = 0.f, y = 0.f;
+        for (int i = 0; i < parts; ++i) {
+            const int row = first + i * p.part_rows + m;
+            const float2 c = __ldcg(&ml[row]);
+            const float f = ex2(c.x - use);
+            if (c.y == 0.f || (f == 0.f && c.y == c.y)) continue; // nothing seen there, or nothing left of it
+            L = fmaf(c.y, f, L);
+            const float2 v = __ldcg(reinterpret_cast<const float2 *>(p.part + (int64_t)row * D + d));
+            x = fmaf(v.x, f, x);
+            y = fmaf(v.y, f, y);
+        }
+        const int t = (m0 + m) / p.r, j = (m0 + m) % p.r;
+        const int64_t head = ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        store2(p.out, p.act, head * D + d, x * inv, y * inv);
+        if (p.lse && d == 0) p.lse[head] = L == 0.f ? -INFINITY : M * 0.6931471805599453f + logf(L);
+    }
+}
+
+// sc = the products of 16 query rows (addresses qa, ql of their fp16 parts) and NT * 8 cached rows (address ka),
 // block scales d[b][col] applied: the accumulator layout of mma.m16n8k16.
 template <int D, int KT, int NT, bool LO>
 __device__ __forceinline__ void scores(float (&sc)[NT][4], uint32_t qa, uint32_t ql, uint32_t ka,

@@ -55,47 +55,6 @@ template <int D> struct Smem {
     int32_t last;
 };
 
-// A V value as stored (the rare path of values that are not finite).
-template <int D, int T>
-__device__ float stored_value(const uint8_t *data, const uint16_t *scales, int32_t R, int d) {
-    if constexpr (T == KVC_F16) {
-        return __half2float(reinterpret_cast<const __half *>(data)[(int64_t)R * D + d]);
-    } else {
-        const float s = __half2float(__ushort_as_half(scales[(int64_t)R * (D / QK) + d / QK]));
-        if constexpr (T == KVC_Q8_0) return (float)((int)data[(int64_t)R * D + d] - 128) * s;
-        const int b = d / QK, e = d % QK;
-        const uint8_t byte = data[(int64_t)R * (D / 2) + b * (QK / 2) + (e & 15)];
-        return (float)((int)(e < 16 ? byte & 15 : byte >> 4) - 8) * s;
-    }
-}
-
-// The values of row R that are not finite, marked in the two-bit words of a query row that gives it weight.
-template <int D, int T>
-__device__ __noinline__ void mark_poison(uint32_t *words, const uint8_t *data, const uint16_t *scales, int32_t R) {
-    for (int d = 0; d < D; ++d) {
-        const float x = stored_value<D, T>(data, scales, R, d);
-        if (fabsf(x) <= 3.4e38f) continue;
-        const uint32_t two = x > 0.f ? 1u : (x < 0.f ? 2u : 3u);
-        atomicOr(&words[d / 16], two << (2 * (d % 16)));
-    }
-}
-
-__device__ __forceinline__ float poisoned(float x, uint32_t two_bits) {
-    if (two_bits == 3) return __int_as_float(0x7fffffff);
-    if (two_bits == 0) return x;
-    return x + (two_bits == 1 ? __int_as_float(0x7f800000) : __int_as_float(0xff800000));
-}
-
-__device__ __forceinline__ void store2(void *out, int act, int64_t at, float a, float b) {
-    if (act == KVC_ACT_F32) {
-        *reinterpret_cast<float2 *>(reinterpret_cast<float *>(out) + at) = make_float2(a, b);
-    } else if (act == KVC_ACT_F16) {
-        *reinterpret_cast<__half2 *>(reinterpret_cast<__half *>(out) + at) = __floats2half2_rn(a, b);
-    } else {
-        *reinterpret_cast<__nv_bfloat162 *>(reinterpret_cast<__nv_bfloat16 *>(out) + at) = __floats2bfloat162_rn(a, b);
-    }
-}
-
 // WM: warps along the query rows (16 each); the 4 / WM warps of a row block
 // share a step's cached rows and are joined at the end.  LO: 32-bit queries.
 template <int D, int KT, int VT, int WM, bool LO>
@@ -110,8 +69,9 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
     // the item: sequence, KV head, query tile, part of the rows
     const BlockSeq q = p.seq[item_seq(p, (int)blockIdx.x)];
     const int local = (int)blockIdx.x - q.item0;
-    const int part = local % q.splits, gt = local / q.splits;
-    const int g = gt / q.tiles, tile = q.tiles - 1 - gt % q.tiles; // later tokens see more: they begin first
+    int unit, part, parts;
+    item_unit(q, local, unit, part, parts);
+    const int g = unit / q.tiles, tile = q.tiles - 1 - unit % q.tiles; // later tokens see more: they begin first
     const int m_all = q.n_tok * p.r, m0 = tile * MROWS, mrows = min(MROWS, m_all - m0);
 
     if (tid == 0) {
@@ -122,7 +82,13 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
     __syncthreads();
     for (int m = warp; m < MROWS; m += THREADS / 32) {
         float scale;
-        const int vis = query_row<D, LO>(p, q, g, m0 + m, m_all, lane, s.qhi[m], s.qlo[m], &scale);
+        uint32_t hi[D / 64], lo[D / 64];
+        const int vis = query_row<D, LO>(p, q, g, m0 + m, m_all, lane, hi, lo, &scale);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            *reinterpret_cast<uint32_t *>(&s.qhi[m][lane * (D / 32) + 2 * i]) = hi[i];
+            if (LO) *reinterpret_cast<uint32_t *>(&s.qlo[m][lane * (D / 32) + 2 * i]) = lo[i];
+        }
         if (lane == 0) {
             s.qscale[m] = scale;
             s.vis[m] = vis;
@@ -132,7 +98,7 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
     }
     __syncthreads();
     const int r0 = part * q.split_rows;
-    const int r1 = min(r0 + q.split_rows, s.vis_max);
+    const int r1 = parts == 1 ? s.vis_max : min(r0 + q.split_rows, s.vis_max);
 
     float o[D / 8][4];
 #pragma unroll
@@ -369,8 +335,8 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
         }
     }
     const bool bad = s.any_bad != 0;
-    const bool whole = q.splits == 1;
-    const int prow = q.part_row0 + local * p.part_rows; // the item's partial rows
+    const bool whole = parts == 1;
+    const int prow = q.part_row0 + (local - q.whole) * p.part_rows; // the item's partial rows
     if (wn == 0) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -406,42 +372,8 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
         }
     }
     if (whole) return;
-
-    // the last part to arrive joins the tile's parts in their order
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-        const int n = atomicAdd(&p.tickets[q.ticket0 + gt], 1);
-        s.last = n == q.splits - 1;
-        if (s.last) p.tickets[q.ticket0 + gt] = 0;
-    }
-    __syncthreads();
-    if (!s.last) return;
-    __threadfence();
-    const int first = q.part_row0 + gt * q.splits * p.part_rows;
-    const float2 *ml = reinterpret_cast<const float2 *>(p.part + p.part_cap * D);
-    for (int at = tid; at < mrows * (D / 2); at += THREADS) {
-        const int m = at / (D / 2), d = (at % (D / 2)) * 2;
-        float M = -INFINITY;
-        for (int i = 0; i < q.splits; ++i) M = fmaxf(M, __ldcg(&ml[first + i * p.part_rows + m]).x);
-        const float use = M == -INFINITY ? 0.f : M;
-        float L = 0.f, x = 0.f, y = 0.f;
-        for (int i = 0; i < q.splits; ++i) {
-            const int row = first + i * p.part_rows + m;
-            const float2 c = __ldcg(&ml[row]);
-            const float f = ex2(c.x - use);
-            if (c.y == 0.f || (f == 0.f && c.y == c.y)) continue; // nothing seen there, or nothing left of it
-            L = fmaf(c.y, f, L);
-            const float2 v = __ldcg(reinterpret_cast<const float2 *>(p.part + (int64_t)row * D + d));
-            x = fmaf(v.x, f, x);
-            y = fmaf(v.y, f, y);
-        }
-        const int t = (m0 + m) / p.r, j = (m0 + m) % p.r;
-        const int64_t head = ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        store2(p.out, p.act, head * D + d, x * inv, y * inv);
-        if (p.lse && d == 0) p.lse[head] = L == 0.f ? -INFINITY : M * 0.6931471805599453f + logf(L);
-    }
+    join_parts<D, THREADS>(p, q, g, m0, mrows, parts, q.ticket0 + unit - q.whole,
+                           q.part_row0 + (unit - q.whole) * q.splits * p.part_rows, &s.last);
 }
 
 template <int D, int KT, int VT, int WM, bool LO> cudaError_t go(const BlockParams &p, cudaStream_t st) {

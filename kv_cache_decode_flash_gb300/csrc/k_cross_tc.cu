@@ -1,0 +1,742 @@
+// k_cross_tc.cu - the block attention for 16-bit queries on the fifth
+// generation's tensor cores (tcgen05): same items, masks and results as
+// k_cross.cu, whose comment has the definition.
+//
+// One CTA per SM, 13 warps: two groups of four softmax warps (one thread owns a
+// query row), one group of four warps that brings the cached rows, one thread
+// that issues the products.  Steps are 128 cached rows:
+//   S = Q K^T    128 x 128 x D, both operands fp16 in shared memory, S in TMEM;
+//   O += P V     P (fp16) written over S in TMEM, V from shared memory, O stays in TMEM.
+// Two jobs are always in flight, so that one's softmax runs under the other's
+// products.  A query tile of more than 128 rows is two halves that share every
+// step (job 2s + h: step s, half h); a smaller one is one half whose even and odd
+// steps run apart, with sums of their own that are joined at the end.
+//
+// What comes from the cache is turned into fp16 on the way to shared memory:
+// halves as they are (cp.async), codes times their block's scale, rounded once
+// to 11 bits (a choice that fits results of 8 or 11 bits; P is rounded to as
+// many).  Scales may lie anywhere in fp16's range, their products need not: a
+// step's K is scaled by a power of two that brings its largest scale to
+// [2^7, 2^8), undone in the score's factor; V's exponent is that of the largest
+// scale met so far, and O is rescaled when it grows.
+// The softmax rescales O only when a row's maximum has grown by more than 2^8
+// since the last time (P <= 2^8 then, well inside fp16, and the final quotient
+// is the same), so O is hardly ever read back before the end.
+#include "block_tile.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr int TM = 128;      // query rows of a half
+constexpr int TN = 128;      // cached rows of a step
+constexpr int THREADS = 416; // 8 softmax warps, 4 loading warps, 1 issuing warp
+constexpr int W_LOAD = 8, W_MMA = 12;
+constexpr int LOADERS = 128;
+constexpr int SLOTS = 4; // steps whose factors are kept: a step's are overwritten four steps later
+constexpr int E_MIN = -24;
+constexpr uint32_t WAIT_LIMIT = 1u << 26;
+constexpr uint64_t WAIT_NS = 2000000000ull;
+constexpr float GROW = 8.f; // log2 growth of a maximum that is let pass before O is rescaled
+constexpr uint32_t TMEM_COLS = 512;
+
+enum Bar { KF0, KF1, KE0, KE1, VF0, VF1, VE0, VE1, SF0, SF1, PF0, PF1, OD0, OD1, DRAIN, N_BARS };
+
+template <int D> struct Lay {
+    static constexpr int REG = TN * 128;          // a region: 128 rows of 64 fp16, 128-byte swizzled
+    static constexpr int TILE = D / 64 * REG;     // bytes of a 128-row tile of fp16
+    static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, AUX = 6 * TILE;
+};
+
+struct Aux {
+    uint64_t bar[N_BARS];
+    int32_t row[2][TN];          // pool rows of a step, -1 past the end
+    float qscale[2 * TM];
+    int32_t vis[2 * TM];
+    float kfac[SLOTS];           // score factor of the step's K exponent
+    int32_t vexp[SLOTS];         // V's exponent as of the step
+    int32_t bad[SLOTS];          // V values of the step that are not finite were left out
+    uint32_t badrow[SLOTS][TN / 32];
+    uint32_t red[2][2][LOADERS / 32];
+    float2 ml[2][TM];
+    uint32_t tmem;
+    int32_t vis_max, vis_min, any_bad, last;
+    volatile int32_t abort;
+};
+
+template <int D> constexpr int smem_bytes() {
+    // TMEM is allocated whole: one CTA per SM, whatever D
+    const int need = Lay<D>::AUX + (int)sizeof(Aux) + 2 * TM * (D / 16) * 4 + 1024;
+    return need > 120 * 1024 ? need : 120 * 1024;
+}
+
+// ---------------------------------------------------------------- PTX ----
+__device__ __forceinline__ void bar_init(uint64_t *b, unsigned n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t *b, unsigned parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(smem_u32(b)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ uint64_t now_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// Bounded: gives up after WAIT_NS (reported, and every other wait of the CTA gives up too).  Nothing is skipped then:
+// the loops run on over whatever the tiles hold, inside their buffers, so that every barrier is met and the CTA ends.
+__device__ __noinline__ void bar_wait_slow(uint64_t *b, unsigned parity, uint32_t *err, Aux *x) {
+    const uint64_t t0 = now_ns();
+    for (uint32_t i = 0; i < WAIT_LIMIT; ++i) {
+        if (bar_try(b, parity) || x->abort) return;
+        if (now_ns() - t0 > WAIT_NS) break;
+    }
+    atomicOr(err, ERR_WAIT_TIMEOUT);
+    x->abort = 1;
+}
+__device__ __forceinline__ void bar_wait(uint64_t *b, unsigned parity, uint32_t *err, Aux *x) {
+    if (!bar_try(b, parity)) bar_wait_slow(b, parity, err, x);
+}
+// The same for a whole warp that goes on to a warp-wide TMEM access.
+__device__ __forceinline__ void bar_wait_warp(uint64_t *b, unsigned parity, uint32_t *err, Aux *x) {
+    bar_wait(b, parity, err, x);
+    __syncwarp();
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t *b) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 32 columns of the warp's 32 lanes: a thread has its own row.
+__device__ __forceinline__ void tm_ld32(float (&v)[32], uint32_t a) {
+    uint32_t r[32];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(a)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tm_st32(uint32_t a, const float (&v)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+                 "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
+                 "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+                 "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15])),
+                 "r"(__float_as_uint(v[16])), "r"(__float_as_uint(v[17])), "r"(__float_as_uint(v[18])), "r"(__float_as_uint(v[19])),
+                 "r"(__float_as_uint(v[20])), "r"(__float_as_uint(v[21])), "r"(__float_as_uint(v[22])), "r"(__float_as_uint(v[23])),
+                 "r"(__float_as_uint(v[24])), "r"(__float_as_uint(v[25])), "r"(__float_as_uint(v[26])), "r"(__float_as_uint(v[27])),
+                 "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])), "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
+                 : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+                 "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+                 : "memory");
+}
+
+// Shared-memory operand descriptor: 128-byte swizzle; sbo: bytes between groups of 8 rows; lbo: bytes between 64-wide
+// blocks of the strided dimension (used by V, whose rows are the products' inner dimension).
+__device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lbo) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)((lbo >> 4) & 0x3fffu) << 16 | (uint64_t)(1024u >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// fp16 x fp16 -> fp32, 128 x n; bit 16: the second operand's rows are the inner dimension.
+__device__ __forceinline__ constexpr uint32_t inst(int n, bool b_mn) {
+    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n / 8) << 17) | ((uint32_t)(TM / 16) << 24);
+}
+
+// Byte of (row, column) of an fp16 tile: regions of 64 columns, rows of 128 bytes, 16-byte pieces swizzled by row.
+template <int D> __device__ __forceinline__ uint32_t at(int row, int col) {
+    return (uint32_t)((col >> 6) * Lay<D>::REG + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4) + (col & 7) * 2);
+}
+
+__device__ __forceinline__ void loaders_sync() { asm volatile("bar.sync 1, %0;" ::"n"(LOADERS) : "memory"); }
+
+// ------------------------------------------------------------- loading ----
+// The loading threads' share of one tensor's rows of a step, in registers.
+template <int D, int T> struct Raw {
+    static constexpr int RB = row_bytes<T>(D), PIECES = RB / 16; // 16-byte pieces of a row: one of them is the thread's, in
+    uint4 u[PIECES];                                              // every (128 / PIECES)-th row
+    uint16_t s[PIECES];
+    __device__ __forceinline__ void load(const uint8_t *data, const uint16_t *scales, const int32_t *row, int t) {
+        const int c = t % PIECES;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int32_t R = row[t / PIECES + i * (LOADERS / PIECES)];
+            u[i] = make_uint4(0, 0, 0, 0);
+            s[i] = 0;
+            if (R >= 0) {
+                u[i] = __ldg(reinterpret_cast<const uint4 *>(data + (int64_t)R * RB) + c);
+                s[i] = __ldg(scales + (int64_t)R * (D / QK) + (T == KVC_Q4_0 ? c : c / 2));
+            }
+        }
+    }
+    // largest finite magnitude of the scales, as fp16 bits; a scale that is not finite becomes 0 and is reported
+    __device__ __forceinline__ uint32_t top(bool drop, uint32_t *badrow, int t) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const uint32_t a = s[i] & 0x7fffu;
+            if (a >= 0x7c00u) {
+                if (drop) {
+                    s[i] = 0;
+                    const int j = t / PIECES + i * (LOADERS / PIECES);
+                    atomicOr(&badrow[j >> 5], 1u << (j & 31));
+                }
+            } else {
+                m = max(m, a);
+            }
+        }
+        return m;
+    }
+    // value = code * scale * 2^up, rounded once
+    __device__ __forceinline__ void store(uint8_t *tile, float up, int t) const {
+        const int c = t % PIECES;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int j = t / PIECES + i * (LOADERS / PIECES);
+            const __half2 d = __half2half2(__float2half_rn(__half2float(__ushort_as_half(s[i])) * up));
+            auto put = [&](int col, uint2 a, uint2 b) {
+                uint4 o;
+                *reinterpret_cast<__half2 *>(&o.x) = __hmul2(*reinterpret_cast<__half2 *>(&a.x), d);
+                *reinterpret_cast<__half2 *>(&o.y) = __hmul2(*reinterpret_cast<__half2 *>(&a.y), d);
+                *reinterpret_cast<__half2 *>(&o.z) = __hmul2(*reinterpret_cast<__half2 *>(&b.x), d);
+                *reinterpret_cast<__half2 *>(&o.w) = __hmul2(*reinterpret_cast<__half2 *>(&b.y), d);
+                *reinterpret_cast<uint4 *>(tile + at<D>(j, col)) = o;
+            };
+            if constexpr (T == KVC_Q8_0) {
+                put(c * 16, codes4(u[i].x), codes4(u[i].y));
+                put(c * 16 + 8, codes4(u[i].z), codes4(u[i].w));
+            } else {
+                put(c * 32, nibbles4(u[i].x), nibbles4(u[i].y));
+                put(c * 32 + 8, nibbles4(u[i].z), nibbles4(u[i].w));
+                put(c * 32 + 16, nibbles4(u[i].x >> 4), nibbles4(u[i].y >> 4));
+                put(c * 32 + 24, nibbles4(u[i].z >> 4), nibbles4(u[i].w >> 4));
+            }
+        }
+    }
+};
+
+// f16 rows go straight to shared memory.
+template <int D> __device__ __forceinline__ void copy_halves(uint8_t *tile, const uint8_t *data, const int32_t *row, int t) {
+    constexpr int PIECES = D / 8;
+    const int c = t % PIECES;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int j = t / PIECES + i * (LOADERS / PIECES);
+        const int32_t R = row[j];
+        const uint8_t *src = data + (int64_t)max(R, 0) * (2 * D) + c * 16;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(tile) + at<D>(j, c * 8)), "l"(src),
+                     "r"(R >= 0 ? 16 : 0)
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// The thread's own pieces of a V tile: values that are not finite become 0, their rows are reported.
+template <int D> __device__ __forceinline__ void drop_halves(uint8_t *tile, uint32_t *badrow, int t) {
+    constexpr int PIECES = D / 8;
+    const int c = t % PIECES;
+#pragma unroll 4
+    for (int i = 0; i < PIECES; ++i) {
+        const int j = t / PIECES + i * (LOADERS / PIECES);
+        uint4 *q = reinterpret_cast<uint4 *>(tile + at<D>(j, c * 8));
+        uint4 u = *q;
+        bool b = drop_nonfinite(u.x);
+        b |= drop_nonfinite(u.y);
+        b |= drop_nonfinite(u.z);
+        b |= drop_nonfinite(u.w);
+        if (b) {
+            *q = u;
+            atomicOr(&badrow[j >> 5], 1u << (j & 31));
+        }
+    }
+}
+
+// ------------------------------------------------------------- kernel ----
+template <int D, int KT, int VT>
+__global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_constant__ BlockParams p) {
+    using L = Lay<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u); // swizzled tiles need 1024-byte alignment
+    Aux &x = *reinterpret_cast<Aux *>(smem + L::AUX);
+    uint32_t(*poison)[D / 16] = reinterpret_cast<uint32_t(*)[D / 16]>(smem + L::AUX + sizeof(Aux));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    const BlockSeq q = p.seq[item_seq(p, (int)blockIdx.x)];
+    const int local = (int)blockIdx.x - q.item0;
+    int unit, part, parts;
+    item_unit(q, local, unit, part, parts);
+    const int g = unit / q.tiles, tile = q.tiles - 1 - unit % q.tiles; // later tokens see more: they begin first
+    const int m_all = q.n_tok * p.r, m0 = tile * 2 * TM, mrows = min(2 * TM, m_all - m0);
+    const bool wide = mrows > TM;
+
+    if (tid == 0) {
+        for (int i = 0; i < N_BARS; ++i) {
+            const bool load = i == KF0 || i == KF1 || i == VF0 || i == VF1;
+            bar_init(&x.bar[i], load ? LOADERS : (i == PF0 || i == PF1 ? TM : 1));
+        }
+        x.vis_max = 0;
+        x.vis_min = 0x7fffffff;
+        x.any_bad = 0;
+        x.abort = 0;
+        for (int i = 0; i < SLOTS; ++i) {
+            x.bad[i] = 0;
+            for (int k = 0; k < TN / 32; ++k) x.badrow[i][k] = 0;
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == W_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&x.tmem)), "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    __syncthreads();
+    // query rows (a warp each), normalised by a power of two that takes the scale's sign too
+    for (int m = warp; m < (wide ? 2 * TM : TM); m += THREADS / 32) {
+        uint32_t h[D / 64], l[D / 64];
+        float scale;
+        const int vis = query_row<D, false>(p, q, g, m < mrows ? m0 + m : m_all, m_all, lane, h, l, &scale);
+        if (scale < 0.f) {
+            scale = -scale;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) h[i] ^= 0x80008000u;
+        }
+        uint8_t *dst = smem + L::Q + (m >> 7) * L::TILE + at<D>(m & 127, lane * (D / 32));
+        if constexpr (D == 128)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(h[0], h[1]);
+        else
+            *reinterpret_cast<uint32_t *>(dst) = h[0];
+        if (lane == 0) {
+            x.qscale[m] = scale;
+            x.vis[m] = vis;
+            if (m < mrows) {
+                atomicMax(&x.vis_max, vis);
+                atomicMin(&x.vis_min, vis);
+            }
+        }
+        if (lane < D / 16) poison[m][lane] = 0;
+    }
+    fence_async();
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tm = x.tmem;
+    const uint32_t tS = tm, tO = tm + 256; // S0, S1: 128 columns each (P over them); O0, O1: D columns each
+    const int r0 = part * q.split_rows;
+    const int r1 = parts == 1 ? x.vis_max : min(r0 + q.split_rows, x.vis_max);
+    const int steps = r1 > r0 ? (r1 - r0 + TN - 1) / TN : 0;
+    const int jobs = wide ? 2 * steps : steps;
+    const int vis_min = x.vis_min;
+
+    float mx = -INFINITY, sum = 0.f; // softmax threads: the row's reference maximum and sum
+    int E = E_MIN;
+    if (warp < W_LOAD) {
+        // -------------------------------------------------- softmax of half h
+        const int h = warp >> 2, mr = wide ? tid : (tid & 127);
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21; // TMEM lane 32 * (warp % 4)
+        const uint32_t S = tS + h * 128 + lanes, O = tO + h * D + lanes;
+        const bool live = __any_sync(0xffffffffu, mr < mrows);
+        const float cq = x.qscale[mr];
+        const int vis = mr < mrows ? x.vis[mr] : 0x7fffffff;
+        const int wvis = __reduce_min_sync(0xffffffffu, vis);
+        int k = 0; // jobs of this half done
+        for (int i = h; i < jobs; i += 2, ++k) {
+            const int s = wide ? i >> 1 : i, base = r0 + s * TN, slot = s % SLOTS;
+            bar_wait_warp(&x.bar[SF0 + h], k & 1, p.err, &x);
+            tc_after();
+            if (live) {
+                const bool masked = base + TN > wvis;
+                const float f = cq * x.kfac[slot];
+                float raw = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v[32];
+                    tm_ld32(v, S + c * 32);
+                    tm_wait_ld();
+                    if (masked) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) raw = base + c * 32 + e < vis ? fmaxf(raw, v[e]) : raw;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) raw = fmaxf(raw, v[e]);
+                    }
+                }
+                const float top = raw == -INFINITY ? raw : raw * f;
+                float al = 1.f;
+                if (top > mx + GROW || (mx == -INFINITY && top > mx)) {
+                    al = ex2(mx - top); // 0 for a first maximum
+                    mx = top;
+                }
+                sum *= al;
+                if (VT != KVC_F16) {
+                    const int e = x.vexp[slot];
+                    if (e != E) al *= ldexpf(1.f, max(E - e, -126));
+                    E = e;
+                }
+                if (k > 0 && __any_sync(0xffffffffu, al != 1.f)) {
+                    bar_wait_warp(&x.bar[OD0 + h], (k - 1) & 1, p.err, &x);
+                    tc_after();
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        float v[32];
+                        tm_ld32(v, O + c * 32);
+                        tm_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] *= al;
+                        tm_st32(O + c * 32, v);
+                    }
+                }
+                bool marks = false; // V values of rows that some token does not see, and that are not finite
+                if (base + TN > vis_min) {
+                    if (VT == KVC_F16) bar_wait_warp(&x.bar[VF0 + (s & 1)], (s >> 1) & 1, p.err, &x);
+                    marks = x.bad[slot] != 0;
+                }
+                const float use = mx == -INFINITY ? 0.f : mx;
+                float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v[32];
+                    tm_ld32(v, S + c * 32);
+                    tm_wait_ld();
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float y = fmaf(v[e], f, -use);
+                        if (masked) y = base + c * 32 + e < vis ? y : -INFINITY;
+                        v[e] = ex2(y);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        a0 += v[e];
+                        a1 += v[e + 1];
+                        a2 += v[e + 2];
+                        a3 += v[e + 3];
+                        w[e / 2] = h2(v[e], v[e + 1]);
+                        w[e / 2 + 1] = h2(v[e + 2], v[e + 3]);
+                    }
+                    if (marks) {
+                        const uint32_t rows = x.badrow[slot][c];
+#pragma unroll 1
+                        for (int e = 0; e < 32; ++e) {
+                            if (!(rows >> e & 1)) continue;
+                            // the weight again from the score's rule: only rows that the token sees, and that count
+                            const bool seen = mr < mrows && base + c * 32 + e < vis;
+                            float pe = 0.f;
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) pe = y == e ? v[y] : pe;
+                            const int32_t R = pool_row(p, q, g, base + c * 32 + e);
+                            if (seen && pe > 0.f && R >= 0) {
+                                mark_poison<D, VT>(poison[mr], p.vdata, p.vs, R);
+                                x.any_bad = 1;
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    tm_st16(S + c * 16, w);
+                }
+                sum += (a0 + a1) + (a2 + a3);
+                tm_wait_st();
+            }
+            tc_before();
+            bar_arrive(&x.bar[PF0 + h]);
+        }
+        if (k > 0) bar_wait_warp(&x.bar[OD0 + h], (k - 1) & 1, p.err, &x);
+        tc_after();
+    } else if (warp < W_MMA) {
+        // -------------------------------------------------- cached rows
+        const int t = tid - W_LOAD * 32;
+        auto find_rows = [&](int s) { // pool rows of step s
+            const int j = r0 + s * TN + t;
+            x.row[s & 1][t] = s < steps ? pool_row(p, q, g, j) : -1;
+        };
+        if (steps > 0) {
+            find_rows(0);
+            loaders_sync();
+            if constexpr (KT == KVC_F16) {
+                // K and V tiles in turn: one is copied while the one before is waited for
+                auto tile_of = [&](int u) { return smem + (u & 1 ? L::V : L::K) + ((u >> 1) & 1) * L::TILE; };
+                auto empty = [&](int u) { return &x.bar[(u & 1 ? VE0 : KE0) + ((u >> 1) & 1)]; };
+                auto issue = [&](int u) {
+                    const int s = u >> 1;
+                    if (!(u & 1) && s + 1 < steps) find_rows(s + 1);
+                    copy_halves<D>(tile_of(u), u & 1 ? p.vdata : p.kdata, x.row[s & 1], t);
+                    if (u & 1) loaders_sync(); // the next step's rows are there, this step's are no longer read
+                };
+                int issued = 0;
+                const int units = 2 * steps;
+                for (int u = 0; u < units; ++u) {
+                    const int s = u >> 1;
+                    while (issued <= u || (issued == u + 1 && issued < units)) {
+                        // a stage is free once the products of two steps before are done
+                        const int n = issued, ns = n >> 1;
+                        if (ns >= 2) bar_wait(empty(n), ((ns >> 1) - 1) & 1, p.err, &x);
+                        issue(n);
+                        ++issued;
+                    }
+                    if (issued > u + 1)
+                        asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    else
+                        asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    if (u & 1) {
+                        const int slot = s % SLOTS;
+                        if (r0 + (s + 1) * TN > vis_min) {
+                            loaders_sync(); // the reports are cleared
+                            drop_halves<D>(tile_of(u), x.badrow[slot], t);
+                            loaders_sync();
+                            if (t == 0) x.bad[slot] = (x.badrow[slot][0] | x.badrow[slot][1] | x.badrow[slot][2] | x.badrow[slot][3]) != 0;
+                        }
+                    } else if (t < TN / 32) {
+                        x.badrow[s % SLOTS][t] = 0;
+                        if (t == 0) x.kfac[s % SLOTS] = 1.f, x.bad[s % SLOTS] = 0;
+                    }
+                    fence_async();
+                    bar_arrive(&x.bar[(u & 1 ? VF0 : KF0) + (s & 1)]);
+                }
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            } else {
+                Raw<D, KT> rk;
+                Raw<D, VT> rv;
+                rk.load(p.kdata, p.ks, x.row[0], t);
+                rv.load(p.vdata, p.vs, x.row[0], t);
+                int Ev = E_MIN;
+                for (int s = 0; s < steps; ++s) {
+                    const int slot = s % SLOTS;
+                    if (s + 1 < steps) find_rows(s + 1);
+                    if (t < TN / 32) x.badrow[slot][t] = 0;
+                    loaders_sync();
+                    // the step's largest scales give its exponents
+                    const uint32_t km = __reduce_max_sync(0xffffffffu, rk.top(false, nullptr, t));
+                    const uint32_t vm = __reduce_max_sync(0xffffffffu, rv.top(r0 + (s + 1) * TN > vis_min, x.badrow[slot], t));
+                    if (lane == 0) {
+                        x.red[s & 1][0][warp - W_LOAD] = km;
+                        x.red[s & 1][1][warp - W_LOAD] = vm;
+                    }
+                    loaders_sync();
+                    const uint32_t *a = x.red[s & 1][0], *b = x.red[s & 1][1];
+                    const uint32_t ka = max(max(a[0], a[1]), max(a[2], a[3])), va = max(max(b[0], b[1]), max(b[2], b[3]));
+                    const int ek = ka ? ilogbf(__half2float(__ushort_as_half((uint16_t)ka))) : E_MIN;
+                    if (va) Ev = max(Ev, ilogbf(__half2float(__ushort_as_half((uint16_t)va))));
+                    if (t == 0) {
+                        x.kfac[slot] = ldexpf(1.f, ek - 7);
+                        x.vexp[slot] = Ev;
+                        x.bad[slot] = (x.badrow[slot][0] | x.badrow[slot][1] | x.badrow[slot][2] | x.badrow[slot][3]) != 0;
+                    }
+                    if (s >= 2) bar_wait(&x.bar[KE0 + (s & 1)], ((s >> 1) - 1) & 1, p.err, &x);
+                    rk.store(smem + L::K + (s & 1) * L::TILE, ldexpf(1.f, 7 - ek), t);
+                    fence_async();
+                    bar_arrive(&x.bar[KF0 + (s & 1)]);
+                    if (s + 1 < steps) rk.load(p.kdata, p.ks, x.row[(s + 1) & 1], t);
+                    if (s >= 2) bar_wait(&x.bar[VE0 + (s & 1)], ((s >> 1) - 1) & 1, p.err, &x);
+                    rv.store(smem + L::V + (s & 1) * L::TILE, ldexpf(1.f, 7 - Ev), t);
+                    fence_async();
+                    bar_arrive(&x.bar[VF0 + (s & 1)]);
+                    if (s + 1 < steps) rv.load(p.vdata, p.vs, x.row[(s + 1) & 1], t);
+                }
+            }
+        }
+    } else if (lane == 0) {
+        // -------------------------------------------------- products
+        const uint32_t sq = smem_u32(smem + L::Q), sk = smem_u32(smem + L::K), sv = smem_u32(smem + L::V);
+        auto qk = [&](int i) { // job i's scores
+            const int s = wide ? i >> 1 : i, h = i & 1;
+            bar_wait(&x.bar[KF0 + (s & 1)], (s >> 1) & 1, p.err, &x);
+            tc_after();
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t o = (k >> 2) * L::REG + (k & 3) * 32;
+                mma_ss(tS + h * 128, desc(sq + (wide ? h * L::TILE : 0) + o, 16), desc(sk + (s & 1) * L::TILE + o, 16),
+                       inst(TN, false), k > 0);
+            }
+            tc_commit(&x.bar[SF0 + h]);
+            if (!wide || h) tc_commit(&x.bar[KE0 + (s & 1)]);
+        };
+        if (jobs > 0) qk(0);
+        if (jobs > 1) qk(1);
+        for (int i = 0; i < jobs; ++i) {
+            const int s = wide ? i >> 1 : i, h = i & 1, k0 = i >> 1; // k0: the half's job
+            bar_wait(&x.bar[VF0 + (s & 1)], (s >> 1) & 1, p.err, &x);
+            bar_wait(&x.bar[PF0 + h], k0 & 1, p.err, &x);
+            tc_after();
+#pragma unroll
+            for (int k = 0; k < TN / 16; ++k)
+                mma_ts(tO + h * D, tS + h * 128 + k * 8, desc(sv + (s & 1) * L::TILE + k * 2048, L::REG), inst(D, true),
+                       k0 > 0 || k > 0);
+            tc_commit(&x.bar[OD0 + h]);
+            if (!wide || h) tc_commit(&x.bar[VE0 + (s & 1)]);
+            if (i + 2 < jobs) qk(i + 2);
+        }
+        // nothing may be in flight when the CTA gives its memory back
+        tc_commit(&x.bar[DRAIN]);
+        const uint64_t t0 = now_ns();
+        while (!bar_try(&x.bar[DRAIN], 0) && now_ns() - t0 < WAIT_NS) {
+        }
+    }
+    __syncwarp();
+    tc_before();
+    __syncthreads();
+    tc_after();
+
+    // ---------------------------------------------------- results
+    const int h = warp >> 2;
+    const int mr = wide ? tid : (tid & 127);
+    const int done = jobs > h ? (jobs - h + 1) / 2 : 0; // jobs of the half
+    const uint32_t O = tO + (warp & 4 ? D : 0) + ((uint32_t)(warp & 3) << 21);
+    const bool live = warp < W_LOAD && __any_sync(0xffffffffu, mr < mrows);
+    float *join = reinterpret_cast<float *>(smem + L::K); // [TM][D + 4]: the odd steps' sums (K and V tiles are free)
+    constexpr int JP = D + 4;
+    const float back = VT == KVC_F16 ? 1.f : ldexpf(1.f, E - 7);
+    if (!wide && h == 1 && live) {
+        x.ml[1][mr] = make_float2(mx, sum);
+        if (done > 0) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                float v[32];
+                __syncwarp();
+                tm_ld32(v, O + c * 32);
+                tm_wait_ld();
+                if (mr < mrows) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4 *>(&join[mr * JP + c * 32 + e]) =
+                            make_float4(v[e] * back, v[e + 1] * back, v[e + 2] * back, v[e + 3] * back);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const bool whole = parts == 1;
+    const int prow = q.part_row0 + (local - q.whole) * p.part_rows;
+    if (live && (wide || h == 0)) {
+        float f0 = 1.f, f1 = 0.f;
+        bool two = false;
+        if (!wide && jobs > 1) { // the even and the odd steps' sums
+            const float2 o = x.ml[1][mr];
+            const float M = fmaxf(mx, o.x), use = M == -INFINITY ? 0.f : M;
+            f0 = ex2(mx - use);
+            f1 = ex2(o.x - use);
+            sum = sum * f0 + o.y * f1;
+            mx = M;
+            two = true;
+        }
+        const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+        const int m = m0 + mr, t = m / p.r, j = m - t * p.r;
+        const int64_t head = ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
+        const bool bad = x.any_bad != 0;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            float v[32];
+            __syncwarp();
+            if (done > 0) {
+                tm_ld32(v, O + c * 32);
+                tm_wait_ld();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = 0.f;
+            }
+            if (mr < mrows) {
+                const float s0 = back * f0;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = sum == 0.f ? 0.f : v[e] * s0;
+                if (two && sum != 0.f) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 y = *reinterpret_cast<const float4 *>(&join[mr * JP + c * 32 + e]);
+                        v[e] = fmaf(y.x, f1, v[e]);
+                        v[e + 1] = fmaf(y.y, f1, v[e + 1]);
+                        v[e + 2] = fmaf(y.z, f1, v[e + 2]);
+                        v[e + 3] = fmaf(y.w, f1, v[e + 3]);
+                    }
+                }
+                if (bad) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = poisoned(v[e], poison[mr][(c * 32 + e) / 16] >> (2 * (e % 16)) & 3u);
+                }
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint4 o;
+                        o.x = pack16(p.act, v[e] * inv, v[e + 1] * inv);
+                        o.y = pack16(p.act, v[e + 2] * inv, v[e + 3] * inv);
+                        o.z = pack16(p.act, v[e + 4] * inv, v[e + 5] * inv);
+                        o.w = pack16(p.act, v[e + 6] * inv, v[e + 7] * inv);
+                        *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) + head * D + c * 32 + e) = o;
+                    }
+                } else {
+                    float *dst = p.part + (int64_t)(prow + mr) * D + c * 32;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4 *>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                }
+            }
+        }
+        if (mr < mrows) {
+            if (whole) {
+                if (p.lse) p.lse[head] = sum == 0.f ? -INFINITY : mx * 0.6931471805599453f + logf(sum);
+            } else {
+                *reinterpret_cast<float2 *>(p.part + p.part_cap * D + 2 * (int64_t)(prow + mr)) = make_float2(mx, sum);
+            }
+        }
+    }
+    tc_before();
+    __syncthreads();
+    if (warp == W_MMA) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(TMEM_COLS));
+    }
+    if (whole) return;
+    join_parts<D, THREADS>(p, q, g, m0, mrows, parts, q.ticket0 + unit - q.whole,
+                           q.part_row0 + (unit - q.whole) * q.splits * p.part_rows, &x.last);
+}
+
+template <int D, int KT, int VT> cudaError_t go(const BlockParams &p, cudaStream_t st) {
+    auto k = cross_tc_kernel<D, KT, VT>;
+    constexpr int bytes = smem_bytes<D>();
+    static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    k<<<(unsigned)p.n_items, THREADS, bytes, st>>>(p);
+    return cudaGetLastError();
+}
+
+} // namespace
+
+cudaError_t launch_cross_tc(int type_k, int type_v, const BlockParams &p, cudaStream_t st) {
+    if (p.n_items <= 0) return cudaSuccess;
+    if (p.D == 64)
+        return type_k == KVC_F16 ? go<64, KVC_F16, KVC_F16>(p, st) : go<64, KVC_Q8_0, KVC_Q8_0>(p, st);
+    if (type_k == KVC_F16) return go<128, KVC_F16, KVC_F16>(p, st);
+    if (type_v == KVC_Q4_0) return go<128, KVC_Q8_0, KVC_Q4_0>(p, st);
+    return go<128, KVC_Q8_0, KVC_Q8_0>(p, st);
+}
+
+} // namespace kvc

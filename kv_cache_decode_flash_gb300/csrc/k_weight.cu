@@ -62,7 +62,13 @@ __global__ void __launch_bounds__(THREADS) weight_kernel(const __grid_constant__
         __syncthreads();
         for (int m = warp; m < MROWS; m += THREADS / 32) {
             float scale;
-            const int vis = query_row<D, LO>(p, q, g, m0 + m, m_all, lane, s.qhi[m], s.qlo[m], &scale);
+            uint32_t hi[D / 64], lo[D / 64];
+            const int vis = query_row<D, LO>(p, q, g, m0 + m, m_all, lane, hi, lo, &scale);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                *reinterpret_cast<uint32_t *>(&s.qhi[m][lane * (D / 32) + 2 * i]) = hi[i];
+                if (LO) *reinterpret_cast<uint32_t *>(&s.qlo[m][lane * (D / 32) + 2 * i]) = lo[i];
+            }
             if (lane == 0) {
                 s.qscale[m] = scale;
                 s.vis[m] = vis;

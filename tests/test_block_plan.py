@@ -20,10 +20,11 @@ def test_plans_cover_every_row_within_the_work_space(H, Hk, D, act):
         n_q = [int(x) for x in np.exp(rng.uniform(0, np.log(600), n_seq)).astype(int) - 1]
         p = _plan(H, Hk, D, act, rows, n_q)
         items = 0
-        for n, t, s, length in zip(rows, n_q, p["splits"], p["split_rows"]):
+        for n, t, w, s, length in zip(rows, n_q, p["whole"], p["splits"], p["split_rows"]):
             assert s >= 1 and length >= 1 and s * length >= n  # every row is in a part
-            assert s == 1 or (s - 1) * length < n              # and every part holds one
-            items += -(-t * r // p["tile_m"]) * Hk * s
+            units = -(-t * r // p["tile_m"]) * Hk
+            assert 0 <= w <= units and (s > 1 or w == units)
+            items += w + (units - w) * s
         assert items == p["items"]
         assert p["part_rows"] <= p["part_cap"] and p["tickets"] <= p["part_cap"]
 
