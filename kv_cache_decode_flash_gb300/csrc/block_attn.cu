@@ -52,11 +52,12 @@ static int ensure_block_space(Ctx *c, cudaStream_t st) {
 // Cut the cached rows of the launch's units into parts.  `want`: items that run
 // at once; a part has two steps at least (`least` rows), and the partial rows
 // of all parts fit the work space.
-//  One sequence: its units are alike, so those of the last, partly filled wave
-// are cut into as many parts as fill it, the others stay whole.
-//  Several: all rows are cut into parts of at most one length, chosen by a
-// model: an item costs `fixed` steps beside its own, and a schedule ends half
-// the longest item after the mean (or with the longest item, in one wave).
+// An item costs `fixed` steps beside its own.
+//  One sequence: its units are alike, so the schedule is whole waves; those of
+// the last one or two are cut into the parts that shorten it most.
+//  Several: all rows are cut into parts of at most one length, the one for
+// which a schedule ends first that ends half the longest item after the mean
+// (or, in one wave, with the longest item).
 static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t part_cap) {
     const int64_t least = 2 * step, fixed = 4;
     auto parts = [](const BlockSeq &s, int64_t len) {
@@ -67,10 +68,23 @@ static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t part
         if (p.seq[i].tiles) longest = std::max<int64_t>(longest, (p.seq[i].n_rows + step - 1) / step * step);
     if (p.n_seq == 1) {
         BlockSeq &s = p.seq[0];
-        const int64_t units = (int64_t)s.tiles * p.Hk, rest = units % want;
-        int64_t k = rest ? std::min<int64_t>({want / rest, s.n_rows / least, part_cap / (rest * p.part_rows)}) : 1;
-        s.splits = (int32_t)std::max<int64_t>(1, k);
-        s.whole = (int32_t)(s.splits > 1 ? units - rest : units);
+        const int64_t units = (int64_t)s.tiles * p.Hk, steps = (s.n_rows + step - 1) / step;
+        const int64_t most = std::max<int64_t>(1, s.n_rows / least);
+        int64_t best_cost = INT64_MAX;
+        for (int64_t full = units / want * want; full >= 0; full = full > 0 ? full - want : -1) {
+            const int64_t rest = units - full;
+            if (rest > 2 * want) break;
+            for (int64_t k = 1; k <= std::min<int64_t>(most, rest ? std::max<int64_t>(8, want / rest) : 1); ++k) {
+                if (k > 1 && rest * k * p.part_rows > part_cap) break;
+                const int64_t cost = full / want * (steps + fixed) +
+                                     (rest * k + want - 1) / want * ((steps + k - 1) / k + fixed + (k > 1 ? 1 : 0));
+                if (cost < best_cost) {
+                    best_cost = cost;
+                    s.splits = (int32_t)k;
+                    s.whole = (int32_t)(k > 1 ? full : units);
+                }
+            }
+        }
     } else {
         double best = 0;
         int64_t best_len = longest;

@@ -126,14 +126,13 @@ __device__ __forceinline__ bool fill(__half (*dst)[D + TILE_PAD], const uint8_t 
 // a page that the pool does not have (reported).
 __device__ __forceinline__ int32_t pool_row(const BlockParams &p, const BlockSeq &q, int g, int j) {
     if (j >= q.n_rows) return -1;
-    const int64_t lr = (int64_t)q.off + j;
-    const int64_t pi = lr / p.P;
-    const int32_t page = pi < p.max_pages ? p.pt[(int64_t)q.id * p.max_pages + pi] : -1;
+    const uint32_t lr = (uint32_t)q.off + (uint32_t)j, pi = lr / (uint32_t)p.P;
+    const int32_t page = pi < (uint32_t)p.max_pages ? p.pt[(int64_t)q.id * p.max_pages + pi] : -1;
     if (page < 0 || page >= p.n_pages) {
         atomicOr(p.err, ERR_BAD_PAGE);
         return -1;
     }
-    return (int32_t)(((int64_t)page * p.Hk + g) * p.P + (lr - pi * p.P));
+    return (page * p.Hk + g) * p.P + (int32_t)(lr - pi * p.P); // rows of a layer's pool are fewer than 2^31
 }
 
 // The launch's sequence that work item `item` belongs to: the last one whose
@@ -233,7 +232,7 @@ __device__ float stored_value(const uint8_t *data, const uint16_t *scales, int32
 
 // The values of row R that are not finite, marked in the two-bit words of a query row that gives it weight.
 template <int D, int T>
-__device__ __noinline__ void mark_poison(uint32_t *words, const uint8_t *data, const uint16_t *scales, int32_t R) {
+__device__ __forceinline__ void mark_poison(uint32_t *words, const uint8_t *data, const uint16_t *scales, int32_t R) {
     for (int d = 0; d < D; ++d) {
         const float x = stored_value<D, T>(data, scales, R, d);
         if (fabsf(x) <= 3.4e38f) continue;
@@ -261,44 +260,90 @@ __device__ __forceinline__ void store2(void *out, int act, int64_t at, float a, 
         *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(out) + at) = pack16(act, a, b);
 }
 
-// The end of an item that is a part of its tile's rows (all threads of the CTA, whose partial rows are written): the
-// part that arrives last joins the tile's parts, in their order.
-template <int D, int NTHREADS>
+// The end of an item that is a part of its tile's rows (NTHREADS threads of the CTA, the first ones, which wrote its
+// partial rows; sync: their barrier): the part that arrives last joins the tile's parts, in their order.
+template <int D, int NTHREADS, class Sync>
 __device__ __forceinline__ void join_parts(const BlockParams &p, const BlockSeq &q, int g, int m0, int mrows, int parts,
-                                           int ticket, int first, int32_t *last) {
+                                           int ticket, int first, int32_t *last, Sync sync) {
     const int tid = threadIdx.x;
     __threadfence();
-    __syncthreads();
+    sync();
     if (tid == 0) {
         const int n = atomicAdd(&p.tickets[ticket], 1);
         *last = n == parts - 1;
         if (*last) p.tickets[ticket] = 0;
     }
-    __syncthreads();
+    sync();
     if (!*last) return;
     __threadfence();
+    // A warp joins ROWS query rows at a time, a lane D / 32 columns of them: what bounds this is the latency of the
+    // loads, so all of a few parts' are on their way together.
+    constexpr int V = D / 32, ROWS = 4, STEP = 2;
     const float2 *ml = reinterpret_cast<const float2 *>(p.part + p.part_cap * D);
-    for (int at = tid; at < mrows * (D / 2); at += NTHREADS) {
-        const int m = at / (D / 2), d = (at % (D / 2)) * 2;
-        float M = -INFINITY;
-        for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(&ml[first + i * p.part_rows + m]).x);
-        const float use = M == -INFINITY ? 0.f : M;
-        float L = 0.f, x = 0.f, y = 0.f;
-        for (int i = 0; i < parts; ++i) {
-            const int row = first + i * p.part_rows + m;
-            const float2 c = __ldcg(&ml[row]);
-            const float f = ex2(c.x - use);
-            if (c.y == 0.f || (f == 0.f && c.y == c.y)) continue; // nothing seen there, or nothing left of it
-            L = fmaf(c.y, f, L);
-            const float2 v = __ldcg(reinterpret_cast<const float2 *>(p.part + (int64_t)row * D + d));
-            x = fmaf(v.x, f, x);
-            y = fmaf(v.y, f, y);
+    const int lane = tid & 31;
+    for (int mb = (tid >> 5) * ROWS; mb < mrows; mb += NTHREADS / 32 * ROWS) {
+        float M[ROWS], L[ROWS], o[ROWS][V];
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            M[k] = -INFINITY;
+            L[k] = 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[k][e] = 0.f;
         }
-        const int t = (m0 + m) / p.r, j = (m0 + m) % p.r;
-        const int64_t head = ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        store2(p.out, p.act, head * D + d, x * inv, y * inv);
-        if (p.lse && d == 0) p.lse[head] = L == 0.f ? -INFINITY : M * 0.6931471805599453f + logf(L);
+        for (int i = lane; i < parts; i += 32) {
+#pragma unroll
+            for (int k = 0; k < ROWS; ++k)
+                M[k] = fmaxf(M[k], __ldcg(&ml[first + i * p.part_rows + min(mb + k, mrows - 1)]).x);
+        }
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+#pragma unroll
+            for (int x = 16; x; x >>= 1) M[k] = fmaxf(M[k], __shfl_xor_sync(0xffffffffu, M[k], x));
+            if (M[k] == -INFINITY) M[k] = 0.f;
+        }
+        for (int i0 = 0; i0 < parts; i0 += STEP) {
+            float2 c[STEP][ROWS];
+            float v[STEP][ROWS][V];
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) {
+#pragma unroll
+                for (int k = 0; k < ROWS; ++k) {
+                    const int64_t row = first + (int64_t)min(i0 + i, parts - 1) * p.part_rows + min(mb + k, mrows - 1);
+                    c[i][k] = __ldcg(&ml[row]);
+                    if constexpr (V == 4) {
+                        const float4 f = __ldcg(reinterpret_cast<const float4 *>(p.part + row * D) + lane);
+                        v[i][k][0] = f.x, v[i][k][1] = f.y, v[i][k][2] = f.z, v[i][k][3] = f.w;
+                    } else {
+                        const float2 f = __ldcg(reinterpret_cast<const float2 *>(p.part + row * D) + lane);
+                        v[i][k][0] = f.x, v[i][k][1] = f.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) {
+                if (i0 + i >= parts) break;
+#pragma unroll
+                for (int k = 0; k < ROWS; ++k) {
+                    const float f = ex2(c[i][k].x - M[k]);
+                    // nothing seen there, or nothing left of it (its sums may be anything)
+                    if (c[i][k].y == 0.f || (f == 0.f && c[i][k].y == c[i][k].y)) continue;
+                    L[k] = fmaf(c[i][k].y, f, L[k]);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) o[k][e] = fmaf(v[i][k][e], f, o[k][e]);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            const int m = mb + k;
+            if (m >= mrows) continue;
+            const int t = (m0 + m) / p.r, j = (m0 + m) % p.r;
+            const int64_t head = ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
+            const float inv = L[k] == 0.f ? 0.f : 1.f / L[k];
+#pragma unroll
+            for (int e = 0; e < V; e += 2) store2(p.out, p.act, head * D + lane * V + e, o[k][e] * inv, o[k][e + 1] * inv);
+            if (p.lse && lane == 0) p.lse[head] = L[k] == 0.f ? -INFINITY : M[k] * 0.6931471805599453f + logf(L[k]);
+        }
     }
 }
 

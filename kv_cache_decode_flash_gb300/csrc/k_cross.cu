@@ -55,6 +55,12 @@ template <int D> struct Smem {
     int32_t last;
 };
 
+// (out of line: the place that calls it is unrolled)
+template <int D, int T>
+__device__ __noinline__ void mark_row(uint32_t *words, const uint8_t *data, const uint16_t *scales, int32_t R) {
+    mark_poison<D, T>(words, data, scales, R);
+}
+
 // WM: warps along the query rows (16 each); the 4 / WM warps of a row block
 // share a step's cached rows and are joined at the end.  LO: 32-bit queries.
 template <int D, int KT, int VT, int WM, bool LO>
@@ -200,7 +206,7 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
                 for (int k = 0; k < 4; ++k) {
                     const int jt = wn * NC + n * 8 + qc * 2 + (k & 1);
                     if (s.badrow[jt] && sc[n][k] > 0.f)
-                        mark_poison<D, VT>(s.poison[mrow + 8 * (k >> 1)], p.vdata, p.vs, s.row[jt]);
+                        mark_row<D, VT>(s.poison[mrow + 8 * (k >> 1)], p.vdata, p.vs, s.row[jt]);
                 }
             s.any_bad = 1;
         }
@@ -373,7 +379,7 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
     }
     if (whole) return;
     join_parts<D, THREADS>(p, q, g, m0, mrows, parts, q.ticket0 + unit - q.whole,
-                           q.part_row0 + (unit - q.whole) * q.splits * p.part_rows, &s.last);
+                           q.part_row0 + (unit - q.whole) * q.splits * p.part_rows, &s.last, [] { __syncthreads(); });
 }
 
 template <int D, int KT, int VT, int WM, bool LO> cudaError_t go(const BlockParams &p, cudaStream_t st) {

@@ -2,9 +2,9 @@
 // generation's tensor cores (tcgen05): same items, masks and results as
 // k_cross.cu, whose comment has the definition.
 //
-// One CTA per SM, 13 warps: two groups of four softmax warps (one thread owns a
-// query row), one group of four warps that brings the cached rows, one thread
-// that issues the products.  Steps are 128 cached rows:
+// One CTA per SM, 17 warps: two groups of four softmax warps (one thread owns a
+// query row), four warps that bring the rows' K and four that bring their V, one
+// thread that issues the products.  Steps are 128 cached rows:
 //   S = Q K^T    128 x 128 x D, both operands fp16 in shared memory, S in TMEM;
 //   O += P V     P (fp16) written over S in TMEM, V from shared memory, O stays in TMEM.
 // Two jobs are always in flight, so that one's softmax runs under the other's
@@ -29,9 +29,12 @@ namespace {
 
 constexpr int TM = 128;      // query rows of a half
 constexpr int TN = 128;      // cached rows of a step
-constexpr int THREADS = 416; // 8 softmax warps, 4 loading warps, 1 issuing warp
-constexpr int W_LOAD = 8, W_MMA = 12;
-constexpr int LOADERS = 128;
+constexpr int GROUP = 128;       // threads of a role: softmax of half 0, of half 1, K, V; then the issuing warp
+constexpr int THREADS = 5 * GROUP;
+// Registers: a launch gives every thread 96, which the loading groups keep; softmax takes what the issuing warp's group leaves.  (No function of
+// theirs may stay a call: its registers would have to fit the smallest role's.)
+constexpr int R_SOFT = 128, R_MMA = 24;
+static_assert(2 * R_SOFT + 2 * 96 + R_MMA <= 5 * 96, "the roles' registers come from the launch's");
 constexpr int SLOTS = 4; // steps whose factors are kept: a step's are overwritten four steps later
 constexpr int E_MIN = -24;
 constexpr uint32_t WAIT_LIMIT = 1u << 26;
@@ -49,15 +52,14 @@ template <int D> struct Lay {
 
 struct Aux {
     uint64_t bar[N_BARS];
-    int32_t row[2][TN];          // pool rows of a step, -1 past the end
+    int32_t row[2][SLOTS][TN];   // K's and V's loaders: pool rows of a step, -1 past the end
     float qscale[2 * TM];
     int32_t vis[2 * TM];
     float kfac[SLOTS];           // score factor of the step's K exponent
     int32_t vexp[SLOTS];         // V's exponent as of the step
-    int32_t bad[SLOTS];          // V values of the step that are not finite were left out
-    uint32_t badrow[SLOTS][TN / 32];
-    uint32_t red[2][2][LOADERS / 32];
-    float2 ml[2][TM];
+    uint32_t badrow[SLOTS][TN / 32]; // rows of the step whose V values that are not finite were left out
+    uint32_t red[2][2][GROUP / 32];
+    float2 ml[TM];
     uint32_t tmem;
     int32_t vis_max, vis_min, any_bad, last;
     volatile int32_t abort;
@@ -93,7 +95,7 @@ __device__ __forceinline__ uint64_t now_ns() {
 }
 // Bounded: gives up after WAIT_NS (reported, and every other wait of the CTA gives up too).  Nothing is skipped then:
 // the loops run on over whatever the tiles hold, inside their buffers, so that every barrier is met and the CTA ends.
-__device__ __noinline__ void bar_wait_slow(uint64_t *b, unsigned parity, uint32_t *err, Aux *x) {
+__device__ __forceinline__ void bar_wait_slow(uint64_t *b, unsigned parity, uint32_t *err, Aux *x) {
     const uint64_t t0 = now_ns();
     for (uint32_t i = 0; i < WAIT_LIMIT; ++i) {
         if (bar_try(b, parity) || x->abort) return;
@@ -128,19 +130,24 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
                  "r"(a), "l"(b), "r"(idesc), "r"(acc)
                  : "memory");
 }
-__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// 32 columns of the warp's 32 lanes: a thread has its own row.
-__device__ __forceinline__ void tm_ld32(float (&v)[32], uint32_t a) {
-    uint32_t r[32];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+// 32 columns of the warp's 32 lanes: a thread has its own row.  The values are there after tm_wait on them.
+__device__ __forceinline__ void tm_ld(uint32_t (&r)[32], uint32_t a) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]),"=r"(r[1]),"=r"(r[2]),"=r"(r[3]),"=r"(r[4]),"=r"(r[5]),"=r"(r[6]),"=r"(r[7]),"=r"(r[8]),"=r"(r[9]),"=r"(r[10]),"=r"(r[11]),"=r"(r[12]),"=r"(r[13]),"=r"(r[14]),"=r"(r[15]),"=r"(r[16]),"=r"(r[17]),"=r"(r[18]),"=r"(r[19]),"=r"(r[20]),"=r"(r[21]),"=r"(r[22]),"=r"(r[23]),"=r"(r[24]),"=r"(r[25]),"=r"(r[26]),"=r"(r[27]),"=r"(r[28]),"=r"(r[29]),"=r"(r[30]),"=r"(r[31])
                  : "r"(a)
                  : "memory");
+}
+__device__ __forceinline__ void tm_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]),"+r"(r[1]),"+r"(r[2]),"+r"(r[3]),"+r"(r[4]),"+r"(r[5]),"+r"(r[6]),"+r"(r[7]),"+r"(r[8]),"+r"(r[9]),"+r"(r[10]),"+r"(r[11]),"+r"(r[12]),"+r"(r[13]),"+r"(r[14]),"+r"(r[15]),"+r"(r[16]),"+r"(r[17]),"+r"(r[18]),"+r"(r[19]),"+r"(r[20]),"+r"(r[21]),"+r"(r[22]),"+r"(r[23]),"+r"(r[24]),"+r"(r[25]),"+r"(r[26]),"+r"(r[27]),"+r"(r[28]),"+r"(r[29]),"+r"(r[30]),"+r"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tm_ld32(float (&v)[32], uint32_t a) {
+    uint32_t r[32];
+    tm_ld(r, a);
+    tm_wait(r);
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
@@ -180,7 +187,37 @@ template <int D> __device__ __forceinline__ uint32_t at(int row, int col) {
     return (uint32_t)((col >> 6) * Lay<D>::REG + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4) + (col & 7) * 2);
 }
 
-__device__ __forceinline__ void loaders_sync() { asm volatile("bar.sync 1, %0;" ::"n"(LOADERS) : "memory"); }
+template <int ID, int N> __device__ __forceinline__ void named_sync() { asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
+template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Two 32-bit operations in one instruction, and the largest of three.
+__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) { return pair(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    uint32_t a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+    return make_float2(__uint_as_float(a), __uint_as_float(b));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 // ------------------------------------------------------------- loading ----
 // The loading threads' share of one tensor's rows of a step, in registers.
@@ -192,12 +229,16 @@ template <int D, int T> struct Raw {
         const int c = t % PIECES;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-            const int32_t R = row[t / PIECES + i * (LOADERS / PIECES)];
+            const int32_t R = row[t / PIECES + i * (GROUP / PIECES)];
             u[i] = make_uint4(0, 0, 0, 0);
             s[i] = 0;
-            if (R >= 0) {
-                u[i] = __ldg(reinterpret_cast<const uint4 *>(data + (int64_t)R * RB) + c);
-                s[i] = __ldg(scales + (int64_t)R * (D / QK) + (T == KVC_Q4_0 ? c : c / 2));
+            if (R >= 0) { // volatile: they are to be under way two steps ahead of their use, whatever registers that takes
+                asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(u[i].x), "=r"(u[i].y), "=r"(u[i].z), "=r"(u[i].w)
+                             : "l"(data + (int64_t)R * RB + c * 16));
+                asm volatile("ld.global.nc.u16 %0, [%1];"
+                             : "=h"(s[i])
+                             : "l"(scales + (int64_t)R * (D / QK) + (T == KVC_Q4_0 ? c : c / 2)));
             }
         }
     }
@@ -210,7 +251,7 @@ template <int D, int T> struct Raw {
             if (a >= 0x7c00u) {
                 if (drop) {
                     s[i] = 0;
-                    const int j = t / PIECES + i * (LOADERS / PIECES);
+                    const int j = t / PIECES + i * (GROUP / PIECES);
                     atomicOr(&badrow[j >> 5], 1u << (j & 31));
                 }
             } else {
@@ -224,7 +265,7 @@ template <int D, int T> struct Raw {
         const int c = t % PIECES;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-            const int j = t / PIECES + i * (LOADERS / PIECES);
+            const int j = t / PIECES + i * (GROUP / PIECES);
             const __half2 d = __half2half2(__float2half_rn(__half2float(__ushort_as_half(s[i])) * up));
             auto put = [&](int col, uint2 a, uint2 b) {
                 uint4 o;
@@ -253,7 +294,7 @@ template <int D> __device__ __forceinline__ void copy_halves(uint8_t *tile, cons
     const int c = t % PIECES;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-        const int j = t / PIECES + i * (LOADERS / PIECES);
+        const int j = t / PIECES + i * (GROUP / PIECES);
         const int32_t R = row[j];
         const uint8_t *src = data + (int64_t)max(R, 0) * (2 * D) + c * 16;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(tile) + at<D>(j, c * 8)), "l"(src),
@@ -268,7 +309,7 @@ template <int D> __device__ __forceinline__ void drop_halves(uint8_t *tile, uint
     const int c = t % PIECES;
 #pragma unroll 4
     for (int i = 0; i < PIECES; ++i) {
-        const int j = t / PIECES + i * (LOADERS / PIECES);
+        const int j = t / PIECES + i * (GROUP / PIECES);
         uint4 *q = reinterpret_cast<uint4 *>(tile + at<D>(j, c * 8));
         uint4 u = *q;
         bool b = drop_nonfinite(u.x);
@@ -280,6 +321,152 @@ template <int D> __device__ __forceinline__ void drop_halves(uint8_t *tile, uint
             atomicOr(&badrow[j >> 5], 1u << (j & 31));
         }
     }
+}
+
+// A loading group's work: tensor T's rows of every step (IS_V: V, else K) into its two stages.
+template <int D, int T, bool IS_V>
+__device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &q, int g, uint8_t *tiles, Aux &x, int r0, int steps,
+                                          int vis_min, int t) {
+    const uint8_t *data = IS_V ? p.vdata : p.kdata;
+    uint64_t *full = &x.bar[IS_V ? VF0 : KF0], *empty = &x.bar[IS_V ? VE0 : KE0];
+    int32_t(*row)[TN] = x.row[IS_V];
+    constexpr int SYNC = IS_V ? 4 : 3;
+    // the pool rows of a step: looked up one step before they are handed to the group, so that nobody waits for the table
+    int32_t next = -1;
+    auto look_up = [&](int s) { next = s < steps ? pool_row(p, q, g, r0 + s * TN + t) : -1; };
+    auto find = [&](int s) { // for all threads after the next barrier
+        row[s % SLOTS][t] = next;
+        look_up(s + 1);
+    };
+    auto clear = [&](int s) { // a step's reports; those of four steps before are read no more
+        if (IS_V && t < TN / 32) x.badrow[s % SLOTS][t] = 0;
+    };
+    auto wait_empty = [&](int s) {
+        if (s >= 2) bar_wait(&empty[s & 1], ((s >> 1) - 1) & 1, p.err, &x);
+    };
+    if (steps == 0) return;
+    look_up(0);
+    find(0);
+    find(1);
+    clear(0);
+    named_sync<SYNC, GROUP>();
+    if constexpr (T == KVC_F16) {
+        // a step's copies are under way while those of the step before are waited for
+        for (int s = 0; s <= steps; ++s) {
+            if (s < steps) {
+                wait_empty(s);
+                copy_halves<D>(tiles + (s & 1) * Lay<D>::TILE, data, row[s % SLOTS], t);
+                if (!IS_V && t == 0) x.kfac[s % SLOTS] = 1.f;
+            }
+            if (s > 0) {
+                if (s < steps)
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                else
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                if (IS_V && r0 + s * TN > vis_min)
+                    drop_halves<D>(tiles + ((s - 1) & 1) * Lay<D>::TILE, x.badrow[(s - 1) % SLOTS], t);
+                fence_async();
+                bar_arrive(&full[(s - 1) & 1]);
+            }
+            find(s + 2);
+            clear(s + 1);
+            named_sync<SYNC, GROUP>();
+        }
+    } else {
+        const uint16_t *scales = IS_V ? p.vs : p.ks;
+        Raw<D, T> raw[2];
+        raw[0].load(data, scales, row[0], t);
+        if (steps > 1) raw[1].load(data, scales, row[1], t);
+        int E = E_MIN;
+        auto step = [&](int s, Raw<D, T> &r) {
+            const int slot = s % SLOTS;
+            // the step's largest scale gives its exponent
+            const uint32_t m = __reduce_max_sync(0xffffffffu, r.top(IS_V && r0 + (s + 1) * TN > vis_min, x.badrow[slot], t));
+            if ((t & 31) == 0) x.red[IS_V][s & 1][t >> 5] = m;
+            find(s + 2);
+            clear(s + 1);
+            named_sync<SYNC, GROUP>();
+            const uint32_t *a = x.red[IS_V][s & 1];
+            const uint32_t top = max(max(a[0], a[1]), max(a[2], a[3]));
+            const int e = top ? ilogbf(__half2float(__ushort_as_half((uint16_t)top))) : E_MIN;
+            E = IS_V ? max(E, e) : e;
+            if (t == 0) {
+                if (IS_V)
+                    x.vexp[slot] = E;
+                else
+                    x.kfac[slot] = ldexpf(1.f, E - 7);
+            }
+            wait_empty(s);
+            r.store(tiles + (s & 1) * Lay<D>::TILE, ldexpf(1.f, 7 - E), t);
+            fence_async();
+            bar_arrive(&full[s & 1]);
+            if (s + 2 < steps) r.load(data, scales, row[(s + 2) % SLOTS], t);
+        };
+        for (int s = 0; s < steps; s += 2) {
+            step(s, raw[0]);
+            if (s + 1 < steps) step(s + 1, raw[1]);
+        }
+    }
+}
+
+// ------------------------------------------------------------ softmax ----
+// Largest of a thread's 128 scores (of those that it sees).
+template <bool MASK> __device__ __forceinline__ float row_max(uint32_t S, int n) {
+    uint32_t r[2][32];
+    float m0 = -INFINITY, m1 = -INFINITY;
+    tm_ld(r[0], S);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        tm_wait(r[c & 1]);
+        if (c < 3) tm_ld(r[(c + 1) & 1], S + (c + 1) * 32);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[k] = __uint_as_float(r[c & 1][e + k]);
+                if (MASK) v[k] = c * 32 + e + k < n ? v[k] : -INFINITY;
+            }
+            m0 = max3(m0, v[0], v[1]);
+            m1 = max3(m1, v[2], v[3]);
+        }
+    }
+    return fmaxf(m0, m1);
+}
+
+// exp2 of the scores (times f, less use) over them as fp16 pairs; returns their sum.  mark(c, v): a look at the 32
+// weights of column block c.
+template <bool MASK, class Mark> __device__ __forceinline__ float row_exp(uint32_t S, int n, float f, float use, Mark mark) {
+    uint32_t r[2][32];
+    const uint64_t ff = pair(f, f), mm = pair(-use, -use);
+    uint64_t a0 = 0, a1 = 0;
+    tm_ld(r[0], S);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        tm_wait(r[c & 1]);
+        if (c < 3) tm_ld(r[(c + 1) & 1], S + (c + 1) * 32);
+        float v[32];
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            float2 y = unpair(fma2(pair(r[c & 1][e], r[c & 1][e + 1]), ff, mm));
+            if (MASK) {
+                y.x = c * 32 + e < n ? y.x : -INFINITY;
+                y.y = c * 32 + e + 1 < n ? y.y : -INFINITY;
+            }
+            v[e] = ex2(y.x);
+            v[e + 1] = ex2(y.y);
+            w[e / 2] = h2(v[e], v[e + 1]);
+            if (e & 2)
+                a1 = add2(a1, pair(v[e], v[e + 1]));
+            else
+                a0 = add2(a0, pair(v[e], v[e + 1]));
+        }
+        mark(c, v);
+        tm_st16(S + c * 16, w);
+    }
+    const float2 s = unpair(add2(a0, a1));
+    return s.x + s.y;
 }
 
 // ------------------------------------------------------------- kernel ----
@@ -303,19 +490,15 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
     if (tid == 0) {
         for (int i = 0; i < N_BARS; ++i) {
             const bool load = i == KF0 || i == KF1 || i == VF0 || i == VF1;
-            bar_init(&x.bar[i], load ? LOADERS : (i == PF0 || i == PF1 ? TM : 1));
+            bar_init(&x.bar[i], load || i == PF0 || i == PF1 ? GROUP : 1);
         }
         x.vis_max = 0;
         x.vis_min = 0x7fffffff;
         x.any_bad = 0;
         x.abort = 0;
-        for (int i = 0; i < SLOTS; ++i) {
-            x.bad[i] = 0;
-            for (int k = 0; k < TN / 32; ++k) x.badrow[i][k] = 0;
-        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == W_MMA) {
+    if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&x.tmem)), "r"(TMEM_COLS)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -358,10 +541,9 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
     const int jobs = wide ? 2 * steps : steps;
     const int vis_min = x.vis_min;
 
-    float mx = -INFINITY, sum = 0.f; // softmax threads: the row's reference maximum and sum
-    int E = E_MIN;
-    if (warp < W_LOAD) {
+    if (warp < 8) {
         // -------------------------------------------------- softmax of half h
+        regs_inc<R_SOFT>();
         const int h = warp >> 2, mr = wide ? tid : (tid & 127);
         const uint32_t lanes = (uint32_t)(warp & 3) << 21; // TMEM lane 32 * (warp % 4)
         const uint32_t S = tS + h * 128 + lanes, O = tO + h * D + lanes;
@@ -369,28 +551,17 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
         const float cq = x.qscale[mr];
         const int vis = mr < mrows ? x.vis[mr] : 0x7fffffff;
         const int wvis = __reduce_min_sync(0xffffffffu, vis);
-        int k = 0; // jobs of this half done
-        for (int i = h; i < jobs; i += 2, ++k) {
+        float mx = -INFINITY, sum = 0.f; // the row's reference maximum and sum
+        int E = E_MIN;
+        int done = 0; // jobs of this half
+        for (int i = h; i < jobs; i += 2, ++done) {
             const int s = wide ? i >> 1 : i, base = r0 + s * TN, slot = s % SLOTS;
-            bar_wait_warp(&x.bar[SF0 + h], k & 1, p.err, &x);
+            bar_wait_warp(&x.bar[SF0 + h], done & 1, p.err, &x);
             tc_after();
             if (live) {
                 const bool masked = base + TN > wvis;
                 const float f = cq * x.kfac[slot];
-                float raw = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float v[32];
-                    tm_ld32(v, S + c * 32);
-                    tm_wait_ld();
-                    if (masked) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) raw = base + c * 32 + e < vis ? fmaxf(raw, v[e]) : raw;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) raw = fmaxf(raw, v[e]);
-                    }
-                }
+                const float raw = masked ? row_max<true>(S, vis - base) : row_max<false>(S, 0);
                 const float top = raw == -INFINITY ? raw : raw * f;
                 float al = 1.f;
                 if (top > mx + GROW || (mx == -INFINITY && top > mx)) {
@@ -398,173 +569,165 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
                     mx = top;
                 }
                 sum *= al;
+                // V's exponent, and whether some of its values were left out, are known once it is there
+                bar_wait_warp(&x.bar[VF0 + (s & 1)], (s >> 1) & 1, p.err, &x);
                 if (VT != KVC_F16) {
                     const int e = x.vexp[slot];
                     if (e != E) al *= ldexpf(1.f, max(E - e, -126));
                     E = e;
                 }
-                if (k > 0 && __any_sync(0xffffffffu, al != 1.f)) {
-                    bar_wait_warp(&x.bar[OD0 + h], (k - 1) & 1, p.err, &x);
+                if (done > 0 && __any_sync(0xffffffffu, al != 1.f)) {
+                    bar_wait_warp(&x.bar[OD0 + h], (done - 1) & 1, p.err, &x);
                     tc_after();
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         float v[32];
                         tm_ld32(v, O + c * 32);
-                        tm_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] *= al;
                         tm_st32(O + c * 32, v);
                     }
                 }
-                bool marks = false; // V values of rows that some token does not see, and that are not finite
-                if (base + TN > vis_min) {
-                    if (VT == KVC_F16) bar_wait_warp(&x.bar[VF0 + (s & 1)], (s >> 1) & 1, p.err, &x);
-                    marks = x.bad[slot] != 0;
-                }
                 const float use = mx == -INFINITY ? 0.f : mx;
-                float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float v[32];
-                    tm_ld32(v, S + c * 32);
-                    tm_wait_ld();
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float y = fmaf(v[e], f, -use);
-                        if (masked) y = base + c * 32 + e < vis ? y : -INFINITY;
-                        v[e] = ex2(y);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        a0 += v[e];
-                        a1 += v[e + 1];
-                        a2 += v[e + 2];
-                        a3 += v[e + 3];
-                        w[e / 2] = h2(v[e], v[e + 1]);
-                        w[e / 2 + 1] = h2(v[e + 2], v[e + 3]);
-                    }
-                    if (marks) {
+                if (!masked) {
+                    sum += row_exp<false>(S, 0, f, use, [](int, const float(&)[32]) {});
+                } else {
+                    sum += row_exp<true>(S, vis - base, f, use, [&](int c, const float(&v)[32]) {
                         const uint32_t rows = x.badrow[slot][c];
+                        if (rows == 0) return; // V values of rows that some token does not see, and that are not finite
 #pragma unroll 1
                         for (int e = 0; e < 32; ++e) {
                             if (!(rows >> e & 1)) continue;
-                            // the weight again from the score's rule: only rows that the token sees, and that count
-                            const bool seen = mr < mrows && base + c * 32 + e < vis;
-                            float pe = 0.f;
+                            float pe = 0.f; // the row's weight: 0 where it is not seen
 #pragma unroll
                             for (int y = 0; y < 32; ++y) pe = y == e ? v[y] : pe;
                             const int32_t R = pool_row(p, q, g, base + c * 32 + e);
-                            if (seen && pe > 0.f && R >= 0) {
+                            if (mr < mrows && pe > 0.f && R >= 0) {
                                 mark_poison<D, VT>(poison[mr], p.vdata, p.vs, R);
                                 x.any_bad = 1;
                             }
                         }
                         __syncwarp();
-                    }
-                    tm_st16(S + c * 16, w);
+                    });
                 }
-                sum += (a0 + a1) + (a2 + a3);
                 tm_wait_st();
             }
             tc_before();
             bar_arrive(&x.bar[PF0 + h]);
         }
-        if (k > 0) bar_wait_warp(&x.bar[OD0 + h], (k - 1) & 1, p.err, &x);
+        if (done > 0) bar_wait_warp(&x.bar[OD0 + h], (done - 1) & 1, p.err, &x);
         tc_after();
-    } else if (warp < W_MMA) {
-        // -------------------------------------------------- cached rows
-        const int t = tid - W_LOAD * 32;
-        auto find_rows = [&](int s) { // pool rows of step s
-            const int j = r0 + s * TN + t;
-            x.row[s & 1][t] = s < steps ? pool_row(p, q, g, j) : -1;
-        };
-        if (steps > 0) {
-            find_rows(0);
-            loaders_sync();
-            if constexpr (KT == KVC_F16) {
-                // K and V tiles in turn: one is copied while the one before is waited for
-                auto tile_of = [&](int u) { return smem + (u & 1 ? L::V : L::K) + ((u >> 1) & 1) * L::TILE; };
-                auto empty = [&](int u) { return &x.bar[(u & 1 ? VE0 : KE0) + ((u >> 1) & 1)]; };
-                auto issue = [&](int u) {
-                    const int s = u >> 1;
-                    if (!(u & 1) && s + 1 < steps) find_rows(s + 1);
-                    copy_halves<D>(tile_of(u), u & 1 ? p.vdata : p.kdata, x.row[s & 1], t);
-                    if (u & 1) loaders_sync(); // the next step's rows are there, this step's are no longer read
-                };
-                int issued = 0;
-                const int units = 2 * steps;
-                for (int u = 0; u < units; ++u) {
-                    const int s = u >> 1;
-                    while (issued <= u || (issued == u + 1 && issued < units)) {
-                        // a stage is free once the products of two steps before are done
-                        const int n = issued, ns = n >> 1;
-                        if (ns >= 2) bar_wait(empty(n), ((ns >> 1) - 1) & 1, p.err, &x);
-                        issue(n);
-                        ++issued;
+        // -------------------------------------------------- results
+        named_sync<2, 2 * GROUP>(); // both halves' products are done: the K and V tiles are free
+        float *join = reinterpret_cast<float *>(smem + L::K); // [TM][D + 4]: the odd steps' sums
+        constexpr int JP = D + 4;
+        const float back = VT == KVC_F16 ? 1.f : ldexpf(1.f, E - 7);
+        if (!wide && h == 1 && live) {
+            x.ml[mr] = make_float2(mx, sum);
+            if (done > 0) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    float v[32];
+                    __syncwarp();
+                    tm_ld32(v, O + c * 32);
+                    if (mr < mrows) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(&join[mr * JP + c * 32 + e]) =
+                                make_float4(v[e] * back, v[e + 1] * back, v[e + 2] * back, v[e + 3] * back);
                     }
-                    if (issued > u + 1)
-                        asm volatile("cp.async.wait_group 1;" ::: "memory");
-                    else
-                        asm volatile("cp.async.wait_group 0;" ::: "memory");
-                    if (u & 1) {
-                        const int slot = s % SLOTS;
-                        if (r0 + (s + 1) * TN > vis_min) {
-                            loaders_sync(); // the reports are cleared
-                            drop_halves<D>(tile_of(u), x.badrow[slot], t);
-                            loaders_sync();
-                            if (t == 0) x.bad[slot] = (x.badrow[slot][0] | x.badrow[slot][1] | x.badrow[slot][2] | x.badrow[slot][3]) != 0;
-                        }
-                    } else if (t < TN / 32) {
-                        x.badrow[s % SLOTS][t] = 0;
-                        if (t == 0) x.kfac[s % SLOTS] = 1.f, x.bad[s % SLOTS] = 0;
-                    }
-                    fence_async();
-                    bar_arrive(&x.bar[(u & 1 ? VF0 : KF0) + (s & 1)]);
-                }
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
-            } else {
-                Raw<D, KT> rk;
-                Raw<D, VT> rv;
-                rk.load(p.kdata, p.ks, x.row[0], t);
-                rv.load(p.vdata, p.vs, x.row[0], t);
-                int Ev = E_MIN;
-                for (int s = 0; s < steps; ++s) {
-                    const int slot = s % SLOTS;
-                    if (s + 1 < steps) find_rows(s + 1);
-                    if (t < TN / 32) x.badrow[slot][t] = 0;
-                    loaders_sync();
-                    // the step's largest scales give its exponents
-                    const uint32_t km = __reduce_max_sync(0xffffffffu, rk.top(false, nullptr, t));
-                    const uint32_t vm = __reduce_max_sync(0xffffffffu, rv.top(r0 + (s + 1) * TN > vis_min, x.badrow[slot], t));
-                    if (lane == 0) {
-                        x.red[s & 1][0][warp - W_LOAD] = km;
-                        x.red[s & 1][1][warp - W_LOAD] = vm;
-                    }
-                    loaders_sync();
-                    const uint32_t *a = x.red[s & 1][0], *b = x.red[s & 1][1];
-                    const uint32_t ka = max(max(a[0], a[1]), max(a[2], a[3])), va = max(max(b[0], b[1]), max(b[2], b[3]));
-                    const int ek = ka ? ilogbf(__half2float(__ushort_as_half((uint16_t)ka))) : E_MIN;
-                    if (va) Ev = max(Ev, ilogbf(__half2float(__ushort_as_half((uint16_t)va))));
-                    if (t == 0) {
-                        x.kfac[slot] = ldexpf(1.f, ek - 7);
-                        x.vexp[slot] = Ev;
-                        x.bad[slot] = (x.badrow[slot][0] | x.badrow[slot][1] | x.badrow[slot][2] | x.badrow[slot][3]) != 0;
-                    }
-                    if (s >= 2) bar_wait(&x.bar[KE0 + (s & 1)], ((s >> 1) - 1) & 1, p.err, &x);
-                    rk.store(smem + L::K + (s & 1) * L::TILE, ldexpf(1.f, 7 - ek), t);
-                    fence_async();
-                    bar_arrive(&x.bar[KF0 + (s & 1)]);
-                    if (s + 1 < steps) rk.load(p.kdata, p.ks, x.row[(s + 1) & 1], t);
-                    if (s >= 2) bar_wait(&x.bar[VE0 + (s & 1)], ((s >> 1) - 1) & 1, p.err, &x);
-                    rv.store(smem + L::V + (s & 1) * L::TILE, ldexpf(1.f, 7 - Ev), t);
-                    fence_async();
-                    bar_arrive(&x.bar[VF0 + (s & 1)]);
-                    if (s + 1 < steps) rv.load(p.vdata, p.vs, x.row[(s + 1) & 1], t);
                 }
             }
         }
-    } else if (lane == 0) {
+        named_sync<2, 2 * GROUP>();
+        const bool whole = parts == 1;
+        const int prow = q.part_row0 + (local - q.whole) * p.part_rows;
+        if (live && (wide || h == 0)) {
+            float f0 = 1.f, f1 = 0.f;
+            bool two = false;
+            if (!wide && jobs > 1) { // the even and the odd steps' sums
+                const float2 o = x.ml[mr];
+                const float M = fmaxf(mx, o.x), use = M == -INFINITY ? 0.f : M;
+                f0 = ex2(mx - use);
+                f1 = ex2(o.x - use);
+                sum = sum * f0 + o.y * f1;
+                mx = M;
+                two = true;
+            }
+            const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+            const int m = m0 + mr, t = m / p.r, j = m - t * p.r;
+            const int64_t head = ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
+            const bool bad = x.any_bad != 0;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                float v[32];
+                __syncwarp();
+                if (done > 0) {
+                    tm_ld32(v, O + c * 32);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                }
+                if (mr < mrows) {
+                    const float s0 = back * f0;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = sum == 0.f ? 0.f : v[e] * s0;
+                    if (two && sum != 0.f) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 y = *reinterpret_cast<const float4 *>(&join[mr * JP + c * 32 + e]);
+                            v[e] = fmaf(y.x, f1, v[e]);
+                            v[e + 1] = fmaf(y.y, f1, v[e + 1]);
+                            v[e + 2] = fmaf(y.z, f1, v[e + 2]);
+                            v[e + 3] = fmaf(y.w, f1, v[e + 3]);
+                        }
+                    }
+                    if (bad) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = poisoned(v[e], poison[mr][(c * 32 + e) / 16] >> (2 * (e % 16)) & 3u);
+                    }
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint4 o;
+                            o.x = pack16(p.act, v[e] * inv, v[e + 1] * inv);
+                            o.y = pack16(p.act, v[e + 2] * inv, v[e + 3] * inv);
+                            o.z = pack16(p.act, v[e + 4] * inv, v[e + 5] * inv);
+                            o.w = pack16(p.act, v[e + 6] * inv, v[e + 7] * inv);
+                            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) + head * D + c * 32 + e) = o;
+                        }
+                    } else {
+                        float *dst = p.part + (int64_t)(prow + mr) * D + c * 32;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    }
+                }
+            }
+            if (mr < mrows) {
+                if (whole) {
+                    if (p.lse) p.lse[head] = sum == 0.f ? -INFINITY : mx * 0.6931471805599453f + logf(sum);
+                } else {
+                    *reinterpret_cast<float2 *>(p.part + p.part_cap * D + 2 * (int64_t)(prow + mr)) = make_float2(mx, sum);
+                }
+            }
+        }
+        tc_before();
+        named_sync<2, 2 * GROUP>();
+        if (warp == 0) {
+            tc_after();
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(TMEM_COLS));
+        }
+        if (whole) return;
+        join_parts<D, 2 * GROUP>(p, q, g, m0, mrows, parts, q.ticket0 + unit - q.whole,
+                                 q.part_row0 + (unit - q.whole) * q.splits * p.part_rows, &x.last, [] { named_sync<2, 2 * GROUP>(); });
+    } else if (warp < 12) {
+        load_rows<D, KT, false>(p, q, g, smem + L::K, x, r0, steps, vis_min, tid - 2 * GROUP);
+    } else if (warp < 16) {
+        load_rows<D, VT, true>(p, q, g, smem + L::V, x, r0, steps, vis_min, tid - 3 * GROUP);
+    } else {
+        regs_dec<R_MMA>();
+        if (warp > 16 || lane > 0) return;
         // -------------------------------------------------- products
         const uint32_t sq = smem_u32(smem + L::Q), sk = smem_u32(smem + L::K), sv = smem_u32(smem + L::V);
         auto qk = [&](int i) { // job i's scores
@@ -601,121 +764,6 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
         while (!bar_try(&x.bar[DRAIN], 0) && now_ns() - t0 < WAIT_NS) {
         }
     }
-    __syncwarp();
-    tc_before();
-    __syncthreads();
-    tc_after();
-
-    // ---------------------------------------------------- results
-    const int h = warp >> 2;
-    const int mr = wide ? tid : (tid & 127);
-    const int done = jobs > h ? (jobs - h + 1) / 2 : 0; // jobs of the half
-    const uint32_t O = tO + (warp & 4 ? D : 0) + ((uint32_t)(warp & 3) << 21);
-    const bool live = warp < W_LOAD && __any_sync(0xffffffffu, mr < mrows);
-    float *join = reinterpret_cast<float *>(smem + L::K); // [TM][D + 4]: the odd steps' sums (K and V tiles are free)
-    constexpr int JP = D + 4;
-    const float back = VT == KVC_F16 ? 1.f : ldexpf(1.f, E - 7);
-    if (!wide && h == 1 && live) {
-        x.ml[1][mr] = make_float2(mx, sum);
-        if (done > 0) {
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                float v[32];
-                __syncwarp();
-                tm_ld32(v, O + c * 32);
-                tm_wait_ld();
-                if (mr < mrows) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4 *>(&join[mr * JP + c * 32 + e]) =
-                            make_float4(v[e] * back, v[e + 1] * back, v[e + 2] * back, v[e + 3] * back);
-                }
-            }
-        }
-    }
-    __syncthreads();
-    const bool whole = parts == 1;
-    const int prow = q.part_row0 + (local - q.whole) * p.part_rows;
-    if (live && (wide || h == 0)) {
-        float f0 = 1.f, f1 = 0.f;
-        bool two = false;
-        if (!wide && jobs > 1) { // the even and the odd steps' sums
-            const float2 o = x.ml[1][mr];
-            const float M = fmaxf(mx, o.x), use = M == -INFINITY ? 0.f : M;
-            f0 = ex2(mx - use);
-            f1 = ex2(o.x - use);
-            sum = sum * f0 + o.y * f1;
-            mx = M;
-            two = true;
-        }
-        const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-        const int m = m0 + mr, t = m / p.r, j = m - t * p.r;
-        const int64_t head = ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
-        const bool bad = x.any_bad != 0;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-            float v[32];
-            __syncwarp();
-            if (done > 0) {
-                tm_ld32(v, O + c * 32);
-                tm_wait_ld();
-            } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = 0.f;
-            }
-            if (mr < mrows) {
-                const float s0 = back * f0;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = sum == 0.f ? 0.f : v[e] * s0;
-                if (two && sum != 0.f) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 y = *reinterpret_cast<const float4 *>(&join[mr * JP + c * 32 + e]);
-                        v[e] = fmaf(y.x, f1, v[e]);
-                        v[e + 1] = fmaf(y.y, f1, v[e + 1]);
-                        v[e + 2] = fmaf(y.z, f1, v[e + 2]);
-                        v[e + 3] = fmaf(y.w, f1, v[e + 3]);
-                    }
-                }
-                if (bad) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = poisoned(v[e], poison[mr][(c * 32 + e) / 16] >> (2 * (e % 16)) & 3u);
-                }
-                if (whole) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint4 o;
-                        o.x = pack16(p.act, v[e] * inv, v[e + 1] * inv);
-                        o.y = pack16(p.act, v[e + 2] * inv, v[e + 3] * inv);
-                        o.z = pack16(p.act, v[e + 4] * inv, v[e + 5] * inv);
-                        o.w = pack16(p.act, v[e + 6] * inv, v[e + 7] * inv);
-                        *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) + head * D + c * 32 + e) = o;
-                    }
-                } else {
-                    float *dst = p.part + (int64_t)(prow + mr) * D + c * 32;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4 *>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                }
-            }
-        }
-        if (mr < mrows) {
-            if (whole) {
-                if (p.lse) p.lse[head] = sum == 0.f ? -INFINITY : mx * 0.6931471805599453f + logf(sum);
-            } else {
-                *reinterpret_cast<float2 *>(p.part + p.part_cap * D + 2 * (int64_t)(prow + mr)) = make_float2(mx, sum);
-            }
-        }
-    }
-    tc_before();
-    __syncthreads();
-    if (warp == W_MMA) {
-        tc_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(TMEM_COLS));
-    }
-    if (whole) return;
-    join_parts<D, THREADS>(p, q, g, m0, mrows, parts, q.ticket0 + unit - q.whole,
-                           q.part_row0 + (unit - q.whole) * q.splits * p.part_rows, &x.last);
 }
 
 template <int D, int KT, int VT> cudaError_t go(const BlockParams &p, cudaStream_t st) {
