@@ -425,12 +425,12 @@ int kvc_debug_chunk_plan_seq(int type, int head_dim, int n_head, int n_head_kv, 
  * head); of sequence i's units (KV head, tile) the first whole[i] are one work
  * item each, the others splits[i] items of split_rows[i] cached rows; *items
  * work items; *part_rows partial rows used of the *part_cap that the work space
- * holds, *tickets arrival counters.  act: kvc_act (16-bit queries run the
+ * holds.  act: kvc_act (16-bit queries run the
  * tcgen05 kernel).  rows, n_q, whole, splits, split_rows: HOST int32[n_seq].
  * Errors: KVC_EINVAL. */
 int kvc_debug_block_plan(int n_head, int n_head_kv, int head_dim, int act, int sms, int n_seq, const int32_t *rows,
                          const int32_t *n_q, int32_t *tile_m, int32_t *whole, int32_t *splits, int32_t *split_rows,
-                         int64_t *items, int64_t *part_rows, int64_t *part_cap, int64_t *tickets);
+                         int64_t *items, int64_t *part_rows, int64_t *part_cap);
 
 /* Test hook, no context and no GPU needed: the rows of a sequence holding
  * positions pos[0 .. n) that the sequence operations select for the range

@@ -23,30 +23,15 @@ int dev_alloc(Ctx *c, void **p, int64_t bytes, const char *what);
 // Partial rows of the work space: every SM four items of a whole query tile.
 static int64_t part_rows_cap(int sms) { return (int64_t)4 * sms * CROSS_TILE_M; }
 
-// The work space of split rows: partial sums [rows][D], (max, sum) pairs
-// [rows] and arrival counters.  Allocated once, with one size: a captured
-// launch keeps its addresses.
+// The work space of split rows: partial sums [rows][D] and (max, sum) pairs
+// [rows].  Allocated once, with one size: a captured launch keeps its address.
 static int ensure_block_space(Ctx *c, cudaStream_t st) {
     if (c->block_part) return KVC_OK;
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     KVC_CU(c, cudaStreamIsCapturing(st, &cap));
     if (cap != cudaStreamCaptureStatusNone)
         return c->fail(KVC_EINVAL, "the first block attention of a context allocates its work space: call it once before a capture");
-    const int64_t rows = part_rows_cap(c->sms);
-    const int64_t floats = rows * (c->D + 2), bytes = floats * 4 + rows * 4;
-    float *p = nullptr;
-    int rc = dev_alloc(c, (void **)&p, bytes, "block attention work space");
-    if (rc) return rc;
-    // the counters start at zero (every launch leaves them at zero)
-    cudaError_t e = cudaMemsetAsync(p + floats, 0, (size_t)rows * 4, c->st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(c->st);
-    if (e != cudaSuccess) {
-        cudaFree(p);
-        c->device_bytes -= bytes;
-        return cuda_fail(c, e, "clearing the block attention work space");
-    }
-    c->block_part = p;
-    return KVC_OK;
+    return dev_alloc(c, (void **)&c->block_part, part_rows_cap(c->sms) * (c->D + 2) * 4, "block attention work space");
 }
 
 // Cut the cached rows of the launch's units into parts.  `want`: items that run
@@ -115,7 +100,8 @@ static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t part
             s.whole = s.splits > 1 ? 0 : s.tiles * p.Hk;
         }
     }
-    int32_t item = 0, row = 0, ticket = 0;
+    int32_t item = 0, row = 0;
+    p.n_cut = 0;
     for (int i = 0; i < p.n_seq; ++i) {
         BlockSeq &s = p.seq[i];
         // equal parts, in whole steps
@@ -124,11 +110,11 @@ static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t part
                                                   std::max<int64_t>(1, (even + step - 1) / step) * step);
         s.item0 = item;
         s.part_row0 = row;
-        s.ticket0 = ticket;
+        s.cut0 = p.n_cut;
         const int32_t cut = s.tiles * p.Hk - s.whole;
         item += s.whole + cut * s.splits;
         row += cut * s.splits * p.part_rows;
-        ticket += cut;
+        p.n_cut += cut;
     }
     p.n_items = item;
 }
@@ -237,7 +223,6 @@ extern "C" int kvc_attn_cross(kvc_ctx *cc, int layer, int n_seq, const int32_t *
         p.n_vis = n_vis;
         p.part = c->block_part;
         p.part_cap = cap;
-        p.tickets = reinterpret_cast<int32_t *>(c->block_part + cap * (c->D + 2));
         int64_t tok0 = 0;
         for (int i = 0; i < n_seq; ++i) {
             const Seq &sq = c->seqs[(size_t)seq_ids[i]];
@@ -315,12 +300,12 @@ extern "C" int kvc_attn_weight(kvc_ctx *cc, int layer, int n_seq, const int32_t 
 
 extern "C" int kvc_debug_block_plan(int n_head, int n_head_kv, int head_dim, int act, int sms, int n_seq,
                                     const int32_t *rows, const int32_t *n_q, int32_t *tile_m, int32_t *whole,
-                                    int32_t *splits, int32_t *split_rows, int64_t *items, int64_t *part_rows, int64_t *part_cap,
-                                    int64_t *tickets) {
+                                    int32_t *splits, int32_t *split_rows, int64_t *items, int64_t *part_rows,
+                                    int64_t *part_cap) {
     if (n_head_kv < 1 || n_head < n_head_kv || n_head % n_head_kv || n_head / n_head_kv > MAX_GROUP ||
         (head_dim != 64 && head_dim != 128) || act < KVC_ACT_F32 || act > KVC_ACT_BF16 || sms < 1 || n_seq < 1 ||
         n_seq > MAX_SEQ_PER_LAUNCH || !rows || !n_q || !tile_m || !whole || !splits || !split_rows || !items || !part_rows ||
-        !part_cap || !tickets)
+        !part_cap)
         return KVC_EINVAL;
     BlockParams p;
     std::memset(&p, 0, sizeof(p));
@@ -341,7 +326,7 @@ extern "C" int kvc_debug_block_plan(int n_head, int n_head_kv, int head_dim, int
     plan_block(p, sms, act != KVC_ACT_F32);
     *tile_m = p.tile_m;
     *items = p.n_items;
-    *part_rows = *tickets = 0;
+    *part_rows = 0;
     *part_cap = part_rows_cap(sms);
     for (int i = 0; i < n_seq; ++i) {
         const BlockSeq &s = p.seq[i];
@@ -350,7 +335,6 @@ extern "C" int kvc_debug_block_plan(int n_head, int n_head_kv, int head_dim, int
         split_rows[i] = s.split_rows;
         const int64_t cut = (int64_t)s.tiles * p.Hk - s.whole;
         *part_rows = std::max<int64_t>(*part_rows, s.part_row0 + cut * s.splits * p.part_rows);
-        *tickets = std::max<int64_t>(*tickets, s.ticket0 + cut);
     }
     return KVC_OK;
 }

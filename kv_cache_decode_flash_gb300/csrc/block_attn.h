@@ -22,7 +22,7 @@ struct BlockSeq {
     int32_t splits;     // parts that the cached rows of a unit are cut into (>= 1)
     int32_t split_rows; // rows of a part (the last one may have fewer)
     int32_t part_row0;  // first partial row of its items (splits > 1)
-    int32_t ticket0;    // first arrival counter of its tiles (splits > 1)
+    int32_t cut0;       // cut units of the launch before its own
     int32_t w_index;    // its accumulators (kvc_attn_weight)
 };
 
@@ -30,6 +30,7 @@ struct BlockParams {
     int32_t H, Hk, D, r, P;
     int32_t n_pages, max_pages; // pages of a layer, entries of a page-table row
     int32_t n_seq, n_items;
+    int32_t n_cut;        // units that are cut into parts
     int32_t act;          // kvc_act of q and out
     int32_t part_rows;    // partial rows of an item at most (min(tile_m, longest block * r))
     int32_t tile_m;
@@ -47,7 +48,6 @@ struct BlockParams {
     int64_t w_stride;
     float *part;          // partials: [row][D] sums, then [row] (max, sum) pairs
     int64_t part_cap;     // partial rows
-    int32_t *tickets;
     uint32_t *err;
     BlockSeq seq[MAX_SEQ_PER_LAUNCH];
 };
@@ -63,6 +63,9 @@ constexpr int CROSS_TC_TILE_N = 128;
 cudaError_t launch_cross(int type_k, int type_v, const BlockParams &p, bool narrow, cudaStream_t st);
 // The same for 16-bit queries, by tcgen05 (tiles of CROSS_TC_TILE_M query rows).
 cudaError_t launch_cross_tc(int type_k, int type_v, const BlockParams &p, cudaStream_t st);
+
+// Joins the parts of the launch's cut units (k_join.cu; the two above end with it).
+cudaError_t launch_join(const BlockParams &p, cudaStream_t st);
 
 // The rows' weights: splits of a sequence are its steps of CROSS_TILE_N rows, items (KV head, step).
 cudaError_t launch_weight(int type_k, const BlockParams &p, bool narrow, cudaStream_t st);

@@ -260,93 +260,6 @@ __device__ __forceinline__ void store2(void *out, int act, int64_t at, float a, 
         *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(out) + at) = pack16(act, a, b);
 }
 
-// The end of an item that is a part of its tile's rows (NTHREADS threads of the CTA, the first ones, which wrote its
-// partial rows; sync: their barrier): the part that arrives last joins the tile's parts, in their order.
-template <int D, int NTHREADS, class Sync>
-__device__ __forceinline__ void join_parts(const BlockParams &p, const BlockSeq &q, int g, int m0, int mrows, int parts,
-                                           int ticket, int first, int32_t *last, Sync sync) {
-    const int tid = threadIdx.x;
-    __threadfence();
-    sync();
-    if (tid == 0) {
-        const int n = atomicAdd(&p.tickets[ticket], 1);
-        *last = n == parts - 1;
-        if (*last) p.tickets[ticket] = 0;
-    }
-    sync();
-    if (!*last) return;
-    __threadfence();
-    // A warp joins ROWS query rows at a time, a lane D / 32 columns of them: what bounds this is the latency of the
-    // loads, so all of a few parts' are on their way together.
-    constexpr int V = D / 32, ROWS = 4, STEP = 2;
-    const float2 *ml = reinterpret_cast<const float2 *>(p.part + p.part_cap * D);
-    const int lane = tid & 31;
-    for (int mb = (tid >> 5) * ROWS; mb < mrows; mb += NTHREADS / 32 * ROWS) {
-        float M[ROWS], L[ROWS], o[ROWS][V];
-#pragma unroll
-        for (int k = 0; k < ROWS; ++k) {
-            M[k] = -INFINITY;
-            L[k] = 0.f;
-#pragma unroll
-            for (int e = 0; e < V; ++e) o[k][e] = 0.f;
-        }
-        for (int i = lane; i < parts; i += 32) {
-#pragma unroll
-            for (int k = 0; k < ROWS; ++k)
-                M[k] = fmaxf(M[k], __ldcg(&ml[first + i * p.part_rows + min(mb + k, mrows - 1)]).x);
-        }
-#pragma unroll
-        for (int k = 0; k < ROWS; ++k) {
-#pragma unroll
-            for (int x = 16; x; x >>= 1) M[k] = fmaxf(M[k], __shfl_xor_sync(0xffffffffu, M[k], x));
-            if (M[k] == -INFINITY) M[k] = 0.f;
-        }
-        for (int i0 = 0; i0 < parts; i0 += STEP) {
-            float2 c[STEP][ROWS];
-            float v[STEP][ROWS][V];
-#pragma unroll
-            for (int i = 0; i < STEP; ++i) {
-#pragma unroll
-                for (int k = 0; k < ROWS; ++k) {
-                    const int64_t row = first + (int64_t)min(i0 + i, parts - 1) * p.part_rows + min(mb + k, mrows - 1);
-                    c[i][k] = __ldcg(&ml[row]);
-                    if constexpr (V == 4) {
-                        const float4 f = __ldcg(reinterpret_cast<const float4 *>(p.part + row * D) + lane);
-                        v[i][k][0] = f.x, v[i][k][1] = f.y, v[i][k][2] = f.z, v[i][k][3] = f.w;
-                    } else {
-                        const float2 f = __ldcg(reinterpret_cast<const float2 *>(p.part + row * D) + lane);
-                        v[i][k][0] = f.x, v[i][k][1] = f.y;
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < STEP; ++i) {
-                if (i0 + i >= parts) break;
-#pragma unroll
-                for (int k = 0; k < ROWS; ++k) {
-                    const float f = ex2(c[i][k].x - M[k]);
-                    // nothing seen there, or nothing left of it (its sums may be anything)
-                    if (c[i][k].y == 0.f || (f == 0.f && c[i][k].y == c[i][k].y)) continue;
-                    L[k] = fmaf(c[i][k].y, f, L[k]);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) o[k][e] = fmaf(v[i][k][e], f, o[k][e]);
-                }
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < ROWS; ++k) {
-            const int m = mb + k;
-            if (m >= mrows) continue;
-            const int t = (m0 + m) / p.r, j = (m0 + m) % p.r;
-            const int64_t head = ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
-            const float inv = L[k] == 0.f ? 0.f : 1.f / L[k];
-#pragma unroll
-            for (int e = 0; e < V; e += 2) store2(p.out, p.act, head * D + lane * V + e, o[k][e] * inv, o[k][e + 1] * inv);
-            if (p.lse && lane == 0) p.lse[head] = L[k] == 0.f ? -INFINITY : M[k] * 0.6931471805599453f + logf(L[k]);
-        }
-    }
-}
-
 // sc = the products of 16 query rows (addresses qa, ql of their fp16 parts) and NT * 8 cached rows (address ka),
 // block scales d[b][col] applied: the accumulator layout of mma.m16n8k16.
 template <int D, int KT, int NT, bool LO>

@@ -23,9 +23,9 @@
 // part, whatever they hold: scores are selected, not added to, and a
 // non-finite V value is kept out of the products (0 x inf is NaN) and put into
 // the result only of rows that give it weight.
-// Few query tiles: the cached rows are split over items, the partial sums are
-// joined in their order by the item that comes last (an arrival counter), so a
-// result does not depend on the order in which items finish.
+// Few query tiles: the cached rows are split over items, and a second kernel
+// joins their partial sums in order, so a result does not depend on the order in
+// which items finish.
 #include "block_tile.cuh"
 
 namespace kvc {
@@ -52,7 +52,6 @@ template <int D> struct Smem {
     uint8_t badrow[TN];
     int32_t vis_max;
     int32_t bad, any_bad;
-    int32_t last;
 };
 
 // (out of line: the place that calls it is unrolled)
@@ -377,9 +376,6 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
             }
         }
     }
-    if (whole) return;
-    join_parts<D, THREADS>(p, q, g, m0, mrows, parts, q.ticket0 + unit - q.whole,
-                           q.part_row0 + (unit - q.whole) * q.splits * p.part_rows, &s.last, [] { __syncthreads(); });
 }
 
 template <int D, int KT, int VT, int WM, bool LO> cudaError_t go(const BlockParams &p, cudaStream_t st) {
@@ -388,7 +384,8 @@ template <int D, int KT, int VT, int WM, bool LO> cudaError_t go(const BlockPara
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     k<<<(unsigned)p.n_items, THREADS, bytes, st>>>(p);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    return e == cudaSuccess ? launch_join(p, st) : e;
 }
 template <int D, int KT, int VT> cudaError_t pick(const BlockParams &p, bool narrow, cudaStream_t st) {
     const bool lo = p.act == KVC_ACT_F32;

@@ -42,7 +42,7 @@ constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr float GROW = 8.f; // log2 growth of a maximum that is let pass before O is rescaled
 constexpr uint32_t TMEM_COLS = 512;
 
-enum Bar { KF0, KF1, KE0, KE1, VF0, VF1, VE0, VE1, SF0, SF1, PF0, PF1, OD0, OD1, DRAIN, N_BARS };
+enum Bar { KF0, KF1, KE0, KE1, VF0, VF1, VE0, VE1, SF0, SF1, PF0, PF1, OD0, OD1, XF0, XF1, XF2, XF3, DRAIN, N_BARS };
 
 template <int D> struct Lay {
     static constexpr int REG = TN * 128;          // a region: 128 rows of 64 fp16, 128-byte swizzled
@@ -58,10 +58,10 @@ struct Aux {
     float kfac[SLOTS];           // score factor of the step's K exponent
     int32_t vexp[SLOTS];         // V's exponent as of the step
     uint32_t badrow[SLOTS][TN / 32]; // rows of the step whose V values that are not finite were left out
-    uint32_t red[2][2][GROUP / 32];
+    alignas(16) uint32_t red[2][2][GROUP / 32];
     float2 ml[TM];
     uint32_t tmem;
-    int32_t vis_max, vis_min, any_bad, last;
+    int32_t vis_max, vis_min, any_bad;
     volatile int32_t abort;
 };
 
@@ -220,70 +220,38 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // ------------------------------------------------------------- loading ----
-// The loading threads' share of one tensor's rows of a step, in registers.
-template <int D, int T> struct Raw {
-    static constexpr int RB = row_bytes<T>(D), PIECES = RB / 16; // 16-byte pieces of a row: one of them is the thread's, in
-    uint4 u[PIECES];                                              // every (128 / PIECES)-th row
-    uint16_t s[PIECES];
-    __device__ __forceinline__ void load(const uint8_t *data, const uint16_t *scales, const int32_t *row, int t) {
-        const int c = t % PIECES;
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-            const int32_t R = row[t / PIECES + i * (GROUP / PIECES)];
-            u[i] = make_uint4(0, 0, 0, 0);
-            s[i] = 0;
-            if (R >= 0) { // volatile: they are to be under way two steps ahead of their use, whatever registers that takes
-                asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(u[i].x), "=r"(u[i].y), "=r"(u[i].z), "=r"(u[i].w)
-                             : "l"(data + (int64_t)R * RB + c * 16));
-                asm volatile("ld.global.nc.u16 %0, [%1];"
-                             : "=h"(s[i])
-                             : "l"(scales + (int64_t)R * (D / QK) + (T == KVC_Q4_0 ? c : c / 2)));
-            }
-        }
+// Codes of one tensor: of every (128 / PIECES)-th row of a step a loading thread has one 16-byte piece.
+template <int D, int T> struct Codes {
+    static constexpr int RB = row_bytes<T>(D), PIECES = RB / 16, ROWS = GROUP / PIECES;
+    static_assert(ROWS % 8 == 0, "a thread's rows share their swizzle");
+    // volatile: a load is to be under way as long before its use as it stands here
+    __device__ __forceinline__ static void load(uint4 &u, const uint8_t *at, int32_t R) {
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "l"(at + (int64_t)R * RB));
     }
-    // largest finite magnitude of the scales, as fp16 bits; a scale that is not finite becomes 0 and is reported
-    __device__ __forceinline__ uint32_t top(bool drop, uint32_t *badrow, int t) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-            const uint32_t a = s[i] & 0x7fffu;
-            if (a >= 0x7c00u) {
-                if (drop) {
-                    s[i] = 0;
-                    const int j = t / PIECES + i * (GROUP / PIECES);
-                    atomicOr(&badrow[j >> 5], 1u << (j & 31));
-                }
-            } else {
-                m = max(m, a);
-            }
-        }
-        return m;
+    __device__ __forceinline__ static void load(uint16_t &s, const uint16_t *at, int32_t R) {
+        asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(s) : "l"(at + (int64_t)R * (D / QK)));
     }
-    // value = code * scale * 2^up, rounded once
-    __device__ __forceinline__ void store(uint8_t *tile, float up, int t) const {
-        const int c = t % PIECES;
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-            const int j = t / PIECES + i * (GROUP / PIECES);
-            const __half2 d = __half2half2(__float2half_rn(__half2float(__ushort_as_half(s[i])) * up));
-            auto put = [&](int col, uint2 a, uint2 b) {
-                uint4 o;
-                *reinterpret_cast<__half2 *>(&o.x) = __hmul2(*reinterpret_cast<__half2 *>(&a.x), d);
-                *reinterpret_cast<__half2 *>(&o.y) = __hmul2(*reinterpret_cast<__half2 *>(&a.y), d);
-                *reinterpret_cast<__half2 *>(&o.z) = __hmul2(*reinterpret_cast<__half2 *>(&b.x), d);
-                *reinterpret_cast<__half2 *>(&o.w) = __hmul2(*reinterpret_cast<__half2 *>(&b.y), d);
-                *reinterpret_cast<uint4 *>(tile + at<D>(j, col)) = o;
-            };
-            if constexpr (T == KVC_Q8_0) {
-                put(c * 16, codes4(u[i].x), codes4(u[i].y));
-                put(c * 16 + 8, codes4(u[i].z), codes4(u[i].w));
-            } else {
-                put(c * 32, nibbles4(u[i].x), nibbles4(u[i].y));
-                put(c * 32 + 8, nibbles4(u[i].z), nibbles4(u[i].w));
-                put(c * 32 + 16, nibbles4(u[i].x >> 4), nibbles4(u[i].y >> 4));
-                put(c * 32 + 24, nibbles4(u[i].z >> 4), nibbles4(u[i].w >> 4));
-            }
+    // values = codes * scale * 2^up, rounded once; dst: the piece's row, a[]: byte offsets of its 8-value pieces
+    __device__ __forceinline__ static void store(uint8_t *dst, const uint32_t *a, const uint4 &u, uint16_t s, float up) {
+        const __half2 d = __half2half2(__float2half_rn(__half2float(__ushort_as_half(s)) * up));
+        auto put = [&](uint32_t o, uint2 x, uint2 y) {
+            uint4 v;
+            *reinterpret_cast<__half2 *>(&v.x) = __hmul2(*reinterpret_cast<__half2 *>(&x.x), d);
+            *reinterpret_cast<__half2 *>(&v.y) = __hmul2(*reinterpret_cast<__half2 *>(&x.y), d);
+            *reinterpret_cast<__half2 *>(&v.z) = __hmul2(*reinterpret_cast<__half2 *>(&y.x), d);
+            *reinterpret_cast<__half2 *>(&v.w) = __hmul2(*reinterpret_cast<__half2 *>(&y.y), d);
+            *reinterpret_cast<uint4 *>(dst + o) = v;
+        };
+        if constexpr (T == KVC_Q8_0) {
+            put(a[0], codes4(u.x), codes4(u.y));
+            put(a[1], codes4(u.z), codes4(u.w));
+        } else {
+            put(a[0], nibbles4(u.x), nibbles4(u.y));
+            put(a[1], nibbles4(u.z), nibbles4(u.w));
+            put(a[2], nibbles4(u.x >> 4), nibbles4(u.y >> 4));
+            put(a[3], nibbles4(u.z >> 4), nibbles4(u.w >> 4));
         }
     }
 };
@@ -341,25 +309,25 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
     auto clear = [&](int s) { // a step's reports; those of four steps before are read no more
         if (IS_V && t < TN / 32) x.badrow[s % SLOTS][t] = 0;
     };
-    auto wait_empty = [&](int s) {
-        if (s >= 2) bar_wait(&empty[s & 1], ((s >> 1) - 1) & 1, p.err, &x);
-    };
     if (steps == 0) return;
-    look_up(0);
-    find(0);
-    find(1);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) row[k][t] = k < steps ? pool_row(p, q, g, r0 + k * TN + t) : -1;
+    look_up(3);
     clear(0);
+    clear(1);
     named_sync<SYNC, GROUP>();
     if constexpr (T == KVC_F16) {
-        // a step's copies are under way while those of the step before are waited for
+        // A step's copies are under way while those of the step before are waited for, if their stage is free by then;
+        // a step that has landed is not held back for a stage.
         for (int s = 0; s <= steps; ++s) {
+            bool ahead = false;
             if (s < steps) {
-                wait_empty(s);
-                copy_halves<D>(tiles + (s & 1) * Lay<D>::TILE, data, row[s % SLOTS], t);
+                ahead = s < 2 || bar_try(&empty[s & 1], ((s >> 1) - 1) & 1);
+                if (ahead) copy_halves<D>(tiles + (s & 1) * Lay<D>::TILE, data, row[s % SLOTS], t);
                 if (!IS_V && t == 0) x.kfac[s % SLOTS] = 1.f;
             }
             if (s > 0) {
-                if (s < steps)
+                if (ahead)
                     asm volatile("cp.async.wait_group 1;" ::: "memory");
                 else
                     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -368,43 +336,92 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
                 fence_async();
                 bar_arrive(&full[(s - 1) & 1]);
             }
-            find(s + 2);
-            clear(s + 1);
+            if (s < steps && !ahead) {
+                bar_wait(&empty[s & 1], ((s >> 1) - 1) & 1, p.err, &x);
+                copy_halves<D>(tiles + (s & 1) * Lay<D>::TILE, data, row[s % SLOTS], t);
+            }
+            find(s + 3);
+            clear(s + 2);
             named_sync<SYNC, GROUP>();
         }
     } else {
-        const uint16_t *scales = IS_V ? p.vs : p.ks;
-        Raw<D, T> raw[2];
-        raw[0].load(data, scales, row[0], t);
-        if (steps > 1) raw[1].load(data, scales, row[1], t);
+        // A thread's piece of the next step is requested as soon as this step's is stored, its scale a step earlier:
+        // the largest scale, which gives a step its exponent, is known before the step's turn.
+        using C = Codes<D, T>;
+        const int c = t % C::PIECES, j0 = t / C::PIECES;
+        const uint8_t *codes = data + c * 16;
+        const uint16_t *scales = (IS_V ? p.vs : p.ks) + (T == KVC_Q4_0 ? c : c / 2);
+        uint32_t a[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            a[k] = T == KVC_Q4_0 ? at<D>(j0, c * 32 + k * 8) : at<D>(j0, c * 16 + (k & 1) * 8);
+        uint4 u[C::PIECES];
+        uint16_t sc[C::PIECES], sn[C::PIECES];
+        auto at_row = [&](int s, int i) { return max(row[s % SLOTS][j0 + i * C::ROWS], 0); };
         int E = E_MIN;
-        auto step = [&](int s, Raw<D, T> &r) {
-            const int slot = s % SLOTS;
-            // the step's largest scale gives its exponent
-            const uint32_t m = __reduce_max_sync(0xffffffffu, r.top(IS_V && r0 + (s + 1) * TN > vis_min, x.badrow[slot], t));
+        auto exponent = [&](int s) { // of step s, whose scales are sc
+            uint32_t m = 0;
+            const int lim = q.n_rows - (r0 + s * TN) - j0; // rows past the end: scale 0
+            const bool drop = IS_V && r0 + (s + 1) * TN > vis_min;
+#pragma unroll
+            for (int i = 0; i < C::PIECES; ++i) {
+                if (i * C::ROWS >= lim) sc[i] = 0;
+                const uint32_t b = sc[i] & 0x7fffu;
+                if (b < 0x7c00u) {
+                    m = max(m, b);
+                } else if (drop) { // not finite, and some token does not see it: reported and left out
+                    const int j = j0 + i * C::ROWS;
+                    sc[i] = 0;
+                    atomicOr(&x.badrow[s % SLOTS][j >> 5], 1u << (j & 31));
+                }
+            }
+            m = __reduce_max_sync(0xffffffffu, m);
             if ((t & 31) == 0) x.red[IS_V][s & 1][t >> 5] = m;
-            find(s + 2);
-            clear(s + 1);
+            find(s + 3);
+            clear(s + 2);
             named_sync<SYNC, GROUP>();
-            const uint32_t *a = x.red[IS_V][s & 1];
-            const uint32_t top = max(max(a[0], a[1]), max(a[2], a[3]));
+            const uint4 r = *reinterpret_cast<const uint4 *>(x.red[IS_V][s & 1]);
+            const uint32_t top = max(max(r.x, r.y), max(r.z, r.w));
             const int e = top ? ilogbf(__half2float(__ushort_as_half((uint16_t)top))) : E_MIN;
             E = IS_V ? max(E, e) : e;
             if (t == 0) {
-                if (IS_V)
-                    x.vexp[slot] = E;
-                else
-                    x.kfac[slot] = ldexpf(1.f, E - 7);
+                if (IS_V) {
+                    x.vexp[s % SLOTS] = E;
+                    bar_arrive(&x.bar[XF0 + s % SLOTS]);
+                } else {
+                    x.kfac[s % SLOTS] = ldexpf(1.f, E - 7);
+                }
             }
-            wait_empty(s);
-            r.store(tiles + (s & 1) * Lay<D>::TILE, ldexpf(1.f, 7 - E), t);
+        };
+#pragma unroll
+        for (int i = 0; i < C::PIECES; ++i) C::load(sc[i], scales, at_row(0, i));
+#pragma unroll
+        for (int i = 0; i < C::PIECES; ++i) C::load(u[i], codes, at_row(0, i));
+#pragma unroll
+        for (int i = 0; i < C::PIECES; ++i) C::load(sn[i], scales, at_row(1, i));
+        exponent(0);
+        for (int s = 0; s < steps; ++s) {
+            if (s >= 2) bar_wait(&empty[s & 1], ((s >> 1) - 1) & 1, p.err, &x);
+            const float up = ldexpf(1.f, 7 - E);
+            uint8_t *tile = tiles + (s & 1) * Lay<D>::TILE;
+            int32_t R[C::PIECES];
+#pragma unroll
+            for (int i = 0; i < C::PIECES; ++i) R[i] = at_row(s + 1, i);
+#pragma unroll
+            for (int i = 0; i < C::PIECES; ++i) {
+                C::store(tile + i * C::ROWS * 128, a, u[i], sc[i], up);
+                if (s + 1 < steps) C::load(u[i], codes, R[i]);
+            }
             fence_async();
             bar_arrive(&full[s & 1]);
-            if (s + 2 < steps) r.load(data, scales, row[(s + 2) % SLOTS], t);
-        };
-        for (int s = 0; s < steps; s += 2) {
-            step(s, raw[0]);
-            if (s + 1 < steps) step(s + 1, raw[1]);
+            if (s + 1 < steps) {
+#pragma unroll
+                for (int i = 0; i < C::PIECES; ++i) {
+                    sc[i] = sn[i];
+                    C::load(sn[i], scales, at_row(s + 2, i));
+                }
+                exponent(s + 1);
+            }
         }
     }
 }
@@ -569,8 +586,11 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
                     mx = top;
                 }
                 sum *= al;
-                // V's exponent, and whether some of its values were left out, are known once it is there
-                bar_wait_warp(&x.bar[VF0 + (s & 1)], (s >> 1) & 1, p.err, &x);
+                // V's exponent and the reports of values that were left out
+                if (VT != KVC_F16)
+                    bar_wait_warp(&x.bar[XF0 + slot], (s / SLOTS) & 1, p.err, &x);
+                else if (base + TN > vis_min)
+                    bar_wait_warp(&x.bar[VF0 + (s & 1)], (s >> 1) & 1, p.err, &x);
                 if (VT != KVC_F16) {
                     const int e = x.vexp[slot];
                     if (e != E) al *= ldexpf(1.f, max(E - e, -126));
@@ -718,9 +738,6 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
             tc_after();
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(TMEM_COLS));
         }
-        if (whole) return;
-        join_parts<D, 2 * GROUP>(p, q, g, m0, mrows, parts, q.ticket0 + unit - q.whole,
-                                 q.part_row0 + (unit - q.whole) * q.splits * p.part_rows, &x.last, [] { named_sync<2, 2 * GROUP>(); });
     } else if (warp < 12) {
         load_rows<D, KT, false>(p, q, g, smem + L::K, x, r0, steps, vis_min, tid - 2 * GROUP);
     } else if (warp < 16) {
@@ -773,7 +790,8 @@ template <int D, int KT, int VT> cudaError_t go(const BlockParams &p, cudaStream
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     k<<<(unsigned)p.n_items, THREADS, bytes, st>>>(p);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    return e == cudaSuccess ? launch_join(p, st) : e;
 }
 
 } // namespace

@@ -100,7 +100,7 @@ def load():
         "kvc_debug_chunk_plan": (i32, [i32, i32, i32, i32, i32, i32, i32, i32, p, C.POINTER(C.c_int32),
                                        C.POINTER(C.c_int32)]),
         "kvc_debug_chunk_plan_seq": (i32, [i32, i32, i32, i32, i32, i32, i32, i32, p, p, C.POINTER(C.c_int32)]),
-        "kvc_debug_block_plan": (i32, [i32] * 6 + [p] * 10),
+        "kvc_debug_block_plan": (i32, [i32] * 6 + [p] * 9),
         "kvc_debug_select_rows": (i32, [p, i32, i32, i32, i32, p, C.POINTER(C.c_int64), C.POINTER(C.c_int64),
                                         C.POINTER(C.c_int32)]),
         "kvc_set_timeout_ms": (i32, [p, i32]),
@@ -412,17 +412,17 @@ def kvc_debug_chunk_plan_seq(type_, head_dim, n_head, n_head_kv, sms, occ, occ2,
 
 def kvc_debug_block_plan(n_head, n_head_kv, head_dim, act, sms, rows, n_q):
     """How a block attention launch cuts its sequences, without a context or a GPU: a dict of
-    tile_m, whole, splits, split_rows, items, part_rows, part_cap and tickets."""
+    tile_m, whole, splits, split_rows, items, part_rows and part_cap."""
     n = len(rows)
     r, t = (C.c_int32 * n)(*[int(x) for x in rows]), (C.c_int32 * n)(*[int(x) for x in n_q])
     wh, sp, sr, tm = (C.c_int32 * n)(), (C.c_int32 * n)(), (C.c_int32 * n)(), C.c_int32()
-    big = [C.c_int64() for _ in range(4)]
+    big = [C.c_int64() for _ in range(3)]
     st = load().kvc_debug_block_plan(n_head, n_head_kv, head_dim, act, sms, n, r, t, C.byref(tm), wh, sp, sr,
                                      *[C.byref(b) for b in big])
     if st != KVC_OK:
         raise KvcError(st, "bad block-plan arguments")
     return {"tile_m": tm.value, "whole": list(wh), "splits": list(sp), "split_rows": list(sr),
-            **{k: b.value for k, b in zip(("items", "part_rows", "part_cap", "tickets"), big)}}
+            **{k: b.value for k, b in zip(("items", "part_rows", "part_cap"), big)}}
 
 
 def kvc_debug_select_rows(pos, p0, p1, linear=False):
