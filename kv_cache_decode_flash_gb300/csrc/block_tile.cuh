@@ -154,17 +154,12 @@ __device__ __forceinline__ void item_unit(const BlockSeq &q, int local, int &uni
     parts = whole ? 1 : q.splits;
 }
 
-// One warp normalises query row m (of m_all rows; the others are zero) of KV
-// head g: lane l gets the D / 32 values from l * D / 32 on as pairs of halves hi
-// (and lo, what hi leaves).  Returns the rows that it sees (0 for no row) and, in
-// *scale, the score per unit of the normalised product, in log2 units.
-template <int D, bool LO>
-__device__ __forceinline__ int query_row(const BlockParams &p, const BlockSeq &q, int g, int m, int m_all, int lane,
-                                         uint32_t (&hi)[D / 64], uint32_t (&lo)[D / 64], float *scale) {
+// Lane l's values l * D / 32 .. of query row m (of m_all rows; the others are zero) of KV head g, one warp a row; returns
+// the rows that it sees (0 for no row).
+template <int D>
+__device__ __forceinline__ int query_load(const BlockParams &p, const BlockSeq &q, int g, int m, int m_all, int lane,
+                                          float (&x)[D / 32]) {
     constexpr int V = D / 32;
-    float x[V];
-    float top = 0.f;
-    int vis = 0;
     if (m < m_all) {
         const int t = m / p.r, j = m % p.r;
         const int64_t tok = (int64_t)q.tok0 + t;
@@ -189,13 +184,22 @@ __device__ __forceinline__ int query_row(const BlockParams &p, const BlockSeq &q
                 x[i] = f.x, x[i + 1] = f.y;
             }
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) top = fmaxf(top, fabsf(x[i]));
-        vis = p.n_vis ? min(max(p.n_vis[tok], 0), q.n_rows) : q.n_rows;
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = 0.f;
+        return p.n_vis ? min(max(p.n_vis[tok], 0), q.n_rows) : q.n_rows;
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = 0.f;
+    return 0;
+}
+
+// The warp normalises the row: a lane's values as pairs of halves hi (and lo, what hi leaves).  Returns the score per unit
+// of the normalised product, in log2 units.
+template <int D, bool LO>
+__device__ __forceinline__ float query_pack(const BlockParams &p, const float (&x)[D / 32], uint32_t (&hi)[D / 64],
+                                            uint32_t (&lo)[D / 64]) {
+    constexpr int V = D / 32;
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = fmaxf(top, fabsf(x[i]));
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     // top = f * 2^e, f in [1/2, 1): scaled by 2^(14 - e)
@@ -212,8 +216,7 @@ __device__ __forceinline__ int query_row(const BlockParams &p, const BlockSeq &q
             lo[i / 2] = h2(isinf(f.x) ? 0.f : a - f.x, isinf(f.y) ? 0.f : b - f.y);
         }
     }
-    *scale = p.scale_log2 / up;
-    return vis;
+    return p.scale_log2 / up;
 }
 
 // A V value as stored (the rare path of values that are not finite).

@@ -31,10 +31,15 @@ constexpr int TM = 128;      // query rows of a half
 constexpr int TN = 128;      // cached rows of a step
 constexpr int GROUP = 128;       // threads of a role: softmax of half 0, of half 1, K, V; then the issuing warp
 constexpr int THREADS = 5 * GROUP;
-// Registers: a launch gives every thread 96, which the loading groups keep; softmax takes what the issuing warp's group leaves.  (No function of
+// Registers: a launch gives every thread 96.  The loading groups and the issuing warp's hand some back (those that turn
+// codes into values need more), the softmax groups take them, so that a thread holds all or half of its row's 128 scores.  (No function of
 // theirs may stay a call: its registers would have to fit the smallest role's.)
-constexpr int R_SOFT = 128, R_MMA = 24;
-static_assert(2 * R_SOFT + 2 * 96 + R_MMA <= 5 * 96, "the roles' registers come from the launch's");
+constexpr int R_MMA = 24;
+template <bool CODES> struct Regs {
+    static constexpr int SOFT = CODES ? 152 : 184, LOAD = CODES ? 72 : 40;
+    static constexpr int HOLD = CODES ? 2 : 4; // blocks of 32 scores that a softmax thread keeps
+    static_assert(2 * SOFT + 2 * LOAD + R_MMA <= 5 * 96, "the roles' registers come from the launch's");
+};
 constexpr int SLOTS = 4; // steps whose factors are kept: a step's are overwritten four steps later
 constexpr int E_MIN = -24;
 constexpr uint32_t WAIT_LIMIT = 1u << 26;
@@ -60,6 +65,7 @@ struct Aux {
     uint32_t badrow[SLOTS][TN / 32]; // rows of the step whose V values that are not finite were left out
     alignas(16) uint32_t red[2][2][GROUP / 32];
     float2 ml[TM];
+    uint16_t scale[2][2][TN * 4]; // K's and V's block scales of a step, [row][block]
     uint32_t tmem;
     int32_t vis_max, vis_min, any_bad;
     volatile int32_t abort;
@@ -230,8 +236,12 @@ template <int D, int T> struct Codes {
                      : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
                      : "l"(at + (int64_t)R * RB));
     }
-    __device__ __forceinline__ static void load(uint16_t &s, const uint16_t *at, int32_t R) {
-        asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(s) : "l"(at + (int64_t)R * (D / QK)));
+    // a row's scales
+    __device__ __forceinline__ static void load(uint32_t (&s)[D / 64], const uint16_t *scales, int32_t R) {
+        if constexpr (D == 128)
+            asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(s[0]), "=r"(s[D / 64 - 1]) : "l"(scales + (int64_t)R * 4));
+        else
+            asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(s[0]) : "l"(scales + (int64_t)R * 2));
     }
     // values = codes * scale * 2^up, rounded once; dst: the piece's row, a[]: byte offsets of its 8-value pieces
     __device__ __forceinline__ static void store(uint8_t *dst, const uint32_t *a, const uint4 &u, uint16_t s, float up) {
@@ -345,35 +355,35 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
             named_sync<SYNC, GROUP>();
         }
     } else {
-        // A thread's piece of the next step is requested as soon as this step's is stored, its scale a step earlier:
-        // the largest scale, which gives a step its exponent, is known before the step's turn.
+        // A thread's piece of the next step is requested as soon as this step's is stored.  It looks after one row's
+        // scales too, a step earlier: the largest scale, which gives a step its exponent, is known before the step's turn.
         using C = Codes<D, T>;
         const int c = t % C::PIECES, j0 = t / C::PIECES;
         const uint8_t *codes = data + c * 16;
-        const uint16_t *scales = (IS_V ? p.vs : p.ks) + (T == KVC_Q4_0 ? c : c / 2);
+        const uint16_t *scales = IS_V ? p.vs : p.ks;
         uint32_t a[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             a[k] = T == KVC_Q4_0 ? at<D>(j0, c * 32 + k * 8) : at<D>(j0, c * 16 + (k & 1) * 8);
         uint4 u[C::PIECES];
-        uint16_t sc[C::PIECES], sn[C::PIECES];
-        auto at_row = [&](int s, int i) { return max(row[s % SLOTS][j0 + i * C::ROWS], 0); };
+        uint32_t sc[D / 64];
+        auto at_row = [&](int s, int j) { return max(row[s % SLOTS][j], 0); };
         int E = E_MIN;
         auto exponent = [&](int s) { // of step s, whose scales are sc
             uint32_t m = 0;
-            const int lim = q.n_rows - (r0 + s * TN) - j0; // rows past the end: scale 0
+            const bool in = r0 + s * TN + t < q.n_rows; // a row past the end: scales 0
             const bool drop = IS_V && r0 + (s + 1) * TN > vis_min;
 #pragma unroll
-            for (int i = 0; i < C::PIECES; ++i) {
-                if (i * C::ROWS >= lim) sc[i] = 0;
-                const uint32_t b = sc[i] & 0x7fffu;
-                if (b < 0x7c00u) {
-                    m = max(m, b);
+            for (int k = 0; k < D / QK; ++k) {
+                uint32_t h = sc[k >> 1] >> (16 * (k & 1)) & 0xffffu;
+                if (!in) h = 0;
+                if ((h & 0x7fffu) < 0x7c00u) {
+                    m = max(m, h & 0x7fffu);
                 } else if (drop) { // not finite, and some token does not see it: reported and left out
-                    const int j = j0 + i * C::ROWS;
-                    sc[i] = 0;
-                    atomicOr(&x.badrow[s % SLOTS][j >> 5], 1u << (j & 31));
+                    h = 0;
+                    atomicOr(&x.badrow[s % SLOTS][t >> 5], 1u << (t & 31));
                 }
+                x.scale[IS_V][s & 1][t * (D / QK) + k] = (uint16_t)h;
             }
             m = __reduce_max_sync(0xffffffffu, m);
             if ((t & 31) == 0) x.red[IS_V][s & 1][t >> 5] = m;
@@ -393,80 +403,90 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
                 }
             }
         };
+        C::load(sc, scales, at_row(0, t));
 #pragma unroll
-        for (int i = 0; i < C::PIECES; ++i) C::load(sc[i], scales, at_row(0, i));
-#pragma unroll
-        for (int i = 0; i < C::PIECES; ++i) C::load(u[i], codes, at_row(0, i));
-#pragma unroll
-        for (int i = 0; i < C::PIECES; ++i) C::load(sn[i], scales, at_row(1, i));
+        for (int i = 0; i < C::PIECES; ++i) C::load(u[i], codes, at_row(0, j0 + i * C::ROWS));
         exponent(0);
+        C::load(sc, scales, at_row(1, t));
         for (int s = 0; s < steps; ++s) {
             if (s >= 2) bar_wait(&empty[s & 1], ((s >> 1) - 1) & 1, p.err, &x);
             const float up = ldexpf(1.f, 7 - E);
             uint8_t *tile = tiles + (s & 1) * Lay<D>::TILE;
-            int32_t R[C::PIECES];
-#pragma unroll
-            for (int i = 0; i < C::PIECES; ++i) R[i] = at_row(s + 1, i);
+            const uint16_t *d = &x.scale[IS_V][s & 1][j0 * (D / QK) + (T == KVC_Q4_0 ? c : c / 2)];
 #pragma unroll
             for (int i = 0; i < C::PIECES; ++i) {
-                C::store(tile + i * C::ROWS * 128, a, u[i], sc[i], up);
-                if (s + 1 < steps) C::load(u[i], codes, R[i]);
+                C::store(tile + i * C::ROWS * 128, a, u[i], d[i * C::ROWS * (D / QK)], up);
+                if (s + 1 < steps) C::load(u[i], codes, at_row(s + 1, j0 + i * C::ROWS));
             }
             fence_async();
             bar_arrive(&full[s & 1]);
             if (s + 1 < steps) {
-#pragma unroll
-                for (int i = 0; i < C::PIECES; ++i) {
-                    sc[i] = sn[i];
-                    C::load(sn[i], scales, at_row(s + 2, i));
-                }
                 exponent(s + 1);
+                C::load(sc, scales, at_row(s + 2, t));
             }
         }
     }
 }
 
 // ------------------------------------------------------------ softmax ----
-// Largest of a thread's 128 scores (of those that it sees).
-template <bool MASK> __device__ __forceinline__ float row_max(uint32_t S, int n) {
-    uint32_t r[2][32];
-    float m0 = -INFINITY, m1 = -INFINITY;
-    tm_ld(r[0], S);
+// A thread's 128 scores, of which it sees the first n (MASK): 32 of them from registers, unseen ones -inf; the largest.
+template <bool MASK> __device__ __forceinline__ void score_block(uint32_t (&r)[32], int c, int n, float (&m)[4]) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        tm_wait(r[c & 1]);
-        if (c < 3) tm_ld(r[(c + 1) & 1], S + (c + 1) * 32);
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-            float v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[k] = __uint_as_float(r[c & 1][e + k]);
-                if (MASK) v[k] = c * 32 + e + k < n ? v[k] : -INFINITY;
-            }
-            m0 = max3(m0, v[0], v[1]);
-            m1 = max3(m1, v[2], v[3]);
+    for (int e = 0; e < 32; e += 2) {
+        float v0 = __uint_as_float(r[e]), v1 = __uint_as_float(r[e + 1]);
+        if (MASK) {
+            v0 = c * 32 + e < n ? v0 : -INFINITY;
+            v1 = c * 32 + e + 1 < n ? v1 : -INFINITY;
+            r[e] = __float_as_uint(v0);
+            r[e + 1] = __float_as_uint(v1);
         }
+        m[e / 2 % 4] = max3(m[e / 2 % 4], v0, v1);
     }
-    return fmaxf(m0, m1);
+}
+// HOLD: blocks of 32 scores that stay in registers between the maximum and the weights; the others are read again (P's
+// 64 columns go over the first two blocks, so those stay).
+template <bool MASK, int HOLD>
+__device__ __forceinline__ float row_scores(uint32_t S, int n, uint32_t (&r)[HOLD][32]) {
+    static_assert(HOLD == 2 || HOLD == 4, "all, or what P overwrites");
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if constexpr (HOLD == 4) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tm_ld(r[c], S + c * 32);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            tm_wait(r[c]);
+            score_block<MASK>(r[c], c, n, m);
+        }
+    } else {
+        uint32_t t[32];
+        tm_ld(r[0], S);
+        tm_ld(r[1], S + 32);
+        tm_ld(t, S + 64);
+        tm_wait(r[0]);
+        score_block<MASK>(r[0], 0, n, m);
+        tm_wait(r[1]);
+        score_block<MASK>(r[1], 1, n, m);
+        tm_wait(t);
+        score_block<MASK>(t, 2, n, m);
+        tm_ld(t, S + 96);
+        tm_wait(t);
+        score_block<MASK>(t, 3, n, m);
+    }
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// exp2 of the scores (times f, less use) over them as fp16 pairs; returns their sum.  mark(c, v): a look at the 32
-// weights of column block c.
-template <bool MASK, class Mark> __device__ __forceinline__ float row_exp(uint32_t S, int n, float f, float use, Mark mark) {
-    uint32_t r[2][32];
+// exp2 of the scores (times f, less use; f >= 0, an unseen one is -inf) as fp16 pairs over them; returns their sum.
+// mark(c, v): a look at the 32 weights of column block c.
+template <bool MASK, int HOLD, class Mark>
+__device__ __forceinline__ float row_exp(uint32_t S, int n, uint32_t (&r)[HOLD][32], float f, float use, Mark mark) {
     const uint64_t ff = pair(f, f), mm = pair(-use, -use);
     uint64_t a0 = 0, a1 = 0;
-    tm_ld(r[0], S);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        tm_wait(r[c & 1]);
-        if (c < 3) tm_ld(r[(c + 1) & 1], S + (c + 1) * 32);
+    auto block = [&](int c, const uint32_t(&x)[32]) {
         float v[32];
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-            float2 y = unpair(fma2(pair(r[c & 1][e], r[c & 1][e + 1]), ff, mm));
+            float2 y = unpair(fma2(pair(x[e], x[e + 1]), ff, mm));
             if (MASK) {
                 y.x = c * 32 + e < n ? y.x : -INFINITY;
                 y.y = c * 32 + e + 1 < n ? y.y : -INFINITY;
@@ -481,12 +501,25 @@ template <bool MASK, class Mark> __device__ __forceinline__ float row_exp(uint32
         }
         mark(c, v);
         tm_st16(S + c * 16, w);
+    };
+    if constexpr (HOLD == 4) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) block(c, r[c]);
+    } else {
+        uint32_t t[32];
+        tm_ld(t, S + 64);
+        block(0, r[0]);
+        tm_ld(r[0], S + 96);
+        block(1, r[1]);
+        tm_wait(t);
+        block(2, t);
+        tm_wait(r[0]);
+        block(3, r[0]);
     }
     const float2 s = unpair(add2(a0, a1));
     return s.x + s.y;
 }
 
-// ------------------------------------------------------------- kernel ----
 template <int D, int KT, int VT>
 __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_constant__ BlockParams p) {
     using L = Lay<D>;
@@ -521,30 +554,40 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     __syncthreads();
-    // query rows (a warp each), normalised by a power of two that takes the scale's sign too
-    for (int m = warp; m < (wide ? 2 * TM : TM); m += THREADS / 32) {
-        uint32_t h[D / 64], l[D / 64];
-        float scale;
-        const int vis = query_row<D, false>(p, q, g, m < mrows ? m0 + m : m_all, m_all, lane, h, l, &scale);
-        if (scale < 0.f) {
-            scale = -scale;
+    // query rows (a warp each, four under way together), normalised by a power of two that takes the scale's sign too
+    constexpr int QR = 4;
+    constexpr int STRIDE = THREADS / 32; // (the rows that there are spread over the warps)
+    for (int mb = warp; mb < (wide ? 2 * TM : TM); mb += STRIDE * QR) {
+        float y[QR][D / 32];
+        int vis[QR];
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) h[i] ^= 0x80008000u;
-        }
-        uint8_t *dst = smem + L::Q + (m >> 7) * L::TILE + at<D>(m & 127, lane * (D / 32));
-        if constexpr (D == 128)
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(h[0], h[1]);
-        else
-            *reinterpret_cast<uint32_t *>(dst) = h[0];
-        if (lane == 0) {
-            x.qscale[m] = scale;
-            x.vis[m] = vis;
-            if (m < mrows) {
-                atomicMax(&x.vis_max, vis);
-                atomicMin(&x.vis_min, vis);
+        for (int k = 0; k < QR; ++k) vis[k] = query_load<D>(p, q, g, mb + k * STRIDE < mrows ? m0 + mb + k * STRIDE : m_all, m_all, lane, y[k]);
+#pragma unroll
+        for (int k = 0; k < QR; ++k) {
+            const int m = mb + k * STRIDE;
+            if (m >= (wide ? 2 * TM : TM)) break;
+            uint32_t h[D / 64], l[D / 64];
+            float scale = query_pack<D, false>(p, y[k], h, l);
+            if (scale < 0.f) {
+                scale = -scale;
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) h[i] ^= 0x80008000u;
             }
+            uint8_t *dst = smem + L::Q + (m >> 7) * L::TILE + at<D>(m & 127, lane * (D / 32));
+            if constexpr (D == 128)
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(h[0], h[1]);
+            else
+                *reinterpret_cast<uint32_t *>(dst) = h[0];
+            if (lane == 0) {
+                x.qscale[m] = scale;
+                x.vis[m] = vis[k];
+                if (m < mrows) {
+                    atomicMax(&x.vis_max, vis[k]);
+                    atomicMin(&x.vis_min, vis[k]);
+                }
+            }
+            if (lane < D / 16) poison[m][lane] = 0;
         }
-        if (lane < D / 16) poison[m][lane] = 0;
     }
     fence_async();
     tc_before();
@@ -560,7 +603,7 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
 
     if (warp < 8) {
         // -------------------------------------------------- softmax of half h
-        regs_inc<R_SOFT>();
+        regs_inc<Regs<KT != KVC_F16>::SOFT>();
         const int h = warp >> 2, mr = wide ? tid : (tid & 127);
         const uint32_t lanes = (uint32_t)(warp & 3) << 21; // TMEM lane 32 * (warp % 4)
         const uint32_t S = tS + h * 128 + lanes, O = tO + h * D + lanes;
@@ -578,7 +621,9 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
             if (live) {
                 const bool masked = base + TN > wvis;
                 const float f = cq * x.kfac[slot];
-                const float raw = masked ? row_max<true>(S, vis - base) : row_max<false>(S, 0);
+                constexpr int HOLD = Regs<KT != KVC_F16>::HOLD;
+                uint32_t sc[HOLD][32];
+                const float raw = masked ? row_scores<true>(S, vis - base, sc) : row_scores<false>(S, 0, sc);
                 const float top = raw == -INFINITY ? raw : raw * f;
                 float al = 1.f;
                 if (top > mx + GROW || (mx == -INFINITY && top > mx)) {
@@ -610,9 +655,9 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
                 }
                 const float use = mx == -INFINITY ? 0.f : mx;
                 if (!masked) {
-                    sum += row_exp<false>(S, 0, f, use, [](int, const float(&)[32]) {});
+                    sum += row_exp<false>(S, 0, sc, f, use, [](int, const float(&)[32]) {});
                 } else {
-                    sum += row_exp<true>(S, vis - base, f, use, [&](int c, const float(&v)[32]) {
+                    sum += row_exp<true>(S, vis - base, sc, f, use, [&](int c, const float(&v)[32]) {
                         const uint32_t rows = x.badrow[slot][c];
                         if (rows == 0) return; // V values of rows that some token does not see, and that are not finite
 #pragma unroll 1
@@ -739,8 +784,10 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(TMEM_COLS));
         }
     } else if (warp < 12) {
+        regs_dec<Regs<KT != KVC_F16>::LOAD>();
         load_rows<D, KT, false>(p, q, g, smem + L::K, x, r0, steps, vis_min, tid - 2 * GROUP);
     } else if (warp < 16) {
+        regs_dec<Regs<KT != KVC_F16>::LOAD>();
         load_rows<D, VT, true>(p, q, g, smem + L::V, x, r0, steps, vis_min, tid - 3 * GROUP);
     } else {
         regs_dec<R_MMA>();

@@ -61,9 +61,10 @@ __global__ void __launch_bounds__(THREADS) weight_kernel(const __grid_constant__
         if (tid == 0) s.vis_max = 0;
         __syncthreads();
         for (int m = warp; m < MROWS; m += THREADS / 32) {
-            float scale;
+            float x[D / 32];
             uint32_t hi[D / 64], lo[D / 64];
-            const int vis = query_row<D, LO>(p, q, g, m0 + m, m_all, lane, hi, lo, &scale);
+            const int vis = query_load<D>(p, q, g, m0 + m, m_all, lane, x);
+            const float scale = query_pack<D, LO>(p, x, hi, lo);
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
                 *reinterpret_cast<uint32_t *>(&s.qhi[m][lane * (D / 32) + 2 * i]) = hi[i];
