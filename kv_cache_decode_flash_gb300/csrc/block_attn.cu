@@ -35,7 +35,7 @@ static int ensure_block_space(Ctx *c, cudaStream_t st) {
 }
 
 // Cut the cached rows of the launch's units into parts.  `want`: items that run
-// at once; a part has two steps at least (`least` rows), and the partial rows
+// at once; a part has `least` rows at least, and the partial rows
 // of all parts fit the work space.
 // An item costs `fixed` steps beside its own.
 //  One sequence: its units are alike, so the schedule is whole waves; those of
@@ -43,8 +43,8 @@ static int ensure_block_space(Ctx *c, cudaStream_t st) {
 //  Several: all rows are cut into parts of at most one length, the one for
 // which a schedule ends first that ends half the longest item after the mean
 // (or, in one wave, with the longest item).
-static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t part_cap) {
-    const int64_t least = 2 * step, fixed = 4;
+static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t least, int64_t part_cap) {
+    const int64_t fixed = 4;
     auto parts = [](const BlockSeq &s, int64_t len) {
         return (int32_t)std::max<int64_t>(1, (s.n_rows + len - 1) / len);
     };
@@ -132,7 +132,8 @@ static bool plan_block(BlockParams &p, int sms, bool tc) {
         BlockSeq &s = p.seq[i];
         s.tiles = (int32_t)(((int64_t)s.n_tok * p.r + p.tile_m - 1) / p.tile_m);
     }
-    plan_splits(p, tc ? sms : 2 * sms, tc ? CROSS_TC_TILE_N : CROSS_TILE_N, part_rows_cap(sms));
+    const int step = tc ? CROSS_TC_TILE_N : CROSS_TILE_N;
+    plan_splits(p, tc ? sms : 2 * sms, step, 2 * step, part_rows_cap(sms));
     return narrow;
 }
 
@@ -273,8 +274,7 @@ extern "C" int kvc_attn_weight(kvc_ctx *cc, int layer, int n_seq, const int32_t 
         p.w = w;
         p.w_stride = w_stride;
         p.n_seq = std::min(MAX_SEQ_PER_LAUNCH, n_seq - base);
-        int32_t most = 0;
-        int64_t item = 0;
+        p.part_rows = 1;
         for (int i = 0; i < p.n_seq; ++i) {
             BlockSeq &s = p.seq[i];
             const Seq &sq = c->seqs[(size_t)seq_ids[base + i]];
@@ -284,15 +284,11 @@ extern "C" int kvc_attn_weight(kvc_ctx *cc, int layer, int n_seq, const int32_t 
             s.tok0 = (int32_t)tok0;
             s.n_tok = n_q[base + i];
             s.w_index = base + i;
-            s.splits = std::max(1, (s.n_rows + CROSS_TILE_N - 1) / CROSS_TILE_N);
-            s.item0 = (int32_t)item;
-            if (s.n_tok > 0 && s.n_rows > 0) item += (int64_t)s.splits * c->Hk;
-            if (item > INT32_MAX) return c->fail(KVC_EINVAL, "too many rows in one block");
+            s.tiles = s.n_tok > 0 && s.n_rows > 0 ? 1 : 0;
             tok0 += s.n_tok;
-            most = std::max(most, s.n_tok);
         }
-        p.n_items = (int32_t)item;
-        cudaError_t e = launch_weight(c->tk, p, (int64_t)most * c->r <= 16, st);
+        plan_splits(p, c->sms, WEIGHT_STEP, WEIGHT_STEP, INT32_MAX); // (no partial rows: a cached row's sum is one item's)
+        cudaError_t e = launch_weight(c->tk, p, st);
         if (e != cudaSuccess) return cuda_fail(c, e, "row weight kernel");
     }
     return KVC_OK;

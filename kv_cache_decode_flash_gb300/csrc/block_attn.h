@@ -67,7 +67,8 @@ cudaError_t launch_cross_tc(int type_k, int type_v, const BlockParams &p, cudaSt
 // Joins the parts of the launch's cut units (k_join.cu; the two above end with it).
 cudaError_t launch_join(const BlockParams &p, cudaStream_t st);
 
-// The rows' weights: splits of a sequence are its steps of CROSS_TILE_N rows, items (KV head, step).
-cudaError_t launch_weight(int type_k, const BlockParams &p, bool narrow, cudaStream_t st);
+// The rows' weights: a unit is a KV head (one tile), a step WEIGHT_STEP rows.
+constexpr int WEIGHT_STEP = 256;
+cudaError_t launch_weight(int type_k, const BlockParams &p, cudaStream_t st);
 
 } // namespace kvc
