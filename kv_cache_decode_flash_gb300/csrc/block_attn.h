@@ -68,7 +68,7 @@ cudaError_t launch_cross_tc(int type_k, int type_v, const BlockParams &p, cudaSt
 cudaError_t launch_join(const BlockParams &p, cudaStream_t st);
 
 // The rows' weights: a unit is a KV head (one tile), a step WEIGHT_STEP rows.
-constexpr int WEIGHT_STEP = 256;
+constexpr int WEIGHT_STEP = 128;
 cudaError_t launch_weight(int type_k, const BlockParams &p, cudaStream_t st);
 
 } // namespace kvc

@@ -4,204 +4,345 @@
 //              exp(scale * q[t][h] . K_j - lse[t][h]),
 // lse the statistics that the attention of the same tokens left behind.
 //
-// A work item is a KV head and a range of cached rows; its query rows (tokens x
-// query heads of the group) lie in shared memory as fp16, up to MG of them at a
-// time, for the whole range.  A warp owns 32 cached rows of a step of 256: it
-// loads them straight into the operand layout of mma.m16n8k16 and keeps them
-// while all query rows pass, so K is read once, scores never leave the
-// registers, and a row's sum is one warp's: its order is fixed without atomics.
-//   The products' order within a block of 32 values is free, so a quad's thread
-// takes 8 consecutive ones of both operands: codes come as 8-byte loads, query
-// rows as 16-byte shared loads.  Codes are exact in fp16 and so is a 16-bit
-// query (32-bit ones are two parts): a block's partial score comes from the
-// tensor cores, its scale is applied in 32 bits.
-// What bounds it: few query rows, the bytes of K; many, the products (the
-// register-operand tensor path, about 600 TFLOP/s here; tcgen05 would have to
-// take K as two fp16 parts, and pad 160 query rows to 256, for the same
-// accuracy, which comes to the same time).
-#include "block_tile.cuh"
+// The scores are formed transposed, S^T = K Q^T, on tcgen05: 128 cached rows of a
+// step are the accumulator's lanes and the query rows (tokens x query heads of
+// the group, up to 256) its columns, so that a thread owns a cached row and the
+// sum over the query rows is its own: no exchange, no atomics, one fixed order.
+// The query rows lie in shared memory for a work item's whole range of cached
+// rows (a KV head's), and K is read once.
+//   Sums of weights are 32-bit results, so operands lose nothing that matters:
+// K = code * scale is taken as two fp16 parts, which hold its 18 bits exactly
+// (halves are one part), a 16-bit query is exact in fp16 and a 32-bit one two
+// parts, whose product with K's second part (2^-22 of the first's) is left out.
+// A power of two brings a step's largest scale to [2^3, 2^4); it changes only
+// when the scales have moved by 2^4, so that the factors per query row, in which
+// it is undone, are seldom rewritten.
+//   One CTA per SM, 17 warps: two softmax groups and two loading groups that take
+// the steps in turn, and the issuing thread; the accumulators alternate in TMEM.
+// What bounds it: few query rows, the bytes of K; many, the loading groups'
+// conversion beside the products (128 x rows x D for each part).
+#include "tc_tile.cuh"
 
 namespace kvc {
 namespace {
 
-constexpr int THREADS = 256, WARPS = THREADS / 32;
-constexpr int NR = 32;            // cached rows of a warp's step
-constexpr int STEP = WEIGHT_STEP; // of the CTA's
-static_assert(STEP == WARPS * NR, "a step is every warp's rows");
+constexpr int THREADS = 5 * GROUP; // roles: softmax of even and of odd steps, loading of even and odd steps, the issuing warp
+constexpr int TN = TC_M;           // cached rows of a step
+static_assert(WEIGHT_STEP == TN, "items are whole steps");
 
-template <int D, bool LO> struct Shape {
-    static constexpr int MG = LO ? 128 : 256; // query rows in shared memory
-    static constexpr int PITCH = D + 32;      // halves: rows 64 bytes off a multiple of 128, so a quarter warp's loads do not collide
-    struct Smem {
-        __half q[LO ? 2 : 1][MG][PITCH];
-        float scale[MG];
-        float lse[MG]; // in log2 units
-        int32_t vis[MG];
-    };
+enum Bar { KF0, KF1, KE0, KE1, SF0, SF1, SE0, SE1, QF, DRAIN, N_BARS };
+
+template <int D, bool CODES, bool LO> struct Lay {
+    static constexpr int MG = LO ? 128 : 256;         // query rows at a time
+    static constexpr int QT = D / 64 * MG * 128;      // bytes of one of their fp16 parts
+    static constexpr int KT = D / 64 * TN * 128;      // bytes of one part of a step
+    static constexpr int KS = (CODES ? 2 : 1) * KT;   // of a stage
+    static constexpr int K = (LO ? 2 : 1) * QT, AUX = K + 2 * KS;
 };
+
+struct Aux {
+    uint64_t bar[N_BARS];
+    alignas(16) float2 fz[2][256];   // per softmax group and query row: score factor, log2 of its sum
+    float2 fz0[256];                 // the same before a step's exponent
+    int32_t vis[256];
+    int32_t row[2][2][TN];           // per loading group: pool rows of its step and of its next one
+    int32_t kexp[2][4];              // exponent of a step, by its group and place
+    alignas(16) uint32_t red[2][2][GROUP / 32];
+    uint16_t scale[2][2][TN * 4];
+    uint32_t tmem;
+    int32_t vis_max, vis_min;
+    volatile int32_t abort;
+};
+
+template <int D, bool CODES, bool LO> constexpr int smem_bytes() {
+    const int need = Lay<D, CODES, LO>::AUX + (int)sizeof(Aux) + 1024;
+    return need > 120 * 1024 ? need : 120 * 1024; // TMEM is allocated whole: one CTA per SM
+}
+
+// codes * scale * 2^up as two fp16 parts, exactly
+template <int D>
+__device__ __forceinline__ void store_parts(uint8_t *hi, uint8_t *lo, const uint32_t *a, const uint4 &u, uint16_t s, float up) {
+    const __half2 d = __half2half2(__float2half_rn(__half2float(__ushort_as_half(s)) * up));
+    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint2 c = codes4(in[2 * k + i]);
+            const uint32_t cc[2] = {c.x, c.y};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const __half2 x = *reinterpret_cast<const __half2 *>(&cc[e]);
+                const __half2 y = __hmul2(x, d);
+                const __half2 z = __hfma2(x, d, __hneg2(y)); // what the first part leaves (one rounding, exact here)
+                h[2 * i + e] = *reinterpret_cast<const uint32_t *>(&y);
+                l[2 * i + e] = *reinterpret_cast<const uint32_t *>(&z);
+            }
+        }
+        *reinterpret_cast<uint4 *>(hi + a[k]) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(lo + a[k]) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+}
 
 template <int D, int KT, bool LO>
 __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constant__ BlockParams p) {
-    using Sh = Shape<D, LO>;
-    constexpr int NB = D / QK, NT = NR / 8;
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    typename Sh::Smem &s = *reinterpret_cast<typename Sh::Smem *>(smem_raw);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, qc = lane & 3;
+    constexpr bool CODES = KT != KVC_F16;
+    using L = Lay<D, CODES, LO>;
+    constexpr int MG = L::MG;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    Aux &x = *reinterpret_cast<Aux *>(smem + L::AUX);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
     const BlockSeq q = p.seq[item_seq(p, (int)blockIdx.x)];
     int g, part, parts;
     item_unit(q, (int)blockIdx.x - q.item0, g, part, parts);
-    const int m_all = q.n_tok * p.r;
-    const int r0 = part * q.split_rows, r1 = parts == 1 ? q.n_rows : min(r0 + q.split_rows, q.n_rows);
-    float *w = p.w + ((int64_t)q.w_index * p.Hk + g) * p.w_stride;
+    const int m_all = q.n_tok * p.r, groups = (m_all + MG - 1) / MG;
+    if (tid == 0) {
+        for (int i = 0; i < N_BARS; ++i)
+            bar_init(&x.bar[i], i == KF0 || i == KF1 || i == SE0 || i == SE1 ? GROUP : (i == QF ? 2 * GROUP : 1));
+        x.vis_max = 0;
+        x.vis_min = 0x7fffffff;
+        x.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&x.tmem)), "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    __syncthreads();
+    for (int t = tid; t < q.n_tok; t += THREADS) {
+        const int v = p.n_vis ? min(max(p.n_vis[(int64_t)q.tok0 + t], 0), q.n_rows) : q.n_rows;
+        atomicMax(&x.vis_max, v);
+        atomicMin(&x.vis_min, v);
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tm = x.tmem; // two accumulators of 256 columns
+    const int r0 = part * q.split_rows, r1 = min(parts == 1 ? q.n_rows : r0 + q.split_rows, x.vis_max);
+    const int steps = r1 > r0 ? (r1 - r0 + TN - 1) / TN : 0, jobs = groups * steps; // job: a step of a group of query rows
+    const int vis_min = x.vis_min;
 
-    for (int mg = 0; mg < m_all; mg += Sh::MG) {
-        const int rows = min(Sh::MG, m_all - mg), tiles = (rows + 15) / 16;
-        __syncthreads(); // the query rows before are done with
-        constexpr int QR = 4;
-        for (int mb = warp; mb < tiles * 16; mb += WARPS * QR) {
-            float x[QR][D / 32];
-            int vis[QR];
-            float z[QR];
+    if (warp < 8) {
+        // -------------------------------------------------- sums, and the query rows
+        const int h = warp >> 2, t = tid & 127;
+        const uint32_t S = tm + h * 256 + ((uint32_t)(warp & 3) << 21);
+        float *w = p.w + ((int64_t)q.w_index * p.Hk + g) * p.w_stride;
+        int done = 0; // jobs of this group
+        for (int mg = 0; mg < groups && steps > 0; ++mg) {
+            const int rows = min(MG, m_all - mg * MG), cols = (rows + 15) / 16 * 16;
+            named_sync<2, 2 * GROUP>(); // every product with the rows before is done: both groups have its scores
+            constexpr int QR = 4;
+            for (int mb = warp; mb < cols; mb += 8 * QR) {
+                float y[QR][D / 32];
+                int vis[QR];
+                float z[QR];
 #pragma unroll
-            for (int k = 0; k < QR; ++k) {
-                const int m = mb + k * WARPS;
-                vis[k] = query_load<D>(p, q, g, m < rows ? mg + m : m_all, m_all, lane, x[k]);
-                z[k] = 0.f;
-                if (m < rows && vis[k] > 0) {
-                    const int t = (mg + m) / p.r, j = (mg + m) % p.r;
-                    z[k] = p.lse[((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j] * 1.44269504f;
+                for (int k = 0; k < QR; ++k) {
+                    const int m = mb + k * 8;
+                    vis[k] = query_load<D>(p, q, g, m < rows ? mg * MG + m : m_all, m_all, lane, y[k]);
+                    z[k] = INFINITY; // a row that is not there, or sees nothing: weight 0
+                    if (m < rows && vis[k] > 0) {
+                        const int tok = (mg * MG + m) / p.r, j = (mg * MG + m) % p.r;
+                        z[k] = p.lse[((int64_t)q.tok0 + tok) * p.H + (int64_t)g * p.r + j] * 1.44269504f;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < QR; ++k) {
+                    const int m = mb + k * 8;
+                    if (m >= cols) break;
+                    uint32_t hi[D / 64], lo[D / 64];
+                    const float scale = query_pack<D, LO>(p, y[k], hi, lo);
+                    uint8_t *dst = smem + at<MG>(m, lane * (D / 32));
+                    if constexpr (D == 128) {
+                        *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
+                        if (LO) *reinterpret_cast<uint2 *>(dst + L::QT) = make_uint2(lo[0], lo[1]);
+                    } else {
+                        *reinterpret_cast<uint32_t *>(dst) = hi[0];
+                        if (LO) *reinterpret_cast<uint32_t *>(dst + L::QT) = lo[0];
+                    }
+                    if (lane == 0) {
+                        x.fz0[m] = make_float2(m < rows ? scale : 0.f, z[k]);
+                        x.vis[m] = vis[k];
+                    }
                 }
             }
-#pragma unroll
-            for (int k = 0; k < QR; ++k) {
-                const int m = mb + k * WARPS;
-                if (m >= tiles * 16) break;
-                uint32_t hi[D / 64], lo[D / 64];
-                const float scale = query_pack<D, LO>(p, x[k], hi, lo);
-#pragma unroll
-                for (int i = 0; i < D / 64; ++i) {
-                    *reinterpret_cast<uint32_t *>(&s.q[0][m][lane * (D / 32) + 2 * i]) = hi[i];
-                    if (LO) *reinterpret_cast<uint32_t *>(&s.q[LO][m][lane * (D / 32) + 2 * i]) = lo[i];
+            fence_async();
+            named_sync<2, 2 * GROUP>(); // the rows' factors are there
+            bar_arrive(&x.bar[QF]);
+            int E = 0x7fffffff; // exponent that this group's factors hold
+            for (int i = mg * steps + ((mg * steps + h) & 1); i < (mg + 1) * steps; i += 2, ++done) {
+                const int base = r0 + (i - mg * steps) * TN, j = base + t;
+                const bool in = j < r1;
+                const float old = in ? w[j] : 0.f;
+                bar_wait_warp(&x.bar[SF0 + h], done & 1, p.err, &x.abort);
+                tc_after();
+                const int e = CODES ? x.kexp[h][done & 3] : 3;
+                if (e != E) {
+                    if (h == 0) named_sync<5, GROUP>(); else named_sync<6, GROUP>(); // the old ones are read no more
+                    const float f = ldexpf(1.f, e - 3);
+                    for (int m = t; m < cols; m += GROUP) x.fz[h][m] = make_float2(x.fz0[m].x * f, -x.fz0[m].y);
+                    if (h == 0) named_sync<5, GROUP>(); else named_sync<6, GROUP>();
+                    E = e;
                 }
-                if (lane == 0) {
-                    s.scale[m] = scale;
-                    s.lse[m] = z[k];
-                    s.vis[m] = vis[k];
+                const bool masked = base + TN > vis_min;
+                float a[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t r[2][16];
+                auto block = [&](int c, const uint32_t(&v)[16]) {
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&x.fz[h][c + k]); // (broadcast)
+                        const float y0 = ex2(fmaf(__uint_as_float(v[k]), f.x, f.y)), y1 = ex2(fmaf(__uint_as_float(v[k + 1]), f.z, f.w));
+                        if (masked) {
+                            a[k & 2] += j < x.vis[c + k] ? y0 : 0.f;
+                            a[(k & 2) + 1] += j < x.vis[c + k + 1] ? y1 : 0.f;
+                        } else {
+                            a[k & 2] += y0;
+                            a[(k & 2) + 1] += y1;
+                        }
+                    }
+                };
+                tm_ld16(r[0], S);
+                for (int c = 0; c < cols; c += 32) {
+                    tm_wait16(r[0]);
+                    if (c + 16 < cols) tm_ld16(r[1], S + c + 16);
+                    block(c, r[0]);
+                    if (c + 16 < cols) {
+                        tm_wait16(r[1]);
+                        if (c + 32 < cols) tm_ld16(r[0], S + c + 32);
+                        block(c + 16, r[1]);
+                    }
+                }
+                tc_before();
+                bar_arrive(&x.bar[SE0 + h]);
+                if (in) w[j] = old + ((a[0] + a[1]) + (a[2] + a[3]));
+            }
+        }
+        tc_before();
+        named_sync<2, 2 * GROUP>();
+        if (warp == 0) {
+            tc_after();
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(TMEM_COLS));
+        }
+    } else if (warp < 16) {
+        // -------------------------------------------------- cached rows: this group's steps into its stage
+        const int y = (warp >> 2) & 1, t = tid & 127;
+        uint8_t *tile = smem + L::K + y * L::KS;
+        int32_t(*row)[TN] = x.row[y];
+        auto sync = [&] {
+            if (y == 0) named_sync<3, GROUP>(); else named_sync<4, GROUP>();
+        };
+        auto find = [&](int i) { return i < jobs ? max(pool_row(p, q, g, min(r0 + i % steps * TN + t, q.n_rows - 1)), 0) : 0; };
+        if (y < jobs) {
+            row[0][t] = find(y);
+            row[1][t] = find(y + 2);
+            int32_t next = find(y + 4);
+            sync();
+            int k = 0; // steps of this group done
+            if constexpr (!CODES) {
+                for (int i = y; i < jobs; i += 2, ++k) {
+                    if (k > 0) bar_wait(&x.bar[KE0 + y], (k - 1) & 1, p.err, &x.abort);
+                    copy_halves<D>(tile, p.kdata, row[k & 1], t);
+                    sync();
+                    row[k & 1][t] = next; // of this group's step after next
+                    next = find(i + 6);
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    fence_async();
+                    bar_arrive(&x.bar[KF0 + y]);
+                    sync();
+                }
+            } else {
+                using C = Codes<D, KT>;
+                const int c = t % C::PIECES, j0 = t / C::PIECES;
+                const uint8_t *codes = p.kdata + c * 16;
+                const uint32_t a[2] = {at(j0, c * 16), at(j0, c * 16 + 8)};
+                uint4 u[C::PIECES];
+                uint32_t sc[D / 64];
+                int E = 0x7fffffff;
+                auto exponent = [&](int n, int i) { // of this group's n-th step (job i), whose scales are sc
+                    uint32_t m = 0;
+                    const bool in = r0 + i % steps * TN + t < q.n_rows;
+#pragma unroll
+                    for (int b = 0; b < D / QK; ++b) {
+                        uint32_t v = sc[b >> 1] >> (16 * (b & 1)) & 0xffffu;
+                        if (!in) v = 0;
+                        if ((v & 0x7fffu) < 0x7c00u) m = max(m, v & 0x7fffu);
+                        x.scale[y][n & 1][t * (D / QK) + b] = (uint16_t)v;
+                    }
+                    m = __reduce_max_sync(0xffffffffu, m);
+                    if ((t & 31) == 0) x.red[y][n & 1][t >> 5] = m;
+                    sync();
+                    const uint4 r = *reinterpret_cast<const uint4 *>(x.red[y][n & 1]);
+                    const uint32_t top = max(max(r.x, r.y), max(r.z, r.w));
+                    const int e = top ? ilogbf(__half2float(__ushort_as_half((uint16_t)top))) : E_MIN;
+                    if (E == 0x7fffffff || e > E + 4 || e < E - 4) E = e;
+                    if (t == 0) x.kexp[y][n & 3] = E;
+                };
+                C::load(sc, p.ks, row[0][t]);
+#pragma unroll
+                for (int b = 0; b < C::PIECES; ++b) C::load(u[b], codes, row[0][j0 + b * C::ROWS]);
+                exponent(0, y);
+                C::load(sc, p.ks, row[1][t]);
+                for (int i = y; i < jobs; i += 2, ++k) {
+                    if (k > 0) bar_wait(&x.bar[KE0 + y], (k - 1) & 1, p.err, &x.abort);
+                    const float up = ldexpf(1.f, 3 - E);
+                    const uint16_t *d = &x.scale[y][k & 1][j0 * (D / QK) + c / 2];
+#pragma unroll
+                    for (int b = 0; b < C::PIECES; ++b) {
+                        store_parts<D>(tile + b * C::ROWS * 128, tile + L::KT + b * C::ROWS * 128, a, u[b], d[b * C::ROWS * (D / QK)], up);
+                        if (i + 2 < jobs) C::load(u[b], codes, row[(k + 1) & 1][j0 + b * C::ROWS]);
+                    }
+                    fence_async();
+                    bar_arrive(&x.bar[KF0 + y]);
+                    if (i + 2 < jobs) {
+                        row[k & 1][t] = next;
+                        next = find(i + 6);
+                        exponent(k + 1, i + 2); // (its barrier: the rows are there too)
+                        C::load(sc, p.ks, row[k & 1][t]);
+                    }
                 }
             }
         }
-        __syncthreads();
-
-        for (int base = r0 + warp * NR; base < r1; base += STEP) {
-            // the warp's rows: lane l looks row l up
-            const int32_t R = max(base + lane < r1 ? pool_row(p, q, g, base + lane) : 0, 0);
-            uint32_t kb[NT][NB][4]; // [8 rows][block of 32 values][operand registers of two products]
+    } else if (warp == 16 && lane == 0) {
+        // -------------------------------------------------- products
+        const uint32_t sq = smem_u32(smem), sk = smem_u32(smem + L::K);
+        int i = 0;
+        for (int mg = 0; mg < groups && steps > 0; ++mg) {
+            const int cols = (min(MG, m_all - mg * MG) + 15) / 16 * 16;
+            bar_wait(&x.bar[QF], mg & 1, p.err, &x.abort);
+            for (int s = 0; s < steps; ++s, ++i) {
+                const int h = i & 1, k = i >> 1;
+                bar_wait(&x.bar[KF0 + h], k & 1, p.err, &x.abort);
+                if (k > 0) bar_wait(&x.bar[SE0 + h], (k - 1) & 1, p.err, &x.abort);
+                tc_after();
+                const uint32_t tS = tm + h * 256, kt = sk + h * L::KS, id = inst(cols, false);
+                for (int n = 0; n < 1 + (CODES ? 1 : 0) + (LO ? 1 : 0); ++n) { // the parts' products, the largest first
+                    const uint32_t ka = kt + (CODES && n == 1 ? L::KT : 0);
+                    const uint32_t qa = sq + (LO && n == (CODES ? 2 : 1) ? L::QT : 0);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int64_t Rn = __shfl_sync(0xffffffffu, R, n * 8 + gid);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    if constexpr (KT == KVC_F16) {
-                        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p.kdata + Rn * (2 * D)) + b * 4 + qc);
-                        kb[n][b][0] = u.x, kb[n][b][1] = u.y, kb[n][b][2] = u.z, kb[n][b][3] = u.w;
-                    } else {
-                        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p.kdata + Rn * D) + b * 4 + qc);
-                        const uint2 lo = codes4(u.x), hi = codes4(u.y);
-                        kb[n][b][0] = lo.x, kb[n][b][1] = lo.y, kb[n][b][2] = hi.x, kb[n][b][3] = hi.y;
-                    }
+                    for (int d = 0; d < D / 16; ++d)
+                        mma_ss(tS, desc(ka + (d >> 2) * (TN * 128) + (d & 3) * 32, 16),
+                               desc(qa + (d >> 2) * (MG * 128) + (d & 3) * 32, 16), id, n > 0 || d > 0);
                 }
+                tc_commit(&x.bar[SF0 + h]);
+                tc_commit(&x.bar[KE0 + h]);
             }
-            uint32_t ds[NT][NB]; // scales of the rows 2 qc and 2 qc + 1 of each eight, a half each
-            if constexpr (KT != KVC_F16) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int64_t Ra = __shfl_sync(0xffffffffu, R, n * 8 + qc * 2), Rb = __shfl_sync(0xffffffffu, R, n * 8 + qc * 2 + 1);
-                    uint32_t a[NB / 2], c[NB / 2];
-#pragma unroll
-                    for (int b = 0; b < NB / 2; ++b) {
-                        a[b] = __ldg(reinterpret_cast<const uint32_t *>(p.ks + Ra * NB) + b);
-                        c[b] = __ldg(reinterpret_cast<const uint32_t *>(p.ks + Rb * NB) + b);
-                    }
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) ds[n][b] = __byte_perm(a[b / 2], c[b / 2], b & 1 ? 0x7632 : 0x5410);
-                }
-            }
-            float acc[NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = 0.f;
-#pragma unroll 1
-            for (int mt = 0; mt < tiles; ++mt) {
-                const int ma = mt * 16 + gid;
-                const int va = s.vis[ma] - base, vb = s.vis[ma + 8] - base;
-                if (!__any_sync(0xffffffffu, va > 0 || vb > 0)) continue; // none of these tokens sees the rows
-                float sc[NT][4];
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) sc[n][k] = 0.f;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    float t[NT][4];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) t[n][k] = 0.f;
-#pragma unroll
-                    for (int l = 0; l < (LO ? 2 : 1); ++l) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(&s.q[l][ma][b * 32 + qc * 8]);
-                        const uint4 y = *reinterpret_cast<const uint4 *>(&s.q[l][ma + 8][b * 32 + qc * 8]);
-                        const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma(t[n], a0, kb[n][b][0], kb[n][b][1]);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma(t[n], a1, kb[n][b][2], kb[n][b][3]);
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if constexpr (KT != KVC_F16) {
-                            const float2 d = f2(ds[n][b]);
-                            sc[n][0] = fmaf(t[n][0], d.x, sc[n][0]);
-                            sc[n][1] = fmaf(t[n][1], d.y, sc[n][1]);
-                            sc[n][2] = fmaf(t[n][2], d.x, sc[n][2]);
-                            sc[n][3] = fmaf(t[n][3], d.y, sc[n][3]);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) sc[n][k] += t[n][k];
-                        }
-                    }
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float f = s.scale[ma + 8 * h], z = s.lse[ma + 8 * h];
-                    const int v = h ? vb : va;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float e = ex2(fmaf(sc[n][2 * h + k], f, -z));
-                            acc[n][k] += n * 8 + qc * 2 + k < v ? e : 0.f;
-                        }
-                }
-            }
-            // over the eight row groups; then lane l has cached row l's sum
-            float mine = 0.f;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) acc[n][k] += __shfl_xor_sync(0xffffffffu, acc[n][k], o);
-                    const float x = __shfl_sync(0xffffffffu, acc[n][k], (lane & 7) >> 1);
-                    if ((lane >> 3) == n && (lane & 1) == k) mine = x;
-                }
-            if (base + lane < r1) w[base + lane] += mine;
+        }
+        // nothing may be in flight when the CTA gives its memory back
+        tc_commit(&x.bar[DRAIN]);
+        const uint64_t t0 = now_ns();
+        while (!bar_try(&x.bar[DRAIN], 0) && now_ns() - t0 < WAIT_NS) {
         }
     }
 }
 
 template <int D, int KT, bool LO> cudaError_t go(const BlockParams &p, cudaStream_t st) {
     auto k = weight_kernel<D, KT, LO>;
-    const int bytes = (int)sizeof(typename Shape<D, LO>::Smem);
+    constexpr int bytes = smem_bytes<D, KT != KVC_F16, LO>();
+    static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     k<<<(unsigned)p.n_items, THREADS, bytes, st>>>(p);
