@@ -81,11 +81,10 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
     uint64_t *full = &x.bar[IS_V ? VF0 : KF0], *empty = &x.bar[IS_V ? VE0 : KE0];
     int32_t(*row)[TN] = x.row[IS_V];
     constexpr int SYNC = IS_V ? 4 : 3;
-    // the pool rows of a step: looked up one step before they are handed to the group, so that nobody waits for the table
-    int32_t next = -1;
-    auto look_up = [&](int s) { next = s < steps ? pool_row(p, q, g, r0 + s * TN + t) : -1; };
+    Lookup next; // of the step whose rows the group gets next
+    auto look_up = [&](int s) { next.ask(p, q, r0 + s * TN + t, s < steps); };
     auto find = [&](int s) { // for all threads after the next barrier
-        row[s % SLOTS][t] = next;
+        row[s % SLOTS][t] = next.row(p, g);
         look_up(s + 1);
     };
     auto clear = [&](int s) { // a step's reports; those of four steps before are read no more
@@ -134,9 +133,8 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
         const uint8_t *codes = data + c * 16;
         const uint16_t *scales = IS_V ? p.vs : p.ks;
         uint32_t a[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            a[k] = T == KVC_Q4_0 ? at(j0, c * 32 + k * 8) : at(j0, c * 16 + (k & 1) * 8);
+        constexpr bool f = false; // (avoiding the stores' bank conflicts costs more instructions here than it saves)
+        C::places(j0, c, a, f);
         uint4 u[C::PIECES];
         uint32_t sc[D / 64];
         auto at_row = [&](int s, int j) { return max(row[s % SLOTS][j], 0); };
@@ -187,7 +185,7 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
             const uint16_t *d = &x.scale[IS_V][s & 1][j0 * (D / QK) + (T == KVC_Q4_0 ? c : c / 2)];
 #pragma unroll
             for (int i = 0; i < C::PIECES; ++i) {
-                C::store(tile + i * C::ROWS * 128, a, u[i], d[i * C::ROWS * (D / QK)], up);
+                C::store(tile + i * C::ROWS * 128, a, u[i], scaled(d[i * C::ROWS * (D / QK)], up), f);
                 if (s + 1 < steps) C::load(u[i], codes, at_row(s + 1, j0 + i * C::ROWS));
             }
             fence_async();

@@ -44,7 +44,7 @@ struct Aux {
     uint64_t bar[N_BARS];
     alignas(16) float2 fz[2][256];   // per softmax group and query row: score factor, log2 of its sum
     float2 fz0[256];                 // the same before a step's exponent
-    int32_t vis[256];
+    alignas(16) int32_t vis[256];
     int32_t row[2][2][TN];           // per loading group: pool rows of its step and of its next one
     int32_t kexp[2][4];              // exponent of a step, by its group and place
     alignas(16) uint32_t red[2][2][GROUP / 32];
@@ -59,11 +59,10 @@ template <int D, bool CODES, bool LO> constexpr int smem_bytes() {
     return need > 120 * 1024 ? need : 120 * 1024; // TMEM is allocated whole: one CTA per SM
 }
 
-// codes * scale * 2^up as two fp16 parts, exactly
+// codes * d as two fp16 parts, exactly
 template <int D>
-__device__ __forceinline__ void store_parts(uint8_t *hi, uint8_t *lo, const uint32_t *a, const uint4 &u, uint16_t s, float up) {
-    const __half2 d = __half2half2(__float2half_rn(__half2float(__ushort_as_half(s)) * up));
-    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void store_parts(uint8_t *hi, uint8_t *lo, const uint32_t (&a)[4], const uint4 &u, __half2 d, bool f) {
+    const uint32_t in[4] = {f ? u.z : u.x, f ? u.w : u.y, f ? u.x : u.z, f ? u.y : u.w};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         uint32_t h[4], l[4];
@@ -83,6 +82,47 @@ __device__ __forceinline__ void store_parts(uint8_t *hi, uint8_t *lo, const uint
         *reinterpret_cast<uint4 *>(hi + a[k]) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4 *>(lo + a[k]) = make_uint4(l[0], l[1], l[2], l[3]);
     }
+}
+
+// The sum of a cached row's weights over `cols` query rows; MASK: of those that see row j.
+template <bool MASK>
+__device__ __forceinline__ float row_sum(uint32_t S, int cols, const float2 *fz, const int32_t *vis, int j) {
+    uint64_t a0 = 0, a1 = 0;
+    uint32_t r[2][16];
+    auto block = [&](int c, const uint32_t(&v)[16]) {
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                const float4 f = *reinterpret_cast<const float4 *>(&fz[c + k + i]); // (a broadcast)
+                y[i] = ex2(fmaf(__uint_as_float(v[k + i]), f.x, f.y));
+                y[i + 1] = ex2(fmaf(__uint_as_float(v[k + i + 1]), f.z, f.w));
+            }
+            if (MASK) {
+                const int4 s = *reinterpret_cast<const int4 *>(&vis[c + k]);
+                y[0] = j < s.x ? y[0] : 0.f;
+                y[1] = j < s.y ? y[1] : 0.f;
+                y[2] = j < s.z ? y[2] : 0.f;
+                y[3] = j < s.w ? y[3] : 0.f;
+            }
+            a0 = add2(a0, pair(y[0], y[1]));
+            a1 = add2(a1, pair(y[2], y[3]));
+        }
+    };
+    tm_ld16(r[0], S);
+    for (int c = 0; c < cols; c += 32) {
+        tm_wait16(r[0]);
+        if (c + 16 < cols) tm_ld16(r[1], S + c + 16);
+        block(c, r[0]);
+        if (c + 16 < cols) {
+            tm_wait16(r[1]);
+            if (c + 32 < cols) tm_ld16(r[0], S + c + 32);
+            block(c + 16, r[1]);
+        }
+    }
+    const float2 s = unpair(add2(a0, a1));
+    return s.x + s.y;
 }
 
 template <int D, int KT, bool LO>
@@ -188,37 +228,10 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
                     if (h == 0) named_sync<5, GROUP>(); else named_sync<6, GROUP>();
                     E = e;
                 }
-                const bool masked = base + TN > vis_min;
-                float a[4] = {0.f, 0.f, 0.f, 0.f};
-                uint32_t r[2][16];
-                auto block = [&](int c, const uint32_t(&v)[16]) {
-#pragma unroll
-                    for (int k = 0; k < 16; k += 2) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&x.fz[h][c + k]); // (broadcast)
-                        const float y0 = ex2(fmaf(__uint_as_float(v[k]), f.x, f.y)), y1 = ex2(fmaf(__uint_as_float(v[k + 1]), f.z, f.w));
-                        if (masked) {
-                            a[k & 2] += j < x.vis[c + k] ? y0 : 0.f;
-                            a[(k & 2) + 1] += j < x.vis[c + k + 1] ? y1 : 0.f;
-                        } else {
-                            a[k & 2] += y0;
-                            a[(k & 2) + 1] += y1;
-                        }
-                    }
-                };
-                tm_ld16(r[0], S);
-                for (int c = 0; c < cols; c += 32) {
-                    tm_wait16(r[0]);
-                    if (c + 16 < cols) tm_ld16(r[1], S + c + 16);
-                    block(c, r[0]);
-                    if (c + 16 < cols) {
-                        tm_wait16(r[1]);
-                        if (c + 32 < cols) tm_ld16(r[0], S + c + 32);
-                        block(c + 16, r[1]);
-                    }
-                }
+                const float add = base + TN > vis_min ? row_sum<true>(S, cols, x.fz[h], x.vis, j) : row_sum<false>(S, cols, x.fz[h], x.vis, j);
                 tc_before();
                 bar_arrive(&x.bar[SE0 + h]);
-                if (in) w[j] = old + ((a[0] + a[1]) + (a[2] + a[3]));
+                if (in) w[j] = old + add;
             }
         }
         tc_before();
@@ -235,11 +248,20 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
         auto sync = [&] {
             if (y == 0) named_sync<3, GROUP>(); else named_sync<4, GROUP>();
         };
-        auto find = [&](int i) { return i < jobs ? max(pool_row(p, q, g, min(r0 + i % steps * TN + t, q.n_rows - 1)), 0) : 0; };
+        Lookup next; // of the step whose rows the group gets next
+        int rs = y % max(steps, 1); // that step's place in the range
+        auto look_up = [&](int i) {
+            next.ask(p, q, r0 + rs * TN + t, i < jobs);
+            rs += 2;
+            while (rs >= steps && steps > 0) rs -= steps;
+        };
+        auto resolve = [&] { return max(next.row(p, g), 0); };
         if (y < jobs) {
-            row[0][t] = find(y);
-            row[1][t] = find(y + 2);
-            int32_t next = find(y + 4);
+            look_up(y);
+            row[0][t] = resolve();
+            look_up(y + 2);
+            row[1][t] = resolve();
+            look_up(y + 4);
             sync();
             int k = 0; // steps of this group done
             if constexpr (!CODES) {
@@ -247,8 +269,8 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
                     if (k > 0) bar_wait(&x.bar[KE0 + y], (k - 1) & 1, p.err, &x.abort);
                     copy_halves<D>(tile, p.kdata, row[k & 1], t);
                     sync();
-                    row[k & 1][t] = next; // of this group's step after next
-                    next = find(i + 6);
+                    row[k & 1][t] = resolve(); // of this group's step after next
+                    look_up(i + 6);
                     asm volatile("cp.async.wait_group 0;" ::: "memory");
                     fence_async();
                     bar_arrive(&x.bar[KF0 + y]);
@@ -258,13 +280,16 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
                 using C = Codes<D, KT>;
                 const int c = t % C::PIECES, j0 = t / C::PIECES;
                 const uint8_t *codes = p.kdata + c * 16;
-                const uint32_t a[2] = {at(j0, c * 16), at(j0, c * 16 + 8)};
+                uint32_t a[4];
+                const bool f = C::swap(c);
+                C::places(j0, c, a, f);
                 uint4 u[C::PIECES];
                 uint32_t sc[D / 64];
                 int E = 0x7fffffff;
-                auto exponent = [&](int n, int i) { // of this group's n-th step (job i), whose scales are sc
+                int ps = y % steps; // the step's place in the range
+                auto exponent = [&](int n, int s) { // of this group's n-th step (place s), whose scales are sc
                     uint32_t m = 0;
-                    const bool in = r0 + i % steps * TN + t < q.n_rows;
+                    const bool in = r0 + s * TN + t < q.n_rows;
 #pragma unroll
                     for (int b = 0; b < D / QK; ++b) {
                         uint32_t v = sc[b >> 1] >> (16 * (b & 1)) & 0xffffu;
@@ -284,23 +309,33 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
                 C::load(sc, p.ks, row[0][t]);
 #pragma unroll
                 for (int b = 0; b < C::PIECES; ++b) C::load(u[b], codes, row[0][j0 + b * C::ROWS]);
-                exponent(0, y);
+                exponent(0, ps);
                 C::load(sc, p.ks, row[1][t]);
                 for (int i = y; i < jobs; i += 2, ++k) {
                     if (k > 0) bar_wait(&x.bar[KE0 + y], (k - 1) & 1, p.err, &x.abort);
                     const float up = ldexpf(1.f, 3 - E);
+                    // (scales and rows first: a shared load would wait for the stores before it)
                     const uint16_t *d = &x.scale[y][k & 1][j0 * (D / QK) + c / 2];
+                    __half2 ds[C::PIECES];
+                    int32_t R[C::PIECES];
 #pragma unroll
                     for (int b = 0; b < C::PIECES; ++b) {
-                        store_parts<D>(tile + b * C::ROWS * 128, tile + L::KT + b * C::ROWS * 128, a, u[b], d[b * C::ROWS * (D / QK)], up);
-                        if (i + 2 < jobs) C::load(u[b], codes, row[(k + 1) & 1][j0 + b * C::ROWS]);
+                        ds[b] = scaled(d[b * C::ROWS * (D / QK)], up);
+                        R[b] = row[(k + 1) & 1][j0 + b * C::ROWS];
+                    }
+#pragma unroll
+                    for (int b = 0; b < C::PIECES; ++b) {
+                        store_parts<D>(tile + b * C::ROWS * 128, tile + L::KT + b * C::ROWS * 128, a, u[b], ds[b], f);
+                        if (i + 2 < jobs) C::load(u[b], codes, R[b]);
                     }
                     fence_async();
                     bar_arrive(&x.bar[KF0 + y]);
                     if (i + 2 < jobs) {
-                        row[k & 1][t] = next;
-                        next = find(i + 6);
-                        exponent(k + 1, i + 2); // (its barrier: the rows are there too)
+                        row[k & 1][t] = resolve();
+                        look_up(i + 6);
+                        ps += 2;
+                        while (ps >= steps) ps -= steps;
+                        exponent(k + 1, ps); // (its barrier: the rows are there too)
                         C::load(sc, p.ks, row[k & 1][t]);
                     }
                 }

@@ -191,9 +191,17 @@ template <int D, int T> struct Codes {
         else
             asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(s[0]) : "l"(scales + (int64_t)R * 2));
     }
-    // values = codes * scale * 2^up, rounded once; dst: the piece's row, a[]: byte offsets of its 8-value pieces
-    __device__ __forceinline__ static void store(uint8_t *dst, const uint32_t *a, const uint4 &u, uint16_t s, float up) {
-        const __half2 d = __half2half2(__float2half_rn(__half2float(__ushort_as_half(s)) * up));
+    // The two halves of a thread's values may go to memory in an order of its own (f = swap), so that the eight threads
+    // of a quarter warp write to eight different 16-byte columns of the banks.
+    __device__ __forceinline__ static bool swap(int c) { return T == KVC_Q4_0 ? c >> 1 : ((c ^ (c >> 2)) & 1); }
+    // byte offsets of the 8-value pieces of codes c * CODES .. of row j, in that order
+    __device__ __forceinline__ static void places(int j, int c, uint32_t (&a)[4], int f) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            a[k] = T == KVC_Q4_0 ? at(j, c * 32 + (k ^ (2 * f)) * 8) : at(j, c * 16 + ((k ^ f) & 1) * 8);
+    }
+    // values = codes * d, rounded once (d: the scale times a power of two); dst: the piece's row
+    __device__ __forceinline__ static void store(uint8_t *dst, const uint32_t (&a)[4], const uint4 &u, __half2 d, bool f) {
         auto put = [&](uint32_t o, uint2 x, uint2 y) {
             uint4 v;
             *reinterpret_cast<__half2 *>(&v.x) = __hmul2(*reinterpret_cast<__half2 *>(&x.x), d);
@@ -203,16 +211,44 @@ template <int D, int T> struct Codes {
             *reinterpret_cast<uint4 *>(dst + o) = v;
         };
         if constexpr (T == KVC_Q8_0) {
-            put(a[0], codes4(u.x), codes4(u.y));
-            put(a[1], codes4(u.z), codes4(u.w));
+            put(a[0], codes4(f ? u.z : u.x), codes4(f ? u.w : u.y));
+            put(a[1], codes4(f ? u.x : u.z), codes4(f ? u.y : u.w));
         } else {
-            put(a[0], nibbles4(u.x), nibbles4(u.y));
-            put(a[1], nibbles4(u.z), nibbles4(u.w));
-            put(a[2], nibbles4(u.x >> 4), nibbles4(u.y >> 4));
-            put(a[3], nibbles4(u.z >> 4), nibbles4(u.w >> 4));
+            const int n = f ? 4 : 0;
+            put(a[0], nibbles4(u.x >> n), nibbles4(u.y >> n));
+            put(a[1], nibbles4(u.z >> n), nibbles4(u.w >> n));
+            put(a[2], nibbles4(u.x >> (4 - n)), nibbles4(u.y >> (4 - n)));
+            put(a[3], nibbles4(u.z >> (4 - n)), nibbles4(u.w >> (4 - n)));
         }
     }
 };
+
+// A row's way through the page table in two steps, so that nobody waits for the table: its entry is requested, and
+// looked at a step later.
+struct Lookup {
+    int32_t page = -1;
+    uint32_t cell = 0;
+    bool in = false;
+    __device__ __forceinline__ void ask(const BlockParams &p, const BlockSeq &q, int j, bool valid) {
+        in = valid && j < q.n_rows;
+        const uint32_t lr = (uint32_t)q.off + (uint32_t)j, pi = lr / (uint32_t)p.P;
+        cell = lr - pi * (uint32_t)p.P;
+        page = -1;
+        if (in && pi < (uint32_t)p.max_pages) page = p.pt[(int64_t)q.id * p.max_pages + pi];
+    }
+    // the pool row, -1 for none (a page that the pool does not have is reported)
+    __device__ __forceinline__ int32_t row(const BlockParams &p, int g) const {
+        if (in && (page < 0 || page >= p.n_pages)) {
+            atomicOr(p.err, ERR_BAD_PAGE);
+            return -1;
+        }
+        return in ? (page * p.Hk + g) * p.P + (int32_t)cell : -1;
+    }
+};
+
+__device__ __forceinline__ __half2 scaled(uint16_t s, float up) {
+    return __half2half2(__float2half_rn(__half2float(__ushort_as_half(s)) * up));
+}
 
 // f16 rows go straight to shared memory.
 template <int D> __device__ __forceinline__ void copy_halves(uint8_t *tile, const uint8_t *data, const int32_t *row, int t) {
