@@ -1303,7 +1303,7 @@ int kvc_seq_evict_weight(kvc_ctx *cc, int seq, int p0, int p1, int32_t n_remove,
     }
     e.pool_rows = c->pool_rows;
     e.err = c->err_dev;
-    if ((rc = upload_pages(c, seq))) return rc;
+    if (q.dev_pages != (int32_t)q.pages.size() && (rc = upload_pages(c, seq))) return rc;
     cudaError_t err = launch_evict(e, c->st);
     if (err != cudaSuccess) return cuda_fail(c, err, "eviction kernels");
     KVC_CU(c, cudaMemcpyAsync(c->gone_host, e.gone, (size_t)k * 4, cudaMemcpyDeviceToHost, c->st));

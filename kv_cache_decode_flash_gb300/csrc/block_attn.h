@@ -5,6 +5,8 @@
 
 #include "kvc_internal.h"
 
+#include <atomic>
+
 namespace kvc {
 
 // One sequence of a launch.  Its query rows are the pairs (token t, query head
@@ -57,6 +59,19 @@ constexpr int CROSS_TILE_M = 64;     // query rows of a tile
 constexpr int CROSS_TILE_N = 64;     // cached rows of a step
 constexpr int CROSS_TC_TILE_M = 256; // the same of the tcgen05 kernel
 constexpr int CROSS_TC_TILE_N = 128;
+
+// A kernel's dynamic shared memory, allowed once in every CUDA context (one
+// of these per kernel; threads may come at once: the worst is a second call).
+struct SharedMemory {
+    std::atomic<uint64_t> ctx{0};
+    cudaError_t allow(const void *kernel, int bytes) {
+        const uint64_t id = current_context_id();
+        if (id && ctx.load(std::memory_order_acquire) == id) return cudaSuccess;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) ctx.store(id, std::memory_order_release);
+        return e;
+    }
+};
 
 // The block attention.  narrow: every sequence's query rows of a KV head fit
 // 16 (one tensor-core row block), so the warps share the cached rows instead.

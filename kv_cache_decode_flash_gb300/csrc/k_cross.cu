@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
 template <int D, int KT, int VT, int WM, bool LO> cudaError_t go(const BlockParams &p, cudaStream_t st) {
     auto k = cross_kernel<D, KT, VT, WM, LO>;
     const int bytes = (int)sizeof(Smem<D>);
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static SharedMemory set;
+    cudaError_t e = set.allow((const void *)k, bytes);
     if (e != cudaSuccess) return e;
     k<<<(unsigned)p.n_items, THREADS, bytes, st>>>(p);
     e = cudaGetLastError();

@@ -604,7 +604,8 @@ template <int D, int KT, int VT> cudaError_t go(const BlockParams &p, cudaStream
     auto k = cross_tc_kernel<D, KT, VT>;
     constexpr int bytes = smem_bytes<D>();
     static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static SharedMemory set;
+    cudaError_t e = set.allow((const void *)k, bytes);
     if (e != cudaSuccess) return e;
     k<<<(unsigned)p.n_items, THREADS, bytes, st>>>(p);
     e = cudaGetLastError();

@@ -378,7 +378,8 @@ template <int D, int KT, bool LO> cudaError_t go(const BlockParams &p, cudaStrea
     auto k = weight_kernel<D, KT, LO>;
     constexpr int bytes = smem_bytes<D, KT != KVC_F16, LO>();
     static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static SharedMemory set;
+    cudaError_t e = set.allow((const void *)k, bytes);
     if (e != cudaSuccess) return e;
     k<<<(unsigned)p.n_items, THREADS, bytes, st>>>(p);
     return cudaGetLastError();

@@ -200,19 +200,36 @@ def kvc_decode_step(ctx, layer, seq_ids, pos, k, v, q, out, kq_scale, stream=Non
                                        float(kq_scale), _stream(stream, device)))
 
 
+_torch = None  # torch, and kvc_act by its dtypes: filled by the first block call
+_ACTS = {}
+
+
+def _load_torch():
+    global _torch
+    if _torch is None:
+        import torch
+
+        _ACTS.update({torch.float32: KVC_ACT_F32, torch.float16: KVC_ACT_F16, torch.bfloat16: KVC_ACT_BF16})
+        _torch = torch
+
+
 def _act(q):
     """kvc_act of a query tensor."""
-    act = {"torch.float32": KVC_ACT_F32, "torch.float16": KVC_ACT_F16, "torch.bfloat16": KVC_ACT_BF16}.get(str(q.dtype))
+    if _torch is None:
+        _load_torch()
+    act = _ACTS.get(getattr(q, "dtype", None))
     if act is None:
-        raise KvcError(KVC_EINVAL, "queries must be float32, float16 or bfloat16, not %s" % q.dtype)
+        raise KvcError(KVC_EINVAL, "queries must be float32, float16 or bfloat16 tensors")
     return act
 
 
 def _block_tensor(name, t, device, dtype, numel):
     """Refuse a tensor that the library would misread (it sees an address only)."""
-    if not (hasattr(t, "is_cuda") and t.is_cuda and t.device.index == device):
+    if _torch is None:
+        _load_torch()
+    if not isinstance(t, _torch.Tensor) or t.get_device() != device:
         raise KvcError(KVC_EINVAL, "%s must be a tensor on cuda:%d" % (name, device))
-    if str(t.dtype) != dtype:
+    if t.dtype is not dtype:
         raise KvcError(KVC_EINVAL, "%s must be %s, not %s" % (name, dtype, t.dtype))
     if not t.is_contiguous():
         raise KvcError(KVC_EINVAL, "%s must be contiguous" % name)
@@ -223,8 +240,8 @@ def _block_tensor(name, t, device, dtype, numel):
 def _block(seq_ids, n_q):
     if len(seq_ids) != len(n_q):
         raise KvcError(KVC_EINVAL, "one token count per sequence")
-    n = len(seq_ids)
-    return (C.c_int32 * n)(*[int(s) for s in seq_ids]), (C.c_int32 * n)(*[int(t) for t in n_q])
+    n = C.c_int32 * len(seq_ids)
+    return n(*map(int, seq_ids)), n(*map(int, n_q))
 
 
 def kvc_attn_cross(ctx, layer, seq_ids, n_q, act, q, out, kq_scale, lse=None, n_vis=None, stream=None, device=0):
@@ -492,38 +509,41 @@ class KVCache:
         """Attention of a block of tokens (n_q[i] of sequence seq_ids[i], packed) over the
         cached rows: q, out [T][n_head][head_dim] (float32, float16 or bfloat16), lse [T][n_head]
         fp32 or None, n_vis [T] int32 (leading rows that a token sees) or None (all)."""
-        act, total = _act(q), sum(int(t) for t in n_q)
+        act, total = _act(q), sum(map(int, n_q))
         self._block_io(q, out, lse, n_vis, total)
         kvc_attn_cross(self.ctx, layer, seq_ids, n_q, act, q, out, kq_scale, lse, n_vis, stream, self.device)
 
     def attn_weight(self, layer, seq_ids, n_q, q, lse, w, kq_scale, n_vis=None, stream=None):
         """Add the attention weight that the cached rows receive from a block of tokens to
         w [n_seq][n_head_kv][rows or more] fp32; lse as attn_cross wrote it for these tokens."""
-        act, total = _act(q), sum(int(t) for t in n_q)
+        act, total = _act(q), sum(map(int, n_q))
         self._block_io(q, None, lse, n_vis, total)
         if w.dim() != 3 or w.shape[0] != len(seq_ids) or w.shape[1] != self.params.n_head_kv:
             raise KvcError(KVC_EINVAL, "w must be [n_seq][n_head_kv][rows]")
-        _block_tensor("w", w, self.device, "torch.float32", 0)
+        _block_tensor("w", w, self.device, _torch.float32, 0)
         kvc_attn_weight(self.ctx, layer, seq_ids, n_q, act, q, lse, w, w.shape[2], kq_scale, n_vis, stream, self.device)
 
     def evict_weight(self, seq, p0, p1, n_remove, w):
         """Evict the n_remove rows of least accumulated weight with positions in [p0, p1);
         w [n_head_kv][rows or more] fp32 follows the rows.  Returns the rows removed."""
+        _load_torch()
         if w.dim() != 2 or w.shape[0] != self.params.n_head_kv:
             raise KvcError(KVC_EINVAL, "w must be [n_head_kv][rows]")
-        _block_tensor("w", w, self.device, "torch.float32", 0)
+        _block_tensor("w", w, self.device, _torch.float32, 0)
         return kvc_seq_evict_weight(self.ctx, seq, p0, p1, n_remove, w, w.shape[1])
 
     def _block_io(self, q, out, lse, n_vis, total):
         p = self.params
+        if total < 0:
+            raise KvcError(KVC_EINVAL, "n_q must not be negative")
         size = total * p.n_head * p.head_dim
-        _block_tensor("q", q, self.device, str(q.dtype), size)
+        _block_tensor("q", q, self.device, q.dtype, size)
         if out is not None:
-            _block_tensor("out", out, self.device, str(q.dtype), size)
+            _block_tensor("out", out, self.device, q.dtype, size)
         if lse is not None:
-            _block_tensor("lse", lse, self.device, "torch.float32", total * p.n_head)
+            _block_tensor("lse", lse, self.device, _torch.float32, total * p.n_head)
         if n_vis is not None:
-            _block_tensor("n_vis", n_vis, self.device, "torch.int32", total)
+            _block_tensor("n_vis", n_vis, self.device, _torch.int32, total)
 
     def seq_rm(self, seq, p0, p1):
         kvc_seq_rm(self.ctx, seq, p0, p1)

@@ -56,6 +56,6 @@ def test_binding_refuses_tensors_it_would_misread():
     with pytest.raises(kvc.KvcError):
         kvc._act(torch.zeros(1, dtype=torch.float64))
     with pytest.raises(kvc.KvcError):
-        kvc._block_tensor("q", torch.zeros(4), 0, "torch.float32", 4)  # not on the device
+        kvc._block_tensor("q", torch.zeros(4), 0, torch.float32, 4)  # not on the device
     with pytest.raises(kvc.KvcError):
         kvc._block([0, 1], [1])
