@@ -174,6 +174,7 @@ static void block_params(const Ctx *c, int layer, float kq_scale, int act, Block
     p.Hk = c->Hk;
     p.D = c->D;
     p.r = c->r;
+    p.r_magic = c->r > 1 ? (uint32_t)((((uint64_t)1 << 32) + c->r - 1) / c->r) : 0;
     p.P = c->P;
     p.n_pages = c->n_pages;
     p.max_pages = c->max_pages;

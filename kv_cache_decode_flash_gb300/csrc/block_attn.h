@@ -33,6 +33,7 @@ struct BlockParams {
     int32_t n_pages, max_pages; // pages of a layer, entries of a page-table row
     int32_t n_seq, n_items;
     int32_t n_cut;        // units that are cut into parts
+    uint32_t r_magic;     // ceil(2^32 / r), r > 1: m / r is the product's upper half
     int32_t act;          // kvc_act of q and out
     int32_t part_rows;    // partial rows of an item at most (min(tile_m, longest block * r))
     int32_t tile_m;

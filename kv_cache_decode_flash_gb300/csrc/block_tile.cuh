@@ -154,6 +154,11 @@ __device__ __forceinline__ void item_unit(const BlockSeq &q, int local, int &uni
     parts = whole ? 1 : q.splits;
 }
 
+// m / r (r <= 8, m < 2^29).
+__device__ __forceinline__ int token_of(const BlockParams &p, int m) {
+    return p.r == 1 ? m : (int)__umulhi((uint32_t)m, p.r_magic);
+}
+
 // Lane l's values l * D / 32 .. of query row m (of m_all rows; the others are zero) of KV head g, one warp a row; returns
 // the rows that it sees (0 for no row).
 template <int D>
@@ -161,7 +166,7 @@ __device__ __forceinline__ int query_load(const BlockParams &p, const BlockSeq &
                                           float (&x)[D / 32]) {
     constexpr int V = D / 32;
     if (m < m_all) {
-        const int t = m / p.r, j = m % p.r;
+        const int t = token_of(p, m), j = m - t * p.r;
         const int64_t tok = (int64_t)q.tok0 + t;
         const int64_t at = (tok * p.H + (int64_t)g * p.r + j) * D + lane * V;
         if (p.act == KVC_ACT_F32) {
@@ -197,15 +202,13 @@ template <int D, bool LO>
 __device__ __forceinline__ float query_pack(const BlockParams &p, const float (&x)[D / 32], uint32_t (&hi)[D / 64],
                                             uint32_t (&lo)[D / 64]) {
     constexpr int V = D / 32;
-    float top = 0.f;
+    uint32_t top = 0; // magnitudes as bits are ordered like the numbers
 #pragma unroll
-    for (int i = 0; i < V; ++i) top = fmaxf(top, fabsf(x[i]));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // top = f * 2^e, f in [1/2, 1): scaled by 2^(14 - e)
-    int e = 0;
-    if (top > 0.f && top < __int_as_float(0x7f800000)) frexpf(top, &e);
-    const float up = ldexpf(1.f, min(14 - e, 127)); // (rows below 2^-113: their scores are as good as 0)
+    for (int i = 0; i < V; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    top = __reduce_max_sync(0xffffffffu, top);
+    // times 2^(140 - exponent): to [2^13, 2^14).  (Rows below 2^-114 become zero scores; one with infinities keeps them.)
+    const uint32_t e = min(max(267 - (int)(top >> 23), 1), 254);
+    const float up = __uint_as_float(e << 23), down = __uint_as_float((254 - e) << 23);
 #pragma unroll
     for (int i = 0; i < V; i += 2) {
         const float a = x[i] * up, b = x[i + 1] * up;
@@ -216,7 +219,7 @@ __device__ __forceinline__ float query_pack(const BlockParams &p, const float (&
             lo[i / 2] = h2(isinf(f.x) ? 0.f : a - f.x, isinf(f.y) ? 0.f : b - f.y);
         }
     }
-    return p.scale_log2 / up;
+    return p.scale_log2 * down;
 }
 
 // A V value as stored (the rare path of values that are not finite).

@@ -85,23 +85,30 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
         s.bad = 0;
     }
     __syncthreads();
-    for (int m = warp; m < MROWS; m += THREADS / 32) {
-        float x[D / 32];
-        uint32_t hi[D / 64], lo[D / 64];
-        const int vis = query_load<D>(p, q, g, m0 + m, m_all, lane, x);
-        const float scale = query_pack<D, LO>(p, x, hi, lo);
+    constexpr int QR = WM == 4 ? 8 : 4; // of a warp's rows, under way together
+    for (int mb = warp; mb < MROWS; mb += THREADS / 32 * QR) {
+        float x[QR][D / 32];
+        int vis[QR];
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-            *reinterpret_cast<uint32_t *>(&s.qhi[m][lane * (D / 32) + 2 * i]) = hi[i];
-            if (LO) *reinterpret_cast<uint32_t *>(&s.qlo[m][lane * (D / 32) + 2 * i]) = lo[i];
+        for (int k = 0; k < QR; ++k) vis[k] = query_load<D>(p, q, g, m0 + mb + k * (THREADS / 32), m_all, lane, x[k]);
+#pragma unroll
+        for (int k = 0; k < QR; ++k) {
+            const int m = mb + k * (THREADS / 32);
+            uint32_t hi[D / 64], lo[D / 64];
+            const float scale = query_pack<D, LO>(p, x[k], hi, lo);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                *reinterpret_cast<uint32_t *>(&s.qhi[m][lane * (D / 32) + 2 * i]) = hi[i];
+                if (LO) *reinterpret_cast<uint32_t *>(&s.qlo[m][lane * (D / 32) + 2 * i]) = lo[i];
+            }
+            if (lane == 0) {
+                s.qscale[m] = scale;
+                s.vis[m] = vis[k];
+                if (vis[k] > 0) atomicMax(&s.vis_max, vis[k]);
+            }
         }
-        if (lane == 0) {
-            s.qscale[m] = scale;
-            s.vis[m] = vis;
-            if (vis > 0) atomicMax(&s.vis_max, vis);
-        }
-        for (int i = lane; i < D / 16; i += 32) s.poison[m][i] = 0;
     }
+    for (int i = tid; i < MROWS * (D / 16); i += THREADS) s.poison[i / (D / 16)][i % (D / 16)] = 0;
     __syncthreads();
     const int r0 = part * q.split_rows;
     const int r1 = parts == 1 ? s.vis_max : min(r0 + q.split_rows, s.vis_max);
@@ -358,7 +365,7 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
                     }
             }
             if (whole) {
-                const int t = (m0 + m) / p.r, j = (m0 + m) % p.r;
+                const int t = token_of(p, m0 + m), j = m0 + m - t * p.r;
                 const int64_t head = ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
                 const float inv = sum[h] == 0.f ? 0.f : 1.f / sum[h];
 #pragma unroll

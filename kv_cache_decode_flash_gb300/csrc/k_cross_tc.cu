@@ -75,11 +75,12 @@ template <int D> constexpr int smem_bytes() {
 // ------------------------------------------------------------- loading ----
 // A loading group's work: tensor T's rows of every step (IS_V: V, else K) into its two stages.
 template <int D, int T, bool IS_V>
-__device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &q, int g, uint8_t *tiles, Aux &x, int r0, int steps,
-                                          int vis_min, int t) {
+__device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &q, int g, uint8_t *tiles, Aux &x, int r0, int r_end,
+                                          int t) {
     const uint8_t *data = IS_V ? p.vdata : p.kdata;
     uint64_t *full = &x.bar[IS_V ? VF0 : KF0], *empty = &x.bar[IS_V ? VE0 : KE0];
     int32_t(*row)[TN] = x.row[IS_V];
+    int steps = 1 << 24, vis_min = 0; // known with the query rows
     constexpr int SYNC = IS_V ? 4 : 3;
     Lookup next; // of the step whose rows the group gets next
     auto look_up = [&](int s) { next.ask(p, q, r0 + s * TN + t, s < steps); };
@@ -90,9 +91,15 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
     auto clear = [&](int s) { // a step's reports; those of four steps before are read no more
         if (IS_V && t < TN / 32) x.badrow[s % SLOTS][t] = 0;
     };
-    if (steps == 0) return;
+    auto begin = [&] { // the query rows are there: how far the tokens see
+        __syncthreads();
+        tc_after();
+        const int r1 = min(r_end, x.vis_max);
+        steps = r1 > r0 ? (r1 - r0 + TN - 1) / TN : 0;
+        vis_min = x.vis_min;
+    };
 #pragma unroll
-    for (int k = 0; k < 3; ++k) row[k][t] = k < steps ? pool_row(p, q, g, r0 + k * TN + t) : -1;
+    for (int k = 0; k < 3; ++k) row[k][t] = pool_row(p, q, g, r0 + k * TN + t);
     look_up(3);
     clear(0);
     clear(1);
@@ -100,11 +107,14 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
     if constexpr (T == KVC_F16) {
         // A step's copies are under way while those of the step before are waited for, if their stage is free by then;
         // a step that has landed is not held back for a stage.
-        for (int s = 0; s <= steps; ++s) {
+        copy_halves<D>(tiles, data, row[0], t);
+        begin();
+        if (steps == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        for (int s = 0; s <= steps && steps > 0; ++s) {
             bool ahead = false;
             if (s < steps) {
                 ahead = s < 2 || bar_try(&empty[s & 1], ((s >> 1) - 1) & 1);
-                if (ahead) copy_halves<D>(tiles + (s & 1) * Lay<D>::TILE, data, row[s % SLOTS], t);
+                if (ahead && s > 0) copy_halves<D>(tiles + (s & 1) * Lay<D>::TILE, data, row[s % SLOTS], t);
                 if (!IS_V && t == 0) x.kfac[s % SLOTS] = 1.f;
             }
             if (s > 0) {
@@ -176,6 +186,8 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
         C::load(sc, scales, at_row(0, t));
 #pragma unroll
         for (int i = 0; i < C::PIECES; ++i) C::load(u[i], codes, at_row(0, j0 + i * C::ROWS));
+        begin();
+        if (steps == 0) return;
         exponent(0);
         C::load(sc, scales, at_row(1, t));
         for (int s = 0; s < steps; ++s) {
@@ -324,18 +336,29 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     __syncthreads();
-    // query rows (a warp each, four under way together), normalised by a power of two that takes the scale's sign too
-    constexpr int QR = 4;
-    constexpr int STRIDE = THREADS / 32; // (the rows that there are spread over the warps)
-    for (int mb = warp; mb < (wide ? 2 * TM : TM); mb += STRIDE * QR) {
+    const int r0 = part * q.split_rows, r_end = parts == 1 ? q.n_rows : min(r0 + q.split_rows, q.n_rows);
+    if (warp >= 8 && warp < 12) {
+        regs_dec<Regs<KT != KVC_F16>::LOAD>();
+        load_rows<D, KT, false>(p, q, g, smem + L::K, x, r0, r_end, tid - 2 * GROUP);
+        return;
+    } else if (warp >= 12 && warp < 16) {
+        regs_dec<Regs<KT != KVC_F16>::LOAD>();
+        load_rows<D, VT, true>(p, q, g, smem + L::V, x, r0, r_end, tid - 3 * GROUP);
+        return;
+    }
+    // The other warps see to the query rows: a warp each, QR of its rows under way together, normalised by a power of two
+    // that takes the scale's sign too; rows that are not there are zero.
+    constexpr int QR = 6, QW = 12; // (the loading warps are at their first rows already)
+    const int qw = warp < 8 ? warp : warp - 8;
+    for (int mb = qw; mb < mrows; mb += QW * QR) {
         float y[QR][D / 32];
         int vis[QR];
 #pragma unroll
-        for (int k = 0; k < QR; ++k) vis[k] = query_load<D>(p, q, g, mb + k * STRIDE < mrows ? m0 + mb + k * STRIDE : m_all, m_all, lane, y[k]);
+        for (int k = 0; k < QR; ++k) vis[k] = query_load<D>(p, q, g, mb + k * QW < mrows ? m0 + mb + k * QW : m_all, m_all, lane, y[k]);
 #pragma unroll
         for (int k = 0; k < QR; ++k) {
-            const int m = mb + k * STRIDE;
-            if (m >= (wide ? 2 * TM : TM)) break;
+            const int m = mb + k * QW;
+            if (m >= mrows) break;
             uint32_t h[D / 64], l[D / 64];
             float scale = query_pack<D, false>(p, y[k], h, l);
             if (scale < 0.f) {
@@ -351,13 +374,20 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
             if (lane == 0) {
                 x.qscale[m] = scale;
                 x.vis[m] = vis[k];
-                if (m < mrows) {
-                    atomicMax(&x.vis_max, vis[k]);
-                    atomicMin(&x.vis_min, vis[k]);
-                }
+                atomicMax(&x.vis_max, vis[k]);
+                atomicMin(&x.vis_min, vis[k]);
             }
-            if (lane < D / 16) poison[m][lane] = 0;
         }
+    }
+    {
+        const int ft = qw * 32 + lane, all = wide ? 2 * TM : TM;
+        for (int i = ft; i < (all - mrows) * (D / 8); i += QW * 32) {
+            const int m = mrows + i / (D / 8), c = i % (D / 8); // 16 bytes of the row, whichever the swizzle makes of them
+            *reinterpret_cast<uint4 *>(smem + L::Q + (m >> 7) * L::TILE + (c >> 3) * L::REG + (m & 127) * 128 + (c & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+            if (c == 0) x.qscale[m] = 0.f;
+        }
+        for (int i = ft; i < all * (D / 16); i += QW * 32) poison[i / (D / 16)][i % (D / 16)] = 0;
     }
     fence_async();
     tc_before();
@@ -365,8 +395,7 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
     tc_after();
     const uint32_t tm = x.tmem;
     const uint32_t tS = tm, tO = tm + 256; // S0, S1: 128 columns each (P over them); O0, O1: D columns each
-    const int r0 = part * q.split_rows;
-    const int r1 = parts == 1 ? x.vis_max : min(r0 + q.split_rows, x.vis_max);
+    const int r1 = min(r_end, x.vis_max);
     const int steps = r1 > r0 ? (r1 - r0 + TN - 1) / TN : 0;
     const int jobs = wide ? 2 * steps : steps;
     const int vis_min = x.vis_min;
@@ -490,7 +519,7 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
                 two = true;
             }
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-            const int m = m0 + mr, t = m / p.r, j = m - t * p.r;
+            const int m = m0 + mr, t = token_of(p, m), j = m - t * p.r;
             const int64_t head = ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
             const bool bad = x.any_bad != 0;
 #pragma unroll
@@ -553,12 +582,6 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
             tc_after();
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(TMEM_COLS));
         }
-    } else if (warp < 12) {
-        regs_dec<Regs<KT != KVC_F16>::LOAD>();
-        load_rows<D, KT, false>(p, q, g, smem + L::K, x, r0, steps, vis_min, tid - 2 * GROUP);
-    } else if (warp < 16) {
-        regs_dec<Regs<KT != KVC_F16>::LOAD>();
-        load_rows<D, VT, true>(p, q, g, smem + L::V, x, r0, steps, vis_min, tid - 3 * GROUP);
     } else {
         regs_dec<R_MMA>();
         if (warp > 16 || lane > 0) return;

@@ -61,7 +61,7 @@ template <int D> __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(con
             for (int e = 0; e < V; ++e) o[e] = fmaf(v[i][e], f, o[e]);
         }
     }
-    const int t = (m0 + m) / p.r, j = (m0 + m) % p.r;
+    const int t = token_of(p, m0 + m), j = m0 + m - t * p.r;
     const int64_t head = ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
     const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
                     vis[k] = query_load<D>(p, q, g, m < rows ? mg * MG + m : m_all, m_all, lane, y[k]);
                     z[k] = INFINITY; // a row that is not there, or sees nothing: weight 0
                     if (m < rows && vis[k] > 0) {
-                        const int tok = (mg * MG + m) / p.r, j = (mg * MG + m) % p.r;
+                        const int tok = token_of(p, mg * MG + m), j = mg * MG + m - tok * p.r;
                         z[k] = p.lse[((int64_t)q.tok0 + tok) * p.H + (int64_t)g * p.r + j] * 1.44269504f;
                     }
                 }
