@@ -137,12 +137,18 @@ static bool plan_block(BlockParams &p, int sms, bool tc) {
     return narrow;
 }
 
-// Which kernel attends a sequence: the tcgen05 one for 16-bit queries, where its rounding of K to 11 bits leaves the
-// log-sum-exp (an average over the rows) exact to 32 bits' needs: halves always, codes from TC_MIN_ROWS rows on.
+// Which kernel attends a sequence of 16-bit queries.  The tcgen05 kernel rounds code * scale to 11 bits: from TC_MIN_ROWS
+// rows on the log-sum-exp, an average over them, is as exact as 32 bits need (halves lose nothing).  It pays where a
+// call has enough to do, by its cached values (rows x KV heads x D) or its products (times query rows of a KV head):
+// measured in us, mma.sync against tcgen05, q8_0, bf16 queries, heads/KV heads/D:
+//   8/2/64,  1024 rows:   1 token   9.2 / 10.6,  256 tokens 14.0 / 18.0    (2^17 values, 2^27 products)
+//   8/2/64,  16384 rows:  1 token  20.6 / 17.5                             (2^21 values)
+//   40/8/128, 256 rows:  64 tokens 15.8 / 17.4,  256 tokens 24.0 / 18.2    (2^18 values; 2^26, 2^28 products)
+//   40/8/128, 4096 rows:  1 token  17.9 / 16.5,  256 tokens 203 / 46       (2^22 values)
 constexpr int TC_MIN_ROWS = 256;
-static bool use_tc(int type_k, int act, int rows) {
-    return act != KVC_ACT_F32 && (type_k == KVC_F16 || rows >= TC_MIN_ROWS);
-}
+constexpr double TC_VALUES = 1 << 21, TC_PRODUCTS = 1 << 28;
+static bool tc_pays(double values, double products) { return values >= TC_VALUES || products >= TC_PRODUCTS; }
+static bool use_tc(int type_k, int rows) { return type_k == KVC_F16 || rows >= TC_MIN_ROWS; }
 
 // Checks that the block operators share; *total: tokens of the block.
 static int block_check(Ctx *c, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_q, int act, const void *q,
@@ -216,6 +222,14 @@ extern "C" int kvc_attn_cross(kvc_ctx *cc, int layer, int n_seq, const int32_t *
     KVC_CU(c, cudaSetDevice(c->dev));
     if ((rc = ensure_block_space(c, st))) return rc;
     const int64_t cap = part_rows_cap(c->sms);
+    double values = 0, products = 0;
+    for (int i = 0; i < n_seq; ++i) {
+        if (n_q[i] == 0) continue;
+        const double v = (double)c->seqs[(size_t)seq_ids[i]].lfill[(size_t)layer] * c->Hk * c->D;
+        values += v;
+        products += v * c->r * n_q[i];
+    }
+    const bool pays = act != KVC_ACT_F32 && (c->block_kernel ? c->block_kernel == 2 : tc_pays(values, products));
     for (int tc = 0; tc < 2; ++tc) { // the sequences of either kernel, as many a launch as it carries
         BlockParams p;
         block_params(c, layer, kq_scale, act, p);
@@ -229,7 +243,7 @@ extern "C" int kvc_attn_cross(kvc_ctx *cc, int layer, int n_seq, const int32_t *
         for (int i = 0; i < n_seq; ++i) {
             const Seq &sq = c->seqs[(size_t)seq_ids[i]];
             const int32_t rows = sq.lfill[(size_t)layer];
-            if (n_q[i] > 0 && use_tc(c->tk, act, rows) == (tc != 0)) {
+            if (n_q[i] > 0 && (pays && (c->block_kernel || use_tc(c->tk, rows))) == (tc != 0)) {
                 BlockSeq &s = p.seq[p.n_seq++];
                 s.id = seq_ids[i];
                 s.off = sq.off;
@@ -292,6 +306,14 @@ extern "C" int kvc_attn_weight(kvc_ctx *cc, int layer, int n_seq, const int32_t 
         cudaError_t e = launch_weight(c->tk, p, st);
         if (e != cudaSuccess) return cuda_fail(c, e, "row weight kernel");
     }
+    return KVC_OK;
+}
+
+extern "C" int kvc_debug_block_kernel(kvc_ctx *cc, int which) {
+    if (!cc) return KVC_EINVAL;
+    Ctx *c = reinterpret_cast<Ctx *>(cc);
+    if (which < 0 || which > 2) return c->fail(KVC_EINVAL, "which must be 0, 1 or 2");
+    c->block_kernel = which;
     return KVC_OK;
 }
 

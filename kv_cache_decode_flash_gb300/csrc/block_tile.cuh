@@ -159,42 +159,57 @@ __device__ __forceinline__ int token_of(const BlockParams &p, int m) {
     return p.r == 1 ? m : (int)__umulhi((uint32_t)m, p.r_magic);
 }
 
-// Lane l's values l * D / 32 .. of query row m (of m_all rows; the others are zero) of KV head g, one warp a row; returns
-// the rows that it sees (0 for no row).
-template <int D>
-__device__ __forceinline__ int query_load(const BlockParams &p, const BlockSeq &q, int g, int m, int m_all, int lane,
-                                          float (&x)[D / 32]) {
-    constexpr int V = D / 32;
-    if (m < m_all) {
+// Lane l's values l * D / 32 .. of query row m of KV head g, one warp a row.  ask() only requests them and the rows that
+// the token sees (of the last row, for a row that is not there), so that several rows can be under way; get() looks.
+template <int D> struct Query {
+    static constexpr int V = D / 32;
+    uint32_t raw[V];
+    int32_t see;
+    bool in;
+    __device__ __forceinline__ void ask(const BlockParams &p, const BlockSeq &q, int g, int m, int m_all, int lane) {
+        in = m < m_all;
+        m = min(m, m_all - 1);
         const int t = token_of(p, m), j = m - t * p.r;
         const int64_t tok = (int64_t)q.tok0 + t;
         const int64_t at = (tok * p.H + (int64_t)g * p.r + j) * D + lane * V;
         if (p.act == KVC_ACT_F32) {
-#pragma unroll
-            for (int i = 0; i < V; i += 2) {
-                const float2 f = *reinterpret_cast<const float2 *>(reinterpret_cast<const float *>(p.q) + at + i);
-                x[i] = f.x, x[i + 1] = f.y;
-            }
-        } else if (p.act == KVC_ACT_F16) {
-#pragma unroll
-            for (int i = 0; i < V; i += 2) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(reinterpret_cast<const __half *>(p.q) + at + i));
-                x[i] = f.x, x[i + 1] = f.y;
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q) + at;
+            if constexpr (V == 4) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(src);
+                raw[0] = u.x, raw[1] = u.y, raw[2] = u.z, raw[3] = u.w;
+            } else {
+                const uint2 u = *reinterpret_cast<const uint2 *>(src);
+                raw[0] = u.x, raw[1] = u.y;
             }
         } else {
-#pragma unroll
-            for (int i = 0; i < V; i += 2) {
-                const float2 f = __bfloat1622float2(
-                    *reinterpret_cast<const __nv_bfloat162 *>(reinterpret_cast<const __nv_bfloat16 *>(p.q) + at + i));
-                x[i] = f.x, x[i + 1] = f.y;
+            const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + at;
+            if constexpr (V == 4) {
+                const uint2 u = *reinterpret_cast<const uint2 *>(src);
+                raw[0] = u.x, raw[1] = u.y;
+            } else {
+                raw[0] = *reinterpret_cast<const uint32_t *>(src);
             }
         }
-        return p.n_vis ? min(max(p.n_vis[tok], 0), q.n_rows) : q.n_rows;
+        see = p.n_vis ? p.n_vis[tok] : q.n_rows;
     }
+    // the rows that it sees: 0 for a row that is not there, whose values are 0
+    __device__ __forceinline__ int get(const BlockParams &p, const BlockSeq &q, float (&x)[V]) const {
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = 0.f;
-    return 0;
-}
+        for (int i = 0; i < V; i += 2) {
+            float2 f;
+            if (p.act == KVC_ACT_F32) {
+                f = make_float2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1]));
+            } else if (p.act == KVC_ACT_F16) {
+                f = f2(raw[i / 2]);
+            } else {
+                f = make_float2(__uint_as_float(raw[i / 2] << 16), __uint_as_float(raw[i / 2] & 0xffff0000u));
+            }
+            x[i] = in ? f.x : 0.f;
+            x[i + 1] = in ? f.y : 0.f;
+        }
+        return in ? min(max(see, 0), q.n_rows) : 0;
+    }
+};
 
 // The warp normalises the row: a lane's values as pairs of halves hi (and lo, what hi leaves).  Returns the score per unit
 // of the normalised product, in log2 units.

@@ -132,6 +132,7 @@ struct Ctx {
     uint32_t *err_dev = nullptr;
     uint32_t *err_host = nullptr; // pinned copy of the error word read by synchronous operations
     int chunk_override = 0;
+    int block_kernel = 0; // forced kernel of the block attention (kvc_debug_block_kernel)
     int32_t *gone_host = nullptr; // pinned: the rows that an eviction by weight removed
     int64_t gone_cap = 0;
     float *block_part = nullptr; // work space of the block operators (block_attn.cu), allocated by their first call

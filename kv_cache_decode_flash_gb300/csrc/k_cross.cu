@@ -87,15 +87,16 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
     __syncthreads();
     constexpr int QR = WM == 4 ? 8 : 4; // of a warp's rows, under way together
     for (int mb = warp; mb < MROWS; mb += THREADS / 32 * QR) {
-        float x[QR][D / 32];
-        int vis[QR];
+        Query<D> y[QR];
 #pragma unroll
-        for (int k = 0; k < QR; ++k) vis[k] = query_load<D>(p, q, g, m0 + mb + k * (THREADS / 32), m_all, lane, x[k]);
+        for (int k = 0; k < QR; ++k) y[k].ask(p, q, g, m0 + mb + k * (THREADS / 32), m_all, lane);
 #pragma unroll
         for (int k = 0; k < QR; ++k) {
             const int m = mb + k * (THREADS / 32);
+            float x[D / 32];
             uint32_t hi[D / 64], lo[D / 64];
-            const float scale = query_pack<D, LO>(p, x[k], hi, lo);
+            const int vis = y[k].get(p, q, x);
+            const float scale = query_pack<D, LO>(p, x, hi, lo);
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
                 *reinterpret_cast<uint32_t *>(&s.qhi[m][lane * (D / 32) + 2 * i]) = hi[i];
@@ -103,8 +104,8 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
             }
             if (lane == 0) {
                 s.qscale[m] = scale;
-                s.vis[m] = vis[k];
-                if (vis[k] > 0) atomicMax(&s.vis_max, vis[k]);
+                s.vis[m] = vis;
+                if (vis > 0) atomicMax(&s.vis_max, vis);
             }
         }
     }

@@ -351,16 +351,18 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
     constexpr int QR = 6, QW = 12; // (the loading warps are at their first rows already)
     const int qw = warp < 8 ? warp : warp - 8;
     for (int mb = qw; mb < mrows; mb += QW * QR) {
-        float y[QR][D / 32];
-        int vis[QR];
+        Query<D> y[QR];
 #pragma unroll
-        for (int k = 0; k < QR; ++k) vis[k] = query_load<D>(p, q, g, mb + k * QW < mrows ? m0 + mb + k * QW : m_all, m_all, lane, y[k]);
+        for (int k = 0; k < QR; ++k)
+            if (mb + k * QW < mrows) y[k].ask(p, q, g, m0 + mb + k * QW, m_all, lane);
 #pragma unroll
         for (int k = 0; k < QR; ++k) {
             const int m = mb + k * QW;
             if (m >= mrows) break;
+            float v[D / 32];
             uint32_t h[D / 64], l[D / 64];
-            float scale = query_pack<D, false>(p, y[k], h, l);
+            const int vis = y[k].get(p, q, v);
+            float scale = query_pack<D, false>(p, v, h, l);
             if (scale < 0.f) {
                 scale = -scale;
 #pragma unroll
@@ -373,9 +375,9 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
                 *reinterpret_cast<uint32_t *>(dst) = h[0];
             if (lane == 0) {
                 x.qscale[m] = scale;
-                x.vis[m] = vis[k];
-                atomicMax(&x.vis_max, vis[k]);
-                atomicMin(&x.vis_min, vis[k]);
+                x.vis[m] = vis;
+                atomicMax(&x.vis_max, vis);
+                atomicMin(&x.vis_min, vis);
             }
         }
     }
@@ -519,8 +521,13 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
                 two = true;
             }
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-            const int m = m0 + mr, t = token_of(p, m), j = m - t * p.r;
-            const int64_t head = ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
+            auto head_of = [&](int row) {
+                const int m = m0 + row, t = token_of(p, m), j = m - t * p.r;
+                return ((int64_t)q.tok0 + t) * p.H + (int64_t)g * p.r + j;
+            };
+            constexpr int SP = 36; // floats of a staging row: 16 bytes off a multiple of 128
+            float *stage = join + (wide ? 0 : TM * JP) + (warp & (wide ? 7 : 3)) * (32 * SP);
+            static_assert((TM * JP + 4 * 32 * SP) * 4 <= 4 * L::TILE && 8 * 32 * SP * 4 <= 4 * L::TILE, "within the K and V tiles");
             const bool bad = x.any_bad != 0;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -550,27 +557,38 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] = poisoned(v[e], poison[mr][(c * 32 + e) / 16] >> (2 * (e % 16)) & 3u);
                     }
-                    if (whole) {
+                }
+                // through the warp's staging rows, so that memory is written a row's 32 columns at a time
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint4 o;
-                            o.x = pack16(p.act, v[e] * inv, v[e + 1] * inv);
-                            o.y = pack16(p.act, v[e + 2] * inv, v[e + 3] * inv);
-                            o.z = pack16(p.act, v[e + 4] * inv, v[e + 5] * inv);
-                            o.w = pack16(p.act, v[e + 6] * inv, v[e + 7] * inv);
-                            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) + head * D + c * 32 + e) = o;
-                        }
-                    } else {
-                        float *dst = p.part + (int64_t)(prow + mr) * D + c * 32;
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4 *>(&stage[lane * SP + e]) =
+                        make_float4(v[e] * inv, v[e + 1] * inv, v[e + 2] * inv, v[e + 3] * inv);
+                __syncwarp();
+                const int mw = mr - lane; // the warp's first row
+                if (whole) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    for (int k = 0; k < 4; ++k) {
+                        const int row = k * 8 + (lane >> 2), e = (lane & 3) * 8;
+                        const float4 a = *reinterpret_cast<const float4 *>(&stage[row * SP + e]);
+                        const float4 b = *reinterpret_cast<const float4 *>(&stage[row * SP + e + 4]);
+                        if (mw + row < mrows)
+                            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) + head_of(mw + row) * D + c * 32 + e) =
+                                make_uint4(pack16(p.act, a.x, a.y), pack16(p.act, a.z, a.w), pack16(p.act, b.x, b.y),
+                                           pack16(p.act, b.z, b.w));
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int row = k * 4 + (lane >> 3), e = (lane & 7) * 4;
+                        const float4 a = *reinterpret_cast<const float4 *>(&stage[row * SP + e]);
+                        if (mw + row < mrows)
+                            *reinterpret_cast<float4 *>(p.part + (int64_t)(prow + mw + row) * D + c * 32 + e) = a;
                     }
                 }
             }
             if (mr < mrows) {
                 if (whole) {
-                    if (p.lse) p.lse[head] = sum == 0.f ? -INFINITY : mx * 0.6931471805599453f + logf(sum);
+                    if (p.lse) p.lse[head_of(mr)] = sum == 0.f ? -INFINITY : mx * 0.6931471805599453f + logf(sum);
                 } else {
                     *reinterpret_cast<float2 *>(p.part + p.part_cap * D + 2 * (int64_t)(prow + mr)) = make_float2(mx, sum);
                 }

@@ -175,27 +175,26 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
         for (int mg = 0; mg < groups && steps > 0; ++mg) {
             const int rows = min(MG, m_all - mg * MG), cols = (rows + 15) / 16 * 16;
             named_sync<2, 2 * GROUP>(); // every product with the rows before is done: both groups have its scores
-            constexpr int QR = 4;
+            constexpr int QR = 5;
             for (int mb = warp; mb < cols; mb += 8 * QR) {
-                float y[QR][D / 32];
-                int vis[QR];
+                Query<D> y[QR];
                 float z[QR];
 #pragma unroll
                 for (int k = 0; k < QR; ++k) {
-                    const int m = mb + k * 8;
-                    vis[k] = query_load<D>(p, q, g, m < rows ? mg * MG + m : m_all, m_all, lane, y[k]);
-                    z[k] = INFINITY; // a row that is not there, or sees nothing: weight 0
-                    if (m < rows && vis[k] > 0) {
-                        const int tok = token_of(p, mg * MG + m), j = mg * MG + m - tok * p.r;
-                        z[k] = p.lse[((int64_t)q.tok0 + tok) * p.H + (int64_t)g * p.r + j] * 1.44269504f;
-                    }
+                    if (mb + k * 8 >= cols) break;
+                    const int m = mg * MG + mb + k * 8;
+                    y[k].ask(p, q, g, m, m_all, lane);
+                    const int mm = min(m, m_all - 1), tok = token_of(p, mm), j = mm - tok * p.r;
+                    z[k] = p.lse[((int64_t)q.tok0 + tok) * p.H + (int64_t)g * p.r + j];
                 }
 #pragma unroll
                 for (int k = 0; k < QR; ++k) {
                     const int m = mb + k * 8;
                     if (m >= cols) break;
+                    float v[D / 32];
                     uint32_t hi[D / 64], lo[D / 64];
-                    const float scale = query_pack<D, LO>(p, y[k], hi, lo);
+                    const int vis = y[k].get(p, q, v); // (a row behind the group's last one is its own part's, or none)
+                    const float scale = query_pack<D, LO>(p, v, hi, lo);
                     uint8_t *dst = smem + at<MG>(m, lane * (D / 32));
                     if constexpr (D == 128) {
                         *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
@@ -205,8 +204,9 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
                         if (LO) *reinterpret_cast<uint32_t *>(dst + L::QT) = lo[0];
                     }
                     if (lane == 0) {
-                        x.fz0[m] = make_float2(m < rows ? scale : 0.f, z[k]);
-                        x.vis[m] = vis[k];
+                        // a row that is not there, or sees nothing: weight 0
+                        x.fz0[m] = make_float2(vis > 0 ? scale : 0.f, vis > 0 ? z[k] * 1.44269504f : INFINITY);
+                        x.vis[m] = vis;
                     }
                 }
             }

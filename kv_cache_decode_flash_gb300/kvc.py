@@ -100,6 +100,7 @@ def load():
         "kvc_debug_chunk_plan": (i32, [i32, i32, i32, i32, i32, i32, i32, i32, p, C.POINTER(C.c_int32),
                                        C.POINTER(C.c_int32)]),
         "kvc_debug_chunk_plan_seq": (i32, [i32, i32, i32, i32, i32, i32, i32, i32, p, p, C.POINTER(C.c_int32)]),
+        "kvc_debug_block_kernel": (i32, [p, i32]),
         "kvc_debug_block_plan": (i32, [i32] * 6 + [p] * 9),
         "kvc_debug_select_rows": (i32, [p, i32, i32, i32, i32, p, C.POINTER(C.c_int64), C.POINTER(C.c_int64),
                                         C.POINTER(C.c_int32)]),
@@ -425,6 +426,11 @@ def kvc_debug_chunk_plan_seq(type_, head_dim, n_head, n_head_kv, sms, occ, occ2,
     if st != KVC_OK:
         raise KvcError(st, "bad chunk-plan arguments")
     return list(out), cfg.value
+
+
+def kvc_debug_block_kernel(ctx, which):
+    """Force the block attention's kernel for 16-bit queries (1 mma.sync, 2 tcgen05, 0 by size)."""
+    _check(ctx, load().kvc_debug_block_kernel(ctx, int(which)))
 
 
 def kvc_debug_block_plan(n_head, n_head_kv, head_dim, act, sms, rows, n_q):

@@ -14,6 +14,26 @@ Q8, F16, Q4 = oracle.Q8_0, oracle.F16, oracle.Q4_0
 KINDS = {"q8": (Q8, Q8), "f16": (F16, F16), "q8q4": (Q8, Q4)}
 
 
+KERNEL = 0
+
+
+@pytest.fixture(autouse=True, params=[0, 1, 2], ids=["by_size", "mma", "tcgen05"])
+def kernel(request):
+    """Every test on the kernel that the sizes choose and on each of the two for 16-bit queries."""
+    global KERNEL
+    act = request.node.callspec.params.get("act") if hasattr(request.node, "callspec") else None
+    if request.param and act == "f32":
+        pytest.skip("32-bit queries have one kernel")
+    KERNEL = request.param
+    yield request.param
+    KERNEL = 0
+
+
+def _force(tw):
+    tw.kvc.kvc_debug_block_kernel(tw.gpu.ctx, KERNEL)
+    return tw
+
+
 def _types():
     import torch
 
@@ -64,7 +84,7 @@ def _compare(tw, ids, n_q, q, scale, vis, got, z, act, layer=0, bits=None, exact
 
 def _cache(kind, H, Hk, D, lens, page=64, seed=1, layers=1, exact=False, sigma=0.5):
     tk, tv = KINDS[kind]
-    tw = Twin(layers, H, Hk, D, sum(lens) + 64, n_seq_max=max(1, len(lens)), type_=tk, type_v=tv, page_rows=page)
+    tw = _force(Twin(layers, H, Hk, D, sum(lens) + 64, n_seq_max=max(1, len(lens)), type_=tk, type_v=tv, page_rows=page))
     rng = np.random.default_rng(seed)
     for i, n in enumerate(lens):
         for layer in range(layers):
@@ -186,7 +206,7 @@ def test_cross_one_token_is_the_decode_attention(act):
 def test_cross_values_of_any_size(kind, act):
     """Scales far apart between rows and tiles, queries of very small and very large magnitude."""
     n, T, D = 400, 20, 64
-    tw = Twin(1, 4, 2, D, n + 64, type_=KINDS[kind][0], page_rows=64)
+    tw = _force(Twin(1, 4, 2, D, n + 64, type_=KINDS[kind][0], page_rows=64))
     try:
         rng = np.random.default_rng(11)
         k = rng.standard_normal((n, 2, D)).astype(np.float32)
@@ -229,7 +249,7 @@ def test_cross_unseen_rows_never_reach_a_token(kind, act, T):
     vis = rng.integers(0, 600, T)
     vis[0] = 600
     for spoil in (False, True):
-        tw = Twin(1, H, Hk, D, n + 64, type_=KINDS[kind][0], page_rows=64)
+        tw = _force(Twin(1, H, Hk, D, n + 64, type_=KINDS[kind][0], page_rows=64))
         try:
             kk, vv = k.copy(), v.copy()
             if spoil:
@@ -260,7 +280,7 @@ def test_cross_infinite_value_of_a_seen_row(act, T):
     k, v = kv_inputs(17, 0, n, 2, D)
     v[100, 0, 3], v[101, 0, 4], v[102, 1, 5] = np.inf, -np.inf, np.nan
     v[400, 0, 3] = -np.inf
-    tw = Twin(1, 4, 2, D, n + 64, type_=F16, page_rows=64)
+    tw = _force(Twin(1, 4, 2, D, n + 64, type_=F16, page_rows=64))
     try:
         tw.gpu.append(0, 0, 0, torch.from_numpy(k).to(tw.dev), torch.from_numpy(v).to(tw.dev))
         q = _queries(np.random.default_rng(1), T, 4, D, act)
