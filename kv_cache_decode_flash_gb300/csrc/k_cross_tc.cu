@@ -82,10 +82,10 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
     int32_t(*row)[TN] = x.row[IS_V];
     int steps = 1 << 24, vis_min = 0; // known with the query rows
     constexpr int SYNC = IS_V ? 4 : 3;
-    Lookup next; // of the step whose rows the group gets next
-    auto look_up = [&](int s) { next.ask(p, q, r0 + s * TN + t, s < steps); };
+    int32_t next = -1; // the pool row of the step whose rows the group gets next, looked up a step before
+    auto look_up = [&](int s) { next = s < steps ? pool_row(p, q, g, r0 + s * TN + t) : -1; };
     auto find = [&](int s) { // for all threads after the next barrier
-        row[s % SLOTS][t] = next.row(p, g);
+        row[s % SLOTS][t] = next;
         look_up(s + 1);
     };
     auto clear = [&](int s) { // a step's reports; those of four steps before are read no more
@@ -198,7 +198,7 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
 #pragma unroll
             for (int i = 0; i < C::PIECES; ++i) {
                 C::store(tile + i * C::ROWS * 128, a, u[i], scaled(d[i * C::ROWS * (D / QK)], up), f);
-                if (s + 1 < steps) C::load(u[i], codes, at_row(s + 1, j0 + i * C::ROWS));
+                C::load(u[i], codes, at_row(s + 1, j0 + i * C::ROWS)); // (behind the last step: a row that is there)
             }
             fence_async();
             bar_arrive(&full[s & 1]);

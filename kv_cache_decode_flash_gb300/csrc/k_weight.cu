@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
 #pragma unroll
                     for (int b = 0; b < C::PIECES; ++b) {
                         store_parts<D>(tile + b * C::ROWS * 128, tile + L::KT + b * C::ROWS * 128, a, u[b], ds[b], f);
-                        if (i + 2 < jobs) C::load(u[b], codes, R[b]);
+                        C::load(u[b], codes, R[b]); // (behind the last step: a row that is there)
                     }
                     fence_async();
                     bar_arrive(&x.bar[KF0 + y]);
