@@ -4,17 +4,17 @@
 //   W_j = (w[0][j] + w[1][j]) + ... over the KV heads, in 32 bits and in that
 //   order; the n_remove candidates of smallest (W_j, j) go.
 //
-// evict_keys sums a candidate's weights into an unsigned key of the same order
-// (a NaN after everything else).  evict_select finds the n_remove-th smallest
+// A candidate's weights are summed into an unsigned key of the same order (a NaN
+// after everything else).  evict_select finds the n_remove-th smallest
 // key digit by digit (four passes of 8 bits over the keys, which stay in L2) and
 // lists the removed rows in ascending order: a warp owns a contiguous range of
 // candidates, counts its smaller and its equal keys, and after one scan over
 // the warps knows where its own go.  Then the sequence's last n_remove rows
 // [n', n) give the places: the kept ones among them move, in order, into the
 // removed places below n' (as many, by counting), so at most n_remove rows are
-// read and written in every layer, whatever the sequence's length.
-// evict_pairs finds each mover's place by a binary search in the list and moves
-// its weights; evict_move copies the K and V rows of all layers and heads.
+// read and written in every layer, whatever the sequence's length.  A mover's
+// place is found by a binary search in the list, and its weights move;
+// evict_move copies the K and V rows of all layers and heads.
 #include "evict.h"
 
 namespace kvc {
@@ -23,9 +23,8 @@ namespace {
 constexpr int SEL = 1024; // threads of the selecting CTA
 constexpr int WARPS = SEL / 32;
 
-__global__ void __launch_bounds__(256) evict_keys(const __grid_constant__ EvictArgs a) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= a.n_cand) return;
+// Candidate i's weight as an unsigned key of the same order.
+__device__ __forceinline__ void key_of(const EvictArgs &a, int64_t i) {
     const int64_t j = a.rows ? a.rows[i] : a.first + i;
     float s = a.w[j];
     for (int g = 1; g < a.Hk; ++g) s = __fadd_rn(s, a.w[g * a.w_stride + j]);
@@ -35,13 +34,60 @@ __global__ void __launch_bounds__(256) evict_keys(const __grid_constant__ EvictA
     if (s != s) u = 0xffffffffu;
     a.keys[i] = u;
 }
+__global__ void __launch_bounds__(256) evict_keys(const __grid_constant__ EvictArgs a) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < a.n_cand) key_of(a, i);
+}
 
-__global__ void __launch_bounds__(SEL) evict_select(const __grid_constant__ EvictArgs a) {
+__device__ __forceinline__ int64_t pool_row0(const EvictArgs &a, int32_t j) {
+    const int64_t lr = (int64_t)a.off + j, pi = lr / a.P;
+    const int32_t page = pi < a.pt_len ? a.pt[pi] : -1;
+    if (page < 0 || page >= a.n_pages) {
+        atomicOr(a.err, ERR_BAD_PAGE);
+        return -1;
+    }
+    return (int64_t)page * a.Hk * a.P + (lr - pi * a.P);
+}
+
+// Row x of the last n_remove ones: its place among the holes, if it stays, and its weights.
+__device__ __forceinline__ void pair_of(const EvictArgs &a, int x) {
+    const int32_t left = a.n - a.n_remove, j = left + x;
+    int lo = 0, hi = a.n_remove; // removed rows before j
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (a.gone[mid] < j) lo = mid + 1; else hi = mid;
+    }
+    int2 pr = make_int2(-1, -1);
+    if (lo >= a.n_remove || a.gone[lo] != j) {
+        // kept: of the x rows before it in the tail, those removed are the removed ones below j that are not holes;
+        // with h holes, lo - h of them, so it is mover x - (lo - h); holes are the first h of the list
+        int hl = 0, hh = a.n_remove;
+        while (hl < hh) {
+            const int mid = (hl + hh) / 2;
+            if (a.gone[mid] < left) hl = mid + 1; else hh = mid;
+        }
+        const int32_t hole = a.gone[x - (lo - hl)];
+        const int64_t to = pool_row0(a, hole), from = pool_row0(a, j);
+        if (to >= 0 && from >= 0) pr = make_int2((int)to, (int)from);
+        for (int g = 0; g < a.Hk; ++g) a.w[g * a.w_stride + hole] = a.w[g * a.w_stride + j];
+    }
+    for (int g = 0; g < a.Hk; ++g) a.w[g * a.w_stride + j] = 0.f;
+    a.pairs[x] = pr;
+}
+__global__ void __launch_bounds__(128) evict_pairs(const __grid_constant__ EvictArgs a) {
+    const int x = (int)blockIdx.x * 128 + threadIdx.x;
+    if (x < a.n_remove) pair_of(a, x);
+}
+
+// ALL: few candidates, whose keys and pairs the one CTA sees to as well.
+template <bool ALL> __global__ void __launch_bounds__(SEL) evict_select(const __grid_constant__ EvictArgs a) {
     __shared__ uint32_t hist[256];
     __shared__ uint32_t prefix, left;
     __shared__ int32_t below[WARPS], equal[WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = a.n_cand;
+    if (ALL)
+        for (int i = tid; i < n; i += SEL) key_of(a, i); // (seen by the CTA after the barriers below)
     if (tid == 0) {
         prefix = 0;
         left = (uint32_t)a.n_remove; // rank of the wanted key among those that share the prefix, from 1
@@ -133,44 +179,10 @@ __global__ void __launch_bounds__(SEL) evict_select(const __grid_constant__ Evic
         b0 += __popc(ml);
         e0 += __popc(me);
     }
-}
-
-__device__ __forceinline__ int64_t pool_row0(const EvictArgs &a, int32_t j) {
-    const int64_t lr = (int64_t)a.off + j, pi = lr / a.P;
-    const int32_t page = pi < a.pt_len ? a.pt[pi] : -1;
-    if (page < 0 || page >= a.n_pages) {
-        atomicOr(a.err, ERR_BAD_PAGE);
-        return -1;
+    if (ALL) {
+        __syncthreads();
+        for (int x = tid; x < a.n_remove; x += SEL) pair_of(a, x);
     }
-    return (int64_t)page * a.Hk * a.P + (lr - pi * a.P);
-}
-
-// A thread for each of the last n_remove rows.
-__global__ void __launch_bounds__(128) evict_pairs(const __grid_constant__ EvictArgs a) {
-    const int x = (int)blockIdx.x * 128 + threadIdx.x;
-    if (x >= a.n_remove) return;
-    const int32_t left = a.n - a.n_remove, j = left + x;
-    int lo = 0, hi = a.n_remove; // removed rows before j
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (a.gone[mid] < j) lo = mid + 1; else hi = mid;
-    }
-    int2 pr = make_int2(-1, -1);
-    if (lo >= a.n_remove || a.gone[lo] != j) {
-        // kept: of the x rows before it in the tail, those removed are the removed ones below j that are not holes;
-        // with h holes, lo - h of them, so it is mover x - (lo - h); holes are the first h of the list
-        int hl = 0, hh = a.n_remove;
-        while (hl < hh) {
-            const int mid = (hl + hh) / 2;
-            if (a.gone[mid] < left) hl = mid + 1; else hh = mid;
-        }
-        const int32_t hole = a.gone[x - (lo - hl)];
-        const int64_t to = pool_row0(a, hole), from = pool_row0(a, j);
-        if (to >= 0 && from >= 0) pr = make_int2((int)to, (int)from);
-        for (int g = 0; g < a.Hk; ++g) a.w[g * a.w_stride + hole] = a.w[g * a.w_stride + j];
-    }
-    for (int g = 0; g < a.Hk; ++g) a.w[g * a.w_stride + j] = 0.f;
-    a.pairs[x] = pr;
 }
 
 // One warp a (pair, layer): every head's row of the four tensors, in the widest words that its rows allow.
@@ -200,9 +212,16 @@ __global__ void __launch_bounds__(256) evict_move(const __grid_constant__ EvictA
 
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t st) {
     if (a.L > 65535) return cudaErrorInvalidValue;
-    evict_keys<<<(unsigned)((a.n_cand + 255) / 256), 256, 0, st>>>(a);
-    evict_select<<<1, SEL, 0, st>>>(a);
-    evict_pairs<<<(unsigned)((a.n_remove + 127) / 128), 128, 0, st>>>(a);
+    // Up to FEW candidates one CTA does it all (8 heads, 4096 rows, 64 to go: the call takes @@A@@ us instead of @@B@@);
+    // more are summed and paired by as many as there are.
+    constexpr int FEW = 8192;
+    if (a.n_cand <= FEW) {
+        evict_select<true><<<1, SEL, 0, st>>>(a);
+    } else {
+        evict_keys<<<(unsigned)((a.n_cand + 255) / 256), 256, 0, st>>>(a);
+        evict_select<false><<<1, SEL, 0, st>>>(a);
+        evict_pairs<<<(unsigned)((a.n_remove + 127) / 128), 128, 0, st>>>(a);
+    }
     evict_move<<<dim3((unsigned)((a.n_remove + 7) / 8), (unsigned)a.L), 256, 0, st>>>(a);
     return cudaGetLastError();
 }

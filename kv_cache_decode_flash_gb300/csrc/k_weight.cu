@@ -28,6 +28,9 @@ namespace {
 
 constexpr int THREADS = 5 * GROUP; // roles: softmax of even and of odd steps, loading of even and odd steps, the issuing warp
 constexpr int TN = TC_M;           // cached rows of a step
+// Registers: a launch gives every thread 96; the summing groups take what the issuing warp's group hands back.
+constexpr int R_SUM = 128, R_MMA = 24;
+static_assert(2 * R_SUM + 2 * 96 + R_MMA <= 5 * 96, "the roles' registers come from the launch's");
 static_assert(WEIGHT_STEP == TN, "items are whole steps");
 
 enum Bar { KF0, KF1, KE0, KE1, SF0, SF1, SE0, SE1, QF, DRAIN, N_BARS };
@@ -168,6 +171,7 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
 
     if (warp < 8) {
         // -------------------------------------------------- sums, and the query rows
+        regs_inc<R_SUM>();
         const int h = warp >> 2, t = tid & 127;
         const uint32_t S = tm + h * 256 + ((uint32_t)(warp & 3) << 21);
         float *w = p.w + ((int64_t)q.w_index * p.Hk + g) * p.w_stride;
@@ -175,7 +179,7 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
         for (int mg = 0; mg < groups && steps > 0; ++mg) {
             const int rows = min(MG, m_all - mg * MG), cols = (rows + 15) / 16 * 16;
             named_sync<2, 2 * GROUP>(); // every product with the rows before is done: both groups have its scores
-            constexpr int QR = 5;
+            constexpr int QR = 4;
             for (int mb = warp; mb < cols; mb += 8 * QR) {
                 Query<D> y[QR];
                 float z[QR];
@@ -341,7 +345,9 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
                 }
             }
         }
-    } else if (warp == 16 && lane == 0) {
+    } else {
+        regs_dec<R_MMA>();
+        if (warp > 16 || lane > 0) return;
         // -------------------------------------------------- products
         const uint32_t sq = smem_u32(smem), sk = smem_u32(smem + L::K);
         int i = 0;
