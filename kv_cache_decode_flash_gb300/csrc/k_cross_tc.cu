@@ -88,7 +88,7 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
         row[s % SLOTS][t] = next;
         look_up(s + 1);
     };
-    auto clear = [&](int s) { // a step's reports; those of four steps before are read no more
+    auto clear = [&](int s) { // a step's reports; the slot's last step, four before, is done with (its V was used up)
         if (IS_V && t < TN / 32) x.badrow[s % SLOTS][t] = 0;
     };
     auto begin = [&] { // the query rows are there: how far the tokens see
@@ -102,7 +102,6 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
     for (int k = 0; k < 3; ++k) row[k][t] = pool_row(p, q, g, r0 + k * TN + t);
     look_up(3);
     clear(0);
-    clear(1);
     named_sync<SYNC, GROUP>();
     if constexpr (T == KVC_F16) {
         // A step's copies are under way while those of the step before are waited for, if their stage is free by then;
@@ -132,7 +131,7 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
                 copy_halves<D>(tiles + (s & 1) * Lay<D>::TILE, data, row[s % SLOTS], t);
             }
             find(s + 3);
-            clear(s + 2);
+            clear(s + 1);
             named_sync<SYNC, GROUP>();
         }
     } else {
@@ -168,7 +167,7 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
             m = __reduce_max_sync(0xffffffffu, m);
             if ((t & 31) == 0) x.red[IS_V][s & 1][t >> 5] = m;
             find(s + 3);
-            clear(s + 2);
+            clear(s + 1);
             named_sync<SYNC, GROUP>();
             const uint4 r = *reinterpret_cast<const uint4 *>(x.red[IS_V][s & 1]);
             const uint32_t top = max(max(r.x, r.y), max(r.z, r.w));

@@ -81,7 +81,9 @@ __global__ void __launch_bounds__(128) evict_pairs(const __grid_constant__ Evict
 
 // ALL: few candidates, whose keys and pairs the one CTA sees to as well.
 template <bool ALL> __global__ void __launch_bounds__(SEL) evict_select(const __grid_constant__ EvictArgs a) {
-    __shared__ uint32_t hist[256];
+    constexpr int COPIES = 8; // of the counts: lanes that share a digit meet on few addresses
+    __shared__ uint32_t hist[COPIES][256];
+    constexpr int AHEAD = 8;  // a thread's keys that are under way together
     __shared__ uint32_t prefix, left;
     __shared__ int32_t below[WARPS], equal[WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -93,21 +95,24 @@ template <bool ALL> __global__ void __launch_bounds__(SEL) evict_select(const __
         left = (uint32_t)a.n_remove; // rank of the wanted key among those that share the prefix, from 1
     }
     for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
+        for (int i = tid; i < COPIES * 256; i += SEL) hist[i >> 8][i & 255] = 0;
         __syncthreads();
         const uint32_t pre = prefix;
         const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-        for (int i0 = 0; i0 < n; i0 += SEL) {
-            const int i = i0 + tid;
-            const uint32_t k = i < n ? a.keys[i] : 0u;
-            const bool mine = i < n && (k & mask) == pre;
-            // equal digits of a warp count once (few distinct digits are common)
-            const uint32_t act = __ballot_sync(0xffffffffu, mine);
-            if (mine) {
-                const uint32_t d = (k >> shift) & 255u;
-                const uint32_t same = __match_any_sync(act, d);
-                if (lane == __ffs(same) - 1) atomicAdd(&hist[d], (uint32_t)__popc(same));
-            }
+        for (int i0 = tid; i0 < n; i0 += SEL * AHEAD) {
+            uint32_t k[AHEAD];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) k[j] = i0 + j * SEL < n ? a.keys[i0 + j * SEL] : ~pre;
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j)
+                if (i0 + j * SEL < n && (k[j] & mask) == pre) atomicAdd(&hist[lane % COPIES][(k[j] >> shift) & 255u], 1u);
+        }
+        __syncthreads();
+        if (tid < 256) {
+            uint32_t c = 0;
+#pragma unroll
+            for (int k = 0; k < COPIES; ++k) c += hist[k][tid];
+            hist[0][tid] = c;
         }
         __syncthreads();
         if (warp == 0) {
@@ -115,7 +120,7 @@ template <bool ALL> __global__ void __launch_bounds__(SEL) evict_select(const __
             uint32_t c[8], sum = 0;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                c[k] = hist[lane * 8 + k];
+                c[k] = hist[0][lane * 8 + k];
                 sum += c[k];
             }
             uint32_t inc = sum;
@@ -145,10 +150,15 @@ template <bool ALL> __global__ void __launch_bounds__(SEL) evict_select(const __
     const int per = (n + WARPS * 32 - 1) / (WARPS * 32) * 32;
     const int lo = min(n, warp * per), hi = min(n, lo + per);
     int nb = 0, ne = 0;
-    for (int i = lo + lane; i < hi; i += 32) {
-        const uint32_t k = a.keys[i];
-        nb += k < key;
-        ne += k == key;
+    for (int i = lo + lane; i < hi; i += 32 * AHEAD) {
+        uint32_t k[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) k[j] = i + j * 32 < hi ? a.keys[i + j * 32] : 0u;
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            nb += i + j * 32 < hi && k[j] < key;
+            ne += i + j * 32 < hi && k[j] == key;
+        }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -165,19 +175,21 @@ template <bool ALL> __global__ void __launch_bounds__(SEL) evict_select(const __
         b0 += below[w];
         e0 += equal[w];
     }
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = i < hi ? a.keys[i] : 0xffffffffu;
-        const bool lt = i < hi && k < key, eq = i < hi && k == key;
-        const uint32_t ml = __ballot_sync(0xffffffffu, lt), me = __ballot_sync(0xffffffffu, eq);
-        const uint32_t under = (1u << lane) - 1u;
-        const int er = e0 + __popc(me & under); // equal keys before this one
-        if (lt || (eq && er < ties)) {
-            const int at = b0 + __popc(ml & under) + min(er, ties);
-            a.gone[at] = a.rows ? a.rows[i] : a.first + i;
+    for (int i0 = lo; i0 < hi; i0 += 32 * AHEAD) {
+        uint32_t k[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) k[j] = i0 + j * 32 + lane < hi ? a.keys[i0 + j * 32 + lane] : 0xffffffffu;
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const int i = i0 + j * 32 + lane;
+            const bool lt = i < hi && k[j] < key, eq = i < hi && k[j] == key;
+            const uint32_t ml = __ballot_sync(0xffffffffu, lt), me = __ballot_sync(0xffffffffu, eq);
+            const uint32_t under = (1u << lane) - 1u;
+            const int er = e0 + __popc(me & under); // equal keys before this one
+            if (lt || (eq && er < ties)) a.gone[b0 + __popc(ml & under) + min(er, ties)] = a.rows ? a.rows[i] : a.first + i;
+            b0 += __popc(ml);
+            e0 += __popc(me);
         }
-        b0 += __popc(ml);
-        e0 += __popc(me);
     }
     if (ALL) {
         __syncthreads();
@@ -212,8 +224,8 @@ __global__ void __launch_bounds__(256) evict_move(const __grid_constant__ EvictA
 
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t st) {
     if (a.L > 65535) return cudaErrorInvalidValue;
-    // Up to FEW candidates one CTA does it all (8 heads, 4096 rows, 64 to go: the call takes @@A@@ us instead of @@B@@);
-    // more are summed and paired by as many as there are.
+    // Up to FEW candidates one CTA does it all, more are summed and paired by as many CTAs as there are.  The whole call,
+    // 8 heads, 64 rows to go: 4096 rows 58.8 us by one CTA, 61.0 by many; 8128 rows 63.4 and 66.6; 32768 rows 134 and 113.
     constexpr int FEW = 8192;
     if (a.n_cand <= FEW) {
         evict_select<true><<<1, SEL, 0, st>>>(a);

@@ -162,6 +162,39 @@ def test_cross_ragged_batch_shared_and_empty_sequences(kind, act):
         tw.close()
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["q8", "f16"])
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+def test_cross_scales_of_zero_and_below(scale, kind, act):
+    n, T = 300, 37
+    tw = _cache(kind, 8, 2, 64, [n], exact=True)
+    try:
+        rng = np.random.default_rng(15)
+        q = _queries(rng, T, 8, 64, act, 0.3)
+        vis = rng.integers(0, n + 1, T)
+        got, z = _run(tw, [0], [T], q, scale, vis)
+        _compare(tw, [0], [T], q, float(np.float32(scale)), vis, got, z, act, exact_kv_=True)
+    finally:
+        tw.close()
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["q8", "f16"])
+@pytest.mark.parametrize("T", [6, 90])
+def test_cross_long_rows_in_few_pages(kind, act, T):
+    """Many steps in a part, whole units beside cut ones, a page that ends inside a step."""
+    n = 9000
+    tw = _cache(kind, 8, 2, 64, [n], page=1008)
+    try:
+        rng = np.random.default_rng(21)
+        q = _queries(rng, T, 8, 64, act)
+        vis = np.sort(rng.integers(n - 300, n + 1, T))
+        got, z = _run(tw, [0], [T], q, 0.125, vis)
+        _compare(tw, [0], [T], q, 0.125, vis, got, z, act)
+    finally:
+        tw.close()
+
+
 def test_cross_more_sequences_than_a_launch_holds():
     import torch
 

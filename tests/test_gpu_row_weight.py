@@ -42,7 +42,10 @@ def _check_weight(tw, ids, n_q, q, scale, vis, pad=5, layer=0, masked=True):
         add, bound = weight(q[t0:t0 + T].double().cpu().numpy(), K, scale, vis[t0:t0 + T], lse[t0:t0 + T].astype(np.float64))
         n = len(K)
         err = np.abs(got[i, :, :n] - (w0[i, :, :n].astype(np.float64) + add))
-        lim = bound + 2.0**-23 * (w0[i, :, :n] + add)
+        # the accumulators take the query rows in groups of 128 or 256: an addition, rounded by half a step (2^-24), for each
+        # group, on a sum that no addition makes smaller; and one more for w0 + add here
+        groups = -(-T * (q.shape[1] // tw.Hk) // 128)
+        lim = bound + (groups + 1) * 2.0**-24 * (w0[i, :, :n] + add)
         assert np.all(err <= lim), "entry %d: off by %.3g, %.2f of its bound" % (i, err.max(), (err / lim).max())
         assert np.array_equal(got[i, :, n:], w0[i, :, n:])  # behind the rows: as it was
         t0 += T
@@ -78,6 +81,45 @@ def test_weight_ragged_batch(act):
         a = _check_weight(tw, ids, n_q, q, 0.125, vis)
         b = _check_weight(tw, ids, n_q, q, 0.125, vis)
         assert np.array_equal(a, b)  # bitwise repeatable
+    finally:
+        tw.close()
+
+
+@pytest.mark.parametrize("kind", ["q8", "f16"])
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_weight_more_query_rows_than_fit_at_a_time(kind, act):
+    """Several groups of query rows over an odd number of steps; scales far apart between the steps."""
+    n, T = 700, 75  # 600 query rows of a KV head
+    tw = Twin(1, 8, 1, 64, n + 64, type_=KINDS[kind][0], page_rows=48)
+    try:
+        rng = np.random.default_rng(31)
+        f = (2.0 ** rng.integers(-8, 9, (n // 100, 1, 1))).astype(np.float32).repeat(100, 0)
+        k = rng.standard_normal((n, 1, 64)).astype(np.float32) * f
+        tw.append(0, 0, 0, k, k)
+        q = _queries(rng, T, 8, 64, act)
+        vis = rng.integers(0, n + 1, T)
+        _check_weight(tw, [0], [T], q, 0.01, vis)
+        _check_weight(tw, [0], [T], q, -0.01, np.full(T, n), masked=False)
+    finally:
+        tw.close()
+
+
+def test_weight_in_a_graph_on_another_stream():
+    import torch
+
+    tw = _cache("q8", 8, 2, 64, [900])
+    try:
+        q = _queries(np.random.default_rng(3), 9, 8, 64, "bf16")
+        _, z = _run(tw, [0], [9], q, 0.125)
+        w, eager = (torch.zeros(1, 2, 900, device="cuda:0") for _ in range(2))
+        st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            tw.gpu.attn_weight(0, [0], [9], q, z, w, 0.125)
+        for _ in range(3):
+            g.replay()
+            tw.gpu.attn_weight(0, [0], [9], q, z, eager, 0.125)
+        torch.cuda.synchronize()
+        assert bool((w == eager).all()) and float(w.sum()) > 0
     finally:
         tw.close()
 
