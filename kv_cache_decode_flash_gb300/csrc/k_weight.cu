@@ -19,8 +19,13 @@
 // it is undone, are seldom rewritten.
 //   One CTA per SM, 17 warps: two softmax groups and two loading groups that take
 // the steps in turn, and the issuing thread; the accumulators alternate in TMEM.
-// What bounds it: few query rows, the bytes of K; many, the loading groups'
-// conversion beside the products (128 x rows x D for each part).
+// What bounds it: with many query rows shared memory, which the products' operands
+// (two parts of K, each against all query rows), the conversion's stores and the
+// factors' loads share (32 tokens of 40 heads over 131072 rows: q8_0 91 us, of which
+// the products alone 36; 32-bit queries 140 us; halves, 32 heads, 62 us); with few,
+// the memory for halves (one token: 55 us, 4.9 TB/s) and the conversion for codes
+// (57 us, 2.5 TB/s).  The register-operand tensor path, which takes codes as they
+// are, reached 228 us on the first of these.
 #include "tc_tile.cuh"
 
 namespace kvc {
