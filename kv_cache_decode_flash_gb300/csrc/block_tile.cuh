@@ -81,19 +81,16 @@ template <int KT> __device__ __forceinline__ constexpr int row_bytes(int D) {
     return KT == KVC_F16 ? 2 * D : (KT == KVC_Q4_0 ? D / 2 : D);
 }
 
-// A step's rows of one tensor as fp16 in shared memory (codes without their scale); returns whether a
-// value of them is not finite (V only: such values are set to 0).
+// A step's rows of one tensor, as they are stored, to fp16 (codes without their scale), both in shared memory; returns
+// whether a value of them is not finite (V only: such values are set to 0).
 template <int D, int T, bool V>
-__device__ __forceinline__ bool fill(__half (*dst)[D + TILE_PAD], const uint8_t *data, const int32_t *row,
-                                     uint8_t *badrow, int tid) {
+__device__ __forceinline__ bool fill(__half (*dst)[D + TILE_PAD], const uint8_t *raw, uint8_t *badrow, int tid) {
     constexpr int RB = row_bytes<T>(D), PIECES = RB / 16;
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < CROSS_TILE_N * PIECES / BLOCK_THREADS; ++i) {
         const int at = tid + i * BLOCK_THREADS, j = at / PIECES, c = at % PIECES;
-        const int32_t R = row[j];
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (R >= 0) u = *reinterpret_cast<const uint4 *>(data + (int64_t)R * RB + c * 16);
+        uint4 u = *reinterpret_cast<const uint4 *>(raw + at * 16);
         if constexpr (T == KVC_F16) {
             if constexpr (V) {
                 bool b = drop_nonfinite(u.x);
@@ -134,6 +131,29 @@ __device__ __forceinline__ int32_t pool_row(const BlockParams &p, const BlockSeq
     }
     return (page * p.Hk + g) * p.P + (int32_t)(lr - pi * p.P); // rows of a layer's pool are fewer than 2^31
 }
+
+// A row's way through the page table in two steps, so that nobody waits for the table: its entry is requested, and
+// looked at a step later.
+struct Lookup {
+    int32_t page = -1;
+    uint32_t cell = 0;
+    bool in = false;
+    __device__ __forceinline__ void ask(const BlockParams &p, const BlockSeq &q, int j, bool valid) {
+        in = valid && j < q.n_rows;
+        const uint32_t lr = (uint32_t)q.off + (uint32_t)j, pi = lr / (uint32_t)p.P;
+        cell = lr - pi * (uint32_t)p.P;
+        page = -1;
+        if (in && pi < (uint32_t)p.max_pages) page = p.pt[(int64_t)q.id * p.max_pages + pi];
+    }
+    // the pool row, -1 for none (a page that the pool does not have is reported)
+    __device__ __forceinline__ int32_t row(const BlockParams &p, int g) const {
+        if (in && (page < 0 || page >= p.n_pages)) {
+            atomicOr(p.err, ERR_BAD_PAGE);
+            return -1;
+        }
+        return in ? (page * p.Hk + g) * p.P + (int32_t)cell : -1;
+    }
+};
 
 // The launch's sequence that work item `item` belongs to: the last one whose
 // first item is not behind it (sequences without items share a first item).

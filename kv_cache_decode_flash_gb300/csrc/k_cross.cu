@@ -40,24 +40,44 @@ constexpr int THREADS = BLOCK_THREADS;
 constexpr int TM = CROSS_TILE_M, TN = CROSS_TILE_N;
 constexpr int E_MIN = -24; // exponent of the smallest fp16 scale
 
-template <int D> struct Smem {
+template <int D, int KT, int VT, bool LO> struct Smem {
     static constexpr int PITCH = D + TILE_PAD;
     __half qhi[TM][PITCH];
-    __half qlo[TM][PITCH];
+    __half qlo[LO ? TM : 1][PITCH];
     __half k[TN][PITCH];
     __half v[TN][PITCH];
-    float ks[D / 32][TN]; // block scales, by block
-    float vs[D / 32][TN];
-    int32_t row[TN];          // pool row of each row of the step, -1 past the end
+    uint8_t rawk[TN * row_bytes<KT>(D)]; // the next step's rows and block scales, as they are stored
+    uint8_t rawv[TN * row_bytes<VT>(D)];
+    uint16_t rks[TN * (D / QK)], rvs[TN * (D / QK)];
+    float ks[D / QK][TN]; // block scales, by block
+    float vs[D / QK][TN];
+    int32_t row[2][TN];       // pool row of each row of a step, -1 past the end
     float qscale[TM];         // score per unit of the normalised product, in log2
     int32_t vis[TM];          // rows that the query row sees
     float red[THREADS / 32];
     float m[4][TM], l[4][TM]; // merge of warps that share query rows
     uint32_t poison[TM][D / 16]; // two bits a value: +inf, -inf (both: NaN) received
-    uint8_t badrow[TN];
+    uint8_t badrow[2][TN];
     int32_t vis_max;
-    int32_t bad, any_bad;
+    int32_t bad[2], any_bad;
 };
+
+// Requests 16 (or a row's scales: 8 or 4) bytes for shared memory; nothing is read, and zeros are written, where there is no row.
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+template <int N> __device__ __forceinline__ void copy_scales(void *dst, const void *src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(N), "r"(in ? N : 0) : "memory");
+}
+template <int RB> __device__ __forceinline__ void copy_rows(uint8_t *dst, const uint8_t *data, const int32_t *row, int tid) {
+    constexpr int PIECES = RB / 16;
+#pragma unroll
+    for (int i = 0; i < TN * PIECES / THREADS; ++i) {
+        const int at = tid + i * THREADS;
+        const int32_t R = row[at / PIECES];
+        copy16(dst + at * 16, data + (int64_t)max(R, 0) * RB + at % PIECES * 16, R >= 0);
+    }
+}
 
 // (out of line: the place that calls it is unrolled)
 template <int D, int T>
@@ -72,7 +92,8 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
     constexpr int WN = 4 / WM, NC = TN / WN, NT = NC / 8, NB = D / QK;
     constexpr int MROWS = 16 * WM;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    Smem<D> &s = *reinterpret_cast<Smem<D> *>(smem_raw);
+    using Sm = Smem<D, KT, VT, LO>;
+    Sm &s = *reinterpret_cast<Sm *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int wm = warp % WM, wn = warp / WM, gid = lane >> 2, qc = lane & 3;
 
@@ -87,7 +108,7 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
     if (tid == 0) {
         s.vis_max = 0;
         s.any_bad = 0;
-        s.bad = 0;
+        s.bad[0] = s.bad[1] = 0;
     }
     __syncthreads();
     constexpr int QR = WM == 4 ? 8 : 4; // of a warp's rows, under way together
@@ -130,28 +151,51 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
     const float qs[2] = {s.qscale[mrow], s.qscale[mrow + 8]};
     const int vis[2] = {s.vis[mrow], s.vis[mrow + 8]};
 
-    for (int base = r0; base < r1; base += TN) {
-        // the step's rows; a page that the pool does not have is reported and its rows are left out
+    // A step's rows come while the step before is computed (as they are stored: they are turned into fp16 once for all
+    // warps), their places in the pool a step earlier still; a page that the pool does not have is reported, its rows are left out.
+    Lookup next;
+    auto request = [&](int i) {
+        const int32_t *row = s.row[i & 1];
+        copy_rows<row_bytes<KT>(D)>(s.rawk, p.kdata, row, tid);
+        copy_rows<row_bytes<VT>(D)>(s.rawv, p.vdata, row, tid);
+        const int j = tid & (TN - 1);
+        const int32_t R = row[j];
+        if (KT != KVC_F16 && tid < TN) copy_scales<NB * 2>(&s.rks[j * NB], p.ks + (int64_t)max(R, 0) * NB, R >= 0);
+        if (VT != KVC_F16 && tid >= TN) copy_scales<NB * 2>(&s.rvs[j * NB], p.vs + (int64_t)max(R, 0) * NB, R >= 0);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (r0 < r1) {
         if (tid < TN) {
-            const int32_t R = pool_row(p, q, g, base + tid);
-            s.row[tid] = R;
-            s.badrow[tid] = 0;
+            s.row[0][tid] = pool_row(p, q, g, r0 + tid);
+            s.badrow[0][tid] = 0;
+            next.ask(p, q, r0 + TN + tid, true);
         }
         __syncthreads();
-        fill<D, KT, false>(s.k, p.kdata, s.row, nullptr, tid);
-        bool bad = fill<D, VT, true>(s.v, p.vdata, s.row, s.badrow, tid);
+        request(0);
+    }
+    for (int base = r0, step = 0; base < r1; base += TN, ++step) {
+        const int cur = step & 1;
+        const int32_t *row = s.row[cur];
+        const uint8_t *badrow = s.badrow[cur];
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads(); // the step's rows are there, the tiles of the step before are done with
+        if (tid < TN) {
+            s.row[cur ^ 1][tid] = next.row(p, g);
+            s.badrow[cur ^ 1][tid] = 0;
+        }
+        if (tid == 0) s.bad[cur ^ 1] = 0;
+        fill<D, KT, false>(s.k, s.rawk, nullptr, tid);
+        bool bad = fill<D, VT, true>(s.v, s.rawv, s.badrow[cur], tid);
         float top = 0.f;
         if constexpr (KT != KVC_F16 || VT != KVC_F16) {
             for (int i = tid; i < TN * NB; i += THREADS) {
                 const int j = i / NB, b = i % NB;
-                const int32_t R = s.row[j];
-                if constexpr (KT != KVC_F16)
-                    s.ks[b][j] = R >= 0 ? __half2float(__ushort_as_half(p.ks[(int64_t)R * NB + b])) : 0.f;
+                if constexpr (KT != KVC_F16) s.ks[b][j] = __half2float(__ushort_as_half(s.rks[i]));
                 if constexpr (VT != KVC_F16) {
-                    float d = R >= 0 ? __half2float(__ushort_as_half(p.vs[(int64_t)R * NB + b])) : 0.f;
+                    float d = __half2float(__ushort_as_half(s.rvs[i]));
                     if (!(fabsf(d) <= 65504.f)) {
                         d = 0.f;
-                        s.badrow[j] = 1;
+                        s.badrow[cur][j] = 1;
                         bad = true;
                     }
                     s.vs[b][j] = d;
@@ -162,8 +206,12 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
             for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
             if (lane == 0) s.red[warp] = top;
         }
-        if (bad) s.bad = 1;
+        if (bad) s.bad[cur] = 1;
         __syncthreads();
+        if (base + TN < r1) {
+            request(step + 1);
+            if (tid < TN) next.ask(p, q, base + 2 * TN + tid, true);
+        }
         float grow = 1.f; // factor of the sums so far when the range exponent grows
         if constexpr (VT != KVC_F16) {
             top = fmaxf(fmaxf(s.red[0], s.red[1]), fmaxf(s.red[2], s.red[3]));
@@ -189,7 +237,7 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
             for (int k = 0; k < 4; ++k) {
                 const int jt = wn * NC + n * 8 + qc * 2 + (k & 1);
                 const float x = sc[n][k] * qs[k >> 1];
-                sc[n][k] = base + jt < vis[k >> 1] && s.row[jt] >= 0 ? x : -INFINITY;
+                sc[n][k] = base + jt < vis[k >> 1] && row[jt] >= 0 ? x : -INFINITY;
                 nm[k >> 1] = fmaxf(nm[k >> 1], sc[n][k]);
             }
         float al[2];
@@ -212,14 +260,14 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
             sum[h] = sum[h] * al[h] + add;
             al[h] *= grow;
         }
-        if (s.bad) { // a V value of this step is not finite: it goes to the rows that give it weight
+        if (s.bad[cur]) { // a V value of this step is not finite: it goes to the rows that give it weight
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int jt = wn * NC + n * 8 + qc * 2 + (k & 1);
-                    if (s.badrow[jt] && sc[n][k] > 0.f)
-                        mark_row<D, VT>(s.poison[mrow + 8 * (k >> 1)], p.vdata, p.vs, s.row[jt]);
+                    if (badrow[jt] && sc[n][k] > 0.f)
+                        mark_row<D, VT>(s.poison[mrow + 8 * (k >> 1)], p.vdata, p.vs, row[jt]);
                 }
             s.any_bad = 1;
         }
@@ -285,9 +333,8 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[b * 4 + n][k] = fmaf(o[b * 4 + n][k], al[k >> 1], t[n][k]);
         }
-        __syncthreads();
-        if (tid == 0) s.bad = 0;
     }
+    __syncthreads();
 
     // the quad's sums, then the values themselves
     const float back = VT == KVC_F16 ? 1.f / 4096.f : ldexpf(1.f, E - 12);
@@ -304,7 +351,7 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
         // warps that share query rows: joined in warp order by the first of them, through the tiles' memory
         __syncthreads();
         float *buf = reinterpret_cast<float *>(&s.k[0][0]); // [WN - 1][MROWS][D]
-        static_assert(sizeof(float) * (WN - 1) * MROWS * D <= sizeof(__half) * 2 * TN * Smem<D>::PITCH, "merge buffer");
+        static_assert(sizeof(float) * (WN - 1) * MROWS * D <= sizeof(__half) * 2 * TN * Sm::PITCH, "merge buffer");
         if (qc == 0) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -394,7 +441,7 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
 
 template <int D, int KT, int VT, int WM, bool LO> cudaError_t go(const BlockParams &p, cudaStream_t st) {
     auto k = cross_kernel<D, KT, VT, WM, LO>;
-    const int bytes = (int)sizeof(Smem<D>);
+    const int bytes = (int)sizeof(Smem<D, KT, VT, LO>);
     static SharedMemory set;
     cudaError_t e = set.allow((const void *)k, bytes);
     if (e != cudaSuccess) return e;

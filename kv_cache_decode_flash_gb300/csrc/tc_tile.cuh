@@ -223,29 +223,6 @@ template <int D, int T> struct Codes {
     }
 };
 
-// A row's way through the page table in two steps, so that nobody waits for the table: its entry is requested, and
-// looked at a step later.
-struct Lookup {
-    int32_t page = -1;
-    uint32_t cell = 0;
-    bool in = false;
-    __device__ __forceinline__ void ask(const BlockParams &p, const BlockSeq &q, int j, bool valid) {
-        in = valid && j < q.n_rows;
-        const uint32_t lr = (uint32_t)q.off + (uint32_t)j, pi = lr / (uint32_t)p.P;
-        cell = lr - pi * (uint32_t)p.P;
-        page = -1;
-        if (in && pi < (uint32_t)p.max_pages) page = p.pt[(int64_t)q.id * p.max_pages + pi];
-    }
-    // the pool row, -1 for none (a page that the pool does not have is reported)
-    __device__ __forceinline__ int32_t row(const BlockParams &p, int g) const {
-        if (in && (page < 0 || page >= p.n_pages)) {
-            atomicOr(p.err, ERR_BAD_PAGE);
-            return -1;
-        }
-        return in ? (page * p.Hk + g) * p.P + (int32_t)cell : -1;
-    }
-};
-
 __device__ __forceinline__ __half2 scaled(uint16_t s, float up) {
     return __half2half2(__float2half_rn(__half2float(__ushort_as_half(s)) * up));
 }
