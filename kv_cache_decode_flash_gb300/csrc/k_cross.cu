@@ -29,8 +29,8 @@
 // It runs 32-bit queries, and 16-bit ones where the tcgen05 kernel does not pay
 // (block_attn.cu has the rule).  What bounds it: the register-operand tensor
 // path with many query rows (257 tokens of 40 heads over 4999 rows, q8_0 / q4_0,
-// 32-bit: two products each, 314 us, 84 TFLOP/s of results), its start and one
-// chain of steps with few (one token of 8 heads over 512 rows: 9 us).
+// 32-bit: two products each, 262 us, 100 TFLOP/s of results), its start and one
+// chain of steps with few (one token of 8 heads over 512 rows: 8.6 us).
 #include "block_tile.cuh"
 
 namespace kvc {
