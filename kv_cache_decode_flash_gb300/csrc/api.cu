@@ -1238,10 +1238,7 @@ int kvc_seq_evict_window(kvc_ctx *cc, int seq, int layer, int n_keep, int n_disc
     return KVC_OK;
 }
 
-int kvc_seq_evict_weight(kvc_ctx *cc, int seq, int p0, int p1, int32_t n_remove, float *w, int64_t w_stride,
-                         int32_t *n_removed) {
-    if (!cc) return KVC_EINVAL;
-    Ctx *c = reinterpret_cast<Ctx *>(cc);
+static int evict_weight(Ctx *c, int seq, int p0, int p1, int32_t n_remove, float *w, int64_t w_stride, int32_t *n_removed) {
     if (c->host) return c->fail(KVC_EINVAL, "sequence operations need a device-resident context");
     if (seq < 0 || seq >= (int)c->seqs.size()) return c->fail(KVC_EINVAL, "sequence id out of range");
     if (n_remove < 0 || !n_removed) return c->fail(KVC_EINVAL, "n_remove must not be negative, n_removed non-null");
@@ -1326,6 +1323,17 @@ int kvc_seq_evict_weight(kvc_ctx *cc, int seq, int p0, int p1, int32_t n_remove,
     release_tail_pages(c, q);
     *n_removed = (int32_t)k;
     return KVC_OK;
+}
+
+int kvc_seq_evict_weight(kvc_ctx *cc, int seq, int p0, int p1, int32_t n_remove, float *w, int64_t w_stride,
+                         int32_t *n_removed) {
+    if (!cc) return KVC_EINVAL;
+    Ctx *c = reinterpret_cast<Ctx *>(cc);
+    try { // (the selection's lists, made before anything changes)
+        return evict_weight(c, seq, p0, p1, n_remove, w, w_stride, n_removed);
+    } catch (const std::bad_alloc &) {
+        return KVC_ENOMEM;
+    }
 }
 
 int kvc_state_get(kvc_ctx *cc, int seq, int p0, int p1, void *dst, size_t cap, size_t *n_written) {

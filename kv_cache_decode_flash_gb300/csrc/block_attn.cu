@@ -1,6 +1,6 @@
 // block_attn.cu - host side of the operators over a block of query tokens
-// (kvc_attn_cross, kvc_attn_weight): checks, the split of the cached rows over work items, the
-// work space and the launches.
+// (kvc_attn_cross, kvc_attn_weight): checks, the split of the cached rows over
+// work items, the work space and the launches.
 #include "block_attn.h"
 #include "ctx.h"
 
@@ -35,9 +35,8 @@ static int ensure_block_space(Ctx *c, cudaStream_t st) {
 }
 
 // Cut the cached rows of the launch's units into parts.  `want`: items that run
-// at once; a part has `least` rows at least, and the partial rows
-// of all parts fit the work space.
-// An item costs `fixed` steps beside its own.
+// at once; a part has `least` rows at least, and the partial rows of all parts
+// fit the work space.  An item costs `fixed` steps beside its own.
 //  One sequence: its units are alike, so the schedule is whole waves; those of
 // the last one or two are cut into the parts that shorten it most.
 //  Several: all rows are cut into parts of at most one length, the one for

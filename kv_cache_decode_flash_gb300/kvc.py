@@ -524,18 +524,18 @@ class KVCache:
         w [n_seq][n_head_kv][rows or more] fp32; lse as attn_cross wrote it for these tokens."""
         act, total = _act(q), sum(map(int, n_q))
         self._block_io(q, None, lse, n_vis, total)
+        _block_tensor("w", w, self.device, _torch.float32, 0)
         if w.dim() != 3 or w.shape[0] != len(seq_ids) or w.shape[1] != self.params.n_head_kv:
             raise KvcError(KVC_EINVAL, "w must be [n_seq][n_head_kv][rows]")
-        _block_tensor("w", w, self.device, _torch.float32, 0)
         kvc_attn_weight(self.ctx, layer, seq_ids, n_q, act, q, lse, w, w.shape[2], kq_scale, n_vis, stream, self.device)
 
     def evict_weight(self, seq, p0, p1, n_remove, w):
         """Evict the n_remove rows of least accumulated weight with positions in [p0, p1);
         w [n_head_kv][rows or more] fp32 follows the rows.  Returns the rows removed."""
         _load_torch()
+        _block_tensor("w", w, self.device, _torch.float32, 0)
         if w.dim() != 2 or w.shape[0] != self.params.n_head_kv:
             raise KvcError(KVC_EINVAL, "w must be [n_head_kv][rows]")
-        _block_tensor("w", w, self.device, _torch.float32, 0)
         return kvc_seq_evict_weight(self.ctx, seq, p0, p1, n_remove, w, w.shape[1])
 
     def _block_io(self, q, out, lse, n_vis, total):

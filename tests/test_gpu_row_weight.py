@@ -389,3 +389,22 @@ def test_evict_allocation_failure_leaves_the_cache():
         assert tw.gpu.evict_weight(0, -1, -1, 20, w) == 20
     finally:
         tw.close()
+
+
+def test_tables_of_weights_that_are_no_tensors_are_refused():
+    import torch
+
+    tw = _cache("q8", 8, 2, 64, [20])
+    try:
+        q = _queries(np.random.default_rng(4), 1, 8, 64, "f32")
+        z, w = torch.zeros(1, 8, device="cuda:0"), torch.zeros(1, 2, 20, device="cuda:0")
+        for bad in (None, w.data_ptr(), w.cpu().numpy()):
+            with pytest.raises(tw.kvc.KvcError) as e:
+                tw.gpu.attn_weight(0, [0], [1], q, z, bad, 0.1)
+            assert e.value.status == tw.kvc.KVC_EINVAL
+            with pytest.raises(tw.kvc.KvcError) as e:
+                tw.gpu.evict_weight(0, 0, -1, 3, bad)
+            assert e.value.status == tw.kvc.KVC_EINVAL
+        assert tw.gpu.n_tokens(0) == 20
+    finally:
+        tw.close()
