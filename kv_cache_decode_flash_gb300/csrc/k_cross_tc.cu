@@ -116,7 +116,10 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
         // a step that has landed is not held back for a stage.
         copy_halves<D>(tiles, data, row[0], t);
         begin();
-        if (steps == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (steps == 0) { // no token sees a row: the results are put together where step 0 lands, so they wait for it
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            bar_arrive(&full[0]);
+        }
         for (int s = 0; s <= steps && steps > 0; ++s) {
             bool ahead = false;
             if (s < steps) {
@@ -489,6 +492,10 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
             bar_arrive(&x.bar[PF0 + h]);
         }
         if (done > 0) bar_wait_warp(&x.bar[OD0 + h], (done - 1) & 1, p.err, &x.abort);
+        if (KT == KVC_F16 && steps == 0) { // halves were requested before it was known that nobody sees them
+            bar_wait_warp(&x.bar[KF0], 0, p.err, &x.abort);
+            bar_wait_warp(&x.bar[VF0], 0, p.err, &x.abort);
+        }
         tc_after();
         // -------------------------------------------------- results
         named_sync<2, 2 * GROUP>(); // both halves' products are done: the K and V tiles are free
