@@ -47,7 +47,13 @@ template <bool CODES> struct Regs {
     static constexpr int HOLD = CODES ? 2 : 4; // blocks of 32 scores that a softmax thread keeps
     static_assert(2 * SOFT + 2 * LOAD + R_MMA <= 5 * 96, "the roles' registers come from the launch's");
 };
-constexpr int SLOTS = 4; // steps whose factors are kept: a step's are overwritten four steps later
+// Steps whose places, V exponents and reports are kept.  The V loaders write those of step s + 1 once P V of step s - 2 is
+// done, before which the softmax groups are through with step s - 3.
+constexpr int SLOTS = 4;
+// Steps whose score factors are kept.  The K loaders write that of step s + 1 once Q K of step s - 2 is done; in a tile of
+// one half that product comes after P V of step s - 4, and step s - 3's softmax may not even have begun: five are
+// needed, and eight make the place a mask.
+constexpr int KFACS = 8;
 constexpr float GROW = 8.f; // log2 growth of a maximum that is let pass before O is rescaled
 
 enum Bar { KF0, KF1, KE0, KE1, VF0, VF1, VE0, VE1, SF0, SF1, PF0, PF1, OD0, OD1, XF0, XF1, XF2, XF3, DRAIN, N_BARS };
@@ -63,7 +69,7 @@ struct Aux {
     int32_t row[2][SLOTS][TN];   // K's and V's loaders: pool rows of a step, -1 past the end
     float qscale[2 * TM];
     int32_t vis[2 * TM];
-    float kfac[SLOTS];           // score factor of the step's K exponent
+    float kfac[KFACS];           // score factor of the step's K exponent
     int32_t vexp[SLOTS];         // V's exponent as of the step
     uint32_t badrow[SLOTS][TN / 32]; // rows of the step whose V values that are not finite were left out
     alignas(16) uint32_t red[2][2][GROUP / 32];
@@ -125,7 +131,7 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
             if (s < steps) {
                 ahead = s < 2 || bar_try(&empty[s & 1], ((s >> 1) - 1) & 1);
                 if (ahead && s > 0) copy_halves<D>(tiles + (s & 1) * Lay<D>::TILE, data, row[s % SLOTS], t);
-                if (!IS_V && t == 0) x.kfac[s % SLOTS] = 1.f;
+                if (!IS_V && t == 0) x.kfac[s % KFACS] = 1.f;
             }
             if (s > 0) {
                 if (ahead)
@@ -189,7 +195,7 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
                     x.vexp[s % SLOTS] = E;
                     bar_arrive(&x.bar[XF0 + s % SLOTS]);
                 } else {
-                    x.kfac[s % SLOTS] = ldexpf(1.f, E - 7);
+                    x.kfac[s % KFACS] = ldexpf(1.f, E - 7);
                 }
             }
         };
@@ -431,7 +437,7 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
             tc_after();
             if (live) {
                 const bool masked = base + TN > wvis;
-                const float f = cq * x.kfac[slot];
+                const float f = cq * x.kfac[s % KFACS];
                 constexpr int HOLD = Regs<KT != KVC_F16>::HOLD;
                 uint32_t sc[HOLD][32];
                 const float raw = masked ? row_scores<true>(S, vis - base, sc) : row_scores<false>(S, 0, sc);
