@@ -209,7 +209,9 @@ typedef enum kvc_act { KVC_ACT_F32 = 0, KVC_ACT_F16 = 1, KVC_ACT_BF16 = 2 } kvc_
  * that sees no row gets out = 0 and lse = -inf; n_q[i] may be 0.  The causal
  * attention of a prompt's tokens over themselves and the rows before them is
  * n_vis[t] = (rows before the block) + (t's place in the block) + 1.
- * What a row holds that a token does not see never reaches that token.
+ * What a row holds that a token does not see never reaches that token; a V
+ * value that is not finite reaches every token that sees its row, whatever the
+ * others see (infinite, or NaN where 16 bits leave the row no weight).
  * seq_ids, n_q: HOST int32[n_seq]; an id may come more than once (decoders
  * that share an encoder's rows).  act: type of q and out (kvc_act).
  * q, out: device [T][n_head][head_dim], contiguous; out may not overlap q.

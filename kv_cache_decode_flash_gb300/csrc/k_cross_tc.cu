@@ -70,8 +70,8 @@ struct Aux {
     float qscale[2 * TM];
     int32_t vis[2 * TM];
     float kfac[KFACS];           // score factor of the step's K exponent
-    int32_t vexp[SLOTS];         // V's exponent as of the step
-    uint32_t badrow[SLOTS][TN / 32]; // rows of the step whose V values that are not finite were left out
+    int32_t vexp[SLOTS];         // V's exponent as of the step, twice, and whether rows of it are reported in badrow
+    alignas(16) uint32_t badrow[SLOTS][TN / 32]; // rows of the step whose V values that are not finite were left out
     alignas(16) uint32_t red[2][2][GROUP / 32];
     float2 ml[TM];
     uint16_t scale[2][2][TN * 4]; // K's and V's block scales of a step, [row][block]
@@ -79,6 +79,11 @@ struct Aux {
     int32_t vis_max, vis_min, any_bad;
     volatile int32_t abort;
 };
+
+__device__ __forceinline__ bool any_bad(const uint32_t (&rows)[TN / 32]) {
+    const uint4 b = *reinterpret_cast<const uint4 *>(rows);
+    return (b.x | b.y | b.z | b.w) != 0;
+}
 
 template <int D> constexpr int smem_bytes() {
     // TMEM is allocated whole: one CTA per SM, whatever D
@@ -168,14 +173,13 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
         auto exponent = [&](int s) { // of step s, whose scales are sc
             uint32_t m = 0;
             const bool in = r0 + s * TN + t < q.n_rows; // a row past the end: scales 0
-            const bool drop = IS_V && r0 + (s + 1) * TN > vis_min;
 #pragma unroll
             for (int k = 0; k < D / QK; ++k) {
                 uint32_t h = sc[k >> 1] >> (16 * (k & 1)) & 0xffffu;
                 if (!in) h = 0;
                 if ((h & 0x7fffu) < 0x7c00u) {
                     m = max(m, h & 0x7fffu);
-                } else if (drop) { // not finite, and some token does not see it: reported and left out
+                } else if (IS_V) { // not finite: reported and left out
                     h = 0;
                     atomicOr(&x.badrow[s % SLOTS][t >> 5], 1u << (t & 31));
                 }
@@ -192,7 +196,7 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
             E = IS_V ? max(E, e) : e;
             if (t == 0) {
                 if (IS_V) {
-                    x.vexp[s % SLOTS] = E;
+                    x.vexp[s % SLOTS] = 2 * E + any_bad(x.badrow[s % SLOTS]);
                     bar_arrive(&x.bar[XF0 + s % SLOTS]);
                 } else {
                     x.kfac[s % KFACS] = ldexpf(1.f, E - 7);
@@ -448,15 +452,18 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
                     mx = top;
                 }
                 sum *= al;
-                // V's exponent and the reports of values that were left out
-                if (VT != KVC_F16)
-                    bar_wait_warp(&x.bar[XF0 + slot], (s / SLOTS) & 1, p.err, &x.abort);
-                else if (base + TN > vis_min)
-                    bar_wait_warp(&x.bar[VF0 + (s & 1)], (s >> 1) & 1, p.err, &x.abort);
+                // V's exponent, and whether values were left out: a row that sees those takes them from the reports, whatever
+                // the tile's other rows see
+                bool reported = false;
                 if (VT != KVC_F16) {
-                    const int e = x.vexp[slot];
+                    bar_wait_warp(&x.bar[XF0 + slot], (s / SLOTS) & 1, p.err, &x.abort);
+                    const int e2 = x.vexp[slot], e = e2 >> 1;
+                    reported = e2 & 1;
                     if (e != E) al *= ldexpf(1.f, max(E - e, -126));
                     E = e;
+                } else if (base + TN > vis_min) {
+                    bar_wait_warp(&x.bar[VF0 + (s & 1)], (s >> 1) & 1, p.err, &x.abort);
+                    reported = any_bad(x.badrow[slot]);
                 }
                 if (done > 0 && __any_sync(0xffffffffu, al != 1.f)) {
                     bar_wait_warp(&x.bar[OD0 + h], (done - 1) & 1, p.err, &x.abort);
@@ -471,12 +478,12 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
                     }
                 }
                 const float use = mx == -INFINITY ? 0.f : mx;
-                if (!masked) {
+                if (!masked && !reported) {
                     sum += row_exp<false>(S, 0, sc, f, use, [](int, const float(&)[32]) {});
                 } else {
                     sum += row_exp<true>(S, vis - base, sc, f, use, [&](int c, const float(&v)[32]) {
                         const uint32_t rows = x.badrow[slot][c];
-                        if (rows == 0) return; // V values of rows that some token does not see, and that are not finite
+                        if (rows == 0) return;
 #pragma unroll 1
                         for (int e = 0; e < 32; ++e) {
                             if (!(rows >> e & 1)) continue;

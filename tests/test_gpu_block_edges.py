@@ -68,3 +68,94 @@ def test_tiles_whose_tokens_see_nothing(kernel, T, kind, D, act):
             assert bool((got[~none].float() >= 999).all()) and bool(torch.isfinite(z[~none]).all())
     finally:
         tw.close()
+
+
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("unseen", [0, 1, 5])
+@pytest.mark.parametrize("T", [12, 40, 130])
+@pytest.mark.parametrize("kernel", [MMA, TC])
+def test_values_that_are_not_finite_reach_the_tokens_that_see_them(kernel, T, unseen, D, act):
+    """Infinities and NaN in V of rows that all but the block's first tokens see (those see nothing, or the rows before the
+    first of them): they come through for every token that sees them, whatever its neighbours see, and for no other."""
+    import torch
+
+    n, H, Hk = 500, 8, 2
+    inf = float("inf")
+    k, v = kv_inputs(19, 0, n, Hk, D, sigma=0.5)
+    v[100, 0, 3], v[170, 0, 35], v[299, 1, 5], v[400, 0, 3] = inf, -inf, np.nan, inf
+    tw = _twin("f16", H, Hk, D, n + 64)
+    try:
+        tw.gpu.append(0, 0, 0, _tensor(k), _tensor(v))
+        q = _tensor(np.random.default_rng(2).standard_normal((T, H, D)), act)
+        for few in (0, 100):  # none of them at all, or the rows before the first one that is not finite
+            vis = np.full(T, n)
+            vis[:unseen] = few
+            got, z = _attend(tw, kernel, [0], [T], q, 0.125, vis)
+            o = got.float()
+            assert bool(torch.isfinite(o[:unseen]).all())
+            assert few or bool((o[:unseen] == 0).all())
+            o = o[unseen:]
+            assert bool((o[:, :4, 3] == inf).all()) and bool((o[:, :4, 35] == -inf).all())
+            assert bool(torch.isnan(o[:, 4:, 5]).all())
+            o[:, :4, 3] = o[:, :4, 35] = o[:, 4:, 5] = 0
+            assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(z[unseen:]).all())
+    finally:
+        tw.close()
+
+
+@pytest.mark.parametrize("kind", ["q8", "q8q4"])
+@pytest.mark.parametrize("T", [12, 130])
+@pytest.mark.parametrize("kernel", [MMA, TC])
+def test_scales_that_are_not_finite_reach_the_tokens_that_see_them(kernel, T, kind):
+    """A block of V whose scale is infinite or NaN (values beyond fp16's scales) is not a number for the tokens that see
+    its row, and nothing for those that do not."""
+    import torch
+
+    n, H, Hk, D = 500, 8, 2, 128
+    k, v = kv_inputs(23, 0, n, Hk, D, sigma=0.5)
+    v[200, 1, 70], v[390, 0, 7] = np.float32(3e38), np.float32(np.nan)
+    tw = _twin(kind, H, Hk, D, n + 64)
+    try:
+        tw.gpu.append(0, 0, 0, _tensor(k), _tensor(v))
+        q = _tensor(np.random.default_rng(2).standard_normal((T, H, D)), "bf16")
+        vis = np.full(T, n)
+        vis[:3] = [0, 200, 390]
+        got, _ = _attend(tw, kernel, [0], [T], q, 0.125, vis)
+        fin = torch.isfinite(got.float())
+        assert bool(fin[:2].all()) and bool(fin[:, :4, 32:].all())  # (heads 0-3 read KV head 0: only its block 0 is spoilt)
+        assert not bool(fin[2:, 4:, 64:96].all(2).any())
+        assert bool(fin[:, 4:, :64].all()) and bool(fin[:, 4:, 96:].all())
+    finally:
+        tw.close()
+
+
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("T", [2, 60])
+@pytest.mark.parametrize("kernel", [MMA, TC])
+def test_infinite_value_of_a_row_of_little_weight(kernel, T, act):
+    """A row's weight of e^-40 is a positive number, too small for fp16: an infinite value there is infinite in the result, not
+    the NaN of 0 x inf (which the tcgen05 kernel may give where all tokens see the row)."""
+    import torch
+
+    n, H, Hk, D = 300, 4, 2, 64
+    k, v = kv_inputs(29, 0, n, Hk, D, sigma=0.5)
+    k[:] = 0
+    k[37, :, 0] = -40.0  # its score
+    v[37, 0, 3], v[37, 1, 40] = np.inf, -np.inf
+    tw = _twin("f16", H, Hk, D, n + 64)
+    try:
+        tw.gpu.append(0, 0, 0, _tensor(k), _tensor(v))
+        q = np.zeros((T, H, D))
+        q[:, :, 0] = 1.0
+        for vis in (None, [n] * (T - 1) + [30]):
+            got, _ = _attend(tw, kernel, [0], [T], _tensor(q, act), 1.0, vis)
+            o = got.float()[:T - 1]
+            if kernel == TC and vis is None:
+                assert not bool(torch.isfinite(o[:, :2, 3]).any()) and not bool(torch.isfinite(o[:, 2:, 40]).any())
+            else:
+                assert bool((o[:, :2, 3] == math.inf).all()) and bool((o[:, 2:, 40] == -math.inf).all())
+            o[:, :2, 3] = o[:, 2:, 40] = 0
+            assert bool(torch.isfinite(o).all())
+    finally:
+        tw.close()
