@@ -218,8 +218,9 @@ typedef enum kvc_act { KVC_ACT_F32 = 0, KVC_ACT_F16 = 1, KVC_ACT_BF16 = 2 } kvc_
  * lse: device fp32 [T][n_head], or NULL.  n_vis: device int32 [T], or NULL.
  * q and out 16-byte aligned, lse and n_vis 4-byte aligned.
  * Results are bitwise repeatable.  32-bit results keep 32-bit accuracy; with
- * 16-bit queries the products' operands have 11 significant bits or more and
- * all sums are fp32.
+ * 16-bit queries the products' operands have 11 significant bits or more
+ * (weights below 2^-21 of a token's largest: an error of 2^-32 of that one at
+ * most) and all sums are fp32.
  * The call only enqueues work on `stream`.  Its work space (split rows'
  * partial sums) is allocated by the context's first such call, has one size
  * for good and is shared by all of them, captured ones too, so order them.

@@ -20,8 +20,12 @@
 // [2^7, 2^8), undone in the score's factor; V's exponent is that of the largest
 // scale met so far, and O is rescaled when it grows.
 // The softmax rescales O only when a row's maximum has grown by more than 2^8
-// since the last time (P <= 2^8 then, well inside fp16, and the final quotient
-// is the same), so O is hardly ever read back before the end.
+// since the last time (the final quotient is the same), so O is hardly ever read
+// back before the end.  P stands 2^7 above its value for that maximum: it is 2^15
+// at most, inside fp16, and keeps its 11 bits down to weights of 2^-21 of the
+// largest; below, it is off by 2^-32 of the largest at most, where a long row's
+// many small weights beside a great one would otherwise vanish.  The sum is
+// formed under the same factor, which lse and the parts' maxima take back.
 // What bounds it: with many query rows the chain of a half's job, softmax and then
 // its two products, against the other half's (2048 tokens of 40 heads over 16384
 // rows: 621 us, 1.11 PFLOP/s, 58 % of a plain matrix product's rate; the products
@@ -55,6 +59,7 @@ constexpr int SLOTS = 4;
 // needed, and eight make the place a mask.
 constexpr int KFACS = 8;
 constexpr float GROW = 8.f; // log2 growth of a maximum that is let pass before O is rescaled
+constexpr float LIFT = 7.f; // log2 of P at the reference maximum: P <= 2^(GROW + LIFT), inside fp16
 
 enum Bar { KF0, KF1, KE0, KE1, VF0, VF1, VE0, VE1, SF0, SF1, PF0, PF1, OD0, OD1, XF0, XF1, XF2, XF3, DRAIN, N_BARS };
 
@@ -477,7 +482,7 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
                         tm_st32(O + c * 32, v);
                     }
                 }
-                const float use = mx == -INFINITY ? 0.f : mx;
+                const float use = mx == -INFINITY ? 0.f : mx - LIFT;
                 if (!masked && !reported) {
                     sum += row_exp<false>(S, 0, sc, f, use, [](int, const float(&)[32]) {});
                 } else {
@@ -547,6 +552,7 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
                 mx = M;
                 two = true;
             }
+            mx -= LIFT; // what the sum's terms are relative to
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
             auto head_of = [&](int row) {
                 const int m = m0 + row, t = token_of(p, m), j = m - t * p.r;

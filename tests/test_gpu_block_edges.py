@@ -159,3 +159,44 @@ def test_infinite_value_of_a_row_of_little_weight(kernel, T, act):
             assert bool(torch.isfinite(o).all())
     finally:
         tw.close()
+
+
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("T", [1, 70, 9728])
+@pytest.mark.parametrize("nats", [14, 16, 17, 20])
+@pytest.mark.parametrize("kernel", [MMA, TC])
+def test_many_small_weights_beside_a_great_one(kernel, nats, T, act):
+    """An attention sink: the first row's score lies `nats` above those of 32767 others, which hold most of the values.
+    With the most tokens a work item walks all rows, so that every small weight is formed beside the great one.
+
+    Off by: half a step of the result and of P (2^-11 each: weights may be rounded alike, so nothing averages out); P below
+    its normal range, 2^-32 of the largest weight a row; the exponential (2^-22) and the scores' sums, (D + 4) 2^-24 of
+    |q| |k| = nats + 1, twice; a chain of n / 16 sums of positive numbers in the products, each losing at most 2^-23 of
+    what is summed there (the denominator's is shorter)."""
+    n, H, Hk, D = 32768, 4, 2, 64
+    rng = np.random.default_rng(nats)
+    k, v = np.zeros((n, Hk, D), np.float32), (0.5 + rng.random((n, Hk, D))).astype(np.float32)
+    k[:, :, 1] = rng.integers(-8, 9, (n, Hk)) / 16.0
+    k[0, :, 0], k[0, :, 1], v[0] = nats, 0, 2.0**-9
+    tw = _twin("f16", H, Hk, D, n + 64, page=256)
+    try:
+        tw.gpu.append(0, 0, 0, _tensor(k), _tensor(v))
+        few = min(T, 7)  # different tokens
+        q = np.zeros((few, H, D), np.float32)
+        q[:, :, 0], q[:, :, 1] = 1.0, np.linspace(-1, 1, few * H).reshape(few, H)
+        qt = _tensor(q, act)
+        got, z = _attend(tw, kernel, [0], [T], qt.repeat(-(-T // few), 1, 1)[:T].contiguous(), 1.0)
+        K, V = k.astype(np.float64), v.astype(np.float16).astype(np.float64)
+        want, wz, mag, _ = cross(qt.double().cpu().numpy(), K, V, 1.0, np.full(few, n))
+        half = {"f16": 2.0**-11, "bf16": 2.0**-8}[act]
+        score = 2.0**-22 + (nats + 1) * (D + 4) * 2.0**-24
+        sums = n / 16 * 2.0**-23
+        lim = mag * (half + 2.0**-11 + 2 * score + sums) + n * 2.0**-32 * np.abs(V).max()
+        got, z = got.double().cpu().numpy(), z.double().cpu().numpy()
+        for t in range(0, T, few):
+            m = min(few, T - t)
+            err = np.abs(got[t:t + m] - want[:m])
+            assert np.all(err <= lim[:m]), "off by %.3g, %.2f of its bound" % (err.max(), (err / lim[:m]).max())
+            assert np.abs(z[t:t + m] - wz[:m]).max() <= score + sums + 2.0**-23 * 2 * nats
+    finally:
+        tw.close()
