@@ -136,18 +136,20 @@ static bool plan_block(BlockParams &p, int sms, bool tc) {
     return narrow;
 }
 
-// Which kernel attends a sequence of 16-bit queries.  The tcgen05 kernel rounds code * scale to 11 bits: from TC_MIN_ROWS
-// rows on the log-sum-exp, an average over them, is as exact as 32 bits need (halves lose nothing).  It pays where a
-// call has enough to do, by its cached values (rows x KV heads x D) or its products (times query rows of a KV head):
-// measured in us, mma.sync against tcgen05, q8_0, bf16 queries, heads/KV heads/D:
-//   8/2/64,  1024 rows:   1 token   9.2 / 10.6,  256 tokens 14.0 / 18.0    (2^17 values, 2^27 products)
-//   8/2/64,  16384 rows:  1 token  20.6 / 17.5                             (2^21 values)
-//   40/8/128, 256 rows:  64 tokens 15.8 / 17.4,  256 tokens 24.0 / 18.2    (2^18 values; 2^26, 2^28 products)
-//   40/8/128, 4096 rows:  1 token  17.9 / 16.5,  256 tokens 203 / 46       (2^22 values)
+// Which kernel attends a sequence of 16-bit queries (both hold scores to 32 bits).  The tcgen05 kernel pays where a call
+// has enough to do, by its cached values (rows x KV heads x D) or its products (times query rows of a KV head); and in
+// such a call for the sequences that have TC_MIN_ROWS rows or enough products of their own: an item of few tokens over
+// fewer rows is all start.  Measured in us, mma.sync against tcgen05, q8_0, bf16 queries, heads/KV heads/D:
+//   8/2/64,  1024 rows:   1 token   8.8 / 11.3,  256 tokens 14.0 / 19.4    (2^17 values, 2^27 products)
+//   8/2/64,  16384 rows:  1 token  20.4 / 17.9                             (2^21 values)
+//   40/8/128, 256 rows:  64 tokens 14.4 / 20.2,  256 tokens 21.5 / 20.3    (2^18 values; 2^26, 2^28 products)
+//   40/8/128, 4096 rows:  1 token  17.1 / 17.5,  256 tokens 173 / 53       (2^22 values)
+//   32/8/128, 64 sequences of 100 rows, 1 token each 19.2 / 58.3,  32 of 200 rows, 4 tokens each 15.1 / 36.7
+//   40/8/128, 200 rows:  64 tokens 16.3 / 21.6,  512 tokens 41.2 / 24.3    (2^26, 2^29 products)
 constexpr int TC_MIN_ROWS = 256;
 constexpr double TC_VALUES = 1 << 21, TC_PRODUCTS = 1 << 28;
 static bool tc_pays(double values, double products) { return values >= TC_VALUES || products >= TC_PRODUCTS; }
-static bool use_tc(int type_k, int rows) { return type_k == KVC_F16 || rows >= TC_MIN_ROWS; }
+static bool use_tc(int rows, double products) { return rows >= TC_MIN_ROWS || products >= TC_PRODUCTS; }
 
 // Checks that the block operators share; *total: tokens of the block.
 static int block_check(Ctx *c, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_q, int act, const void *q,
@@ -221,12 +223,14 @@ extern "C" int kvc_attn_cross(kvc_ctx *cc, int layer, int n_seq, const int32_t *
     KVC_CU(c, cudaSetDevice(c->dev));
     if ((rc = ensure_block_space(c, st))) return rc;
     const int64_t cap = part_rows_cap(c->sms);
+    auto products_of = [&](int i) {
+        return (double)c->seqs[(size_t)seq_ids[i]].lfill[(size_t)layer] * c->Hk * c->D * c->r * n_q[i];
+    };
     double values = 0, products = 0;
     for (int i = 0; i < n_seq; ++i) {
         if (n_q[i] == 0) continue;
-        const double v = (double)c->seqs[(size_t)seq_ids[i]].lfill[(size_t)layer] * c->Hk * c->D;
-        values += v;
-        products += v * c->r * n_q[i];
+        values += (double)c->seqs[(size_t)seq_ids[i]].lfill[(size_t)layer] * c->Hk * c->D;
+        products += products_of(i);
     }
     const bool pays = act != KVC_ACT_F32 && (c->block_kernel ? c->block_kernel == 2 : tc_pays(values, products));
     for (int tc = 0; tc < 2; ++tc) { // the sequences of either kernel, as many a launch as it carries
@@ -242,7 +246,7 @@ extern "C" int kvc_attn_cross(kvc_ctx *cc, int layer, int n_seq, const int32_t *
         for (int i = 0; i < n_seq; ++i) {
             const Seq &sq = c->seqs[(size_t)seq_ids[i]];
             const int32_t rows = sq.lfill[(size_t)layer];
-            if (n_q[i] > 0 && (pays && (c->block_kernel || use_tc(c->tk, rows))) == (tc != 0)) {
+            if (n_q[i] > 0 && (pays && (c->block_kernel || use_tc(rows, products_of(i)))) == (tc != 0)) {
                 BlockSeq &s = p.seq[p.n_seq++];
                 s.id = seq_ids[i];
                 s.off = sq.off;

@@ -63,12 +63,17 @@ constexpr int CROSS_TC_TILE_N = 128;
 
 // A kernel's dynamic shared memory, allowed once in every CUDA context (one
 // of these per kernel; threads may come at once: the worst is a second call).
+// regs: registers that its roles share out, 0 for none: with fewer at launch
+// they would wait for them forever, so that such a build is refused.
 struct SharedMemory {
     std::atomic<uint64_t> ctx{0};
-    cudaError_t allow(const void *kernel, int bytes) {
+    cudaError_t allow(const void *kernel, int bytes, int regs = 0) {
         const uint64_t id = current_context_id();
         if (id && ctx.load(std::memory_order_acquire) == id) return cudaSuccess;
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        cudaFuncAttributes a;
+        cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+        if (e == cudaSuccess && a.numRegs < regs) e = cudaErrorInvalidConfiguration;
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e == cudaSuccess) ctx.store(id, std::memory_order_release);
         return e;
     }

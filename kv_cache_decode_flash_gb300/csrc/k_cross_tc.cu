@@ -2,9 +2,9 @@
 // generation's tensor cores (tcgen05): same items, masks and results as
 // k_cross.cu, whose comment has the definition.
 //
-// One CTA per SM, 17 warps: two groups of four softmax warps (one thread owns a
-// query row), four warps that bring the rows' K and four that bring their V, one
-// thread that issues the products.  Steps are 128 cached rows:
+// One CTA per SM: two groups of four softmax warps (one thread owns a query row),
+// four warps that bring the rows' K (eight for codes) and four that bring their V,
+// and a group of four of which one thread issues the products.  Steps are 128 cached rows:
 //   S = Q K^T    128 x 128 x D, both operands fp16 in shared memory, S in TMEM;
 //   O += P V     P (fp16) written over S in TMEM, V from shared memory, O stays in TMEM.
 // Two jobs are always in flight, so that one's softmax runs under the other's
@@ -13,9 +13,13 @@
 // steps run apart, with sums of their own that are joined at the end.
 //
 // What comes from the cache is turned into fp16 on the way to shared memory:
-// halves as they are (cp.async), codes times their block's scale, rounded once
-// to 11 bits (a choice that fits results of 8 or 11 bits; P is rounded to as
-// many).  Scales may lie anywhere in fp16's range, their products need not: a
+// halves as they are (cp.async), codes times their block's scale.  Of V those
+// products are rounded once to 11 bits (a choice that fits results of 8 or 11
+// bits; P is rounded to as many).  K they leave whole, as two fp16 parts that hold
+// the 18 bits: scores make the log-sum-exp, a result of 32 bits, whose error from
+// 11 bits of K was 2e-4 for tokens of few rows and 3e-3 for peaked softmaxes, and
+// every row weight formed from it was off by as much.  Both parts are multiplied
+// with Q into the same scores.  Scales may lie anywhere in fp16's range, their products need not: a
 // step's K is scaled by a power of two that brings its largest scale to
 // [2^7, 2^8), undone in the score's factor; V's exponent is that of the largest
 // scale met so far, and O is rescaled when it grows.
@@ -41,15 +45,19 @@ namespace {
 
 constexpr int TM = 128;      // query rows of a half
 constexpr int TN = 128;      // cached rows of a step
-constexpr int THREADS = 5 * GROUP; // roles: softmax of half 0, of half 1, K, V; then the issuing warp
-// Registers: a launch gives every thread 96.  The loading groups and the issuing warp's hand some back (those that turn
+// Roles by groups of four warps: softmax of half 0, of half 1, K, V, then the issuing thread's.  K's codes have two groups:
+// one takes about 2200 cycles to form a tile, and there are two a step (5 tokens over 131072 rows: 199 us by one, 139 by two).
+template <bool CODES> constexpr int K_GROUPS = CODES ? 2 : 1;
+template <bool CODES> constexpr int THREADS = (4 + K_GROUPS<CODES>) * GROUP;
+// Registers: a launch gives every thread LAUNCH.  The loading groups and the issuing thread's hand some back (those that turn
 // codes into values need more), the softmax groups take them, so that a thread holds all or half of its row's 128 scores.  (No function of
-// theirs may stay a call: its registers would have to fit the smallest role's.)
-constexpr int R_MMA = 24;
+// theirs may stay a call: its registers would have to fit the smallest role's.)  Few are to spare: shared memory leaves
+// spilled ones next to no cache (V's codes by two groups as well, with 72 a thread at launch: 139 to 199 us).
 template <bool CODES> struct Regs {
-    static constexpr int SOFT = CODES ? 152 : 184, LOAD = CODES ? 72 : 40;
+    static constexpr int LAUNCH = CODES ? 80 : 96;
+    static constexpr int SOFT = CODES ? 136 : 184, K = CODES ? 56 : 40, V = CODES ? 72 : 40, MMA = 24;
     static constexpr int HOLD = CODES ? 2 : 4; // blocks of 32 scores that a softmax thread keeps
-    static_assert(2 * SOFT + 2 * LOAD + R_MMA <= 5 * 96, "the roles' registers come from the launch's");
+    static_assert(2 * SOFT + K_GROUPS<CODES> * K + V + MMA <= THREADS<CODES> / GROUP * LAUNCH, "the roles' registers come from the launch's");
 };
 // Steps whose places, V exponents and reports are kept.  The V loaders write those of step s + 1 once P V of step s - 2 is
 // done, before which the softmax groups are through with step s - 3.
@@ -61,12 +69,19 @@ constexpr int KFACS = 8;
 constexpr float GROW = 8.f; // log2 growth of a maximum that is let pass before O is rescaled
 constexpr float LIFT = 7.f; // log2 of P at the reference maximum: P <= 2^(GROW + LIFT), inside fp16
 
-enum Bar { KF0, KF1, KE0, KE1, VF0, VF1, VE0, VE1, SF0, SF1, PF0, PF1, OD0, OD1, XF0, XF1, XF2, XF3, DRAIN, N_BARS };
+enum Bar { KF0, KF1, KF2, KF3, KE0, KE1, KE2, KE3, VF0, VF1, VE0, VE1, SF0, SF1, PF0, PF1, OD0, OD1, XF0, XF1, XF2, XF3, DRAIN, N_BARS };
 
-template <int D> struct Lay {
+// A step's K is one tile, or with codes two, its values' first and second parts, which take the K tiles' places in turn.
+template <int D, bool CODES> struct Lay {
     static constexpr int REG = TN * 128;          // a region: 128 rows of 64 fp16, 128-byte swizzled
     static constexpr int TILE = D / 64 * REG;     // bytes of a 128-row tile of fp16
-    static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, AUX = 6 * TILE;
+    static constexpr int PARTS = CODES ? 2 : 1;
+    static constexpr int K_TILES = CODES && D == 64 ? 4 : 2; // (D 128 has room for no more)
+    static constexpr int Q = 0, K = 2 * TILE, V = K + K_TILES * TILE, AUX = V + 2 * TILE;
+    // a query tile of one half leaves the other half's place free: one more for K
+    static constexpr int MORE = CODES && D == 128 ? 1 : 0;
+    __device__ static __forceinline__ int k_tiles(bool wide) { return K_TILES + (wide ? 0 : MORE); }
+    __device__ static __forceinline__ int k(bool wide) { return K - (wide ? 0 : MORE) * TILE; }
 };
 
 struct Aux {
@@ -90,26 +105,29 @@ __device__ __forceinline__ bool any_bad(const uint32_t (&rows)[TN / 32]) {
     return (b.x | b.y | b.z | b.w) != 0;
 }
 
-template <int D> constexpr int smem_bytes() {
+template <int D, bool CODES> constexpr int smem_bytes() {
     // TMEM is allocated whole: one CTA per SM, whatever D
-    const int need = Lay<D>::AUX + (int)sizeof(Aux) + 2 * TM * (D / 16) * 4 + 1024;
+    const int need = Lay<D, CODES>::AUX + (int)sizeof(Aux) + 2 * TM * (D / 16) * 4 + 1024;
     return need > 120 * 1024 ? need : 120 * 1024;
 }
 
 // ------------------------------------------------------------- loading ----
-// A loading group's work: tensor T's rows of every step (IS_V: V, else K) into its two stages.
+// A loading group's work: tensor T's rows of every step (IS_V: V, else K) into its n_tiles stages (two, but for K's codes).
 template <int D, int T, bool IS_V>
-__device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &q, int g, uint8_t *tiles, Aux &x, int r0, int r_end,
-                                          int t) {
+__device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &q, int g, uint8_t *tiles, int n_tiles, Aux &x, int r0,
+                                          int r_end, int t) {
+    constexpr bool TWO = !IS_V && T != KVC_F16; // a step is two tiles
+    constexpr int TILE = Lay<D, TWO>::TILE;
     const uint8_t *data = IS_V ? p.vdata : p.kdata;
     uint64_t *full = &x.bar[IS_V ? VF0 : KF0], *empty = &x.bar[IS_V ? VE0 : KE0];
     int32_t(*row)[TN] = x.row[IS_V];
     int steps = 1 << 24, vis_min = 0; // known with the query rows
-    constexpr int SYNC = IS_V ? 4 : 3;
-    int32_t next = -1; // the pool row of the step whose rows the group gets next, looked up a step before
-    auto look_up = [&](int s) { next = s < steps ? pool_row(p, q, g, r0 + s * TN + t) : -1; };
+    constexpr int SYNC = IS_V ? 4 : 3, NT = IS_V ? GROUP : K_GROUPS<TWO> * GROUP; // threads
+    const bool has_row = NT == TN || t < TN;   // whose place and scales it sees to
+    Lookup next; // of the step whose rows the group gets next
+    auto look_up = [&](int s) { next.ask(p, q, r0 + s * TN + t, has_row && s < steps); };
     auto find = [&](int s) { // for all threads after the next barrier
-        row[s % SLOTS][t] = next;
+        if (has_row) row[s % SLOTS][t] = next.row(p, g);
         look_up(s + 1);
     };
     auto clear = [&](int s) { // a step's reports; the slot's last step, four before, is done with (its V was used up)
@@ -123,10 +141,11 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
         vis_min = x.vis_min;
     };
 #pragma unroll
-    for (int k = 0; k < 3; ++k) row[k][t] = pool_row(p, q, g, r0 + k * TN + t);
+    for (int k = 0; k < 3; ++k)
+        if (has_row) row[k][t] = pool_row(p, q, g, r0 + k * TN + t);
     look_up(3);
     clear(0);
-    named_sync<SYNC, GROUP>();
+    named_sync<SYNC, NT>();
     if constexpr (T == KVC_F16) {
         // A step's copies are under way while those of the step before are waited for, if their stage is free by then;
         // a step that has landed is not held back for a stage.
@@ -140,7 +159,7 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
             bool ahead = false;
             if (s < steps) {
                 ahead = s < 2 || bar_try(&empty[s & 1], ((s >> 1) - 1) & 1);
-                if (ahead && s > 0) copy_halves<D>(tiles + (s & 1) * Lay<D>::TILE, data, row[s % SLOTS], t);
+                if (ahead && s > 0) copy_halves<D>(tiles + (s & 1) * TILE, data, row[s % SLOTS], t);
                 if (!IS_V && t == 0) x.kfac[s % KFACS] = 1.f;
             }
             if (s > 0) {
@@ -149,29 +168,29 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
                 else
                     asm volatile("cp.async.wait_group 0;" ::: "memory");
                 if (IS_V && r0 + s * TN > vis_min)
-                    drop_halves<D>(tiles + ((s - 1) & 1) * Lay<D>::TILE, x.badrow[(s - 1) % SLOTS], t);
+                    drop_halves<D>(tiles + ((s - 1) & 1) * TILE, x.badrow[(s - 1) % SLOTS], t);
                 fence_async();
                 bar_arrive(&full[(s - 1) & 1]);
             }
             if (s < steps && !ahead) {
                 bar_wait(&empty[s & 1], ((s >> 1) - 1) & 1, p.err, &x.abort);
-                copy_halves<D>(tiles + (s & 1) * Lay<D>::TILE, data, row[s % SLOTS], t);
+                copy_halves<D>(tiles + (s & 1) * TILE, data, row[s % SLOTS], t);
             }
             find(s + 3);
             clear(s + 1);
-            named_sync<SYNC, GROUP>();
+            named_sync<SYNC, NT>();
         }
     } else {
         // A thread's piece of the next step is requested as soon as this step's is stored.  It looks after one row's
         // scales too, a step earlier: the largest scale, which gives a step its exponent, is known before the step's turn.
-        using C = Codes<D, T>;
+        using C = Codes<D, T, NT>;
         const int c = t % C::PIECES, j0 = t / C::PIECES;
         const uint8_t *codes = data + c * 16;
         const uint16_t *scales = IS_V ? p.vs : p.ks;
         uint32_t a[4];
         constexpr bool f = false; // (avoiding the stores' bank conflicts costs more instructions here than it saves)
         C::places(j0, c, a, f);
-        uint4 u[C::PIECES];
+        uint4 u[C::MINE];
         uint32_t sc[D / 64];
         auto at_row = [&](int s, int j) { return max(row[s % SLOTS][j], 0); };
         int E = E_MIN;
@@ -179,7 +198,7 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
             uint32_t m = 0;
             const bool in = r0 + s * TN + t < q.n_rows; // a row past the end: scales 0
 #pragma unroll
-            for (int k = 0; k < D / QK; ++k) {
+            for (int k = 0; has_row && k < D / QK; ++k) {
                 uint32_t h = sc[k >> 1] >> (16 * (k & 1)) & 0xffffu;
                 if (!in) h = 0;
                 if ((h & 0x7fffu) < 0x7c00u) {
@@ -191,10 +210,10 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
                 x.scale[IS_V][s & 1][t * (D / QK) + k] = (uint16_t)h;
             }
             m = __reduce_max_sync(0xffffffffu, m);
-            if ((t & 31) == 0) x.red[IS_V][s & 1][t >> 5] = m;
+            if (has_row && (t & 31) == 0) x.red[IS_V][s & 1][t >> 5] = m;
             find(s + 3);
             clear(s + 1);
-            named_sync<SYNC, GROUP>();
+            named_sync<SYNC, NT>();
             const uint4 r = *reinterpret_cast<const uint4 *>(x.red[IS_V][s & 1]);
             const uint32_t top = max(max(r.x, r.y), max(r.z, r.w));
             const int e = top ? ilogbf(__half2float(__ushort_as_half((uint16_t)top))) : E_MIN;
@@ -208,28 +227,62 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
                 }
             }
         };
-        C::load(sc, scales, at_row(0, t));
+        if (has_row) C::load(sc, scales, at_row(0, t));
 #pragma unroll
-        for (int i = 0; i < C::PIECES; ++i) C::load(u[i], codes, at_row(0, j0 + i * C::ROWS));
+        for (int i = 0; i < C::MINE; ++i) C::load(u[i], codes, at_row(0, j0 + i * C::ROWS));
         begin();
         if (steps == 0) return;
         exponent(0);
-        C::load(sc, scales, at_row(1, t));
+        if (has_row) C::load(sc, scales, at_row(1, t));
+        int place = 0, use = 0; // TWO: of the next tile, and how often the places have been used
         for (int s = 0; s < steps; ++s) {
-            if (s >= 2) bar_wait(&empty[s & 1], ((s >> 1) - 1) & 1, p.err, &x.abort);
             const float up = ldexpf(1.f, 7 - E);
-            uint8_t *tile = tiles + (s & 1) * Lay<D>::TILE;
             const uint16_t *d = &x.scale[IS_V][s & 1][j0 * (D / QK) + (T == KVC_Q4_0 ? c : c / 2)];
+            if constexpr (TWO) {
+                // (scales and rows first: a shared load would wait for the stores before it)
+                __half2 ds[C::MINE];
+                int32_t next_row[C::MINE];
 #pragma unroll
-            for (int i = 0; i < C::PIECES; ++i) {
-                C::store(tile + i * C::ROWS * 128, a, u[i], scaled(d[i * C::ROWS * (D / QK)], up), f);
-                C::load(u[i], codes, at_row(s + 1, j0 + i * C::ROWS)); // (behind the last step: a row that is there)
+                for (int i = 0; i < C::MINE; ++i) {
+                    ds[i] = scaled(d[i * C::ROWS * (D / QK)], up);
+                    next_row[i] = at_row(s + 1, j0 + i * C::ROWS);
+                }
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    if (use > 0) bar_wait(&empty[place], (use - 1) & 1, p.err, &x.abort);
+                    uint8_t *tile = tiles + place * TILE;
+#pragma unroll
+                    for (int i = 0; i < C::MINE; ++i) {
+                        if (part == 0) {
+                            C::store(tile + i * C::ROWS * 128, a, u[i], ds[i], f);
+                        } else {
+                            // (opaque: the first part's values are formed again, there are no registers to keep them)
+                            asm volatile("" : "+r"(u[i].x), "+r"(u[i].y), "+r"(u[i].z), "+r"(u[i].w));
+                            C::store_rest(tile + i * C::ROWS * 128, a, u[i], ds[i], f);
+                            C::load(u[i], codes, next_row[i]); // (behind the last step: a row that is there)
+                        }
+                    }
+                    fence_async();
+                    bar_arrive(&full[place]);
+                    if (++place == n_tiles) {
+                        place = 0;
+                        ++use;
+                    }
+                }
+            } else {
+                if (s >= 2) bar_wait(&empty[s & 1], ((s >> 1) - 1) & 1, p.err, &x.abort);
+                uint8_t *tile = tiles + (s & 1) * TILE;
+#pragma unroll
+                for (int i = 0; i < C::MINE; ++i) {
+                    C::store(tile + i * C::ROWS * 128, a, u[i], scaled(d[i * C::ROWS * (D / QK)], up), f);
+                    C::load(u[i], codes, at_row(s + 1, j0 + i * C::ROWS)); // (behind the last step: a row that is there)
+                }
+                fence_async();
+                bar_arrive(&full[s & 1]);
             }
-            fence_async();
-            bar_arrive(&full[s & 1]);
             if (s + 1 < steps) {
                 exponent(s + 1);
-                C::load(sc, scales, at_row(s + 2, t));
+                if (has_row) C::load(sc, scales, at_row(s + 2, t));
             }
         }
     }
@@ -283,14 +336,13 @@ __device__ __forceinline__ float row_scores(uint32_t S, int n, uint32_t (&r)[HOL
 }
 
 // exp2 of the scores (times f, less use; f >= 0, an unseen one is -inf) as fp16 pairs over them; returns their sum.
-// mark(c, v): a look at the 32 weights of column block c.
+// mark(c, rows): a look at which of column block c's 32 rows have weight (MASK).
 template <bool MASK, int HOLD, class Mark>
 __device__ __forceinline__ float row_exp(uint32_t S, int n, uint32_t (&r)[HOLD][32], float f, float use, Mark mark) {
     const uint64_t ff = pair(f, f), mm = pair(-use, -use);
     uint64_t a0 = 0, a1 = 0;
     auto block = [&](int c, const uint32_t(&x)[32]) {
-        float v[32];
-        uint32_t w[16];
+        uint32_t w[16], some = 0; // MASK: the rows that have weight
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
             float2 y = unpair(fma2(pair(x[e], x[e + 1]), ff, mm));
@@ -298,15 +350,16 @@ __device__ __forceinline__ float row_exp(uint32_t S, int n, uint32_t (&r)[HOLD][
                 y.x = c * 32 + e < n ? y.x : -INFINITY;
                 y.y = c * 32 + e + 1 < n ? y.y : -INFINITY;
             }
-            v[e] = ex2(y.x);
-            v[e + 1] = ex2(y.y);
-            w[e / 2] = h2(v[e], v[e + 1]);
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+            if (MASK) some |= (y.x > 0.f ? 1u << e : 0u) | (y.y > 0.f ? 2u << e : 0u);
+            w[e / 2] = h2(y.x, y.y);
             if (e & 2)
-                a1 = add2(a1, pair(v[e], v[e + 1]));
+                a1 = add2(a1, pair(y.x, y.y));
             else
-                a0 = add2(a0, pair(v[e], v[e + 1]));
+                a0 = add2(a0, pair(y.x, y.y));
         }
-        mark(c, v);
+        if (MASK) mark(c, some);
         tm_st16(S + c * 16, w);
     };
     if constexpr (HOLD == 4) {
@@ -328,8 +381,10 @@ __device__ __forceinline__ float row_exp(uint32_t S, int n, uint32_t (&r)[HOLD][
 }
 
 template <int D, int KT, int VT>
-__global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_constant__ BlockParams p) {
-    using L = Lay<D>;
+__global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(const __grid_constant__ BlockParams p) {
+    constexpr bool CODES = KT != KVC_F16;
+    using L = Lay<D, CODES>;
+    using R = Regs<CODES>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u); // swizzled tiles need 1024-byte alignment
     Aux &x = *reinterpret_cast<Aux *>(smem + L::AUX);
@@ -343,11 +398,12 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
     const int g = unit / q.tiles, tile = q.tiles - 1 - unit % q.tiles; // later tokens see more: they begin first
     const int m_all = q.n_tok * p.r, m0 = tile * 2 * TM, mrows = min(2 * TM, m_all - m0);
     const bool wide = mrows > TM;
+    constexpr int WK = 8, WV = WK + 4 * K_GROUPS<CODES>, WI = WV + 4; // first warps of K's, V's and the issuing role
 
     if (tid == 0) {
         for (int i = 0; i < N_BARS; ++i) {
-            const bool load = i == KF0 || i == KF1 || i == VF0 || i == VF1;
-            bar_init(&x.bar[i], load || i == PF0 || i == PF1 ? GROUP : 1);
+            const bool load = (i >= KF0 && i <= KF3) || i == VF0 || i == VF1;
+            bar_init(&x.bar[i], load || i == PF0 || i == PF1 ? (i <= KF3 ? K_GROUPS<CODES> : 1) * GROUP : 1);
         }
         x.vis_max = 0;
         x.vis_min = 0x7fffffff;
@@ -362,19 +418,19 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
     }
     __syncthreads();
     const int r0 = part * q.split_rows, r_end = parts == 1 ? q.n_rows : min(r0 + q.split_rows, q.n_rows);
-    if (warp >= 8 && warp < 12) {
-        regs_dec<Regs<KT != KVC_F16>::LOAD>();
-        load_rows<D, KT, false>(p, q, g, smem + L::K, x, r0, r_end, tid - 2 * GROUP);
+    if (warp >= WK && warp < WV) {
+        regs_dec<R::K>();
+        load_rows<D, KT, false>(p, q, g, smem + L::k(wide), L::k_tiles(wide), x, r0, r_end, tid - WK * 32);
         return;
-    } else if (warp >= 12 && warp < 16) {
-        regs_dec<Regs<KT != KVC_F16>::LOAD>();
-        load_rows<D, VT, true>(p, q, g, smem + L::V, x, r0, r_end, tid - 3 * GROUP);
+    } else if (warp >= WV && warp < WI) {
+        regs_dec<R::V>();
+        load_rows<D, VT, true>(p, q, g, smem + L::V, 2, x, r0, r_end, tid - WV * 32);
         return;
     }
     // The other warps see to the query rows: a warp each, QR of its rows under way together, normalised by a power of two
     // that takes the scale's sign too; rows that are not there are zero.
     constexpr int QR = 6, QW = 12; // (the loading warps are at their first rows already)
-    const int qw = warp < 8 ? warp : warp - 8;
+    const int qw = warp < 8 ? warp : warp - WI + 8;
     for (int mb = qw; mb < mrows; mb += QW * QR) {
         Query<D> y[QR];
 #pragma unroll
@@ -429,7 +485,7 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
 
     if (warp < 8) {
         // -------------------------------------------------- softmax of half h
-        regs_inc<Regs<KT != KVC_F16>::SOFT>();
+        regs_inc<R::SOFT>();
         const int h = warp >> 2, mr = wide ? tid : (tid & 127);
         const uint32_t lanes = (uint32_t)(warp & 3) << 21; // TMEM lane 32 * (warp % 4)
         const uint32_t S = tS + h * 128 + lanes, O = tO + h * D + lanes;
@@ -447,7 +503,7 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
             if (live) {
                 const bool masked = base + TN > wvis;
                 const float f = cq * x.kfac[s % KFACS];
-                constexpr int HOLD = Regs<KT != KVC_F16>::HOLD;
+                constexpr int HOLD = R::HOLD;
                 uint32_t sc[HOLD][32];
                 const float raw = masked ? row_scores<true>(S, vis - base, sc) : row_scores<false>(S, 0, sc);
                 const float top = raw == -INFINITY ? raw : raw * f;
@@ -484,19 +540,16 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
                 }
                 const float use = mx == -INFINITY ? 0.f : mx - LIFT;
                 if (!masked && !reported) {
-                    sum += row_exp<false>(S, 0, sc, f, use, [](int, const float(&)[32]) {});
+                    sum += row_exp<false>(S, 0, sc, f, use, [](int, uint32_t) {});
                 } else {
-                    sum += row_exp<true>(S, vis - base, sc, f, use, [&](int c, const float(&v)[32]) {
+                    sum += row_exp<true>(S, vis - base, sc, f, use, [&](int c, uint32_t some) {
                         const uint32_t rows = x.badrow[slot][c];
                         if (rows == 0) return;
 #pragma unroll 1
                         for (int e = 0; e < 32; ++e) {
                             if (!(rows >> e & 1)) continue;
-                            float pe = 0.f; // the row's weight: 0 where it is not seen
-#pragma unroll
-                            for (int y = 0; y < 32; ++y) pe = y == e ? v[y] : pe;
                             const int32_t R = pool_row(p, q, g, base + c * 32 + e);
-                            if (mr < mrows && pe > 0.f && R >= 0) {
+                            if (mr < mrows && (some >> e & 1) && R >= 0) {
                                 mark_poison<D, VT>(poison[mr], p.vdata, p.vs, R);
                                 x.any_bad = 1;
                             }
@@ -560,7 +613,7 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
             };
             constexpr int SP = 36; // floats of a staging row: 16 bytes off a multiple of 128
             float *stage = join + (wide ? 0 : TM * JP) + (warp & (wide ? 7 : 3)) * (32 * SP);
-            static_assert((TM * JP + 4 * 32 * SP) * 4 <= 4 * L::TILE && 8 * 32 * SP * 4 <= 4 * L::TILE, "within the K and V tiles");
+            static_assert((TM * JP + 4 * 32 * SP) * 4 <= L::AUX - L::K && 8 * 32 * SP * 4 <= L::AUX - L::K, "within the K and V tiles");
             const bool bad = x.any_bad != 0;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -634,22 +687,37 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(TMEM_COLS));
         }
     } else {
-        regs_dec<R_MMA>();
-        if (warp > 16 || lane > 0) return;
+        regs_dec<R::MMA>();
+        if (warp > WI || lane > 0) return;
         // -------------------------------------------------- products
-        const uint32_t sq = smem_u32(smem + L::Q), sk = smem_u32(smem + L::K), sv = smem_u32(smem + L::V);
-        auto qk = [&](int i) { // job i's scores
-            const int s = wide ? i >> 1 : i, h = i & 1;
-            bar_wait(&x.bar[KF0 + (s & 1)], (s >> 1) & 1, p.err, &x.abort);
-            tc_after();
+        const int n_tiles = L::k_tiles(wide);
+        const uint64_t dq = desc(smem_u32(smem + L::Q), 16), dk = desc(smem_u32(smem + L::k(wide)), 16);
+        const uint32_t sv = smem_u32(smem + L::V);
+        int place = 0, odd = 0; // of the step's first K tile, and its barriers' phase
+        auto qk = [&](int i) {  // job i's scores
+            const int h = i & 1;
+            int at = place, phase = odd;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t o = (k >> 2) * L::REG + (k & 3) * 32;
-                mma_ss(tS + h * 128, desc(sq + (wide ? h * L::TILE : 0) + o, 16), desc(sk + (s & 1) * L::TILE + o, 16),
-                       inst(TN, false), k > 0);
+            for (int part = 0; part < L::PARTS; ++part) { // (the larger part first)
+                bar_wait(&x.bar[KF0 + at], phase, p.err, &x.abort);
+                tc_after();
+                const uint64_t a = dq + (uint32_t)(wide ? h * (L::TILE >> 4) : 0), b = dk + (uint32_t)(at * (L::TILE >> 4));
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t o = ((k >> 2) * L::REG + (k & 3) * 32) >> 4;
+                    mma_ss(tS + h * 128, a + o, b + o, inst(TN, false), part > 0 || k > 0);
+                }
+                if (part == L::PARTS - 1) tc_commit(&x.bar[SF0 + h]);
+                if (!wide || h) tc_commit(&x.bar[KE0 + at]);
+                if (++at == n_tiles) {
+                    at = 0;
+                    phase ^= 1;
+                }
             }
-            tc_commit(&x.bar[SF0 + h]);
-            if (!wide || h) tc_commit(&x.bar[KE0 + (s & 1)]);
+            if (!wide || h) {
+                place = at;
+                odd = phase;
+            }
         };
         if (jobs > 0) qk(0);
         if (jobs > 1) qk(1);
@@ -675,13 +743,14 @@ __global__ void __launch_bounds__(THREADS, 1) cross_tc_kernel(const __grid_const
 }
 
 template <int D, int KT, int VT> cudaError_t go(const BlockParams &p, cudaStream_t st) {
+    constexpr bool CODES = KT != KVC_F16;
     auto k = cross_tc_kernel<D, KT, VT>;
-    constexpr int bytes = smem_bytes<D>();
+    constexpr int bytes = smem_bytes<D, CODES>();
     static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
     static SharedMemory set;
-    cudaError_t e = set.allow((const void *)k, bytes);
+    cudaError_t e = set.allow((const void *)k, bytes, Regs<CODES>::LAUNCH);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)p.n_items, THREADS, bytes, st>>>(p);
+    k<<<(unsigned)p.n_items, THREADS<CODES>, bytes, st>>>(p);
     e = cudaGetLastError();
     return e == cudaSuccess ? launch_join(p, st) : e;
 }

@@ -34,8 +34,8 @@ namespace {
 constexpr int THREADS = 5 * GROUP; // roles: softmax of even and of odd steps, loading of even and odd steps, the issuing warp
 constexpr int TN = TC_M;           // cached rows of a step
 // Registers: a launch gives every thread 96; the summing groups take what the issuing warp's group hands back.
-constexpr int R_SUM = 128, R_MMA = 24;
-static_assert(2 * R_SUM + 2 * 96 + R_MMA <= 5 * 96, "the roles' registers come from the launch's");
+constexpr int R_LAUNCH = 96, R_SUM = 128, R_MMA = 24;
+static_assert(2 * R_SUM + 2 * R_LAUNCH + R_MMA <= 5 * R_LAUNCH, "the roles' registers come from the launch's");
 static_assert(WEIGHT_STEP == TN, "items are whole steps");
 
 enum Bar { KF0, KF1, KE0, KE1, SF0, SF1, SE0, SE1, QF, DRAIN, N_BARS };
@@ -390,7 +390,7 @@ template <int D, int KT, bool LO> cudaError_t go(const BlockParams &p, cudaStrea
     constexpr int bytes = smem_bytes<D, KT != KVC_F16, LO>();
     static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
     static SharedMemory set;
-    cudaError_t e = set.allow((const void *)k, bytes);
+    cudaError_t e = set.allow((const void *)k, bytes, R_LAUNCH);
     if (e != cudaSuccess) return e;
     k<<<(unsigned)p.n_items, THREADS, bytes, st>>>(p);
     return cudaGetLastError();

@@ -174,9 +174,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// Codes of one tensor: of every (128 / PIECES)-th row of a step a loading thread has one 16-byte piece.
-template <int D, int T> struct Codes {
-    static constexpr int RB = row_bytes<T>(D), PIECES = RB / 16, ROWS = GROUP / PIECES;
+// Codes of one tensor: of every ROWS-th row of a step one of NT loading threads has one 16-byte piece, MINE in all.
+template <int D, int T, int NT = GROUP> struct Codes {
+    static constexpr int RB = row_bytes<T>(D), PIECES = RB / 16, ROWS = NT / PIECES, MINE = TC_M / ROWS;
     static_assert(ROWS % 8 == 0, "a thread's rows share their swizzle");
     // volatile: a load is to be under way as long before its use as it stands here
     __device__ __forceinline__ static void load(uint4 &u, const uint8_t *at, int32_t R) {
@@ -199,6 +199,22 @@ template <int D, int T> struct Codes {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             a[k] = T == KVC_Q4_0 ? at(j, c * 32 + (k ^ (2 * f)) * 8) : at(j, c * 16 + ((k ^ f) & 1) * 8);
+    }
+    // what store() rounds away of values of 8-bit codes: exact in fp16, as the product of a code and d has 18 bits
+    __device__ __forceinline__ static void store_rest(uint8_t *dst, const uint32_t (&a)[4], const uint4 &u, __half2 d, bool f) {
+        static_assert(T == KVC_Q8_0, "codes of 8 bits");
+        auto put = [&](uint32_t o, uint2 x, uint2 y) {
+            const uint32_t in[4] = {x.x, x.y, y.x, y.y};
+            uint32_t r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __half2 c = *reinterpret_cast<const __half2 *>(&in[i]), z = __hfma2(c, d, __hneg2(__hmul2(c, d)));
+                r[i] = *reinterpret_cast<const uint32_t *>(&z);
+            }
+            *reinterpret_cast<uint4 *>(dst + o) = make_uint4(r[0], r[1], r[2], r[3]);
+        };
+        put(a[0], codes4(f ? u.z : u.x), codes4(f ? u.w : u.y));
+        put(a[1], codes4(f ? u.x : u.z), codes4(f ? u.y : u.w));
     }
     // values = codes * d, rounded once (d: the scale times a power of two); dst: the piece's row
     __device__ __forceinline__ static void store(uint8_t *dst, const uint32_t (&a)[4], const uint4 &u, __half2 d, bool f) {

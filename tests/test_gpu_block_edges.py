@@ -200,3 +200,50 @@ def test_many_small_weights_beside_a_great_one(kernel, nats, T, act):
             assert np.abs(z[t:t + m] - wz[:m]).max() <= score + sums + 2.0**-23 * 2 * nats
     finally:
         tw.close()
+
+
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("kind,D", [("q8", 64), ("q8", 128), ("q8q4", 128), ("f16", 128)])
+@pytest.mark.parametrize("sigma", [1.0, 8.0])
+@pytest.mark.parametrize("T", [9, 100])
+@pytest.mark.parametrize("kernel", [MMA, TC])
+def test_lse_holds_32_bits_whatever_a_token_sees(kernel, T, sigma, kind, D, act):
+    """The log-sum-exp of tokens that see one row, four, 64 and all of a long sequence, of flat and of peaked softmaxes, on
+    either kernel: within the bound of operands of 20 bits; and the rows' weights that are formed from it sum to one for every
+    query row that sees any, within the bounds of both."""
+    import torch
+
+    n, H, Hk, scale = 4096, 8, 2, float(np.float32(D**-0.5))
+    tw = _twin(kind, H, Hk, D, n + 64, page=256)
+    try:
+        k, v = kv_inputs(31, 0, n, Hk, D, sigma=0.5)
+        tw.append(0, 0, 0, k, v)
+        q = _tensor(np.random.default_rng(T).standard_normal((T, H, D)) * sigma, act)
+        vis = np.resize([1, 4, 64, n, 2, 1, 129, 0, 3000], T)
+        got, z = _attend(tw, kernel, [0], [T], q, scale, vis)
+        K, V = values(tw.ref.seqs[0].K[0]), values(tw.ref.seqs[0].V[0])
+        qd = q.double().cpu().numpy()
+        want, wz, mag, size = cross(qd, K, V, scale, vis)
+        bo, bz = cross_bound(mag, size, n, D, act, 20, 11)
+        zz = z.double().cpu().numpy()
+        seen = vis > 0
+        err = np.abs(zz[seen] - wz[seen])
+        assert np.all(err <= bz[seen]), "lse off by %.3g, %.2f of its bound" % (err.max(), (err / bz[seen]).max())
+        # out: P and V lose 11 bits each, K nothing.  A peaked softmax whose row holds a 0 leaves results of next to nothing:
+        # below f16's normal range (2^-14) a result is off by half of 2^-24, whatever its size, and the weights of at most n
+        # rows, where fp16 has no bits left for them, by 2^-32 of the largest each
+        out = np.abs(got.double().cpu().numpy() - want)
+        bo = bo + (2.0**-25 if act == "f16" else 0) + n * 2.0**-32 * np.abs(V).max()
+        assert np.all(out <= bo), "out off by %.3g, %.2f of its bound" % (out.max(), (out / bo).max())
+        w = torch.zeros(1, Hk, n, device="cuda:0")
+        nv = torch.from_numpy(vis.astype(np.int32)).to("cuda:0")
+        tw.gpu.attn_weight(0, [0], [T], q, z, w, scale, n_vis=nv)
+        total = w.double().sum(2).cpu().numpy()[0]
+        for g in range(Hk):
+            hs = slice(g * H // Hk, (g + 1) * H // Hk)
+            rows = seen.sum() * H // Hk
+            # each query row's weights: e^(lse's error), e^(a score's error) and the sums' (T r + 4) 2^-24
+            lim = (2 * bz[seen, hs]).sum() + rows * (T * H // Hk + 4) * 2.0**-24
+            assert abs(total[g] - rows) <= lim, "weights sum to %.6f of %d" % (total[g], rows)
+    finally:
+        tw.close()
