@@ -288,7 +288,8 @@ int kvc_seq_add(kvc_ctx *c, int seq, int p0, int p1, int delta);
  * w: device fp32 [n_head_kv][w_stride], w_stride at least the sequence's rows: the
  * weights move with their rows, and w[g][n' .. n) becomes 0, for rows to come.
  * *n_removed: rows removed.  Synchronous, like the other sequence operations.
- * Errors: KVC_EINVAL, KVC_ENOMEM, KVC_ECUDA. */
+ * With a device error reported by then (KVC_EINTERNAL) nothing has changed.
+ * Errors: KVC_EINVAL, KVC_ENOMEM, KVC_EINTERNAL, KVC_ECUDA. */
 int kvc_seq_evict_weight(kvc_ctx *c, int seq, int p0, int p1, int32_t n_remove, float *w, int64_t w_stride,
                          int32_t *n_removed);
 
@@ -459,6 +460,11 @@ int kvc_set_timeout_ms(kvc_ctx *c, int ms);
 /* Host-side fault injection for tests: the next `n` internal allocations
  * succeed and the ones after fail with KVC_ENOMEM; n < 0 disables it. */
 int kvc_debug_fail_alloc_after(kvc_ctx *c, int n);
+
+/* Test hook: set the device error word as if a kernel had reported `word`
+ * (kvc_check_device_error reads and clears it).  Device-resident contexts only.
+ * Errors: KVC_EINVAL, KVC_ECUDA. */
+int kvc_debug_set_device_error(kvc_ctx *c, uint32_t word);
 
 /* Timeline of the host-resident transport, for measuring it (the pages show
  * the pipeline's engagement by a scheduler dump; [R4] section Measurements).

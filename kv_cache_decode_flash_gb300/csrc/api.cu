@@ -1256,7 +1256,7 @@ static int evict_weight(Ctx *c, int seq, int p0, int p1, int32_t n_remove, float
     int rc = enter_sync(c);
     if (rc) return rc;
     auto al = [](int64_t x) { return (x + 255) / 256 * 256; };
-    const int64_t o_gone = al(sel.count * 4), o_pairs = o_gone + al(k * 4), o_rows = o_pairs + al(k * 8);
+    const int64_t o_gone = al(sel.count * 4), o_pairs = o_gone + al(k * 4), o_rows = o_pairs + al(k * 16);
     if ((rc = ensure_staging(c, o_rows + (sel.contiguous ? 0 : al(sel.count * 4))))) return rc;
     if (k > c->gone_cap) {
         if (!take_alloc(c)) return c->fail(KVC_ENOMEM, "injected allocation failure: removed rows");
@@ -1285,7 +1285,7 @@ static int evict_weight(Ctx *c, int seq, int p0, int p1, int32_t n_remove, float
     e.w_stride = w_stride;
     e.keys = reinterpret_cast<uint32_t *>(c->staging);
     e.gone = reinterpret_cast<int32_t *>(c->staging + o_gone);
-    e.pairs = reinterpret_cast<int2 *>(c->staging + o_pairs);
+    e.pairs = reinterpret_cast<int4 *>(c->staging + o_pairs);
     e.pt = c->pt_dev + (int64_t)seq * c->max_pages;
     e.pt_len = c->max_pages;
     e.n_pages = c->n_pages;
@@ -1612,6 +1612,16 @@ int kvc_debug_fail_alloc_after(kvc_ctx *cc, int n) {
         return KVC_OK;
     }
     c->fail_after = n < 0 ? -1 : n;
+    return KVC_OK;
+}
+
+int kvc_debug_set_device_error(kvc_ctx *cc, uint32_t word) {
+    if (!cc) return KVC_EINVAL;
+    Ctx *c = reinterpret_cast<Ctx *>(cc);
+    if (c->host || c->split) return c->fail(KVC_EINVAL, "the test hook needs a device-resident context");
+    KVC_CU(c, cudaSetDevice(c->dev));
+    KVC_CU(c, cudaDeviceSynchronize());
+    KVC_CU(c, cudaMemcpy(c->err_dev, &word, 4, cudaMemcpyHostToDevice));
     return KVC_OK;
 }
 

@@ -15,14 +15,14 @@ struct EvictArgs {
     int64_t w_stride;
     uint32_t *keys;       // work: [n_cand]
     int32_t *gone;        // out: the removed rows, ascending [n_remove]
-    int2 *pairs;          // work: (hole, mover) pool rows of KV head 0, layer 0; [n_remove], (-1, -1) where none
+    int4 *pairs;          // work: hole's and mover's pool rows of KV head 0, layer 0, the hole; [n_remove], -1 where none
     // the pools
     const int32_t *pt;    // the sequence's page table
     int32_t pt_len, n_pages, off, P, Hk, L;
     uint8_t *base[4];     // K codes, V codes, K scales, V scales (null: absent)
     int32_t rowb[4];
     int64_t pool_rows;
-    uint32_t *err;
+    uint32_t *err;        // set: nothing is changed
 };
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t st);
 

@@ -13,8 +13,11 @@
 // [n', n) give the places: the kept ones among them move, in order, into the
 // removed places below n' (as many, by counting), so at most n_remove rows are
 // read and written in every layer, whatever the sequence's length.  A mover's
-// place is found by a binary search in the list, and its weights move;
-// evict_move copies the K and V rows of all layers and heads.
+// place is found by a binary search in the list; nothing of the cache has
+// changed by then.  evict_move, the last kernel, moves the weights and the K and V
+// rows of all layers and heads, unless the device's error word is set (by a page
+// that the pool does not have, or by a kernel before): the call fails then, and
+// weights, rows and positions are as they were.
 // What bounds it: the chain of launches, barriers and two waits for the device with
 // few rows (64 of 512 rows: 42 us for the call); the one CTA's passes over the keys
 // with many (1024 of 32768: 113 us; 16 layers more move in 11 us).
@@ -52,7 +55,7 @@ __device__ __forceinline__ int64_t pool_row0(const EvictArgs &a, int32_t j) {
     return (int64_t)page * a.Hk * a.P + (lr - pi * a.P);
 }
 
-// Row x of the last n_remove ones: its place among the holes, if it stays, and its weights.
+// Row x of the last n_remove ones: its place among the holes, if it stays.
 __device__ __forceinline__ void pair_of(const EvictArgs &a, int x) {
     const int32_t left = a.n - a.n_remove, j = left + x;
     int lo = 0, hi = a.n_remove; // removed rows before j
@@ -60,7 +63,7 @@ __device__ __forceinline__ void pair_of(const EvictArgs &a, int x) {
         const int mid = (lo + hi) / 2;
         if (a.gone[mid] < j) lo = mid + 1; else hi = mid;
     }
-    int2 pr = make_int2(-1, -1);
+    int4 pr = make_int4(-1, -1, -1, 0);
     if (lo >= a.n_remove || a.gone[lo] != j) {
         // kept: of the x rows before it in the tail, those removed are the removed ones below j that are not holes;
         // with h holes, lo - h of them, so it is mover x - (lo - h); holes are the first h of the list
@@ -71,10 +74,8 @@ __device__ __forceinline__ void pair_of(const EvictArgs &a, int x) {
         }
         const int32_t hole = a.gone[x - (lo - hl)];
         const int64_t to = pool_row0(a, hole), from = pool_row0(a, j);
-        if (to >= 0 && from >= 0) pr = make_int2((int)to, (int)from);
-        for (int g = 0; g < a.Hk; ++g) a.w[g * a.w_stride + hole] = a.w[g * a.w_stride + j];
+        if (to >= 0 && from >= 0) pr = make_int4((int)to, (int)from, hole, 0);
     }
-    for (int g = 0; g < a.Hk; ++g) a.w[g * a.w_stride + j] = 0.f;
     a.pairs[x] = pr;
 }
 __global__ void __launch_bounds__(128) evict_pairs(const __grid_constant__ EvictArgs a) {
@@ -200,7 +201,8 @@ template <bool ALL> __global__ void __launch_bounds__(SEL) evict_select(const __
     }
 }
 
-// One warp a (pair, layer): every head's row of the four tensors, in the widest words that its rows allow.
+// One warp a (pair, layer): every head's row of the four tensors, in the widest words that its rows allow; the first
+// layer's sees to the pair's weights too.
 template <class W>
 __device__ __forceinline__ void move_rows(uint8_t *base, int rowb, int64_t to, int64_t from, int64_t head, int Hk, int lane) {
     const int words = rowb / (int)sizeof(W), all = words * Hk;
@@ -213,8 +215,15 @@ __device__ __forceinline__ void move_rows(uint8_t *base, int rowb, int64_t to, i
 __global__ void __launch_bounds__(256) evict_move(const __grid_constant__ EvictArgs a) {
     const int lane = threadIdx.x & 31;
     const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (i >= a.n_remove) return;
-    const int2 pr = a.pairs[i];
+    if (i >= a.n_remove || *a.err != 0) return;
+    const int4 pr = a.pairs[i];
+    if (blockIdx.y == 0) {
+        for (int g = lane; g < a.Hk; g += 32) {
+            float *w = a.w + g * a.w_stride, *tail = w + (a.n - a.n_remove + i);
+            if (pr.z >= 0) w[pr.z] = *tail;
+            *tail = 0.f;
+        }
+    }
     if (pr.x < 0) return;
     const int64_t lo = (int64_t)blockIdx.y * a.pool_rows, to = lo + pr.x, from = lo + pr.y;
     move_rows<uint4>(a.base[0], a.rowb[0], to, from, a.P, a.Hk, lane);

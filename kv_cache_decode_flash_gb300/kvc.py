@@ -106,6 +106,7 @@ def load():
                                         C.POINTER(C.c_int32)]),
         "kvc_set_timeout_ms": (i32, [p, i32]),
         "kvc_debug_fail_alloc_after": (i32, [p, i32]),
+        "kvc_debug_set_device_error": (i32, [p, C.c_uint32]),
         "kvc_check_device_error": (i32, [p, C.POINTER(C.c_uint32)]),
         "kvc_cold_create": (i32, [C.c_int64, C.POINTER(p)]),
         "kvc_cold_destroy": (None, [p]),
@@ -465,6 +466,11 @@ def kvc_debug_select_rows(pos, p0, p1, linear=False):
 
 def kvc_debug_fail_alloc_after(ctx, n):
     _check(ctx, load().kvc_debug_fail_alloc_after(ctx, n))
+
+
+def kvc_debug_set_device_error(ctx, word):
+    """Set the device error word as if a kernel had reported it."""
+    _check(ctx, load().kvc_debug_set_device_error(ctx, int(word)))
 
 
 def kvc_check_device_error(ctx) -> int:
