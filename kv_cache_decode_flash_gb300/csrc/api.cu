@@ -1276,6 +1276,7 @@ static int evict_weight(Ctx *c, int seq, int p0, int p1, int32_t n_remove, float
     e.n_cand = (int32_t)sel.count;
     e.first = (int32_t)sel.first;
     if (!sel.contiguous) {
+        if (!take_alloc(c)) throw std::bad_alloc(); // (an injected failure)
         std::vector<int32_t> rows(sel.idx.begin(), sel.idx.end());
         if ((rc = upload(c, c->staging + o_rows, rows.data(), (int64_t)rows.size() * 4))) return rc;
         e.rows = reinterpret_cast<const int32_t *>(c->staging + o_rows);
@@ -1332,6 +1333,7 @@ int kvc_seq_evict_weight(kvc_ctx *cc, int seq, int p0, int p1, int32_t n_remove,
     try { // (the selection's lists, made before anything changes)
         return evict_weight(c, seq, p0, p1, n_remove, w, w_stride, n_removed);
     } catch (const std::bad_alloc &) {
+        c->err.assign("no host memory"); // (fits a string's own room: no allocation)
         return KVC_ENOMEM;
     }
 }

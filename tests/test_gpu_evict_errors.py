@@ -29,3 +29,26 @@ def test_evict_with_a_device_error_reported_changes_nothing(n, k, kind):
         _evict_and_check(tw, 0, -1, -1, k, w0)
     finally:
         tw.close()
+
+
+def test_evict_without_host_memory_says_so():
+    """The list of candidates that are not consecutive rows cannot be allocated: KVC_ENOMEM with a message of its own, and
+    nothing has changed."""
+    import torch
+
+    tw = _cache("q8", 8, 2, 64, [300])
+    try:
+        w = torch.rand(2, 300, device="cuda:0")
+        assert tw.gpu.evict_weight(0, -1, -1, 20, w) == 20  # (the rows are out of order from here on)
+        blob, w0 = tw.gpu.state_get(0, -1, -1), w.clone()
+        with pytest.raises(tw.kvc.KvcError):
+            tw.gpu.evict_weight(5, -1, -1, 20, w)  # leaves another message
+        tw.kvc.kvc_debug_fail_alloc_after(tw.gpu.ctx, 0)
+        with pytest.raises(tw.kvc.KvcError) as e:
+            tw.gpu.evict_weight(0, 0, 290, 20, w)
+        assert e.value.status == tw.kvc.KVC_ENOMEM and "no host memory" in str(e.value)
+        tw.kvc.kvc_debug_fail_alloc_after(tw.gpu.ctx, -1)
+        assert tw.gpu.state_get(0, -1, -1) == blob and bool((w == w0).all())
+        assert tw.gpu.evict_weight(0, 0, 290, 20, w) == 20
+    finally:
+        tw.close()
