@@ -209,7 +209,9 @@ typedef enum kvc_act { KVC_ACT_F32 = 0, KVC_ACT_F16 = 1, KVC_ACT_BF16 = 2 } kvc_
  * that sees no row gets out = 0 and lse = -inf; n_q[i] may be 0.  The causal
  * attention of a prompt's tokens over themselves and the rows before them is
  * n_vis[t] = (rows before the block) + (t's place in the block) + 1.
- * What a row holds that a token does not see never reaches that token; a V
+ * What a row holds that a token does not see never reaches that token.  (Codes
+ * share a power of two among neighbouring rows that some token of the block
+ * sees: values 2^14 times those that a token sees may cost it accuracy.)  A V
  * value that is not finite reaches every token that sees its row, whatever the
  * others see (infinite, or NaN where 16 bits leave the row no weight).
  * seq_ids, n_q: HOST int32[n_seq]; an id may come more than once (decoders

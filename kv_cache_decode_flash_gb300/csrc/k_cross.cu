@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
                 const int j = i / NB, b = i % NB;
                 if constexpr (KT != KVC_F16) s.ks[b][j] = __half2float(__ushort_as_half(s.rks[i]));
                 if constexpr (VT != KVC_F16) {
-                    float d = __half2float(__ushort_as_half(s.rvs[i]));
+                    float d = base + j < r1 ? __half2float(__ushort_as_half(s.rvs[i])) : 0.f; // (nobody sees it: no say in E)
                     if (!(fabsf(d) <= 65504.f)) {
                         d = 0.f;
                         s.badrow[cur][j] = 1;

@@ -121,7 +121,7 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
     const uint8_t *data = IS_V ? p.vdata : p.kdata;
     uint64_t *full = &x.bar[IS_V ? VF0 : KF0], *empty = &x.bar[IS_V ? VE0 : KE0];
     int32_t(*row)[TN] = x.row[IS_V];
-    int steps = 1 << 24, vis_min = 0; // known with the query rows
+    int steps = 1 << 24, vis_min = 0, r1 = 0; // known with the query rows; r1: the end of the rows that some token sees
     constexpr int SYNC = IS_V ? 4 : 3, NT = IS_V ? GROUP : K_GROUPS<TWO> * GROUP; // threads
     const bool has_row = NT == TN || t < TN;   // whose place and scales it sees to
     Lookup next; // of the step whose rows the group gets next
@@ -136,7 +136,7 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
     auto begin = [&] { // the query rows are there: how far the tokens see
         __syncthreads();
         tc_after();
-        const int r1 = min(r_end, x.vis_max);
+        r1 = min(r_end, x.vis_max);
         steps = r1 > r0 ? (r1 - r0 + TN - 1) / TN : 0;
         vis_min = x.vis_min;
     };
@@ -196,7 +196,7 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
         int E = E_MIN;
         auto exponent = [&](int s) { // of step s, whose scales are sc
             uint32_t m = 0;
-            const bool in = r0 + s * TN + t < q.n_rows; // a row past the end: scales 0
+            const bool in = r0 + s * TN + t < r1; // a row past the end, or that nobody sees: scales 0
 #pragma unroll
             for (int k = 0; has_row && k < D / QK; ++k) {
                 uint32_t h = sc[k >> 1] >> (16 * (k & 1)) & 0xffffu;

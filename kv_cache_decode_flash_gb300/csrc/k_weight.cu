@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(THREADS, 1) weight_kernel(const __grid_constan
                 int ps = y % steps; // the step's place in the range
                 auto exponent = [&](int n, int s) { // of this group's n-th step (place s), whose scales are sc
                     uint32_t m = 0;
-                    const bool in = r0 + s * TN + t < q.n_rows;
+                    const bool in = r0 + s * TN + t < r1; // (rows that nobody sees have no say in the exponent)
 #pragma unroll
                     for (int b = 0; b < D / QK; ++b) {
                         uint32_t v = sc[b >> 1] >> (16 * (b & 1)) & 0xffffu;

@@ -247,3 +247,40 @@ def test_lse_holds_32_bits_whatever_a_token_sees(kernel, T, sigma, kind, D, act)
             assert abs(total[g] - rows) <= lim, "weights sum to %.6f of %d" % (total[g], rows)
     finally:
         tw.close()
+
+
+@pytest.mark.parametrize("act", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("kind,D", [("q8", 64), ("q8", 128), ("q8q4", 128), ("f16", 64)])
+@pytest.mark.parametrize("T", [3, 150])
+@pytest.mark.parametrize("kernel", [MMA, TC])
+def test_large_values_that_nobody_sees_change_nothing(kernel, T, kind, D, act):
+    """Rows behind the last one that any token sees, whatever finite values they hold, leave results, log-sum-exps and weights
+    as they are without them, bit by bit: the operands' powers of two come from rows that are seen."""
+    import torch
+
+    if act == "f32" and kernel == TC:
+        pytest.skip("32-bit queries have one kernel")
+    n, seen, H, Hk = 300, 150, 4, 2
+    k, v = kv_inputs(37, 0, n, Hk, D, sigma=0.1)
+    rng = np.random.default_rng(T)
+    q = _tensor(rng.standard_normal((T, H, D)), act)
+    vis = rng.integers(1, seen + 1, T)
+    vis[0] = seen
+    got = []
+    for big in (1.0, 6e4 if kind == "f16" else 6e6):  # (q8_0 and q4_0 hold up to 127 and 8 x 65504, of either sign)
+        kk, vv = k.copy(), v.copy()
+        kk[seen:] *= np.float32(big) / np.abs(kk[seen:]).max()
+        vv[seen:] *= np.float32(min(big, 5e5) if kind == "q8q4" else big) / np.abs(vv[seen:]).max()
+        tw = _twin(kind, H, Hk, D, n + 64)
+        try:
+            tw.gpu.append(0, 0, 0, _tensor(kk), _tensor(vv))
+            o, z = _attend(tw, kernel, [0], [T], q, D**-0.5, vis)
+            w = torch.zeros(1, Hk, n, device="cuda:0")
+            tw.gpu.attn_weight(0, [0], [T], q, z, w, D**-0.5, n_vis=torch.from_numpy(vis.astype(np.int32)).to("cuda:0"))
+            got.append((o, z, w))
+            assert tw.kvc.kvc_check_device_error(tw.gpu.ctx) == 0
+        finally:
+            tw.close()
+    for a, b in zip(*got):
+        assert bool(torch.isfinite(a.float()).all()) and bool((a == b).all())
+    assert bool((got[0][2][:, :, seen:] == 0).all())
