@@ -219,14 +219,15 @@ typedef enum kvc_act { KVC_ACT_F32 = 0, KVC_ACT_F16 = 1, KVC_ACT_BF16 = 2 } kvc_
  * q, out: device [T][n_head][head_dim], contiguous; out may not overlap q.
  * lse: device fp32 [T][n_head], or NULL.  n_vis: device int32 [T], or NULL.
  * q and out 16-byte aligned, lse and n_vis 4-byte aligned.
- * Results are bitwise repeatable.  32-bit results keep 32-bit accuracy; with
- * 16-bit queries the products' operands have 11 significant bits or more
- * (weights below 2^-21 of a token's largest: an error of 2^-32 of that one at
- * most) and all sums are fp32.
+ * Results are bitwise repeatable.  32-bit results keep 32-bit accuracy, lse with
+ * any type of q among them.  16-bit ones come from weights and V of 11
+ * significant bits or more (a weight below 2^-21 of a token's largest: an error
+ * of 2^-32 of that one at most) and fp32 sums.
  * The call only enqueues work on `stream`.  Its work space (split rows'
  * partial sums) is allocated by the context's first such call, has one size
  * for good and is shared by all of them, captured ones too, so order them.
- * That first call cannot be captured into a graph (KVC_EINVAL).
+ * That first call cannot be captured into a graph (KVC_EINVAL).  A captured call
+ * keeps the rows (their number and first place) that its sequences had then.
  * Device-resident contexts only.
  * Errors: KVC_EINVAL, KVC_ENOMEM, KVC_ECUDA. */
 int kvc_attn_cross(kvc_ctx *c, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_q, int act,
@@ -242,9 +243,14 @@ int kvc_attn_cross(kvc_ctx *c, int layer, int n_seq, const int32_t *seq_ids, con
  * (device fp32 [T][n_head]) as that call wrote it for these tokens and rows.
  * w: device fp32 [n_seq][n_head_kv][w_stride], w_stride at least the rows of
  * every sequence; entries behind a sequence's rows are left as they are.  An
- * id may come more than once (each entry has its own accumulators).  The order of the
- * sums is fixed: results are bitwise repeatable.  32-bit accuracy for every type
- * of q.  The call only enqueues work on `stream`; no work space.
+ * id may come more than once (each entry has its own accumulators).  The order
+ * of the sums is fixed: results are bitwise repeatable.  32-bit accuracy for
+ * every type of q.
+ * The accumulators are the caller's, and only kvc_seq_evict_weight moves them
+ * with their rows: after kvc_seq_rm, kvc_seq_evict_window, kvc_seq_cp or
+ * kvc_state_set it is for the caller to bring w into the new row order.
+ * The call only enqueues work on `stream`; no work space.  A captured call keeps
+ * the rows that its sequences had then, as kvc_attn_cross does.
  * Device-resident contexts only.  Errors: KVC_EINVAL, KVC_ECUDA. */
 int kvc_attn_weight(kvc_ctx *c, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_q, int act,
                     const void *q, const float *lse, const int32_t *n_vis, float kq_scale, float *w,

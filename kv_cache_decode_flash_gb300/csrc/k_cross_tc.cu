@@ -19,10 +19,10 @@
 // the 18 bits: scores make the log-sum-exp, a result of 32 bits, whose error from
 // 11 bits of K was 2e-4 for tokens of few rows and 3e-3 for peaked softmaxes, and
 // every row weight formed from it was off by as much.  Both parts are multiplied
-// with Q into the same scores.  Scales may lie anywhere in fp16's range, their products need not: a
-// step's K is scaled by a power of two that brings its largest scale to
-// [2^7, 2^8), undone in the score's factor; V's exponent is that of the largest
-// scale met so far, and O is rescaled when it grows.
+// with Q into the same scores.  Scales may lie anywhere in fp16's range, their
+// products need not: a step's K is scaled by a power of two that brings its largest
+// scale to [2^7, 2^8), undone in the score's factor; V's exponent is that of the
+// largest scale met so far, and O is rescaled when it grows.
 // The softmax rescales O only when a row's maximum has grown by more than 2^8
 // since the last time (the final quotient is the same), so O is hardly ever read
 // back before the end.  P stands 2^7 above its value for that maximum: it is 2^15
@@ -30,14 +30,14 @@
 // largest; below, it is off by 2^-32 of the largest at most, where a long row's
 // many small weights beside a great one would otherwise vanish.  The sum is
 // formed under the same factor, which lse and the parts' maxima take back.
-// What bounds it: with many query rows the chain of a half's job, softmax and then
-// its two products, against the other half's (2048 tokens of 40 heads over 16384
-// rows: 621 us, 1.11 PFLOP/s, 58 % of a plain matrix product's rate; the products
-// alone would take 2048 of a step's 3500 cycles); with few, halves run at the
-// memory's rate (131072 rows, 5 tokens: 91 us, 5.9 TB/s of 6.8), codes at that of
-// their conversion (114 us, 2.5 TB/s: four warps turn a tile of K, four one of V,
-// in about 2200 cycles), short ones at start, first tiles and join (16384 rows, 5
-// tokens: 28 us, of which the seven steps are half).
+// What bounds it: with many query rows the chain of a half's job, softmax and its
+// products, against the other half's, whose products the one issuing thread takes
+// in turn (2048 tokens of 40 heads over 16384 rows, causal: halves 598 us, 1.08
+// PFLOP/s of seen pairs, 57 % of a plain matrix product's rate; codes, with three
+// products a job, 806 us, 0.80 PFLOP/s).  With few, halves run at the memory's rate
+// (131072 rows, 5 tokens: 90 us, 6.0 TB/s of 6.8), codes at that of their
+// conversion (136 us, 2.1 TB/s), short ones at start, first tiles and join (16384
+// rows, 5 tokens: 31 us, of which the seven steps are half).
 #include "tc_tile.cuh"
 
 namespace kvc {

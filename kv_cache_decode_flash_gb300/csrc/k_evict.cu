@@ -19,8 +19,8 @@
 // that the pool does not have, or by a kernel before): the call fails then, and
 // weights, rows and positions are as they were.
 // What bounds it: the chain of launches, barriers and two waits for the device with
-// few rows (64 of 512 rows: 42 us for the call); the one CTA's passes over the keys
-// with many (1024 of 32768: 113 us; 16 layers more move in 11 us).
+// few rows (64 of 512 rows: 43 us for the call); the one CTA's passes over the keys
+// with many (1024 of 32768: 117 us; 16 layers more move in 14 us).
 #include "evict.h"
 
 namespace kvc {

@@ -17,8 +17,8 @@
 // A power of two brings a step's largest scale to [2^3, 2^4); it changes only
 // when the scales have moved by 2^4, so that the factors per query row, in which
 // it is undone, are seldom rewritten.
-//   One CTA per SM, 17 warps: two softmax groups and two loading groups that take
-// the steps in turn, and the issuing thread; the accumulators alternate in TMEM.
+//   One CTA per SM, five groups of four warps: two softmax groups and two loading groups that
+// take the steps in turn, and that of the issuing thread; the accumulators alternate in TMEM.
 // What bounds it: with many query rows shared memory, which the products' operands
 // (two parts of K, each against all query rows), the conversion's stores and the
 // factors' loads share (32 tokens of 40 heads over 131072 rows: q8_0 91 us, of which
