@@ -23,10 +23,11 @@
  *    pointers, e.g. torch tensors) and all host byte buffers; the library
  *    never keeps a caller pointer after a call returns.
  *  - Streams: `stream` is a cudaStream_t passed as void* (NULL = the legacy
- *    default stream).  kvc_append, kvc_attn_decode and kvc_decode_step only
+ *    default stream).  The calls that take one (kvc_append, kvc_append_rope, the
+ *    attentions, kvc_decode_step, kvc_seq_keep) only
  *    enqueue work on it and return without waiting; calls on one context must be issued from one
  *    host thread and be ordered on the device (one stream, or events).
- *    The sequence and state operations are synchronous: they wait for all
+ *    The other sequence and state operations are synchronous: they wait for all
  *    device work already issued in the process, run, and return when their
  *    effect is complete (kvc_state_get's bytes are valid at return).
  *  - A context is not thread-safe; distinct contexts are independent.
@@ -149,6 +150,38 @@ const char *kvc_status_str(int status);
 int kvc_append(kvc_ctx *c, int layer, int seq, int pos0, int n_tok, const float *k,
                const float *v, void *stream);
 
+/* Append rows as a model's projections leave them: entry i of the call brings
+ * n_tok[i] tokens of sequence seq_ids[i] (packed one entry after the other: T =
+ * sum of n_tok in all) at positions pos[t].  Of every head-row x of a token's
+ * queries and keys
+ *   n = x * w / sqrt(mean(x^2) + eps)    with w = q_norm or k_norm; n = x without
+ *   (a, b) -> (a cos - b sin, a sin + b cos),  angle = pos[t] * rope_base^(-2i/D)
+ * over n's rotary pairs i (see kvc_rope; kvc_seq_add turns by the same angles).
+ * Turned queries go to q_out in their own type; turned keys and the values as
+ * they are become the sequence's next rows of that layer, in order, stored as
+ * kvc_append stores them.  Computed in fp32, the angle exact to 2^-32 of a turn
+ * whatever the position, and rounded once.  Positions may be any (the tokens of a
+ * drafted tree share those of their depth); as with kvc_append the first layer to
+ * append creates the rows, and the others must append the same positions.
+ * seq_ids, n_tok: HOST int32[n_seq], ids distinct, n_tok[i] may be 0; pos: HOST
+ * int32[T].  act: type (kvc_act) of q, k, v and q_out.
+ * q: device [T] tokens of [n_head][head_dim], q_stride elements from one token to
+ * the next; k, v: [n_head_kv][head_dim], k_stride and v_stride: the three may be
+ * columns of one projection's result.  q_out: device [T][n_head][head_dim],
+ * contiguous; it may be q itself where that is contiguous too, and overlaps q, k
+ * and v in no other way.  q and q_out may both be NULL (no queries).  q_norm,
+ * k_norm: device fp32 [head_dim] or NULL (no norm).  Pointers are 16-byte
+ * aligned, strides multiples of 16 bytes.
+ * The call only enqueues work on `stream` and can be captured: a captured call
+ * keeps the cells and positions that it had then.  Every check is made before
+ * anything changes.  Device-resident contexts only.
+ * Errors: KVC_EINVAL (ids, shapes, positions not matching the rows other layers
+ * created), KVC_ERANGE (a negative position), KVC_ENOSPC (no free pages),
+ * KVC_ENOMEM, KVC_ECUDA. */
+int kvc_append_rope(kvc_ctx *c, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_tok, const int32_t *pos,
+                    int act, const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                    int64_t v_stride, const float *q_norm, const float *k_norm, float eps, void *q_out, void *stream);
+
 /* Single-token decode attention for n_seq sequences of one layer:
  *   out[i][h][:] = softmax_j(kq_scale * q[i][h] . K_j) V_j
  * over every row j the sequence holds for that layer, with K/V read as
@@ -193,7 +226,8 @@ int kvc_decode_step(kvc_ctx *c, int layer, int n_seq, const int32_t *seq_ids, co
                     const float *k, const float *v, const float *q, float *out, float kq_scale,
                     void *stream);
 
-/* Type of a block's queries and outputs (kvc_attn_cross, kvc_attn_weight). */
+/* Type of a block's queries and outputs (kvc_attn_cross, kvc_attn_weight,
+ * kvc_attn_tree) and of the rows that kvc_append_rope takes. */
 typedef enum kvc_act { KVC_ACT_F32 = 0, KVC_ACT_F16 = 1, KVC_ACT_BF16 = 2 } kvc_act;
 
 /* Attention of a block of query tokens over the cached rows of one layer:
@@ -233,6 +267,36 @@ typedef enum kvc_act { KVC_ACT_F32 = 0, KVC_ACT_F16 = 1, KVC_ACT_BF16 = 2 } kvc_
 int kvc_attn_cross(kvc_ctx *c, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_q, int act,
                    const void *q, void *out, float *lse, const int32_t *n_vis, float kq_scale, void *stream);
 
+/* Attention of a tree of drafted tokens: sequence entry i brings n_q[i] tokens
+ * (packed one entry after the other: T = sum of n_q in all), which are the last
+ * n_q[i] rows that the sequence holds for that layer, in the same order.  Token t
+ * sees every row before those, the rows of its ancestors and its own:
+ *   out[t][h][:] = sum_j softmax_j(kq_scale * q[t][h] . K_j) V_j
+ * with K/V read as stored and query head h reading KV head h / (H/Hk) ([F5]
+ * sections M2/M3: grouped-query heads stay in whole KV-head groups).  parent[t]
+ * is t's parent, counted within its entry; one that is not a token of the entry
+ * before t (negative, t itself, a later one) makes t a root.  Without parent
+ * the tokens are a chain: each sees all before it.  n_q[i] may be 0; at most 256.
+ * What a row holds that a token does not see never reaches that token.  (Codes
+ * share a power of two among neighbouring rows that some token of the block sees:
+ * V values 2^14 times those that a token sees may cost it accuracy.)  A V value
+ * that is not finite reaches every token that sees its row (infinite, or NaN
+ * where 32 bits, with 16-bit queries 16, leave the row no weight).
+ * seq_ids, n_q: HOST int32[n_seq]; an id may come more than once (trees over the
+ * same last rows).  act: type of q and out (kvc_act).
+ * q, out: device [T][n_head][head_dim], contiguous, 16-byte aligned; out may not
+ * overlap q.  parent: device int32 [T], 4-byte aligned, or NULL.
+ * Results are bitwise repeatable.  32-bit results keep 32-bit accuracy.  16-bit
+ * ones come from scores of 32 bits, weights of 11 significant bits (one below
+ * 2^-20 of a token's largest: an error of 2^-31 of that one at most), V as stored
+ * and fp32 sums.
+ * The call only enqueues work on `stream`.  It shares the work space of
+ * kvc_attn_cross, with what is said there about first calls, order and captures.
+ * Device-resident contexts only.  Errors: KVC_EINVAL (a sequence with fewer rows
+ * than n_q[i] among them), KVC_ENOMEM, KVC_ECUDA. */
+int kvc_attn_tree(kvc_ctx *c, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_q, int act,
+                  const void *q, void *out, const int32_t *parent, float kq_scale, void *stream);
+
 /* Accumulate the attention weight that the cached rows of one layer receive
  * from a block of query tokens (the statistic behind evicting rows by
  * accumulated attention; see kvc_seq_evict_weight): for sequence entry i, KV
@@ -262,6 +326,22 @@ int kvc_attn_weight(kvc_ctx *c, int layer, int n_seq, const int32_t *seq_ids, co
  * order; whole pages are freed, partly used boundary pages are compacted
  * on the device.  An empty range is a no-op.  Errors: KVC_EINVAL. */
 int kvc_seq_rm(kvc_ctx *c, int seq, int p0, int p1);
+
+/* Of the last n_last[i] rows of each sequence seq_ids[i] keep those at the places
+ * keep[..] among them (ascending, n_keep[i] of them, packed one sequence after the
+ * other); the others leave, in every layer and head: the accepted path of a
+ * drafted tree (kvc_attn_tree), whose rows kvc_seq_rm cannot name, as siblings
+ * share positions.  Kept rows close up in order, positions and stored bytes with
+ * them; rows before the last n_last[i] do not change, and a row that is kept with
+ * all of the last ones before it does not move.  Pages left empty are freed.
+ * n_keep[i] = 0 drops all of the last rows (keep may be NULL if nothing is kept).
+ * seq_ids (distinct), n_last, n_keep, keep: HOST int32.  Unlike the other
+ * sequence operations the call only enqueues work on `stream`: it belongs to the
+ * decoding loop.  Under a capture the bookkeeping happens at the capture, the moves
+ * at each replay.  Every layer must hold the same rows (KVC_EINVAL).
+ * Device-resident contexts only.  Errors: KVC_EINVAL, KVC_ENOMEM, KVC_ECUDA. */
+int kvc_seq_keep(kvc_ctx *c, int n_seq, const int32_t *seq_ids, const int32_t *n_last, const int32_t *n_keep,
+                 const int32_t *keep, void *stream);
 
 /* Copy the rows of `src` whose position is in [p0, p1) to the end of `dst`,
  * all layers, K and V, positions unchanged (MemorySeqCopy, [COLD] section
@@ -448,6 +528,18 @@ int kvc_debug_block_kernel(kvc_ctx *c, int which);
 int kvc_debug_block_plan(int n_head, int n_head_kv, int head_dim, int act, int sms, int n_seq, const int32_t *rows,
                          const int32_t *n_q, int32_t *tile_m, int32_t *whole, int32_t *splits, int32_t *split_rows,
                          int64_t *items, int64_t *part_rows, int64_t *part_cap);
+
+/* Test hook, no context and no GPU needed: the same of a tree attention launch
+ * over n_seq (1 .. 64) sequences of rows[i] rows, the last n_q[i] of them the
+ * tree's, off[i] cells behind the start of the first page.  Errors: KVC_EINVAL. */
+int kvc_debug_tree_plan(int n_head, int n_head_kv, int sms, int n_seq, const int32_t *rows, const int32_t *off,
+                        const int32_t *n_q, int32_t *tile_m, int32_t *whole, int32_t *splits, int32_t *split_rows,
+                        int64_t *items, int64_t *part_rows, int64_t *part_cap);
+
+/* Test hook, no context and no GPU needed: the angles of kvc_append_rope: of
+ * every rotary pair i the turn that one position adds, rope_base^(-2i/D) / (2 pi),
+ * in units of 2^-64.  turns: HOST uint64[head_dim / 2].  Errors: KVC_EINVAL. */
+int kvc_debug_rope_turns(float rope_base, int head_dim, uint64_t *turns);
 
 /* Test hook, no context and no GPU needed: the rows of a sequence holding
  * positions pos[0 .. n) that the sequence operations select for the range

@@ -153,18 +153,9 @@ static int upload_pages(Ctx *c, int s) {
         if (rc) return rc;
     }
     q.dev_pages = (int32_t)q.pages.size();
+    if (q.dev_table.size() < q.pages.size()) q.dev_table.resize(q.pages.size());
+    std::copy(q.pages.begin(), q.pages.end(), q.dev_table.begin());
     return KVC_OK;
-}
-
-// Physical row index of (page, kv head, cell) in a layer pool.
-static inline int64_t prow(const Ctx *c, int32_t page, int g, int32_t cell) {
-    return ((int64_t)page * c->Hk + g) * c->P + cell;
-}
-
-static inline void phys(const Ctx *c, const Seq &q, int64_t r, int32_t &page, int32_t &cell) {
-    const int64_t lr = r + q.off;
-    page = q.pages[(size_t)(lr / c->P)];
-    cell = (int32_t)(lr % c->P);
 }
 
 // The rows of a sequence whose positions fall in [p0, p1), in row order.
@@ -178,14 +169,9 @@ struct RowSel {
     int64_t row(int64_t i) const { return contiguous ? first + i : idx[(size_t)i]; }
 };
 
-// Pages needed to hold rows [0, n) of a sequence with offset off.
-static inline int32_t pages_for(const Ctx *c, int32_t off, int64_t n) {
-    return n <= 0 ? 0 : (int32_t)((off + n + c->P - 1) / c->P);
-}
-
 // Grow sequence `s` by `add` rows (pages only; positions and counts are the
 // caller's).  Returns the indices of the new pages in q.pages via `first_new`.
-static int grow_pages(Ctx *c, Seq &q, int64_t add, size_t *first_new) {
+int grow_pages(Ctx *c, Seq &q, int64_t add, size_t *first_new) {
     *first_new = q.pages.size();
     const int32_t need = pages_for(c, q.off, (int64_t)q.n + add);
     if (need > c->max_pages) return c->fail(KVC_ENOSPC, "sequence would exceed the page table");
@@ -198,7 +184,7 @@ static int grow_pages(Ctx *c, Seq &q, int64_t add, size_t *first_new) {
     return KVC_OK;
 }
 
-static void release_tail_pages(Ctx *c, Seq &q) {
+void release_tail_pages(Ctx *c, Seq &q) {
     const int32_t need = pages_for(c, q.off, q.n);
     while ((int32_t)q.pages.size() > need) {
         c->free_pages.push_back(q.pages.back());
@@ -321,7 +307,7 @@ static void zero_payload_pads(const Ctx *c, uint8_t *payload, int64_t n) {
 }
 
 // Whether p[0 .. n) are consecutive integers in order.
-static bool consecutive(const int32_t *p, int64_t n) {
+bool consecutive(const int32_t *p, int64_t n) {
     if (n <= 1) return true;
     const int64_t p0 = p[0];
     int32_t bad = 0;
@@ -755,6 +741,8 @@ static int device_append_dst(Ctx *c, int layer, int seq, bool creates, int n_tok
             cudaError_t e = launch_pt_update(c->pt_dev, (int)idx.size(), idx.data(), val.data(), st);
             if (e != cudaSuccess) return cuda_fail(c, e, "page table update");
             q.dev_pages = (int32_t)q.pages.size();
+            if (q.dev_table.size() < q.pages.size()) q.dev_table.resize(q.pages.size());
+            std::copy(q.pages.begin(), q.pages.end(), q.dev_table.begin());
         }
     }
     const int64_t lo = (int64_t)layer * c->pool_rows;

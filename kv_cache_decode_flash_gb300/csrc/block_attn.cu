@@ -1,6 +1,6 @@
 // block_attn.cu - host side of the operators over a block of query tokens
-// (kvc_attn_cross, kvc_attn_weight): checks, the split of the cached rows over
-// work items, the work space and the launches.
+// (kvc_attn_cross, kvc_attn_weight, kvc_attn_tree): checks, the split of the
+// cached rows over work items, the work space and the launches.
 #include "block_attn.h"
 #include "ctx.h"
 
@@ -136,6 +136,23 @@ static bool plan_block(BlockParams &p, int sms, bool tc) {
     return narrow;
 }
 
+// The query tiles and items of a tree attention: tiles of 16, 32 or 64 query rows (a warp's products are of 16 or 32 of
+// them, so that a tile larger than the rows is only waste), one item at a time on an SM.  The kernel counts cached rows
+// from the 16-row boundary at or below the sequence's first.
+static void plan_tree(BlockParams &p, int sms) {
+    int64_t most = 0;
+    for (int i = 0; i < p.n_seq; ++i) most = std::max<int64_t>(most, (int64_t)p.seq[i].n_tok * p.r);
+    p.tile_m = most <= 16 ? 16 : (most <= 32 ? 32 : 64);
+    p.part_rows = (int32_t)std::max<int64_t>(1, std::min<int64_t>(p.tile_m, most));
+    for (int i = 0; i < p.n_seq; ++i) {
+        BlockSeq &s = p.seq[i];
+        s.tiles = (int32_t)(((int64_t)s.n_tok * p.r + p.tile_m - 1) / p.tile_m);
+        s.n_rows += s.off % 16;
+    }
+    plan_splits(p, sms, TREE_STEP, 2 * TREE_STEP, part_rows_cap(sms));
+    for (int i = 0; i < p.n_seq; ++i) p.seq[i].n_rows -= p.seq[i].off % 16;
+}
+
 // Which kernel attends a sequence of 16-bit queries (both hold scores to 32 bits).  The tcgen05 kernel pays where a call
 // has enough to do, by its cached values (rows x KV heads x D) or its products (times query rows of a KV head); and in
 // such a call for the sequences that have TC_MIN_ROWS rows or enough products of their own: an item of few tokens over
@@ -265,6 +282,56 @@ extern "C" int kvc_attn_cross(kvc_ctx *cc, int layer, int n_seq, const int32_t *
     return KVC_OK;
 }
 
+extern "C" int kvc_attn_tree(kvc_ctx *cc, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_q, int act,
+                             const void *q, void *out, const int32_t *parent, float kq_scale, void *stream) {
+    if (!cc) return KVC_EINVAL;
+    Ctx *c = reinterpret_cast<Ctx *>(cc);
+    int64_t total = 0;
+    int rc = block_check(c, layer, n_seq, seq_ids, n_q, act, q, kq_scale, &total);
+    if (rc) return rc;
+    for (int i = 0; i < n_seq; ++i) {
+        if (n_q[i] > TREE_MAX) return c->fail(KVC_EINVAL, "a tree has at most 256 tokens");
+        if (n_q[i] > c->seqs[(size_t)seq_ids[i]].lfill[(size_t)layer])
+            return c->fail(KVC_EINVAL, "a sequence has fewer rows than its tree has tokens");
+    }
+    if (total == 0) return KVC_OK;
+    if (!out) return c->fail(KVC_EINVAL, "out must be non-null");
+    if ((uintptr_t)out & 15) return c->fail(KVC_EINVAL, "out must be 16-byte aligned");
+    if ((uintptr_t)parent & 3) return c->fail(KVC_EINVAL, "parent must be 4-byte aligned");
+    if (overlap(q, out, total * c->H * c->D * (act == KVC_ACT_F32 ? 4 : 2)))
+        return c->fail(KVC_EINVAL, "out may not overlap q");
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    KVC_CU(c, cudaSetDevice(c->dev));
+    if ((rc = ensure_block_space(c, st))) return rc;
+    auto *launch = c->tk == KVC_F16 ? launch_tree_f16 : (c->tv == KVC_Q4_0 ? launch_tree_q4 : launch_tree_q8);
+    BlockParams p;
+    block_params(c, layer, kq_scale, act, p);
+    p.q = q;
+    p.out = out;
+    p.parent = parent;
+    p.part = c->block_part;
+    p.part_cap = part_rows_cap(c->sms);
+    int64_t tok0 = 0;
+    for (int i = 0; i < n_seq; ++i) {
+        if (n_q[i] > 0) {
+            const Seq &sq = c->seqs[(size_t)seq_ids[i]];
+            BlockSeq &s = p.seq[p.n_seq++];
+            s.id = seq_ids[i];
+            s.off = sq.off;
+            s.n_rows = sq.lfill[(size_t)layer];
+            s.tok0 = (int32_t)tok0;
+            s.n_tok = n_q[i];
+        }
+        tok0 += n_q[i];
+        if (p.n_seq == 0 || (p.n_seq < MAX_SEQ_PER_LAUNCH && i + 1 < n_seq)) continue;
+        plan_tree(p, c->sms);
+        cudaError_t e = launch(p, c->tmk[2 * (size_t)layer], c->tmv[2 * (size_t)layer], st);
+        if (e != cudaSuccess) return cuda_fail(c, e, "tree attention kernel");
+        p.n_seq = 0;
+    }
+    return KVC_OK;
+}
+
 extern "C" int kvc_attn_weight(kvc_ctx *cc, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_q, int act,
                                const void *q, const float *lse, const int32_t *n_vis, float kq_scale, float *w,
                                int64_t w_stride, void *stream) {
@@ -346,6 +413,41 @@ extern "C" int kvc_debug_block_plan(int n_head, int n_head_kv, int head_dim, int
     }
     if (total * p.r > INT32_MAX / 4 / p.Hk) return KVC_EINVAL;
     plan_block(p, sms, act != KVC_ACT_F32);
+    *tile_m = p.tile_m;
+    *items = p.n_items;
+    *part_rows = 0;
+    *part_cap = part_rows_cap(sms);
+    for (int i = 0; i < n_seq; ++i) {
+        const BlockSeq &s = p.seq[i];
+        whole[i] = s.whole;
+        splits[i] = s.splits;
+        split_rows[i] = s.split_rows;
+        const int64_t cut = (int64_t)s.tiles * p.Hk - s.whole;
+        *part_rows = std::max<int64_t>(*part_rows, s.part_row0 + cut * s.splits * p.part_rows);
+    }
+    return KVC_OK;
+}
+
+extern "C" int kvc_debug_tree_plan(int n_head, int n_head_kv, int sms, int n_seq, const int32_t *rows, const int32_t *off,
+                                   const int32_t *n_q, int32_t *tile_m, int32_t *whole, int32_t *splits, int32_t *split_rows,
+                                   int64_t *items, int64_t *part_rows, int64_t *part_cap) {
+    if (n_head_kv < 1 || n_head < n_head_kv || n_head % n_head_kv || n_head / n_head_kv > MAX_GROUP || sms < 1 || n_seq < 1 ||
+        n_seq > MAX_SEQ_PER_LAUNCH || !rows || !off || !n_q || !tile_m || !whole || !splits || !split_rows || !items ||
+        !part_rows || !part_cap)
+        return KVC_EINVAL;
+    BlockParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.H = n_head;
+    p.Hk = n_head_kv;
+    p.r = n_head / n_head_kv;
+    p.n_seq = n_seq;
+    for (int i = 0; i < n_seq; ++i) {
+        if (n_q[i] < 1 || n_q[i] > TREE_MAX || rows[i] < n_q[i] || off[i] < 0) return KVC_EINVAL;
+        p.seq[i].n_rows = rows[i];
+        p.seq[i].off = off[i];
+        p.seq[i].n_tok = n_q[i];
+    }
+    plan_tree(p, sms);
     *tile_m = p.tile_m;
     *items = p.n_items;
     *part_rows = 0;

@@ -47,6 +47,7 @@ struct BlockParams {
     void *out;
     float *lse;           // cross: written (may be null); weight: read
     const int32_t *n_vis; // null: every token sees all rows
+    const int32_t *parent; // tree attention: the tokens' parents (null: a chain)
     float *w;             // weight: accumulators [..][Hk][w_stride]
     int64_t w_stride;
     float *part;          // partials: [row][D] sums, then [row] (max, sum) pairs
@@ -85,7 +86,15 @@ cudaError_t launch_cross(int type_k, int type_v, const BlockParams &p, bool narr
 // The same for 16-bit queries, by tcgen05 (tiles of CROSS_TC_TILE_M query rows).
 cudaError_t launch_cross_tc(int type_k, int type_v, const BlockParams &p, cudaStream_t st);
 
-// Joins the parts of the launch's cut units (k_join.cu; the two above end with it).
+// The attention of a tree of drafted tokens (tiles of 16, 32 or 64 query rows, steps of TREE_STEP cached ones), by the
+// cache's types; tmk, tmv: the layer's maps of 16-row boxes.
+constexpr int TREE_STEP = 64;
+constexpr int TREE_MAX = 256; // tokens of a tree
+cudaError_t launch_tree_q8(const BlockParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t launch_tree_f16(const BlockParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t launch_tree_q4(const BlockParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+
+// Joins the parts of the launch's cut units (k_join.cu; the attentions above end with it).
 cudaError_t launch_join(const BlockParams &p, cudaStream_t st);
 
 // The rows' weights: a unit is a KV head (one tile), a step WEIGHT_STEP rows.

@@ -26,6 +26,7 @@ struct Seq {
     bool linear = true;
     std::vector<int32_t> lfill;
     int32_t dev_pages = 0; // leading entries of `pages` known to match the device table
+    std::vector<int32_t> dev_table; // what the device table's row holds, as far as it was written (stale entries too)
     bool synced() const {
         for (int32_t f : lfill)
             if (f != n) return false;
@@ -168,5 +169,25 @@ struct Ctx {
         return code;
     }
 };
+
+// Physical row index of (page, kv head, cell) in a layer pool.
+inline int64_t prow(const Ctx *c, int32_t page, int g, int32_t cell) { return ((int64_t)page * c->Hk + g) * c->P + cell; }
+
+inline void phys(const Ctx *c, const Seq &q, int64_t r, int32_t &page, int32_t &cell) {
+    const int64_t lr = r + q.off;
+    page = q.pages[(size_t)(lr / c->P)];
+    cell = (int32_t)(lr % c->P);
+}
+
+// Pages needed to hold rows [0, n) of a sequence with offset off.
+inline int32_t pages_for(const Ctx *c, int32_t off, int64_t n) {
+    return n <= 0 ? 0 : (int32_t)((off + n + c->P - 1) / c->P);
+}
+
+// Shared by the translation units of the host side (api.cu).
+int cuda_fail(Ctx *c, cudaError_t e, const char *what);
+int grow_pages(Ctx *c, Seq &q, int64_t add, size_t *first_new);
+void release_tail_pages(Ctx *c, Seq &q);
+bool consecutive(const int32_t *p, int64_t n);
 
 } // namespace kvc

@@ -1,0 +1,279 @@
+// k_draft.cu - the two kernels around the attention over a drafted block.
+//
+// rope_append (kvc_append_rope): a token's head-rows come as the projections
+// leave them, n = x * w / sqrt(mean(x^2) + eps) where a norm's weights are given, and
+//   (a, b) -> (a cos - b sin, a sin + b cos),  angle = pos * base^(-2i/D),
+// of its queries and keys; queries are handed back in their own type, keys and
+// values become the sequence's next row, quantised by the steps of quant_row.cuh.
+// Everything is fp32 from the load to the one rounding at the end.
+//  A warp takes 2 (D 128) or 4 (D 64) head-rows at a time: a lane has four
+// values of a row's first half and the four that are D/2 further, so that the pairs of
+// either pairing and the halves of a quantisation block of 8 lanes are its
+// own.  The angles are a lane's for all rows of a token that the warp takes.
+//  An angle is formed in turns, as the fraction of pos * f in 64-bit fixed point
+// (f = base^(-2i/D) / 2 pi): one integer product is exact for positions of any
+// size, where a 32-bit product would be off by 2^-24 of the whole angle.
+//
+// keep (kvc_seq_keep): rows of the accepted path move down over the others.  A
+// warp has one (layer, KV head) of a sequence, a lane a piece of 16 bytes (a row's
+// scales: one of 8 or 4) of every row; it goes through the moves in order, eight
+// loads and then their eight stores.  A row moves down or stays where it is, and the
+// rows are ascending, so that no store reaches a row that is still to be read.
+#include "draft.h"
+#include "quant_row.cuh"
+
+#include <cuda_bf16.h>
+
+namespace kvc {
+namespace {
+
+constexpr int ROPE_THREADS = 128;
+
+template <int ACT> struct Four; // four values of an activation type
+template <> struct Four<KVC_ACT_F32> {
+    using T = float;
+    uint4 u;
+    __device__ __forceinline__ void load(const T *p) { u = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void get(float *x) const {
+        x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
+    }
+    __device__ __forceinline__ static void store(T *p, const float *x) {
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+};
+template <> struct Four<KVC_ACT_F16> {
+    using T = __half;
+    uint2 u;
+    __device__ __forceinline__ void load(const T *p) { u = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void get(float *x) const {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
+        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+    }
+    __device__ __forceinline__ static void store(T *p, const float *x) {
+        const __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
+        *reinterpret_cast<uint2 *>(p) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+};
+template <> struct Four<KVC_ACT_BF16> {
+    using T = __nv_bfloat16;
+    uint2 u;
+    __device__ __forceinline__ void load(const T *p) { u = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void get(float *x) const {
+        x[0] = __uint_as_float(u.x << 16), x[1] = __uint_as_float(u.x & 0xffff0000u);
+        x[2] = __uint_as_float(u.y << 16), x[3] = __uint_as_float(u.y & 0xffff0000u);
+    }
+    __device__ __forceinline__ static void store(T *p, const float *x) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+        *reinterpret_cast<uint2 *>(p) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+};
+
+// Four values, dims d .. d + 3 of pool row R, of a block that eight lanes hold (in: whether the row is to be written).
+template <int D>
+__device__ __forceinline__ void store_four(int type, const TensorView &tv, int64_t R, int d, int lane, const float (&x)[4], bool in) {
+    if (type == KVC_Q8_0) {
+        int8_t c[4];
+        float s;
+        quantise<4, 8>(x, c, s);
+        if (!in) return;
+        const uint32_t w = (uint32_t)(uint8_t)c[0] | (uint32_t)(uint8_t)c[1] << 8 | (uint32_t)(uint8_t)c[2] << 16 |
+                           (uint32_t)(uint8_t)c[3] << 24;
+        *reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(tv.data) + R * D + d) = w ^ CODE_FLIP;
+        if (d % QK == 0) tv.scales[R * (D / QK) + d / QK] = __half_as_ushort(__float2half_rn(s));
+    } else if (type == KVC_Q4_0) {
+        int c[4];
+        float s;
+        quantise_q4<4, 8>(x, lane, c, s);
+        const uint32_t mine = (uint32_t)c[0] | (uint32_t)c[1] << 8 | (uint32_t)c[2] << 16 | (uint32_t)c[3] << 24;
+        const uint32_t high = __shfl_xor_sync(0xffffffffu, mine, 4);
+        if (!in) return;
+        if (d % QK < QK / 2)
+            *reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(tv.data) + R * (D / 2) + d / QK * (QK / 2) + d % QK) =
+                mine | high << 4;
+        if (d % QK == 0) tv.scales[R * (D / QK) + d / QK] = __half_as_ushort(__float2half_rn(s));
+    } else if (in) {
+        Four<KVC_ACT_F16>::store(reinterpret_cast<__half *>(tv.data) + R * D + d, x);
+    }
+}
+
+template <int D, int ACT> __global__ void __launch_bounds__(ROPE_THREADS) rope_append_kernel(const __grid_constant__ RopeArgs a) {
+    constexpr int LANES = D / 8, ROWS = 32 / LANES; // of a head-row; head-rows at a time
+    using F = Four<ACT>;
+    using T = typename F::T;
+    // The next kernel may be scheduled now (see the append kernel: what it reads before its own wait is not written here);
+    // inputs may come from the one before, so they are read behind the wait.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31, li = lane % LANES, sub = lane / LANES;
+    const int64_t w = (int64_t)blockIdx.x * (ROPE_THREADS / 32) + (threadIdx.x >> 5);
+    if (w >= (int64_t)a.n_tok * a.warps) return;
+    const int t = (int)(w / a.warps), w0 = (int)(w % a.warps);
+    int lo = 0, hi = a.n_pieces - 1;
+    while (lo < hi) { // the last piece whose first token is not behind ours
+        const int mid = (lo + hi + 1) / 2;
+        if (a.piece[mid].first <= t) lo = mid; else hi = mid - 1;
+    }
+    const RopePiece &pc = a.piece[lo];
+    const int at = t - pc.first;
+    const int64_t tok = (int64_t)pc.tok0 + at;
+    const int pos = pc.listed >= 0 ? a.pos[pc.listed + at] : pc.pos + at;
+
+    // the lane's pairs: j, j + D/2 for four j (NEOX), or two neighbours twice in each half (NORM)
+    float cs[4], sn[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int pr = a.neox ? 4 * li + i : (i < 2 ? 2 * li + i : D / 4 + 2 * li + i - 2);
+        // the fraction of a turn in [-1/2, 1/2): its upper 32 bits are off by 2^-33 at most
+        const int32_t f = (int32_t)((((uint64_t)(uint32_t)pos * a.turn[pr]) + 0x80000000ull) >> 32);
+        sincospif((float)f * 0x1p-31f, &sn[i], &cs[i]);
+    }
+    const int nq = a.q ? (a.H + ROWS - 1) / ROWS : 0, nk = (a.Hk + ROWS - 1) / ROWS;
+    const int64_t lr = (int64_t)pc.off + pc.row0 + at, pi = lr / a.P;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int page = pi < a.max_pages ? a.pt[(int64_t)pc.id * a.max_pages + pi] : -1;
+    const bool there = page >= 0 && page < a.n_pages;
+    if (!there && lane == 0) atomicOr(a.err, ERR_BAD_PAGE);
+
+    // pass i: query rows, then keys', then values'; the next pass's are asked for before this one's are looked at
+    F x0, x1;
+    auto ask = [&](int i) {
+        const bool is_q = i < nq, is_k = !is_q && i < nq + nk;
+        const int h = (i - (is_q ? 0 : (is_k ? nq : nq + nk))) * ROWS + sub, n = is_q ? a.H : a.Hk;
+        const T *src = reinterpret_cast<const T *>(is_q ? a.q : (is_k ? a.k : a.v)) +
+                       tok * (is_q ? a.q_stride : (is_k ? a.k_stride : a.v_stride)) + (int64_t)min(h, n - 1) * D + 4 * li;
+        x0.load(src);
+        x1.load(src + D / 2);
+    };
+    if (w0 < a.passes) ask(w0);
+    for (int i = w0; i < a.passes; i += a.warps) {
+        const bool is_q = i < nq, is_k = !is_q && i < nq + nk;
+        const int h = (i - (is_q ? 0 : (is_k ? nq : nq + nk))) * ROWS + sub;
+        float x[8];
+        x0.get(x);
+        x1.get(x + 4);
+        if (i + a.warps < a.passes) ask(i + a.warps);
+        const float *wt = is_q ? a.q_norm : (is_k ? a.k_norm : nullptr);
+        if (wt) {
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s = fmaf(x[j], x[j], s);
+#pragma unroll
+            for (int m = 1; m < LANES; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+            const float inv = 1.0f / sqrtf(s * (1.0f / D) + a.eps);
+            const float4 w4 = *reinterpret_cast<const float4 *>(wt + 4 * li), w5 = *reinterpret_cast<const float4 *>(wt + D / 2 + 4 * li);
+            x[0] *= inv * w4.x, x[1] *= inv * w4.y, x[2] *= inv * w4.z, x[3] *= inv * w4.w;
+            x[4] *= inv * w5.x, x[5] *= inv * w5.y, x[6] *= inv * w5.z, x[7] *= inv * w5.w;
+        }
+        if (is_q || is_k) {
+            if (a.neox) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float y = x[j], z = x[j + 4];
+                    x[j] = y * cs[j] - z * sn[j];
+                    x[j + 4] = y * sn[j] + z * cs[j];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float y = x[2 * j], z = x[2 * j + 1];
+                    x[2 * j] = y * cs[j] - z * sn[j];
+                    x[2 * j + 1] = y * sn[j] + z * cs[j];
+                }
+            }
+        }
+        if (is_q) {
+            if (h < a.H) {
+                T *dst = reinterpret_cast<T *>(a.q_out) + (tok * a.H + h) * D + 4 * li;
+                F::store(dst, x);
+                F::store(dst + D / 2, x + 4);
+            }
+        } else {
+            const int64_t R = ((int64_t)page * a.Hk + h) * a.P + (int)(lr - pi * a.P);
+            const bool in = there && h < a.Hk;
+            const float y[4] = {x[0], x[1], x[2], x[3]}, z[4] = {x[4], x[5], x[6], x[7]};
+            const TensorView &tv = is_k ? a.lv.k : a.lv.v;
+            const int type = is_k ? a.type_k : a.type_v;
+            store_four<D>(type, tv, R, 4 * li, lane, y, in);
+            store_four<D>(type, tv, R, D / 2 + 4 * li, lane, z, in);
+        }
+    }
+}
+
+constexpr int KEEP_THREADS = 128;
+
+__global__ void __launch_bounds__(KEEP_THREADS) keep_kernel(const __grid_constant__ KeepArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int64_t w = (int64_t)blockIdx.x * (KEEP_THREADS / 32) + (threadIdx.x >> 5);
+    if (w >= (int64_t)a.L * a.Hk * a.n_entries) return;
+    const int e = (int)(w % a.n_entries), g = (int)(w / a.n_entries % a.Hk), l = (int)(w / a.n_entries / a.Hk);
+    // the lane's piece: 16 bytes of a row's K or V, or the row's scales of one of them
+    const int uk = a.rowb[0] / 16, uv = a.rowb[1] / 16;
+    const int which = lane < uk ? 0 : (lane < uk + uv ? 1 : (lane == uk + uv ? 2 : (lane == uk + uv + 1 ? 3 : 4)));
+    if (which == 4 || !a.base[which]) return;
+    const int rb = a.rowb[which], wide = which < 2 ? 16 : rb;
+    uint8_t *pool = a.base[which] + ((int64_t)l * a.pool_rows + (int64_t)g * a.P) * rb +
+                    (which == 0 ? lane * 16 : (which == 1 ? (lane - uk) * 16 : 0));
+    constexpr int AHEAD = 8;
+    for (int i0 = a.first[e]; i0 < a.first[e + 1]; i0 += AHEAD) {
+        uint4 v[AHEAD];
+        const int n = min(AHEAD, a.first[e + 1] - i0);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (i >= n) break;
+            const uint8_t *src = pool + (int64_t)a.move[i0 + i].x * rb;
+            if (wide == 16)
+                v[i] = *reinterpret_cast<const uint4 *>(src);
+            else if (wide == 8)
+                *reinterpret_cast<uint2 *>(&v[i]) = *reinterpret_cast<const uint2 *>(src);
+            else
+                v[i].x = *reinterpret_cast<const uint32_t *>(src);
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (i >= n) break;
+            uint8_t *dst = pool + (int64_t)a.move[i0 + i].y * rb;
+            if (wide == 16)
+                *reinterpret_cast<uint4 *>(dst) = v[i];
+            else if (wide == 8)
+                *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(&v[i]);
+            else
+                *reinterpret_cast<uint32_t *>(dst) = v[i].x;
+        }
+    }
+}
+
+template <int D> cudaError_t rope_pick(int act, const RopeArgs &a, const cudaLaunchConfig_t &cfg) {
+    switch (act) {
+    case KVC_ACT_F32: return cudaLaunchKernelEx(&cfg, rope_append_kernel<D, KVC_ACT_F32>, a);
+    case KVC_ACT_F16: return cudaLaunchKernelEx(&cfg, rope_append_kernel<D, KVC_ACT_F16>, a);
+    default: return cudaLaunchKernelEx(&cfg, rope_append_kernel<D, KVC_ACT_BF16>, a);
+    }
+}
+
+} // namespace
+
+cudaError_t launch_rope_append(int D, int act, const RopeArgs &a, cudaStream_t st) {
+    const int64_t warps = (int64_t)a.n_tok * a.warps;
+    if (warps <= 0) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((warps + ROPE_THREADS / 32 - 1) / (ROPE_THREADS / 32)));
+    cfg.blockDim = dim3(ROPE_THREADS);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return D == 64 ? rope_pick<64>(act, a, cfg) : rope_pick<128>(act, a, cfg);
+}
+
+cudaError_t launch_keep(const KeepArgs &a, cudaStream_t st) {
+    const int64_t warps = (int64_t)a.L * a.Hk * a.n_entries;
+    if (warps <= 0) return cudaSuccess;
+    keep_kernel<<<(unsigned)((warps + KEEP_THREADS / 32 - 1) / (KEEP_THREADS / 32)), KEEP_THREADS, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+} // namespace kvc

@@ -80,6 +80,10 @@ def load():
         "kvc_decode_step": (i32, [p, i32, i32, p, p, p, p, p, p, C.c_float, p]),
         "kvc_attn_cross": (i32, [p, i32, i32, p, p, i32, p, p, p, p, C.c_float, p]),
         "kvc_attn_weight": (i32, [p, i32, i32, p, p, i32, p, p, p, C.c_float, p, C.c_int64, p]),
+        "kvc_attn_tree": (i32, [p, i32, i32, p, p, i32, p, p, p, C.c_float, p]),
+        "kvc_append_rope": (i32, [p, i32, i32, p, p, p, i32, p, C.c_int64, p, C.c_int64, p, C.c_int64, p, p, C.c_float,
+                                  p, p]),
+        "kvc_seq_keep": (i32, [p, i32, p, p, p, p, p]),
         "kvc_seq_rm": (i32, [p, i32, i32, i32]),
         "kvc_seq_cp": (i32, [p, i32, i32, i32, i32]),
         "kvc_seq_add": (i32, [p, i32, i32, i32, i32]),
@@ -102,6 +106,8 @@ def load():
         "kvc_debug_chunk_plan_seq": (i32, [i32, i32, i32, i32, i32, i32, i32, i32, p, p, C.POINTER(C.c_int32)]),
         "kvc_debug_block_kernel": (i32, [p, i32]),
         "kvc_debug_block_plan": (i32, [i32] * 6 + [p] * 9),
+        "kvc_debug_tree_plan": (i32, [i32] * 4 + [p] * 10),
+        "kvc_debug_rope_turns": (i32, [C.c_float, i32, p]),
         "kvc_debug_select_rows": (i32, [p, i32, i32, i32, i32, p, C.POINTER(C.c_int64), C.POINTER(C.c_int64),
                                         C.POINTER(C.c_int32)]),
         "kvc_set_timeout_ms": (i32, [p, i32]),
@@ -239,6 +245,21 @@ def _block_tensor(name, t, device, dtype, numel):
         raise KvcError(KVC_EINVAL, "%s holds %d values, %d are needed" % (name, t.numel(), numel))
 
 
+def _head_rows(name, t, device, dtype, tokens, heads, dim):
+    """Refuse what is not [tokens][heads][dim] with contiguous tokens; returns the elements from token to token."""
+    if not isinstance(t, _torch.Tensor) or t.get_device() != device:
+        raise KvcError(KVC_EINVAL, "%s must be a tensor on cuda:%d" % (name, device))
+    if t.dtype is not dtype:
+        raise KvcError(KVC_EINVAL, "%s must be %s, not %s" % (name, dtype, t.dtype))
+    shape = t.shape
+    if len(shape) != 3 or shape[0] < tokens or shape[1] != heads or shape[2] != dim:
+        raise KvcError(KVC_EINVAL, "%s must be [%d][%d][%d]" % (name, tokens, heads, dim))
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != dim):
+        raise KvcError(KVC_EINVAL, "%s: a token's head-rows must be contiguous" % name)
+    return st[0] if shape[0] > 1 else max(st[0], heads * dim)
+
+
 def _block(seq_ids, n_q):
     if len(seq_ids) != len(n_q):
         raise KvcError(KVC_EINVAL, "one token count per sequence")
@@ -256,6 +277,49 @@ def kvc_attn_weight(ctx, layer, seq_ids, n_q, act, q, lse, w, w_stride, kq_scale
     ids, nq = _block(seq_ids, n_q)
     _check(ctx, load().kvc_attn_weight(ctx, layer, len(seq_ids), ids, nq, int(act), _addr(q), _addr(lse), _addr(n_vis),
                                        float(kq_scale), _addr(w), int(w_stride), _stream(stream, device)))
+
+
+def kvc_attn_tree(ctx, layer, seq_ids, n_q, act, q, out, kq_scale, parent=None, stream=None, device=0):
+    ids, nq = _block(seq_ids, n_q)
+    _check(ctx, load().kvc_attn_tree(ctx, layer, len(seq_ids), ids, nq, int(act), _addr(q), _addr(out), _addr(parent),
+                                     float(kq_scale), _stream(stream, device)))
+
+
+def _host_ints(x):
+    """Host int32 values as ctypes can pass them: (address or array, count); the first is to be kept until the call."""
+    if hasattr(x, "ctypes"):
+        import numpy as np
+
+        a = np.ascontiguousarray(x, np.int32) if x.dtype != np.int32 or not x.flags.c_contiguous else x
+        if a.size and not np.array_equal(a.ravel(), x.ravel()):
+            raise KvcError(KVC_ERANGE, "positions must fit 32 bits")
+        return a, a.size
+    x = [int(v) for v in x]
+    if any(v != C.c_int32(v).value for v in x):
+        raise KvcError(KVC_ERANGE, "positions must fit 32 bits")
+    return (C.c_int32 * len(x))(*x), len(x)
+
+
+def kvc_append_rope(ctx, layer, seq_ids, n_tok, pos, act, q, q_stride, k, k_stride, v, v_stride, q_out, q_norm=None,
+                    k_norm=None, eps=1e-6, stream=None, device=0):
+    ids, nt = _block(seq_ids, n_tok)
+    ps, n = _host_ints(pos)
+    if n < sum(nt):
+        raise KvcError(KVC_EINVAL, "%d positions for %d tokens" % (n, sum(nt)))
+    at = ps.ctypes.data if hasattr(ps, "ctypes") else ps
+    _check(ctx, load().kvc_append_rope(ctx, layer, len(seq_ids), ids, nt, at, int(act), _addr(q), int(q_stride),
+                                       _addr(k), int(k_stride), _addr(v), int(v_stride), _addr(q_norm), _addr(k_norm),
+                                       float(eps), _addr(q_out), _stream(stream, device)))
+
+
+def kvc_seq_keep(ctx, seq_ids, n_last, keep, stream=None, device=0):
+    """keep: for each sequence the places among its last n_last rows that stay, ascending."""
+    if len(keep) != len(seq_ids):
+        raise KvcError(KVC_EINVAL, "one list of places per sequence")
+    ids, nl = _block(seq_ids, n_last)
+    nk = (C.c_int32 * len(keep))(*map(len, keep))
+    flat = (C.c_int32 * sum(nk))(*(int(p) for places in keep for p in places))
+    _check(ctx, load().kvc_seq_keep(ctx, len(seq_ids), ids, nl, nk, flat, _stream(stream, device)))
 
 
 class kvc_trace_event(C.Structure):
@@ -449,6 +513,29 @@ def kvc_debug_block_plan(n_head, n_head_kv, head_dim, act, sms, rows, n_q):
             **{k: b.value for k, b in zip(("items", "part_rows", "part_cap"), big)}}
 
 
+def kvc_debug_tree_plan(n_head, n_head_kv, sms, rows, off, n_q):
+    """How a tree attention launch cuts its sequences, without a context or a GPU (as kvc_debug_block_plan)."""
+    n = len(rows)
+    r, o, t = ((C.c_int32 * n)(*[int(x) for x in a]) for a in (rows, off, n_q))
+    wh, sp, sr, tm = (C.c_int32 * n)(), (C.c_int32 * n)(), (C.c_int32 * n)(), C.c_int32()
+    big = [C.c_int64() for _ in range(3)]
+    st = load().kvc_debug_tree_plan(n_head, n_head_kv, sms, n, r, o, t, C.byref(tm), wh, sp, sr,
+                                    *[C.byref(b) for b in big])
+    if st != KVC_OK:
+        raise KvcError(st, "bad tree-plan arguments")
+    return {"tile_m": tm.value, "whole": list(wh), "splits": list(sp), "split_rows": list(sr),
+            **{k: b.value for k, b in zip(("items", "part_rows", "part_cap"), big)}}
+
+
+def kvc_debug_rope_turns(rope_base, head_dim):
+    """The turn that one position adds to every rotary pair, in units of 2^-64, without a context or a GPU."""
+    out = (C.c_uint64 * 64)()
+    st = load().kvc_debug_rope_turns(float(rope_base), int(head_dim), out)
+    if st != KVC_OK:
+        raise KvcError(st, "bad rotary base or head size")
+    return list(out)[:head_dim // 2]
+
+
 def kvc_debug_select_rows(pos, p0, p1, linear=False):
     """The rows a sequence operation selects for positions [p0, p1) of a
     sequence holding `pos`, without a context or a GPU: (rows, first,
@@ -525,6 +612,37 @@ class KVCache:
         self._block_io(q, out, lse, n_vis, total)
         kvc_attn_cross(self.ctx, layer, seq_ids, n_q, act, q, out, kq_scale, lse, n_vis, stream, self.device)
 
+    def attn_tree(self, layer, seq_ids, n_q, q, out, kq_scale, parent=None, stream=None):
+        """Attention of drafted tokens that are the last n_q[i] rows of sequence seq_ids[i]: each sees the rows
+        before those, its ancestors' and its own.  q, out [T][n_head][head_dim]; parent [T] int32 on the device, counted
+        within a sequence's tokens (negative: a root), or None (a chain)."""
+        act, total = _act(q), sum(map(int, n_q))
+        self._block_io(q, out, None, parent, total, "parent")
+        kvc_attn_tree(self.ctx, layer, seq_ids, n_q, act, q, out, kq_scale, parent, stream, self.device)
+
+    def append_rope(self, layer, seq_ids, n_tok, pos, q, k, v, q_out, q_norm=None, k_norm=None, eps=1e-6, stream=None):
+        """Append n_tok[i] tokens to sequence seq_ids[i] (packed) at the host positions pos [T]: q, q_out
+        [T][n_head][head_dim] (or both None) and k, v [T][n_head_kv][head_dim] of one type, q, k and v possibly columns
+        of one tensor; q_norm, k_norm [head_dim] fp32 or None."""
+        act, total, p = _act(k), sum(map(int, n_tok)), self.params
+        if (q is None) != (q_out is None):
+            raise KvcError(KVC_EINVAL, "q and q_out come together")
+        strides = [_head_rows("k", k, self.device, k.dtype, total, p.n_head_kv, p.head_dim),
+                   _head_rows("v", v, self.device, k.dtype, total, p.n_head_kv, p.head_dim), 0]
+        if q is not None:
+            strides[2] = _head_rows("q", q, self.device, k.dtype, total, p.n_head, p.head_dim)
+            _block_tensor("q_out", q_out, self.device, k.dtype, total * p.n_head * p.head_dim)
+        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if w is not None:
+                _block_tensor(name, w, self.device, _torch.float32, p.head_dim)
+        kvc_append_rope(self.ctx, layer, seq_ids, n_tok, pos, act, q, strides[2], k, strides[0], v, strides[1], q_out,
+                        q_norm, k_norm, eps, stream, self.device)
+
+    def keep(self, seq_ids, n_last, keep, stream=None):
+        """Of the last n_last[i] rows of sequence seq_ids[i] keep those at the places keep[i] (ascending); the
+        others leave.  Enqueued on the stream."""
+        kvc_seq_keep(self.ctx, seq_ids, n_last, keep, stream, self.device)
+
     def attn_weight(self, layer, seq_ids, n_q, q, lse, w, kq_scale, n_vis=None, stream=None):
         """Add the attention weight that the cached rows receive from a block of tokens to
         w [n_seq][n_head_kv][rows or more] fp32; lse as attn_cross wrote it for these tokens."""
@@ -544,7 +662,7 @@ class KVCache:
             raise KvcError(KVC_EINVAL, "w must be [n_head_kv][rows]")
         return kvc_seq_evict_weight(self.ctx, seq, p0, p1, n_remove, w, w.shape[1])
 
-    def _block_io(self, q, out, lse, n_vis, total):
+    def _block_io(self, q, out, lse, n_vis, total, per_token="n_vis"):
         p = self.params
         if total < 0:
             raise KvcError(KVC_EINVAL, "n_q must not be negative")
@@ -555,7 +673,7 @@ class KVCache:
         if lse is not None:
             _block_tensor("lse", lse, self.device, _torch.float32, total * p.n_head)
         if n_vis is not None:
-            _block_tensor("n_vis", n_vis, self.device, _torch.int32, total)
+            _block_tensor(per_token, n_vis, self.device, _torch.int32, total)
 
     def seq_rm(self, seq, p0, p1):
         kvc_seq_rm(self.ctx, seq, p0, p1)
