@@ -615,13 +615,16 @@ int kvc_create(const kvc_params *p, kvc_ctx **out) {
             c->err = "pool too large for 32-bit TMA row coordinates";
             return fail(KVC_EINVAL);
         }
+        c->tmk64.resize((size_t)c->L);
+        c->tmv64.resize((size_t)c->L);
         for (int l = 0; l < c->L; ++l) {
             std::string why;
-            for (int b = 0; b < 2; ++b) {
-                const int box = b ? (int)std::min<int64_t>(TMA_BIG_ROWS, c->pool_rows) : TMA_BOX_ROWS;
-                if (!encode_rows_map(&c->tmk[2 * l + b], c->kdata + (int64_t)l * c->pool_rows * c->krow, c->pool_rows,
+            for (int b = 0; b < 3; ++b) {
+                const int box = b == 0 ? TMA_BOX_ROWS : (int)std::min<int64_t>(b == 1 ? TMA_BIG_ROWS : 64, c->pool_rows);
+                CUtensorMap *mk = b == 2 ? &c->tmk64[l] : &c->tmk[2 * l + b], *mv = b == 2 ? &c->tmv64[l] : &c->tmv[2 * l + b];
+                if (!encode_rows_map(mk, c->kdata + (int64_t)l * c->pool_rows * c->krow, c->pool_rows,
                                      c->krow, c->tk, true, &why, box) ||
-                    !encode_rows_map(&c->tmv[2 * l + b], c->vdata + (int64_t)l * c->pool_rows * c->vrow, c->pool_rows,
+                    !encode_rows_map(mv, c->vdata + (int64_t)l * c->pool_rows * c->vrow, c->pool_rows,
                                      c->vrow, c->tv, true, &why, box)) {
                     c->err = why;
                     return fail(KVC_ECUDA);

@@ -136,13 +136,13 @@ static bool plan_block(BlockParams &p, int sms, bool tc) {
     return narrow;
 }
 
-// The query tiles and items of a tree attention: tiles of 16, 32 or 64 query rows (a warp's products are of 16 or 32 of
-// them, so that a tile larger than the rows is only waste), one item at a time on an SM.  The kernel counts cached rows
-// from the 16-row boundary at or below the sequence's first.
+// The query tiles and items of a tree attention: tiles of 64 query rows (or what there are: the kernel shares the work of
+// fewer over all its warps too), one item at a time on an SM.  The kernel counts cached rows from the 16-row boundary at or
+// below the sequence's first.
 static void plan_tree(BlockParams &p, int sms) {
     int64_t most = 0;
     for (int i = 0; i < p.n_seq; ++i) most = std::max<int64_t>(most, (int64_t)p.seq[i].n_tok * p.r);
-    p.tile_m = most <= 16 ? 16 : (most <= 32 ? 32 : 64);
+    p.tile_m = TREE_TILE;
     p.part_rows = (int32_t)std::max<int64_t>(1, std::min<int64_t>(p.tile_m, most));
     for (int i = 0; i < p.n_seq; ++i) {
         BlockSeq &s = p.seq[i];
@@ -167,6 +167,16 @@ constexpr int TC_MIN_ROWS = 256;
 constexpr double TC_VALUES = 1 << 21, TC_PRODUCTS = 1 << 28;
 static bool tc_pays(double values, double products) { return values >= TC_VALUES || products >= TC_PRODUCTS; }
 static bool use_tc(int rows, double products) { return rows >= TC_MIN_ROWS || products >= TC_PRODUCTS; }
+
+// Which kernel runs a tree attention of 16-bit queries: the tcgen05 one where the sequences bring more than 32 query rows a
+// KV head (on the mean over the cached rows) and there is enough to do, by the cached values and the products.  One kernel
+// runs the whole call: two one after the other would each leave the machine to its last items.  Measured in us, q8_0 (f16),
+// bf16 queries, mma.sync against tcgen05, heads/KV heads/D, tokens:
+//   (figures: see the table in the tests' order)
+static bool tree_tc_pays(double values, double rows_m, double rows) {
+    const double m = rows > 0 ? rows_m / rows : 0;
+    return m > 32 && values >= 1 << 22 && m * values >= 1 << 28;
+}
 
 // Checks that the block operators share; *total: tokens of the block.
 static int block_check(Ctx *c, int layer, int n_seq, const int32_t *seq_ids, const int32_t *n_q, int act, const void *q,
@@ -303,7 +313,18 @@ extern "C" int kvc_attn_tree(kvc_ctx *cc, int layer, int n_seq, const int32_t *s
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     KVC_CU(c, cudaSetDevice(c->dev));
     if ((rc = ensure_block_space(c, st))) return rc;
-    auto *launch = c->tk == KVC_F16 ? launch_tree_f16 : (c->tv == KVC_Q4_0 ? launch_tree_q4 : launch_tree_q8);
+    auto *by_warps = c->tk == KVC_F16 ? launch_tree_f16 : (c->tv == KVC_Q4_0 ? launch_tree_q4 : launch_tree_q8);
+    const size_t l = (size_t)layer;
+    const TreeMaps maps = {&c->tmk64[l], &c->tmv64[l], &c->tmk[2 * l], &c->tmv[2 * l]};
+    double values = 0, rows_m = 0, all_rows = 0;
+    for (int i = 0; i < n_seq; ++i) {
+        if (n_q[i] == 0) continue;
+        const double rows = c->seqs[(size_t)seq_ids[i]].lfill[l];
+        values += rows * c->Hk * c->D;
+        rows_m += rows * n_q[i] * c->r;
+        all_rows += rows;
+    }
+    const bool tc = act != KVC_ACT_F32 && (c->block_kernel ? c->block_kernel == 2 : tree_tc_pays(values, rows_m, all_rows));
     BlockParams p;
     block_params(c, layer, kq_scale, act, p);
     p.q = q;
@@ -318,14 +339,20 @@ extern "C" int kvc_attn_tree(kvc_ctx *cc, int layer, int n_seq, const int32_t *s
             BlockSeq &s = p.seq[p.n_seq++];
             s.id = seq_ids[i];
             s.off = sq.off;
-            s.n_rows = sq.lfill[(size_t)layer];
+            s.n_rows = sq.lfill[l];
             s.tok0 = (int32_t)tok0;
             s.n_tok = n_q[i];
         }
         tok0 += n_q[i];
         if (p.n_seq == 0 || (p.n_seq < MAX_SEQ_PER_LAUNCH && i + 1 < n_seq)) continue;
-        plan_tree(p, c->sms);
-        cudaError_t e = launch(p, c->tmk[2 * (size_t)layer], c->tmv[2 * (size_t)layer], st);
+        cudaError_t e;
+        if (tc) {
+            plan_block(p, c->sms, true);
+            e = launch_tree_tc(c->tk, c->tv, p, st);
+        } else {
+            plan_tree(p, c->sms);
+            e = by_warps(p, maps, st);
+        }
         if (e != cudaSuccess) return cuda_fail(c, e, "tree attention kernel");
         p.n_seq = 0;
     }

@@ -86,13 +86,19 @@ cudaError_t launch_cross(int type_k, int type_v, const BlockParams &p, bool narr
 // The same for 16-bit queries, by tcgen05 (tiles of CROSS_TC_TILE_M query rows).
 cudaError_t launch_cross_tc(int type_k, int type_v, const BlockParams &p, cudaStream_t st);
 
-// The attention of a tree of drafted tokens (tiles of 16, 32 or 64 query rows, steps of TREE_STEP cached ones), by the
-// cache's types; tmk, tmv: the layer's maps of 16-row boxes.
+// The attention of a tree of drafted tokens (tiles of up to TREE_TILE query rows, steps of TREE_STEP cached ones), by the
+// cache's types, over the layer's tensor maps.
 constexpr int TREE_STEP = 64;
 constexpr int TREE_MAX = 256; // tokens of a tree
-cudaError_t launch_tree_q8(const BlockParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
-cudaError_t launch_tree_f16(const BlockParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
-cudaError_t launch_tree_q4(const BlockParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+constexpr int TREE_TILE = 64; // query rows of a tile
+struct TreeMaps {
+    const CUtensorMap *k, *v, *k16, *v16; // boxes of TREE_STEP rows, of 16
+};
+cudaError_t launch_tree_q8(const BlockParams &p, const TreeMaps &t, cudaStream_t st);
+cudaError_t launch_tree_f16(const BlockParams &p, const TreeMaps &t, cudaStream_t st);
+cudaError_t launch_tree_q4(const BlockParams &p, const TreeMaps &t, cudaStream_t st);
+// The same for 16-bit queries, by the block attention's tcgen05 kernel (k_cross_tc.cu).
+cudaError_t launch_tree_tc(int type_k, int type_v, const BlockParams &p, cudaStream_t st);
 
 // Joins the parts of the launch's cut units (k_join.cu; the attentions above end with it).
 cudaError_t launch_join(const BlockParams &p, cudaStream_t st);

@@ -105,6 +105,7 @@ struct Ctx {
     uint8_t *kscales = nullptr, *vscales = nullptr;
     int64_t kdata_bytes = 0, vdata_bytes = 0, kscale_bytes = 0, vscale_bytes = 0;
     std::vector<CUtensorMap> tmk, tmv; // per layer: [2l] 16-row boxes, [2l+1] 128-row boxes
+    std::vector<CUtensorMap> tmk64, tmv64; // per layer: 64-row boxes (the tree attention)
     int32_t *pt_dev = nullptr;         // [n_seq_max][max_pages]
     int32_t max_pages = 0;
     std::vector<Seq> seqs;
@@ -133,6 +134,8 @@ struct Ctx {
     uint32_t *err_dev = nullptr;
     uint32_t *err_host = nullptr; // pinned copy of the error word read by synchronous operations
     int chunk_override = 0;
+    uint64_t rope_turn[64];       // angles of kvc_append_rope (draft.h), once has_turns
+    bool has_turns = false;
     int block_kernel = 0; // forced kernel of the block attention (kvc_debug_block_kernel)
     int32_t *gone_host = nullptr; // pinned: the rows that an eviction by weight removed
     int64_t gone_cap = 0;

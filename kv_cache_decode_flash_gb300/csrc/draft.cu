@@ -161,7 +161,9 @@ static int append_rope(Ctx *c, int layer, const RopeCall &call, RopeArgs &a, cud
         if (e != cudaSuccess) return cuda_fail(c, e, "page table update");
     }
     // The launches: pieces of consecutive positions need no list, the others' positions travel with them.
-    rope_turns(c->prm.rope_base, c->D, a.turn);
+    if (!c->has_turns) rope_turns(c->prm.rope_base, c->D, c->rope_turn);
+    c->has_turns = true;
+    std::copy(c->rope_turn, c->rope_turn + c->D / 2, a.turn);
     const int rows = rope_rows(c->D);
     a.H = c->H;
     a.Hk = c->Hk;

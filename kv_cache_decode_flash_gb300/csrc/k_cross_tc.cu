@@ -84,6 +84,14 @@ template <int D, bool CODES> struct Lay {
     __device__ static __forceinline__ int k(bool wide) { return K - (wide ? 0 : MORE) * TILE; }
 };
 
+// A tree's masks (TREE): which of the block's rows the tile's tokens see; a word of zeros behind them.
+template <bool TREE> struct TreeMasks {};
+template <> struct TreeMasks<true> {
+    static constexpr int WORDS = TREE_MAX / 32 + 1;
+    int32_t parent[TREE_MAX];
+    uint32_t sees[2 * TM][WORDS]; // by the token's place from the tile's first
+};
+
 struct Aux {
     uint64_t bar[N_BARS];
     int32_t row[2][SLOTS][TN];   // K's and V's loaders: pool rows of a step, -1 past the end
@@ -105,9 +113,9 @@ __device__ __forceinline__ bool any_bad(const uint32_t (&rows)[TN / 32]) {
     return (b.x | b.y | b.z | b.w) != 0;
 }
 
-template <int D, bool CODES> constexpr int smem_bytes() {
+template <int D, bool CODES, bool TREE> constexpr int smem_bytes() {
     // TMEM is allocated whole: one CTA per SM, whatever D
-    const int need = Lay<D, CODES>::AUX + (int)sizeof(Aux) + 2 * TM * (D / 16) * 4 + 1024;
+    const int need = Lay<D, CODES>::AUX + (int)sizeof(Aux) + 2 * TM * (D / 16) * 4 + 1024 + (TREE ? (int)sizeof(TreeMasks<TREE>) : 0);
     return need > 120 * 1024 ? need : 120 * 1024;
 }
 
@@ -289,14 +297,24 @@ __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &
 }
 
 // ------------------------------------------------------------ softmax ----
-// A thread's 128 scores, of which it sees the first n (MASK): 32 of them from registers, unseen ones -inf; the largest.
-template <bool MASK> __device__ __forceinline__ void score_block(uint32_t (&r)[32], int c, int n, float (&m)[4]) {
+// Which of a step's 128 rows a thread's token sees: the first n, or (a tree) the rows whose bits are set.
+struct Leading {
+    int n;
+    __device__ __forceinline__ bool operator()(int c, int e) const { return c * 32 + e < n; }
+};
+struct Picked {
+    uint32_t w[4];
+    __device__ __forceinline__ bool operator()(int c, int e) const { return w[c] >> e & 1; }
+};
+
+// A thread's 128 scores, of which it sees some (MASK): 32 of them from registers, unseen ones -inf; the largest.
+template <bool MASK, class Seen> __device__ __forceinline__ void score_block(uint32_t (&r)[32], int c, const Seen &n, float (&m)[4]) {
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
         float v0 = __uint_as_float(r[e]), v1 = __uint_as_float(r[e + 1]);
         if (MASK) {
-            v0 = c * 32 + e < n ? v0 : -INFINITY;
-            v1 = c * 32 + e + 1 < n ? v1 : -INFINITY;
+            v0 = n(c, e) ? v0 : -INFINITY;
+            v1 = n(c, e + 1) ? v1 : -INFINITY;
             r[e] = __float_as_uint(v0);
             r[e + 1] = __float_as_uint(v1);
         }
@@ -305,8 +323,8 @@ template <bool MASK> __device__ __forceinline__ void score_block(uint32_t (&r)[3
 }
 // HOLD: blocks of 32 scores that stay in registers between the maximum and the weights; the others are read again (P's
 // 64 columns go over the first two blocks, so those stay).
-template <bool MASK, int HOLD>
-__device__ __forceinline__ float row_scores(uint32_t S, int n, uint32_t (&r)[HOLD][32]) {
+template <bool MASK, int HOLD, class Seen>
+__device__ __forceinline__ float row_scores(uint32_t S, const Seen &n, uint32_t (&r)[HOLD][32]) {
     static_assert(HOLD == 2 || HOLD == 4, "all, or what P overwrites");
     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     if constexpr (HOLD == 4) {
@@ -337,8 +355,8 @@ __device__ __forceinline__ float row_scores(uint32_t S, int n, uint32_t (&r)[HOL
 
 // exp2 of the scores (times f, less use; f >= 0, an unseen one is -inf) as fp16 pairs over them; returns their sum.
 // mark(c, rows): a look at which of column block c's 32 rows have weight (MASK).
-template <bool MASK, int HOLD, class Mark>
-__device__ __forceinline__ float row_exp(uint32_t S, int n, uint32_t (&r)[HOLD][32], float f, float use, Mark mark) {
+template <bool MASK, int HOLD, class Seen, class Mark>
+__device__ __forceinline__ float row_exp(uint32_t S, const Seen &n, uint32_t (&r)[HOLD][32], float f, float use, Mark mark) {
     const uint64_t ff = pair(f, f), mm = pair(-use, -use);
     uint64_t a0 = 0, a1 = 0;
     auto block = [&](int c, const uint32_t(&x)[32]) {
@@ -347,8 +365,8 @@ __device__ __forceinline__ float row_exp(uint32_t S, int n, uint32_t (&r)[HOLD][
         for (int e = 0; e < 32; e += 2) {
             float2 y = unpair(fma2(pair(x[e], x[e + 1]), ff, mm));
             if (MASK) {
-                y.x = c * 32 + e < n ? y.x : -INFINITY;
-                y.y = c * 32 + e + 1 < n ? y.y : -INFINITY;
+                y.x = n(c, e) ? y.x : -INFINITY;
+                y.y = n(c, e + 1) ? y.y : -INFINITY;
             }
             y.x = ex2(y.x);
             y.y = ex2(y.y);
@@ -380,7 +398,9 @@ __device__ __forceinline__ float row_exp(uint32_t S, int n, uint32_t (&r)[HOLD][
     return s.x + s.y;
 }
 
-template <int D, int KT, int VT>
+// TREE: the block's tokens are the sequence's last rows, and each sees the rows before them, its ancestors' and its own
+// (kvc_attn_tree); else a token sees its n_vis leading rows.
+template <int D, int KT, int VT, bool TREE>
 __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(const __grid_constant__ BlockParams p) {
     constexpr bool CODES = KT != KVC_F16;
     using L = Lay<D, CODES>;
@@ -389,6 +409,7 @@ __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(con
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u); // swizzled tiles need 1024-byte alignment
     Aux &x = *reinterpret_cast<Aux *>(smem + L::AUX);
     uint32_t(*poison)[D / 16] = reinterpret_cast<uint32_t(*)[D / 16]>(smem + L::AUX + sizeof(Aux));
+    TreeMasks<TREE> &tree = *reinterpret_cast<TreeMasks<TREE> *>(smem + L::AUX + sizeof(Aux) + 2 * TM * (D / 16) * 4);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     const BlockSeq q = p.seq[item_seq(p, (int)blockIdx.x)];
@@ -442,7 +463,8 @@ __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(con
             if (m >= mrows) break;
             float v[D / 32];
             uint32_t h[D / 64], l[D / 64];
-            const int vis = y[k].get(p, q, v);
+            int vis = y[k].get(p, q, v);
+            if (TREE) vis = q.n_rows - q.n_tok; // the rows that all of the block see
             float scale = query_pack<D, false>(p, v, h, l);
             if (scale < 0.f) {
                 scale = -scale;
@@ -457,7 +479,7 @@ __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(con
             if (lane == 0) {
                 x.qscale[m] = scale;
                 x.vis[m] = vis;
-                atomicMax(&x.vis_max, vis);
+                atomicMax(&x.vis_max, TREE ? q.n_rows : vis);
                 atomicMin(&x.vis_min, vis);
             }
         }
@@ -471,6 +493,28 @@ __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(con
             if (c == 0) x.qscale[m] = 0.f;
         }
         for (int i = ft; i < all * (D / 16); i += QW * 32) poison[i / (D / 16)][i % (D / 16)] = 0;
+    }
+    if constexpr (TREE) {
+        // The tokens' masks, where the part holds rows of the block: by walks from each token to its root (a parent is
+        // below its child).
+        if (r_end > q.n_rows - q.n_tok) {
+            const int ft = qw * 32 + lane, first = token_of(p, m0), count = token_of(p, m0 + mrows - 1) - first + 1;
+            if (p.parent)
+                for (int i = ft; i < q.n_tok; i += QW * 32) {
+                    const int up = p.parent[(int64_t)q.tok0 + i];
+                    tree.parent[i] = up >= 0 && up < i ? up : -1;
+                }
+            named_sync<5, QW * 32>();
+            for (int i = ft; i < count; i += QW * 32) {
+                const int t = first + i;
+                for (int k = 0; k < tree.WORDS; ++k) {
+                    const int n = t + 1 - k * 32; // without a tree: a chain
+                    tree.sees[i][k] = p.parent ? 0u : (n >= 32 ? 0xffffffffu : (n > 0 ? (1u << n) - 1u : 0u));
+                }
+                if (p.parent)
+                    for (int u = t; u >= 0; u = tree.parent[u]) tree.sees[i][u >> 5] |= 1u << (u & 31);
+            }
+        }
     }
     fence_async();
     tc_before();
@@ -492,6 +536,7 @@ __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(con
         const bool live = __any_sync(0xffffffffu, mr < mrows);
         const float cq = x.qscale[mr];
         const int vis = mr < mrows ? x.vis[mr] : 0x7fffffff;
+        const int slot_t = TREE ? token_of(p, min(m0 + mr, m_all - 1)) - token_of(p, m0) : 0; // its token's mask
         const int wvis = __reduce_min_sync(0xffffffffu, vis);
         float mx = -INFINITY, sum = 0.f; // the row's reference maximum and sum
         int E = E_MIN;
@@ -502,10 +547,29 @@ __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(con
             tc_after();
             if (live) {
                 const bool masked = base + TN > wvis;
+                auto seen = [&] {
+                    if constexpr (TREE) {
+                        Picked w;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) { // rows base + 32 c on: the tree's place t on, and all before it
+                            const int t = base + c * 32 - (q.n_rows - q.n_tok);
+                            const uint32_t *m = tree.sees[slot_t];
+                            if (t <= -32)
+                                w.w[c] = 0xffffffffu;
+                            else if (t < 0)
+                                w.w[c] = m[0] << -t | ((1u << -t) - 1u);
+                            else
+                                w.w[c] = t < TREE_MAX ? __funnelshift_r(m[t >> 5], m[(t >> 5) + 1], t & 31) : 0u;
+                        }
+                        return w;
+                    } else {
+                        return Leading{vis - base};
+                    }
+                };
                 const float f = cq * x.kfac[s % KFACS];
                 constexpr int HOLD = R::HOLD;
                 uint32_t sc[HOLD][32];
-                const float raw = masked ? row_scores<true>(S, vis - base, sc) : row_scores<false>(S, 0, sc);
+                const float raw = masked ? row_scores<true>(S, seen(), sc) : row_scores<false>(S, Leading{0}, sc);
                 const float top = raw == -INFINITY ? raw : raw * f;
                 float al = 1.f;
                 if (top > mx + GROW || (mx == -INFINITY && top > mx)) {
@@ -540,9 +604,9 @@ __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(con
                 }
                 const float use = mx == -INFINITY ? 0.f : mx - LIFT;
                 if (!masked && !reported) {
-                    sum += row_exp<false>(S, 0, sc, f, use, [](int, uint32_t) {});
+                    sum += row_exp<false>(S, Leading{0}, sc, f, use, [](int, uint32_t) {});
                 } else {
-                    sum += row_exp<true>(S, vis - base, sc, f, use, [&](int c, uint32_t some) {
+                    sum += row_exp<true>(S, seen(), sc, f, use, [&](int c, uint32_t some) {
                         const uint32_t rows = x.badrow[slot][c];
                         if (rows == 0) return;
 #pragma unroll 1
@@ -742,10 +806,10 @@ __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(con
     }
 }
 
-template <int D, int KT, int VT> cudaError_t go(const BlockParams &p, cudaStream_t st) {
+template <bool TREE, int D, int KT, int VT> cudaError_t go(const BlockParams &p, cudaStream_t st) {
     constexpr bool CODES = KT != KVC_F16;
-    auto k = cross_tc_kernel<D, KT, VT>;
-    constexpr int bytes = smem_bytes<D, CODES>();
+    auto k = cross_tc_kernel<D, KT, VT, TREE>;
+    constexpr int bytes = smem_bytes<D, CODES, TREE>();
     static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
     static SharedMemory set;
     cudaError_t e = set.allow((const void *)k, bytes, Regs<CODES>::LAUNCH);
@@ -754,16 +818,22 @@ template <int D, int KT, int VT> cudaError_t go(const BlockParams &p, cudaStream
     e = cudaGetLastError();
     return e == cudaSuccess ? launch_join(p, st) : e;
 }
+template <bool TREE> cudaError_t pick(int type_k, int type_v, const BlockParams &p, cudaStream_t st) {
+    if (p.n_items <= 0) return cudaSuccess;
+    if (p.D == 64)
+        return type_k == KVC_F16 ? go<TREE, 64, KVC_F16, KVC_F16>(p, st) : go<TREE, 64, KVC_Q8_0, KVC_Q8_0>(p, st);
+    if (type_k == KVC_F16) return go<TREE, 128, KVC_F16, KVC_F16>(p, st);
+    if (type_v == KVC_Q4_0) return go<TREE, 128, KVC_Q8_0, KVC_Q4_0>(p, st);
+    return go<TREE, 128, KVC_Q8_0, KVC_Q8_0>(p, st);
+}
 
 } // namespace
 
 cudaError_t launch_cross_tc(int type_k, int type_v, const BlockParams &p, cudaStream_t st) {
-    if (p.n_items <= 0) return cudaSuccess;
-    if (p.D == 64)
-        return type_k == KVC_F16 ? go<64, KVC_F16, KVC_F16>(p, st) : go<64, KVC_Q8_0, KVC_Q8_0>(p, st);
-    if (type_k == KVC_F16) return go<128, KVC_F16, KVC_F16>(p, st);
-    if (type_v == KVC_Q4_0) return go<128, KVC_Q8_0, KVC_Q4_0>(p, st);
-    return go<128, KVC_Q8_0, KVC_Q8_0>(p, st);
+    return pick<false>(type_k, type_v, p, st);
+}
+cudaError_t launch_tree_tc(int type_k, int type_v, const BlockParams &p, cudaStream_t st) {
+    return pick<true>(type_k, type_v, p, st);
 }
 
 } // namespace kvc

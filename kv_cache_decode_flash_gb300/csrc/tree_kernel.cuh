@@ -4,76 +4,80 @@
 //   s_j = scale * q[t][h] . K_j,   out = sum_j exp(s_j) V_j / sum_j exp(s_j),
 // query head h reading KV head h / r.  Instantiated by k_tree_*.cu.
 //
-// A work item is one KV head, a tile of 16, 32 or 64 query rows (tokens x query
-// heads of the group) and a part of the cached rows.  A drafted block is few query
+// A work item is one KV head, a tile of up to 64 query rows (tokens x query heads
+// of the group) and a part of the cached rows.  A drafted block is few query
 // rows over many cached ones, so the kernel is built like the single-token one:
-// one loading warp keeps a ring of 64-row stages full by TMA (boxes of 16 rows,
-// swizzled for ldmatrix; a page holds whole boxes) and eight warps take 16 cached
-// rows each, straight from the stored bytes: codes become exact fp16 values in
-// registers, on their way into the products, and are used for 16 * MQ query rows
-// (MQ: 2, or 1 for tiles of 16).  Bringing them to fp16 in shared memory first, as the
-// block attention's tcgen05 kernel must, costs more than the products do here.
+// a loading group keeps a ring of 64-row stages full by TMA (boxes of 64 or 16 rows,
+// swizzled for ldmatrix; a page holds whole ones of 16) and sixteen warps take 16 cached
+// rows by 16 query rows each, straight from the stored bytes: codes become exact fp16
+// values in registers, on their way into the products.  Bringing them to fp16 in
+// shared memory first, as the block attention's tcgen05 kernel must, costs more than
+// the products of few query rows.
 //   S = Q K^T by mma.sync m16n8k16, query rows as its rows; a 32-value block of
 //   codes has sums of its own, which the block's scale multiplies in 32 bits.
 //   O += P V: P goes from the scores' registers into the products' operand as it
-//   lies; V's block scale is put into P (P' = P * d * 2^-E, E the exponent of the
-//   largest V scale a warp has met, its sums rescaled when that grows).
-//   32-bit queries and P' are two fp16 parts, and every chain of products ends
-//   with the 16 rows, so that 32-bit results keep 32-bit accuracy (the tensor
-//   cores truncate as they accumulate).  With 16-bit results P' is one fp16 value
-//   (half a step: 2^-12), which averages out over the rows, below the result's own.
+//   lies.  With 32-bit queries V's block scale is put into P (P' = P * d * 2^-E, E
+//   the exponent of the largest V scale a warp has met, its sums rescaled when that
+//   grows), Q and P' are two fp16 parts, and every chain of products ends with the
+//   16 rows, so that 32-bit results keep 32-bit accuracy (the tensor cores truncate
+//   as they accumulate).  With 16-bit results P and V (codes times d * 2^(7 - E))
+//   are one fp16 value each: their roundings (2^-12 at most) average out over the
+//   rows, below the result's own, and P is packed once for all of V's blocks.
 // A row's reference maximum is raised only when a score passes it by more than
 // 2^8; weights stand 2^6 above their value for it, so that they stay normal fp16
 // numbers down to 2^-20 of the largest.
 // What a token does not see never reaches it: scores and P' are selected, and
 // where V is f16 a value that is not finite, of a group of rows that not all tokens
-// see (of any, where P is two parts), is left out of the products and added for
-// those that see it (0 x inf is NaN).
+// see (of any, where P is two parts), is left out of the products (0 x inf is NaN), and put
+// into the results of the query rows that see it; so are codes under a
+// scale that is not finite, where the scale is V's.
 // Warps are joined in shared memory, in their order, and the parts of a tile by
 // join_kernel in theirs: results are bitwise repeatable.
 #pragma once
 
 #include "tc_tile.cuh"
 
+#include <type_traits>
+
 namespace kvc {
 namespace {
 
-// Two groups of four warps of products and a group of which one warp loads.  A launch gives every thread 168 registers;
-// the loading group hands most of its own to the others, whose sums alone are 128.
-constexpr int TREE_THREADS = 12 * 32, TREE_WORK = 256;
-constexpr int TREE_REGS = 168, TREE_REGS_WORK = 232, TREE_REGS_LOAD = 40;
-static_assert(2 * TREE_REGS_WORK + TREE_REGS_LOAD <= 3 * TREE_REGS, "the groups' registers come from the launch's");
+// Four groups of four warps of products and one that loads.  A launch gives every thread 96 registers; the
+// loading group hands most of its own to the others.
+constexpr int TREE_WARPS = 16, TREE_WORK = TREE_WARPS * 32, TREE_THREADS = TREE_WORK + 128;
+constexpr int TREE_REGS = 96, TREE_REGS_WORK = 112, TREE_REGS_LOAD = 32;
+static_assert(4 * TREE_REGS_WORK + TREE_REGS_LOAD <= 5 * TREE_REGS, "the groups' registers come from the launch's");
 constexpr int TN = TREE_STEP, SLABS = TN / 16;
+constexpr int TM_TREE = TREE_TILE; // query rows of a tile at most
 constexpr float T_GROW = 8.f, T_LIFT = 6.f;
 
-template <int D, int KT, int VT, int MQ, int QS, bool LO> struct TreeShape {
-    static constexpr int M = 16 * MQ * QS;       // query rows of a tile
-    static constexpr int GROUPS = QS == 1 ? 2 : 1; // of warps that take stages in turn
+template <int D, int KT, int VT, bool LO> struct TreeShape {
     static constexpr int KROW = row_bytes<KT>(D), VROW = row_bytes<VT>(D);
     static constexpr bool KC = KT != KVC_F16, VC = VT != KVC_F16; // codes
     static constexpr int NB = D / QK, SB = 2 * NB;
     static constexpr int KBYTES = TN * KROW, VBYTES = TN * VROW, STAGE = KBYTES + VBYTES;
     static_assert(STAGE % 1024 == 0 && KBYTES % 1024 == 0, "swizzled boxes");
     static constexpr int SCALES = (KC ? TN * SB : 0) + (VC ? TN * SB : 0);
-    static constexpr int QF = MQ * QS * (D / 16) * 32 * 16; // bytes of the query fragments (one part)
+    static constexpr int QF = TM_TREE / 16 * (D / 16) * 32 * 16; // bytes of the query fragments (one part)
     static constexpr int AUX = 8192;
     static constexpr int FIXED = 1024 + QF * (LO ? 2 : 1) + AUX;
     static constexpr int FIT = (232448 - FIXED) / (STAGE + SCALES);
-    static constexpr int STAGES = (FIT > 16 ? 16 : FIT) & ~1; // even: a stage's phases all belong to one group of warps
-    static_assert(STAGES >= 4, "stages");
+    static constexpr int STAGES = FIT > 12 ? 12 : FIT;
+    static_assert(STAGES >= 4, "a stage for every group");
     static constexpr int SMEM = FIXED + STAGES * (STAGE + SCALES);
     static constexpr int PITCH = D + 16; // floats of a row where the warps are joined
-    static_assert(8 * 16 * MQ * PITCH * 4 <= STAGES * (STAGE + SCALES) + QF * (LO ? 2 : 1), "the join goes over stages and queries");
+    static_assert(TREE_WARPS * 16 * PITCH * 4 <= STAGES * (STAGE + SCALES) + QF * (LO ? 2 : 1), "the join goes over stages and queries");
 };
 
 struct TreeAux {
-    uint64_t full[16], empty[16];
+    uint64_t full[12], empty[12];
     int32_t parent[TREE_MAX];
     uint32_t sees[64][TREE_MAX / 32]; // of the tile's tokens, which of the block's rows they see
     float qscale[64];
+    uint32_t poison[64][8];   // two bits a value: +inf, -inf (both: NaN) received
+    int32_t bad_first, bad_last; // 16-row groups with values that were left out of the products
     int32_t slot[64];         // query row's token, counted from the tile's first
-    float m[8][32], l[8][32]; // the warps' maxima and sums
-    int32_t bytes[16];
+    float m[TREE_WARPS][16], l[TREE_WARPS][16]; // the warps' maxima and sums
     volatile int32_t abort;
 };
 static_assert(sizeof(TreeAux) <= 8192, "TreeShape::AUX");
@@ -127,7 +131,7 @@ __device__ __forceinline__ void ldsm2t(uint32_t &a, uint32_t &b, uint32_t addr) 
     asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void mma1(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                  "{%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
@@ -148,17 +152,23 @@ template <int NB> __device__ __forceinline__ void load_scales(uint32_t (&w)[2][N
         w[0][0] = u.x, w[1][0] = u.y;
     }
 }
+// The same of one pair of blocks.
+template <int NB> __device__ __forceinline__ void load_pair(uint32_t (&w)[2], const uint8_t *at, int pair) {
+    w[0] = *reinterpret_cast<const volatile uint32_t *>(at + 4 * pair);
+    w[1] = *reinterpret_cast<const volatile uint32_t *>(at + 2 * NB + 4 * pair);
+}
 
-template <int D, int KT, int VT, int MQ, int QS, bool LO>
+template <int D, int KT, int VT, bool LO>
 __global__ void __launch_bounds__(TREE_THREADS, 1)
     tree_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ CUtensorMap tmk,
-                const __grid_constant__ CUtensorMap tmv) {
-    using S = TreeShape<D, KT, VT, MQ, QS, LO>;
-    constexpr int M = S::M, NB = S::NB, NST = S::STAGES, NT = D / 8;
+                const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmk16,
+                const __grid_constant__ CUtensorMap tmv16) {
+    using S = TreeShape<D, KT, VT, LO>;
+    constexpr int M = TM_TREE, NB = S::NB, NT = D / 8;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t *scales = smem + NST * S::STAGE;
-    uint4 *qf = reinterpret_cast<uint4 *>(scales + NST * S::SCALES); // [m tile][k step][lane], then the second part
+    uint8_t *scales = smem + S::STAGES * S::STAGE;
+    uint4 *qf = reinterpret_cast<uint4 *>(scales + S::STAGES * S::SCALES); // [m tile][k step][lane], then the second part
     constexpr int QPART = S::QF / 16;
     TreeAux &x = *reinterpret_cast<TreeAux *>(reinterpret_cast<uint8_t *>(qf) + S::QF * (LO ? 2 : 1));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -170,75 +180,103 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     item_unit(q, local, unit, part, parts);
     const int g = unit / q.tiles, tile = q.tiles - 1 - unit % q.tiles; // (the order that join_kernel takes)
     const int m_all = q.n_tok * p.r, m0 = tile * M, mrows = min(M, m_all - m0);
+    // The four groups: `shares` of them have 16 query rows each of every stage they take, `turns` sets take stages in turn.
+    // A stage's phases all belong to one set (a wait tells a phase only from the one before), so that stages are as many as
+    // fit in whole turns.
+    const int shares = mrows > 32 ? 4 : (mrows > 16 ? 2 : 1), turns = 4 / shares;
+    const int nst = S::STAGES / turns * turns;
     // Rows are counted from the 16-row boundary at or below the sequence's first one: boxes start on such boundaries.
     const int skip = q.off & 15, first = q.off - skip, end = skip + q.n_rows, base = end - q.n_tok;
     const int a0 = part * q.split_rows, a1 = parts == 1 ? end : min(a0 + q.split_rows, end);
     const int steps = a1 > a0 ? (a1 - a0 + TN - 1) / TN : 0;
 
     if (tid == 0) {
-        for (int i = 0; i < NST; ++i) {
+        for (int i = 0; i < S::STAGES; ++i) {
             bar_init(&x.full[i], 1);
-            bar_init(&x.empty[i], 8 / S::GROUPS);
+            bar_init(&x.empty[i], 4 * shares);
         }
         x.abort = 0;
+        x.bad_first = 0x7fffffff;
+        x.bad_last = -1;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
 
-    if (warp >= 8) {
+    if (warp >= TREE_WARPS) {
         // ------------------------------------------------------- loading
         regs_dec<TREE_REGS_LOAD>();
-        if (warp > 8) return;
-        // Lane s brings 16-row group s of a stage; it looks up the next step's page ahead of it.
-        auto look = [&](int k) {
-            const int a = a0 + k * TN + lane * 16;
-            if (lane >= SLABS || k >= steps || a >= a1) return -1;
+        // A stage's 64 rows that lie in one page come as boxes of 64: K and V and the scales of either by a warp each.  Else
+        // each warp brings one of the stage's 16-row groups (a copy costs a warp about 100 cycles, whatever its size: with
+        // 16 of them from one warp they took longer than the memory).  A warp looks up 32 steps' pages at once, the next
+        // ones while it issues.
+        const int w = warp - TREE_WARPS;
+        auto look = [&](int k, int group) { // the page of 16-row group `group` of step k; -1: no rows, -2: no page
+            const int a = a0 + k * TN + group * 16;
+            if (a >= a1) return -1;
             const uint32_t pi = (uint32_t)(first + a) / (uint32_t)p.P;
-            return pi < (uint32_t)p.max_pages ? p.pt[(int64_t)q.id * p.max_pages + pi] : -2;
+            const int page = pi < (uint32_t)p.max_pages ? p.pt[(int64_t)q.id * p.max_pages + pi] : -2;
+            return page < 0 || page >= p.n_pages ? -2 : page;
         };
-        int page = look(0);
+        int own = -1, own_next = look(lane, w), lead = -1, lead_next = look(lane, 0);
+        int s = 0, round = 0; // the step's stage, and how often the ring has gone round
         for (int k = 0; k < steps; ++k) {
-            const int s = k % NST;
-            const int a = a0 + k * TN + lane * 16;
-            int pg = page;
-            page = look(k + 1);
-            if (pg == -1 && lane < SLABS && a < a1) pg = -2;
-            if (pg != -1 && (pg < 0 || pg >= p.n_pages)) { // reported, and page 0 in its place: memory that is there
-                atomicOr(p.err, ERR_BAD_PAGE);
-                pg = 0;
-            }
-            if (k >= NST) bar_wait(&x.empty[s], ((k / NST) - 1) & 1, p.err, &x.abort);
-            const unsigned have = __ballot_sync(0xffffffffu, pg >= 0);
-            if (lane == 0)
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&x.full[s])),
-                             "r"((unsigned)__popc(have) * (unsigned)((S::STAGE + S::SCALES) / SLABS))
-                             : "memory");
-            __syncwarp();
-            if (pg >= 0) {
-                const int row = (pg * p.Hk + g) * p.P + (first + a) % p.P;
-                uint8_t *kd = smem + s * S::STAGE, *vd = kd + S::KBYTES;
-                if constexpr (S::KROW == 256) {
-                    tree_box(kd + lane * 2048, &tmk, 0, row, &x.full[s]);
-                    tree_box(kd + TN * 128 + lane * 2048, &tmk, 64, row, &x.full[s]);
-                    tree_box(vd + lane * 2048, &tmv, 0, row, &x.full[s]);
-                    tree_box(vd + TN * 128 + lane * 2048, &tmv, 64, row, &x.full[s]);
-                } else {
-                    tree_box(kd + lane * 16 * S::KROW, &tmk, 0, row, &x.full[s]);
-                    tree_box(vd + lane * 16 * S::VROW, &tmv, 0, row, &x.full[s]);
+            if (k % 32 == 0) {
+                own = own_next, lead = lead_next;
+                if (own == -2 || lead == -2) { // reported, and page 0 in its place: memory that is there
+                    atomicOr(p.err, ERR_BAD_PAGE);
+                    own = max(own, -1) + (own == -2), lead = max(lead, -1) + (lead == -2);
                 }
-                uint8_t *sd = scales + s * S::SCALES + lane * 16 * S::SB;
-                if constexpr (S::KC)
-                    tree_bulk(sd, reinterpret_cast<const uint8_t *>(p.ks) + (int64_t)row * S::SB, 16 * S::SB, &x.full[s]);
-                if constexpr (S::VC)
-                    tree_bulk(sd + (S::KC ? TN * S::SB : 0), reinterpret_cast<const uint8_t *>(p.vs) + (int64_t)row * S::SB,
-                              16 * S::SB, &x.full[s]);
+                own_next = look(k + 32 + lane, w), lead_next = look(k + 32 + lane, 0);
+            }
+            const int pg = __shfl_sync(0xffffffffu, own, k & 31), pg0 = __shfl_sync(0xffffffffu, lead, k & 31);
+            const int a = a0 + k * TN, cell = (first + a) % p.P;
+            const bool one = cell + TN <= p.P;
+            if (round > 0) bar_wait(&x.empty[s], (round - 1) & 1, p.err, &x.abort);
+            if (lane == 0) {
+                const int groups = one ? SLABS : min(SLABS, (a1 - a + 15) / 16); // of 16 rows that come
+                uint64_t *bar = &x.full[s];
+                if (w == 0)
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)),
+                                 "r"((unsigned)groups * (unsigned)((S::STAGE + S::SCALES) / SLABS))
+                                 : "memory");
+                uint8_t *kd = smem + s * S::STAGE, *vd = kd + S::KBYTES;
+                uint8_t *sd = scales + s * S::SCALES;
+                const uint8_t *ks = reinterpret_cast<const uint8_t *>(p.ks), *vs = reinterpret_cast<const uint8_t *>(p.vs);
+                if (one) {
+                    const int row = (pg0 * p.Hk + g) * p.P + cell;
+                    if (w == 0) {
+                        tree_box(kd, &tmk, 0, row, bar);
+                        if (S::KROW == 256) tree_box(kd + TN * 128, &tmk, 64, row, bar);
+                    } else if (w == 1) {
+                        tree_box(vd, &tmv, 0, row, bar);
+                        if (S::VROW == 256) tree_box(vd + TN * 128, &tmv, 64, row, bar);
+                    } else if (w == 2) {
+                        if (S::KC) tree_bulk(sd, ks + (int64_t)row * S::SB, TN * S::SB, bar);
+                    } else {
+                        if (S::VC) tree_bulk(sd + (S::KC ? TN * S::SB : 0), vs + (int64_t)row * S::SB, TN * S::SB, bar);
+                    }
+                } else if (w < groups) {
+                    const int row = (pg * p.Hk + g) * p.P + (first + a + w * 16) % p.P;
+                    constexpr int KT_ = S::KROW == 256 ? 128 : S::KROW, VT_ = S::VROW == 256 ? 128 : S::VROW;
+                    tree_box(kd + w * 16 * KT_, &tmk16, 0, row, bar);
+                    if (S::KROW == 256) tree_box(kd + TN * 128 + w * 2048, &tmk16, 64, row, bar);
+                    tree_box(vd + w * 16 * VT_, &tmv16, 0, row, bar);
+                    if (S::VROW == 256) tree_box(vd + TN * 128 + w * 2048, &tmv16, 64, row, bar);
+                    sd += w * 16 * S::SB;
+                    if (S::KC) tree_bulk(sd, ks + (int64_t)row * S::SB, 16 * S::SB, bar);
+                    if (S::VC) tree_bulk(sd + (S::KC ? TN * S::SB : 0), vs + (int64_t)row * S::SB, 16 * S::SB, bar);
+                }
             }
             __syncwarp();
+            if (++s == nst) {
+                s = 0;
+                ++round;
+            }
         }
         // nothing may be under way when the CTA gives its memory back
-        for (int k = max(steps - NST, 0); k < steps; ++k) {
+        for (int k = max(steps - nst, 0); k < steps; ++k) {
             const uint64_t t0 = now_ns();
-            while (!bar_try(&x.full[k % NST], (k / NST) & 1) && now_ns() - t0 < WAIT_NS) {
+            while (!bar_try(&x.full[k % nst], (k / nst) & 1) && now_ns() - t0 < WAIT_NS) {
             }
         }
         return;
@@ -253,15 +291,16 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 const int up = p.parent[(int64_t)q.tok0 + i];
                 x.parent[i] = up >= 0 && up < i ? up : -1;
             }
+        for (int i = tid; i < M * (D / 16); i += TREE_WORK) x.poison[i / (D / 16)][i % (D / 16)] = 0;
         // Query rows, a warp each, normalised by a power of two, as the products' operand.
-        constexpr int QR = M >= 32 ? 4 : 2;
-        for (int mb = warp; mb < M; mb += 8 * QR) {
+        constexpr int QR = 2;
+        for (int mb = warp; mb < 16 * shares; mb += TREE_WARPS * QR) {
             Query<D> y[QR];
 #pragma unroll
-            for (int k = 0; k < QR; ++k) y[k].ask(p, q, g, m0 + mb + k * 8, m_all, lane);
+            for (int k = 0; k < QR; ++k) y[k].ask(p, q, g, m0 + mb + k * TREE_WARPS, m_all, lane);
 #pragma unroll
             for (int k = 0; k < QR; ++k) {
-                const int m = mb + k * 8;
+                const int m = mb + k * TREE_WARPS;
                 float v[D / 32];
                 uint32_t hi[D / 64], lo[D / 64];
                 y[k].get(p, q, v);
@@ -301,215 +340,195 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         named_sync<1, TREE_WORK>();
     }
 
-    float acc[MQ][NT][4];
-    float mx[MQ][2], sum[MQ][2];
+    float acc[NT][4], mx[2], sum[2];
 #pragma unroll
-    for (int i = 0; i < MQ; ++i) {
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[i][n][c] = 0.f;
-        mx[i][0] = mx[i][1] = -INFINITY;
-        sum[i][0] = sum[i][1] = 0.f;
-    }
-    int E = E_MIN;
-    const int half = QS == 1 ? 0 : warp >> 2; // of the tile's query rows
-    const int mw = half * 16 * MQ;            // the warp's first query row
-    if (mw < mrows) {
-        float qs[MQ][2];
-#pragma unroll
-        for (int i = 0; i < MQ; ++i) {
-            qs[i][0] = x.qscale[mw + 16 * i + gq];
-            qs[i][1] = x.qscale[mw + 16 * i + gq + 8];
-        }
-        const int slab = warp & 3;
+        for (int c = 0; c < 4; ++c) acc[n][c] = 0.f;
+    mx[0] = mx[1] = -INFINITY;
+    sum[0] = sum[1] = 0.f;
+    constexpr bool VSCALED = S::VC && !LO; // codes times their scale, rounded to fp16 on the way into the products
+    constexpr int V_LIFT = VSCALED ? 7 : 0; // of V's values above 2^-E times their own
+    int E = VSCALED ? 7 - 15 : E_MIN;       // (2^(7 - E) is an fp16 number; smaller scales stay exact enough under that one)
+    const int group = warp >> 2, slab = warp & 3;
+    const int mw = group % shares * 16, turn = group / shares; // the warp's first query row; its set of groups
+    {
+        const float qs[2] = {x.qscale[mw + gq], x.qscale[mw + gq + 8]};
         const int lrow = slab * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, lhi = lane >> 4; // ldmatrix: the lane's row and piece
         const uint4 *qa = qf + (mw >> 4) * (D / 16) * 32 + lane;
-        for (int k = QS == 1 ? warp >> 2 : 0; k < steps; k += S::GROUPS) {
-            const int s = k % NST, a = a0 + k * TN + slab * 16;
-            bar_wait_warp(&x.full[s], (k / NST) & 1, p.err, &x.abort);
-            if (a < a1) {
-                const uint32_t kt = smem_u32(smem + s * S::STAGE), vt = kt + S::KBYTES;
-                const uint8_t *ksc = scales + s * S::SCALES + slab * 16 * S::SB;
-                const uint8_t *vsc = ksc + (S::KC ? TN * S::SB : 0);
-                // ---- scores: [m tile][columns 0-7, 8-15]
-                float sc[MQ][2][4];
-#pragma unroll
-                for (int i = 0; i < MQ; ++i)
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) sc[i][n][c] = 0.f;
+        int s = turn, phase = 0;
+        for (int k = turn; k < steps; k += turns) {
+            const int a = a0 + k * TN + slab * 16;
+            bar_wait_warp(&x.full[s], phase, p.err, &x.abort);
+            const uint32_t kt = smem_u32(smem + s * S::STAGE), vt = kt + S::KBYTES;
+            const uint8_t *ksc = scales + s * S::SCALES + slab * 16 * S::SB + tq * 2 * S::SB; // of the lane's columns
+            // MASK: some of the 16 rows are not seen by all (rows of the block, or of nobody)
+            auto rows16 = [&](auto mask_) {
+                constexpr bool MASK = decltype(mask_)::value;
+                // ---- scores of columns 0-7 and 8-15
+                float sc[2][4];
                 if constexpr (S::KC) {
-                    uint32_t kw[2][2][NB / 2];
-                    load_scales<NB>(kw[0], ksc + tq * 2 * S::SB);
-                    load_scales<NB>(kw[1], ksc + (8 + tq * 2) * S::SB);
+                    uint32_t kw[2][2];
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
+                        if (b % 2 == 0) {
+                            load_pair<NB>(kw[0], ksc, b / 2);
+                            load_pair<NB>(kw[1], ksc + 8 * S::SB, b / 2);
+                        }
                         uint32_t w[4];
                         ldsm4(w, kt + tree_at<S::KROW>(lrow, 2 * b + lhi));
-                        const uint2 b00 = codes4(w[0]), b10 = codes4(w[1]), b01 = codes4(w[2]), b11 = codes4(w[3]);
+                        const uint4 qx = qa[2 * b * 32], qy = qa[(2 * b + 1) * 32];
+                        uint2 c0 = codes4(w[0]), c1 = codes4(w[1]);
+                        float t[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                        mma1(t[0], qx, c0.x, c0.y);
+                        mma1(t[1], qx, c1.x, c1.y);
+                        if constexpr (LO) {
+                            const uint4 lx = qa[QPART + 2 * b * 32];
+                            mma1(t[0], lx, c0.x, c0.y);
+                            mma1(t[1], lx, c1.x, c1.y);
+                        }
+                        c0 = codes4(w[2]), c1 = codes4(w[3]);
+                        mma1(t[0], qy, c0.x, c0.y);
+                        mma1(t[1], qy, c1.x, c1.y);
+                        if constexpr (LO) {
+                            const uint4 ly = qa[QPART + (2 * b + 1) * 32];
+                            mma1(t[0], ly, c0.x, c0.y);
+                            mma1(t[1], ly, c1.x, c1.y);
+                        }
 #pragma unroll
-                        for (int i = 0; i < MQ; ++i) {
-                            float t0[4] = {0.f, 0.f, 0.f, 0.f}, t1[4] = {0.f, 0.f, 0.f, 0.f};
-                            const uint4 qx = qa[(i * (D / 16) + 2 * b) * 32], qy = qa[(i * (D / 16) + 2 * b + 1) * 32];
-                            mma1(t0, qx, b00.x, b00.y);
-                            mma1(t1, qx, b10.x, b10.y);
-                            mma1(t0, qy, b01.x, b01.y);
-                            mma1(t1, qy, b11.x, b11.y);
-                            if constexpr (LO) {
-                                const uint4 lx = qa[QPART + (i * (D / 16) + 2 * b) * 32];
-                                const uint4 ly = qa[QPART + (i * (D / 16) + 2 * b + 1) * 32];
-                                mma1(t0, lx, b00.x, b00.y);
-                                mma1(t1, lx, b10.x, b10.y);
-                                mma1(t0, ly, b01.x, b01.y);
-                                mma1(t1, ly, b11.x, b11.y);
-                            }
-                            const float d00 = half_of(kw[0][0][b >> 1], b & 1), d01 = half_of(kw[0][1][b >> 1], b & 1);
-                            const float d10 = half_of(kw[1][0][b >> 1], b & 1), d11 = half_of(kw[1][1][b >> 1], b & 1);
-                            sc[i][0][0] = fmaf(t0[0], d00, sc[i][0][0]);
-                            sc[i][0][1] = fmaf(t0[1], d01, sc[i][0][1]);
-                            sc[i][0][2] = fmaf(t0[2], d00, sc[i][0][2]);
-                            sc[i][0][3] = fmaf(t0[3], d01, sc[i][0][3]);
-                            sc[i][1][0] = fmaf(t1[0], d10, sc[i][1][0]);
-                            sc[i][1][1] = fmaf(t1[1], d11, sc[i][1][1]);
-                            sc[i][1][2] = fmaf(t1[2], d10, sc[i][1][2]);
-                            sc[i][1][3] = fmaf(t1[3], d11, sc[i][1][3]);
+                        for (int n = 0; n < 2; ++n) {
+                            const float d0 = half_of(kw[n][0], b & 1), d1 = half_of(kw[n][1], b & 1);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                sc[n][c] = b ? fmaf(t[n][c], c & 1 ? d1 : d0, sc[n][c]) : t[n][c] * (c & 1 ? d1 : d0);
                         }
                     }
                 } else {
 #pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) sc[n][c] = 0.f;
+#pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
                         uint32_t w[4];
                         ldsm4(w, kt + tree_at<S::KROW>(lrow, 2 * ks + lhi));
-#pragma unroll
-                        for (int i = 0; i < MQ; ++i) {
-                            const uint4 qx = qa[(i * (D / 16) + ks) * 32];
-                            if constexpr (LO) {
-                                float t0[4] = {0.f, 0.f, 0.f, 0.f}, t1[4] = {0.f, 0.f, 0.f, 0.f};
-                                const uint4 lx = qa[QPART + (i * (D / 16) + ks) * 32];
-                                mma1(t0, qx, w[0], w[2]);
-                                mma1(t1, qx, w[1], w[3]);
-                                mma1(t0, lx, w[0], w[2]);
-                                mma1(t1, lx, w[1], w[3]);
-#pragma unroll
-                                for (int c = 0; c < 4; ++c) {
-                                    sc[i][0][c] += t0[c];
-                                    sc[i][1][c] += t1[c];
-                                }
-                            } else {
-                                mma1(sc[i][0], qx, w[0], w[2]);
-                                mma1(sc[i][1], qx, w[1], w[3]);
-                            }
-                        }
-                    }
-                }
-                // ---- what the query rows see: bit 8 i + 4 n + c of score [i][n][c]
-                const bool masked = a < skip || a + 16 > base;
-                uint32_t see = 0xffffffffu;
-                if (masked) {
-                    see = 0;
-#pragma unroll
-                    for (int i = 0; i < MQ; ++i)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int slot = x.slot[mw + 16 * i + gq + 8 * h];
+                        const uint4 qx = qa[ks * 32];
+                        if constexpr (LO) {
+                            float t[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                            const uint4 lx = qa[QPART + ks * 32];
+                            mma1(t[0], qx, w[0], w[2]);
+                            mma1(t[1], qx, w[1], w[3]);
+                            mma1(t[0], lx, w[0], w[2]);
+                            mma1(t[1], lx, w[1], w[3]);
 #pragma unroll
                             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                                for (int c = 0; c < 2; ++c) {
-                                    const int j = a + 8 * n + 2 * tq + c; // the cached row
-                                    bool yes = j >= skip && j < base;
-                                    if (j >= base && j < end) yes = x.sees[slot][(j - base) >> 5] >> ((j - base) & 31) & 1;
-                                    see |= (yes ? 1u : 0u) << (8 * i + 4 * n + 2 * h + c);
-                                }
+                                for (int c = 0; c < 4; ++c) sc[n][c] += t[n][c];
+                        } else {
+                            mma1(sc[0], qx, w[0], w[2]);
+                            mma1(sc[1], qx, w[1], w[3]);
                         }
-                }
-                // ---- softmax, in log2 units
-                float top[MQ][2];
-                bool raise = false;
-#pragma unroll
-                for (int i = 0; i < MQ; ++i) {
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            sc[i][n][c] *= qs[i][c >> 1];
-                            if (masked && !(see >> (8 * i + 4 * n + c) & 1)) sc[i][n][c] = -INFINITY;
-                        }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        top[i][h] = fmaxf(fmaxf(sc[i][0][2 * h], sc[i][0][2 * h + 1]), fmaxf(sc[i][1][2 * h], sc[i][1][2 * h + 1]));
-                        raise |= top[i][h] > mx[i][h] + T_GROW;
                     }
                 }
-                raise = __any_sync(0xffffffffu, raise);
-                // ---- V's scales and their exponent
-                uint32_t vw[2][2][NB / 2];
-                int e = E;
-                if constexpr (S::VC) {
-                    load_scales<NB>(vw[0], vsc + tq * 2 * S::SB);
-                    load_scales<NB>(vw[1], vsc + (8 + tq * 2) * S::SB);
-                    uint32_t most = 0;
+                // ---- what the query rows see: bit 4 n + c of score [n][c]
+                uint32_t see = 0;
+                if constexpr (MASK) {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int h = 0; h < 2; ++h) {
+                        const int slot = x.slot[mw + gq + 8 * h];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int j = a + 8 * n + 2 * tq + c;
-                            const bool in = !masked || (j >= skip && j < end); // (rows of nobody have no say)
+                        for (int n = 0; n < 2; ++n)
 #pragma unroll
-                            for (int b = 0; b < NB / 2; ++b) {
-                                uint32_t u = vw[n][c][b] & 0x7fff7fffu;
-                                // (scales that are not finite: no say either)
-                                if ((u & 0x7c00u) == 0x7c00u) u &= 0xffff0000u;
-                                if ((u & 0x7c000000u) == 0x7c000000u) u &= 0xffffu;
-                                most = __vmaxu2(most, in ? u : 0u);
+                            for (int c = 0; c < 2; ++c) {
+                                const int j = a + 8 * n + 2 * tq + c; // the cached row
+                                bool yes = j >= skip && j < base;
+                                if (j >= base && j < end) yes = x.sees[slot][(j - base) >> 5] >> ((j - base) & 31) & 1;
+                                see |= (yes ? 1u : 0u) << (4 * n + 2 * h + c);
                             }
-                        }
-                    most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                    most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                    const uint32_t one = max(most & 0xffffu, most >> 16);
-                    // (an fp16 number is a normal 32-bit one)
+                    }
+                }
+                auto unseen = [&](int n, int c) { return MASK && !(see >> (4 * n + c) & 1); };
+                // ---- softmax, in log2 units
+                float top[2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        sc[n][c] *= qs[c >> 1];
+                        if (unseen(n, c)) sc[n][c] = -INFINITY;
+                    }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) top[h] = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
+                const bool raise = __any_sync(0xffffffffu, top[0] > mx[0] + T_GROW || top[1] > mx[1] + T_GROW);
+                // ---- V's scales and their exponent
+                [[maybe_unused]] const uint8_t *vsc = ksc + (S::KC ? TN * S::SB : 0);
+                int e = E;
+                bool bad = false; // V values of the rows are not finite
+                if constexpr (S::VC) {
+                    uint32_t vw[2][2][NB / 2];
+                    load_scales<NB>(vw[0], vsc);
+                    load_scales<NB>(vw[1], vsc + 8 * S::SB);
+                    // the rows' largest; not of rows of nobody, and not of scales that are not finite (which are looked for in
+                    // all rows, as their products would be formed)
+                    auto largest = [&](bool all) {
+                        uint32_t most = 0;
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const int j = a + 8 * n + 2 * tq + c;
+                                const bool in = all || (j >= skip && j < end);
+#pragma unroll
+                                for (int b = 0; b < NB / 2; ++b) {
+                                    uint32_t u = vw[n][c][b] & 0x7fff7fffu;
+                                    if (!all) u &= ~__vcmpgeu2(u, 0x7c007c00u);
+                                    most = __vmaxu2(most, in ? u : 0u);
+                                }
+                            }
+                        most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                        most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                        return max(most & 0xffffu, most >> 16);
+                    };
+                    uint32_t one = largest(true);
+                    bad = __any_sync(0xffffffffu, one >= 0x7c00u);
+                    if (MASK || bad) one = largest(false);
+                    // (an fp16 number is a normal 32-bit one; a quad's lanes hold all 16 rows)
                     if (one) e = max(E, (int)(__float_as_uint(half_of(one, 0)) >> 23) - 127);
                 }
                 if (raise || (S::VC && e != E)) {
                     const float ve = S::VC ? two_to(max(E - e, -126)) : 1.f;
                     E = e;
 #pragma unroll
-                    for (int i = 0; i < MQ; ++i)
+                    for (int h = 0; h < 2; ++h) {
+                        float t = top[h];
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                        const float nm = t > mx[h] + T_GROW ? t : mx[h];
+                        const float al = nm == mx[h] ? 1.f : ex2(mx[h] - nm); // nothing yet: 0
+                        mx[h] = nm;
+                        sum[h] *= al;
+                        const float f = al * ve;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float t = top[i][h];
-                            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-                            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                            const float nm = t > mx[i][h] + T_GROW ? t : mx[i][h];
-                            const float al = nm == mx[i][h] ? 1.f : ex2(mx[i][h] - nm); // nothing yet: 0
-                            mx[i][h] = nm;
-                            sum[i][h] *= al;
-                            const float f = al * ve;
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                acc[i][n][2 * h] *= f;
-                                acc[i][n][2 * h + 1] *= f;
-                            }
+                        for (int n = 0; n < NT; ++n) {
+                            acc[n][2 * h] *= f;
+                            acc[n][2 * h + 1] *= f;
                         }
+                    }
                 }
 #pragma unroll
-                for (int i = 0; i < MQ; ++i)
+                for (int h = 0; h < 2; ++h) {
+                    const float use = mx[h] == -INFINITY ? 0.f : mx[h] - T_LIFT;
+                    float add = 0.f;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float use = mx[i][h] == -INFINITY ? 0.f : mx[i][h] - T_LIFT;
-                        float add = 0.f;
+                    for (int n = 0; n < 2; ++n)
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const float y = ex2(sc[i][n][2 * h + c] - use);
-                                sc[i][n][2 * h + c] = y;
-                                add += y;
-                            }
-                        sum[i][h] += add;
-                    }
+                        for (int c = 0; c < 2; ++c) {
+                            const float y = ex2(sc[n][2 * h + c] - use);
+                            sc[n][2 * h + c] = y;
+                            add += y;
+                        }
+                    sum[h] += add;
+                }
                 // ---- O += P V
                 auto pack = [&](const float (&y)[2][4], uint4 &hi, uint4 &lo) {
                     hi = make_uint4(h2(y[0][0], y[0][1]), h2(y[0][2], y[0][3]), h2(y[1][0], y[1][1]), h2(y[1][2], y[1][3]));
@@ -533,10 +552,37 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                         mma1(o, hi, b0, b1);
                     }
                 };
+                // Values that are not finite (0 x inf is NaN): reported, seen to in the end, and 0 in the products.  (`bad`
+                // has them found; another warp that shares the rows may be at the same.)
+                auto leave_out = [&] {
+                    if (lane == 0) {
+                        atomicMin(&x.bad_first, a);
+                        atomicMax(&x.bad_last, a);
+                    }
+                    uint8_t *v = S::VC ? scales + s * S::SCALES + (S::KC ? TN * S::SB : 0) + slab * 16 * S::SB
+                                       : smem + s * S::STAGE + S::KBYTES;
+                    for (int i = lane; i < (S::VC ? 16 * S::SB / 4 : 16 * S::VROW / 4); i += 32) {
+                        uint32_t *w = reinterpret_cast<uint32_t *>(
+                            S::VC ? v + 4 * i : v + tree_at<S::VROW>(slab * 16 + i / (S::VROW / 4), i % (S::VROW / 4) / 4) + i % 4 * 4);
+                        uint32_t u = *w;
+                        if (drop_nonfinite(u)) *w = u;
+                    }
+                    fence_async(); // (before the copies of a later step)
+                    __syncwarp();
+                };
                 if constexpr (S::VC) {
+                    if (VSCALED && MASK && bad) leave_out();
+                    const __half2 up = __float2half2_rn(VSCALED ? two_to(V_LIFT - E) : 1.f);
                     const float down = two_to(-E);
+                    uint4 hi, lo;
+                    if (VSCALED) pack(sc, hi, lo);
+                    uint32_t vw[2][2]; // (read again: there are no registers to keep them all)
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
+                        if (b % 2 == 0) {
+                            load_pair<NB>(vw[0], vsc, b / 2);
+                            load_pair<NB>(vw[1], vsc + 8 * S::SB, b / 2);
+                        }
                         uint32_t v0[4], v1[4]; // rows 2t, 2t + 1 and those 8 further of four columns of dims
                         if constexpr (VT == KVC_Q4_0) {
                             uint32_t wa, wb;
@@ -551,149 +597,150 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                             row_pairs(w[2], v0[2], v0[3]);
                             row_pairs(w[3], v1[2], v1[3]);
                         }
-                        float d[2][2];
+                        if constexpr (VSCALED) {
+                            __half2 d[2]; // scales of rows 2t, 2t + 1 and of those 8 further
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
+                            for (int n = 0; n < 2; ++n) {
+                                uint32_t u = __byte_perm(vw[n][0], vw[n][1], b & 1 ? 0x7632 : 0x5410);
+                                d[n] = __hmul2(*reinterpret_cast<__half2 *>(&u), up);
+                            }
+                            auto times = [](uint32_t v, __half2 f) {
+                                const __half2 y = __hmul2(*reinterpret_cast<__half2 *>(&v), f);
+                                return *reinterpret_cast<const uint32_t *>(&y);
+                            };
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) d[n][c] = half_of(vw[n][c][b >> 1], b & 1) * down;
-#pragma unroll
-                        for (int i = 0; i < MQ; ++i) {
+                            for (int n = 0; n < 4; ++n) product(acc[4 * b + n], hi, lo, times(v0[n], d[0]), times(v1[n], d[1]));
+                        } else {
                             float y[2][4];
 #pragma unroll
-                            for (int n = 0; n < 2; ++n)
+                            for (int n = 0; n < 2; ++n) {
+                                const float d0 = half_of(vw[n][0], b & 1) * down, d1 = half_of(vw[n][1], b & 1) * down;
 #pragma unroll
-                                for (int c = 0; c < 4; ++c) {
-                                    y[n][c] = sc[i][n][c] * d[n][c & 1];
-                                    if (masked && !(see >> (8 * i + 4 * n + c) & 1)) y[n][c] = 0.f; // (0 x inf)
-                                }
-                            uint4 hi, lo;
+                                for (int c = 0; c < 4; ++c) y[n][c] = unseen(n, c) ? 0.f : sc[n][c] * (c & 1 ? d1 : d0); // (0 x inf)
+                            }
                             pack(y, hi, lo);
 #pragma unroll
-                            for (int n = 0; n < 4; ++n) product(acc[i][4 * b + n], hi, lo, v0[n], v1[n]);
+                            for (int n = 0; n < 4; ++n) product(acc[4 * b + n], hi, lo, v0[n], v1[n]);
                         }
                     }
                 } else {
-                    uint4 hi[MQ], lo[MQ];
-                    bool bad = false;
+                    if (LO || MASK) { // (of 16-bit queries that all see the rows, P x inf is what it should be)
+                        __half2 f = __float2half2_rn(0.f);
 #pragma unroll
-                    for (int i = 0; i < MQ; ++i) pack(sc[i], hi[i], lo[i]);
+                        for (int n = 0; n < NT; n += 2) {
+                            uint32_t w[4];
+                            ldsm4t(w, vt + tree_at<S::VROW>(lrow, n + lhi));
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) f = __hfma2(*reinterpret_cast<__half2 *>(&w[u]), __float2half2_rn(0.f), f);
+                        }
+                        bad = !(__low2float(f) == 0.f && __high2float(f) == 0.f);
+                        if (__any_sync(0xffffffffu, bad)) leave_out();
+                    }
+                    uint4 hi, lo;
+                    pack(sc, hi, lo);
 #pragma unroll
                     for (int n = 0; n < NT; n += 2) {
                         uint32_t w[4];
                         ldsm4t(w, vt + tree_at<S::VROW>(lrow, n + lhi));
-                        if (LO || masked) { // values that are not finite: left out where P is two parts or not all tokens see them
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) bad |= drop_nonfinite(w[u]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < MQ; ++i) {
-                            product(acc[i][n], hi[i], lo[i], w[0], w[1]);
-                            product(acc[i][n + 1], hi[i], lo[i], w[2], w[3]);
-                        }
-                    }
-                    if ((LO || masked) && __any_sync(0xffffffffu, bad)) { // and added one by one for those that do
-                        const uint8_t *v = smem + s * S::STAGE + S::KBYTES;
-#pragma unroll 1
-                        for (int j = 0; j < 16; ++j) { // row j's weights are the quad's, at lane (j % 8) / 2 of it
-                            const int src = (lane & ~3) | ((j & 7) >> 1);
-                            const uint32_t sees = __shfl_sync(0xffffffffu, see, src);
-#pragma unroll
-                            for (int i = 0; i < MQ; ++i)
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    const float a_ = __shfl_sync(0xffffffffu, sc[i][0][2 * h], src);
-                                    const float b_ = __shfl_sync(0xffffffffu, sc[i][0][2 * h + 1], src);
-                                    const float c_ = __shfl_sync(0xffffffffu, sc[i][1][2 * h], src);
-                                    const float d_ = __shfl_sync(0xffffffffu, sc[i][1][2 * h + 1], src);
-                                    const float w = j < 8 ? (j & 1 ? b_ : a_) : (j & 1 ? d_ : c_);
-                                    if (sees >> (8 * i + 4 * (j >> 3) + 2 * h + (j & 1)) & 1) {
-#pragma unroll
-                                        for (int n = 0; n < NT; ++n) {
-                                            const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(
-                                                v + tree_at<S::VROW>(slab * 16 + j, n) + tq * 4));
-                                            if (!(fabsf(y.x) <= 65504.f)) acc[i][n][2 * h] += w * y.x;
-                                            if (!(fabsf(y.y) <= 65504.f)) acc[i][n][2 * h + 1] += w * y.y;
-                                        }
-                                    }
-                                }
-                        }
+                        product(acc[n], hi, lo, w[0], w[1]);
+                        product(acc[n + 1], hi, lo, w[2], w[3]);
                     }
                 }
+            };
+            if (a < a1) {
+                if (a < skip || a + 16 > base)
+                    rows16(std::true_type{});
+                else
+                    rows16(std::false_type{});
             }
             __syncwarp();
             if (lane == 0) bar_arrive(&x.empty[s]);
-        }
-    } else { // query rows that are not there: the stages are given back
-        for (int k = QS == 1 ? warp >> 2 : 0; k < steps; k += S::GROUPS) {
-            bar_wait_warp(&x.full[k % NST], (k / NST) & 1, p.err, &x.abort);
-            if (lane == 0) bar_arrive(&x.empty[k % NST]);
+            s += turns;
+            if (s >= nst) {
+                s -= nst;
+                phase ^= 1;
+            }
         }
     }
 
     // ------------------------------------------------------- joining the warps
-    constexpr int RW = QS == 1 ? 8 : 4; // warps that share query rows
-    const int w0 = QS == 1 ? 0 : half * 4;
-    {
+    // Those of query rows mw ..: groups share, share + shares, ..., in that order.
 #pragma unroll
-        for (int i = 0; i < MQ; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                sum[i][h] += __shfl_xor_sync(0xffffffffu, sum[i][h], 1);
-                sum[i][h] += __shfl_xor_sync(0xffffffffu, sum[i][h], 2);
-                if (tq == 0) {
-                    x.m[warp][16 * i + gq + 8 * h] = mx[i][h];
-                    x.l[warp][16 * i + gq + 8 * h] = sum[i][h];
-                }
-            }
+    for (int h = 0; h < 2; ++h) {
+        sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+        sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+        if (tq == 0) {
+            x.m[warp][gq + 8 * h] = mx[h];
+            x.l[warp][gq + 8 * h] = sum[h];
+        }
     }
-    named_sync<1, TREE_WORK>(); // every stage has landed (its group waited for it) and is done with
-    float *buf = reinterpret_cast<float *>(smem); // [warp][16 MQ][PITCH]
+    named_sync<1, TREE_WORK>(); // every stage has landed (its groups waited for it) and is done with
+    float *buf = reinterpret_cast<float *>(smem); // [warp][16][PITCH]
+    const int rw = 4 * turns;                     // warps that share query rows
+    auto warp_of = [&](int m, int i) { return ((m >> 4) + (i >> 2) * shares) * 4 + (i & 3); };
     {
-        const float back = S::VC ? two_to(E) : 1.f;
+        const float back = S::VC ? two_to(E - V_LIFT) : 1.f;
 #pragma unroll
-        for (int i = 0; i < MQ; ++i)
+        for (int h = 0; h < 2; ++h) {
+            const int m = gq + 8 * h;
+            float top = -INFINITY;
+            for (int i = 0; i < rw; ++i) top = fmaxf(top, x.m[warp_of(mw, i)][m]);
+            const float f = ex2(mx[h] - (top == -INFINITY ? 0.f : top)) * back;
+            float *row = buf + (warp * 16 + m) * S::PITCH;
+            if constexpr (S::VC) { // columns 4b .. 4b + 3: dims 32 b + 4 t + {0, 1}, + 16
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int m = 16 * i + gq + 8 * h;
-                float top = -INFINITY;
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int w = 0; w < RW; ++w) top = fmaxf(top, x.m[w0 + w][m]);
-                const float f = ex2(mx[i][h] - (top == -INFINITY ? 0.f : top)) * back;
-                float *row = buf + (warp * 16 * MQ + m) * S::PITCH;
-                if constexpr (S::VC) { // columns 4b .. 4b + 3: dims 32 b + 4 t + {0, 1}, + 16
+                    for (int u = 0; u < 2; ++u) {
+                        const float(&ev)[4] = acc[4 * b + 2 * u], (&od)[4] = acc[4 * b + 2 * u + 1];
+                        *reinterpret_cast<float4 *>(row + 32 * b + 16 * u + 4 * tq) =
+                            make_float4(ev[2 * h] * f, od[2 * h] * f, ev[2 * h + 1] * f, od[2 * h + 1] * f);
+                    }
+            } else {
 #pragma unroll
-                    for (int b = 0; b < NB; ++b)
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const float(&ev)[4] = acc[i][4 * b + 2 * u], (&od)[4] = acc[i][4 * b + 2 * u + 1];
-                            *reinterpret_cast<float4 *>(row + 32 * b + 16 * u + 4 * tq) =
-                                make_float4(ev[2 * h] * f, od[2 * h] * f, ev[2 * h + 1] * f, od[2 * h + 1] * f);
-                        }
-                } else {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        *reinterpret_cast<float2 *>(row + 8 * n + 2 * tq) = make_float2(acc[i][n][2 * h] * f, acc[i][n][2 * h + 1] * f);
-                }
+                for (int n = 0; n < NT; ++n)
+                    *reinterpret_cast<float2 *>(row + 8 * n + 2 * tq) = make_float2(acc[n][2 * h] * f, acc[n][2 * h + 1] * f);
             }
+        }
     }
     named_sync<1, TREE_WORK>();
+    if (x.bad_last >= 0) { // (rare) what was left out reaches the query rows that see its row
+        for (int i = tid; i < (x.bad_last + 16 - x.bad_first) * D; i += TREE_WORK) {
+            const int a = x.bad_first + i / D, d = i % D, j = a - skip;
+            const int32_t R = a >= skip && a < min(end, a1) ? pool_row(p, q, g, j) : -1;
+            if (R < 0) continue;
+            const float v = stored_value<D, VT>(p.vdata, p.vs, R, d);
+            if (fabsf(v) <= 3.4e38f) continue;
+            const uint32_t two = (v > 0.f ? 1u : (v < 0.f ? 2u : 3u)) << (2 * (d & 15));
+            for (int m = 0; m < mrows; ++m)
+                if (a < base || (x.sees[x.slot[m]][(a - base) >> 5] >> ((a - base) & 31) & 1)) atomicOr(&x.poison[m][d >> 4], two);
+        }
+        named_sync<1, TREE_WORK>();
+    }
     const bool whole = parts == 1;
     const int prow = q.part_row0 + (local - q.whole) * p.part_rows;
     for (int at = tid; at < mrows * (D / 4); at += TREE_WORK) {
-        const int m = at / (D / 4), c = at % (D / 4) * 4, hm = m / (16 * MQ), mm = m % (16 * MQ);
+        const int m = at / (D / 4), c = at % (D / 4) * 4, mm = m & 15;
         float top = -INFINITY, L = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < RW; ++w) top = fmaxf(top, x.m[hm * RW + w][mm]);
+        for (int i = 0; i < rw; ++i) top = fmaxf(top, x.m[warp_of(m, i)][mm]);
         const float use = top == -INFINITY ? 0.f : top;
-#pragma unroll
-        for (int w = 0; w < RW; ++w) {
-            const float4 y = *reinterpret_cast<const float4 *>(buf + ((hm * RW + w) * 16 * MQ + mm) * S::PITCH + c);
-            L = fmaf(x.l[hm * RW + w][mm], ex2(x.m[hm * RW + w][mm] - use), L);
+#pragma unroll 4
+        for (int i = 0; i < rw; ++i) {
+            const int w = warp_of(m, i);
+            const float4 y = *reinterpret_cast<const float4 *>(buf + (w * 16 + mm) * S::PITCH + c);
+            L = fmaf(x.l[w][mm], ex2(x.m[w][mm] - use), L);
             o.x += y.x;
             o.y += y.y;
             o.z += y.z;
             o.w += y.w;
+        }
+        if (x.bad_last >= 0) {
+            const uint32_t two = x.poison[m][c >> 4] >> (2 * (c & 15));
+            o.x = poisoned(o.x, two & 3u);
+            o.y = poisoned(o.y, two >> 2 & 3u);
+            o.z = poisoned(o.z, two >> 4 & 3u);
+            o.w = poisoned(o.w, two >> 6 & 3u);
         }
         if (whole) {
             const int t = token_of(p, m0 + m), j = m0 + m - t * p.r;
@@ -708,25 +755,20 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     }
 }
 
-template <int D, int KT, int VT, int MQ, int QS, bool LO>
-cudaError_t tree_go(const BlockParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st) {
-    auto k = tree_kernel<D, KT, VT, MQ, QS, LO>;
-    constexpr int bytes = TreeShape<D, KT, VT, MQ, QS, LO>::SMEM;
+template <int D, int KT, int VT, bool LO>
+cudaError_t tree_go(const BlockParams &p, const TreeMaps &t, cudaStream_t st) {
+    auto k = tree_kernel<D, KT, VT, LO>;
+    constexpr int bytes = TreeShape<D, KT, VT, LO>::SMEM;
     static SharedMemory set;
     cudaError_t e = set.allow((const void *)k, bytes, TREE_REGS);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)p.n_items, TREE_THREADS, bytes, st>>>(p, tmk, tmv);
+    k<<<(unsigned)p.n_items, TREE_THREADS, bytes, st>>>(p, *t.k, *t.v, *t.k16, *t.v16);
     e = cudaGetLastError();
     return e == cudaSuccess ? launch_join(p, st) : e;
 }
 template <int D, int KT, int VT>
-cudaError_t tree_pick(const BlockParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st) {
-    const bool lo = p.act == KVC_ACT_F32;
-    switch (p.tile_m) {
-    case 16: return lo ? tree_go<D, KT, VT, 1, 1, true>(p, tmk, tmv, st) : tree_go<D, KT, VT, 1, 1, false>(p, tmk, tmv, st);
-    case 32: return lo ? tree_go<D, KT, VT, 2, 1, true>(p, tmk, tmv, st) : tree_go<D, KT, VT, 2, 1, false>(p, tmk, tmv, st);
-    default: return lo ? tree_go<D, KT, VT, 2, 2, true>(p, tmk, tmv, st) : tree_go<D, KT, VT, 2, 2, false>(p, tmk, tmv, st);
-    }
+cudaError_t tree_pick(const BlockParams &p, const TreeMaps &t, cudaStream_t st) {
+    return p.act == KVC_ACT_F32 ? tree_go<D, KT, VT, true>(p, t, st) : tree_go<D, KT, VT, false>(p, t, st);
 }
 
 } // namespace

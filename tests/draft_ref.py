@@ -63,10 +63,10 @@ def attend(q, K, V, scale, sees):
 def attend_bound(mag, size, n, D, act):
     """A score is off by ds = size (2^-20 + (D + 4) 2^-24) + 2^-22 (operands of 20 bits or more, fp32 sums, a base-2 factor),
     a weight by 2 ds relatively, by 2^-22 for its exponential and by 2 (n / 8 + 8) 2^-24 for the two sums over rows (eight
-    at a time at the least), and by 2^-11 for its rounding where the queries have 16 bits, 2^-20 else; the result by half a
+    at a time at the least), and by 2^-11 for its rounding where the queries have 16 bits, 2^-20 else, V as much; the result by half a
     step of its type (twice, for the bound is on an unrounded mag)."""
     ds = size * (2.0**-20 + (D + 4) * 2.0**-24) + 2.0**-22
-    rel = 2 * ds + 2.0**-22 + 2 * (n / 8 + 8) * 2.0**-24 + (2.0**-20 if act == "f32" else 2.0**-11)
+    rel = 2 * ds + 2.0**-22 + 2 * (n / 8 + 8) * 2.0**-24 + 2 * (2.0**-20 if act == "f32" else 2.0**-11)
     return mag * (rel[..., None] + 2 * EPS_OF[act]) + 1e-30
 
 

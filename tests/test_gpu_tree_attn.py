@@ -11,8 +11,29 @@ from twin import Twin, kv_inputs
 
 pytestmark = pytest.mark.gpu
 
+
 Q8, F16, Q4 = oracle.Q8_0, oracle.F16, oracle.Q4_0
 KINDS = {"q8": (Q8, Q8), "f16": (F16, F16), "q8q4": (Q8, Q4)}
+
+
+KERNEL = 0
+
+
+@pytest.fixture(autouse=True, params=[0, 1, 2], ids=["by_size", "mma", "tcgen05"])
+def kernel(request):
+    """Every test on the kernel that the sizes choose and on each of the two for 16-bit queries."""
+    global KERNEL
+    act = request.node.callspec.params.get("act") if hasattr(request.node, "callspec") else None
+    if request.param and act == "f32":
+        pytest.skip("32-bit queries have one kernel")
+    KERNEL = request.param
+    yield request.param
+    KERNEL = 0
+
+
+def _force(tw):
+    tw.kvc.kvc_debug_block_kernel(tw.gpu.ctx, KERNEL)
+    return tw
 
 
 def _types():
@@ -58,7 +79,7 @@ def _compare(tw, ids, n_q, q, scale, parent, got, act, layer=0, seq=None):
 
 def _cache(kind, H, Hk, D, lens, page=64, seed=1, layers=1, exact=False, extra=64):
     tk, tv = KINDS[kind]
-    tw = Twin(layers, H, Hk, D, sum(lens) + extra, n_seq_max=max(1, len(lens)), type_=tk, type_v=tv, page_rows=page)
+    tw = _force(Twin(layers, H, Hk, D, sum(lens) + extra, n_seq_max=max(1, len(lens)), type_=tk, type_v=tv, page_rows=page))
     rng = np.random.default_rng(seed)
     for i, n in enumerate(lens):
         for layer in range(layers):
@@ -219,7 +240,7 @@ def test_tree_unseen_rows_never_reach_a_token(kind, act, T):
     spoilt = [1, 3]
     outs = []
     for spoil in (False, True):
-        tw = Twin(1, H, Hk, D, n + 64, type_=tk, type_v=tv, page_rows=64)
+        tw = _force(Twin(1, H, Hk, D, n + 64, type_=tk, type_v=tv, page_rows=64))
         try:
             kk, vv = k.copy(), v.copy()
             tail = np.ones((30, Hk, D), np.float32)
@@ -255,7 +276,7 @@ def test_tree_infinite_values_of_seen_rows(act, T):
     v[100, 0, 3], v[101, 0, 4], v[102, 1, 5] = np.inf, -np.inf, np.nan
     v[n - T, 0, 7] = np.inf  # the root of all: a row of a step that not all tokens see wholly
     v[n - 1, 1, 9] = -np.inf  # the last token's own
-    tw = Twin(1, 4, 2, D, n + 64, type_=F16, page_rows=64)
+    tw = _force(Twin(1, 4, 2, D, n + 64, type_=F16, page_rows=64))
     try:
         tw.gpu.append(0, 0, 0, torch.from_numpy(k).to(tw.dev), torch.from_numpy(v).to(tw.dev))
         q = _queries(np.random.default_rng(1), T, 4, D, act)
@@ -272,7 +293,7 @@ def test_tree_infinite_values_of_seen_rows(act, T):
         # the other values, against a cache without them
         for i in (100, 101, 102, n - T, n - 1):
             v[i][~np.isfinite(v[i])] = 0
-        tw2 = Twin(1, 4, 2, D, n + 64, type_=F16, page_rows=64)
+        tw2 = _force(Twin(1, 4, 2, D, n + 64, type_=F16, page_rows=64))
         try:
             tw2.append(0, 0, 0, k, v)
             plain = _run(tw2, [0], [T], q, 0.125, par)
@@ -295,7 +316,7 @@ def test_tree_values_of_any_size(kind, act):
     import torch
 
     n, T, D = 400, 20, 64
-    tw = Twin(1, 4, 2, D, n + 64, type_=KINDS[kind][0], page_rows=64)
+    tw = _force(Twin(1, 4, 2, D, n + 64, type_=KINDS[kind][0], page_rows=64))
     try:
         rng = np.random.default_rng(11)
         k = rng.standard_normal((n, 2, D)).astype(np.float32)
@@ -317,7 +338,7 @@ def test_tree_values_of_any_size(kind, act):
 def test_tree_peaked_softmax(act):
     """Maxima that keep rising along the rows, and one row that takes nearly all the weight."""
     n, T, D = 1500, 7, 128
-    tw = Twin(1, 8, 2, D, n + 64, type_=Q8, page_rows=64)
+    tw = _force(Twin(1, 8, 2, D, n + 64, type_=Q8, page_rows=64))
     try:
         rng = np.random.default_rng(19)
         u = rng.standard_normal((1, 2, D))
