@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from array import array
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libkvc.so")
@@ -158,11 +159,18 @@ def _addr(x):
     raise TypeError("expected a tensor or an address")
 
 
-def _stream(stream, device: int):
-    if stream is None:
-        import torch
+_raw_stream = None  # torch's current stream of a device as an address, without an object around it
 
-        return torch.cuda.current_stream(device).cuda_stream
+
+def _stream(stream, device: int):
+    global _raw_stream
+    if stream is None:
+        if _raw_stream is None:
+            import torch
+
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda d: torch.cuda.current_stream(d).cuda_stream)
+        return _raw_stream(device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -251,13 +259,12 @@ def _head_rows(name, t, device, dtype, tokens, heads, dim):
         raise KvcError(KVC_EINVAL, "%s must be a tensor on cuda:%d" % (name, device))
     if t.dtype is not dtype:
         raise KvcError(KVC_EINVAL, "%s must be %s, not %s" % (name, dtype, t.dtype))
-    shape = t.shape
+    shape, st = t.shape, t.stride()
     if len(shape) != 3 or shape[0] < tokens or shape[1] != heads or shape[2] != dim:
         raise KvcError(KVC_EINVAL, "%s must be [%d][%d][%d]" % (name, tokens, heads, dim))
-    st = t.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != dim):
+    if st[2] != 1 or (st[1] != dim and heads > 1):
         raise KvcError(KVC_EINVAL, "%s: a token's head-rows must be contiguous" % name)
-    return st[0] if shape[0] > 1 else max(st[0], heads * dim)
+    return st[0] if shape[0] > 1 else heads * dim
 
 
 def _block(seq_ids, n_q):
@@ -279,47 +286,69 @@ def kvc_attn_weight(ctx, layer, seq_ids, n_q, act, q, lse, w, w_stride, kq_scale
                                        float(kq_scale), _addr(w), int(w_stride), _stream(stream, device)))
 
 
-def kvc_attn_tree(ctx, layer, seq_ids, n_q, act, q, out, kq_scale, parent=None, stream=None, device=0):
-    ids, nq = _block(seq_ids, n_q)
-    _check(ctx, load().kvc_attn_tree(ctx, layer, len(seq_ids), ids, nq, int(act), _addr(q), _addr(out), _addr(parent),
-                                     float(kq_scale), _stream(stream, device)))
-
-
 def _host_ints(x):
-    """Host int32 values as ctypes can pass them: (address or array, count); the first is to be kept until the call."""
-    if hasattr(x, "ctypes"):
-        import numpy as np
+    """Host int32 values as (address, count, what is to be kept until the call)."""
+    t = type(x)
+    if t is list or t is tuple:
+        try:
+            a = array("i", x)
+        except OverflowError:
+            raise KvcError(KVC_ERANGE, "values must fit 32 bits") from None
+        except TypeError:
+            a = array("i", [int(v) for v in x])
+        return a.buffer_info()[0], len(a), a
+    if hasattr(x, "__array_interface__"):
+        if x.dtype != "int32" or not x.flags.c_contiguous:
+            import numpy as np
 
-        a = np.ascontiguousarray(x, np.int32) if x.dtype != np.int32 or not x.flags.c_contiguous else x
-        if a.size and not np.array_equal(a.ravel(), x.ravel()):
-            raise KvcError(KVC_ERANGE, "positions must fit 32 bits")
-        return a, a.size
-    x = [int(v) for v in x]
-    if any(v != C.c_int32(v).value for v in x):
-        raise KvcError(KVC_ERANGE, "positions must fit 32 bits")
-    return (C.c_int32 * len(x))(*x), len(x)
+            a = np.ascontiguousarray(x, np.int32)
+            if not np.array_equal(a, x):
+                raise KvcError(KVC_ERANGE, "values must fit 32 bits")
+            x = a
+        return x.__array_interface__["data"][0], x.size, x
+    return _host_ints(list(x))
+
+
+def _same_count(n, m):
+    if n != m:
+        raise KvcError(KVC_EINVAL, "one count per sequence")
+
+
+def kvc_attn_tree(ctx, layer, seq_ids, n_q, act, q, out, kq_scale, parent=None, stream=None, device=0):
+    ids, n, keep_ids = _host_ints(seq_ids)
+    nq, m, keep_nq = _host_ints(n_q)
+    _same_count(n, m)
+    status = load().kvc_attn_tree(ctx, layer, n, ids, nq, act, _addr(q), _addr(out), _addr(parent), kq_scale,
+                                  _stream(stream, device))
+    if status:
+        _check(ctx, status)
 
 
 def kvc_append_rope(ctx, layer, seq_ids, n_tok, pos, act, q, q_stride, k, k_stride, v, v_stride, q_out, q_norm=None,
                     k_norm=None, eps=1e-6, stream=None, device=0):
-    ids, nt = _block(seq_ids, n_tok)
-    ps, n = _host_ints(pos)
-    if n < sum(nt):
-        raise KvcError(KVC_EINVAL, "%d positions for %d tokens" % (n, sum(nt)))
-    at = ps.ctypes.data if hasattr(ps, "ctypes") else ps
-    _check(ctx, load().kvc_append_rope(ctx, layer, len(seq_ids), ids, nt, at, int(act), _addr(q), int(q_stride),
-                                       _addr(k), int(k_stride), _addr(v), int(v_stride), _addr(q_norm), _addr(k_norm),
-                                       float(eps), _addr(q_out), _stream(stream, device)))
+    ids, n, keep_ids = _host_ints(seq_ids)
+    nt, m, keep_nt = _host_ints(n_tok)
+    ps, have, keep_ps = _host_ints(pos)
+    _same_count(n, m)
+    if have < sum(n_tok):
+        raise KvcError(KVC_EINVAL, "%d positions for %d tokens" % (have, sum(n_tok)))
+    status = load().kvc_append_rope(ctx, layer, n, ids, nt, ps, act, _addr(q), q_stride, _addr(k), k_stride, _addr(v),
+                                    v_stride, _addr(q_norm), _addr(k_norm), eps, _addr(q_out), _stream(stream, device))
+    if status:
+        _check(ctx, status)
 
 
 def kvc_seq_keep(ctx, seq_ids, n_last, keep, stream=None, device=0):
     """keep: for each sequence the places among its last n_last rows that stay, ascending."""
-    if len(keep) != len(seq_ids):
-        raise KvcError(KVC_EINVAL, "one list of places per sequence")
-    ids, nl = _block(seq_ids, n_last)
-    nk = (C.c_int32 * len(keep))(*map(len, keep))
-    flat = (C.c_int32 * sum(nk))(*(int(p) for places in keep for p in places))
-    _check(ctx, load().kvc_seq_keep(ctx, len(seq_ids), ids, nl, nk, flat, _stream(stream, device)))
+    ids, n, keep_ids = _host_ints(seq_ids)
+    nl, m, keep_nl = _host_ints(n_last)
+    _same_count(n, m)
+    _same_count(n, len(keep))
+    nk, _, keep_nk = _host_ints(list(map(len, keep)))
+    at, _, keep_at = _host_ints([p for places in keep for p in places])
+    status = load().kvc_seq_keep(ctx, n, ids, nl, nk, at, _stream(stream, device))
+    if status:
+        _check(ctx, status)
 
 
 class kvc_trace_event(C.Structure):
@@ -616,7 +645,7 @@ class KVCache:
         """Attention of drafted tokens that are the last n_q[i] rows of sequence seq_ids[i]: each sees the rows
         before those, its ancestors' and its own.  q, out [T][n_head][head_dim]; parent [T] int32 on the device, counted
         within a sequence's tokens (negative: a root), or None (a chain)."""
-        act, total = _act(q), sum(map(int, n_q))
+        act, total = _act(q), sum(n_q)
         self._block_io(q, out, None, parent, total, "parent")
         kvc_attn_tree(self.ctx, layer, seq_ids, n_q, act, q, out, kq_scale, parent, stream, self.device)
 
@@ -624,19 +653,23 @@ class KVCache:
         """Append n_tok[i] tokens to sequence seq_ids[i] (packed) at the host positions pos [T]: q, q_out
         [T][n_head][head_dim] (or both None) and k, v [T][n_head_kv][head_dim] of one type, q, k and v possibly columns
         of one tensor; q_norm, k_norm [head_dim] fp32 or None."""
-        act, total, p = _act(k), sum(map(int, n_tok)), self.params
-        if (q is None) != (q_out is None):
+        act, total, p, device, dtype = _act(k), sum(n_tok), self.params, self.device, k.dtype
+        dim, hk = p.head_dim, p.n_head_kv
+        ks = _head_rows("k", k, device, dtype, total, hk, dim)
+        vs = _head_rows("v", v, device, dtype, total, hk, dim)
+        qs = 0
+        if q is not None and q_out is not None:
+            heads = p.n_head
+            qs = _head_rows("q", q, device, dtype, total, heads, dim)
+            _block_tensor("q_out", q_out, device, dtype, total * heads * dim)
+        elif q is not None or q_out is not None:
             raise KvcError(KVC_EINVAL, "q and q_out come together")
-        strides = [_head_rows("k", k, self.device, k.dtype, total, p.n_head_kv, p.head_dim),
-                   _head_rows("v", v, self.device, k.dtype, total, p.n_head_kv, p.head_dim), 0]
-        if q is not None:
-            strides[2] = _head_rows("q", q, self.device, k.dtype, total, p.n_head, p.head_dim)
-            _block_tensor("q_out", q_out, self.device, k.dtype, total * p.n_head * p.head_dim)
-        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-            if w is not None:
-                _block_tensor(name, w, self.device, _torch.float32, p.head_dim)
-        kvc_append_rope(self.ctx, layer, seq_ids, n_tok, pos, act, q, strides[2], k, strides[0], v, strides[1], q_out,
-                        q_norm, k_norm, eps, stream, self.device)
+        if q_norm is not None:
+            _block_tensor("q_norm", q_norm, device, _torch.float32, dim)
+        if k_norm is not None:
+            _block_tensor("k_norm", k_norm, device, _torch.float32, dim)
+        kvc_append_rope(self.ctx, layer, seq_ids, n_tok, pos, act, q, qs, k, ks, v, vs, q_out, q_norm, k_norm, eps,
+                        stream, device)
 
     def keep(self, seq_ids, n_last, keep, stream=None):
         """Of the last n_last[i] rows of sequence seq_ids[i] keep those at the places keep[i] (ascending); the

@@ -60,12 +60,13 @@ def attend(q, K, V, scale, sees):
     return out, mag, size
 
 
-def attend_bound(mag, size, n, D, act):
-    """A score is off by ds = size (2^-20 + (D + 4) 2^-24) + 2^-22 (operands of 20 bits or more, fp32 sums, a base-2 factor),
-    a weight by 2 ds relatively, by 2^-22 for its exponential and by 2 (n / 8 + 8) 2^-24 for the two sums over rows (eight
-    at a time at the least), and by 2^-11 for its rounding where the queries have 16 bits, 2^-20 else, V as much; the result by half a
-    step of its type (twice, for the bound is on an unrounded mag)."""
-    ds = size * (2.0**-20 + (D + 4) * 2.0**-24) + 2.0**-22
+def attend_bound(mag, size, n, D, act, exact=False):
+    """A score is off by ds = size (2^-s + (D + 4) 2^-24) + 2^-22 (operands of s = 20 bits or more, 11 for K where the
+    queries have 16 bits, unless fp16 holds K exactly; fp32 sums, a base-2 factor), a weight by 2 ds relatively, by 2^-22 for
+    its exponential and by 2 (n / 8 + 8) 2^-24 for the two sums over rows (eight at a time at the least), and by 2^-11 for
+    its rounding where the queries have 16 bits, 2^-20 else, V as much; the result by half a step of its type (twice, for
+    the bound is on an unrounded mag)."""
+    ds = size * (2.0 ** -(20 if act == "f32" or exact else 11) + (D + 4) * 2.0**-24) + 2.0**-22
     rel = 2 * ds + 2.0**-22 + 2 * (n / 8 + 8) * 2.0**-24 + 2 * (2.0**-20 if act == "f32" else 2.0**-11)
     return mag * (rel[..., None] + 2 * EPS_OF[act]) + 1e-30
 

@@ -93,7 +93,8 @@ def test_positions_that_do_not_fit_are_refused_by_the_binding():
     for pos in ([2**31], [-2**31 - 1], np.array([2**40])):
         with pytest.raises(kvc.KvcError):
             kvc._host_ints(pos)
-    a, n = kvc._host_ints(np.arange(10)[::2])
-    assert n == 5 and list(a) == [0, 2, 4, 6, 8] and a.dtype == np.int32
-    a, n = kvc._host_ints([3, -1])
-    assert n == 2 and list(a) == [3, -1]
+    at, n, a = kvc._host_ints(np.arange(10)[::2])
+    assert n == 5 and list(a) == [0, 2, 4, 6, 8] and a.dtype == np.int32 and at == a.ctypes.data
+    for x in ([3, -1], (3, -1), iter([3, -1]), [np.int64(3), np.int32(-1)], [3.0, -1.0]):
+        at, n, a = kvc._host_ints(x)
+        assert n == 2 and list(a) == [3, -1]

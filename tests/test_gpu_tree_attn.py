@@ -63,15 +63,15 @@ def _run(tw, ids, n_q, q, scale, parent=None, layer=0):
     return out
 
 
-def _compare(tw, ids, n_q, q, scale, parent, got, act, layer=0, seq=None):
+def _compare(tw, ids, n_q, q, scale, parent, got, act, layer=0, exact=False):
     qa, o, t0 = q.double().cpu().numpy(), got.double().cpu().numpy(), 0
     for i, T in zip(ids, n_q):
-        s = (seq or tw.ref.seqs)[i]
+        s = tw.ref.seqs[i]
         K, V = values(s.K[layer]), values(s.V[layer])
         sl = slice(t0, t0 + T)
         par = None if parent is None else parent[sl]
         want, mag, size = attend(qa[sl], K, V, float(np.float32(scale)), tree_sees(par, len(K), T))
-        bound = attend_bound(mag, size, len(K), q.shape[-1], act)
+        bound = attend_bound(mag, size, len(K), q.shape[-1], act, exact)
         err = np.abs(o[sl] - want)
         assert np.all(err <= bound), "sequence %d: off by %.3g, %.2f of its bound" % (i, err.max(), (err / bound).max())
         t0 += T
@@ -127,7 +127,7 @@ def test_tree_masks_on_exact_values(kind, act, H, Hk, D, shape):
         if shape == "odd":
             par[[3, 9, 17, 30]] = [3, 40, 2**31 - 1, -2**31]
         got = _run(tw, [0], [T], q, 0.07, par)
-        _compare(tw, [0], [T], q, 0.07, par, got, act)
+        _compare(tw, [0], [T], q, 0.07, par, got, act, exact=True)
         if shape == "none":
             assert bool((_run(tw, [0], [T], q, 0.07, np.arange(T) - 1) == got).all())
     finally:
@@ -146,7 +146,7 @@ def test_tree_of_many_tokens(kind, act, T):
             q = _queries(rng, T, 4, 64, act, 0.3)
             par = _parents(rng, T, 40)
             got = _run(tw, [0], [T], q, 0.05, par)
-            _compare(tw, [0], [T], q, 0.05, par, got, act)
+            _compare(tw, [0], [T], q, 0.05, par, got, act, exact=True)
         finally:
             tw.close()
 
