@@ -71,31 +71,57 @@ template <> struct Four<KVC_ACT_BF16> {
     }
 };
 
-// Four values, dims d .. d + 3 of pool row R, of a block that eight lanes hold (in: whether the row is to be written).
+// A lane's eight values of a head-row, dims d .. d + 3 and those D/2 further, of two blocks that eight lanes hold, into pool
+// row R (in: whether it is to be written).  The steps, and so the bytes, are quant_row.cuh's.
 template <int D>
-__device__ __forceinline__ void store_four(int type, const TensorView &tv, int64_t R, int d, int lane, const float (&x)[4], bool in) {
+__device__ __forceinline__ void store_eight(int type, const TensorView &tv, int64_t R, int d, int lane, const float (&x)[8], bool in) {
     if (type == KVC_Q8_0) {
-        int8_t c[4];
-        float s;
-        quantise<4, 8>(x, c, s);
+        // Each half of the eight lanes runs one block's two divisions; halves away from zero as the truncation of
+        // y + copysign(0.49999997, y) (exact for |y| < 2^22).
+        float top[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            top[h] = fmaxf(fmaxf(fabsf(x[4 * h]), fabsf(x[4 * h + 1])), fmaxf(fabsf(x[4 * h + 2]), fabsf(x[4 * h + 3])));
+#pragma unroll
+            for (int m = 1; m < 8; m <<= 1) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], m));
+        }
+        const bool second = lane & 4;
+        const float s = __fdiv_rn(second ? top[1] : top[0], 127.0f);
+        const float inv = s != 0.0f ? __fdiv_rn(1.0f, s) : 0.0f, other = __shfl_xor_sync(0xffffffffu, inv, 4);
+        const float by[2] = {second ? other : inv, second ? inv : other};
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float y = __fmul_rn(x[i], by[i / 4]);
+            const int c = __float2int_rz(__fadd_rn(y, copysignf(0.49999997f, y)));
+            w[i / 4] |= ((uint32_t)c & 0xffu) << (8 * (i & 3));
+        }
         if (!in) return;
-        const uint32_t w = (uint32_t)(uint8_t)c[0] | (uint32_t)(uint8_t)c[1] << 8 | (uint32_t)(uint8_t)c[2] << 16 |
-                           (uint32_t)(uint8_t)c[3] << 24;
-        *reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(tv.data) + R * D + d) = w ^ CODE_FLIP;
-        if (d % QK == 0) tv.scales[R * (D / QK) + d / QK] = __half_as_ushort(__float2half_rn(s));
+        uint8_t *row = reinterpret_cast<uint8_t *>(tv.data) + R * D + d;
+        *reinterpret_cast<uint32_t *>(row) = w[0] ^ CODE_FLIP;
+        *reinterpret_cast<uint32_t *>(row + D / 2) = w[1] ^ CODE_FLIP;
+        if ((lane & 3) == 0) // lanes 0 and 4 of the eight: the first block's scale, the second's
+            tv.scales[R * (D / QK) + d / QK + (second ? D / QK / 2 : 0)] = __half_as_ushort(__float2half_rn(s));
     } else if (type == KVC_Q4_0) {
-        int c[4];
-        float s;
-        quantise_q4<4, 8>(x, lane, c, s);
-        const uint32_t mine = (uint32_t)c[0] | (uint32_t)c[1] << 8 | (uint32_t)c[2] << 16 | (uint32_t)c[3] << 24;
-        const uint32_t high = __shfl_xor_sync(0xffffffffu, mine, 4);
-        if (!in) return;
-        if (d % QK < QK / 2)
-            *reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(tv.data) + R * (D / 2) + d / QK * (QK / 2) + d % QK) =
-                mine | high << 4;
-        if (d % QK == 0) tv.scales[R * (D / QK) + d / QK] = __half_as_ushort(__float2half_rn(s));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float y[4] = {x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]};
+            const int at = d + h * (D / 2);
+            int c[4];
+            float s;
+            quantise_q4<4, 8>(y, lane, c, s);
+            const uint32_t mine = (uint32_t)c[0] | (uint32_t)c[1] << 8 | (uint32_t)c[2] << 16 | (uint32_t)c[3] << 24;
+            const uint32_t high = __shfl_xor_sync(0xffffffffu, mine, 4);
+            if (!in) continue;
+            if (d % QK < QK / 2)
+                *reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(tv.data) + R * (D / 2) + at / QK * (QK / 2) + at % QK) =
+                    mine | high << 4;
+            if (d % QK == 0) tv.scales[R * (D / QK) + at / QK] = __half_as_ushort(__float2half_rn(s));
+        }
     } else if (in) {
-        Four<KVC_ACT_F16>::store(reinterpret_cast<__half *>(tv.data) + R * D + d, x);
+        __half *row = reinterpret_cast<__half *>(tv.data) + R * D + d;
+        Four<KVC_ACT_F16>::store(row, x);
+        Four<KVC_ACT_F16>::store(row + D / 2, x + 4);
     }
 }
 
@@ -168,7 +194,7 @@ template <int D, int ACT> __global__ void __launch_bounds__(ROPE_THREADS) rope_a
                 for (int j = 0; j < 8; ++j) s = fmaf(x[j], x[j], s);
 #pragma unroll
                 for (int m = 1; m < LANES; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-                const float inv = 1.0f / sqrtf(s * (1.0f / D) + a.eps);
+                const float inv = rsqrtf(s * (1.0f / D) + a.eps);
                 x[0] *= inv * w4.x, x[1] *= inv * w4.y, x[2] *= inv * w4.z, x[3] *= inv * w4.w;
                 x[4] *= inv * w5.x, x[5] *= inv * w5.y, x[6] *= inv * w5.z, x[7] *= inv * w5.w;
             }
@@ -198,11 +224,7 @@ template <int D, int ACT> __global__ void __launch_bounds__(ROPE_THREADS) rope_a
             } else {
                 const int64_t R = ((int64_t)page * a.Hk + h) * a.P + (int)(lr - pi * a.P);
                 const bool is_in = there && h < a.Hk;
-                const float y[4] = {x[0], x[1], x[2], x[3]}, z[4] = {x[4], x[5], x[6], x[7]};
-                const TensorView &tv = which == 1 ? a.lv.k : a.lv.v;
-                const int type = which == 1 ? a.type_k : a.type_v;
-                store_four<D>(type, tv, R, 4 * li, lane, y, is_in);
-                store_four<D>(type, tv, R, D / 2 + 4 * li, lane, z, is_in);
+                store_eight<D>(which == 1 ? a.type_k : a.type_v, which == 1 ? a.lv.k : a.lv.v, R, 4 * li, lane, x, is_in);
             }
         }
     }

@@ -21,11 +21,11 @@ def turned(x, pos, base, neox, w=None, eps=1e-6):
     y[..., a] = x[..., a] * c - x[..., b] * s
     y[..., b] = x[..., a] * s + x[..., b] * c
     size[..., a] = size[..., b] = np.abs(x[..., a]) + np.abs(x[..., b])
-    # The norm: 12 additions at most after the products, halved by the root, then a root, a division and two products
-    # (each 2^-24): 11 x 2^-24.  Cosine and sine: the angle is off by 2^-25 of itself (at most pi) and the function by 2^-23
+    # The norm: 12 additions at most after the products, halved by the root, then a reciprocal root (two units in the last
+    # place: 4 x 2^-24) and two products (each 2^-24): 13 x 2^-24.  Cosine and sine: the angle is off by 2^-25 of itself (at most pi) and the function by 2^-23
     # (two units in the last place of values of at most 1): 3.6 x 2^-23 = 7.2 x 2^-24.  The turn itself: 3 x 2^-24.  In 64
     # bits the angle of a position of 2^21 is off by 2^-31: nothing beside it.
-    return y, size * 22 * 2.0**-24
+    return y, size * 24 * 2.0**-24
 
 
 def tree_sees(parent, n, T):

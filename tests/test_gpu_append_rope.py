@@ -118,7 +118,7 @@ def test_append_rope_far_positions(act, base):
         out = _call(c, 0, [0], [len(pos)], pos, qkv)
         y, s = turned(_np(qkv[0]), pos, base, True)
         # pos * theta in 64 bits is off by half a unit of 2^-53 relatively, and theta by one: 3 x 2^-54 of the angle
-        far = (pos.astype(np.float64) * 3 * 2.0**-54)[:, None, None] * (s / (22 * 2.0**-24))
+        far = (pos.astype(np.float64) * 3 * 2.0**-54)[:, None, None] * (s / (24 * 2.0**-24))
         assert np.all(np.abs(_np(out) - y) <= s * (1 + 2.0**-7) + far + np.abs(y) * EPS_OF[act] + 2.0**-25)
     finally:
         c.close()
