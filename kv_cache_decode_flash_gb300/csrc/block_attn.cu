@@ -136,7 +136,7 @@ static bool plan_block(BlockParams &p, int sms, bool tc) {
     return narrow;
 }
 
-// The query tiles and items of a tree attention: tiles of 64 query rows (or what there are: the kernel shares the work of
+// The query tiles and items of a tree attention: tiles of 32 query rows (or what there are: the kernel shares the work of
 // fewer over all its warps too), one item at a time on an SM.  The kernel counts cached rows from the 16-row boundary at or
 // below the sequence's first.
 static void plan_tree(BlockParams &p, int sms) {

@@ -90,7 +90,7 @@ cudaError_t launch_cross_tc(int type_k, int type_v, const BlockParams &p, cudaSt
 // cache's types, over the layer's tensor maps.
 constexpr int TREE_STEP = 64;
 constexpr int TREE_MAX = 256; // tokens of a tree
-constexpr int TREE_TILE = 64; // query rows of a tile
+constexpr int TREE_TILE = 32; // query rows of a tile
 struct TreeMaps {
     const CUtensorMap *k, *v, *k16, *v16; // boxes of TREE_STEP rows, of 16
 };

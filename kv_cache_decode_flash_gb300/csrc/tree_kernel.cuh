@@ -4,12 +4,12 @@
 //   s_j = scale * q[t][h] . K_j,   out = sum_j exp(s_j) V_j / sum_j exp(s_j),
 // query head h reading KV head h / r.  Instantiated by k_tree_*.cu.
 //
-// A work item is one KV head, a tile of up to 64 query rows (tokens x query heads
+// A work item is one KV head, a tile of up to 32 query rows (tokens x query heads
 // of the group) and a part of the cached rows.  A drafted block is few query
 // rows over many cached ones, so the kernel is built like the single-token one:
 // a loading group keeps a ring of 64-row stages full by TMA (boxes of 64 or 16 rows,
-// swizzled for ldmatrix; a page holds whole ones of 16) and sixteen warps take 16 cached
-// rows by 16 query rows each, straight from the stored bytes: codes become exact fp16
+// swizzled for ldmatrix; a page holds whole ones of 16) and eight warps take 16 cached
+// rows (twice, of neighbouring stages) by 16 query rows each, straight from the stored bytes: codes become exact fp16
 // values in registers, on their way into the products.  Bringing them to fp16 in
 // shared memory first, as the block attention's tcgen05 kernel must, costs more than
 // the products of few query rows.
@@ -42,13 +42,12 @@
 namespace kvc {
 namespace {
 
-// Four groups of four warps of products and one that loads.  A launch gives every thread 96 registers; the
-// loading group hands most of its own to the others.
-constexpr int TREE_WARPS = 16, TREE_WORK = TREE_WARPS * 32, TREE_THREADS = TREE_WORK + 128;
-constexpr int TREE_REGS = 96, TREE_REGS_WORK = 112, TREE_REGS_LOAD = 32;
-static_assert(4 * TREE_REGS_WORK + TREE_REGS_LOAD <= 5 * TREE_REGS, "the groups' registers come from the launch's");
+// Two groups of four warps of products and one that loads.  A launch gives every thread 168 registers; the loading group
+// hands most of its own to the others.
+constexpr int TREE_WARPS = 8, TREE_WORK = TREE_WARPS * 32, TREE_THREADS = TREE_WORK + 128;
+constexpr int TREE_REGS = 168, TREE_REGS_WORK = 232, TREE_REGS_LOAD = 40;
+static_assert(2 * TREE_REGS_WORK + TREE_REGS_LOAD <= 3 * TREE_REGS, "the groups' registers come from the launch's");
 constexpr int TN = TREE_STEP, SLABS = TN / 16;
-constexpr int TM_TREE = TREE_TILE; // query rows of a tile at most
 constexpr float T_GROW = 8.f, T_LIFT = 6.f;
 
 template <int D, int KT, int VT, bool LO> struct TreeShape {
@@ -58,7 +57,7 @@ template <int D, int KT, int VT, bool LO> struct TreeShape {
     static constexpr int KBYTES = TN * KROW, VBYTES = TN * VROW, STAGE = KBYTES + VBYTES;
     static_assert(STAGE % 1024 == 0 && KBYTES % 1024 == 0, "swizzled boxes");
     static constexpr int SCALES = (KC ? TN * SB : 0) + (VC ? TN * SB : 0);
-    static constexpr int QF = TM_TREE / 16 * (D / 16) * 32 * 16; // bytes of the query fragments (one part)
+    static constexpr int QF = TREE_TILE / 16 * (D / 16) * 32 * 16; // bytes of the query fragments (one part)
     static constexpr int AUX = 8192;
     static constexpr int FIXED = 1024 + QF * (LO ? 2 : 1) + AUX;
     static constexpr int FIT = (232448 - FIXED) / (STAGE + SCALES);
@@ -164,7 +163,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmk16,
                 const __grid_constant__ CUtensorMap tmv16) {
     using S = TreeShape<D, KT, VT, LO>;
-    constexpr int M = TM_TREE, NB = S::NB, NT = D / 8;
+    constexpr int M = TREE_TILE, NB = S::NB, NT = D / 8;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *scales = smem + S::STAGES * S::STAGE;
@@ -180,11 +179,11 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     item_unit(q, local, unit, part, parts);
     const int g = unit / q.tiles, tile = q.tiles - 1 - unit % q.tiles; // (the order that join_kernel takes)
     const int m_all = q.n_tok * p.r, m0 = tile * M, mrows = min(M, m_all - m0);
-    // The four groups: `shares` of them have 16 query rows each of every stage they take, `turns` sets take stages in turn.
-    // A stage's phases all belong to one set (a wait tells a phase only from the one before), so that stages are as many as
-    // fit in whole turns.
-    const int shares = mrows > 32 ? 4 : (mrows > 16 ? 2 : 1), turns = 4 / shares;
-    const int nst = S::STAGES / turns * turns;
+    // More than 16 query rows: the two groups have 16 of them each, over all stages; else they take pairs of stages in turn.
+    // A stage's phases all belong to the same warps (a wait tells a phase only from the one before), so that stages are as
+    // many as fit in whole turns of pairs.
+    const int shares = mrows > 16 ? 2 : 1, turns = 2 / shares;
+    const int nst = S::STAGES / (2 * turns) * (2 * turns);
     // Rows are counted from the 16-row boundary at or below the sequence's first one: boxes start on such boundaries.
     const int skip = q.off & 15, first = q.off - skip, end = skip + q.n_rows, base = end - q.n_tok;
     const int a0 = part * q.split_rows, a1 = parts == 1 ? end : min(a0 + q.split_rows, end);
@@ -356,66 +355,74 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         const float qs[2] = {x.qscale[mw + gq], x.qscale[mw + gq + 8]};
         const int lrow = slab * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, lhi = lane >> 4; // ldmatrix: the lane's row and piece
         const uint4 *qa = qf + (mw >> 4) * (D / 16) * 32 + lane;
-        int s = turn, phase = 0;
-        for (int k = turn; k < steps; k += turns) {
-            const int a = a0 + k * TN + slab * 16;
-            bar_wait_warp(&x.full[s], phase, p.err, &x.abort);
-            const uint32_t kt = smem_u32(smem + s * S::STAGE), vt = kt + S::KBYTES;
-            const uint8_t *ksc = scales + s * S::SCALES + slab * 16 * S::SB + tq * 2 * S::SB; // of the lane's columns
-            // MASK: some of the 16 rows are not seen by all (rows of the block, or of nobody)
-            auto rows16 = [&](auto mask_) {
-                constexpr bool MASK = decltype(mask_)::value;
-                // ---- scores of columns 0-7 and 8-15
-                float sc[2][4];
-                if constexpr (S::KC) {
-                    uint32_t kw[2][2];
+        // SL groups of 16 rows, a first at row a of stage s and the others a stage further: a warp's two chains of products
+        // and softmax run beside each other where nothing is masked.  MASK: some of the rows are not seen by all (rows of
+        // the block, or of nobody).
+        auto rows = [&](int s, int a, auto sl_) {
+            constexpr int SL = decltype(sl_)::value;
+            constexpr bool MASK = SL == 1;
+            // ---- scores of columns 0-7 and 8-15
+            float sc[SL][2][4];
+            auto k_tile = [&](int l) { return smem_u32(smem + (s + l) * S::STAGE); };
+            auto scale_at = [&](int l) { return scales + (s + l) * S::SCALES + slab * 16 * S::SB + tq * 2 * S::SB; }; // of the lane's columns
+            constexpr int VS = S::KC ? TN * S::SB : 0; // V's behind K's
+            if constexpr (S::KC) {
+                uint32_t kw[SL][2][2];
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
+                for (int b = 0; b < NB; ++b) {
+                    const uint4 qx = qa[2 * b * 32], qy = qa[(2 * b + 1) * 32];
+                    uint4 lx, ly;
+                    if (LO) lx = qa[QPART + 2 * b * 32], ly = qa[QPART + (2 * b + 1) * 32];
+#pragma unroll
+                    for (int l = 0; l < SL; ++l) {
                         if (b % 2 == 0) {
-                            load_pair<NB>(kw[0], ksc, b / 2);
-                            load_pair<NB>(kw[1], ksc + 8 * S::SB, b / 2);
+                            load_pair<NB>(kw[l][0], scale_at(l), b / 2);
+                            load_pair<NB>(kw[l][1], scale_at(l) + 8 * S::SB, b / 2);
                         }
                         uint32_t w[4];
-                        ldsm4(w, kt + tree_at<S::KROW>(lrow, 2 * b + lhi));
-                        const uint4 qx = qa[2 * b * 32], qy = qa[(2 * b + 1) * 32];
+                        ldsm4(w, k_tile(l) + tree_at<S::KROW>(lrow, 2 * b + lhi));
                         uint2 c0 = codes4(w[0]), c1 = codes4(w[1]);
                         float t[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
                         mma1(t[0], qx, c0.x, c0.y);
                         mma1(t[1], qx, c1.x, c1.y);
-                        if constexpr (LO) {
-                            const uint4 lx = qa[QPART + 2 * b * 32];
+                        if (LO) {
                             mma1(t[0], lx, c0.x, c0.y);
                             mma1(t[1], lx, c1.x, c1.y);
                         }
                         c0 = codes4(w[2]), c1 = codes4(w[3]);
                         mma1(t[0], qy, c0.x, c0.y);
                         mma1(t[1], qy, c1.x, c1.y);
-                        if constexpr (LO) {
-                            const uint4 ly = qa[QPART + (2 * b + 1) * 32];
+                        if (LO) {
                             mma1(t[0], ly, c0.x, c0.y);
                             mma1(t[1], ly, c1.x, c1.y);
                         }
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
-                            const float d0 = half_of(kw[n][0], b & 1), d1 = half_of(kw[n][1], b & 1);
+                            const float d0 = half_of(kw[l][n][0], b & 1), d1 = half_of(kw[l][n][1], b & 1);
 #pragma unroll
                             for (int c = 0; c < 4; ++c)
-                                sc[n][c] = b ? fmaf(t[n][c], c & 1 ? d1 : d0, sc[n][c]) : t[n][c] * (c & 1 ? d1 : d0);
+                                sc[l][n][c] = b ? fmaf(t[n][c], c & 1 ? d1 : d0, sc[l][n][c]) : t[n][c] * (c & 1 ? d1 : d0);
                         }
                     }
-                } else {
+                }
+            } else {
+#pragma unroll
+                for (int l = 0; l < SL; ++l)
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) sc[n][c] = 0.f;
+                        for (int c = 0; c < 4; ++c) sc[l][n][c] = 0.f;
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint4 qx = qa[ks * 32];
+                    uint4 lx;
+                    if (LO) lx = qa[QPART + ks * 32];
+#pragma unroll
+                    for (int l = 0; l < SL; ++l) {
                         uint32_t w[4];
-                        ldsm4(w, kt + tree_at<S::KROW>(lrow, 2 * ks + lhi));
-                        const uint4 qx = qa[ks * 32];
+                        ldsm4(w, k_tile(l) + tree_at<S::KROW>(lrow, 2 * ks + lhi));
                         if constexpr (LO) {
                             float t[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                            const uint4 lx = qa[QPART + ks * 32];
                             mma1(t[0], qx, w[0], w[2]);
                             mma1(t[1], qx, w[1], w[3]);
                             mma1(t[0], lx, w[0], w[2]);
@@ -423,165 +430,180 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
 #pragma unroll
                             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                                for (int c = 0; c < 4; ++c) sc[n][c] += t[n][c];
+                                for (int c = 0; c < 4; ++c) sc[l][n][c] += t[n][c];
                         } else {
-                            mma1(sc[0], qx, w[0], w[2]);
-                            mma1(sc[1], qx, w[1], w[3]);
+                            mma1(sc[l][0], qx, w[0], w[2]);
+                            mma1(sc[l][1], qx, w[1], w[3]);
                         }
                     }
                 }
-                // ---- what the query rows see: bit 4 n + c of score [n][c]
-                uint32_t see = 0;
-                if constexpr (MASK) {
+            }
+            // ---- what the query rows see: bit 4 n + c of score [n][c]
+            uint32_t see = 0;
+            if constexpr (MASK) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int slot = x.slot[mw + gq + 8 * h];
+                for (int h = 0; h < 2; ++h) {
+                    const int slot = x.slot[mw + gq + 8 * h];
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < 2; ++n)
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const int j = a + 8 * n + 2 * tq + c; // the cached row
-                                bool yes = j >= skip && j < base;
-                                if (j >= base && j < end) yes = x.sees[slot][(j - base) >> 5] >> ((j - base) & 31) & 1;
-                                see |= (yes ? 1u : 0u) << (4 * n + 2 * h + c);
-                            }
-                    }
+                        for (int c = 0; c < 2; ++c) {
+                            const int j = a + 8 * n + 2 * tq + c; // the cached row
+                            bool yes = j >= skip && j < base;
+                            if (j >= base && j < end) yes = x.sees[slot][(j - base) >> 5] >> ((j - base) & 31) & 1;
+                            see |= (yes ? 1u : 0u) << (4 * n + 2 * h + c);
+                        }
                 }
-                auto unseen = [&](int n, int c) { return MASK && !(see >> (4 * n + c) & 1); };
-                // ---- softmax, in log2 units
-                float top[2];
+            }
+            auto unseen = [&](int n, int c) { return MASK && !(see >> (4 * n + c) & 1); };
+            // ---- softmax, in log2 units
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int l = 0; l < SL; ++l)
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        sc[n][c] *= qs[c >> 1];
-                        if (unseen(n, c)) sc[n][c] = -INFINITY;
+                        sc[l][n][c] *= qs[c >> 1];
+                        if (unseen(n, c)) sc[l][n][c] = -INFINITY;
+                        top[c >> 1] = fmaxf(top[c >> 1], sc[l][n][c]);
                     }
+            const bool raise = __any_sync(0xffffffffu, top[0] > mx[0] + T_GROW || top[1] > mx[1] + T_GROW);
+            // ---- V's scales and their exponent
+            int e = E;
+            bool bad = false; // V values of the rows are not finite
+            if constexpr (S::VC) {
+                uint32_t vw[SL][2][2][NB / 2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) top[h] = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
-                const bool raise = __any_sync(0xffffffffu, top[0] > mx[0] + T_GROW || top[1] > mx[1] + T_GROW);
-                // ---- V's scales and their exponent
-                [[maybe_unused]] const uint8_t *vsc = ksc + (S::KC ? TN * S::SB : 0);
-                int e = E;
-                bool bad = false; // V values of the rows are not finite
-                if constexpr (S::VC) {
-                    uint32_t vw[2][2][NB / 2];
-                    load_scales<NB>(vw[0], vsc);
-                    load_scales<NB>(vw[1], vsc + 8 * S::SB);
-                    // the rows' largest; not of rows of nobody, and not of scales that are not finite (which are looked for in
-                    // all rows, as their products would be formed)
-                    auto largest = [&](bool all) {
-                        uint32_t most = 0;
+                for (int l = 0; l < SL; ++l) {
+                    load_scales<NB>(vw[l][0], scale_at(l) + VS);
+                    load_scales<NB>(vw[l][1], scale_at(l) + VS + 8 * S::SB);
+                }
+                // the rows' largest; not of rows of nobody, and not of scales that are not finite (which are looked for in
+                // all rows, as their products would be formed)
+                auto largest = [&](bool all) {
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int l = 0; l < SL; ++l)
 #pragma unroll
                         for (int n = 0; n < 2; ++n)
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
                                 const int j = a + 8 * n + 2 * tq + c;
-                                const bool in = all || (j >= skip && j < end);
+                                const bool in = all || !MASK || (j >= skip && j < end);
 #pragma unroll
                                 for (int b = 0; b < NB / 2; ++b) {
-                                    uint32_t u = vw[n][c][b] & 0x7fff7fffu;
+                                    uint32_t u = vw[l][n][c][b] & 0x7fff7fffu;
                                     if (!all) u &= ~__vcmpgeu2(u, 0x7c007c00u);
                                     most = __vmaxu2(most, in ? u : 0u);
                                 }
                             }
-                        most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                        most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                        return max(most & 0xffffu, most >> 16);
-                    };
-                    uint32_t one = largest(true);
-                    bad = __any_sync(0xffffffffu, one >= 0x7c00u);
-                    if (MASK || bad) one = largest(false);
-                    // (an fp16 number is a normal 32-bit one; a quad's lanes hold all 16 rows)
-                    if (one) e = max(E, (int)(__float_as_uint(half_of(one, 0)) >> 23) - 127);
-                }
-                if (raise || (S::VC && e != E)) {
-                    const float ve = S::VC ? two_to(max(E - e, -126)) : 1.f;
-                    E = e;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float t = top[h];
-                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                        const float nm = t > mx[h] + T_GROW ? t : mx[h];
-                        const float al = nm == mx[h] ? 1.f : ex2(mx[h] - nm); // nothing yet: 0
-                        mx[h] = nm;
-                        sum[h] *= al;
-                        const float f = al * ve;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            acc[n][2 * h] *= f;
-                            acc[n][2 * h + 1] *= f;
-                        }
-                    }
-                }
+                    most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                    most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                    return max(most & 0xffffu, most >> 16);
+                };
+                uint32_t one = largest(true);
+                bad = __any_sync(0xffffffffu, one >= 0x7c00u);
+                if (MASK || bad) one = largest(false);
+                // (an fp16 number is a normal 32-bit one; a quad's lanes hold all rows)
+                if (one) e = max(E, (int)(__float_as_uint(half_of(one, 0)) >> 23) - 127);
+            }
+            if (raise || (S::VC && e != E)) {
+                const float ve = S::VC ? two_to(max(E - e, -126)) : 1.f;
+                E = e;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float use = mx[h] == -INFINITY ? 0.f : mx[h] - T_LIFT;
-                    float add = 0.f;
+                    float t = top[h];
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                    const float nm = t > mx[h] + T_GROW ? t : mx[h];
+                    const float al = nm == mx[h] ? 1.f : ex2(mx[h] - nm); // nothing yet: 0
+                    mx[h] = nm;
+                    sum[h] *= al;
+                    const float f = al * ve;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        acc[n][2 * h] *= f;
+                        acc[n][2 * h + 1] *= f;
+                    }
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float use = mx[h] == -INFINITY ? 0.f : mx[h] - T_LIFT;
+                float add = 0.f;
+#pragma unroll
+                for (int l = 0; l < SL; ++l)
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const float y = ex2(sc[n][2 * h + c] - use);
-                            sc[n][2 * h + c] = y;
+                            const float y = ex2(sc[l][n][2 * h + c] - use);
+                            sc[l][n][2 * h + c] = y;
                             add += y;
                         }
-                    sum[h] += add;
+                sum[h] += add;
+            }
+            // ---- O += P V
+            auto pack = [&](const float (&y)[2][4], uint4 &hi, uint4 &lo) {
+                hi = make_uint4(h2(y[0][0], y[0][1]), h2(y[0][2], y[0][3]), h2(y[1][0], y[1][1]), h2(y[1][2], y[1][3]));
+                if constexpr (LO) {
+                    auto rest = [](uint32_t h, float u, float v) { // (an infinite scale: nothing)
+                        const float2 f = f2(h);
+                        return h2(isinf(f.x) ? 0.f : u - f.x, isinf(f.y) ? 0.f : v - f.y);
+                    };
+                    lo = make_uint4(rest(hi.x, y[0][0], y[0][1]), rest(hi.y, y[0][2], y[0][3]), rest(hi.z, y[1][0], y[1][1]),
+                                    rest(hi.w, y[1][2], y[1][3]));
                 }
-                // ---- O += P V
-                auto pack = [&](const float (&y)[2][4], uint4 &hi, uint4 &lo) {
-                    hi = make_uint4(h2(y[0][0], y[0][1]), h2(y[0][2], y[0][3]), h2(y[1][0], y[1][1]), h2(y[1][2], y[1][3]));
-                    if constexpr (LO) {
-                        auto rest = [](uint32_t h, float u, float v) { // (an infinite scale: nothing)
-                            const float2 f = f2(h);
-                            return h2(isinf(f.x) ? 0.f : u - f.x, isinf(f.y) ? 0.f : v - f.y);
-                        };
-                        lo = make_uint4(rest(hi.x, y[0][0], y[0][1]), rest(hi.y, y[0][2], y[0][3]), rest(hi.z, y[1][0], y[1][1]),
-                                        rest(hi.w, y[1][2], y[1][3]));
-                    }
-                };
-                auto product = [&](float (&o)[4], const uint4 &hi, const uint4 &lo, uint32_t b0, uint32_t b1) {
-                    if constexpr (LO) {
-                        float t[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma1(t, hi, b0, b1);
-                        mma1(t, lo, b0, b1);
+            };
+            auto product = [&](float (&o)[4], const uint4 &hi, const uint4 &lo, uint32_t b0, uint32_t b1) {
+                if constexpr (LO) {
+                    float t[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma1(t, hi, b0, b1);
+                    mma1(t, lo, b0, b1);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) o[c] += t[c];
-                    } else {
-                        mma1(o, hi, b0, b1);
-                    }
-                };
-                // Values that are not finite (0 x inf is NaN): reported, seen to in the end, and 0 in the products.  (`bad`
-                // has them found; another warp that shares the rows may be at the same.)
-                auto leave_out = [&] {
+                    for (int c = 0; c < 4; ++c) o[c] += t[c];
+                } else {
+                    mma1(o, hi, b0, b1);
+                }
+            };
+            // Values that are not finite (0 x inf is NaN): reported, seen to in the end, and 0 in the products.  (`bad`
+            // has them found; another warp that shares the rows may be at the same.)
+            auto leave_out = [&] {
+                for (int l = 0; l < SL; ++l) {
                     if (lane == 0) {
-                        atomicMin(&x.bad_first, a);
-                        atomicMax(&x.bad_last, a);
+                        atomicMin(&x.bad_first, a + l * TN);
+                        atomicMax(&x.bad_last, a + l * TN);
                     }
-                    uint8_t *v = S::VC ? scales + s * S::SCALES + (S::KC ? TN * S::SB : 0) + slab * 16 * S::SB
-                                       : smem + s * S::STAGE + S::KBYTES;
+                    uint8_t *v = S::VC ? scales + (s + l) * S::SCALES + VS + slab * 16 * S::SB : smem + (s + l) * S::STAGE + S::KBYTES;
                     for (int i = lane; i < (S::VC ? 16 * S::SB / 4 : 16 * S::VROW / 4); i += 32) {
                         uint32_t *w = reinterpret_cast<uint32_t *>(
                             S::VC ? v + 4 * i : v + tree_at<S::VROW>(slab * 16 + i / (S::VROW / 4), i % (S::VROW / 4) / 4) + i % 4 * 4);
                         uint32_t u = *w;
                         if (drop_nonfinite(u)) *w = u;
                     }
-                    fence_async(); // (before the copies of a later step)
-                    __syncwarp();
-                };
-                if constexpr (S::VC) {
-                    if (VSCALED && MASK && bad) leave_out();
-                    const __half2 up = __float2half2_rn(VSCALED ? two_to(V_LIFT - E) : 1.f);
-                    const float down = two_to(-E);
-                    uint4 hi, lo;
-                    if (VSCALED) pack(sc, hi, lo);
-                    uint32_t vw[2][2]; // (read again: there are no registers to keep them all)
+                }
+                fence_async(); // (before the copies of a later step)
+                __syncwarp();
+            };
+            if constexpr (S::VC) {
+                if (VSCALED && MASK && bad) leave_out();
+                const __half2 up = __float2half2_rn(VSCALED ? two_to(V_LIFT - E) : 1.f);
+                const float down = two_to(-E);
+                uint4 hi[SL], lo[SL];
+                if (VSCALED) {
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
+                    for (int l = 0; l < SL; ++l) pack(sc[l], hi[l], lo[l]);
+                }
+                uint32_t vw[SL][2][2]; // (read again: a pair of blocks at a time)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                    for (int l = 0; l < SL; ++l) {
+                        const uint32_t vt = k_tile(l) + S::KBYTES;
                         if (b % 2 == 0) {
-                            load_pair<NB>(vw[0], vsc, b / 2);
-                            load_pair<NB>(vw[1], vsc + 8 * S::SB, b / 2);
+                            load_pair<NB>(vw[l][0], scale_at(l) + VS, b / 2);
+                            load_pair<NB>(vw[l][1], scale_at(l) + VS + 8 * S::SB, b / 2);
                         }
                         uint32_t v0[4], v1[4]; // rows 2t, 2t + 1 and those 8 further of four columns of dims
                         if constexpr (VT == KVC_Q4_0) {
@@ -601,7 +623,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                             __half2 d[2]; // scales of rows 2t, 2t + 1 and of those 8 further
 #pragma unroll
                             for (int n = 0; n < 2; ++n) {
-                                uint32_t u = __byte_perm(vw[n][0], vw[n][1], b & 1 ? 0x7632 : 0x5410);
+                                uint32_t u = __byte_perm(vw[l][n][0], vw[l][n][1], b & 1 ? 0x7632 : 0x5410);
                                 d[n] = __hmul2(*reinterpret_cast<__half2 *>(&u), up);
                             }
                             auto times = [](uint32_t v, __half2 f) {
@@ -609,53 +631,70 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                                 return *reinterpret_cast<const uint32_t *>(&y);
                             };
 #pragma unroll
-                            for (int n = 0; n < 4; ++n) product(acc[4 * b + n], hi, lo, times(v0[n], d[0]), times(v1[n], d[1]));
+                            for (int n = 0; n < 4; ++n) product(acc[4 * b + n], hi[l], lo[l], times(v0[n], d[0]), times(v1[n], d[1]));
                         } else {
                             float y[2][4];
 #pragma unroll
                             for (int n = 0; n < 2; ++n) {
-                                const float d0 = half_of(vw[n][0], b & 1) * down, d1 = half_of(vw[n][1], b & 1) * down;
+                                const float d0 = half_of(vw[l][n][0], b & 1) * down, d1 = half_of(vw[l][n][1], b & 1) * down;
 #pragma unroll
-                                for (int c = 0; c < 4; ++c) y[n][c] = unseen(n, c) ? 0.f : sc[n][c] * (c & 1 ? d1 : d0); // (0 x inf)
+                                for (int c = 0; c < 4; ++c) y[n][c] = unseen(n, c) ? 0.f : sc[l][n][c] * (c & 1 ? d1 : d0); // (0 x inf)
                             }
-                            pack(y, hi, lo);
+                            pack(y, hi[l], lo[l]);
 #pragma unroll
-                            for (int n = 0; n < 4; ++n) product(acc[4 * b + n], hi, lo, v0[n], v1[n]);
+                            for (int n = 0; n < 4; ++n) product(acc[4 * b + n], hi[l], lo[l], v0[n], v1[n]);
                         }
                     }
-                } else {
-                    if (LO || MASK) { // (of 16-bit queries that all see the rows, P x inf is what it should be)
-                        __half2 f = __float2half2_rn(0.f);
+                }
+            } else {
+                if (LO || MASK) { // (of 16-bit queries that all see the rows, P x inf is what it should be)
+                    __half2 f = __float2half2_rn(0.f);
+#pragma unroll
+                    for (int l = 0; l < SL; ++l)
 #pragma unroll
                         for (int n = 0; n < NT; n += 2) {
                             uint32_t w[4];
-                            ldsm4t(w, vt + tree_at<S::VROW>(lrow, n + lhi));
+                            ldsm4t(w, k_tile(l) + S::KBYTES + tree_at<S::VROW>(lrow, n + lhi));
 #pragma unroll
                             for (int u = 0; u < 4; ++u) f = __hfma2(*reinterpret_cast<__half2 *>(&w[u]), __float2half2_rn(0.f), f);
                         }
-                        bad = !(__low2float(f) == 0.f && __high2float(f) == 0.f);
-                        if (__any_sync(0xffffffffu, bad)) leave_out();
-                    }
-                    uint4 hi, lo;
-                    pack(sc, hi, lo);
+                    bad = !(__low2float(f) == 0.f && __high2float(f) == 0.f);
+                    if (__any_sync(0xffffffffu, bad)) leave_out();
+                }
+                uint4 hi[SL], lo[SL];
 #pragma unroll
-                    for (int n = 0; n < NT; n += 2) {
+                for (int l = 0; l < SL; ++l) pack(sc[l], hi[l], lo[l]);
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+#pragma unroll
+                    for (int l = 0; l < SL; ++l) {
                         uint32_t w[4];
-                        ldsm4t(w, vt + tree_at<S::VROW>(lrow, n + lhi));
-                        product(acc[n], hi, lo, w[0], w[1]);
-                        product(acc[n + 1], hi, lo, w[2], w[3]);
+                        ldsm4t(w, k_tile(l) + S::KBYTES + tree_at<S::VROW>(lrow, n + lhi));
+                        product(acc[n], hi[l], lo[l], w[0], w[1]);
+                        product(acc[n + 1], hi[l], lo[l], w[2], w[3]);
                     }
                 }
-            };
-            if (a < a1) {
-                if (a < skip || a + 16 > base)
-                    rows16(std::true_type{});
-                else
-                    rows16(std::false_type{});
+            }
+        };
+        int s = 2 * turn, phase = 0;
+        for (int k = 2 * turn; k < steps; k += 2 * turns) {
+            const int a = a0 + k * TN + slab * 16, a2 = a + TN;
+            const bool two = k + 1 < steps;
+            bar_wait_warp(&x.full[s], phase, p.err, &x.abort);
+            if (two) bar_wait_warp(&x.full[s + 1], phase, p.err, &x.abort);
+            if (two && a >= skip && a2 + 16 <= base && a2 < a1) {
+                rows(s, a, std::integral_constant<int, 2>{});
+            } else {
+#pragma unroll 1
+                for (int l = 0; l < 2; ++l)
+                    if (a + l * TN < a1) rows(s + l, a + l * TN, std::integral_constant<int, 1>{});
             }
             __syncwarp();
-            if (lane == 0) bar_arrive(&x.empty[s]);
-            s += turns;
+            if (lane == 0) {
+                bar_arrive(&x.empty[s]);
+                if (two) bar_arrive(&x.empty[s + 1]);
+            }
+            s += 2 * turns;
             if (s >= nst) {
                 s -= nst;
                 phase ^= 1;
@@ -755,8 +794,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     }
 }
 
-template <int D, int KT, int VT, bool LO>
-cudaError_t tree_go(const BlockParams &p, const TreeMaps &t, cudaStream_t st) {
+template <int D, int KT, int VT, bool LO> cudaError_t tree_go(const BlockParams &p, const TreeMaps &t, cudaStream_t st) {
     auto k = tree_kernel<D, KT, VT, LO>;
     constexpr int bytes = TreeShape<D, KT, VT, LO>::SMEM;
     static SharedMemory set;
@@ -766,8 +804,7 @@ cudaError_t tree_go(const BlockParams &p, const TreeMaps &t, cudaStream_t st) {
     e = cudaGetLastError();
     return e == cudaSuccess ? launch_join(p, st) : e;
 }
-template <int D, int KT, int VT>
-cudaError_t tree_pick(const BlockParams &p, const TreeMaps &t, cudaStream_t st) {
+template <int D, int KT, int VT> cudaError_t tree_pick(const BlockParams &p, const TreeMaps &t, cudaStream_t st) {
     return p.act == KVC_ACT_F32 ? tree_go<D, KT, VT, true>(p, t, st) : tree_go<D, KT, VT, false>(p, t, st);
 }
 

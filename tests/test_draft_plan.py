@@ -21,7 +21,7 @@ def test_tree_plans_cover_every_row_within_the_work_space(H, Hk):
         rows = [t + int(np.exp(rng.uniform(0, np.log(200000)))) - 1 for t in n_q]
         off = [int(x) for x in rng.integers(0, 300, n_seq)]
         p = _kvc().kvc_debug_tree_plan(H, Hk, 152, rows, off, n_q)
-        assert p["tile_m"] == 64
+        assert p["tile_m"] == 32
         items = 0
         for n, o, t, w, s, length in zip(rows, off, n_q, p["whole"], p["splits"], p["split_rows"]):
             # rows are counted from the 16-row boundary below the first; parts are whole steps of 64
