@@ -36,13 +36,14 @@ static int ensure_block_space(Ctx *c, cudaStream_t st) {
 
 // Cut the cached rows of the launch's units into parts.  `want`: items that run
 // at once; a part has `least` rows at least, and the partial rows of all parts
-// fit the work space.  An item costs `fixed` steps beside its own.
+// fit the work space.  An item costs `fixed` steps beside its own, joining
+// a sequence's `join` (one sequence).
 //  One sequence: its units are alike, so the schedule is whole waves; those of
 // the last one or two are cut into the parts that shorten it most.
 //  Several: all rows are cut into parts of at most one length, the one for
 // which a schedule ends first that ends half the longest item after the mean
 // (or, in one wave, with the longest item).
-static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t least, int64_t part_cap) {
+static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t least, int64_t part_cap, int64_t join = 1) {
     const int64_t fixed = 4;
     auto parts = [](const BlockSeq &s, int64_t len) {
         return (int32_t)std::max<int64_t>(1, (s.n_rows + len - 1) / len);
@@ -61,7 +62,7 @@ static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t leas
             for (int64_t k = 1; k <= std::min<int64_t>(most, rest ? std::max<int64_t>(8, want / rest) : 1); ++k) {
                 if (k > 1 && rest * k * p.part_rows > part_cap) break;
                 const int64_t cost = full / want * (steps + fixed) +
-                                     (rest * k + want - 1) / want * ((steps + k - 1) / k + fixed + (k > 1 ? 1 : 0));
+                                     (rest * k + want - 1) / want * ((steps + k - 1) / k + fixed + (k > 1 ? join : 0));
                 if (cost < best_cost) {
                     best_cost = cost;
                     s.splits = (int32_t)k;
@@ -140,6 +141,7 @@ static bool plan_block(BlockParams &p, int sms, bool tc) {
 // fewer over all its warps too), one item at a time on an SM.  The kernel counts cached rows from the 16-row boundary at or
 // below the sequence's first.
 static void plan_tree(BlockParams &p, int sms) {
+    constexpr int64_t JOIN = 4;
     int64_t most = 0;
     for (int i = 0; i < p.n_seq; ++i) most = std::max<int64_t>(most, (int64_t)p.seq[i].n_tok * p.r);
     p.tile_m = TREE_TILE;
@@ -149,7 +151,7 @@ static void plan_tree(BlockParams &p, int sms) {
         s.tiles = (int32_t)(((int64_t)s.n_tok * p.r + p.tile_m - 1) / p.tile_m);
         s.n_rows += s.off % 16;
     }
-    plan_splits(p, sms, TREE_STEP, 2 * TREE_STEP, part_rows_cap(sms));
+    plan_splits(p, sms, TREE_STEP, 2 * TREE_STEP, part_rows_cap(sms), JOIN);
     for (int i = 0; i < p.n_seq; ++i) p.seq[i].n_rows -= p.seq[i].off % 16;
 }
 
@@ -170,9 +172,14 @@ static bool use_tc(int rows, double products) { return rows >= TC_MIN_ROWS || pr
 
 // Which kernel runs a tree attention of 16-bit queries: the tcgen05 one where the sequences bring more than 32 query rows a
 // KV head (on the mean over the cached rows) and there is enough to do, by the cached values and the products.  One kernel
-// runs the whole call: two one after the other would each leave the machine to its last items.  Measured in us, q8_0 (f16),
-// bf16 queries, mma.sync against tcgen05, heads/KV heads/D, tokens:
-//   (figures: see the table in the tests' order)
+// runs the whole call: two one after the other would each leave the machine to its last items (32 sequences of 1024 to 32768
+// f16 rows, 4 to 16 tokens: 509 us by two, 394 by the tcgen05 one).  f16 queries over codes stay with the other: the tcgen05
+// one rounds both P and the scaled V to 11 bits, which results of 11 bits would show (3.6e-4 rms against 2.9e-4, and 2.1e-4
+// for the result's own rounding).  Measured in us, bf16 queries, mma.sync against tcgen05, heads/KV heads/D, rows: tokens
+//   40/8/128 q8_0   512:  16 11.6 / 19.4,  64 14.6 / 27.3          4096:  8 16.1 / 21.4,  32 25.7 / 26.2,  64 47.6 / 32.0
+//                 16384:  4 22.0 / 26.5,   8 31.9 / 28.1,  32 71.0 / 37.2      65536:  4 53.7 / 72.4,  8 95.1 / 73.7
+//   32/8/128 f16   4096:  16 13.9 / 19.5,  64 26.5 / 29.3         65536:  8 50.8 / 60.5,  16 65.5 / 60.4,  64 228 / 85.5
+//   8/2/64 q8_0   16384:  64 23.9 / 29.6                          65536:  16 26.5 / 27.6,  64 70.3 / 36.8
 static bool tree_tc_pays(double values, double rows_m, double rows) {
     const double m = rows > 0 ? rows_m / rows : 0;
     return m > 32 && values >= 1 << 22 && m * values >= 1 << 28;
@@ -324,7 +331,8 @@ extern "C" int kvc_attn_tree(kvc_ctx *cc, int layer, int n_seq, const int32_t *s
         rows_m += rows * n_q[i] * c->r;
         all_rows += rows;
     }
-    const bool tc = act != KVC_ACT_F32 && (c->block_kernel ? c->block_kernel == 2 : tree_tc_pays(values, rows_m, all_rows));
+    const bool sixteen = act == KVC_ACT_BF16 || (act == KVC_ACT_F16 && c->tv == KVC_F16);
+    const bool tc = act != KVC_ACT_F32 && (c->block_kernel ? c->block_kernel == 2 : sixteen && tree_tc_pays(values, rows_m, all_rows));
     BlockParams p;
     block_params(c, layer, kq_scale, act, p);
     p.q = q;

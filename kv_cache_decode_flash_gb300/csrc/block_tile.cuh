@@ -17,6 +17,9 @@
 
 namespace kvc {
 
+// What preceding kernels wrote may be read behind this (launches by launch_behind).
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 constexpr int BLOCK_THREADS = 128;
 constexpr int TILE_PAD = 8; // halves behind a row: 16 bytes off a multiple of 128, so ldmatrix has no bank conflicts
 

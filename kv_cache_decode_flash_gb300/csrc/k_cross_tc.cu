@@ -441,6 +441,7 @@ __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(con
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     __syncthreads();
+    if (TREE) wait_for_previous();
     const int r0 = part * q.split_rows, r_end = parts == 1 ? q.n_rows : min(r0 + q.split_rows, q.n_rows);
     if (warp >= WK && warp < WV) {
         regs_dec<R::K>();
@@ -817,8 +818,12 @@ template <bool TREE, int D, int KT, int VT> cudaError_t go(const BlockParams &p,
     static SharedMemory set;
     cudaError_t e = set.allow((const void *)k, bytes, Regs<CODES>::LAUNCH);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)p.n_items, THREADS<CODES>, bytes, st>>>(p);
-    e = cudaGetLastError();
+    if (TREE) {
+        e = launch_behind(k, (unsigned)p.n_items, THREADS<CODES>, bytes, st, p);
+    } else {
+        k<<<(unsigned)p.n_items, THREADS<CODES>, bytes, st>>>(p);
+        e = cudaGetLastError();
+    }
     return e == cudaSuccess ? launch_join(p, st) : e;
 }
 template <bool TREE> cudaError_t pick(int type_k, int type_v, const BlockParams &p, cudaStream_t st) {

@@ -15,6 +15,7 @@ constexpr int JOIN_THREADS = 128, JOIN_ROWS = JOIN_THREADS / 32, AHEAD = 8;
 
 template <int D> __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ BlockParams p, int chunks) {
     constexpr int V = D / 32;
+    wait_for_previous();
     const int cut = (int)blockIdx.x / chunks, lane = threadIdx.x & 31;
     int lo = 0, hi = p.n_seq - 1;
     while (lo < hi) { // the last sequence whose first cut unit is not behind ours
@@ -75,11 +76,7 @@ cudaError_t launch_join(const BlockParams &p, cudaStream_t st) {
     if (p.n_cut <= 0) return cudaSuccess;
     const int chunks = (p.part_rows + JOIN_ROWS - 1) / JOIN_ROWS;
     const unsigned grid = (unsigned)p.n_cut * (unsigned)chunks;
-    if (p.D == 64)
-        join_kernel<64><<<grid, JOIN_THREADS, 0, st>>>(p, chunks);
-    else
-        join_kernel<128><<<grid, JOIN_THREADS, 0, st>>>(p, chunks);
-    return cudaGetLastError();
+    return launch_behind(p.D == 64 ? join_kernel<64> : join_kernel<128>, grid, JOIN_THREADS, 0, st, p, chunks);
 }
 
 } // namespace kvc

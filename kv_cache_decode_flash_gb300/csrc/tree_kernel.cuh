@@ -16,13 +16,14 @@
 //   S = Q K^T by mma.sync m16n8k16, query rows as its rows; a 32-value block of
 //   codes has sums of its own, which the block's scale multiplies in 32 bits.
 //   O += P V: P goes from the scores' registers into the products' operand as it
-//   lies.  With 32-bit queries V's block scale is put into P (P' = P * d * 2^-E, E
-//   the exponent of the largest V scale a warp has met, its sums rescaled when that
-//   grows), Q and P' are two fp16 parts, and every chain of products ends with the
+//   lies, with V's block scale in it (P' = P * d * 2^-E, E the exponent of the
+//   largest V scale a warp has met, its sums rescaled when that grows).  With 32-bit
+//   queries Q and P' are two fp16 parts, and every chain of products ends with the
 //   16 rows, so that 32-bit results keep 32-bit accuracy (the tensor cores truncate
-//   as they accumulate).  With 16-bit results P and V (codes times d * 2^(7 - E))
-//   are one fp16 value each: their roundings (2^-12 at most) average out over the
-//   rows, below the result's own, and P is packed once for all of V's blocks.
+//   as they accumulate).  With f16 ones P' is one fp16 value, whose rounding (2^-11 at
+//   most) is as large as the result's.  With bf16 ones, whose results round eight times
+//   as much, V's codes take the scale (times 2^(7 - E)) instead and are rounded too,
+//   so that P is packed once for all of V's blocks (26 tokens over 16k: 10 % of the time).
 // A row's reference maximum is raised only when a score passes it by more than
 // 2^8; weights stand 2^6 above their value for it, so that they stay normal fp16
 // numbers down to 2^-20 of the largest.
@@ -157,11 +158,12 @@ template <int NB> __device__ __forceinline__ void load_pair(uint32_t (&w)[2], co
     w[1] = *reinterpret_cast<const volatile uint32_t *>(at + 2 * NB + 4 * pair);
 }
 
-template <int D, int KT, int VT, bool LO>
+template <int D, int KT, int VT, int ACT>
 __global__ void __launch_bounds__(TREE_THREADS, 1)
     tree_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ CUtensorMap tmk,
                 const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmk16,
                 const __grid_constant__ CUtensorMap tmv16) {
+    constexpr bool LO = ACT == KVC_ACT_F32; // second parts of Q and P
     using S = TreeShape<D, KT, VT, LO>;
     constexpr int M = TREE_TILE, NB = S::NB, NT = D / 8;
     extern __shared__ uint8_t smem_raw[];
@@ -200,6 +202,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
+    wait_for_previous();
 
     if (warp >= TREE_WARPS) {
         // ------------------------------------------------------- loading
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         for (int c = 0; c < 4; ++c) acc[n][c] = 0.f;
     mx[0] = mx[1] = -INFINITY;
     sum[0] = sum[1] = 0.f;
-    constexpr bool VSCALED = S::VC && !LO; // codes times their scale, rounded to fp16 on the way into the products
+    constexpr bool VSCALED = S::VC && ACT == KVC_ACT_BF16; // codes times their scale, rounded to fp16 on the way into the products
     constexpr int V_LIFT = VSCALED ? 7 : 0; // of V's values above 2^-E times their own
     int E = VSCALED ? 7 - 15 : E_MIN;       // (2^(7 - E) is an fp16 number; smaller scales stay exact enough under that one)
     const int group = warp >> 2, slab = warp & 3;
@@ -794,18 +797,20 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     }
 }
 
-template <int D, int KT, int VT, bool LO> cudaError_t tree_go(const BlockParams &p, const TreeMaps &t, cudaStream_t st) {
-    auto k = tree_kernel<D, KT, VT, LO>;
-    constexpr int bytes = TreeShape<D, KT, VT, LO>::SMEM;
+template <int D, int KT, int VT, int ACT> cudaError_t tree_go(const BlockParams &p, const TreeMaps &t, cudaStream_t st) {
+    auto k = tree_kernel<D, KT, VT, ACT>;
+    constexpr int bytes = TreeShape<D, KT, VT, ACT == KVC_ACT_F32>::SMEM;
     static SharedMemory set;
     cudaError_t e = set.allow((const void *)k, bytes, TREE_REGS);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)p.n_items, TREE_THREADS, bytes, st>>>(p, *t.k, *t.v, *t.k16, *t.v16);
-    e = cudaGetLastError();
+    e = launch_behind(k, (unsigned)p.n_items, TREE_THREADS, bytes, st, p, *t.k, *t.v, *t.k16, *t.v16);
     return e == cudaSuccess ? launch_join(p, st) : e;
 }
 template <int D, int KT, int VT> cudaError_t tree_pick(const BlockParams &p, const TreeMaps &t, cudaStream_t st) {
-    return p.act == KVC_ACT_F32 ? tree_go<D, KT, VT, true>(p, t, st) : tree_go<D, KT, VT, false>(p, t, st);
+    if (p.act == KVC_ACT_F32) return tree_go<D, KT, VT, KVC_ACT_F32>(p, t, st);
+    // (halves need no scale: f16 and bf16 queries are one instance)
+    constexpr int HALF = VT == KVC_F16 ? KVC_ACT_BF16 : KVC_ACT_F16;
+    return p.act == KVC_ACT_F16 ? tree_go<D, KT, VT, HALF>(p, t, st) : tree_go<D, KT, VT, KVC_ACT_BF16>(p, t, st);
 }
 
 } // namespace
