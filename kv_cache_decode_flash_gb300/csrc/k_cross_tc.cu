@@ -53,9 +53,9 @@ template <bool CODES> constexpr int THREADS = (4 + K_GROUPS<CODES>) * GROUP;
 // codes into values need more), the softmax groups take them, so that a thread holds all or half of its row's 128 scores.  (No function of
 // theirs may stay a call: its registers would have to fit the smallest role's.)  Few are to spare: shared memory leaves
 // spilled ones next to no cache (V's codes by two groups as well, with 72 a thread at launch: 139 to 199 us).
-template <bool CODES> struct Regs {
+template <bool CODES, bool TREE> struct Regs {
     static constexpr int LAUNCH = CODES ? 80 : 96;
-    static constexpr int SOFT = CODES ? 136 : 184, K = CODES ? 56 : 40, V = CODES ? 72 : 40, MMA = 24;
+    static constexpr int SOFT = CODES ? (TREE ? 144 : 136) : 184, K = CODES ? (TREE ? 48 : 56) : 40, V = CODES ? 72 : 40, MMA = 24;
     static constexpr int HOLD = CODES ? 2 : 4; // blocks of 32 scores that a softmax thread keeps
     static_assert(2 * SOFT + K_GROUPS<CODES> * K + V + MMA <= THREADS<CODES> / GROUP * LAUNCH, "the roles' registers come from the launch's");
 };
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(con
     constexpr bool CODES = KT != KVC_F16;
     constexpr bool TWO = CODES && !TREE; // K in two parts (a tree has no log-sum-exp that would show the second)
     using L = Lay<D, TWO>;
-    using R = Regs<CODES>;
+    using R = Regs<CODES, TREE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u); // swizzled tiles need 1024-byte alignment
     Aux &x = *reinterpret_cast<Aux *>(smem + L::AUX);
@@ -816,7 +816,7 @@ template <bool TREE, int D, int KT, int VT> cudaError_t go(const BlockParams &p,
     constexpr int bytes = smem_bytes<D, CODES, TREE>();
     static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
     static SharedMemory set;
-    cudaError_t e = set.allow((const void *)k, bytes, Regs<CODES>::LAUNCH);
+    cudaError_t e = set.allow((const void *)k, bytes, Regs<CODES, TREE>::LAUNCH);
     if (e != cudaSuccess) return e;
     if (TREE) {
         e = launch_behind(k, (unsigned)p.n_items, THREADS<CODES>, bytes, st, p);

@@ -6,13 +6,14 @@
 //
 // A work item is one KV head, a tile of up to 32 query rows (tokens x query heads
 // of the group) and a part of the cached rows.  A drafted block is few query
-// rows over many cached ones, so the kernel is built like the single-token one:
-// a loading group keeps a ring of 64-row stages full by TMA (boxes of 64 or 16 rows,
-// swizzled for ldmatrix; a page holds whole ones of 16) and eight warps take 16 cached
-// rows (twice, of neighbouring stages) by 16 query rows each, straight from the stored bytes: codes become exact fp16
-// values in registers, on their way into the products.  Bringing them to fp16 in
-// shared memory first, as the block attention's tcgen05 kernel must, costs more than
-// the products of few query rows.
+// rows over many cached ones, so the kernel is built like the single-token one: a
+// loading group keeps a ring of 64-row stages full by TMA (boxes of 64 or 16 rows,
+// swizzled for ldmatrix; a page holds whole ones of 16) and eight warps take 16
+// cached rows (twice, of neighbouring stages) by 16 query rows each, straight from
+// the stored bytes: codes become exact fp16 values in registers, on their way into
+// the products.  Bringing them to fp16 in shared memory first, as the block
+// attention's tcgen05 kernel must, costs more than the products of few query rows
+// (block_attn.cu has the rule between the two, and both sides measured).
 //   S = Q K^T by mma.sync m16n8k16, query rows as its rows; a 32-value block of
 //   codes has sums of its own, which the block's scale multiplies in 32 bits.
 //   O += P V: P goes from the scores' registers into the products' operand as it
@@ -20,20 +21,26 @@
 //   largest V scale a warp has met, its sums rescaled when that grows).  With 32-bit
 //   queries Q and P' are two fp16 parts, and every chain of products ends with the
 //   16 rows, so that 32-bit results keep 32-bit accuracy (the tensor cores truncate
-//   as they accumulate).  With f16 ones P' is one fp16 value, whose rounding (2^-11 at
-//   most) is as large as the result's.  With bf16 ones, whose results round eight times
-//   as much, V's codes take the scale (times 2^(7 - E)) instead and are rounded too,
-//   so that P is packed once for all of V's blocks (26 tokens over 16k: 10 % of the time).
+//   as they accumulate).  With 16-bit ones P' is one fp16 value, whose rounding (2^-11
+//   at most) is no larger than the result's.  (V's codes times their scale, rounded,
+//   let P be packed once for all of V's blocks: 2 % of the time, one rounding more.)
 // A row's reference maximum is raised only when a score passes it by more than
 // 2^8; weights stand 2^6 above their value for it, so that they stay normal fp16
 // numbers down to 2^-20 of the largest.
 // What a token does not see never reaches it: scores and P' are selected, and
 // where V is f16 a value that is not finite, of a group of rows that not all tokens
-// see (of any, where P is two parts), is left out of the products (0 x inf is NaN), and put
-// into the results of the query rows that see it; so are codes under a
-// scale that is not finite, where the scale is V's.
+// see (of any, where P is two parts), is left out of the products (0 x inf is NaN)
+// and put into the results of the query rows that see it.
 // Warps are joined in shared memory, in their order, and the parts of a tile by
 // join_kernel in theirs: results are bitwise repeatable.
+// What bounds it: with up to 16 query rows a KV head memory (halves: 65536 rows of 8
+// KV heads of D 128 in 49 us, 5.5 TB/s; 16 sequences of 4096 rows 46 us) or, of codes,
+// the instructions between their bytes and the products (38 us, 3.7 TB/s); with more
+// of both the latter, two thirds of mma.sync's rate at the most.  What it cost to find:
+// copies of 16 rows issued by one warp, 100 cycles each whatever their size (62 us),
+// sixteen warps of 96 registers, whose spilled ones have no cache beside this much
+// shared memory (59 against 54 us of 4 tokens), the next rows' scores among the weights
+// and products of these (76 against 68 us of 26 tokens over 16k, by the first build).
 #pragma once
 
 #include "tc_tile.cuh"
@@ -72,11 +79,11 @@ template <int D, int KT, int VT, bool LO> struct TreeShape {
 struct TreeAux {
     uint64_t full[12], empty[12];
     int32_t parent[TREE_MAX];
-    uint32_t sees[64][TREE_MAX / 32]; // of the tile's tokens, which of the block's rows they see
-    float qscale[64];
-    uint32_t poison[64][8];   // two bits a value: +inf, -inf (both: NaN) received
+    uint32_t sees[TREE_TILE][TREE_MAX / 32]; // of the tile's tokens, which of the block's rows they see
+    float qscale[TREE_TILE];
+    uint32_t poison[TREE_TILE][8]; // two bits a value: +inf, -inf (both: NaN) received
     int32_t bad_first, bad_last; // 16-row groups with values that were left out of the products
-    int32_t slot[64];         // query row's token, counted from the tile's first
+    int32_t slot[TREE_TILE];  // query row's token, counted from the tile's first
     float m[TREE_WARPS][16], l[TREE_WARPS][16]; // the warps' maxima and sums
     volatile int32_t abort;
 };
@@ -158,12 +165,11 @@ template <int NB> __device__ __forceinline__ void load_pair(uint32_t (&w)[2], co
     w[1] = *reinterpret_cast<const volatile uint32_t *>(at + 2 * NB + 4 * pair);
 }
 
-template <int D, int KT, int VT, int ACT>
+template <int D, int KT, int VT, bool LO>
 __global__ void __launch_bounds__(TREE_THREADS, 1)
     tree_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ CUtensorMap tmk,
                 const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmk16,
                 const __grid_constant__ CUtensorMap tmv16) {
-    constexpr bool LO = ACT == KVC_ACT_F32; // second parts of Q and P
     using S = TreeShape<D, KT, VT, LO>;
     constexpr int M = TREE_TILE, NB = S::NB, NT = D / 8;
     extern __shared__ uint8_t smem_raw[];
@@ -349,9 +355,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         for (int c = 0; c < 4; ++c) acc[n][c] = 0.f;
     mx[0] = mx[1] = -INFINITY;
     sum[0] = sum[1] = 0.f;
-    constexpr bool VSCALED = S::VC && ACT == KVC_ACT_BF16; // codes times their scale, rounded to fp16 on the way into the products
-    constexpr int V_LIFT = VSCALED ? 7 : 0; // of V's values above 2^-E times their own
-    int E = VSCALED ? 7 - 15 : E_MIN;       // (2^(7 - E) is an fp16 number; smaller scales stay exact enough under that one)
+    int E = E_MIN;
     const int group = warp >> 2, slab = warp & 3;
     const int mw = group % shares * 16, turn = group / shares; // the warp's first query row; its set of groups
     {
@@ -368,7 +372,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             float sc[SL][2][4];
             auto k_tile = [&](int l) { return smem_u32(smem + (s + l) * S::STAGE); };
             auto scale_at = [&](int l) { return scales + (s + l) * S::SCALES + slab * 16 * S::SB + tq * 2 * S::SB; }; // of the lane's columns
-            constexpr int VS = S::KC ? TN * S::SB : 0; // V's behind K's
+            [[maybe_unused]] constexpr int VS = S::KC ? TN * S::SB : 0; // V's behind K's
             if constexpr (S::KC) {
                 uint32_t kw[SL][2][2];
 #pragma unroll
@@ -578,10 +582,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                         atomicMin(&x.bad_first, a + l * TN);
                         atomicMax(&x.bad_last, a + l * TN);
                     }
-                    uint8_t *v = S::VC ? scales + (s + l) * S::SCALES + VS + slab * 16 * S::SB : smem + (s + l) * S::STAGE + S::KBYTES;
-                    for (int i = lane; i < (S::VC ? 16 * S::SB / 4 : 16 * S::VROW / 4); i += 32) {
+                    uint8_t *v = smem + (s + l) * S::STAGE + S::KBYTES;
+                    for (int i = lane; i < 16 * S::VROW / 4; i += 32) {
                         uint32_t *w = reinterpret_cast<uint32_t *>(
-                            S::VC ? v + 4 * i : v + tree_at<S::VROW>(slab * 16 + i / (S::VROW / 4), i % (S::VROW / 4) / 4) + i % 4 * 4);
+                            v + tree_at<S::VROW>(slab * 16 + i / (S::VROW / 4), i % (S::VROW / 4) / 4) + i % 4 * 4);
                         uint32_t u = *w;
                         if (drop_nonfinite(u)) *w = u;
                     }
@@ -590,14 +594,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 __syncwarp();
             };
             if constexpr (S::VC) {
-                if (VSCALED && MASK && bad) leave_out();
-                const __half2 up = __float2half2_rn(VSCALED ? two_to(V_LIFT - E) : 1.f);
                 const float down = two_to(-E);
-                uint4 hi[SL], lo[SL];
-                if (VSCALED) {
-#pragma unroll
-                    for (int l = 0; l < SL; ++l) pack(sc[l], hi[l], lo[l]);
-                }
                 uint32_t vw[SL][2][2]; // (read again: a pair of blocks at a time)
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
@@ -622,31 +619,17 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                             row_pairs(w[2], v0[2], v0[3]);
                             row_pairs(w[3], v1[2], v1[3]);
                         }
-                        if constexpr (VSCALED) {
-                            __half2 d[2]; // scales of rows 2t, 2t + 1 and of those 8 further
+                        float y[2][4];
 #pragma unroll
-                            for (int n = 0; n < 2; ++n) {
-                                uint32_t u = __byte_perm(vw[l][n][0], vw[l][n][1], b & 1 ? 0x7632 : 0x5410);
-                                d[n] = __hmul2(*reinterpret_cast<__half2 *>(&u), up);
-                            }
-                            auto times = [](uint32_t v, __half2 f) {
-                                const __half2 y = __hmul2(*reinterpret_cast<__half2 *>(&v), f);
-                                return *reinterpret_cast<const uint32_t *>(&y);
-                            };
+                        for (int n = 0; n < 2; ++n) {
+                            const float d0 = half_of(vw[l][n][0], b & 1) * down, d1 = half_of(vw[l][n][1], b & 1) * down;
 #pragma unroll
-                            for (int n = 0; n < 4; ++n) product(acc[4 * b + n], hi[l], lo[l], times(v0[n], d[0]), times(v1[n], d[1]));
-                        } else {
-                            float y[2][4];
-#pragma unroll
-                            for (int n = 0; n < 2; ++n) {
-                                const float d0 = half_of(vw[l][n][0], b & 1) * down, d1 = half_of(vw[l][n][1], b & 1) * down;
-#pragma unroll
-                                for (int c = 0; c < 4; ++c) y[n][c] = unseen(n, c) ? 0.f : sc[l][n][c] * (c & 1 ? d1 : d0); // (0 x inf)
-                            }
-                            pack(y, hi[l], lo[l]);
-#pragma unroll
-                            for (int n = 0; n < 4; ++n) product(acc[4 * b + n], hi[l], lo[l], v0[n], v1[n]);
+                            for (int c = 0; c < 4; ++c) y[n][c] = unseen(n, c) ? 0.f : sc[l][n][c] * (c & 1 ? d1 : d0); // (0 x inf)
                         }
+                        uint4 hi, lo;
+                        pack(y, hi, lo);
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) product(acc[4 * b + n], hi, lo, v0[n], v1[n]);
                     }
                 }
             } else {
@@ -721,7 +704,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     const int rw = 4 * turns;                     // warps that share query rows
     auto warp_of = [&](int m, int i) { return ((m >> 4) + (i >> 2) * shares) * 4 + (i & 3); };
     {
-        const float back = S::VC ? two_to(E - V_LIFT) : 1.f;
+        const float back = S::VC ? two_to(E) : 1.f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int m = gq + 8 * h;
@@ -797,9 +780,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     }
 }
 
-template <int D, int KT, int VT, int ACT> cudaError_t tree_go(const BlockParams &p, const TreeMaps &t, cudaStream_t st) {
-    auto k = tree_kernel<D, KT, VT, ACT>;
-    constexpr int bytes = TreeShape<D, KT, VT, ACT == KVC_ACT_F32>::SMEM;
+template <int D, int KT, int VT, bool LO> cudaError_t tree_go(const BlockParams &p, const TreeMaps &t, cudaStream_t st) {
+    auto k = tree_kernel<D, KT, VT, LO>;
+    constexpr int bytes = TreeShape<D, KT, VT, LO>::SMEM;
     static SharedMemory set;
     cudaError_t e = set.allow((const void *)k, bytes, TREE_REGS);
     if (e != cudaSuccess) return e;
@@ -807,10 +790,7 @@ template <int D, int KT, int VT, int ACT> cudaError_t tree_go(const BlockParams 
     return e == cudaSuccess ? launch_join(p, st) : e;
 }
 template <int D, int KT, int VT> cudaError_t tree_pick(const BlockParams &p, const TreeMaps &t, cudaStream_t st) {
-    if (p.act == KVC_ACT_F32) return tree_go<D, KT, VT, KVC_ACT_F32>(p, t, st);
-    // (halves need no scale: f16 and bf16 queries are one instance)
-    constexpr int HALF = VT == KVC_F16 ? KVC_ACT_BF16 : KVC_ACT_F16;
-    return p.act == KVC_ACT_F16 ? tree_go<D, KT, VT, HALF>(p, t, st) : tree_go<D, KT, VT, KVC_ACT_BF16>(p, t, st);
+    return p.act == KVC_ACT_F32 ? tree_go<D, KT, VT, true>(p, t, st) : tree_go<D, KT, VT, false>(p, t, st);
 }
 
 } // namespace
