@@ -150,12 +150,12 @@ def _check(ctx, status: int):
 
 
 def _addr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or type(x) is int:
         return x
     if hasattr(x, "data_ptr"):
         return x.data_ptr()
+    if isinstance(x, int):
+        return int(x)
     raise TypeError("expected a tensor or an address")
 
 
@@ -259,12 +259,14 @@ def _head_rows(name, t, device, dtype, tokens, heads, dim):
         raise KvcError(KVC_EINVAL, "%s must be a tensor on cuda:%d" % (name, device))
     if t.dtype is not dtype:
         raise KvcError(KVC_EINVAL, "%s must be %s, not %s" % (name, dtype, t.dtype))
-    shape, st = t.shape, t.stride()
-    if len(shape) != 3 or shape[0] < tokens or shape[1] != heads or shape[2] != dim:
+    if t.dim() != 3:
         raise KvcError(KVC_EINVAL, "%s must be [%d][%d][%d]" % (name, tokens, heads, dim))
-    if st[2] != 1 or (st[1] != dim and heads > 1):
+    (n, h, d), (s0, s1, s2) = t.shape, t.stride()
+    if n < tokens or h != heads or d != dim:
+        raise KvcError(KVC_EINVAL, "%s must be [%d][%d][%d]" % (name, tokens, heads, dim))
+    if s2 != 1 or (s1 != dim and heads > 1):
         raise KvcError(KVC_EINVAL, "%s: a token's head-rows must be contiguous" % name)
-    return st[0] if shape[0] > 1 else heads * dim
+    return s0 if n > 1 else heads * dim
 
 
 def _block(seq_ids, n_q):
@@ -297,16 +299,17 @@ def _host_ints(x):
         except TypeError:
             a = array("i", [int(v) for v in x])
         return a.buffer_info()[0], len(a), a
-    if hasattr(x, "__array_interface__"):
-        if x.dtype != "int32" or not x.flags.c_contiguous:
-            import numpy as np
+    view = getattr(x, "__array_interface__", None)
+    if view is None:
+        return _host_ints(list(x))
+    if view["typestr"] != "<i4" or view["strides"] is not None:  # (None: contiguous)
+        import numpy as np
 
-            a = np.ascontiguousarray(x, np.int32)
-            if not np.array_equal(a, x):
-                raise KvcError(KVC_ERANGE, "values must fit 32 bits")
-            x = a
-        return x.__array_interface__["data"][0], x.size, x
-    return _host_ints(list(x))
+        a = np.ascontiguousarray(x, np.int32)
+        if not np.array_equal(a, x):
+            raise KvcError(KVC_ERANGE, "values must fit 32 bits")
+        return a.__array_interface__["data"][0], a.size, a
+    return view["data"][0], x.size, x
 
 
 def _same_count(n, m):
@@ -668,8 +671,8 @@ class KVCache:
             _block_tensor("q_norm", q_norm, device, _torch.float32, dim)
         if k_norm is not None:
             _block_tensor("k_norm", k_norm, device, _torch.float32, dim)
-        kvc_append_rope(self.ctx, layer, seq_ids, n_tok, pos, act, q, qs, k, ks, v, vs, q_out, q_norm, k_norm, eps,
-                        stream, device)
+        kvc_append_rope(self.ctx, layer, seq_ids, n_tok, pos, act, q, qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                        q_out, q_norm, k_norm, eps, stream, device)
 
     def keep(self, seq_ids, n_last, keep, stream=None):
         """Of the last n_last[i] rows of sequence seq_ids[i] keep those at the places keep[i] (ascending); the
