@@ -511,8 +511,9 @@ int kvc_debug_chunk_plan(int type, int head_dim, int n_head, int n_head_kv, int 
 int kvc_debug_chunk_plan_seq(int type, int head_dim, int n_head, int n_head_kv, int sms, int occ, int occ2,
                              int n_seq, const int32_t *rows, int32_t *chunk_rows_seq, int32_t *cfg);
 
-/* Test hook: the kernel that kvc_attn_cross runs for 16-bit queries: 1 the
- * mma.sync one, 2 the tcgen05 one, 0 the one that the sizes choose (the default).
+/* Test hook: the kernel that kvc_attn_cross and kvc_attn_tree run for 16-bit
+ * queries: 1 the mma.sync one, 2 the tcgen05 one, 0 the one that the sizes choose
+ * (the default).
  * 32-bit queries always run the mma.sync one.  Errors: KVC_EINVAL. */
 int kvc_debug_block_kernel(kvc_ctx *c, int which);
 

@@ -321,8 +321,8 @@ def kvc_attn_tree(ctx, layer, seq_ids, n_q, act, q, out, kq_scale, parent=None, 
     ids, n, keep_ids = _host_ints(seq_ids)
     nq, m, keep_nq = _host_ints(n_q)
     _same_count(n, m)
-    status = load().kvc_attn_tree(ctx, layer, n, ids, nq, act, _addr(q), _addr(out), _addr(parent), kq_scale,
-                                  _stream(stream, device))
+    status = load().kvc_attn_tree(ctx, layer, n, ids, nq, act, _addr(q), _addr(out), _addr(parent),
+                                  float(kq_scale), _stream(stream, device))
     if status:
         _check(ctx, status)
 
@@ -336,7 +336,8 @@ def kvc_append_rope(ctx, layer, seq_ids, n_tok, pos, act, q, q_stride, k, k_stri
     if have < sum(n_tok):
         raise KvcError(KVC_EINVAL, "%d positions for %d tokens" % (have, sum(n_tok)))
     status = load().kvc_append_rope(ctx, layer, n, ids, nt, ps, act, _addr(q), q_stride, _addr(k), k_stride, _addr(v),
-                                    v_stride, _addr(q_norm), _addr(k_norm), eps, _addr(q_out), _stream(stream, device))
+                                    v_stride, _addr(q_norm), _addr(k_norm), float(eps), _addr(q_out),
+                                    _stream(stream, device))
     if status:
         _check(ctx, status)
 
