@@ -37,13 +37,14 @@ static int ensure_block_space(Ctx *c, cudaStream_t st) {
 // Cut the cached rows of the launch's units into parts.  `want`: items that run
 // at once; a part has `least` rows at least, and the partial rows of all parts
 // fit the work space.  An item costs `fixed` steps beside its own, joining
-// a sequence's `join` (one sequence).
+// a sequence's `join` (one sequence).  may_sort: the launch's sequences may change places.
 //  One sequence: its units are alike, so the schedule is whole waves; those of
 // the last one or two are cut into the parts that shorten it most.
 //  Several: all rows are cut into parts of at most one length, the one for
 // which a schedule ends first that ends half the longest item after the mean
 // (or, in one wave, with the longest item).
-static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t least, int64_t part_cap, int64_t join = 1) {
+static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t least, int64_t part_cap, int64_t join = 1,
+                        bool may_sort = false) {
     const int64_t fixed = 4;
     auto parts = [](const BlockSeq &s, int64_t len) {
         return (int32_t)std::max<int64_t>(1, (s.n_rows + len - 1) / len);
@@ -100,6 +101,20 @@ static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t leas
             s.whole = s.splits > 1 ? 0 : s.tiles * p.Hk;
         }
     }
+    int64_t items = 0;
+    for (int i = 0; i < p.n_seq; ++i) {
+        const BlockSeq &s = p.seq[i];
+        items += s.whole + ((int64_t)s.tiles * p.Hk - s.whole) * s.splits;
+    }
+    // In up to two waves the longest items begin first, so that none of them
+    // begins late (6 tokens each, q8_0, 8 heads of 128, as given and sorted: 32
+    // sequences of 64 to 400 rows 21.0 and 18.1 us, 16 of 300 to 3000 rows 35.2
+    // and 33.1).  Over more waves the order as given is no worse (1 token each,
+    // 32 sequences of 1024 to 8000 rows: 99 us as given, 103 sorted).
+    if (may_sort && items <= 2 * want)
+        std::stable_sort(p.seq, p.seq + p.n_seq, [](const BlockSeq &a, const BlockSeq &b) {
+            return (int64_t)a.n_rows * b.splits > (int64_t)b.n_rows * a.splits;
+        });
     int32_t item = 0, row = 0;
     p.n_cut = 0;
     for (int i = 0; i < p.n_seq; ++i) {
@@ -151,7 +166,7 @@ static void plan_tree(BlockParams &p, int sms) {
         s.tiles = (int32_t)(((int64_t)s.n_tok * p.r + p.tile_m - 1) / p.tile_m);
         s.n_rows += s.off % 16;
     }
-    plan_splits(p, sms, TREE_STEP, 2 * TREE_STEP, part_rows_cap(sms), JOIN);
+    plan_splits(p, sms, TREE_STEP, 2 * TREE_STEP, part_rows_cap(sms), JOIN, true);
     for (int i = 0; i < p.n_seq; ++i) p.seq[i].n_rows -= p.seq[i].off % 16;
 }
 
@@ -481,6 +496,7 @@ extern "C" int kvc_debug_tree_plan(int n_head, int n_head_kv, int sms, int n_seq
         p.seq[i].n_rows = rows[i];
         p.seq[i].off = off[i];
         p.seq[i].n_tok = n_q[i];
+        p.seq[i].id = i;
     }
     plan_tree(p, sms);
     *tile_m = p.tile_m;
@@ -489,9 +505,9 @@ extern "C" int kvc_debug_tree_plan(int n_head, int n_head_kv, int sms, int n_seq
     *part_cap = part_rows_cap(sms);
     for (int i = 0; i < n_seq; ++i) {
         const BlockSeq &s = p.seq[i];
-        whole[i] = s.whole;
-        splits[i] = s.splits;
-        split_rows[i] = s.split_rows;
+        whole[s.id] = s.whole;
+        splits[s.id] = s.splits;
+        split_rows[s.id] = s.split_rows;
         const int64_t cut = (int64_t)s.tiles * p.Hk - s.whole;
         *part_rows = std::max<int64_t>(*part_rows, s.part_row0 + cut * s.splits * p.part_rows);
     }

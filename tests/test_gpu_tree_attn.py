@@ -168,6 +168,34 @@ def test_tree_ragged_batch(kind, act):
         tw.close()
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("kind,lens", [("q8", [90, 1500, 64, 2200, 333]), ("f16", [1, 700, 40, 1300, 2])])
+def test_tree_order_of_the_sequences_changes_no_bit(kind, lens, act):
+    """Short and long sequences in either order: the kernel begins with the longest, a sequence's result is its own."""
+    import torch
+
+    H, Hk, D = 8, 2, 64
+    tw = _force(_cache(kind, H, Hk, D, lens))
+    try:
+        rng = np.random.default_rng(11)
+        n_q = [6, 3, 33, 1, 2]
+        n_q = [min(t, n) for t, n in zip(n_q, lens)]
+        qs = [_queries(rng, t, H, D, act) for t in n_q]
+        ps = [_parents(rng, t) for t in n_q]
+        results = []
+        for order in ([0, 1, 2, 3, 4], [4, 3, 2, 1, 0], [2, 4, 1, 0, 3]):
+            q, m = torch.cat([qs[i] for i in order]), [n_q[i] for i in order]
+            parent = np.concatenate([ps[i] for i in order])
+            got = _run(tw, order, m, q, 0.125, parent)
+            _compare(tw, order, m, q, 0.125, parent, got, act)
+            results.append(dict(zip(order, got.split(m))))
+        for i in range(5):
+            for r in results[1:]:
+                assert torch.equal(r[i].view(torch.uint8), results[0][i].view(torch.uint8))
+    finally:
+        tw.close()
+
+
 def test_tree_more_sequences_than_a_launch_holds():
     import torch
 
