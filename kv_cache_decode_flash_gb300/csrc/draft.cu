@@ -63,7 +63,7 @@ static void make_room(std::vector<int32_t> &v, size_t n) {
 
 static bool run_of(const int32_t *pos, int n) {
     for (int i = 1; i < n; ++i)
-        if (pos[i] != pos[0] + i) return false;
+        if (pos[i] != (int64_t)pos[0] + i) return false;
     return true;
 }
 
@@ -300,7 +300,7 @@ static int seq_keep(Ctx *c, int n_seq, const int32_t *ids, const int32_t *n_last
         q.n = (int32_t)base + n_keep[i];
         q.pos.resize((size_t)q.n);
         if (!q.linear) q.linear = consecutive(q.pos.data(), q.n);
-        else if (n_keep[i]) q.linear = consecutive(q.pos.data() + base, n_keep[i]) && (base == 0 || q.pos[base] == q.pos[base - 1] + 1);
+        else if (n_keep[i]) q.linear = consecutive(q.pos.data() + base, n_keep[i]) && (base == 0 || q.pos[base] == (int64_t)q.pos[base - 1] + 1);
         release_tail_pages(c, q);
         for (auto &f : q.lfill) f = q.n;
         // rows that moved were written by a kernel that the next one may overlap
