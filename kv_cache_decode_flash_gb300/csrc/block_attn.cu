@@ -37,17 +37,23 @@ static int ensure_block_space(Ctx *c, cudaStream_t st) {
 // Cut the cached rows of the launch's units into parts.  `want`: items that run
 // at once; a part has `least` rows at least, and the partial rows of all parts
 // fit the work space.  An item costs `fixed` steps beside its own, joining
-// a sequence's `join` (one sequence).  may_sort: the launch's sequences may change places.
+// a sequence's `join` (one sequence).  tree: the launch's sequences may change
+// places, and four waves of items are enough (32 sequences of 1024 to 8000 rows,
+// 16 tokens each: 276 us with up to nine, 262 so; f16 190 and 177).  weighted: a
+// step of a unit that fills half a tile at most costs 5/8 of another's.
 //  One sequence: its units are alike, so the schedule is whole waves; those of
 // the last one or two are cut into the parts that shorten it most.
 //  Several: all rows are cut into parts of at most one length, the one for
 // which a schedule ends first that ends half the longest item after the mean
 // (or, in one wave, with the longest item).
 static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t least, int64_t part_cap, int64_t join = 1,
-                        bool may_sort = false) {
+                        bool tree = false, bool weighted = false) {
     const int64_t fixed = 4;
-    auto parts = [](const BlockSeq &s, int64_t len) {
-        return (int32_t)std::max<int64_t>(1, (s.n_rows + len - 1) / len);
+    auto eighths = [&](const BlockSeq &s) {
+        return weighted && (int64_t)s.n_tok * p.r - (int64_t)s.tile0 * p.tile_m <= p.tile_m / 2 ? 5 : 8;
+    };
+    auto parts = [&](const BlockSeq &s, int64_t len) {
+        return (int32_t)std::max<int64_t>(1, ((int64_t)s.n_rows * eighths(s) / 8 + len - 1) / len);
     };
     int64_t longest = step;
     for (int i = 0; i < p.n_seq; ++i)
@@ -74,14 +80,15 @@ static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t leas
     } else {
         double best = 0;
         int64_t best_len = longest;
-        for (int64_t len = longest;; len = std::max(least, len * 3 / 4 / step * step)) {
+        int64_t cuts = 1; // of few sequences every length counts
+        for (int64_t len = longest;;) {
             int64_t items = 0, slots = 0, most = 0;
             double total = 0;
             for (int i = 0; i < p.n_seq; ++i) {
                 const BlockSeq &s = p.seq[i];
                 const int64_t k = parts(s, len), n = (int64_t)s.tiles * p.Hk * k;
                 if (!n) continue;
-                const int64_t cost = fixed + ((s.n_rows + k - 1) / k + step - 1) / step;
+                const int64_t cost = fixed + (((s.n_rows + k - 1) / k + step - 1) / step * eighths(s) + 7) / 8;
                 items += n;
                 if (k > 1) slots += n;
                 total += (double)n * (double)cost;
@@ -93,7 +100,11 @@ static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t leas
                 best = est;
                 best_len = len;
             }
-            if (len <= least) break;
+            if (len <= least || (tree && items > 4 * want)) break;
+            if (weighted && p.n_seq <= 4)
+                len = std::max(least, (longest / ++cuts + step - 1) / step * step);
+            else
+                len = std::max(least, len * 3 / 4 / step * step);
         }
         for (int i = 0; i < p.n_seq; ++i) {
             BlockSeq &s = p.seq[i];
@@ -111,9 +122,9 @@ static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t leas
     // sequences of 64 to 400 rows 21.0 and 18.1 us, 16 of 300 to 3000 rows 35.2
     // and 33.1).  Over more waves the order as given is no worse (1 token each,
     // 32 sequences of 1024 to 8000 rows: 99 us as given, 103 sorted).
-    if (may_sort && items <= 2 * want)
-        std::stable_sort(p.seq, p.seq + p.n_seq, [](const BlockSeq &a, const BlockSeq &b) {
-            return (int64_t)a.n_rows * b.splits > (int64_t)b.n_rows * a.splits;
+    if (tree && items <= 2 * want)
+        std::stable_sort(p.seq, p.seq + p.n_seq, [&](const BlockSeq &a, const BlockSeq &b) {
+            return (int64_t)a.n_rows * eighths(a) * b.splits > (int64_t)b.n_rows * eighths(b) * a.splits;
         });
     int32_t item = 0, row = 0;
     p.n_cut = 0;
@@ -170,6 +181,29 @@ static void plan_tree(BlockParams &p, int sms) {
     for (int i = 0; i < p.n_seq; ++i) p.seq[i].n_rows -= p.seq[i].off % 16;
 }
 
+// The same for the tcgen05 kernel.  A last tile whose query rows fill half of it at most costs less a step (65536 q8_0 rows of
+// 8 KV heads: 125 rows 76 us, 255 rows 108), so it is an entry of its own, with longer parts, where the launch has room (64
+// tokens of 5 heads over 32768 rows 108 us as one entry, 95 as two; 32 sequences of 20 to 80 tokens over 1024 to 8000 rows 419
+// and 374).
+static void plan_tree_tc(BlockParams &p, int sms) {
+    int32_t most = 0;
+    for (int i = 0; i < p.n_seq; ++i) most = std::max(most, p.seq[i].n_tok);
+    p.tile_m = CROSS_TC_TILE_M;
+    p.part_rows = (int32_t)std::max<int64_t>(1, std::min<int64_t>(p.tile_m, (int64_t)most * p.r));
+    for (int i = 0, n = p.n_seq; i < n; ++i) {
+        BlockSeq &s = p.seq[i];
+        const int64_t m = (int64_t)s.n_tok * p.r;
+        s.tiles = (int32_t)((m + p.tile_m - 1) / p.tile_m);
+        s.tile0 = 0;
+        if (s.tiles < 2 || m - (int64_t)(s.tiles - 1) * p.tile_m > p.tile_m / 2 || p.n_seq == MAX_SEQ_PER_LAUNCH) continue;
+        BlockSeq &last = p.seq[p.n_seq++];
+        last = s;
+        last.tile0 = --s.tiles;
+        last.tiles = 1;
+    }
+    plan_splits(p, sms, CROSS_TC_TILE_N, 2 * CROSS_TC_TILE_N, part_rows_cap(sms), 1, true, true);
+}
+
 // Which kernel attends a sequence of 16-bit queries (both hold scores to 32 bits).  The tcgen05 kernel pays where a call
 // has enough to do, by its cached values (rows x KV heads x D) or its products (times query rows of a KV head); and in
 // such a call for the sequences that have TC_MIN_ROWS rows or enough products of their own: an item of few tokens over
@@ -191,7 +225,7 @@ static bool use_tc(int rows, double products) { return rows >= TC_MIN_ROWS || pr
 // f16 rows, 4 to 16 tokens: 509 us by two, 394 by the tcgen05 one).  f16 queries over codes stay with the other: the tcgen05
 // one rounds both P and the scaled V to 11 bits, which results of 11 bits would show (3.6e-4 rms against 2.9e-4, and 2.1e-4
 // for the result's own rounding).  Measured in us, bf16 queries, mma.sync against tcgen05, heads/KV heads/D, rows: tokens
-//   40/8/128 q8_0   512:  16 11.6 / 19.4,  64 14.6 / 27.3          4096:  8 16.1 / 21.4,  32 25.7 / 26.2,  64 47.6 / 32.0
+//   40/8/128 q8_0   512:  16 11.6 / 19.4,  64 14.6 / 27.3          4096:  8 16.1 / 21.4,  32 25.7 / 26.2,  64 47.6 / 28.9
 //                 16384:  4 22.0 / 26.5,   8 31.9 / 28.1,  32 71.0 / 37.2      65536:  4 53.7 / 72.4,  8 95.1 / 73.7
 //   32/8/128 f16   4096:  16 13.9 / 19.5,  64 26.5 / 29.3         65536:  8 50.8 / 60.5,  16 65.5 / 60.4,  64 228 / 85.5
 //   8/2/64 q8_0   16384:  64 23.9 / 29.6                          65536:  16 26.5 / 27.6,  64 70.3 / 36.8
@@ -370,7 +404,7 @@ extern "C" int kvc_attn_tree(kvc_ctx *cc, int layer, int n_seq, const int32_t *s
         if (p.n_seq == 0 || (p.n_seq < MAX_SEQ_PER_LAUNCH && i + 1 < n_seq)) continue;
         cudaError_t e;
         if (tc) {
-            plan_block(p, c->sms, true);
+            plan_tree_tc(p, c->sms);
             e = launch_tree_tc(c->tk, c->tv, p, st);
         } else {
             plan_tree(p, c->sms);

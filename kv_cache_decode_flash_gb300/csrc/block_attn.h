@@ -18,6 +18,7 @@ struct BlockSeq {
     int32_t n_rows;     // cached rows
     int32_t tok0;       // its first token in q / out / lse / n_vis
     int32_t n_tok;      // its tokens
+    int32_t tile0;      // its first query tile (a tree's short last one may be an entry of its own)
     int32_t tiles;      // query tiles of a KV head
     int32_t item0;      // first work item of the launch that is this sequence's
     int32_t whole;      // leading units (KV head, query tile) that are one item each; the others are `splits` items

@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(con
     const int local = (int)blockIdx.x - q.item0;
     int unit, part, parts;
     item_unit(q, local, unit, part, parts);
-    const int g = unit / q.tiles, tile = q.tiles - 1 - unit % q.tiles; // later tokens see more: they begin first
+    const int g = unit / q.tiles, tile = q.tile0 + q.tiles - 1 - unit % q.tiles; // later tokens see more: they begin first
     const int m_all = q.n_tok * p.r, m0 = tile * 2 * TM, mrows = min(2 * TM, m_all - m0);
     const bool wide = mrows > TM;
     constexpr int WK = 8, WV = WK + 4 * K_GROUPS<CODES>, WI = WV + 4; // first warps of K's, V's and the issuing role

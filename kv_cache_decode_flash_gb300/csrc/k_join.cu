@@ -24,7 +24,7 @@ template <int D> __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(con
     }
     const BlockSeq q = p.seq[lo];
     const int unit = q.whole + cut - q.cut0, parts = q.splits;
-    const int g = unit / q.tiles, m0 = (q.tiles - 1 - unit % q.tiles) * p.tile_m;
+    const int g = unit / q.tiles, m0 = (q.tile0 + q.tiles - 1 - unit % q.tiles) * p.tile_m;
     const int m = (int)blockIdx.x % chunks * JOIN_ROWS + (threadIdx.x >> 5);
     if (m >= min(p.tile_m, q.n_tok * p.r - m0)) return;
     const int64_t row0 = (int64_t)q.part_row0 + (int64_t)(cut - q.cut0) * parts * p.part_rows + m;

@@ -168,6 +168,38 @@ def test_tree_ragged_batch(kind, act):
         tw.close()
 
 
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("kind,D", [("q8", 64), ("f16", 128), ("q8q4", 128)])
+@pytest.mark.parametrize("n_q", [[52], [76], [77], [103, 5], [20, 52, 154, 77, 1]])
+def test_tree_last_tile_of_few_rows(kind, D, act, n_q):
+    """Blocks whose query rows (5 a token) end shortly behind a tile, at its half and behind that."""
+    H, Hk = 10, 2
+    lens = [max(n_q) + 37 * (i + 1) + 900 * (i % 2) for i in range(len(n_q))]
+    tw = _force(_cache(kind, H, Hk, D, lens))
+    try:
+        rng = np.random.default_rng(13)
+        q = _queries(rng, sum(n_q), H, D, act)
+        par = np.concatenate([_parents(rng, t) for t in n_q])
+        ids = list(range(len(n_q)))
+        _compare(tw, ids, n_q, q, 0.11, par, _run(tw, ids, n_q, q, 0.11, par), act)
+    finally:
+        tw.close()
+
+
+def test_tree_more_last_tiles_than_a_launch_has_room_for():
+    """40 sequences of two tiles a KV head each, then 25 of one in the same call."""
+    H, Hk, D = 10, 2, 64
+    tw = _force(_cache("q8", H, Hk, D, [60 + 5 * i for i in range(40)]))
+    try:
+        rng = np.random.default_rng(14)
+        ids, n_q = list(range(40)) + list(range(25)), [52] * 40 + [3] * 25
+        q = _queries(rng, sum(n_q), H, D, "bf16")
+        par = np.concatenate([_parents(rng, t) for t in n_q])
+        _compare(tw, ids, n_q, q, 0.11, par, _run(tw, ids, n_q, q, 0.11, par), "bf16")
+    finally:
+        tw.close()
+
+
 @pytest.mark.parametrize("act", ["f32", "bf16"])
 @pytest.mark.parametrize("kind,lens", [("q8", [90, 1500, 64, 2200, 333]), ("f16", [1, 700, 40, 1300, 2])])
 def test_tree_order_of_the_sequences_changes_no_bit(kind, lens, act):
