@@ -40,7 +40,9 @@ static int ensure_block_space(Ctx *c, cudaStream_t st) {
 // a sequence's `join` (one sequence).  tree: the launch's sequences may change
 // places, and four waves of items are enough (32 sequences of 1024 to 8000 rows,
 // 16 tokens each: 276 us with up to nine, 262 so; f16 190 and 177).  weighted: a
-// step of a unit that fills half a tile at most costs 5/8 of another's.
+// step of a unit that fills half a tile at most costs 5/8 of another's, and an
+// item six of them beside its own (4 to 16 tokens of 32 f16 sequences of 1024 to
+// 8000 rows: 167 us with four, 147 so).
 //  One sequence: its units are alike, so the schedule is whole waves; those of
 // the last one or two are cut into the parts that shorten it most.
 //  Several: all rows are cut into parts of at most one length, the one for
@@ -49,9 +51,9 @@ static int ensure_block_space(Ctx *c, cudaStream_t st) {
 static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t least, int64_t part_cap, int64_t join = 1,
                         bool tree = false, bool weighted = false) {
     const int64_t fixed = 4;
-    auto eighths = [&](const BlockSeq &s) {
-        return weighted && (int64_t)s.n_tok * p.r - (int64_t)s.tile0 * p.tile_m <= p.tile_m / 2 ? 5 : 8;
-    };
+    auto half = [&](const BlockSeq &s) { return (int64_t)s.n_tok * p.r - (int64_t)s.tile0 * p.tile_m <= p.tile_m / 2; };
+    const bool alike = !weighted || std::all_of(p.seq, p.seq + p.n_seq, half);
+    auto eighths = [&](const BlockSeq &s) { return !alike && half(s) ? 5 : 8; };
     auto parts = [&](const BlockSeq &s, int64_t len) {
         return (int32_t)std::max<int64_t>(1, ((int64_t)s.n_rows * eighths(s) / 8 + len - 1) / len);
     };
@@ -80,6 +82,7 @@ static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t leas
     } else {
         double best = 0;
         int64_t best_len = longest;
+        const int64_t own = weighted ? 6 : fixed;
         int64_t cuts = 1; // of few sequences every length counts
         for (int64_t len = longest;;) {
             int64_t items = 0, slots = 0, most = 0;
@@ -88,7 +91,7 @@ static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t leas
                 const BlockSeq &s = p.seq[i];
                 const int64_t k = parts(s, len), n = (int64_t)s.tiles * p.Hk * k;
                 if (!n) continue;
-                const int64_t cost = fixed + (((s.n_rows + k - 1) / k + step - 1) / step * eighths(s) + 7) / 8;
+                const int64_t cost = own + (((s.n_rows + k - 1) / k + step - 1) / step * eighths(s) + 7) / 8;
                 items += n;
                 if (k > 1) slots += n;
                 total += (double)n * (double)cost;
@@ -117,12 +120,11 @@ static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t leas
         const BlockSeq &s = p.seq[i];
         items += s.whole + ((int64_t)s.tiles * p.Hk - s.whole) * s.splits;
     }
-    // In up to two waves the longest items begin first, so that none of them
-    // begins late (6 tokens each, q8_0, 8 heads of 128, as given and sorted: 32
-    // sequences of 64 to 400 rows 21.0 and 18.1 us, 16 of 300 to 3000 rows 35.2
-    // and 33.1).  Over more waves the order as given is no worse (1 token each,
-    // 32 sequences of 1024 to 8000 rows: 99 us as given, 103 sorted).
-    if (tree && items <= 2 * want)
+    // The longest items begin first, so that none of them begins late (q8_0, 8 heads of 128, as given and sorted: 6 tokens of
+    // 32 sequences of 64 to 400 rows 21.0 and 18.1 us, of 16 of 300 to 3000 rows 35.2 and 33.1; 20 to 80 tokens of 32 of 1024
+    // to 8000 rows 375 and 340).  Not in more than two waves of items of alike steps, which the memory bounds: there the order
+    // as given is no worse (1 token of 32 sequences of 1024 to 8000 rows: 99 as given, 103 sorted; f16 111 and 120).
+    if (tree && (weighted || items <= 2 * want))
         std::stable_sort(p.seq, p.seq + p.n_seq, [&](const BlockSeq &a, const BlockSeq &b) {
             return (int64_t)a.n_rows * eighths(a) * b.splits > (int64_t)b.n_rows * eighths(b) * a.splits;
         });

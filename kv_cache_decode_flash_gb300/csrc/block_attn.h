@@ -18,7 +18,6 @@ struct BlockSeq {
     int32_t n_rows;     // cached rows
     int32_t tok0;       // its first token in q / out / lse / n_vis
     int32_t n_tok;      // its tokens
-    int32_t tile0;      // its first query tile (a tree's short last one may be an entry of its own)
     int32_t tiles;      // query tiles of a KV head
     int32_t item0;      // first work item of the launch that is this sequence's
     int32_t whole;      // leading units (KV head, query tile) that are one item each; the others are `splits` items
@@ -26,7 +25,10 @@ struct BlockSeq {
     int32_t split_rows; // rows of a part (the last one may have fewer)
     int32_t part_row0;  // first partial row of its items (splits > 1)
     int32_t cut0;       // cut units of the launch before its own
-    int32_t w_index;    // its accumulators (kvc_attn_weight)
+    union {
+        int32_t w_index; // kvc_attn_weight: its accumulators
+        int32_t tile0;   // the attentions: its first query tile (a tree's short last one may be an entry of its own)
+    };
 };
 
 struct BlockParams {

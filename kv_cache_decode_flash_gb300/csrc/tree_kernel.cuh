@@ -780,6 +780,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     }
 }
 
+static_assert(sizeof(BlockParams) + 4 * sizeof(CUtensorMap) <= 4096, "launch parameters stay within 4 KB");
 template <int D, int KT, int VT, bool LO> cudaError_t tree_go(const BlockParams &p, const TreeMaps &t, cudaStream_t st) {
     auto k = tree_kernel<D, KT, VT, LO>;
     constexpr int bytes = TreeShape<D, KT, VT, LO>::SMEM;
