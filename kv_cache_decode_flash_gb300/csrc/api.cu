@@ -145,6 +145,14 @@ static int ensure_copy_stream(Ctx *c) {
     return KVC_OK;
 }
 
+// The entries of q's pages from `from` on are in the device's table.
+static void entries_known(Seq &q, size_t from) {
+    if (q.dev_table.size() < q.pages.size()) q.dev_table.resize(q.pages.size(), -1);
+    for (size_t k = from; k < q.pages.size(); ++k)
+        if (q.dev_table[k] != Seq::IN_GRAPH) q.dev_table[k] = q.pages[k];
+    q.dev_pages = (int32_t)q.pages.size();
+}
+
 // Re-upload the page tables of `s` (synchronous path).
 static int upload_pages(Ctx *c, int s) {
     Seq &q = c->seqs[s];
@@ -152,9 +160,7 @@ static int upload_pages(Ctx *c, int s) {
         const int rc = upload(c, c->pt_dev + (int64_t)s * c->max_pages, q.pages.data(), (int64_t)q.pages.size() * 4);
         if (rc) return rc;
     }
-    q.dev_pages = (int32_t)q.pages.size();
-    if (q.dev_table.size() < q.pages.size()) q.dev_table.resize(q.pages.size());
-    std::copy(q.pages.begin(), q.pages.end(), q.dev_table.begin());
+    entries_known(q, 0);
     return KVC_OK;
 }
 
@@ -192,6 +198,48 @@ void release_tail_pages(Ctx *c, Seq &q) {
     }
     if (q.n == 0) q.off = 0;
     q.dev_pages = std::min<int32_t>(q.dev_pages, (int32_t)q.pages.size());
+    q.cap_pages = std::min<int32_t>(q.cap_pages, (int32_t)q.pages.size());
+}
+
+// Sends the table entries of pages that sequences ids[0 .. n) grew by (grow_pages), on st, as kernel arguments.  An entry
+// that the device is known to hold, of a page that left and came back, is not sent again.  On a capturing stream the
+// entries are only recorded: that capture's replays have all of theirs from it, whatever was replayed before, and calls
+// outside it send them again.
+int send_pages(Ctx *c, const int32_t *ids, int n, cudaStream_t st) {
+    bool any = false;
+    for (int i = 0; i < n; ++i) any = any || c->seqs[(size_t)ids[i]].dev_pages != (int32_t)c->seqs[(size_t)ids[i]].pages.size();
+    if (!any) return KVC_OK;
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long capture = 0;
+    cudaError_t e = cudaStreamGetCaptureInfo(st, &status, &capture);
+    const bool captured = status != cudaStreamCaptureStatusNone;
+    auto first = [&](const Seq &q) {
+        return (size_t)(captured && q.cap_id == capture ? std::max(q.dev_pages, q.cap_pages) : q.dev_pages);
+    };
+    if (e != cudaSuccess) return cuda_fail(c, e, "page table update");
+    std::vector<int32_t> idx, val;
+    for (int i = 0; i < n; ++i) {
+        Seq &q = c->seqs[(size_t)ids[i]];
+        if (q.dev_table.size() < q.pages.size()) q.dev_table.resize(q.pages.size(), -1);
+        for (size_t k = first(q); k < q.pages.size(); ++k) {
+            if (!captured && q.dev_table[k] == q.pages[k]) continue;
+            idx.push_back((int32_t)((int64_t)ids[i] * c->max_pages + (int64_t)k));
+            val.push_back(q.pages[k]);
+        }
+    }
+    if (!idx.empty()) e = launch_pt_update(c->pt_dev, (int)idx.size(), idx.data(), val.data(), st);
+    if (e != cudaSuccess) return cuda_fail(c, e, "page table update");
+    for (int i = 0; i < n; ++i) {
+        Seq &q = c->seqs[(size_t)ids[i]];
+        if (captured) {
+            std::fill(q.dev_table.begin() + (int64_t)first(q), q.dev_table.begin() + (int64_t)q.pages.size(), Seq::IN_GRAPH);
+            q.cap_id = capture;
+            q.cap_pages = (int32_t)q.pages.size();
+        } else {
+            entries_known(q, (size_t)q.dev_pages);
+        }
+    }
+    return KVC_OK;
 }
 
 // Pool copy arguments of this context (no payload).
@@ -735,18 +783,8 @@ static int device_append_dst(Ctx *c, int layer, int seq, bool creates, int n_tok
         size_t first_new;
         int rc = grow_pages(c, q, n_tok, &first_new);
         if (rc) return rc;
-        std::vector<int32_t> idx, val;
-        for (size_t i = (size_t)q.dev_pages; i < q.pages.size(); ++i) {
-            idx.push_back((int32_t)((int64_t)seq * c->max_pages + (int64_t)i));
-            val.push_back(q.pages[i]);
-        }
-        if (!idx.empty()) {
-            cudaError_t e = launch_pt_update(c->pt_dev, (int)idx.size(), idx.data(), val.data(), st);
-            if (e != cudaSuccess) return cuda_fail(c, e, "page table update");
-            q.dev_pages = (int32_t)q.pages.size();
-            if (q.dev_table.size() < q.pages.size()) q.dev_table.resize(q.pages.size());
-            std::copy(q.pages.begin(), q.pages.end(), q.dev_table.begin());
-        }
+        const int32_t id = seq;
+        if ((rc = send_pages(c, &id, 1, st))) return rc;
     }
     const int64_t lo = (int64_t)layer * c->pool_rows;
     d->lv.k.data = c->kdata + lo * c->krow;

@@ -26,7 +26,12 @@ struct Seq {
     bool linear = true;
     std::vector<int32_t> lfill;
     int32_t dev_pages = 0; // leading entries of `pages` known to match the device table
-    std::vector<int32_t> dev_table; // what the device table's row holds, as far as it was written (stale entries too)
+    // What the device table's row holds (stale entries too), -1 where that is not known.  IN_GRAPH: a captured call writes
+    // the entry, at replays that nobody here sees, so that it is never known and always sent again.
+    static constexpr int32_t IN_GRAPH = -2;
+    std::vector<int32_t> dev_table;
+    unsigned long long cap_id = 0; // the last capture that entries were sent in,
+    int32_t cap_pages = 0;         // and the leading entries of `pages` that its later calls need not send
     bool synced() const {
         for (int32_t f : lfill)
             if (f != n) return false;
@@ -190,6 +195,7 @@ inline int32_t pages_for(const Ctx *c, int32_t off, int64_t n) {
 // Shared by the translation units of the host side (api.cu).
 int cuda_fail(Ctx *c, cudaError_t e, const char *what);
 int grow_pages(Ctx *c, Seq &q, int64_t add, size_t *first_new);
+int send_pages(Ctx *c, const int32_t *ids, int n, cudaStream_t st);
 void release_tail_pages(Ctx *c, Seq &q);
 bool consecutive(const int32_t *p, int64_t n);
 

@@ -128,7 +128,8 @@ static int append_rope(Ctx *c, int layer, const RopeCall &call, RopeArgs &a, cud
     if (new_pages > (int64_t)c->free_pages.size()) return c->fail(KVC_ENOSPC, "no free pages");
     KVC_CU(c, cudaSetDevice(c->dev));
     // (host memory for all of it before the first change)
-    size_t entries = 0;
+    std::vector<int32_t> grown;
+    grown.reserve((size_t)n_seq);
     for (int i = 0; i < n_seq; ++i) {
         if (!creates[(size_t)i]) continue;
         Seq &q = c->seqs[(size_t)ids[i]];
@@ -136,30 +137,15 @@ static int append_rope(Ctx *c, int layer, const RopeCall &call, RopeArgs &a, cud
         make_room(q.pos, (size_t)q.n + (size_t)n_tok[i]);
         make_room(q.pages, pages);
         make_room(q.dev_table, pages);
-        entries += pages - (size_t)q.dev_pages;
+        grown.push_back(ids[i]);
     }
-    std::vector<int32_t> idx, val;
-    idx.reserve(entries);
-    val.reserve(entries);
     for (int i = 0; i < n_seq; ++i) {
         if (!creates[(size_t)i]) continue;
-        Seq &q = c->seqs[(size_t)ids[i]];
         size_t first_new;
-        int rc = grow_pages(c, q, n_tok[i], &first_new);
+        int rc = grow_pages(c, c->seqs[(size_t)ids[i]], n_tok[i], &first_new);
         if (rc) return rc; // (cannot happen: checked above)
-        if (q.dev_table.size() < q.pages.size()) q.dev_table.resize(q.pages.size(), -1);
-        for (size_t k = (size_t)q.dev_pages; k < q.pages.size(); ++k) {
-            if (q.dev_table[k] == q.pages[k]) continue; // a page that left and came back
-            q.dev_table[k] = q.pages[k];
-            idx.push_back((int32_t)((int64_t)ids[i] * c->max_pages + (int64_t)k));
-            val.push_back(q.pages[k]);
-        }
-        q.dev_pages = (int32_t)q.pages.size();
     }
-    if (!idx.empty()) {
-        cudaError_t e = launch_pt_update(c->pt_dev, (int)idx.size(), idx.data(), val.data(), st);
-        if (e != cudaSuccess) return cuda_fail(c, e, "page table update");
-    }
+    if (int rc = send_pages(c, grown.data(), (int)grown.size(), st)) return rc;
     // The launches: pieces of consecutive positions need no list, the others' positions travel with them.
     if (!c->has_turns) rope_turns(c->prm.rope_base, c->D, c->rope_turn);
     c->has_turns = true;
