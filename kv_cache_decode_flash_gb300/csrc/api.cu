@@ -204,7 +204,8 @@ void release_tail_pages(Ctx *c, Seq &q) {
 // Sends the table entries of pages that sequences ids[0 .. n) grew by (grow_pages), on st, as kernel arguments.  An entry
 // that the device is known to hold, of a page that left and came back, is not sent again.  On a capturing stream the
 // entries are only recorded: that capture's replays have all of theirs from it, whatever was replayed before, and calls
-// outside it send them again.
+// outside it send them again.  If they cannot be sent, the pages go back, and nothing relies on what the launches that did
+// run may have left.
 int send_pages(Ctx *c, const int32_t *ids, int n, cudaStream_t st) {
     bool any = false;
     for (int i = 0; i < n; ++i) any = any || c->seqs[(size_t)ids[i]].dev_pages != (int32_t)c->seqs[(size_t)ids[i]].pages.size();
@@ -216,30 +217,41 @@ int send_pages(Ctx *c, const int32_t *ids, int n, cudaStream_t st) {
     auto first = [&](const Seq &q) {
         return (size_t)(captured && q.cap_id == capture ? std::max(q.dev_pages, q.cap_pages) : q.dev_pages);
     };
-    if (e != cudaSuccess) return cuda_fail(c, e, "page table update");
+    bool memory = true;
     std::vector<int32_t> idx, val;
-    for (int i = 0; i < n; ++i) {
-        Seq &q = c->seqs[(size_t)ids[i]];
-        if (q.dev_table.size() < q.pages.size()) q.dev_table.resize(q.pages.size(), -1);
-        for (size_t k = first(q); k < q.pages.size(); ++k) {
-            if (!captured && q.dev_table[k] == q.pages[k]) continue;
-            idx.push_back((int32_t)((int64_t)ids[i] * c->max_pages + (int64_t)k));
-            val.push_back(q.pages[k]);
+    try {
+        for (int i = 0; i < n; ++i) {
+            Seq &q = c->seqs[(size_t)ids[i]];
+            if (q.dev_table.size() < q.pages.size()) q.dev_table.resize(q.pages.size(), -1);
+            for (size_t k = first(q); k < q.pages.size(); ++k) {
+                if (!captured && q.dev_table[k] == q.pages[k]) continue;
+                idx.push_back((int32_t)((int64_t)ids[i] * c->max_pages + (int64_t)k));
+                val.push_back(q.pages[k]);
+            }
         }
+    } catch (const std::bad_alloc &) {
+        memory = false;
     }
-    if (!idx.empty()) e = launch_pt_update(c->pt_dev, (int)idx.size(), idx.data(), val.data(), st);
-    if (e != cudaSuccess) return cuda_fail(c, e, "page table update");
+    if (memory && e == cudaSuccess && !idx.empty()) e = launch_pt_update(c->pt_dev, (int)idx.size(), idx.data(), val.data(), st);
+    const bool sent = memory && e == cudaSuccess;
     for (int i = 0; i < n; ++i) {
         Seq &q = c->seqs[(size_t)ids[i]];
-        if (captured) {
-            std::fill(q.dev_table.begin() + (int64_t)first(q), q.dev_table.begin() + (int64_t)q.pages.size(), Seq::IN_GRAPH);
-            q.cap_id = capture;
-            q.cap_pages = (int32_t)q.pages.size();
-        } else {
+        if (sent && !captured) {
             entries_known(q, (size_t)q.dev_pages);
+        } else {
+            const int32_t now = captured ? Seq::IN_GRAPH : -1;
+            for (size_t k = first(q); k < std::min(q.pages.size(), q.dev_table.size()); ++k)
+                if (q.dev_table[k] != Seq::IN_GRAPH) q.dev_table[k] = now;
+            if (sent) {
+                q.cap_id = capture;
+                q.cap_pages = (int32_t)q.pages.size();
+            } else {
+                release_tail_pages(c, q);
+            }
         }
     }
-    return KVC_OK;
+    if (!memory) return c->fail(KVC_ENOMEM, "no host memory");
+    return sent ? KVC_OK : cuda_fail(c, e, "page table update");
 }
 
 // Pool copy arguments of this context (no payload).

@@ -176,7 +176,9 @@ static int append_rope(Ctx *c, int layer, const RopeCall &call, RopeArgs &a, cud
         a.warps = (int)std::min<int64_t>(a.passes, std::max<int64_t>(4, (int64_t)c->sms * 48 / a.n_tok));
         cudaError_t e = launch_rope_append(c->D, call.act, a, st);
         a.n_pieces = a.n_tok = listed = 0;
-        return e == cudaSuccess ? KVC_OK : cuda_fail(c, e, "append kernel");
+        if (e == cudaSuccess) return KVC_OK;
+        for (int32_t id : grown) release_tail_pages(c, c->seqs[(size_t)id]);
+        return cuda_fail(c, e, "append kernel");
     };
     t0 = 0;
     for (int i = 0; i < n_seq; t0 += n_tok[i++]) {

@@ -1,5 +1,7 @@
-"""Entries of the device's page tables that captured and released appends write or leave: whatever of these came
+"""Entries of the device's page tables that captured, released and failed appends write or leave: whatever of these came
 before, a call's rows reach the pages that the sequence has, and no other sequence's."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -189,4 +191,30 @@ def test_a_capture_of_several_appends_sends_an_entry_once(two):
     same(a.rows(), b.rows())
     for c in (a, b):
         c.rope(0, c.draw(50, 20), PAGE + 24)
+    same(a.rows(), b.rows())
+
+
+@pytest.mark.parametrize("then", ["rope", "plain"])
+def test_an_append_whose_launch_failed_leaves_no_entry_behind(two, then):
+    """A capture that is no longer valid refuses the launches of an append; the next one must not rely on them."""
+    a, b = (c.start() for c in two)
+    torch, kvc = a.torch, a.kvc
+    x, y = a.draw(3, 5), b.draw(4, 7)
+    free = a.c.stats()["pages_free"]
+    cu = ctypes.CDLL("libcuda.so.1")
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    stream, graph = ctypes.c_void_p(st.cuda_stream), ctypes.c_void_p()
+    assert cu.cuStreamBeginCapture_v2(stream, 2) == 0  # relaxed: no other stream is concerned
+    assert cu.cuStreamSynchronize(stream) != 0         # not allowed there: the capture is void
+    with pytest.raises(kvc.KvcError) as e:
+        a.c.append_rope(0, [0], [5], list(range(PAGE, PAGE + 5)), None, x[:, H:H + Hk], x[:, H + Hk:], None, stream=st)
+    assert e.value.status == kvc.KVC_ECUDA
+    assert cu.cuStreamEndCapture(stream, ctypes.byref(graph)) != 0
+    assert a.c.n_tokens(0) == PAGE and a.c.stats()["pages_free"] == free
+    for c in (a, b):
+        if then == "rope":
+            c.rope(0, y, PAGE)
+        else:
+            c.plain(0, y, PAGE)()
     same(a.rows(), b.rows())
