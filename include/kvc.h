@@ -287,9 +287,9 @@ int kvc_attn_cross(kvc_ctx *c, int layer, int n_seq, const int32_t *seq_ids, con
  * q, out: device [T][n_head][head_dim], contiguous, 16-byte aligned; out may not
  * overlap q.  parent: device int32 [T], 4-byte aligned, or NULL.
  * Results are bitwise repeatable.  32-bit results keep 32-bit accuracy.  16-bit
- * ones come from K, V and weights of 11 significant bits or more (a weight below
+ * ones come from weights and V of 11 significant bits or more (a weight below
  * 2^-20 of a token's largest: an error of 2^-31 of that one at most) and fp32
- * sums.
+ * sums; K is taken as stored.
  * The call only enqueues work on `stream`.  It shares the work space of
  * kvc_attn_cross, with what is said there about first calls, order and captures.
  * Device-resident contexts only.  Errors: KVC_EINVAL (a sequence with fewer rows

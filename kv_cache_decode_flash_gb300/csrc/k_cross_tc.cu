@@ -53,9 +53,9 @@ template <bool CODES> constexpr int THREADS = (4 + K_GROUPS<CODES>) * GROUP;
 // codes into values need more), the softmax groups take them, so that a thread holds all or half of its row's 128 scores.  (No function of
 // theirs may stay a call: its registers would have to fit the smallest role's.)  Few are to spare: shared memory leaves
 // spilled ones next to no cache (V's codes by two groups as well, with 72 a thread at launch: 139 to 199 us).
-template <bool CODES, bool TREE> struct Regs {
+template <bool CODES> struct Regs {
     static constexpr int LAUNCH = CODES ? 80 : 96;
-    static constexpr int SOFT = CODES ? (TREE ? 144 : 136) : 184, K = CODES ? (TREE ? 48 : 56) : 40, V = CODES ? 72 : 40, MMA = 24;
+    static constexpr int SOFT = CODES ? 136 : 184, K = CODES ? 56 : 40, V = CODES ? 72 : 40, MMA = 24;
     static constexpr int HOLD = CODES ? 2 : 4; // blocks of 32 scores that a softmax thread keeps
     static_assert(2 * SOFT + K_GROUPS<CODES> * K + V + MMA <= THREADS<CODES> / GROUP * LAUNCH, "the roles' registers come from the launch's");
 };
@@ -71,15 +71,15 @@ constexpr float LIFT = 7.f; // log2 of P at the reference maximum: P <= 2^(GROW 
 
 enum Bar { KF0, KF1, KF2, KF3, KE0, KE1, KE2, KE3, VF0, VF1, VE0, VE1, SF0, SF1, PF0, PF1, OD0, OD1, XF0, XF1, XF2, XF3, DRAIN, N_BARS };
 
-// A step's K is one tile, or (TWO) two, its values' first and second parts, which take the K tiles' places in turn.
-template <int D, bool TWO> struct Lay {
+// A step's K is one tile, or with codes two, its values' first and second parts, which take the K tiles' places in turn.
+template <int D, bool CODES> struct Lay {
     static constexpr int REG = TN * 128;          // a region: 128 rows of 64 fp16, 128-byte swizzled
     static constexpr int TILE = D / 64 * REG;     // bytes of a 128-row tile of fp16
-    static constexpr int PARTS = TWO ? 2 : 1;
-    static constexpr int K_TILES = TWO && D == 64 ? 4 : 2; // (D 128 has room for no more)
+    static constexpr int PARTS = CODES ? 2 : 1;
+    static constexpr int K_TILES = CODES && D == 64 ? 4 : 2; // (D 128 has room for no more)
     static constexpr int Q = 0, K = 2 * TILE, V = K + K_TILES * TILE, AUX = V + 2 * TILE;
     // a query tile of one half leaves the other half's place free: one more for K
-    static constexpr int MORE = TWO && D == 128 ? 1 : 0;
+    static constexpr int MORE = CODES && D == 128 ? 1 : 0;
     __device__ static __forceinline__ int k_tiles(bool wide) { return K_TILES + (wide ? 0 : MORE); }
     __device__ static __forceinline__ int k(bool wide) { return K - (wide ? 0 : MORE) * TILE; }
 };
@@ -115,22 +115,22 @@ __device__ __forceinline__ bool any_bad(const uint32_t (&rows)[TN / 32]) {
 
 template <int D, bool CODES, bool TREE> constexpr int smem_bytes() {
     // TMEM is allocated whole: one CTA per SM, whatever D
-    const int need = Lay<D, CODES && !TREE>::AUX + (int)sizeof(Aux) + 2 * TM * (D / 16) * 4 + 1024 + (TREE ? (int)sizeof(TreeMasks<TREE>) : 0);
+    const int need = Lay<D, CODES>::AUX + (int)sizeof(Aux) + 2 * TM * (D / 16) * 4 + 1024 + (TREE ? (int)sizeof(TreeMasks<TREE>) : 0);
     return need > 120 * 1024 ? need : 120 * 1024;
 }
 
 // ------------------------------------------------------------- loading ----
 // A loading group's work: tensor T's rows of every step (IS_V: V, else K) into its n_tiles stages (two, but for K's codes).
-template <int D, int T, bool IS_V, bool TWO>
+template <int D, int T, bool IS_V>
 __device__ __forceinline__ void load_rows(const BlockParams &p, const BlockSeq &q, int g, uint8_t *tiles, int n_tiles, Aux &x, int r0,
                                           int r_end, int t) {
-    // TWO: a step is two tiles
+    constexpr bool TWO = !IS_V && T != KVC_F16; // a step is two tiles
     constexpr int TILE = Lay<D, TWO>::TILE;
     const uint8_t *data = IS_V ? p.vdata : p.kdata;
     uint64_t *full = &x.bar[IS_V ? VF0 : KF0], *empty = &x.bar[IS_V ? VE0 : KE0];
     int32_t(*row)[TN] = x.row[IS_V];
     int steps = 1 << 24, vis_min = 0, r1 = 0; // known with the query rows; r1: the end of the rows that some token sees
-    constexpr int SYNC = IS_V ? 4 : 3, NT = IS_V ? GROUP : K_GROUPS<T != KVC_F16> * GROUP; // threads
+    constexpr int SYNC = IS_V ? 4 : 3, NT = IS_V ? GROUP : K_GROUPS<TWO> * GROUP; // threads
     const bool has_row = NT == TN || t < TN;   // whose place and scales it sees to
     Lookup next; // of the step whose rows the group gets next
     auto look_up = [&](int s) { next.ask(p, q, r0 + s * TN + t, has_row && s < steps); };
@@ -399,15 +399,14 @@ __device__ __forceinline__ float row_exp(uint32_t S, const Seen &n, uint32_t (&r
 }
 
 // TREE: the block's tokens are the sequence's last rows, and each sees the rows before them, its ancestors' and its own
-// (kvc_attn_tree); else a token sees its n_vis leading rows.  A tree's results have 16 bits and no log-sum-exp comes with
-// them, so that K's codes times their scale are one fp16 value there, like V's (a third of the products and of the
-// conversion less).
+// (kvc_attn_tree); else a token sees its n_vis leading rows.  K's codes have two parts there too, although no log-sum-exp
+// comes with a tree: with one of 11 bits (26 tokens over 16384 rows 36 us, 40 with both; 64 over 32768 95 and 101) scores of
+// 300 were off by 0.07 and results by as much, ten roundings of bf16.
 template <int D, int KT, int VT, bool TREE>
 __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(const __grid_constant__ BlockParams p) {
     constexpr bool CODES = KT != KVC_F16;
-    constexpr bool TWO = CODES && !TREE; // K in two parts (a tree has no log-sum-exp that would show the second)
-    using L = Lay<D, TWO>;
-    using R = Regs<CODES, TREE>;
+    using L = Lay<D, CODES>;
+    using R = Regs<CODES>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u); // swizzled tiles need 1024-byte alignment
     Aux &x = *reinterpret_cast<Aux *>(smem + L::AUX);
@@ -445,11 +444,11 @@ __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(con
     const int r0 = part * q.split_rows, r_end = parts == 1 ? q.n_rows : min(r0 + q.split_rows, q.n_rows);
     if (warp >= WK && warp < WV) {
         regs_dec<R::K>();
-        load_rows<D, KT, false, TWO>(p, q, g, smem + L::k(wide), L::k_tiles(wide), x, r0, r_end, tid - WK * 32);
+        load_rows<D, KT, false>(p, q, g, smem + L::k(wide), L::k_tiles(wide), x, r0, r_end, tid - WK * 32);
         return;
     } else if (warp >= WV && warp < WI) {
         regs_dec<R::V>();
-        load_rows<D, VT, true, false>(p, q, g, smem + L::V, 2, x, r0, r_end, tid - WV * 32);
+        load_rows<D, VT, true>(p, q, g, smem + L::V, 2, x, r0, r_end, tid - WV * 32);
         return;
     }
     // The other warps see to the query rows: a warp each, QR of its rows under way together, normalised by a power of two
@@ -816,7 +815,7 @@ template <bool TREE, int D, int KT, int VT> cudaError_t go(const BlockParams &p,
     constexpr int bytes = smem_bytes<D, CODES, TREE>();
     static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
     static SharedMemory set;
-    cudaError_t e = set.allow((const void *)k, bytes, Regs<CODES, TREE>::LAUNCH);
+    cudaError_t e = set.allow((const void *)k, bytes, Regs<CODES>::LAUNCH);
     if (e != cudaSuccess) return e;
     if (TREE) {
         e = launch_behind(k, (unsigned)p.n_items, THREADS<CODES>, bytes, st, p);

@@ -1,0 +1,89 @@
+"""Tree attention (kvc_attn_tree) on values where bits or rows are easily lost: keys that are no 11-bit numbers under a
+softmax of large scores.  On each of the two kernels."""
+import numpy as np
+import pytest
+
+import oracle
+from block_ref import values
+from draft_ref import attend, attend_bound, tree_sees
+from twin import Twin
+
+pytestmark = pytest.mark.gpu
+
+Q8, F16, Q4 = oracle.Q8_0, oracle.F16, oracle.Q4_0
+KINDS = {"q8": (Q8, Q8), "f16": (F16, F16), "q8q4": (Q8, Q4)}
+MMA, TCGEN05 = 1, 2
+
+
+def _types():
+    import torch
+
+    return {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def _twin(kind, H, Hk, D, n, k, v, kernel, page=64, ref=True):
+    tk, tv = KINDS[kind]
+    tw = Twin(1, H, Hk, D, n + 64, type_=tk, type_v=tv, page_rows=page)
+    tw.kvc.kvc_debug_block_kernel(tw.gpu.ctx, kernel)
+    import torch
+
+    if ref:
+        tw.append(0, 0, 0, k, v)
+    else:
+        tw.gpu.append(0, 0, 0, torch.from_numpy(k).to(tw.dev), torch.from_numpy(v).to(tw.dev))
+    return tw
+
+
+def _run(tw, T, q, scale, parent):
+    import torch
+
+    out = torch.full_like(q, float("nan"))
+    tw.gpu.attn_tree(0, [0], [T], q, out, scale, parent=torch.from_numpy(parent).to(q.device))
+    torch.cuda.synchronize()
+    assert tw.kvc.kvc_check_device_error(tw.gpu.ctx) == 0
+    return out
+
+
+def _level_rows(rng, n, Hk, D, spread):
+    """Rows whose keys are alike but for the first of every 32, which gives the block its scale and which the queries leave out:
+    a code of 90 to 126, another one in every row, times a scale of 11 bits, 1 to 1 + spread together.  Rounding a row's keys to
+    11 bits then goes the same way in every product of its score; V's sign is that of this rounding."""
+    a, c = 1 + spread * rng.random((n, Hk, 1)), rng.integers(90, 127, (n, Hk, 1))
+    k = np.broadcast_to(a, (n, Hk, D)).astype(np.float32)
+    k[..., ::32] = (127 * a / c).astype(np.float32)
+    held = np.float16(a / c).astype(np.float64) * c
+    sign = np.where(np.float16(held).astype(np.float64) > held, 1.0, -1.0)
+    v = sign * (1 + 0.1 * rng.random((n, Hk, D)))
+    return k, v.astype(np.float32)
+
+
+# The bound is attend_bound's with operands of 20 bits or more: both kernels take the codes of K exactly (mma.sync) or as two
+# fp16 parts (tcgen05: 18 bits, all that a code times its scale has).  One part of 11 bits is off by up to 2^-12 of a score of
+# 100, 0.02, where the bound has 100 (2^-20 + 132 x 2^-24) = 0.0009, and the results move by as much with V as it is here.
+@pytest.mark.parametrize("kernel", [MMA, TCGEN05], ids=["mma", "tcgen05"])
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("kind,D", [("q8", 64), ("q8", 128), ("q8q4", 128)])
+@pytest.mark.parametrize("T,n", [(9, 300), (30, 1500), (70, 900)])
+@pytest.mark.parametrize("score,spread", [(30, 0.05), (100, 0.02), (300, 0.01)])
+def test_keys_keep_their_bits_under_large_scores(kind, D, act, T, n, score, spread, kernel):
+    H, Hk = 10, 2
+    rng = np.random.default_rng(31)
+    k, v = _level_rows(rng, n, Hk, D, spread)
+    tw = _twin(kind, H, Hk, D, n, k, v, kernel)
+    try:
+        import torch
+
+        one = np.ones((T, H, D))
+        one[..., ::32] = 0
+        q = torch.from_numpy(one).to("cuda:0", _types()[act])
+        par = np.array([-1 if t == 0 else rng.integers(max(-1, t - 6), t) for t in range(T)], np.int32)
+        scale = float(np.float32(score / D))
+        got = _run(tw, T, q, scale, par).double().cpu().numpy()
+        s = tw.ref.seqs[0]
+        K, V = values(s.K[0]), values(s.V[0])
+        want, mag, size = attend(one, K, V, scale, tree_sees(par, n, T))
+        bound = attend_bound(mag, size, n, D, act, exact=True)
+        ratio = np.abs(got - want) / bound
+        assert ratio.max() <= 1, "%.2f of its bound" % ratio.max()
+    finally:
+        tw.close()
