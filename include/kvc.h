@@ -247,7 +247,8 @@ typedef enum kvc_act { KVC_ACT_F32 = 0, KVC_ACT_F16 = 1, KVC_ACT_BF16 = 2 } kvc_
  * share a power of two among neighbouring rows that some token of the block
  * sees: values 2^14 times those that a token sees may cost it accuracy.)  A V
  * value that is not finite reaches every token that sees its row, whatever the
- * others see (infinite, or NaN where 16 bits leave the row no weight).
+ * others see (infinite, or NaN where 32 bits, with 16-bit queries 16, leave the
+ * row no weight).
  * seq_ids, n_q: HOST int32[n_seq]; an id may come more than once (decoders
  * that share an encoder's rows).  act: type of q and out (kvc_act).
  * q, out: device [T][n_head][head_dim], contiguous; out may not overlap q.

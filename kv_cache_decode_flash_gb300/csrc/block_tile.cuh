@@ -274,7 +274,7 @@ __device__ float stored_value(const uint8_t *data, const uint16_t *scales, int32
     }
 }
 
-// The values of row R that are not finite, marked in the two-bit words of a query row that gives it weight.
+// The values of row R that are not finite, marked in the two-bit words of a query row that sees it.
 template <int D, int T>
 __device__ __forceinline__ void mark_poison(uint32_t *words, const uint8_t *data, const uint16_t *scales, int32_t R) {
     for (int d = 0; d < D; ++d) {

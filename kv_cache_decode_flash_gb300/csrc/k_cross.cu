@@ -22,7 +22,7 @@
 // Rows behind the sequence's last and rows that a token does not see take no
 // part, whatever they hold: scores are selected, not added to, and a
 // non-finite V value is kept out of the products (0 x inf is NaN) and put into
-// the result only of rows that give it weight.
+// the result only of rows that see it.
 // Few query tiles: the cached rows are split over items, and a second kernel
 // joins their partial sums in order, so a result does not depend on the order in
 // which items finish.
@@ -79,10 +79,13 @@ template <int RB> __device__ __forceinline__ void copy_rows(uint8_t *dst, const 
     }
 }
 
-// (out of line: the place that calls it is unrolled)
+// Of a step's rows j < n that a query row sees, those that the quad's lane qc looks after and whose values were left out.
+// (Out of line: in place it costs the step's registers, 10 % of 32-bit queries over f16 rows.)
 template <int D, int T>
-__device__ __noinline__ void mark_row(uint32_t *words, const uint8_t *data, const uint16_t *scales, int32_t R) {
-    mark_poison<D, T>(words, data, scales, R);
+__device__ __noinline__ void mark_rows(uint32_t *words, const uint8_t *data, const uint16_t *scales, const int32_t *row,
+                                       const uint8_t *badrow, int qc, int n) {
+    for (int j = qc; j < n; j += 4)
+        if (badrow[j] && row[j] >= 0) mark_poison<D, T>(words, data, scales, row[j]);
 }
 
 // WM: warps along the query rows (16 each); the 4 / WM warps of a row block
@@ -260,15 +263,10 @@ __global__ void __launch_bounds__(THREADS, 2) cross_kernel(const __grid_constant
             sum[h] = sum[h] * al[h] + add;
             al[h] *= grow;
         }
-        if (s.bad[cur]) { // a V value of this step is not finite: it goes to the rows that give it weight
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int jt = wn * NC + n * 8 + qc * 2 + (k & 1);
-                    if (badrow[jt] && sc[n][k] > 0.f)
-                        mark_row<D, VT>(s.poison[mrow + 8 * (k >> 1)], p.vdata, p.vs, row[jt]);
-                }
+        if (s.bad[cur]) { // a V value of this step is not finite: it goes to the rows that see it, of whatever weight
+            for (int h = 0; h < 2; ++h)
+                mark_rows<D, VT>(s.poison[mrow + 8 * h], p.vdata, p.vs, row + wn * NC, badrow + wn * NC, qc,
+                                 min(s.vis[mrow + 8 * h] - base - wn * NC, NC));
             s.any_bad = 1;
         }
         // P V, a 32-value block of V at a time.  The tensor cores truncate their sums, so a chain of products is no

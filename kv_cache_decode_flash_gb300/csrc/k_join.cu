@@ -54,9 +54,8 @@ template <int D> __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(con
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const float f = ex2(c[i].x - M);
-            // nothing seen there, or nothing left of it (its sums may be anything)
-            const bool skip = i0 + i >= parts || c[i].y == 0.f || (f == 0.f && c[i].y == c[i].y);
-            if (skip) continue;
+            // nothing seen there; where nothing is left of what was seen, values that are not finite come through (0 x inf)
+            if (i0 + i >= parts || c[i].y == 0.f) continue;
             L = fmaf(c[i].y, f, L);
 #pragma unroll
             for (int e = 0; e < V; ++e) o[e] = fmaf(v[i][e], f, o[e]);

@@ -1,5 +1,5 @@
 """Tree attention (kvc_attn_tree) on values where bits or rows are easily lost: keys that are no 11-bit numbers under a
-softmax of large scores.  On each of the two kernels."""
+softmax of large scores, and V values that are not finite in rows of next to no weight.  On each of the two kernels."""
 import numpy as np
 import pytest
 
@@ -85,5 +85,47 @@ def test_keys_keep_their_bits_under_large_scores(kind, D, act, T, n, score, spre
         bound = attend_bound(mag, size, n, D, act, exact=True)
         ratio = np.abs(got - want) / bound
         assert ratio.max() <= 1, "%.2f of its bound" % ratio.max()
+    finally:
+        tw.close()
+
+
+@pytest.mark.parametrize("kernel", [MMA, TCGEN05], ids=["mma", "tcgen05"])
+@pytest.mark.parametrize("act", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("kind,D", [("q8", 64), ("f16", 64), ("q8", 128), ("f16", 128), ("q8q4", 128)])
+@pytest.mark.parametrize("T", [3, 30, 70])
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("n,low", [(700, 0), (6000, 3000)])
+def test_values_that_are_not_finite_in_rows_of_no_weight(kind, D, act, T, n, low, bad, kernel):
+    """A seen row whose score lies 600 below the others': its weight is 0 in 32 bits, and what its V holds reaches the tokens
+    that see it all the same (as an infinity or as 0 x inf).  One row far before the block (alone, or among 3000 like it, whole
+    parts of the rows that are nothing beside the others), one just before it and one of the block that some of its tokens do
+    not see; a q8_0 or q4_0 value spoils its block of 32."""
+    if act == "f32" and kernel == TCGEN05:
+        pytest.skip("32-bit queries have one kernel")
+    if kind != "f16" and np.isnan(bad):
+        pytest.skip("codes hold no NaN: a block's scale is formed without it")
+    H, Hk = 4, 2
+    rng = np.random.default_rng(37)
+    k = rng.standard_normal((n, Hk, D)).astype(np.float32) * 0.1
+    v = rng.standard_normal((n, Hk, D)).astype(np.float32)
+    k[:low] = -40
+    spoilt = {100: (0, 3), n - T - 2: (1, 35), n - T + 1: (0, 40)}  # row: (KV head, dim)
+    for row, (g, d) in spoilt.items():
+        k[row] = -40
+        v[row, g, d] = bad
+    tw = _twin(kind, H, Hk, D, n, k, v, kernel, ref=False)
+    try:
+        import torch
+
+        q = (15 + torch.rand(T, H, D, generator=torch.Generator().manual_seed(5))).to("cuda:0", _types()[act])
+        par = np.array([-1, 0] + [0 if t % 3 else 1 for t in range(2, T)], np.int32)[:T]
+        o = _run(tw, T, q, 1.0 / D, par).float().cpu().numpy()
+        sees = tree_sees(par, n, T)
+        spoil = np.zeros((T, H, D), bool)
+        for row, (g, d) in spoilt.items():
+            dims = slice(d, d + 1) if kind == "f16" else slice(d // 32 * 32, d // 32 * 32 + 32)
+            spoil[sees[:, row], g * 2:g * 2 + 2, dims] = True
+        assert sees[:, n - T + 1].any() and not sees[:, n - T + 1].all()
+        assert np.array_equal(~np.isfinite(o), spoil)
     finally:
         tw.close()
