@@ -531,6 +531,11 @@ int kvc_debug_block_plan(int n_head, int n_head_kv, int head_dim, int act, int s
                          const int32_t *n_q, int32_t *tile_m, int32_t *whole, int32_t *splits, int32_t *split_rows,
                          int64_t *items, int64_t *part_rows, int64_t *part_cap);
 
+/* Test hook: the rows at the end of a sequence's layer that the next decode
+ * attention takes for rows still being written, and so requests only behind its
+ * wait for the kernels before it.  Errors: KVC_EINVAL. */
+int kvc_debug_recent_rows(kvc_ctx *c, int layer, int seq, int32_t *rows);
+
 /* Test hook, no context and no GPU needed: the same of a tree attention launch
  * over n_seq (1 .. 64) sequences of rows[i] rows, the last n_q[i] of them the
  * tree's, off[i] cells behind the start of the first page.  Errors: KVC_EINVAL. */

@@ -819,7 +819,7 @@ static void append_commit(Ctx *c, int layer, int seq, int pos0, int n_tok, bool 
         q.n += n_tok;
     }
     q.lfill[layer] += n_tok;
-    c->recent[(size_t)seq][(size_t)layer] += n_tok;
+    c->appended(seq, layer, n_tok);
 }
 
 static int append_impl(Ctx *c, int layer, int seq, int pos0, int n_tok, const float *k, const float *v,

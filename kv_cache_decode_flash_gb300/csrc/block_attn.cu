@@ -415,6 +415,9 @@ extern "C" int kvc_attn_tree(kvc_ctx *cc, int layer, int n_seq, const int32_t *s
         if (e != cudaSuccess) return cuda_fail(c, e, "tree attention kernel");
         p.n_seq = 0;
     }
+    // Kernels after these start only once they have waited for all before them (captured ones wait at their replays).
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusActive;
+    if (cudaStreamIsCapturing(st, &status) == cudaSuccess && status == cudaStreamCaptureStatusNone) c->clear_recent();
     return KVC_OK;
 }
 
@@ -511,6 +514,14 @@ extern "C" int kvc_debug_block_plan(int n_head, int n_head_kv, int head_dim, int
         const int64_t cut = (int64_t)s.tiles * p.Hk - s.whole;
         *part_rows = std::max<int64_t>(*part_rows, s.part_row0 + cut * s.splits * p.part_rows);
     }
+    return KVC_OK;
+}
+
+extern "C" int kvc_debug_recent_rows(kvc_ctx *cc, int layer, int seq, int32_t *rows) {
+    if (!cc || !rows) return KVC_EINVAL;
+    Ctx *c = reinterpret_cast<Ctx *>(cc);
+    if (layer < 0 || layer >= c->L || seq < 0 || seq >= (int)c->recent.size()) return c->fail(KVC_EINVAL, "ids out of range");
+    *rows = c->recent[(size_t)seq][(size_t)layer];
     return KVC_OK;
 }
 

@@ -115,9 +115,14 @@ struct Ctx {
     int32_t max_pages = 0;
     std::vector<Seq> seqs;
     // rows appended per (sequence, layer) since the last fence (an attention
-    // launch or a synchronous operation); an attention launched with a
-    // programmatic dependency may read every other row before it waits
+    // launch or a synchronous operation), at most those that the layer holds; an
+    // attention launched with a programmatic dependency may read every other row
+    // before it waits
     std::vector<std::vector<int32_t>> recent;
+    void appended(int seq, int layer, int32_t n) { // (lfill has them already)
+        int32_t &r = recent[(size_t)seq][(size_t)layer];
+        r = (int32_t)std::min<int64_t>((int64_t)r + n, seqs[(size_t)seq].lfill[(size_t)layer]);
+    }
     void clear_recent() {
         for (auto &v : recent) std::fill(v.begin(), v.end(), 0);
     }

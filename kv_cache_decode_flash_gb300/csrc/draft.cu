@@ -215,7 +215,7 @@ static int append_rope(Ctx *c, int layer, const RopeCall &call, RopeArgs &a, cud
             q.n += n_tok[i];
         }
         q.lfill[(size_t)layer] += n_tok[i];
-        c->recent[(size_t)ids[i]][(size_t)layer] += n_tok[i];
+        c->appended(ids[i], layer, n_tok[i]);
     }
     return KVC_OK;
 }
@@ -291,8 +291,8 @@ static int seq_keep(Ctx *c, int n_seq, const int32_t *ids, const int32_t *n_last
         else if (n_keep[i]) q.linear = consecutive(q.pos.data() + base, n_keep[i]) && (base == 0 || q.pos[base] == (int64_t)q.pos[base - 1] + 1);
         release_tail_pages(c, q);
         for (auto &f : q.lfill) f = q.n;
-        // rows that moved were written by a kernel that the next one may overlap
-        for (auto &r : c->recent[(size_t)ids[i]]) r = std::max(r, n_keep[i]);
+        // rows that moved were written by a kernel that the next one may overlap; those that left need no wait
+        for (auto &r : c->recent[(size_t)ids[i]]) r = std::max(r - (n_last[i] - n_keep[i]), n_keep[i]);
     }
     return KVC_OK;
 }

@@ -109,6 +109,7 @@ def load():
         "kvc_debug_block_plan": (i32, [i32] * 6 + [p] * 9),
         "kvc_debug_tree_plan": (i32, [i32] * 4 + [p] * 10),
         "kvc_debug_rope_turns": (i32, [C.c_float, i32, p]),
+        "kvc_debug_recent_rows": (i32, [p, i32, i32, p]),
         "kvc_debug_select_rows": (i32, [p, i32, i32, i32, i32, p, C.POINTER(C.c_int64), C.POINTER(C.c_int64),
                                         C.POINTER(C.c_int32)]),
         "kvc_set_timeout_ms": (i32, [p, i32]),
@@ -558,6 +559,13 @@ def kvc_debug_tree_plan(n_head, n_head_kv, sms, rows, off, n_q):
         raise KvcError(st, "bad tree-plan arguments")
     return {"tile_m": tm.value, "whole": list(wh), "splits": list(sp), "split_rows": list(sr),
             **{k: b.value for k, b in zip(("items", "part_rows", "part_cap"), big)}}
+
+
+def kvc_debug_recent_rows(ctx, layer, seq) -> int:
+    """The last rows of a sequence's layer that the next decode attention takes for rows still being written."""
+    n = C.c_int32()
+    _check(ctx, load().kvc_debug_recent_rows(ctx, layer, seq, C.byref(n)))
+    return n.value
 
 
 def kvc_debug_rope_turns(rope_base, head_dim):
