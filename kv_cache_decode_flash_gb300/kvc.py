@@ -289,6 +289,17 @@ def kvc_attn_weight(ctx, layer, seq_ids, n_q, act, q, lse, w, w_stride, kq_scale
                                        float(kq_scale), _addr(w), int(w_stride), _stream(stream, device)))
 
 
+def _whole(x):
+    """The int that a number of another type is."""
+    try:
+        v = int(x)
+    except (OverflowError, ValueError):  # an infinity, NaN
+        v = None
+    if v is None or v != x or not -2**31 <= v < 2**31:
+        raise KvcError(KVC_ERANGE, "values must be whole numbers of 32 bits")
+    return v
+
+
 def _host_ints(x):
     """Host int32 values as (address, count, what is to be kept until the call)."""
     t = type(x)
@@ -296,9 +307,9 @@ def _host_ints(x):
         try:
             a = array("i", x)
         except OverflowError:
-            raise KvcError(KVC_ERANGE, "values must fit 32 bits") from None
+            raise KvcError(KVC_ERANGE, "values must be whole numbers of 32 bits") from None
         except TypeError:
-            a = array("i", [int(v) for v in x])
+            a = array("i", map(_whole, x))
         return a.buffer_info()[0], len(a), a
     view = getattr(x, "__array_interface__", None)
     if view is None:
@@ -308,7 +319,7 @@ def _host_ints(x):
 
         a = np.ascontiguousarray(x, np.int32)
         if not np.array_equal(a, x):
-            raise KvcError(KVC_ERANGE, "values must fit 32 bits")
+            raise KvcError(KVC_ERANGE, "values must be whole numbers of 32 bits")
         return a.__array_interface__["data"][0], a.size, a
     return view["data"][0], x.size, x
 
