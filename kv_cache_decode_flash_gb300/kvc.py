@@ -160,17 +160,20 @@ def _addr(x):
     raise TypeError("expected a tensor or an address")
 
 
-_raw_stream = None  # torch's current stream of a device as an address, without an object around it
+_raw_stream = None  # torch's current stream of a device number as an address, without an object around it
 
 
-def _stream(stream, device: int):
+def _stream(stream, device):
+    """The stream given, or torch's current one of a device (a number, or what else torch takes for one: None, torch.device)."""
     global _raw_stream
     if stream is None:
-        if _raw_stream is None:
+        if _raw_stream is None or type(device) is not int:
             import torch
 
             _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
                 lambda d: torch.cuda.current_stream(d).cuda_stream)
+            if type(device) is not int:
+                return torch.cuda.current_stream(device).cuda_stream
         return _raw_stream(device)
     if isinstance(stream, int):
         return stream
