@@ -536,12 +536,25 @@ int kvc_debug_block_plan(int n_head, int n_head_kv, int head_dim, int act, int s
  * wait for the kernels before it.  Errors: KVC_EINVAL. */
 int kvc_debug_recent_rows(kvc_ctx *c, int layer, int seq, int32_t *rows);
 
-/* Test hook, no context and no GPU needed: the same of a tree attention launch
- * over n_seq (1 .. 64) sequences of rows[i] rows, the last n_q[i] of them the
+/* Test hook, no context and no GPU needed: the same of a tree attention launch of
+ * the mma.sync kernel over n_seq (1 .. 64) sequences of rows[i] rows, the last n_q[i] of them the
  * tree's, off[i] cells behind the start of the first page.  Errors: KVC_EINVAL. */
 int kvc_debug_tree_plan(int n_head, int n_head_kv, int sms, int n_seq, const int32_t *rows, const int32_t *off,
                         const int32_t *n_q, int32_t *tile_m, int32_t *whole, int32_t *splits, int32_t *split_rows,
                         int64_t *items, int64_t *part_rows, int64_t *part_cap);
+
+/* Test hook, no context and no GPU needed: the plan of a tree attention launch of
+ * the tcgen05 kernel over n_seq (1 .. 64) sequences.  entries: HOST
+ * kvc_debug_entry[64], in the launch's order; *n_entries receives their number.
+ * Errors: KVC_EINVAL. */
+typedef struct kvc_debug_entry {
+    int32_t id, tile0, tiles;          /* the sequence, its first tile here and their number */
+    int32_t whole, splits, split_rows; /* units (a KV head's tile) taken whole; parts of the others, and their rows */
+    int32_t item0, part_row0, part_rows, cut0; /* first item; first partial row and their number; cut units before its own */
+} kvc_debug_entry;
+int kvc_debug_tree_plan_tc(int n_head, int n_head_kv, int sms, int n_seq, const int32_t *rows, const int32_t *n_q,
+                           int32_t *tile_m, int32_t *n_entries, kvc_debug_entry *entries, int64_t *items,
+                           int64_t *part_rows, int64_t *part_cap);
 
 /* Test hook, no context and no GPU needed: the angles of kvc_append_rope: of
  * every rotary pair i the turn that one position adds, rope_base^(-2i/D) / (2 pi),

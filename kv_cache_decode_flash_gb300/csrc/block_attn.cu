@@ -525,38 +525,77 @@ extern "C" int kvc_debug_recent_rows(kvc_ctx *cc, int layer, int seq, int32_t *r
     return KVC_OK;
 }
 
-extern "C" int kvc_debug_tree_plan(int n_head, int n_head_kv, int sms, int n_seq, const int32_t *rows, const int32_t *off,
-                                   const int32_t *n_q, int32_t *tile_m, int32_t *whole, int32_t *splits, int32_t *split_rows,
-                                   int64_t *items, int64_t *part_rows, int64_t *part_cap) {
+// The launch of a tree attention test hook, checked.
+static bool tree_launch(int n_head, int n_head_kv, int sms, int n_seq, const int32_t *rows, const int32_t *off, const int32_t *n_q,
+                        BlockParams &p) {
     if (n_head_kv < 1 || n_head < n_head_kv || n_head % n_head_kv || n_head / n_head_kv > MAX_GROUP || sms < 1 || n_seq < 1 ||
-        n_seq > MAX_SEQ_PER_LAUNCH || !rows || !off || !n_q || !tile_m || !whole || !splits || !split_rows || !items ||
-        !part_rows || !part_cap)
-        return KVC_EINVAL;
-    BlockParams p;
+        n_seq > MAX_SEQ_PER_LAUNCH || !rows || !n_q)
+        return false;
     std::memset(&p, 0, sizeof(p));
     p.H = n_head;
     p.Hk = n_head_kv;
     p.r = n_head / n_head_kv;
     p.n_seq = n_seq;
     for (int i = 0; i < n_seq; ++i) {
-        if (n_q[i] < 1 || n_q[i] > TREE_MAX || rows[i] < n_q[i] || off[i] < 0) return KVC_EINVAL;
+        if (n_q[i] < 1 || n_q[i] > TREE_MAX || rows[i] < n_q[i] || (off && off[i] < 0)) return false;
         p.seq[i].n_rows = rows[i];
-        p.seq[i].off = off[i];
+        p.seq[i].off = off ? off[i] : 0;
         p.seq[i].n_tok = n_q[i];
         p.seq[i].id = i;
     }
+    return true;
+}
+
+// Partial rows that the launch's parts take up.
+static int64_t part_rows_of(const BlockParams &p) {
+    int64_t most = 0;
+    for (int i = 0; i < p.n_seq; ++i) {
+        const BlockSeq &s = p.seq[i];
+        const int64_t cut = (int64_t)s.tiles * p.Hk - s.whole;
+        most = std::max<int64_t>(most, s.part_row0 + cut * s.splits * p.part_rows);
+    }
+    return most;
+}
+
+extern "C" int kvc_debug_tree_plan(int n_head, int n_head_kv, int sms, int n_seq, const int32_t *rows, const int32_t *off,
+                                   const int32_t *n_q, int32_t *tile_m, int32_t *whole, int32_t *splits, int32_t *split_rows,
+                                   int64_t *items, int64_t *part_rows, int64_t *part_cap) {
+    BlockParams p;
+    if (!off || !tile_m || !whole || !splits || !split_rows || !items || !part_rows || !part_cap ||
+        !tree_launch(n_head, n_head_kv, sms, n_seq, rows, off, n_q, p))
+        return KVC_EINVAL;
     plan_tree(p, sms);
     *tile_m = p.tile_m;
     *items = p.n_items;
-    *part_rows = 0;
+    *part_rows = part_rows_of(p);
     *part_cap = part_rows_cap(sms);
     for (int i = 0; i < n_seq; ++i) {
         const BlockSeq &s = p.seq[i];
         whole[s.id] = s.whole;
         splits[s.id] = s.splits;
         split_rows[s.id] = s.split_rows;
+    }
+    return KVC_OK;
+}
+
+extern "C" int kvc_debug_tree_plan_tc(int n_head, int n_head_kv, int sms, int n_seq, const int32_t *rows, const int32_t *n_q,
+                                      int32_t *tile_m, int32_t *n_entries, kvc_debug_entry *entries, int64_t *items,
+                                      int64_t *part_rows, int64_t *part_cap) {
+    BlockParams p;
+    if (!tile_m || !n_entries || !entries || !items || !part_rows || !part_cap ||
+        !tree_launch(n_head, n_head_kv, sms, n_seq, rows, nullptr, n_q, p))
+        return KVC_EINVAL;
+    plan_tree_tc(p, sms);
+    *tile_m = p.tile_m;
+    *items = p.n_items;
+    *part_rows = part_rows_of(p);
+    *part_cap = part_rows_cap(sms);
+    *n_entries = p.n_seq;
+    for (int i = 0; i < p.n_seq; ++i) {
+        const BlockSeq &s = p.seq[i];
         const int64_t cut = (int64_t)s.tiles * p.Hk - s.whole;
-        *part_rows = std::max<int64_t>(*part_rows, s.part_row0 + cut * s.splits * p.part_rows);
+        entries[i] = {s.id, s.tile0, s.tiles, s.whole, s.splits, s.split_rows, s.item0, s.part_row0, (int32_t)(cut * s.splits * p.part_rows),
+                      s.cut0};
     }
     return KVC_OK;
 }

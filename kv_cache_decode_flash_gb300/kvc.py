@@ -108,6 +108,7 @@ def load():
         "kvc_debug_block_kernel": (i32, [p, i32]),
         "kvc_debug_block_plan": (i32, [i32] * 6 + [p] * 9),
         "kvc_debug_tree_plan": (i32, [i32] * 4 + [p] * 10),
+        "kvc_debug_tree_plan_tc": (i32, [i32] * 4 + [p] * 8),
         "kvc_debug_rope_turns": (i32, [C.c_float, i32, p]),
         "kvc_debug_recent_rows": (i32, [p, i32, i32, p]),
         "kvc_debug_select_rows": (i32, [p, i32, i32, i32, i32, p, C.POINTER(C.c_int64), C.POINTER(C.c_int64),
@@ -572,6 +573,25 @@ def kvc_debug_tree_plan(n_head, n_head_kv, sms, rows, off, n_q):
     if st != KVC_OK:
         raise KvcError(st, "bad tree-plan arguments")
     return {"tile_m": tm.value, "whole": list(wh), "splits": list(sp), "split_rows": list(sr),
+            **{k: b.value for k, b in zip(("items", "part_rows", "part_cap"), big)}}
+
+
+class kvc_debug_entry(C.Structure):
+    _fields_ = [(k, C.c_int32) for k in ("id", "tile0", "tiles", "whole", "splits", "split_rows", "item0", "part_row0", "part_rows",
+                                         "cut0")]
+
+
+def kvc_debug_tree_plan_tc(n_head, n_head_kv, sms, rows, n_q):
+    """The entries of a tree attention launch of the tcgen05 kernel, in its order, without a context or a GPU."""
+    n = len(rows)
+    r, t = ((C.c_int32 * n)(*[int(x) for x in a]) for a in (rows, n_q))
+    entries, ne, tm = (kvc_debug_entry * 64)(), C.c_int32(), C.c_int32()
+    big = [C.c_int64() for _ in range(3)]
+    st = load().kvc_debug_tree_plan_tc(n_head, n_head_kv, sms, n, r, t, C.byref(tm), C.byref(ne), entries,
+                                       *[C.byref(b) for b in big])
+    if st != KVC_OK:
+        raise KvcError(st, "bad tree-plan arguments")
+    return {"tile_m": tm.value, "entries": [{k: getattr(e, k) for k, _ in e._fields_} for e in entries[:ne.value]],
             **{k: b.value for k, b in zip(("items", "part_rows", "part_cap"), big)}}
 
 
