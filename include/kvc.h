@@ -159,7 +159,7 @@ int kvc_append(kvc_ctx *c, int layer, int seq, int pos0, int n_tok, const float 
  * over n's rotary pairs i (see kvc_rope; kvc_seq_add turns by the same angles).
  * Turned queries go to q_out in their own type; turned keys and the values as
  * they are become the sequence's next rows of that layer, in order, stored as
- * kvc_append stores them.  Computed in fp32, the angle exact to 2^-32 of a turn
+ * kvc_append stores them.  Computed in fp32, the angle within 1.6e-8 of a turn
  * whatever the position, and rounded once.  Positions may be any (the tokens of a
  * drafted tree share those of their depth); as with kvc_append the first layer to
  * append creates the rows, and the others must append the same positions.

@@ -156,7 +156,7 @@ template <int D, int ACT> __global__ void __launch_bounds__(ROPE_THREADS) rope_a
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int pr = a.neox ? 4 * li + i : (i < 2 ? 2 * li + i : D / 4 + 2 * li + i - 2);
-        // the fraction of a turn in [-1/2, 1/2): its upper 32 bits are off by 2^-33 at most
+        // the fraction of a turn in [-1/2, 1/2): its upper 32 bits are off by 2^-33 at most, as fp32 by 2^-26 more
         const int32_t f = (int32_t)((((uint64_t)(uint32_t)pos * a.turn[pr]) + 0x80000000ull) >> 32);
         sincospif((float)f * 0x1p-31f, &sn[i], &cs[i]);
     }
