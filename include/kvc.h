@@ -280,9 +280,10 @@ int kvc_attn_cross(kvc_ctx *c, int layer, int n_seq, const int32_t *seq_ids, con
  * the tokens are a chain: each sees all before it.  n_q[i] may be 0; at most 256.
  * What a row holds that a token does not see never reaches that token.  (Codes
  * share a power of two among neighbouring rows that some token of the block sees:
- * V values 2^14 times those that a token sees may cost it accuracy.)  A V value
- * that is not finite reaches every token that sees its row (infinite, or NaN
- * where 32 bits, with 16-bit queries 16, leave the row no weight).
+ * scales of K 2^21 times, or values of V 2^14 times those of the rows that a token
+ * sees may cost it accuracy.)  A V value that is not finite reaches every token
+ * that sees its row (infinite, or NaN where 32 bits, with 16-bit queries 16,
+ * leave the row no weight).
  * seq_ids, n_q: HOST int32[n_seq]; an id may come more than once (trees over the
  * same last rows).  act: type of q and out (kvc_act).
  * q, out: device [T][n_head][head_dim], contiguous, 16-byte aligned; out may not

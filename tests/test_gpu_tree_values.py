@@ -90,6 +90,36 @@ def test_keys_keep_their_bits_under_large_scores(kind, D, act, T, n, score, spre
 
 
 @pytest.mark.parametrize("kernel", [MMA, TCGEN05], ids=["mma", "tcgen05"])
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("kind,D", [("q8", 64), ("q8", 128), ("q8q4", 128)])
+def test_keys_beside_an_unseen_one_of_a_million_times_their_size(kind, D, act, kernel):
+    """A step's codes of K share a power of two on tcgen05: both parts of a code times its scale are whole up to 2^21 below the
+    step's largest scale, also one of a row that most tokens do not see."""
+    import torch
+
+    H, Hk, T, n = 10, 2, 30, 600
+    rng = np.random.default_rng(43)
+    k, v = _level_rows(rng, n, Hk, D, 0.02)
+    k *= 2.0**-6
+    k[n - T + 1] = 2.0**14  # token 1's, a sibling of all but itself
+    tw = _twin(kind, H, Hk, D, n, k, v, kernel)
+    try:
+        one = np.full((T, H, D), 2.0**6)
+        one[..., ::32] = 0
+        par = np.zeros(T, np.int32)
+        par[:2] = -1
+        scale = float(np.float32(100 / D))
+        got = _run(tw, T, torch.from_numpy(one).to("cuda:0", _types()[act]), scale, par).double().cpu().numpy()
+        s = tw.ref.seqs[0]
+        want, mag, size = attend(one, values(s.K[0]), values(s.V[0]), scale, tree_sees(par, n, T))
+        bound = attend_bound(mag, size, n, D, act, exact=True)
+        ratio = (np.abs(got - want) / bound)[[t for t in range(T) if t != 1]]
+        assert ratio.max() <= 1, "%.2f of its bound" % ratio.max()
+    finally:
+        tw.close()
+
+
+@pytest.mark.parametrize("kernel", [MMA, TCGEN05], ids=["mma", "tcgen05"])
 @pytest.mark.parametrize("act", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("kind,D", [("q8", 64), ("f16", 64), ("q8", 128), ("f16", 128), ("q8q4", 128)])
 @pytest.mark.parametrize("T", [3, 30, 70])
