@@ -54,7 +54,6 @@ struct KeepArgs {
     int64_t pool_rows; // rows of one layer pool
     int32_t L, Hk, P;
     int32_t n_entries;
-    uint32_t *err;
     int32_t first[KEEP_ENTRIES + 1]; // an entry's (sequence's) moves
     int2 move[KEEP_MOVES];
 };
