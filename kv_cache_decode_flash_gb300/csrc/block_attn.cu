@@ -122,7 +122,7 @@ static void plan_splits(BlockParams &p, int64_t want, int64_t step, int64_t leas
     }
     // The longest items begin first, so that none of them begins late (q8_0, 8 heads of 128, as given and sorted: 6 tokens of
     // 32 sequences of 64 to 400 rows 21.0 and 18.1 us, of 16 of 300 to 3000 rows 35.2 and 33.1; 20 to 80 tokens of 32 of 1024
-    // to 8000 rows 418 and 374).  Not in more than two waves of items of alike steps, which the memory bounds: there the order
+    // to 8000 rows 412 and 370).  Not in more than two waves of items of alike steps, which the memory bounds: there the order
     // as given is no worse (1 token of 32 sequences of 1024 to 8000 rows: 99 as given, 103 sorted; f16 111 and 120).
     if (tree && (weighted || items <= 2 * want))
         std::stable_sort(p.seq, p.seq + p.n_seq, [&](const BlockSeq &a, const BlockSeq &b) {
@@ -184,9 +184,9 @@ static void plan_tree(BlockParams &p, int sms) {
 }
 
 // The same for the tcgen05 kernel.  A last tile whose query rows fill half of it at most costs less a step (65536 q8_0 rows of
-// 8 KV heads: 125 rows 80 us, 255 rows 117), so it is an entry of its own, with longer parts, where the launch has room (64
-// tokens of 5 heads over 32768 rows 110 us as one entry, 101 as two; 32 sequences of 20 to 80 tokens over 1024 to 8000 rows 391
-// and 374).
+// 8 KV heads: 125 rows 80 us, 255 rows 116), so it is an entry of its own, with longer parts, where the launch has room (64
+// tokens of 5 heads over 32768 rows 111 us as one entry, 99 as two; 32 sequences of 20 to 80 tokens over 1024 to 8000 rows 388
+// and 370).
 static void plan_tree_tc(BlockParams &p, int sms) {
     int32_t most = 0;
     for (int i = 0; i < p.n_seq; ++i) most = std::max(most, p.seq[i].n_tok);
@@ -227,10 +227,10 @@ static bool use_tc(int rows, double products) { return rows >= TC_MIN_ROWS || pr
 // f16 rows, 4 to 16 tokens: 509 us by two, 394 by the tcgen05 one).  f16 queries over codes stay with the other: the tcgen05
 // one rounds both P and the scaled V to 11 bits, which results of 11 bits would show (3.6e-4 rms against 2.9e-4, and 2.1e-4
 // for the result's own rounding).  Measured in us, bf16 queries, mma.sync against tcgen05, heads/KV heads/D, rows: tokens
-//   40/8/128 q8_0   512:  16 11.4 / 20.6,  64 14.2 / 27.7          4096:  8 16.7 / 22.6,  32 26.5 / 27.6,  64 48.3 / 31.0
-//                 16384:  4 22.6 / 30.6,   8 32.7 / 31.6,  32 72.9 / 41.2      65536:  4 55.2 / 76.4,  8 98.2 / 77.3
-//   32/8/128 f16   4096:  16 14.4 / 19.4,  64 25.5 / 28.0         65536:  8 51.3 / 60.7,  16 66.5 / 59.8,  64 229 / 85.7
-//   8/2/64 q8_0   16384:  64 24.5 / 29.5                          65536:  16 26.9 / 30.2,  64 70.5 / 39.5
+//   40/8/128 q8_0   512:  16 11.6 / 19.5,  64 14.1 / 25.3          4096:  8 16.6 / 21.1,  32 26.4 / 26.1,  64 48.3 / 30.4
+//                 16384:  4 22.7 / 31.3,   8 32.7 / 32.4,  32 73.1 / 40.8      65536:  4 55.2 / 76.0,  8 98.1 / 76.5
+//   32/8/128 f16   4096:  16 14.5 / 18.4,  64 25.4 / 26.3         65536:  8 51.4 / 59.1,  16 66.3 / 58.7,  64 229 / 83.8
+//   8/2/64 q8_0   16384:  64 24.2 / 24.0                          65536:  16 26.5 / 29.3,  64 70.4 / 35.3
 static bool tree_tc_pays(double values, double rows_m, double rows) {
     const double m = rows > 0 ? rows_m / rows : 0;
     return m > 32 && values >= 1 << 22 && m * values >= 1 << 28;

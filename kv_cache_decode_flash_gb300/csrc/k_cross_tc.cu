@@ -359,9 +359,9 @@ __device__ __forceinline__ float row_scores(uint32_t S, const Seen &n, uint32_t 
 }
 
 // exp2 of the scores (times f, less use; f >= 0, an unseen one is -inf) as fp16 pairs over them; returns their sum.
-// mark(c, rows): a look at which of column block c's 32 rows are seen, of whatever weight (MASK; with all scores held their
-// bits are gathered on the way, which the compiler makes more of: 6 tokens over 16384 rows, halves 22.8 us so and 24.2
-// with the bits made for the look, codes 31.9 and 30.4).
+// mark(c, rows): a look at column block c's 32 rows (MASK); with all scores held, rows are those that are seen, of whatever
+// weight.  (Gathered on the way, where the registers are there: 6 tokens over 16384 rows, halves 23.0 us so and 24.2 with the
+// bits made when they are needed; codes 31.9 and 30.3, and their trees 386 and 370 us of 32 sequences of 20 to 80 tokens.)
 template <bool MASK, int HOLD, class Seen, class Mark>
 __device__ __forceinline__ float row_exp(uint32_t S, const Seen &n, uint32_t (&r)[HOLD][32], float f, float use, Mark mark) {
     const uint64_t ff = pair(f, f), mm = pair(-use, -use);
@@ -384,7 +384,7 @@ __device__ __forceinline__ float row_exp(uint32_t S, const Seen &n, uint32_t (&r
             else
                 a0 = add2(a0, pair(y.x, y.y));
         }
-        if (MASK) mark(c, HOLD == 4 ? own : n.block(c));
+        if (MASK) mark(c, own);
         tm_st16(S + c * 16, w);
     };
     if constexpr (HOLD == 4) {
@@ -407,7 +407,7 @@ __device__ __forceinline__ float row_exp(uint32_t S, const Seen &n, uint32_t (&r
 
 // TREE: the block's tokens are the sequence's last rows, and each sees the rows before them, its ancestors' and its own
 // (kvc_attn_tree); else a token sees its n_vis leading rows.  K's codes have two parts there too, although no log-sum-exp
-// comes with a tree: with one of 11 bits (26 tokens over 16384 rows 36 us, 40 with both; 64 over 32768 95 and 101) scores of
+// comes with a tree: with one of 11 bits (26 tokens over 16384 rows 36 us, 40 with both; 64 over 32768 95 and 99) scores of
 // 300 were off by 0.07 and results by as much, ten roundings of bf16.
 template <int D, int KT, int VT, bool TREE>
 __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(const __grid_constant__ BlockParams p) {
@@ -619,6 +619,7 @@ __global__ void __launch_bounds__(THREADS<KT != KVC_F16>, 1) cross_tc_kernel(con
                     sum += row_exp<true>(S, seen(), sc, f, use, [&](int c, uint32_t own) {
                         const uint32_t rows = x.badrow[slot][c];
                         if (rows == 0) return;
+                        if (HOLD != 4) own = seen().block(c);
 #pragma unroll 1
                         for (int e = 0; e < 32; ++e) {
                             if (!(rows >> e & 1)) continue;
