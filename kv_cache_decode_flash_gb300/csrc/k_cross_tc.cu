@@ -32,9 +32,9 @@
 // formed under the same factor, which lse and the parts' maxima take back.
 // What bounds it: with many query rows the chain of a half's job, softmax and its
 // products, against the other half's, whose products the one issuing thread takes
-// in turn (2048 tokens of 40 heads over 16384 rows, causal: halves 598 us, 1.08
+// in turn (2048 tokens of 40 heads over 16384 rows, causal: halves 606 us, 1.07
 // PFLOP/s of seen pairs, 57 % of a plain matrix product's rate; codes, with three
-// products a job, 806 us, 0.80 PFLOP/s).  With few, halves run at the memory's rate
+// products a job, 789 us, 0.82 PFLOP/s).  With few, halves run at the memory's rate
 // (131072 rows, 5 tokens: 90 us, 6.0 TB/s of 6.8), codes at that of their
 // conversion (136 us, 2.1 TB/s), short ones at start, first tiles and join (16384
 // rows, 5 tokens: 31 us, of which the seven steps are half).

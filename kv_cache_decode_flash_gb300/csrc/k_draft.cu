@@ -16,7 +16,7 @@
 //
 //  What bounds it: the launch for few tokens (1 token of 56 head-rows 2.2 us, 32
 //  sequences 2.3), instructions for many (2048 tokens 17 us, 3.2 TB/s of projections
-//  read and rows written; 250 a pass, issued in 64 % of the cycles), of which the
+//  read and rows written; 248 a pass, issued in 64 % of the cycles), of which the
 //  quantiser's are most: eight passes of 28 bring keys and values.
 //
 // keep (kvc_seq_keep): rows of the accepted path move down over the others.  A
