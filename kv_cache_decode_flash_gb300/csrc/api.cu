@@ -19,6 +19,7 @@ namespace kvc {
 // ---------------------------------------------------------------- helpers --
 
 int cuda_fail(Ctx *c, cudaError_t e, const char *what) {
+    cudaGetLastError(); // reported here: the next launch that asks is not to find it
     return c->fail(KVC_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 

@@ -218,3 +218,30 @@ def test_an_append_whose_launch_failed_leaves_no_entry_behind(two, then):
         else:
             c.plain(0, y, PAGE)()
     same(a.rows(), b.rows())
+
+
+@pytest.mark.parametrize("then", ["rope", "plain"])
+def test_a_failed_launch_is_reported_once(two, then):
+    """An append into a page that is there, refused by a void capture; the next one, which takes a page, is not told of it."""
+    a, b = (c.start() for c in two)
+    torch, kvc = a.torch, a.kvc
+    for c in (a, b):
+        c.rope(0, c.draw(6, 2), PAGE)
+    x, y = a.draw(3, 5), b.draw(4, 20)
+    cu = ctypes.CDLL("libcuda.so.1")
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    stream, graph = ctypes.c_void_p(st.cuda_stream), ctypes.c_void_p()
+    assert cu.cuStreamBeginCapture_v2(stream, 2) == 0
+    assert cu.cuStreamSynchronize(stream) != 0
+    with pytest.raises(kvc.KvcError) as e:
+        a.c.append_rope(0, [0], [5], list(range(PAGE + 2, PAGE + 7)), None, x[:, H:H + Hk], x[:, H + Hk:], None, stream=st)
+    assert e.value.status == kvc.KVC_ECUDA
+    assert cu.cuStreamEndCapture(stream, ctypes.byref(graph)) != 0
+    assert a.c.n_tokens(0) == PAGE + 2
+    for c in (a, b):
+        if then == "rope":
+            c.rope(0, y, PAGE + 2)
+        else:
+            c.plain(0, y, PAGE + 2)()
+    same(a.rows(), b.rows())
