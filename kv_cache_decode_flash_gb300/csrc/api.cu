@@ -202,11 +202,11 @@ void release_tail_pages(Ctx *c, Seq &q) {
     q.cap_pages = std::min<int32_t>(q.cap_pages, (int32_t)q.pages.size());
 }
 
-// Sends the table entries of pages that sequences ids[0 .. n) grew by (grow_pages), on st, as kernel arguments.  An entry
-// that the device is known to hold, of a page that left and came back, is not sent again.  On a capturing stream the
-// entries are only recorded: that capture's replays have all of theirs from it, whatever was replayed before, and calls
-// outside it send them again.  If they cannot be sent, the pages go back, and nothing relies on what the launches that did
-// run may have left.
+// Sends the table entries that the device may lack of sequences ids[0 .. n), whose rows are about to be written, on st as
+// kernel arguments: those of pages that they grew by (grow_pages) and of pages that a captured call took.  An entry that
+// the device is known to hold, of a page that left and came back, is not sent again.  On a capturing stream the entries are
+// only recorded: that capture's replays have all of theirs from it, whatever was replayed before, and calls outside it send
+// them again.  If they cannot be sent, the pages go back, and nothing relies on what the launches that did run may have left.
 int send_pages(Ctx *c, const int32_t *ids, int n, cudaStream_t st) {
     bool any = false;
     for (int i = 0; i < n; ++i) any = any || c->seqs[(size_t)ids[i]].dev_pages != (int32_t)c->seqs[(size_t)ids[i]].pages.size();
@@ -788,17 +788,17 @@ static int append_check(Ctx *c, int layer, int seq, int pos0, int n_tok, bool *c
 }
 
 // Destination of the next n_tok rows of `seq` in `layer` of a device context;
-// when the layer creates them, their pages are allocated and new page-table
-// entries are sent on st (as kernel arguments, no host copy).
+// when the layer creates them, their pages are allocated.  Page-table entries
+// that the device lacks are sent on st (as kernel arguments, no host copy).
 static int device_append_dst(Ctx *c, int layer, int seq, bool creates, int n_tok, cudaStream_t st, AppendDst *d) {
     Seq &q = c->seqs[seq];
     if (creates) {
         size_t first_new;
         int rc = grow_pages(c, q, n_tok, &first_new);
         if (rc) return rc;
-        const int32_t id = seq;
-        if ((rc = send_pages(c, &id, 1, st))) return rc;
     }
+    const int32_t id = seq;
+    if (int rc = send_pages(c, &id, 1, st)) return rc;
     const int64_t lo = (int64_t)layer * c->pool_rows;
     d->lv.k.data = c->kdata + lo * c->krow;
     d->lv.k.scales = c->ksb ? reinterpret_cast<uint16_t *>(c->kscales + lo * c->ksb) : nullptr;

@@ -417,7 +417,8 @@ extern "C" int kvc_attn_tree(kvc_ctx *cc, int layer, int n_seq, const int32_t *s
     }
     // Kernels after these start only once they have waited for all before them (captured ones wait at their replays).
     cudaStreamCaptureStatus status = cudaStreamCaptureStatusActive;
-    if (cudaStreamIsCapturing(st, &status) == cudaSuccess && status == cudaStreamCaptureStatusNone) c->clear_recent();
+    KVC_CU(c, cudaStreamIsCapturing(st, &status));
+    if (status == cudaStreamCaptureStatusNone) c->clear_recent();
     return KVC_OK;
 }
 

@@ -128,16 +128,16 @@ static int append_rope(Ctx *c, int layer, const RopeCall &call, RopeArgs &a, cud
     if (new_pages > (int64_t)c->free_pages.size()) return c->fail(KVC_ENOSPC, "no free pages");
     KVC_CU(c, cudaSetDevice(c->dev));
     // (host memory for all of it before the first change)
-    std::vector<int32_t> grown;
-    grown.reserve((size_t)n_seq);
+    std::vector<int32_t> written;
+    written.reserve((size_t)n_seq);
     for (int i = 0; i < n_seq; ++i) {
+        if (n_tok[i] > 0) written.push_back(ids[i]);
         if (!creates[(size_t)i]) continue;
         Seq &q = c->seqs[(size_t)ids[i]];
         const size_t pages = std::max(q.pages.size(), (size_t)pages_for(c, q.off, (int64_t)q.n + n_tok[i]));
         make_room(q.pos, (size_t)q.n + (size_t)n_tok[i]);
         make_room(q.pages, pages);
         make_room(q.dev_table, pages);
-        grown.push_back(ids[i]);
     }
     for (int i = 0; i < n_seq; ++i) {
         if (!creates[(size_t)i]) continue;
@@ -145,7 +145,7 @@ static int append_rope(Ctx *c, int layer, const RopeCall &call, RopeArgs &a, cud
         int rc = grow_pages(c, c->seqs[(size_t)ids[i]], n_tok[i], &first_new);
         if (rc) return rc; // (cannot happen: checked above)
     }
-    if (int rc = send_pages(c, grown.data(), (int)grown.size(), st)) return rc;
+    if (int rc = send_pages(c, written.data(), (int)written.size(), st)) return rc;
     // The launches: pieces of consecutive positions need no list, the others' positions travel with them.
     if (!c->has_turns) rope_turns(c->prm.rope_base, c->D, c->rope_turn);
     c->has_turns = true;
@@ -177,7 +177,7 @@ static int append_rope(Ctx *c, int layer, const RopeCall &call, RopeArgs &a, cud
         cudaError_t e = launch_rope_append(c->D, call.act, a, st);
         a.n_pieces = a.n_tok = listed = 0;
         if (e == cudaSuccess) return KVC_OK;
-        for (int32_t id : grown) release_tail_pages(c, c->seqs[(size_t)id]);
+        for (int32_t id : written) release_tail_pages(c, c->seqs[(size_t)id]);
         return cuda_fail(c, e, "append kernel");
     };
     t0 = 0;

@@ -15,13 +15,13 @@ H, Hk, D, PAGE = 4, 2, 64, 16
 class Cache:
     """Two sequences of 16-bit rows in small pages; draws by number, so that two caches can be given the same ones."""
 
-    def __init__(self):
+    def __init__(self, layers=1):
         import torch
 
         from kv_cache_decode_flash_gb300 import kvc
 
         self.torch, self.kvc = torch, kvc
-        self.c = kvc.KVCache(1, H, Hk, D, 192, 2, oracle.F16, oracle.F16, page_rows=PAGE)
+        self.c = kvc.KVCache(layers, H, Hk, D, 192, 2, oracle.F16, oracle.F16, page_rows=PAGE)
         self.held = []
 
     def draw(self, number, n):
@@ -245,3 +245,41 @@ def test_a_failed_launch_is_reported_once(two, then):
         else:
             c.plain(0, y, PAGE + 2)()
     same(a.rows(), b.rows())
+
+
+@pytest.mark.parametrize("first", ["rope", "plain"])
+@pytest.mark.parametrize("then", ["rope", "plain", "step"])
+def test_another_layers_append_behind_a_captured_one(first, then):
+    """The first layer's append takes a page in a capture; the second layer's rows of the same tokens come outside it, ahead of
+    the replay."""
+    a, b = caches = [Cache(2), Cache(2)]
+    try:
+        n = 1 if then == "step" else 5
+
+        def rows(c, how, layer, number):
+            x = c.draw(number, n)
+            k, v = x[:, H:H + Hk].float().contiguous(), x[:, H + Hk:].float().contiguous()
+            q = x[:, :H].float().contiguous()
+            c.held.append((k, v, q))
+            if how == "rope":
+                return lambda: c.c.append_rope(layer, [0], [n], list(range(PAGE, PAGE + n)), None, x[:, H:H + Hk],
+                                               x[:, H + Hk:], None)
+            if how == "plain":
+                return lambda: c.c.append(layer, 0, PAGE, k, v)
+            return lambda: c.c.decode_step(layer, [0], [PAGE], k, v, q, c.torch.empty_like(q), 0.125)
+
+        for c in caches:
+            for seq, m in ((1, 5 * PAGE), (0, PAGE)):
+                for layer in range(2):
+                    x = c.draw(10 * seq + layer, m)
+                    c.c.append_rope(layer, [seq], [m], list(range(m)), None, x[:, H:H + Hk], x[:, H + Hk:], None)
+            c.rows()
+        g = a.capture(rows(a, first, 0, 30))
+        rows(b, first, 0, 30)()
+        for c in caches:
+            rows(c, then, 1, 31)()
+        g.replay()
+        same(a.rows(), b.rows())
+    finally:
+        for c in caches:
+            c.c.close()
